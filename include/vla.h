@@ -47,7 +47,8 @@ typedef enum {
     VLA_ERR_UNSUPPORTED = 2,   /* head dimension not in {32, 64, 96, 128} */
     VLA_ERR_CUDA = 3,          /* a CUDA runtime call or kernel launch failed */
     VLA_ERR_TIMEOUT = 4,       /* a bounded in-kernel wait ran out; outputs are invalid */
-    VLA_ERR_NONFINITE = 5      /* a NaN/Inf appeared in delta_t or the gate norm */
+    VLA_ERR_NONFINITE = 5,     /* a NaN/Inf appeared in delta_t or the gate norm (or in what vla_layer.h names) */
+    VLA_ERR_BAD_SLOT = 6       /* a slot out of range or used twice in one call (vla_layer.h) */
 } vla_status;
 
 typedef enum {
@@ -194,10 +195,12 @@ vla_status vla_forward_ex(const void* q, const void* k, const void* v, const voi
 
 /*
  * Synchronise `stream`, read and clear the status record that kernels on it
- * wrote into `workspace`. Returns VLA_OK, VLA_ERR_TIMEOUT (takes precedence)
- * or VLA_ERR_NONFINITE, or VLA_ERR_CUDA if the copy/sync itself failed.
+ * wrote into `workspace`. Returns VLA_OK, VLA_ERR_TIMEOUT (takes precedence),
+ * VLA_ERR_BAD_SLOT or VLA_ERR_NONFINITE, or VLA_ERR_CUDA if the copy/sync
+ * itself failed.
  * If `detail` is not NULL it receives {role, head, token} of the first
- * recorded failure (role: 0 staging, 1 gate, 2 A-pass, 3 S-pass), or -1s.
+ * recorded failure (role: 0 staging, 1 gate, 2 A-pass, 3 S-pass; 4 a slot,
+ * with {sequence, slot}), or -1s.
  */
 vla_status vla_get_last_device_status(void* workspace, void* stream, int* detail);
 

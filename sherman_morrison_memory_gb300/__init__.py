@@ -12,6 +12,12 @@ q, k, v, u: [B, H, T, d] float32 or bfloat16 tensors (d in 32, 64, 96, 128).
 CUDA tensors run on their device's current stream; CPU tensors are copied to
 the current CUDA device, run, and the results copied back (the end-to-end
 path of a caller holding host buffers).
+
+Around it (``include/vla_layer.h``, CUDA tensors): linear attention with a
+decay per head (``vla_decay_forward``, ``vla_decay_backward``,
+``vla_decay_step``), the layer norm of each head's readout (``vla_head_norm``,
+``vla_head_norm_backward``) and a quantised cache of states
+(``vla_state_cache``, ``vla_state_store``, ``vla_state_load``).
 """
 from __future__ import annotations
 
@@ -22,6 +28,7 @@ from ._binding import (  # noqa: F401
     VLA_ERR_CUDA,
     VLA_ERR_TIMEOUT,
     VLA_ERR_NONFINITE,
+    VLA_ERR_BAD_SLOT,
     VLA_ALGO_AUTO,
     VLA_ALGO_PER_TOKEN,
     VLA_ALGO_CHUNKED,
@@ -39,6 +46,16 @@ from ._binding import (  # noqa: F401
     vla_status_string,
     vla_workspace_bytes,
 )
+from ._layer import (  # noqa: F401
+    vla_decay_backward,
+    vla_decay_forward,
+    vla_decay_step,
+    vla_head_norm,
+    vla_head_norm_backward,
+    vla_state_cache,
+    vla_state_load,
+    vla_state_store,
+)
 
 __all__ = [
     "vla_forward",
@@ -47,5 +64,13 @@ __all__ = [
     "vla_linear_attention_state",
     "vla_status_string",
     "vla_workspace_bytes",
+    "vla_decay_forward",
+    "vla_decay_backward",
+    "vla_decay_step",
+    "vla_head_norm",
+    "vla_head_norm_backward",
+    "vla_state_cache",
+    "vla_state_store",
+    "vla_state_load",
     "VLAError",
 ]

@@ -22,6 +22,7 @@ VLA_ERR_UNSUPPORTED = 2
 VLA_ERR_CUDA = 3
 VLA_ERR_TIMEOUT = 4
 VLA_ERR_NONFINITE = 5
+VLA_ERR_BAD_SLOT = 6
 VLA_ALGO_AUTO = 0
 VLA_ALGO_PER_TOKEN = 1
 VLA_ALGO_CHUNKED = 2
@@ -51,6 +52,31 @@ class _Options(ctypes.Structure):
     _fields_ = [("wait_limit_us", ctypes.c_uint), ("test_stall_producer", ctypes.c_int),
                 ("trace", ctypes.c_void_p), ("algo", ctypes.c_int), ("fixed_a", ctypes.c_int),
                 ("scratch", ctypes.c_void_p), ("scratch_bytes", ctypes.c_size_t)]
+
+
+class _Seq(ctypes.Structure):
+    """vla_seq and vla_seq_out of include/vla_layer.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+                ("stride_t", ctypes.c_longlong)]
+
+
+def _layer_prototypes(lib):
+    """Argument types of the entry points in include/vla_layer.h."""
+    vp, ci, cf, cl, cz, sq = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_size_t,
+                              ctypes.POINTER(_Seq))
+    for name, args, res in (
+            ("vla_decay_scratch_bytes", [ci] * 5, cz),
+            ("vla_decay_forward", [sq] * 3 + [ci] * 5 + [vp, cf, vp, vp, sq, vp, vp, cz, vp, vp], ci),
+            ("vla_decay_backward", [sq] * 4 + [ci] * 5 + [vp, cf, vp, vp, vp, sq, sq, sq, vp, vp, cz, vp, vp], ci),
+            ("vla_decay_step", [vp] * 3 + [ci] * 4 + [vp, cf, vp, ci, vp, vp, vp, vp], ci),
+            ("vla_head_norm", [sq] + [ci] * 5 + [vp, vp, ci, cf, sq, vp, vp, vp], ci),
+            ("vla_head_norm_scratch_bytes", [ci] * 4, cz),
+            ("vla_head_norm_backward", [sq] * 2 + [ci] * 5 + [vp, ci, vp, vp, sq, vp, vp, vp, cz, vp], ci),
+            ("vla_state_store", [vp, ci, cl, ci, ci, vp, vp, ci, vp, vp, vp], ci),
+            ("vla_state_load", [vp, vp, ci, vp, ci, cl, ci, ci, vp, vp, vp], ci)):
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = res
 
 
 def library_path() -> str:
@@ -108,6 +134,7 @@ def load_library():
         lib.vla_probe_ffma_flop.argtypes = [ci, ci, ci, ci]
         lib.vla_probe_ffma_flop.restype = ctypes.c_double
         del cp
+        _layer_prototypes(lib)
         _LIB = lib
         return lib
 

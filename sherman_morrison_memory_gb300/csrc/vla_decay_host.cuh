@@ -1,0 +1,308 @@
+// vla_decay_host.cuh -- linear attention with a decay per head: entry points, the
+// cut into segments, the single-token kernel (include/vla_layer.h).
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+
+#include "vla_decay.cuh"
+#include "vla_decay_fma.cuh"
+
+namespace vla_layer {
+namespace {
+
+// States of the segments (each its own, from zero) to the states they start
+// from: the running sum over the segments in the role's order, with the whole
+// decays between; the sum over all of them is the final state. A thread per
+// value of S.
+struct ScanRole {
+    const float* init;
+    float* fin;
+    int init_t;   // init and fin hold the transposed state
+    int reverse;
+};
+struct ScanArgs {
+    ScanRole role[2];
+    const float* log_decay;
+    vla::DeviceStatus* status;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) vla_decay_scan_kernel(const __grid_constant__ DecayArgs p,
+                                                             const __grid_constant__ ScanArgs q) {
+    const int bh = blockIdx.x / (D * D / 256), i = (blockIdx.x % (D * D / 256)) * 256 + threadIdx.x;
+    const int b = bh / p.H, h = bh % p.H;
+    const ScanRole& r = q.role[blockIdx.y];
+    const float g = p.log_decay[h];
+    const int at = r.init_t ? (i % D) * D + i / D : i;
+    float s = r.init ? r.init[(size_t)bh * D * D + at] : 0.f;
+    float* seg = p.seg + ((size_t)blockIdx.y * p.B * p.H + bh) * p.nseg * D * D + i;
+#pragma unroll 4
+    for (int k = 0; k < p.nseg; ++k) {
+        const int m = r.reverse ? p.nseg - 1 - k : k;
+        const float own = seg[(size_t)m * D * D];
+        seg[(size_t)m * D * D] = s;
+        s = fmaf(decay_pow(g, span_of(p, b, m).n), s, own);
+    }
+    if (r.fin) {
+        r.fin[(size_t)bh * D * D + at] = s;
+        if (!(fabsf(s) <= 3.4028235e38f) && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, p.T);
+    }
+}
+
+// One token: S <- l S + v k^T, o = scale S q. Bound by reading and writing S.
+// Eight lanes hold a row, lane i the float4s i, i + 8, ... of it, so that a
+// warp moves four rows in whole 128-byte lines; a warp has eight rows in
+// flight.
+constexpr int STEP_THREADS = 128;
+constexpr int STEP_ROWS = 32;  // rows of S a block handles
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+    if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float4*>(p);
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xFFFF0000u));
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(STEP_THREADS) vla_decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                                      const T* __restrict__ v, int H,
+                                                                      const float* __restrict__ log_decay, float scale,
+                                                                      float* states, int N, const int* slots, T* o,
+                                                                      vla::DeviceStatus* status) {
+    constexpr int V = D / 32;  // float4s of a row in a lane
+    const int blocks = D / STEP_ROWS;
+    const int bh = blockIdx.x / blocks, row0 = (blockIdx.x % blocks) * STEP_ROWS, b = bh / H, h = bh % H;
+    const int lane = threadIdx.x % 8, r0 = row0 + threadIdx.x / 8;
+    const int slot = slot_of(slots, b, N, true, h == 0 && row0 == 0 ? status : nullptr);
+    const size_t in = (size_t)bh * D;
+    if (slot < 0) {
+        if (lane == 0) o[in + r0] = o[in + r0 + 16] = (T)0.f;
+        return;
+    }
+    float4* S = reinterpret_cast<float4*>(states + ((size_t)slot * H + h) * D * D);
+    float4 s[2][V];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[m][i] = S[(size_t)(r0 + 16 * m) * (D / 4) + lane + 8 * i];
+    const float l = expf(log_decay[h]);
+    float4 kk[V], qq[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        kk[i] = load4(k + in + (lane + 8 * i) * 4);
+        qq[i] = load4(q + in + (lane + 8 * i) * 4);
+    }
+    float bad = 0.f;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const float vv = (float)v[in + r0 + 16 * m];
+        float acc = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float4& x = s[m][i];
+            x.x = fmaf(l, x.x, vv * kk[i].x);
+            x.y = fmaf(l, x.y, vv * kk[i].y);
+            x.z = fmaf(l, x.z, vv * kk[i].z);
+            x.w = fmaf(l, x.w, vv * kk[i].w);
+            acc = fmaf(x.x, qq[i].x, fmaf(x.y, qq[i].y, fmaf(x.z, qq[i].z, fmaf(x.w, qq[i].w, acc))));
+            bad = fmaf(x.x, 0.f, fmaf(x.y, 0.f, fmaf(x.z, 0.f, fmaf(x.w, 0.f, bad))));
+            S[(size_t)(r0 + 16 * m) * (D / 4) + lane + 8 * i] = x;
+        }
+        acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+        acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+        acc += __shfl_xor_sync(0xffffffffu, acc, 4);
+        acc *= scale;
+        bad = fmaf(acc, 0.f, bad);
+        if (lane == 0) o[in + r0 + 16 * m] = (T)acc;
+    }
+    if (bad != bad && status) vla::record_failure(status, vla::BIT_NONFINITE, 3, bh, 0);
+}
+
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+// The cut of a call with `heads` independent rows of blocks (roles x B x H)
+// into segments.
+void plan(long long heads, int T, int* nseg, int* seg_len) {
+    const long long want = 2LL * sm_count() / std::max(1LL, heads);
+    int n = (int)std::max(1LL, std::min<long long>(want, T / 256));
+    const int len = ((T + n - 1) / n + 63) / 64 * 64;
+    *seg_len = std::max(64, len);
+    *nseg = std::max(1, (T + *seg_len - 1) / *seg_len);
+}
+
+template <int D, typename T>
+vla_status launch(DecayArgs& p, int roles, const ScanArgs& q, const DecayArgs& states, int state_roles, cudaStream_t s) {
+    const long long BH = (long long)p.B * p.H;
+    const long long grid = BH * p.nseg;
+    if (grid > 2147483647LL || BH * (D * D / 256) > 2147483647LL) return VLA_ERR_INVALID_ARG;
+    using L = FmaLay<D>;
+    auto main = vla_decay_fma_kernel<D, T, false>;
+    auto own = vla_decay_fma_kernel<D, T, true>;
+    if (cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess ||
+        cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
+        return VLA_ERR_CUDA;
+    if (p.nseg > 1) {
+        own<<<dim3((unsigned)grid, state_roles), L::THREADS, L::SMEM, s>>>(states);
+        vla_decay_scan_kernel<D><<<dim3((unsigned)(BH * (D * D / 256)), state_roles), 256, 0, s>>>(p, q);
+    }
+    main<<<dim3((unsigned)grid, roles), L::THREADS, L::SMEM, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
+}
+
+template <typename T>
+vla_status launch_d(int d, DecayArgs& p, int roles, const ScanArgs& q, const DecayArgs& st, int state_roles,
+                    cudaStream_t s) {
+    switch (d) {
+        case 32: return launch<32, T>(p, roles, q, st, state_roles, s);
+        case 64: return launch<64, T>(p, roles, q, st, state_roles, s);
+        case 96: return launch<96, T>(p, roles, q, st, state_roles, s);
+        default: return launch<128, T>(p, roles, q, st, state_roles, s);
+    }
+}
+
+size_t scratch_bytes_of(int B, int H, int T, int d, bool backward) {
+    if (!good_sizes(B, H, T) || !good_d(d) || B == 0 || H == 0 || T == 0) return 0;
+    const long long BH = (long long)B * H;
+    int nseg, len;
+    plan(BH * (backward ? 3 : 1), T, &nseg, &len);
+    return nseg > 1 ? (size_t)BH * nseg * (backward ? 2 : 1) * d * d * sizeof(float) : 0;
+}
+
+vla_status copy_state(float* dst, const float* src, size_t n, cudaStream_t s) {
+    if (!dst || dst == src || n == 0) return VLA_OK;
+    const cudaError_t e = src ? cudaMemcpyAsync(dst, src, n * sizeof(float), cudaMemcpyDeviceToDevice, s)
+                              : cudaMemsetAsync(dst, 0, n * sizeof(float), s);
+    return e == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace vla_layer
+
+extern "C" {
+
+size_t vla_decay_scratch_bytes(int B, int H, int T, int d, int backward) {
+    return vla_layer::scratch_bytes_of(B, H, T, d, backward != 0);
+}
+
+vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* v, vla_dtype dtype, int B, int H,
+                             int T, int d, const float* log_decay, float scale, const int* lengths, const float* S0,
+                             const vla_seq_out* o, float* S_out, void* scratch, size_t scratch_bytes, void* status,
+                             void* stream) {
+    using namespace vla_layer;
+    if (!good_sizes(B, H, T) || !good_dtype(dtype) || !std::isfinite(scale)) return VLA_ERR_INVALID_ARG;
+    if (!good_d(d)) return VLA_ERR_UNSUPPORTED;
+    if (B == 0 || H == 0) return VLA_OK;
+    if (!log_decay || !S_out || !aligned(log_decay, 4) || !aligned(lengths, 4) || !aligned(S0, 16) ||
+        !aligned(S_out, 16) || !aligned(status, 16))
+        return VLA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) return copy_state(S_out, S0, (size_t)B * H * d * d, s);
+    const int es = dtype == VLA_BF16 ? 2 : 4;
+    if (!good_seq(q, B, H, T, es) || !good_seq(k, B, H, T, es) || !good_seq(v, B, H, T, es) ||
+        !good_seq(o, B, H, T, es))
+        return VLA_ERR_INVALID_ARG;
+    const size_t need = scratch_bytes_of(B, H, T, d, false);
+    if (need && (!scratch || !aligned(scratch, 256) || scratch_bytes < need)) return VLA_ERR_INVALID_ARG;
+    DecayArgs p{};
+    p.B = B, p.H = H, p.T = T;
+    p.log_decay = log_decay;
+    p.lengths = lengths;
+    p.status = static_cast<vla::DeviceStatus*>(status);
+    p.wait_ns = kWaitNs;
+    plan((long long)B * H, T, &p.nseg, &p.seg_len);
+    p.seg = static_cast<float*>(scratch);
+    Role& r = p.role[0];
+    r = Role{to_seq(q, B, H, T), to_seq(k, B, H, T), to_seq(v, B, H, T), to_seq(o, B, H, T), S0, S_out, 0, 0, scale,
+             scale, 1.f};
+    const DecayArgs st = p;
+    ScanArgs sc{};
+    sc.role[0] = ScanRole{S0, S_out, 0, 0};
+    return dtype == VLA_BF16 ? launch_d<__nv_bfloat16>(d, p, 1, sc, st, 1, s) : launch_d<float>(d, p, 1, sc, st, 1, s);
+}
+
+vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO,
+                              vla_dtype dtype, int B, int H, int T, int d, const float* log_decay, float scale,
+                              const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,
+                              const vla_seq_out* dk, const vla_seq_out* dv, float* dS0, void* scratch,
+                              size_t scratch_bytes, void* status, void* stream) {
+    using namespace vla_layer;
+    if (!good_sizes(B, H, T) || !good_dtype(dtype) || !std::isfinite(scale)) return VLA_ERR_INVALID_ARG;
+    if (!good_d(d)) return VLA_ERR_UNSUPPORTED;
+    if (B == 0 || H == 0) return VLA_OK;
+    if (!log_decay || !aligned(log_decay, 4) || !aligned(lengths, 4) || !aligned(S0, 16) || !aligned(dS_T, 16) ||
+        !aligned(dS0, 16) || !aligned(status, 16))
+        return VLA_ERR_INVALID_ARG;
+    // the blocks of dk read dS_T and those of dq S0, when those of dv write dS0
+    if (dS0 && (dS0 == S0 || dS0 == dS_T)) return VLA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T == 0) return copy_state(dS0, dS_T, (size_t)B * H * d * d, s);
+    const int es = dtype == VLA_BF16 ? 2 : 4;
+    if (!good_seq(q, B, H, T, es) || !good_seq(k, B, H, T, es) || !good_seq(v, B, H, T, es) ||
+        !good_seq(dO, B, H, T, es) || !good_seq(dq, B, H, T, es) || !good_seq(dk, B, H, T, es) ||
+        !good_seq(dv, B, H, T, es))
+        return VLA_ERR_INVALID_ARG;
+    const size_t need = scratch_bytes_of(B, H, T, d, true);
+    if (need && (!scratch || !aligned(scratch, 256) || scratch_bytes < need)) return VLA_ERR_INVALID_ARG;
+    const Seq Q = to_seq(q, B, H, T), K = to_seq(k, B, H, T), V = to_seq(v, B, H, T), G = to_seq(dO, B, H, T);
+    DecayArgs p{};
+    p.B = B, p.H = H, p.T = T;
+    p.log_decay = log_decay;
+    p.lengths = lengths;
+    p.status = static_cast<vla::DeviceStatus*>(status);
+    p.wait_ns = kWaitNs;
+    plan(3LL * B * H, T, &p.nseg, &p.seg_len);
+    p.seg = static_cast<float*>(scratch);
+    p.role[0] = Role{G, V, K, to_seq(dq, B, H, T), S0, nullptr, 1, 0, scale, scale, 1.f};
+    p.role[1] = Role{V, G, Q, to_seq(dk, B, H, T), dS_T, nullptr, 1, 1, scale, 1.f, scale};
+    p.role[2] = Role{K, Q, G, to_seq(dv, B, H, T), dS_T, dS0, 0, 1, scale, 1.f, scale};
+    // the segments' own states: those of dq's role and of dv's, which is dk's transposed
+    DecayArgs st = p;
+    st.role[1] = p.role[2];
+    p.seg_role[0] = 0, p.seg_role[1] = 1, p.seg_role[2] = 1;
+    p.seg_t[1] = 1;
+    ScanArgs sc{};
+    sc.role[0] = ScanRole{S0, nullptr, 1, 0};
+    sc.role[1] = ScanRole{dS_T, dS0, 0, 1};
+    return dtype == VLA_BF16 ? launch_d<__nv_bfloat16>(d, p, 3, sc, st, 2, s) : launch_d<float>(d, p, 3, sc, st, 2, s);
+}
+
+vla_status vla_decay_step(const void* q, const void* k, const void* v, vla_dtype dtype, int B, int H, int d,
+                          const float* log_decay, float scale, float* states, int N, const int* slots, void* o,
+                          void* status, void* stream) {
+    using namespace vla_layer;
+    if (!good_sizes(B, H, 1) || N < 0 || !good_dtype(dtype) || !std::isfinite(scale)) return VLA_ERR_INVALID_ARG;
+    if (!good_d(d)) return VLA_ERR_UNSUPPORTED;
+    if (!slots && B > N) return VLA_ERR_INVALID_ARG;
+    if (B == 0 || H == 0) return VLA_OK;
+    if (!q || !k || !v || !o || !log_decay || (!states && N > 0) || !aligned(q, 16) || !aligned(k, 16) ||
+        !aligned(v, 16) || !aligned(o, 16) || !aligned(log_decay, 4) || !aligned(states, 16) || !aligned(slots, 4) ||
+        !aligned(status, 16))
+        return VLA_ERR_INVALID_ARG;
+    const long long grid = (long long)B * H * (d / STEP_ROWS);
+    if (grid > 2147483647LL) return VLA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto* ds = static_cast<vla::DeviceStatus*>(status);
+    auto go = [&](auto tag, auto dim) {
+        using T = decltype(tag);
+        vla_decay_step_kernel<decltype(dim)::value, T><<<(unsigned)grid, STEP_THREADS, 0, s>>>(
+            static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), H, log_decay, scale, states,
+            N, slots, static_cast<T*>(o), ds);
+    };
+    auto pick = [&](auto tag) {
+        switch (d) {
+            case 32: go(tag, std::integral_constant<int, 32>{}); break;
+            case 64: go(tag, std::integral_constant<int, 64>{}); break;
+            case 96: go(tag, std::integral_constant<int, 96>{}); break;
+            default: go(tag, std::integral_constant<int, 128>{}); break;
+        }
+    };
+    if (dtype == VLA_BF16)
+        pick(__nv_bfloat16{});
+    else
+        pick(float{});
+    return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -607,6 +607,7 @@ vla_status vla_get_last_device_status(void* workspace, void* stream, int* detail
         detail[2] = h.token;
     }
     if (h.bits & vla::BIT_TIMEOUT) return VLA_ERR_TIMEOUT;
+    if (h.bits & vla_impl::kBitBadSlot) return VLA_ERR_BAD_SLOT;
     return VLA_ERR_NONFINITE;
 }
 
@@ -685,7 +686,8 @@ const char* vla_status_string(vla_status st) {
         case VLA_ERR_UNSUPPORTED: return "unsupported head dimension (use 32, 64, 96 or 128)";
         case VLA_ERR_CUDA: return "CUDA runtime error";
         case VLA_ERR_TIMEOUT: return "in-kernel wait timed out; outputs are invalid";
-        case VLA_ERR_NONFINITE: return "non-finite value in delta or the gate norm";
+        case VLA_ERR_NONFINITE: return "non-finite value in delta, the gate norm, an output or a state";
+        case VLA_ERR_BAD_SLOT: return "slot out of range or used twice";
         default: return "unknown status";
     }
 }

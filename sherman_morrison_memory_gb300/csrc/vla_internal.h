@@ -21,4 +21,7 @@ vla_status forward(const void* q, const void* k, const void* v, const void* u, v
 // record): with only this much, VLA_ALGO_AUTO never takes the segmented path.
 size_t status_bytes();
 
+// Status record bit of VLA_ERR_BAD_SLOT, beside those of vla_device.cuh.
+constexpr int kBitBadSlot = 4;
+
 }  // namespace vla_impl

@@ -1,0 +1,120 @@
+// vla_layer.cuh -- what the operators of include/vla_layer.h share: sequences
+// with strides, eight values of a row at a time, status bits, argument checks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+// vla_device.cuh defines this function with external linkage: it has another
+// name in this translation unit than in vla_forward.cu's
+#define mbar_wait_slow mbar_wait_slow_layer
+#include "vla_device.cuh"
+#include "vla_internal.h"
+#include "vla_layer.h"
+
+namespace vla_layer {
+
+constexpr int kRoleSlot = 4;
+
+// element strides of a [B, H, T, d] sequence; a dimension of length 1 has stride 0
+struct Seq {
+    char* p;
+    long long sb, sh, st;
+};
+
+template <typename T>
+__device__ __forceinline__ T* row_of(const Seq& s, int b, int h, long long t) {
+    return reinterpret_cast<T*>(s.p) + (b * s.sb + h * s.sh + t * s.st);
+}
+
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// exp(g n) for a whole number n >= 0: 1 for n = 0 also where g is -inf
+__device__ __forceinline__ float decay_pow(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
+
+// The pool entry of sequence b, or -1 for none: a negative slot, or, recorded
+// in the status, one out of range or (`unique`) one that an earlier sequence
+// of the call has. Called by a whole block, which gets one answer.
+__device__ __forceinline__ int slot_of(const int* slots, int b, int N, bool unique, vla::DeviceStatus* status) {
+    if (!slots) return b;
+    const int s = slots[b];
+    if (s < 0) return -1;
+    int bad = s >= N;
+    if (unique) {
+        for (int i = threadIdx.x; i < b; i += blockDim.x) bad |= slots[i] == s;
+        bad = __syncthreads_or(bad);
+    }
+    if (!bad) return s;
+    if (status && threadIdx.x == 0) vla::record_failure(status, vla_impl::kBitBadSlot, kRoleSlot, b, s);
+    return -1;
+}
+
+// ---- host side -----------------------------------------------------------
+
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool good_d(int d) { return d == 32 || d == 64 || d == 96 || d == 128; }
+inline bool good_dtype(vla_dtype t) { return t == VLA_F32 || t == VLA_BF16; }
+
+// sizes that every index of the kernels can hold
+inline bool good_sizes(int B, int H, int T) {
+    if (B < 0 || H < 0 || T < 0) return false;
+    const long long BH = (long long)B * H;
+    return BH <= 2147483647LL && (unsigned long long)BH * (unsigned long long)T <= (1ull << 48);
+}
+
+inline bool good_seq(const void* data, long long sb, long long sh, long long st, int B, int H, int T, int es) {
+    if (!data || !aligned(data, 16)) return false;
+    const long long lim = 1LL << 40;
+    const long long s[3] = {sb, sh, st};
+    const int n[3] = {B, H, T};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (s[i] <= 0 || s[i] >= lim || (s[i] * es) % 16 != 0)) return false;
+    return true;
+}
+inline bool good_seq(const vla_seq* s, int B, int H, int T, int es) {
+    return s && good_seq(s->data, s->stride_b, s->stride_h, s->stride_t, B, H, T, es);
+}
+inline bool good_seq(const vla_seq_out* s, int B, int H, int T, int es) {
+    return s && good_seq(s->data, s->stride_b, s->stride_h, s->stride_t, B, H, T, es);
+}
+template <typename S>
+inline Seq to_seq(const S* s, int B, int H, int T) {
+    return Seq{(char*)s->data, B > 1 ? s->stride_b : 0, H > 1 ? s->stride_h : 0, T > 1 ? s->stride_t : 0};
+}
+
+// SMs of the current device, asked once per device (152 where none answers)
+inline int sm_count() {
+    static int known[64] = {};
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+    if (known[dev]) return known[dev];
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+    return known[dev] = n;
+}
+
+}  // namespace vla_layer
