@@ -32,6 +32,7 @@ struct Role {
     int init_t;         // init holds S^T
     int reverse;        // against the order of time
     float w_in, w_st, k_st;
+    int map_a, map_b, map_c;  // of the tensor-core kernel's tensor maps
 };
 
 struct DecayArgs {

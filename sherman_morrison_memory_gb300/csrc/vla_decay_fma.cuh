@@ -41,7 +41,8 @@ __device__ __forceinline__ float dot4(float4 x, float4 y, float s) {
 template <int D, typename T, bool STATE>
 __global__ void __launch_bounds__(256, 1) vla_decay_fma_kernel(const __grid_constant__ DecayArgs p) {
     using L = FmaLay<D>;
-    extern __shared__ __align__(16) float sm[];
+    extern __shared__ __align__(16) float fma_sm[];
+    float* sm = fma_sm;
     const int tid = threadIdx.x;
     const int seg = blockIdx.x % p.nseg, bh = blockIdx.x / p.nseg, b = bh / p.H, h = bh % p.H;
     const Role& r = p.role[blockIdx.y];

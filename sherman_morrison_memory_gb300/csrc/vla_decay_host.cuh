@@ -7,6 +7,7 @@
 
 #include "vla_decay.cuh"
 #include "vla_decay_fma.cuh"
+#include "vla_decay_tc.cuh"
 
 namespace vla_layer {
 namespace {
@@ -122,52 +123,124 @@ __global__ void __launch_bounds__(STEP_THREADS) vla_decay_step_kernel(const T* _
 
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
-// The cut of a call with `heads` independent rows of blocks (roles x B x H)
-// into segments.
-void plan(long long heads, int T, int* nseg, int* seg_len) {
-    const long long want = 2LL * sm_count() / std::max(1LL, heads);
-    int n = (int)std::max(1LL, std::min<long long>(want, T / 256));
+// The cut of a call with `heads` independent runs of blocks (roles x B x H)
+// into segments. A cut costs a second pass over two of the three sequences, so
+// it is taken only where it at least halves a block's run: a whole number of
+// segments for every run within one wave of blocks, of 256 tokens at least.
+void plan(long long heads, int T, int d, vla_dtype dt, int* nseg, int* seg_len) {
+    const int occ = dt == VLA_BF16 && d > 64 ? 1 : 2;
+    const long long want = (long long)occ * sm_count() / std::max(1LL, heads);
+    const int n = (int)std::max(1LL, std::min<long long>(want, T / 256));
     const int len = ((T + n - 1) / n + 63) / 64 * 64;
     *seg_len = std::max(64, len);
     *nseg = std::max(1, (T + *seg_len - 1) / *seg_len);
 }
 
-template <int D, typename T>
-vla_status launch(DecayArgs& p, int roles, const ScanArgs& q, const DecayArgs& states, int state_roles, cudaStream_t s) {
-    const long long BH = (long long)p.B * p.H;
-    const long long grid = BH * p.nseg;
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+// Map of a bf16 sequence in boxes of 64 columns x 64 tokens; columns behind d
+// and tokens behind T read as zero.
+template <typename S>
+bool make_map(CUtensorMap* m, const S* s, int B, int H, int T, int d) {
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return false;
+    auto bytes = [](int n, long long st) { return (cuuint64_t)(n > 1 ? st * 2 : 16); };
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
+    const cuuint64_t strides[3] = {bytes(T, s->stride_t), bytes(H, s->stride_h), bytes(B, s->stride_b)};
+    const cuuint32_t box[4] = {64, 64, 1, 1}, one[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (void*)s->data, dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A call's launches: with segments, their own states, the scan over them, and
+// the outputs; else the outputs alone.
+struct Call {
+    DecayArgs main, states;  // states.role: the state roles
+    int roles, state_roles;
+    ScanArgs scan;
+    DecayMaps maps;
+};
+
+template <int D, bool TC, typename T>
+vla_status launch(const Call& c, cudaStream_t s) {
+    const long long BH = (long long)c.main.B * c.main.H;
+    const long long grid = BH * c.main.nseg * c.roles;
     if (grid > 2147483647LL || BH * (D * D / 256) > 2147483647LL) return VLA_ERR_INVALID_ARG;
-    using L = FmaLay<D>;
-    auto main = vla_decay_fma_kernel<D, T, false>;
-    auto own = vla_decay_fma_kernel<D, T, true>;
-    if (cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess ||
-        cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
-        return VLA_ERR_CUDA;
-    if (p.nseg > 1) {
-        own<<<dim3((unsigned)grid, state_roles), L::THREADS, L::SMEM, s>>>(states);
-        vla_decay_scan_kernel<D><<<dim3((unsigned)(BH * (D * D / 256)), state_roles), 256, 0, s>>>(p, q);
+    const unsigned blocks = (unsigned)(BH * c.main.nseg);
+    auto scan = [&] {
+        vla_decay_scan_kernel<D><<<dim3((unsigned)(BH * (D * D / 256)), c.state_roles), 256, 0, s>>>(c.main, c.scan);
+    };
+    if constexpr (TC) {
+        using L = TcLay<D>;
+        auto main = vla_decay_tc_kernel<D, false>;
+        auto own = vla_decay_tc_kernel<D, true>;
+        if (cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
+            return VLA_ERR_CUDA;
+        if (c.main.nseg > 1) {
+            own<<<blocks * c.state_roles, L::THREADS, L::SMEM, s>>>(c.states, c.maps, c.state_roles);
+            scan();
+        }
+        main<<<blocks * c.roles, L::THREADS, L::SMEM, s>>>(c.main, c.maps, c.roles);
+    } else {
+        using L = FmaLay<D>;
+        auto main = vla_decay_fma_kernel<D, T, false>;
+        auto own = vla_decay_fma_kernel<D, T, true>;
+        if (cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
+            return VLA_ERR_CUDA;
+        if (c.main.nseg > 1) {
+            own<<<dim3(blocks, c.state_roles), L::THREADS, L::SMEM, s>>>(c.states);
+            scan();
+        }
+        main<<<dim3(blocks, c.roles), L::THREADS, L::SMEM, s>>>(c.main);
     }
-    main<<<dim3((unsigned)grid, roles), L::THREADS, L::SMEM, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
 }
 
-template <typename T>
-vla_status launch_d(int d, DecayArgs& p, int roles, const ScanArgs& q, const DecayArgs& st, int state_roles,
-                    cudaStream_t s) {
+vla_status launch_call(const Call& c, int d, vla_dtype dt, cudaStream_t s) {
+    if (dt == VLA_BF16) {
+        switch (d) {
+            case 32: return launch<32, true, __nv_bfloat16>(c, s);
+            case 64: return launch<64, true, __nv_bfloat16>(c, s);
+            case 96: return launch<96, true, __nv_bfloat16>(c, s);
+            default: return launch<128, true, __nv_bfloat16>(c, s);
+        }
+    }
     switch (d) {
-        case 32: return launch<32, T>(p, roles, q, st, state_roles, s);
-        case 64: return launch<64, T>(p, roles, q, st, state_roles, s);
-        case 96: return launch<96, T>(p, roles, q, st, state_roles, s);
-        default: return launch<128, T>(p, roles, q, st, state_roles, s);
+        case 32: return launch<32, false, float>(c, s);
+        case 64: return launch<64, false, float>(c, s);
+        case 96: return launch<96, false, float>(c, s);
+        default: return launch<128, false, float>(c, s);
     }
 }
 
+// scratch of the larger of the two types' cuts, so that it need not be told the type
 size_t scratch_bytes_of(int B, int H, int T, int d, bool backward) {
     if (!good_sizes(B, H, T) || !good_d(d) || B == 0 || H == 0 || T == 0) return 0;
     const long long BH = (long long)B * H;
-    int nseg, len;
-    plan(BH * (backward ? 3 : 1), T, &nseg, &len);
-    return nseg > 1 ? (size_t)BH * nseg * (backward ? 2 : 1) * d * d * sizeof(float) : 0;
+    int most = 1;
+    for (vla_dtype dt : {VLA_F32, VLA_BF16}) {
+        int nseg, len;
+        plan(BH * (backward ? 3 : 1), T, d, dt, &nseg, &len);
+        most = std::max(most, nseg);
+    }
+    return most > 1 ? (size_t)BH * most * (backward ? 2 : 1) * d * d * sizeof(float) : 0;
 }
 
 vla_status copy_state(float* dst, const float* src, size_t n, cudaStream_t s) {
@@ -205,21 +278,24 @@ vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
         return VLA_ERR_INVALID_ARG;
     const size_t need = scratch_bytes_of(B, H, T, d, false);
     if (need && (!scratch || !aligned(scratch, 256) || scratch_bytes < need)) return VLA_ERR_INVALID_ARG;
-    DecayArgs p{};
+    Call c{};
+    DecayArgs& p = c.main;
     p.B = B, p.H = H, p.T = T;
     p.log_decay = log_decay;
     p.lengths = lengths;
     p.status = static_cast<vla::DeviceStatus*>(status);
     p.wait_ns = kWaitNs;
-    plan((long long)B * H, T, &p.nseg, &p.seg_len);
+    plan((long long)B * H, T, d, dtype, &p.nseg, &p.seg_len);
     p.seg = static_cast<float*>(scratch);
-    Role& r = p.role[0];
-    r = Role{to_seq(q, B, H, T), to_seq(k, B, H, T), to_seq(v, B, H, T), to_seq(o, B, H, T), S0, S_out, 0, 0, scale,
-             scale, 1.f};
-    const DecayArgs st = p;
-    ScanArgs sc{};
-    sc.role[0] = ScanRole{S0, S_out, 0, 0};
-    return dtype == VLA_BF16 ? launch_d<__nv_bfloat16>(d, p, 1, sc, st, 1, s) : launch_d<float>(d, p, 1, sc, st, 1, s);
+    p.role[0] = Role{to_seq(q, B, H, T), to_seq(k, B, H, T), to_seq(v, B, H, T), to_seq(o, B, H, T),
+                     S0, S_out, 0, 0, scale, scale, 1.f, 0, 1, 2};
+    c.states = p;
+    c.roles = c.state_roles = 1;
+    c.scan.role[0] = ScanRole{S0, S_out, 0, 0};
+    if (dtype == VLA_BF16 && (!make_map(&c.maps.m[0], q, B, H, T, d) || !make_map(&c.maps.m[1], k, B, H, T, d) ||
+                              !make_map(&c.maps.m[2], v, B, H, T, d) || !make_map(&c.maps.out[0], o, B, H, T, d)))
+        return VLA_ERR_CUDA;
+    return launch_call(c, d, dtype, s);
 }
 
 vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO,
@@ -246,26 +322,34 @@ vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
     const size_t need = scratch_bytes_of(B, H, T, d, true);
     if (need && (!scratch || !aligned(scratch, 256) || scratch_bytes < need)) return VLA_ERR_INVALID_ARG;
     const Seq Q = to_seq(q, B, H, T), K = to_seq(k, B, H, T), V = to_seq(v, B, H, T), G = to_seq(dO, B, H, T);
-    DecayArgs p{};
+    Call c{};
+    DecayArgs& p = c.main;
     p.B = B, p.H = H, p.T = T;
     p.log_decay = log_decay;
     p.lengths = lengths;
     p.status = static_cast<vla::DeviceStatus*>(status);
     p.wait_ns = kWaitNs;
-    plan(3LL * B * H, T, &p.nseg, &p.seg_len);
+    plan(3LL * B * H, T, d, dtype, &p.nseg, &p.seg_len);
     p.seg = static_cast<float*>(scratch);
-    p.role[0] = Role{G, V, K, to_seq(dq, B, H, T), S0, nullptr, 1, 0, scale, scale, 1.f};
-    p.role[1] = Role{V, G, Q, to_seq(dk, B, H, T), dS_T, nullptr, 1, 1, scale, 1.f, scale};
-    p.role[2] = Role{K, Q, G, to_seq(dv, B, H, T), dS_T, dS0, 0, 1, scale, 1.f, scale};
+    p.role[0] = Role{G, V, K, to_seq(dq, B, H, T), S0, nullptr, 1, 0, scale, scale, 1.f, 3, 2, 1};
+    p.role[1] = Role{V, G, Q, to_seq(dk, B, H, T), dS_T, nullptr, 1, 1, scale, 1.f, scale, 2, 3, 0};
+    p.role[2] = Role{K, Q, G, to_seq(dv, B, H, T), dS_T, dS0, 0, 1, scale, 1.f, scale, 1, 0, 3};
     // the segments' own states: those of dq's role and of dv's, which is dk's transposed
-    DecayArgs st = p;
-    st.role[1] = p.role[2];
+    c.states = p;
+    c.states.role[1] = p.role[2];
     p.seg_role[0] = 0, p.seg_role[1] = 1, p.seg_role[2] = 1;
     p.seg_t[1] = 1;
-    ScanArgs sc{};
-    sc.role[0] = ScanRole{S0, nullptr, 1, 0};
-    sc.role[1] = ScanRole{dS_T, dS0, 0, 1};
-    return dtype == VLA_BF16 ? launch_d<__nv_bfloat16>(d, p, 3, sc, st, 2, s) : launch_d<float>(d, p, 3, sc, st, 2, s);
+    c.roles = 3;
+    c.state_roles = 2;
+    c.scan.role[0] = ScanRole{S0, nullptr, 1, 0};
+    c.scan.role[1] = ScanRole{dS_T, dS0, 0, 1};
+    if (dtype == VLA_BF16 && (!make_map(&c.maps.m[0], q, B, H, T, d) || !make_map(&c.maps.m[1], k, B, H, T, d) ||
+                              !make_map(&c.maps.m[2], v, B, H, T, d) || !make_map(&c.maps.m[3], dO, B, H, T, d) ||
+                              !make_map(&c.maps.out[0], dq, B, H, T, d) ||
+                              !make_map(&c.maps.out[1], dk, B, H, T, d) ||
+                              !make_map(&c.maps.out[2], dv, B, H, T, d)))
+        return VLA_ERR_CUDA;
+    return launch_call(c, d, dtype, s);
 }
 
 vla_status vla_decay_step(const void* q, const void* k, const void* v, vla_dtype dtype, int B, int H, int d,
