@@ -54,28 +54,27 @@ struct TcLay {
     static constexpr int NST = 3;              // chunks in flight
     static constexpr int PARTS = 3;            // of the decayed b
     static constexpr int OCC = DP == 64 ? 2 : 1;
-    static constexpr int NT = DP == 64 ? 1 : 2;  // buffers of T
+    // buffers of T, of SC with OI behind it, and of P: one each where two blocks share an SM
+    static constexpr int NT = DP == 64 ? 1 : 2, NX = NT, NP = NT;
     static constexpr int THREADS = 512;
     // shared memory
     static constexpr int ST = 0;                           // [NST] a | b | c
     static constexpr int KW = ST + NST * 3 * TILE;         // [PARTS]
     static constexpr int P = KW + PARTS * TILE;
-    static constexpr int OUT = P + BOX;
+    static constexpr int OUT = P + NP * BOX;
     // weights of 64 each: the state to tokens, tokens to the state, pairs by
     // their lag. Tokens behind a chunk's end read into the next table and pairs
     // against the order of time into the one before; what they get is thrown away
     static constexpr int WO = OUT + TILE, WK = WO + 64 * 4, WP = WK + 64 * 4;
     static constexpr int BAR = WP + 64 * 4;
-    static constexpr int NBAR = 2 * NST + 2 * NT + 8;
+    static constexpr int NBAR = 2 * NST + 2 * NT + 11;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int SMEM = MISC + 16;
     static_assert((SMEM + 1024) * OCC <= 228 * 1024, "shared memory");
-    // TMEM columns; OI takes SC's place where two blocks share the SM's 512
-    static constexpr int T = 0, SB = T + NT * DP, SC = SB + DP / 2, OE = SC + 64;
-    static constexpr bool ALIAS = DP == 64;
-    static constexpr int OI = ALIAS ? SC : OE + 64;
+    // TMEM columns; OI takes SC's place once P is made of it
+    static constexpr int T = 0, SB = T + NT * DP, OE = SB + DP / 2, X = OE + 64;
     static constexpr int COLS = DP == 64 ? 256 : 512;
-    static_assert((ALIAS ? OE + 64 : OI + 64) <= COLS, "tensor memory");
+    static_assert(X + NX * 64 <= COLS, "tensor memory");
 };
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -121,6 +120,13 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int t, 
                  : "memory");
 }
 
+// true in one lane of a whole warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // two fp32 operations in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -130,10 +136,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
 }
-__device__ __forceinline__ float2 sub_bf16x2(float2 a, uint32_t h) {  // a minus the pair's values
-    return make_float2(a.x - __uint_as_float(h << 16), a.y - __uint_as_float(h & 0xFFFF0000u));
-}
-
 template <int D, bool STATE>
 __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
     vla_decay_tc_kernel(const __grid_constant__ DecayArgs p, const __grid_constant__ DecayMaps maps, int roles) {
@@ -143,14 +145,15 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
     const uint32_t sb = vla::smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
     uint64_t *full = bar, *empty = full + L::NST, *t_done = empty + L::NST, *t_free = t_done + L::NT;
-    uint64_t *sc_done = t_free + L::NT, *p_ready = sc_done + 1, *sb_ready = sc_done + 2, *oe_done = sc_done + 3,
-             *o_done = sc_done + 4, *o_free = sc_done + 5, *kw_full = sc_done + 6, *drained = sc_done + 7;
+    uint64_t *sc_done = t_free + L::NT, *o_done = sc_done + 2, *p_ready = sc_done + 4, *sb_ready = sc_done + 5,
+             *oe_done = sc_done + 6, *oe_free = sc_done + 7, *o_free = sc_done + 8, *kw_full = sc_done + 9,
+             *drained = sc_done + 10;
     float *WP = reinterpret_cast<float*>(sm + L::WP), *WK = reinterpret_cast<float*>(sm + L::WK),
           *WO = reinterpret_cast<float*>(sm + L::WO);
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC + 4);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int ri = blockIdx.x % roles, rest = blockIdx.x / roles;
     const int seg = rest % p.nseg, bh = rest / p.nseg, b = bh / p.H, h = bh % p.H;
     const Role& r = p.role[ri];
@@ -168,17 +171,17 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
         WO[tid] = r.w_st * decay_pow(g, rev ? down : up);
         WP[tid] = r.w_in * decay_pow(g, tid);
     }
-    for (int i = tid; i < L::BOX / 16; i += L::THREADS)  // the pairs that no chunk writes stay zero
+    for (int i = tid; i < L::NP * L::BOX / 16; i += L::THREADS)  // the pairs that no chunk writes stay zero
         *reinterpret_cast<uint4*>(sm + L::P + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     vla::fence_proxy_async_smem();
     if (tid == 0) {
         for (int i = 0; i < L::NST; ++i) vla::mbar_init(full + i, 1), vla::mbar_init(empty + i, 1);
         for (int i = 0; i < L::NT; ++i) vla::mbar_init(t_done + i, 1), vla::mbar_init(t_free + i, 8);
-        vla::mbar_init(sc_done, 1);
+        for (int i = 0; i < 2; ++i) vla::mbar_init(sc_done + i, 1), vla::mbar_init(o_done + i, 1);
         vla::mbar_init(p_ready, 2);
         vla::mbar_init(sb_ready, 8);
         vla::mbar_init(oe_done, 1);
-        vla::mbar_init(o_done, 1);
+        vla::mbar_init(oe_free, 4);
         vla::mbar_init(o_free, 4);
         vla::mbar_init(kw_full, 8);
         vla::mbar_init(drained, 1);
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
     vla::tc_fence_before();
     __syncthreads();
     vla::tc_fence_after();
-    const uint32_t tm = *tmem_ptr;
+    const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_ptr, 0);
     float2 bad = make_float2(0.f, 0.f);  // NaN once an output or a final state is not finite
     const float2 zero2 = make_float2(0.f, 0.f);
 
@@ -229,30 +232,40 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
                     vla::mbar_wait(full + i % L::NST, (i / L::NST) & 1, nullptr, p.wait_ns);
         }
     } else if (warp == 15) {  // ---- MMA
-        if (lane == 0) {
-            const uint32_t id_k = idesc_bf16(128, 64, 0, 0);    // SC, OE
-            const uint32_t id_oi = idesc_bf16(128, 64, 1, 0);
-            const uint32_t id_t = idesc_bf16(128, D, 1, 1);
-            constexpr uint32_t HALF = L::NB == 2 ? L::BOX : 0;  // second 64 rows of an A operand: the next box, or again
-            const uint64_t dk = desc_sw128(0, 16, 1024), dm = desc_sw128(0, HALF, 1024);
-            auto at = [](uint64_t d, uint32_t addr) { return d + (uint64_t)(addr >> 4); };
-            for (int m = 0; m < chunks; ++m) {
-                const int st = m % L::NST, tbuf = m % L::NT;
-                const uint32_t ta = sb + L::ST + st * 3 * L::TILE, tb = ta + L::TILE, tc = tb + L::TILE;
-                if (!wait(full + st, m / L::NST)) break;
-                if (!STATE) {
-                    if (L::ALIAS && m > 0 && !wait(o_free, m - 1)) break;
-                    vla::tc_fence_after();
+        // The whole warp runs the loop, so that operands stay in uniform
+        // registers, and one elected thread issues: issued under a test of the
+        // lane, each MMA took 100 cycles.
+        const bool one = elect_one();
+        const uint32_t id_k = idesc_bf16(128, 64, 0, 0);    // SC, OE
+        const uint32_t id_oi = idesc_bf16(128, 64, 1, 0);
+        const uint32_t id_t = idesc_bf16(128, D, 1, 1);
+        constexpr uint32_t HALF = L::NB == 2 ? L::BOX : 0;  // second 64 rows of an A operand: the next box, or again
+        const uint64_t dk = desc_sw128(0, 16, 1024), dm = desc_sw128(0, HALF, 1024);
+        auto at = [](uint64_t d, uint32_t addr) { return d + (uint64_t)(addr >> 4); };
+        auto pairs = [&](int m) {  // SC of chunk m
+            const uint32_t ta = sb + L::ST + (m % L::NST) * 3 * L::TILE;
+            if (!wait_warp(full + m % L::NST, m / L::NST)) return false;
+            if (m >= L::NX && !wait_warp(o_free, m - L::NX)) return false;
+            vla::tc_fence_after();
+            if (one) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k / 4) * L::BOX + (k % 4) * 32;
-                        mma_ss(tm + L::SC, at(dk, ta + off), at(dk, tb + off), id_k, k > 0);
-                    }
-                    vla::tc_commit(sc_done);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * L::BOX + (k % 4) * 32;
+                    mma_ss(tm + L::X + (m % L::NX) * 64, at(dk, ta + off), at(dk, ta + L::TILE + off), id_k, k > 0);
                 }
-                if (!wait(kw_full, m)) break;
-                if (m >= L::NT && !wait(t_free + tbuf, m / L::NT - 1)) break;
-                vla::tc_fence_after();
+                vla::tc_commit(sc_done + m % 2);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = STATE || L::NX == 1 || chunks == 0 || pairs(0);
+        for (int m = 0; ok && m < chunks; ++m) {
+            const int st = m % L::NST, tbuf = m % L::NT;
+            const uint32_t ta = sb + L::ST + st * 3 * L::TILE, tc = ta + 2 * L::TILE;
+            if (!wait_warp(kw_full, m)) break;
+            if (m >= L::NT && !wait_warp(t_free + tbuf, m / L::NT - 1)) break;
+            vla::tc_fence_after();
+            if (one) {
 #pragma unroll
                 for (int part = 0; part < L::PARTS; ++part)
 #pragma unroll
@@ -260,26 +273,38 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
                         mma_ss(tm + L::T + tbuf * L::DP, at(dm, tc + k * 2048),
                                at(dm, sb + L::KW + part * L::TILE + k * 2048), id_t, part > 0 || k > 0);
                 vla::tc_commit(t_done + tbuf);
-                if (!STATE) {
-                    if (!wait(sb_ready, m)) break;
-                    if (!L::ALIAS && m > 0 && !wait(o_free, m - 1)) break;
-                    vla::tc_fence_after();
+            }
+            __syncwarp();
+            if (!STATE) {
+                if (L::NX == 1 && !pairs(m)) break;
+                if (!wait_warp(sb_ready, m)) break;
+                if (m > 0 && !wait_warp(oe_free, m - 1)) break;
+                vla::tc_fence_after();
+                if (one) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         mma_ts(tm + L::OE, tm + L::SB + k * 8, at(dk, ta + (k / 4) * L::BOX + (k % 4) * 32), id_k, k > 0);
                     vla::tc_commit(oe_done);
-                    if (!wait(p_ready, m)) break;
-                    vla::tc_fence_after();
+                }
+                __syncwarp();
+                if (L::NX > 1 && m + 1 < chunks && !pairs(m + 1)) break;
+                if (!wait_warp(p_ready, m)) break;
+                vla::tc_fence_after();
+                if (one) {
 #pragma unroll
                     for (int k = 0; k < L::C / 16; ++k)
-                        mma_ss(tm + L::OI, at(dm, tc + k * 2048), at(dk, sb + L::P + k * 32), id_oi, k > 0);
-                    vla::tc_commit(o_done);
+                        mma_ss(tm + L::X + (m % L::NX) * 64, at(dm, tc + k * 2048),
+                               at(dk, sb + L::P + (m % L::NP) * L::BOX + k * 32), id_oi, k > 0);
+                    vla::tc_commit(o_done + m % 2);
                 }
-                vla::tc_commit(empty + st);
+                __syncwarp();
             }
-            vla::tc_commit(drained);  // what was issued has finished before the block frees its TMEM
-            vla::mbar_wait(drained, 0, nullptr, p.wait_ns);
+            if (one) vla::tc_commit(empty + st);
+            __syncwarp();
         }
+        if (one) vla::tc_commit(drained);  // what was issued has finished before the block frees its TMEM
+        __syncwarp();
+        vla::mbar_wait(drained, 0, nullptr, p.wait_ns);
     } else if (warp >= 12) {  // ---- P
         // Of the four 32 x 32 blocks of pairs the two on the diagonal are cut
         // by it, one is whole and one empty; a warp has two of them in a row.
@@ -288,11 +313,12 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
             const uint32_t lanes = (uint32_t)(rb * 32) << 16;
             const bool whole = rb == (rev ? 0 : 1);
             const uint32_t tri = rev ? ~((1u << lane) - 1u) : (2u << lane) - 1u;
-            unsigned char* row = sm + L::P + i * 128;
             for (int m = 0; m < chunks; ++m) {
                 const int n = min(L::C, sp.n - chunk0(m));
-                if (!wait_warp(sc_done, m)) break;
-                if (m > 0 && !wait_warp(o_done, m - 1)) break;  // P's last reader
+                if (!wait_warp(sc_done + m % 2, m / 2)) break;
+                const int was = m - L::NP;  // the chunk whose P was here: read by its OI
+                if (was >= 0 && !wait_warp(o_done + was % 2, was / 2)) break;
+                unsigned char* row = sm + L::P + (m % L::NP) * L::BOX + i * 128;
                 vla::tc_fence_after();
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk) {
@@ -305,7 +331,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
                     for (int q = 0; q < 2; ++q) {
                         float v[16];
                         __syncwarp();
-                        vla::tc_ld16(tm + lanes + L::SC + cb * 32 + q * 16, v);
+                        vla::tc_ld16(tm + lanes + L::X + (m % L::NX) * 64 + cb * 32 + q * 16, v);
                         vla::tc_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -369,20 +395,25 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
             unsigned char* tb = sm + L::ST + st * 3 * L::TILE + L::TILE;
             const float* w = WK + (rev ? 0 : L::C - n);
             auto part16 = [&](int o, int j) {
+                const uint4 raw = *reinterpret_cast<const uint4*>(tb + o);
+                const uint32_t y[4] = {raw.x, raw.y, raw.z, raw.w};
                 const bool in = j < n;
-                float y[8];
-                load8(reinterpret_cast<const __nv_bfloat16*>(tb + o), y);
                 const float wj = in ? w[j] : 0.f;
                 uint32_t u[3][4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float2 z = fma2(make_float2(y[2 * e], y[2 * e + 1]), make_float2(wj, wj), zero2);
-                    if (!in) z = zero2;
-                    u[0][e] = pack_bf16(z.x, z.y);
-                    z = sub_bf16x2(z, u[0][e]);
-                    u[1][e] = pack_bf16(z.x, z.y);
-                    z = sub_bf16x2(z, u[1][e]);
-                    u[2][e] = pack_bf16(z.x, z.y);
+                    // the leading eight bits of what is left, cut off, three times: nothing remains
+                    float2 z = fma2(make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xFFFF0000u)),
+                                    make_float2(wj, wj), zero2);
+                    if (n < L::C && !in) z = zero2;
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        u[k][e] = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
+                        if (k < 2)
+                            z = fma2(make_float2(__uint_as_float(__float_as_uint(z.x) & 0xFFFF0000u),
+                                                 __uint_as_float(__float_as_uint(z.y) & 0xFFFF0000u)),
+                                     make_float2(-1.f, -1.f), z);
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
@@ -450,35 +481,62 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
         const int i0 = L::DP == 64 ? (warp / 2) * 32 : 0;
         unsigned char* col = sm + L::OUT + (x / 64) * L::BOX + i0 * 128 + (x % 8) * 2;
         const int c16 = (x % 64) / 8;
+        uint32_t at8[8];  // of tokens i, i + 8, ...: their 16 bytes of the swizzled row
+#pragma unroll
+        for (int i = 0; i < 8; ++i) at8[i] = (uint32_t)((c16 ^ i) << 4);
         for (int m = 0; m < chunks; ++m) {
             const int c0 = chunk0(m), n = min(L::C, sp.n - c0);
-            if (!wait_warp(o_done, m)) break;
+            float2 y[NI / 2];
+            bool ok = wait_warp(oe_done, m);
+            if (ok) {
+                vla::tc_fence_after();
+                const float* w = WO + i0 + (rev ? L::C - n : 0);
+#pragma unroll
+                for (int q = 0; q < NI / 16; ++q) {
+                    float v[16];
+                    __syncwarp();
+                    vla::tc_ld16(tm + lanes + L::OE + i0 + q * 16, v);
+                    vla::tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int i = q * 16 + 2 * e;
+                        y[q * 8 + e] = fma2(make_float2(w[i], w[i + 1]), make_float2(v[2 * e], v[2 * e + 1]), zero2);
+                    }
+                }
+                vla::tc_fence_before();
+                arrive_warp(oe_free);
+                ok = wait_warp(o_done + m % 2, m / 2);
+            }
             if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            vla::named_bar(1, 128);  // the last chunk has left the buffer
+            // the last chunk has left the buffer; the four warps leave together if a wait ran out
+            if (vla::bar_red_or(1, 128, !ok)) break;
             vla::tc_fence_after();
-            const float* w = WO + i0 + (rev ? L::C - n : 0);
 #pragma unroll
             for (int q = 0; q < NI / 16; ++q) {
-                float u[16], v[16];
+                float v[16];
                 __syncwarp();
-                vla::tc_ld16(tm + lanes + L::OI + i0 + q * 16, u);
-                vla::tc_ld16(tm + lanes + L::OE + i0 + q * 16, v);
+                vla::tc_ld16(tm + lanes + L::X + (m % L::NX) * 64 + i0 + q * 16, v);
                 vla::tc_wait_ld();
-                if (q == NI / 16 - 1) {
-                    vla::tc_fence_before();
-                    arrive_warp(o_free);
-                }
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const int i = q * 16 + e;  // from i0
-                    float2 y = fma2(make_float2(w[i], w[i + 1]), make_float2(v[e], v[e + 1]), make_float2(u[e], u[e + 1]));
-                    if (i0 + i >= n) y.x = 0.f;
-                    if (i0 + i + 1 >= n) y.y = 0.f;
-                    bad = fma2(y, zero2, bad);
-                    const uint32_t z = pack_bf16(y.x, y.y);
-                    *reinterpret_cast<uint16_t*>(col + i * 128 + ((c16 ^ (i & 7)) << 4)) = (uint16_t)z;
-                    *reinterpret_cast<uint16_t*>(col + (i + 1) * 128 + ((c16 ^ ((i + 1) & 7)) << 4)) = (uint16_t)(z >> 16);
+                for (int e = 0; e < 8; ++e)
+                    y[q * 8 + e] = fma2(make_float2(1.f, 1.f), y[q * 8 + e], make_float2(v[2 * e], v[2 * e + 1]));
+            }
+            vla::tc_fence_before();
+            arrive_warp(o_free);
+            if (n < L::C) {
+#pragma unroll
+                for (int e = 0; e < NI / 2; ++e) {
+                    if (i0 + 2 * e >= n) y[e].x = 0.f;
+                    if (i0 + 2 * e + 1 >= n) y[e].y = 0.f;
                 }
+            }
+#pragma unroll
+            for (int e = 0; e < NI / 2; ++e) {
+                const int i = 2 * e;
+                bad = fma2(y[e], zero2, bad);
+                const uint32_t z = pack_bf16(y[e].x, y[e].y);
+                *reinterpret_cast<uint16_t*>(col + i * 128 + at8[i & 7]) = (uint16_t)z;
+                *reinterpret_cast<uint16_t*>(col + (i + 1) * 128 + at8[(i + 1) & 7]) = (uint16_t)(z >> 16);
             }
             vla::fence_proxy_async_smem();
             vla::named_bar(1, 128);
