@@ -8,31 +8,38 @@
 //   OE[x][i] = sum_y Sb[x][y] a_i[y],  Sb = bf16(S)     A from TMEM
 //   OI[x][i] = sum_j c_j[x] P[i][j]
 //   out_i    = OI[.][i] + w_st w^(i+1) OE[.][i]
-//   T[x][y]  = sum_j c_j[x] (k_st w^(n-1-j) b_j[y])
+//   T[x][y]  = sum_j (k_st w^(n-1-j) c_j[x]) b_j[y]     A from TMEM
 //   S[x][y]  = w^n S[x][y] + T[x][y]                    fp32, in registers
 //
 // All but SC have the state's rows x on the 128 TMEM lanes, so that S is added
-// up and turned into the A operand Sb by the lane's own threads, and only P
-// (64 x 64) and the decayed b go through shared memory. OI and OE are kept
-// apart because their weights would otherwise be one more rounding. The
-// decayed b is split in three bf16 parts, which hold its 24 bits: S is an fp32
+// up and turned into the A operand Sb by the lane's own threads. OI and OE are
+// kept apart because their weights would otherwise be one more rounding. The
+// decayed c is cut into three bf16 parts, which hold its 24 bits: S is an fp32
 // result (two parts left it 2e-6 off). P and Sb are rounded to bf16 once: o is
 // rounded to bf16 afterwards anyway, and a term meets only one of the two.
 //
-// d is padded to DP = 64 or 128 columns by TMA's zero fill. Where DP is 64 the
-// A operand repeats its 64 rows (stride 0 between its 64-row halves), so that
-// lanes 64-127 hold a copy and the output's four warps take half of the tokens
-// each. SC uses M = 128 with the upper 64 rows reading what follows the tile
-// in shared memory; nothing reads those lanes.
+// What bounds it: shared memory. Per chunk at d = 128 its 128 bytes a cycle
+// carry 48 KB of loads and 16 KB of results through TMA, and the operands that
+// the MMAs fetch. So the decayed c goes to TMEM, not to shared memory, from
+// ldmatrix's transposed fragments; SC and the outputs are read in fragments
+// (16x256b) that stmatrix writes in whole 16-byte rows; and the weights, which
+// in fragments depend on the lane alone, stay in registers.
 //
-// Warps: 0-3 output, 4-11 decayed b and S (half of the columns each), 12-13 P,
-// 14 TMA loads, 15 MMA. Every wait is bounded; one that runs out raises the
-// block's abort flag.
+// d is padded to DP = 64 or 128 columns by TMA's zero fill. Where DP is 64 the
+// A operands repeat their 64 rows (in shared memory by a stride of 0 between
+// the 64-row halves), so that lanes 64-127 hold a copy and the output's four
+// warps take half of the tokens each. SC uses M = 128 with the upper 64 rows
+// reading what follows the tile in shared memory; nothing reads those lanes.
+//
+// Warps: 0-3 output, 4-11 decayed c and S, 12-13 P, 14 TMA loads, 15 MMA.
+// Every wait is bounded; one that runs out raises the block's abort flag.
 //
 // STATE: only the segment's own state, from zero (b and c).
 #pragma once
 
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "vla_decay.cuh"
 
@@ -51,30 +58,31 @@ struct TcLay {
     static constexpr int NB = DP / 64;         // boxes of a tile
     static constexpr int BOX = C * 128;        // bytes
     static constexpr int TILE = NB * BOX;
-    static constexpr int NST = 3;              // chunks in flight
-    static constexpr int PARTS = 3;            // of the decayed b
+    static constexpr int NST = 4;              // chunks in flight
+    static constexpr int PARTS = 3;            // of the decayed c
     static constexpr int OCC = DP == 64 ? 2 : 1;
-    // buffers of T, of SC with OI behind it, and of P: one each where two blocks share an SM
-    static constexpr int NT = DP == 64 ? 1 : 2, NX = NT, NP = NT;
+    static constexpr int NCW = DP == 64 ? 1 : 2;  // buffers of the decayed c: one where two blocks share an SM
     static constexpr int THREADS = 512;
     // shared memory
     static constexpr int ST = 0;                           // [NST] a | b | c
-    static constexpr int KW = ST + NST * 3 * TILE;         // [PARTS]
-    static constexpr int P = KW + PARTS * TILE;
-    static constexpr int OUT = P + NP * BOX;
+    static constexpr int P = ST + NST * 3 * TILE;
+    static constexpr int OUT = P + BOX;
     // weights of 64 each: the state to tokens, tokens to the state, pairs by
     // their lag. Tokens behind a chunk's end read into the next table and pairs
     // against the order of time into the one before; what they get is thrown away
     static constexpr int WO = OUT + TILE, WK = WO + 64 * 4, WP = WK + 64 * 4;
     static constexpr int BAR = WP + 64 * 4;
-    static constexpr int NBAR = 2 * NST + 2 * NT + 11;
+    static constexpr int NBAR = 2 * NST + 11;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int SMEM = MISC + 16;
     static_assert((SMEM + 1024) * OCC <= 228 * 1024, "shared memory");
-    // TMEM columns; OI takes SC's place once P is made of it
-    static constexpr int T = 0, SB = T + NT * DP, OE = SB + DP / 2, X = OE + 64;
+    // TMEM columns. OI takes SC's place once P is made of it. Where two blocks
+    // share the SM's 512, T takes OE's once that is read.
+    static constexpr bool ALIAS = DP == 64;
+    static constexpr int SB = 0, CW = SB + DP / 2, OE = CW + NCW * PARTS * 32, X = OE + 64;
+    static constexpr int T = ALIAS ? OE : X + 64;
     static constexpr int COLS = DP == 64 ? 256 : 512;
-    static_assert(X + NX * 64 <= COLS, "tensor memory");
+    static_assert((ALIAS ? X + 64 : T + DP) <= COLS, "tensor memory");
 };
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -108,6 +116,57 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         "l"(map), "r"(x), "r"(t), "r"(h), "r"(b), "r"(vla::smem_u32(bar))
         : "memory");
 }
+// Fragments: of 16 lanes, thread l holds rows l / 4 and l / 4 + 8. ld_frag:
+// columns 8 k + 2 (l % 4) + {0, 1} of both rows in v[4 k ..]; st_frag8: column
+// 4 k + l % 4 of the two rows in v[2 k], v[2 k + 1].
+__device__ __forceinline__ void ld_frag64(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void ld_frag32(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void st_frag8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// four 8 x 8 blocks of 16-bit values: lane l gives the address of row l % 8 of
+// block l / 8; _t: rows and columns swapped on the way
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void stmatrix4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
 __device__ __forceinline__ void st_cols8(uint32_t taddr, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -136,6 +195,16 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
     return d;
 }
+// A wait that did not end at once, for at most p.wait_ns: false, recorded and
+// the abort flag raised, if it or another of the block's ran out.
+__device__ __noinline__ bool wait_on(uint64_t* w, uint32_t parity, volatile int* abort_flag, unsigned long long ns,
+                                     vla::DeviceStatus* status, int role, int bh) {
+    if (vla::mbar_wait_slow(w, parity, (const volatile int*)abort_flag, ns)) return true;
+    if (*abort_flag == 0 && status) vla::record_failure(status, vla::BIT_TIMEOUT, role, bh, 0);
+    *abort_flag = 1;
+    return false;
+}
+
 template <int D, bool STATE>
 __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
     vla_decay_tc_kernel(const __grid_constant__ DecayArgs p, const __grid_constant__ DecayMaps maps, int roles) {
@@ -144,10 +213,9 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
     unsigned char* sm = tc_sm;
     const uint32_t sb = vla::smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
-    uint64_t *full = bar, *empty = full + L::NST, *t_done = empty + L::NST, *t_free = t_done + L::NT;
-    uint64_t *sc_done = t_free + L::NT, *o_done = sc_done + 2, *p_ready = sc_done + 4, *sb_ready = sc_done + 5,
-             *oe_done = sc_done + 6, *oe_free = sc_done + 7, *o_free = sc_done + 8, *kw_full = sc_done + 9,
-             *drained = sc_done + 10;
+    uint64_t *full = bar, *empty = full + L::NST, *cw_full = empty + L::NST, *p_ready = cw_full + 2,
+             *sc_done = cw_full + 3, *o_done = cw_full + 4, *sb_ready = cw_full + 5, *oe_done = cw_full + 6,
+             *oe_free = cw_full + 7, *o_free = cw_full + 8, *t_done = cw_full + 9, *drained = cw_full + 10;
     float *WP = reinterpret_cast<float*>(sm + L::WP), *WK = reinterpret_cast<float*>(sm + L::WK),
           *WO = reinterpret_cast<float*>(sm + L::WO);
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::MISC);
@@ -171,19 +239,21 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
         WO[tid] = r.w_st * decay_pow(g, rev ? down : up);
         WP[tid] = r.w_in * decay_pow(g, tid);
     }
-    for (int i = tid; i < L::NP * L::BOX / 16; i += L::THREADS)  // the pairs that no chunk writes stay zero
+    for (int i = tid; i < L::BOX / 16; i += L::THREADS)  // the pairs that no chunk writes stay zero
         *reinterpret_cast<uint4*>(sm + L::P + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     vla::fence_proxy_async_smem();
     if (tid == 0) {
         for (int i = 0; i < L::NST; ++i) vla::mbar_init(full + i, 1), vla::mbar_init(empty + i, 1);
-        for (int i = 0; i < L::NT; ++i) vla::mbar_init(t_done + i, 1), vla::mbar_init(t_free + i, 8);
-        for (int i = 0; i < 2; ++i) vla::mbar_init(sc_done + i, 1), vla::mbar_init(o_done + i, 1);
+        // two, by the chunk's parity: a warp may be a chunk ahead of the others here
+        for (int i = 0; i < 2; ++i) vla::mbar_init(cw_full + i, 8);
+        vla::mbar_init(sc_done, 1);
+        vla::mbar_init(o_done, 1);
         vla::mbar_init(p_ready, 2);
         vla::mbar_init(sb_ready, 8);
         vla::mbar_init(oe_done, 1);
         vla::mbar_init(oe_free, 4);
         vla::mbar_init(o_free, 4);
-        vla::mbar_init(kw_full, 8);
+        vla::mbar_init(t_done, 1);
         vla::mbar_init(drained, 1);
         *abort_flag = 0;
         vla::fence_mbar_init();
@@ -198,10 +268,8 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
 
     // bounded wait: false once this or another wait of the block has run out
     auto wait = [&](uint64_t* w, uint32_t parity) {
-        if (vla::mbar_wait(w, parity & 1, (const volatile int*)abort_flag, p.wait_ns)) return true;
-        if (*abort_flag == 0 && p.status) vla::record_failure(p.status, vla::BIT_TIMEOUT, warp / 4, bh, sp.t0);
-        *abort_flag = 1;
-        return false;
+        return vla::mbar_try_wait(w, parity & 1) ||
+               wait_on(w, parity & 1, abort_flag, p.wait_ns, p.status, warp / 4, bh);
     };
     auto wait_warp = [&](uint64_t* w, uint32_t parity) { return __all_sync(0xffffffffu, wait(w, parity)) != 0; };
     auto arrive_warp = [&](uint64_t* w) {  // one arrival a warp
@@ -238,119 +306,153 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
         const bool one = elect_one();
         const uint32_t id_k = idesc_bf16(128, 64, 0, 0);    // SC, OE
         const uint32_t id_oi = idesc_bf16(128, 64, 1, 0);
-        const uint32_t id_t = idesc_bf16(128, D, 1, 1);
+        const uint32_t id_t = idesc_bf16(128, D, 0, 1);
         constexpr uint32_t HALF = L::NB == 2 ? L::BOX : 0;  // second 64 rows of an A operand: the next box, or again
         const uint64_t dk = desc_sw128(0, 16, 1024), dm = desc_sw128(0, HALF, 1024);
         auto at = [](uint64_t d, uint32_t addr) { return d + (uint64_t)(addr >> 4); };
-        auto pairs = [&](int m) {  // SC of chunk m
-            const uint32_t ta = sb + L::ST + (m % L::NST) * 3 * L::TILE;
-            if (!wait_warp(full + m % L::NST, m / L::NST)) return false;
-            if (m >= L::NX && !wait_warp(o_free, m - L::NX)) return false;
+        auto tile = [&](int i) { return sb + L::ST + i * 3 * L::TILE; };
+        auto pairs = [&](int m, int i) {  // SC of chunk m, in stage i
+            const uint32_t ta = tile(i);
+            if (!wait_warp(full + i, m / L::NST)) return false;
+            if (m > 0 && !wait_warp(o_free, m - 1)) return false;
             vla::tc_fence_after();
             if (one) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = (k / 4) * L::BOX + (k % 4) * 32;
-                    mma_ss(tm + L::X + (m % L::NX) * 64, at(dk, ta + off), at(dk, ta + L::TILE + off), id_k, k > 0);
+                    mma_ss(tm + L::X, at(dk, ta + off), at(dk, ta + L::TILE + off), id_k, k > 0);
                 }
-                vla::tc_commit(sc_done + m % 2);
+                vla::tc_commit(sc_done);
             }
             __syncwarp();
             return true;
         };
-        bool ok = STATE || L::NX == 1 || chunks == 0 || pairs(0);
-        for (int m = 0; ok && m < chunks; ++m) {
-            const int st = m % L::NST, tbuf = m % L::NT;
-            const uint32_t ta = sb + L::ST + st * 3 * L::TILE, tc = ta + 2 * L::TILE;
-            if (!wait_warp(kw_full, m)) break;
-            if (m >= L::NT && !wait_warp(t_free + tbuf, m / L::NT - 1)) break;
+        auto from_state = [&](int m, int i) {  // OE
+            if (!wait_warp(sb_ready, m)) return false;
+            if (m > 0 && !wait_warp(oe_free, m - 1)) return false;
+            if (!wait_warp(full + i, m / L::NST)) return false;
+            vla::tc_fence_after();
+            if (one) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ts(tm + L::OE, tm + L::SB + k * 8, at(dk, tile(i) + (k / 4) * L::BOX + (k % 4) * 32), id_k, k > 0);
+                vla::tc_commit(oe_done);
+            }
+            __syncwarp();
+            return true;
+        };
+        auto to_state = [&](int m, int i) {  // T, whose last reader is done with it when it publishes the state
+            if (STATE && (!wait_warp(full + i, m / L::NST) || !wait_warp(sb_ready, m))) return false;
+            if (!wait_warp(cw_full + m % 2, m / 2)) return false;
+            const uint32_t cw = tm + L::CW + (m % L::NCW) * L::PARTS * 32;
+            if (!STATE && L::ALIAS && !wait_warp(oe_free, m)) return false;
             vla::tc_fence_after();
             if (one) {
 #pragma unroll
                 for (int part = 0; part < L::PARTS; ++part)
 #pragma unroll
                     for (int k = 0; k < L::C / 16; ++k)
-                        mma_ss(tm + L::T + tbuf * L::DP, at(dm, tc + k * 2048),
-                               at(dm, sb + L::KW + part * L::TILE + k * 2048), id_t, part > 0 || k > 0);
-                vla::tc_commit(t_done + tbuf);
+                        mma_ts(tm + L::T, cw + part * 32 + k * 8, at(dm, tile(i) + L::TILE + k * 2048), id_t,
+                               part > 0 || k > 0);
+                vla::tc_commit(t_done);
             }
             __syncwarp();
-            if (!STATE) {
-                if (L::NX == 1 && !pairs(m)) break;
-                if (!wait_warp(sb_ready, m)) break;
-                if (m > 0 && !wait_warp(oe_free, m - 1)) break;
-                vla::tc_fence_after();
-                if (one) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_ts(tm + L::OE, tm + L::SB + k * 8, at(dk, ta + (k / 4) * L::BOX + (k % 4) * 32), id_k, k > 0);
-                    vla::tc_commit(oe_done);
-                }
-                __syncwarp();
-                if (L::NX > 1 && m + 1 < chunks && !pairs(m + 1)) break;
-                if (!wait_warp(p_ready, m)) break;
+            return true;
+        };
+        auto chunk = [&](int m, int i) {
+            if (STATE) {
+                if (!to_state(m, i)) return false;
+            } else {
+                if (!pairs(m, i) || !from_state(m, i) || !to_state(m, i)) return false;
+                if (!wait_warp(p_ready, m)) return false;
                 vla::tc_fence_after();
                 if (one) {
 #pragma unroll
                     for (int k = 0; k < L::C / 16; ++k)
-                        mma_ss(tm + L::X + (m % L::NX) * 64, at(dm, tc + k * 2048),
-                               at(dk, sb + L::P + (m % L::NP) * L::BOX + k * 32), id_oi, k > 0);
-                    vla::tc_commit(o_done + m % 2);
+                        mma_ss(tm + L::X, at(dm, tile(i) + 2 * L::TILE + k * 2048),
+                               at(dk, sb + L::P + k * 32), id_oi, k > 0);
+                    vla::tc_commit(o_done);
                 }
                 __syncwarp();
             }
-            if (one) vla::tc_commit(empty + st);
+            if (one) vla::tc_commit(empty + i);
             __syncwarp();
-        }
+            return true;
+        };
+        bool ok = true;
+        for (int m = 0; ok && m < chunks; ++m) ok = chunk(m, m % L::NST);
         if (one) vla::tc_commit(drained);  // what was issued has finished before the block frees its TMEM
         __syncwarp();
         vla::mbar_wait(drained, 0, nullptr, p.wait_ns);
     } else if (warp >= 12) {  // ---- P
-        // Of the four 32 x 32 blocks of pairs the two on the diagonal are cut
-        // by it, one is whole and one empty; a warp has two of them in a row.
+        // In blocks of 8 x 8 pairs: those of the later half of pairs are never
+        // written and stay zero, those on the diagonal are cut by it. A warp
+        // has 32 rows, 16 at a time; the weights depend on the blocks' distance.
         if (!STATE) {
-            const int rb = warp - 12, i = rb * 32 + lane;
-            const uint32_t lanes = (uint32_t)(rb * 32) << 16;
-            const bool whole = rb == (rev ? 0 : 1);
-            const uint32_t tri = rev ? ~((1u << lane) - 1u) : (2u << lane) - 1u;
-            for (int m = 0; m < chunks; ++m) {
-                const int n = min(L::C, sp.n - chunk0(m));
-                if (!wait_warp(sc_done + m % 2, m / 2)) break;
-                const int was = m - L::NP;  // the chunk whose P was here: read by its OI
-                if (was >= 0 && !wait_warp(o_done + was % 2, was / 2)) break;
-                unsigned char* row = sm + L::P + (m % L::NP) * L::BOX + i * 128;
-                vla::tc_fence_after();
+            const int lr = lane >> 2, lc = 2 * (lane & 3);
+            auto body = [&](auto rbc, auto revc) {
+                constexpr int RB = decltype(rbc)::value;
+                constexpr bool REV = decltype(revc)::value;
+                float2 w[8];
 #pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
-                    if (blk == 1 && !whole) break;
-                    const int cb = blk == 0 ? rb : 1 - rb;
-                    uint32_t mask = blk == 0 ? tri : 0xFFFFFFFFu;
-                    if (n < cb * 32 + 32) mask &= n > cb * 32 ? (1u << (n - cb * 32)) - 1u : 0u;
-                    const float* w = rev ? WP + (cb * 32 - i) : WP + (i - cb * 32);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float v[16];
-                        __syncwarp();
-                        vla::tc_ld16(tm + lanes + L::X + (m % L::NX) * 64 + cb * 32 + q * 16, v);
-                        vla::tc_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int j = q * 16 + e;
-                            v[e] = (mask >> j) & 1 ? v[e] * (rev ? w[j] : w[-j]) : 0.f;
-                        }
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            *reinterpret_cast<uint4*>(row + (((cb * 4 + q * 2 + c) ^ (i & 7)) << 4)) =
-                                make_uint4(pack_bf16(v[c * 8], v[c * 8 + 1]), pack_bf16(v[c * 8 + 2], v[c * 8 + 3]),
-                                           pack_bf16(v[c * 8 + 4], v[c * 8 + 5]), pack_bf16(v[c * 8 + 6], v[c * 8 + 7]));
-                    }
+                for (int q = 0; q < 8; ++q) {
+                    const int lag = 8 * q + (REV ? lc - lr : lr - lc);
+                    w[q] = make_float2(WP[lag], WP[REV ? lag + 1 : lag - 1]);
                 }
-                vla::tc_fence_before();
-                vla::fence_proxy_async_smem();
-                arrive_warp(p_ready);
-            }
+                const bool in0 = REV ? lc >= lr : lc <= lr, in1 = REV ? lc + 1 >= lr : lc + 1 <= lr;
+                // rows of the blocks (r, k), (r + 1, k), (r, k + 1), (r + 1, k + 1)
+                const int row8 = ((lane >> 3) & 1) * 8 + (lane & 7), kk = lane >> 4;
+                for (int m = 0; m < chunks; ++m) {
+                    const int n = min(L::C, sp.n - chunk0(m));
+                    if (!wait_warp(sc_done, m)) return;  // behind OI of chunk m - 1, P's last reader
+                    vla::tc_fence_after();
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int r = RB * 4 + hh * 2;  // first of two rows of blocks
+                        float v[32];
+                        __syncwarp();
+                        ld_frag64(tm + ((uint32_t)(RB * 32 + hh * 16) << 16) + L::X, v);
+                        vla::tc_wait_ld();
+                        const uint32_t dst = sb + L::P + (r * 8 + row8) * 128;
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2) {
+                            if (REV ? k < r : k > r) continue;
+                            uint32_t u[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int kb = k + e / 2, dist = REV ? kb - (r + e % 2) : r + e % 2 - kb;
+                                if (dist < 0) {
+                                    u[e] = 0u;
+                                    continue;
+                                }
+                                float2 z = fma2(make_float2(v[kb * 4 + (e % 2) * 2], v[kb * 4 + (e % 2) * 2 + 1]), w[dist], zero2);
+                                if (dist == 0) {
+                                    if (!in0) z.x = 0.f;
+                                    if (!in1) z.y = 0.f;
+                                }
+                                if (REV && n < L::C) {
+                                    if (kb * 8 + lc >= n) z.x = 0.f;
+                                    if (kb * 8 + lc + 1 >= n) z.y = 0.f;
+                                }
+                                u[e] = pack_bf16(z.x, z.y);
+                            }
+                            stmatrix4(dst + (((k + kk) ^ (lane & 7)) << 4), u[0], u[1], u[2], u[3]);
+                        }
+                    }
+                    vla::tc_fence_before();
+                    vla::fence_proxy_async_smem();
+                    arrive_warp(p_ready);
+                }
+            };
+            using std::integral_constant;
+            if (warp == 12)
+                rev ? body(integral_constant<int, 0>{}, integral_constant<bool, true>{})
+                    : body(integral_constant<int, 0>{}, integral_constant<bool, false>{});
+            else
+                rev ? body(integral_constant<int, 1>{}, integral_constant<bool, true>{})
+                    : body(integral_constant<int, 1>{}, integral_constant<bool, false>{});
         }
-    } else if (warp >= 4) {  // ---- the decayed b in parts, and S
+    } else if (warp >= 4) {  // ---- the decayed c in parts, and S
         constexpr int HC = D / 2;  // columns of S a thread holds
         const int id = tid - 128, half = id / 128, quad = warp & 3;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
@@ -373,75 +475,90 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
                                   : *reinterpret_cast<const float2*>(init + x * D + y);
             }
         }
-        auto publish = [&] {  // Sb = bf16(S)
+        auto publish = [&] {  // Sb = bf16(S); T has been read
+            if (!STATE) {
 #pragma unroll
-            for (int q = 0; q < HC / 16; ++q) {
-                uint32_t u[8];
+                for (int q = 0; q < HC / 16; ++q) {
+                    uint32_t u[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] = pack_bf16(S[q * 8 + e].x, S[q * 8 + e].y);
-                __syncwarp();
-                st_cols8(tm + lanes + L::SB + half * (HC / 2) + q * 8, u);
+                    for (int e = 0; e < 8; ++e) u[e] = pack_bf16(S[q * 8 + e].x, S[q * 8 + e].y);
+                    __syncwarp();
+                    st_cols8(tm + lanes + L::SB + half * (HC / 2) + q * 8, u);
+                }
+                vla::tc_wait_st();
             }
-            vla::tc_wait_st();
             vla::tc_fence_before();
             arrive_warp(sb_ready);
         };
-        // Chunk m's b (rows behind its end cleared there and in c), 16 bytes a
-        // thread at a time: whole boxes of 64 columns, then a half box where d
-        // ends in one.
+        const int j0 = half * 32 + 2 * (lane & 3);  // this lane's tokens: j0 + 8 k + {0, 1}
+        // the row of c that this lane addresses for ldmatrix: blocks (x, j), (x + 8, j), (x, j + 8), (x + 8, j + 8)
+        const int xb = (quad * 32) & (L::DP - 1);
+        const uint32_t src = (xb / 64) * L::BOX + (half * 32 + (lane >> 4) * 8 + (lane & 7)) * 128;
+        const int chunk16 = (xb % 64) / 8 + ((lane >> 3) & 1);
+        // Chunk m's c, decayed to the chunk's end, for this warp's 32 rows and
+        // 32 tokens; rows behind the chunk's end cleared in b and c.
         auto decayed = [&](int m) {
             const int st = m % L::NST, n = min(L::C, sp.n - chunk0(m));
             if (!wait_warp(full + st, m / L::NST)) return false;
-            unsigned char* tb = sm + L::ST + st * 3 * L::TILE + L::TILE;
-            const float* w = WK + (rev ? 0 : L::C - n);
-            auto part16 = [&](int o, int j) {
-                const uint4 raw = *reinterpret_cast<const uint4*>(tb + o);
-                const uint32_t y[4] = {raw.x, raw.y, raw.z, raw.w};
-                const bool in = j < n;
-                const float wj = in ? w[j] : 0.f;
-                uint32_t u[3][4];
+            const uint32_t tc = L::ST + st * 3 * L::TILE + 2 * L::TILE;
+            const float* w = WK + j0 + (rev ? 0 : L::C - n);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // the leading eight bits of what is left, cut off, three times: nothing remains
-                    float2 z = fma2(make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xFFFF0000u)),
-                                    make_float2(wj, wj), zero2);
-                    if (n < L::C && !in) z = zero2;
+            for (int hh = 0; hh < 2; ++hh) {
+                uint32_t y[8];
+                float2 z[8];
+                __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        u[k][e] = __byte_perm(__float_as_uint(z.x), __float_as_uint(z.y), 0x7632);
-                        if (k < 2)
-                            z = fma2(make_float2(__uint_as_float(__float_as_uint(z.x) & 0xFFFF0000u),
-                                                 __uint_as_float(__float_as_uint(z.y) & 0xFFFF0000u)),
-                                     make_float2(-1.f, -1.f), z);
+                for (int k = 0; k < 2; ++k)
+                    ldmatrix4_t(sb + tc + src + k * 2048 + (((chunk16 + 2 * hh) ^ (lane & 7)) << 4), y[4 * k], y[4 * k + 1],
+                                y[4 * k + 2], y[4 * k + 3]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = 8 * (e / 2);
+                    z[e] = fma2(make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xFFFF0000u)),
+                                make_float2(w[j], w[j + 1]), zero2);
+                    if (n < L::C) {
+                        if (j0 + j >= n) z[e].x = 0.f;
+                        if (j0 + j + 1 >= n) z[e].y = 0.f;
                     }
                 }
+                // the leading eight bits of what is left, cut off, three times: nothing remains
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    *reinterpret_cast<uint4*>(sm + L::KW + k * L::TILE + o) = make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
-            };
+                for (int k = 0; k < 3; ++k) {
+                    uint32_t u[8];
 #pragma unroll
-            for (int it = 0; it < (D / 64) * 2; ++it) part16(it * 4096 + id * 16, (it & 1) * 32 + id / 8);
-            if constexpr (D % 64 != 0) {
-                const int j = id / 4;
-                part16((D / 64) * L::BOX + j * 128 + (((id & 3) ^ (j & 7)) << 4), j);
+                    for (int e = 0; e < 8; ++e) {
+                        u[e] = __byte_perm(__float_as_uint(z[e].x), __float_as_uint(z[e].y), 0x7632);
+                        if (k < 2)
+                            z[e] = fma2(make_float2(__uint_as_float(__float_as_uint(z[e].x) & 0xFFFF0000u),
+                                                    __uint_as_float(__float_as_uint(z[e].y) & 0xFFFF0000u)),
+                                        make_float2(-1.f, -1.f), z[e]);
+                    }
+                    st_frag8(tm + lanes + ((uint32_t)(hh * 16) << 16) + L::CW + (m % L::NCW) * L::PARTS * 32 + k * 32 + half * 16, u);
+                }
             }
-            if (n < L::C)
+            if (n < L::C) {
                 for (int o = n * 128 + id * 16; o < L::BOX; o += 256 * 16)
 #pragma unroll
-                    for (int k = 0; k < L::NB; ++k)
-                        *reinterpret_cast<uint4*>(tb + L::TILE + k * L::BOX + o) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int k = 0; k < L::NB; ++k) {
+                        *reinterpret_cast<uint4*>(sm + tc + k * L::BOX + o) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(sm + tc - L::TILE + k * L::BOX + o) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+            }
+            vla::tc_wait_st();
+            vla::tc_fence_before();
             vla::fence_proxy_async_smem();
-            arrive_warp(kw_full);
+            arrive_warp(cw_full + m % 2);
             return true;
         };
         bool ok = true;
-        if (!STATE && chunks > 0) publish();
-        if (chunks > 0) ok = decayed(0);
-        int m = 0;
-        for (; ok && m < chunks; ++m) {
-            const int tbuf = m % L::NT;
-            if (!(ok = wait_warp(t_done + tbuf, m / L::NT))) break;
-            if (m + 1 < chunks && !(ok = decayed(m + 1))) break;
+        if (chunks > 0) {
+            publish();
+            ok = decayed(0);
+        }
+        for (int m = 0; ok && m < chunks; ++m) {
+            // the buffer's last reader, T of chunk m - 1, is done
+            if (L::NCW > 1 && m + 1 < chunks && !(ok = decayed(m + 1))) break;
+            if (!(ok = wait_warp(t_done, m))) break;
             vla::tc_fence_after();
             const float wn = decay_pow(g, min(L::C, sp.n - chunk0(m)));
             const float2 w2 = make_float2(wn, wn);
@@ -449,18 +566,18 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
             for (int q = 0; q < HC / 16; ++q) {
                 float v[16];
                 __syncwarp();
-                vla::tc_ld16(tm + lanes + L::T + tbuf * L::DP + half * HC + q * 16, v);
+                vla::tc_ld16(tm + lanes + L::T + half * HC + q * 16, v);
                 vla::tc_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) S[q * 8 + e] = fma2(w2, S[q * 8 + e], make_float2(v[2 * e], v[2 * e + 1]));
             }
-            vla::tc_fence_before();
-            arrive_warp(t_free + tbuf);
-            if (!STATE && m + 1 < chunks) {
+            if (m + 1 == chunks) break;
+            if (!STATE) {
                 if (!(ok = wait_warp(oe_done, m))) break;  // Sb's last reader
                 vla::tc_fence_after();
-                publish();
             }
+            publish();
+            if (L::NCW == 1) ok = decayed(m + 1);
         }
         float* fin = STATE ? p.seg + (((size_t)ri * p.B * p.H + bh) * p.nseg + seg) * D * D
                            : (p.nseg > 1 || !r.fin ? nullptr : r.fin + (size_t)bh * D * D);
@@ -474,69 +591,89 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
             }
         }
     } else if (!STATE) {  // ---- output
-        const uint32_t lanes = (uint32_t)warp * 32 << 16;
-        const int x = (warp * 32 + lane) & (L::DP - 1);
         // where the lanes hold the rows twice, each copy's warps take half of the tokens
-        constexpr int NI = L::DP == 64 ? 32 : 64;
+        constexpr int NI = L::DP == 64 ? 32 : 64, NR = NI / 2;  // tokens; values a thread has of 16 rows
         const int i0 = L::DP == 64 ? (warp / 2) * 32 : 0;
-        unsigned char* col = sm + L::OUT + (x / 64) * L::BOX + i0 * 128 + (x % 8) * 2;
-        const int c16 = (x % 64) / 8;
-        uint32_t at8[8];  // of tokens i, i + 8, ...: their 16 bytes of the swizzled row
+        const int lc = 2 * (lane & 3);
+        const int xb = (warp * 32) & (L::DP - 1);
+        // the row of the output that this lane addresses for stmatrix: blocks (x, i), (x + 8, i), (x, i + 8), (x + 8, i + 8)
+        const uint32_t dst = sb + L::OUT + (xb / 64) * L::BOX + (i0 + (lane >> 4) * 8 + (lane & 7)) * 128;
+        const int chunk16 = (xb % 64) / 8 + ((lane >> 3) & 1);
+        float2 wo[NI / 8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) at8[i] = (uint32_t)((c16 ^ i) << 4);
+        for (int k = 0; k < NI / 8; ++k) wo[k] = *reinterpret_cast<const float2*>(WO + i0 + lc + 8 * k);
+        auto load = [&](uint32_t col, int hh, float (&v)[NR]) {
+            const uint32_t at = tm + ((uint32_t)(warp * 32 + hh * 16) << 16) + col + i0;
+            __syncwarp();
+            if constexpr (NI == 64)
+                ld_frag64(at, v);
+            else
+                ld_frag32(at, v);
+        };
         for (int m = 0; m < chunks; ++m) {
             const int c0 = chunk0(m), n = min(L::C, sp.n - c0);
-            float2 y[NI / 2];
+            float oe[2][NR];
             bool ok = wait_warp(oe_done, m);
             if (ok) {
                 vla::tc_fence_after();
-                const float* w = WO + i0 + (rev ? L::C - n : 0);
-#pragma unroll
-                for (int q = 0; q < NI / 16; ++q) {
-                    float v[16];
-                    __syncwarp();
-                    vla::tc_ld16(tm + lanes + L::OE + i0 + q * 16, v);
-                    vla::tc_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int i = q * 16 + 2 * e;
-                        y[q * 8 + e] = fma2(make_float2(w[i], w[i + 1]), make_float2(v[2 * e], v[2 * e + 1]), zero2);
-                    }
-                }
+                load(L::OE, 0, oe[0]);
+                load(L::OE, 1, oe[1]);
+                vla::tc_wait_ld();
                 vla::tc_fence_before();
                 arrive_warp(oe_free);
-                ok = wait_warp(o_done + m % 2, m / 2);
+                ok = wait_warp(o_done, m);
             }
             if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             // the last chunk has left the buffer; the four warps leave together if a wait ran out
             if (vla::bar_red_or(1, 128, !ok)) break;
             vla::tc_fence_after();
+            if (rev && n < L::C) {
 #pragma unroll
-            for (int q = 0; q < NI / 16; ++q) {
-                float v[16];
-                __syncwarp();
-                vla::tc_ld16(tm + lanes + L::X + (m % L::NX) * 64 + i0 + q * 16, v);
+                for (int k = 0; k < NI / 8; ++k) {
+                    const int i = i0 + lc + 8 * k + L::C - n;
+                    wo[k] = make_float2(WO[i], WO[i + 1]);
+                }
+            }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                float v[NR];
+                load(L::X, hh, v);
                 vla::tc_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[q * 8 + e] = fma2(make_float2(1.f, 1.f), y[q * 8 + e], make_float2(v[2 * e], v[2 * e + 1]));
+                for (int e = 0; e < NR; e += 2) {
+                    const float2 y = fma2(wo[e / 4], make_float2(oe[hh][e], oe[hh][e + 1]), make_float2(v[e], v[e + 1]));
+                    oe[hh][e] = y.x, oe[hh][e + 1] = y.y;
+                }
             }
             vla::tc_fence_before();
             arrive_warp(o_free);
             if (n < L::C) {
 #pragma unroll
-                for (int e = 0; e < NI / 2; ++e) {
-                    if (i0 + 2 * e >= n) y[e].x = 0.f;
-                    if (i0 + 2 * e + 1 >= n) y[e].y = 0.f;
+                for (int e = 0; e < NR; e += 2) {
+                    const int i = i0 + (e / 4) * 8 + lc;
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        if (i >= n) oe[hh][e] = 0.f;
+                        if (i + 1 >= n) oe[hh][e + 1] = 0.f;
+                    }
                 }
             }
 #pragma unroll
-            for (int e = 0; e < NI / 2; ++e) {
-                const int i = 2 * e;
-                bad = fma2(y[e], zero2, bad);
-                const uint32_t z = pack_bf16(y[e].x, y[e].y);
-                *reinterpret_cast<uint16_t*>(col + i * 128 + at8[i & 7]) = (uint16_t)z;
-                *reinterpret_cast<uint16_t*>(col + (i + 1) * 128 + at8[(i + 1) & 7]) = (uint16_t)(z >> 16);
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int k = 0; k < NI / 8; k += 2) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = make_float2(oe[hh][(k + e / 2) * 4 + (e % 2) * 2], oe[hh][(k + e / 2) * 4 + (e % 2) * 2 + 1]);
+                        bad = fma2(y, zero2, bad);
+                        u[e] = pack_bf16(y.x, y.y);
+                    }
+                    stmatrix4_t(dst + k * 1024 + (((chunk16 + 2 * hh) ^ (lane & 7)) << 4), u[0], u[1], u[2], u[3]);
+                }
+            if (rev && n < L::C) {
+#pragma unroll
+                for (int k = 0; k < NI / 8; ++k) wo[k] = *reinterpret_cast<const float2*>(WO + i0 + lc + 8 * k);
             }
             vla::fence_proxy_async_smem();
             vla::named_bar(1, 128);
