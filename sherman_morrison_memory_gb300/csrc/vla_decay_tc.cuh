@@ -31,7 +31,8 @@
 // warps take half of the tokens each. SC uses M = 128 with the upper 64 rows
 // reading what follows the tile in shared memory; nothing reads those lanes.
 //
-// Warps: 0-3 output, 4-11 decayed c and S, 12-13 P, 14 TMA loads, 15 MMA.
+// Warps: 0-3 output, 4-11 decayed c and S, 12-13 P, 14 TMA loads and the MMAs of
+// the state (OE, T), 15 those of the pairs (SC, OI).
 // Every wait is bounded; one that runs out raises the block's abort flag.
 //
 // STATE: only the segment's own state, from zero (b and c).
@@ -72,7 +73,7 @@ struct TcLay {
     // against the order of time into the one before; what they get is thrown away
     static constexpr int WO = OUT + TILE, WK = WO + 64 * 4, WP = WK + 64 * 4;
     static constexpr int BAR = WP + 64 * 4;
-    static constexpr int NBAR = 2 * NST + 11;
+    static constexpr int NBAR = 2 * NST + 13;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int SMEM = MISC + 16;
     static_assert((SMEM + 1024) * OCC <= 228 * 1024, "shared memory");
@@ -143,6 +144,15 @@ __device__ __forceinline__ void ld_frag32(uint32_t taddr, float (&v)[16]) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void ld_frag16(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void st_frag8(uint32_t taddr, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
@@ -215,7 +225,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
     uint64_t *full = bar, *empty = full + L::NST, *cw_full = empty + L::NST, *p_ready = cw_full + 2,
              *sc_done = cw_full + 3, *o_done = cw_full + 4, *sb_ready = cw_full + 5, *oe_done = cw_full + 6,
-             *oe_free = cw_full + 7, *o_free = cw_full + 8, *t_done = cw_full + 9, *drained = cw_full + 10;
+             *oe_free = cw_full + 7, *o_free = cw_full + 8, *t_done = cw_full + 9, *cleared = cw_full + 10, *drained = cw_full + 11;
     float *WP = reinterpret_cast<float*>(sm + L::WP), *WK = reinterpret_cast<float*>(sm + L::WK),
           *WO = reinterpret_cast<float*>(sm + L::WO);
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::MISC);
@@ -243,7 +253,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
         *reinterpret_cast<uint4*>(sm + L::P + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     vla::fence_proxy_async_smem();
     if (tid == 0) {
-        for (int i = 0; i < L::NST; ++i) vla::mbar_init(full + i, 1), vla::mbar_init(empty + i, 1);
+        for (int i = 0; i < L::NST; ++i) vla::mbar_init(full + i, 1), vla::mbar_init(empty + i, STATE ? 1 : 2);
         // two, by the chunk's parity: a warp may be a chunk ahead of the others here
         for (int i = 0; i < 2; ++i) vla::mbar_init(cw_full + i, 8);
         vla::mbar_init(sc_done, 1);
@@ -254,7 +264,8 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
         vla::mbar_init(oe_free, 4);
         vla::mbar_init(o_free, 4);
         vla::mbar_init(t_done, 1);
-        vla::mbar_init(drained, 1);
+        vla::mbar_init(cleared, 8);
+        for (int i = 0; i < 2; ++i) vla::mbar_init(drained + i, 1);
         *abort_flag = 0;
         vla::fence_mbar_init();
     }
@@ -279,111 +290,109 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
     // first token (within the segment) of the m-th chunk in the role's order
     auto chunk0 = [&](int m) { return (rev ? chunks - 1 - m : m) * L::C; };
 
-    if (warp == 14) {  // ---- TMA loads
-        if (lane == 0) {
-            int m = 0;
-            for (; m < chunks; ++m) {
-                const int st = m % L::NST;
-                if (m >= L::NST && !wait(empty + st, m / L::NST - 1)) break;
-                const int t = sp.t0 + chunk0(m);
-                const uint32_t dst = sb + L::ST + st * 3 * L::TILE;
-                vla::mbar_arrive_expect_tx(full + st, (STATE ? 2 : 3) * L::TILE);
-                const int id[3] = {r.map_a, r.map_b, r.map_c};
+    // The whole warps run the MMA loops, so that operands stay in uniform
+    // registers, and one elected thread issues: issued under a test of the lane,
+    // each MMA took 100 cycles.
+    const uint32_t id_k = idesc_bf16(128, 64, 0, 0);    // SC, OE
+    constexpr uint32_t HALF = L::NB == 2 ? L::BOX : 0;  // second 64 rows of an A operand: the next box, or again
+    const uint64_t dk = desc_sw128(0, 16, 1024), dm = desc_sw128(0, HALF, 1024);
+    auto at = [](uint64_t d, uint32_t addr) { return d + (uint64_t)(addr >> 4); };
+
+    if (warp == 14) {  // ---- TMA loads, MMAs of the state
+        const bool one = elect_one();
+        const uint32_t id_t = idesc_bf16(128, D, 0, 1);
+        const int id[3] = {r.map_a, r.map_b, r.map_c};
+        auto load = [&](int m) {
+            const int i = m % L::NST, t = sp.t0 + chunk0(m);
+            const uint32_t dst = sb + L::ST + i * 3 * L::TILE;
+            if (one) {
+                vla::mbar_arrive_expect_tx(full + i, (STATE ? 2 : 3) * L::TILE);
 #pragma unroll
                 for (int q = STATE ? 1 : 0; q < 3; ++q)
 #pragma unroll
                     for (int x = 0; x < L::NB; ++x)
-                        tma_load(dst + q * L::TILE + x * L::BOX, &maps.m[id[q]], x * 64, t, h, b, full + st);
+                        tma_load(dst + q * L::TILE + x * L::BOX, &maps.m[id[q]], x * 64, t, h, b, full + i);
             }
-            if (*abort_flag)  // leave only once the copies under way have landed
-                for (int i = max(0, m - L::NST); i < m; ++i)
-                    vla::mbar_wait(full + i % L::NST, (i / L::NST) & 1, nullptr, p.wait_ns);
-        }
-    } else if (warp == 15) {  // ---- MMA
-        // The whole warp runs the loop, so that operands stay in uniform
-        // registers, and one elected thread issues: issued under a test of the
-        // lane, each MMA took 100 cycles.
-        const bool one = elect_one();
-        const uint32_t id_k = idesc_bf16(128, 64, 0, 0);    // SC, OE
-        const uint32_t id_oi = idesc_bf16(128, 64, 1, 0);
-        const uint32_t id_t = idesc_bf16(128, D, 0, 1);
-        constexpr uint32_t HALF = L::NB == 2 ? L::BOX : 0;  // second 64 rows of an A operand: the next box, or again
-        const uint64_t dk = desc_sw128(0, 16, 1024), dm = desc_sw128(0, HALF, 1024);
-        auto at = [](uint64_t d, uint32_t addr) { return d + (uint64_t)(addr >> 4); };
-        auto tile = [&](int i) { return sb + L::ST + i * 3 * L::TILE; };
-        auto pairs = [&](int m, int i) {  // SC of chunk m, in stage i
-            const uint32_t ta = tile(i);
-            if (!wait_warp(full + i, m / L::NST)) return false;
-            if (m > 0 && !wait_warp(o_free, m - 1)) return false;
-            vla::tc_fence_after();
-            if (one) {
+            __syncwarp();
+        };
+        int loaded = min(chunks, L::NST);
+        for (int m = 0; m < loaded; ++m) load(m);
+        for (int m = 0; m < chunks; ++m) {
+            const int i = m % L::NST;
+            const uint32_t ta = sb + L::ST + i * 3 * L::TILE, tb = ta + L::TILE;
+            if (!wait_warp(full + i, m / L::NST)) break;
+            if (!wait_warp(sb_ready, m)) break;  // and T's last reader is done
+            if (!STATE) {
+                if (m > 0 && !wait_warp(oe_free, m - 1)) break;
+                vla::tc_fence_after();
+                if (one) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k / 4) * L::BOX + (k % 4) * 32;
-                    mma_ss(tm + L::X, at(dk, ta + off), at(dk, ta + L::TILE + off), id_k, k > 0);
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_ts(tm + L::OE, tm + L::SB + k * 8, at(dk, ta + (k / 4) * L::BOX + (k % 4) * 32), id_k, k > 0);
+                    vla::tc_commit(oe_done);
                 }
-                vla::tc_commit(sc_done);
+                __syncwarp();
             }
-            __syncwarp();
-            return true;
-        };
-        auto from_state = [&](int m, int i) {  // OE
-            if (!wait_warp(sb_ready, m)) return false;
-            if (m > 0 && !wait_warp(oe_free, m - 1)) return false;
-            if (!wait_warp(full + i, m / L::NST)) return false;
-            vla::tc_fence_after();
-            if (one) {
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_ts(tm + L::OE, tm + L::SB + k * 8, at(dk, tile(i) + (k / 4) * L::BOX + (k % 4) * 32), id_k, k > 0);
-                vla::tc_commit(oe_done);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto to_state = [&](int m, int i) {  // T, whose last reader is done with it when it publishes the state
-            if (STATE && (!wait_warp(full + i, m / L::NST) || !wait_warp(sb_ready, m))) return false;
-            if (!wait_warp(cw_full + m % 2, m / 2)) return false;
+            if (!wait_warp(cw_full + m % 2, m / 2)) break;
+            if (!STATE && L::ALIAS && !wait_warp(oe_free, m)) break;
             const uint32_t cw = tm + L::CW + (m % L::NCW) * L::PARTS * 32;
-            if (!STATE && L::ALIAS && !wait_warp(oe_free, m)) return false;
             vla::tc_fence_after();
             if (one) {
 #pragma unroll
                 for (int part = 0; part < L::PARTS; ++part)
 #pragma unroll
                     for (int k = 0; k < L::C / 16; ++k)
-                        mma_ts(tm + L::T, cw + part * 32 + k * 8, at(dm, tile(i) + L::TILE + k * 2048), id_t,
-                               part > 0 || k > 0);
+                        mma_ts(tm + L::T, cw + part * 32 + k * 8, at(dm, tb + k * 2048), id_t, part > 0 || k > 0);
                 vla::tc_commit(t_done);
+                vla::tc_commit(empty + i);
             }
             __syncwarp();
-            return true;
-        };
-        auto chunk = [&](int m, int i) {
-            if (STATE) {
-                if (!to_state(m, i)) return false;
-            } else {
-                if (!pairs(m, i) || !from_state(m, i) || !to_state(m, i)) return false;
-                if (!wait_warp(p_ready, m)) return false;
+            if (m > 0 && loaded < chunks) {  // the stage of the chunk before takes a new one
+                if (!wait_warp(empty + (m - 1) % L::NST, (m - 1) / L::NST)) break;
+                load(loaded++);
+            }
+        }
+        if (*abort_flag)  // leave only once the copies under way have landed
+            for (int m = max(0, loaded - L::NST); m < loaded; ++m)
+                vla::mbar_wait(full + m % L::NST, (m / L::NST) & 1, nullptr, p.wait_ns);
+        if (one) vla::tc_commit(drained);  // what was issued has finished before the block frees its TMEM
+        __syncwarp();
+        vla::mbar_wait(drained, 0, nullptr, p.wait_ns);
+    } else if (warp == 15) {  // ---- MMAs of the pairs
+        const bool one = elect_one();
+        const uint32_t id_oi = idesc_bf16(128, 64, 1, 0);
+        if (!STATE) {
+            for (int m = 0; m < chunks; ++m) {
+                const int i = m % L::NST;
+                const uint32_t ta = sb + L::ST + i * 3 * L::TILE, tb = ta + L::TILE, tc = tb + L::TILE;
+                if (!wait_warp(full + i, m / L::NST)) break;
+                if (m > 0 && !wait_warp(o_free, m - 1)) break;
+                vla::tc_fence_after();
+                if (one) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = (k / 4) * L::BOX + (k % 4) * 32;
+                        mma_ss(tm + L::X, at(dk, ta + off), at(dk, tb + off), id_k, k > 0);
+                    }
+                    vla::tc_commit(sc_done);
+                }
+                __syncwarp();
+                if (!wait_warp(p_ready, m)) break;
+                if (sp.n - chunk0(m) < L::C && !wait_warp(cleared, 0)) break;  // c's rows behind the end, once
                 vla::tc_fence_after();
                 if (one) {
 #pragma unroll
                     for (int k = 0; k < L::C / 16; ++k)
-                        mma_ss(tm + L::X, at(dm, tile(i) + 2 * L::TILE + k * 2048),
-                               at(dk, sb + L::P + k * 32), id_oi, k > 0);
+                        mma_ss(tm + L::X, at(dm, tc + k * 2048), at(dk, sb + L::P + k * 32), id_oi, k > 0);
                     vla::tc_commit(o_done);
+                    vla::tc_commit(empty + i);
                 }
                 __syncwarp();
             }
-            if (one) vla::tc_commit(empty + i);
+            if (one) vla::tc_commit(drained + 1);
             __syncwarp();
-            return true;
-        };
-        bool ok = true;
-        for (int m = 0; ok && m < chunks; ++m) ok = chunk(m, m % L::NST);
-        if (one) vla::tc_commit(drained);  // what was issued has finished before the block frees its TMEM
-        __syncwarp();
-        vla::mbar_wait(drained, 0, nullptr, p.wait_ns);
+            vla::mbar_wait(drained + 1, 0, nullptr, p.wait_ns);
+        }
     } else if (warp >= 12) {  // ---- P
         // In blocks of 8 x 8 pairs: those of the later half of pairs are never
         // written and stay zero, those on the diagonal are cut by it. A warp
@@ -502,7 +511,8 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
             if (!wait_warp(full + st, m / L::NST)) return false;
             const uint32_t tc = L::ST + st * 3 * L::TILE + 2 * L::TILE;
             const float* w = WK + j0 + (rev ? 0 : L::C - n);
-#pragma unroll
+            // rolled: the four roles' code of a scheduler is more than its instruction cache
+#pragma unroll 1
             for (int hh = 0; hh < 2; ++hh) {
                 uint32_t y[8];
                 float2 z[8];
@@ -516,24 +526,28 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
                     const int j = 8 * (e / 2);
                     z[e] = fma2(make_float2(__uint_as_float(y[e] << 16), __uint_as_float(y[e] & 0xFFFF0000u)),
                                 make_float2(w[j], w[j + 1]), zero2);
-                    if (n < L::C) {
-                        if (j0 + j >= n) z[e].x = 0.f;
-                        if (j0 + j + 1 >= n) z[e].y = 0.f;
+                }
+                if (n < L::C) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int j = j0 + 8 * (e / 2);
+                        if (j >= n) z[e].x = 0.f;
+                        if (j + 1 >= n) z[e].y = 0.f;
                     }
                 }
                 // the leading eight bits of what is left, cut off, three times: nothing remains
-#pragma unroll
-                for (int k = 0; k < 3; ++k) {
+                uint32_t dst = tm + lanes + ((uint32_t)(hh * 16) << 16) + L::CW + (m % L::NCW) * L::PARTS * 32 + half * 16;
+#pragma unroll 1
+                for (int k = 0; k < L::PARTS; ++k, dst += 32) {
                     uint32_t u[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         u[e] = __byte_perm(__float_as_uint(z[e].x), __float_as_uint(z[e].y), 0x7632);
-                        if (k < 2)
-                            z[e] = fma2(make_float2(__uint_as_float(__float_as_uint(z[e].x) & 0xFFFF0000u),
-                                                    __uint_as_float(__float_as_uint(z[e].y) & 0xFFFF0000u)),
-                                        make_float2(-1.f, -1.f), z[e]);
+                        z[e] = fma2(make_float2(__uint_as_float(__float_as_uint(z[e].x) & 0xFFFF0000u),
+                                                __uint_as_float(__float_as_uint(z[e].y) & 0xFFFF0000u)),
+                                    make_float2(-1.f, -1.f), z[e]);
                     }
-                    st_frag8(tm + lanes + ((uint32_t)(hh * 16) << 16) + L::CW + (m % L::NCW) * L::PARTS * 32 + k * 32 + half * 16, u);
+                    st_frag8(dst, u);
                 }
             }
             if (n < L::C) {
@@ -548,6 +562,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
             vla::tc_fence_before();
             vla::fence_proxy_async_smem();
             arrive_warp(cw_full + m % 2);
+            if (n < L::C) arrive_warp(cleared);
             return true;
         };
         bool ok = true;
@@ -602,13 +617,14 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
         float2 wo[NI / 8];
 #pragma unroll
         for (int k = 0; k < NI / 8; ++k) wo[k] = *reinterpret_cast<const float2*>(WO + i0 + lc + 8 * k);
-        auto load = [&](uint32_t col, int hh, float (&v)[NR]) {
-            const uint32_t at = tm + ((uint32_t)(warp * 32 + hh * 16) << 16) + col + i0;
+        constexpr int NV = NR / 2;  // values of one load: half of the tokens
+        auto load = [&](uint32_t col, int hh, int part, float* v) {
+            const uint32_t from = tm + ((uint32_t)(warp * 32 + hh * 16) << 16) + col + i0 + part * (NI / 2);
             __syncwarp();
             if constexpr (NI == 64)
-                ld_frag64(at, v);
+                ld_frag32(from, *reinterpret_cast<float(*)[16]>(v));
             else
-                ld_frag32(at, v);
+                ld_frag16(from, *reinterpret_cast<float(*)[8]>(v));
         };
         for (int m = 0; m < chunks; ++m) {
             const int c0 = chunk0(m), n = min(L::C, sp.n - c0);
@@ -616,8 +632,8 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
             bool ok = wait_warp(oe_done, m);
             if (ok) {
                 vla::tc_fence_after();
-                load(L::OE, 0, oe[0]);
-                load(L::OE, 1, oe[1]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) load(L::OE, k / 2, k % 2, oe[k / 2] + (k % 2) * NV);
                 vla::tc_wait_ld();
                 vla::tc_fence_before();
                 arrive_warp(oe_free);
@@ -635,14 +651,14 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
                 }
             }
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                float v[NR];
-                load(L::X, hh, v);
+            for (int k = 0; k < 4; ++k) {
+                float v[NV], *o = oe[k / 2] + (k % 2) * NV;
+                load(L::X, k / 2, k % 2, v);
                 vla::tc_wait_ld();
 #pragma unroll
-                for (int e = 0; e < NR; e += 2) {
-                    const float2 y = fma2(wo[e / 4], make_float2(oe[hh][e], oe[hh][e + 1]), make_float2(v[e], v[e + 1]));
-                    oe[hh][e] = y.x, oe[hh][e + 1] = y.y;
+                for (int e = 0; e < NV; e += 2) {
+                    const float2 y = fma2(wo[((k % 2) * NV + e) / 4], make_float2(o[e], o[e + 1]), make_float2(v[e], v[e + 1]));
+                    o[e] = y.x, o[e + 1] = y.y;
                 }
             }
             vla::tc_fence_before();
