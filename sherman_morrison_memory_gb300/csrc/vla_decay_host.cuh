@@ -123,17 +123,29 @@ __global__ void __launch_bounds__(STEP_THREADS) vla_decay_step_kernel(const T* _
 
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
-// The cut of a call with `heads` independent runs of blocks (roles x B x H)
-// into segments. A cut costs a second pass over two of the three sequences, so
-// it is taken only where it at least halves a block's run: a whole number of
-// segments for every run within one wave of blocks, of 256 tokens at least.
-void plan(long long heads, int T, int d, vla_dtype dt, int* nseg, int* seg_len) {
-    const int occ = dt == VLA_BF16 && d > 64 ? 1 : 2;
-    const long long want = (long long)occ * sm_count() / std::max(1LL, heads);
-    const int n = (int)std::max(1LL, std::min<long long>(want, T / 256));
-    const int len = ((T + n - 1) / n + 63) / 64 * 64;
-    *seg_len = std::max(64, len);
-    *nseg = std::max(1, (T + *seg_len - 1) / *seg_len);
+// The cut of a call into segments: `runs` runs of blocks (roles x B x H) for the
+// outputs and `state_runs` for the segments' own states. A cut costs the second
+// pass, over two of the three sequences, which takes 0.7 of the first; it pays
+// where the runs leave SMs idle. Time is counted in chunks of 64 tokens: the
+// waves of blocks that the SMs hold at once, each as long as a segment and what
+// a block's start and end take (6 chunks; 1 of the fp32 kernel's, which are as
+// much slower), and 5 for the scan. (At 32 heads
+// of 65,536 tokens, d = 128: 2.1 ms in one piece, 0.66 ms in 4, 0.58 ms in 19.)
+void plan(long long runs, long long state_runs, int T, int d, vla_dtype dt, int* nseg, int* seg_len) {
+    const long long slots = (long long)(dt == VLA_BF16 ? 1 : 2) * sm_count();
+    const int chunks = (T + 63) / 64;
+    auto waves = [&](long long blocks) { return (blocks + slots - 1) / slots; };
+    const double ends = dt == VLA_BF16 ? 6 : 1;
+    double best = 0;
+    int best_len = chunks;
+    for (int n = 1; n <= 64 && n * 4 <= std::max(4, chunks); ++n) {
+        const int len = (chunks + n - 1) / n, segs = (chunks + len - 1) / len;
+        double t = (double)waves(runs * segs) * (len + ends);
+        if (segs > 1) t += 0.7 * (double)waves(state_runs * segs) * (len + ends) + 5 * ends / 6 + 0.1 * segs;
+        if (n == 1 || t < best) best = t, best_len = len;
+    }
+    *seg_len = std::max(1, best_len) * 64;
+    *nseg = std::max(1, (chunks + best_len - 1) / std::max(1, best_len));
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -237,7 +249,7 @@ size_t scratch_bytes_of(int B, int H, int T, int d, bool backward) {
     int most = 1;
     for (vla_dtype dt : {VLA_F32, VLA_BF16}) {
         int nseg, len;
-        plan(BH * (backward ? 3 : 1), T, d, dt, &nseg, &len);
+        plan(BH * (backward ? 3 : 1), BH * (backward ? 2 : 1), T, d, dt, &nseg, &len);
         most = std::max(most, nseg);
     }
     return most > 1 ? (size_t)BH * most * (backward ? 2 : 1) * d * d * sizeof(float) : 0;
@@ -285,7 +297,7 @@ vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
     p.lengths = lengths;
     p.status = static_cast<vla::DeviceStatus*>(status);
     p.wait_ns = kWaitNs;
-    plan((long long)B * H, T, d, dtype, &p.nseg, &p.seg_len);
+    plan((long long)B * H, (long long)B * H, T, d, dtype, &p.nseg, &p.seg_len);
     p.seg = static_cast<float*>(scratch);
     p.role[0] = Role{to_seq(q, B, H, T), to_seq(k, B, H, T), to_seq(v, B, H, T), to_seq(o, B, H, T),
                      S0, S_out, 0, 0, scale, scale, 1.f, 0, 1, 2};
@@ -329,7 +341,7 @@ vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
     p.lengths = lengths;
     p.status = static_cast<vla::DeviceStatus*>(status);
     p.wait_ns = kWaitNs;
-    plan(3LL * B * H, T, d, dtype, &p.nseg, &p.seg_len);
+    plan(3LL * B * H, 2LL * B * H, T, d, dtype, &p.nseg, &p.seg_len);
     p.seg = static_cast<float*>(scratch);
     p.role[0] = Role{G, V, K, to_seq(dq, B, H, T), S0, nullptr, 1, 0, scale, scale, 1.f, 3, 2, 1};
     p.role[1] = Role{V, G, Q, to_seq(dk, B, H, T), dS_T, nullptr, 1, 1, scale, 1.f, scale, 2, 3, 0};

@@ -59,10 +59,9 @@ struct TcLay {
     static constexpr int NB = DP / 64;         // boxes of a tile
     static constexpr int BOX = C * 128;        // bytes
     static constexpr int TILE = NB * BOX;
-    static constexpr int NST = 4;              // chunks in flight
-    static constexpr int PARTS = 3;            // of the decayed c
-    static constexpr int OCC = DP == 64 ? 2 : 1;
-    static constexpr int NCW = DP == 64 ? 1 : 2;  // buffers of the decayed c: one where two blocks share an SM
+    static constexpr int NST = DP == 64 ? 8 : 4;  // chunks in flight
+    static constexpr int PARTS = 3;               // of the decayed c
+    static constexpr int NCW = 2;                 // its buffers
     static constexpr int THREADS = 512;
     // shared memory
     static constexpr int ST = 0;                           // [NST] a | b | c
@@ -76,14 +75,11 @@ struct TcLay {
     static constexpr int NBAR = 2 * NST + 13;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int SMEM = MISC + 16;
-    static_assert((SMEM + 1024) * OCC <= 228 * 1024, "shared memory");
-    // TMEM columns. OI takes SC's place once P is made of it. Where two blocks
-    // share the SM's 512, T takes OE's once that is read.
-    static constexpr bool ALIAS = DP == 64;
-    static constexpr int SB = 0, CW = SB + DP / 2, OE = CW + NCW * PARTS * 32, X = OE + 64;
-    static constexpr int T = ALIAS ? OE : X + 64;
-    static constexpr int COLS = DP == 64 ? 256 : 512;
-    static_assert((ALIAS ? X + 64 : T + DP) <= COLS, "tensor memory");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    // TMEM columns. OI takes SC's place once P is made of it.
+    static constexpr int SB = 0, CW = SB + DP / 2, OE = CW + NCW * PARTS * 32, X = OE + 64, T = X + 64;
+    static constexpr int COLS = 512;
+    static_assert(T + DP <= COLS, "tensor memory");
 };
 
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
@@ -216,7 +212,7 @@ __device__ __noinline__ bool wait_on(uint64_t* w, uint32_t parity, volatile int*
 }
 
 template <int D, bool STATE>
-__global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
+__global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
     vla_decay_tc_kernel(const __grid_constant__ DecayArgs p, const __grid_constant__ DecayMaps maps, int roles) {
     using L = TcLay<D>;
     extern __shared__ __align__(1024) unsigned char tc_sm[];
@@ -334,7 +330,6 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
                 __syncwarp();
             }
             if (!wait_warp(cw_full + m % 2, m / 2)) break;
-            if (!STATE && L::ALIAS && !wait_warp(oe_free, m)) break;
             const uint32_t cw = tm + L::CW + (m % L::NCW) * L::PARTS * 32;
             vla::tc_fence_after();
             if (one) {
@@ -513,7 +508,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
             const float* w = WK + j0 + (rev ? 0 : L::C - n);
             // rolled: the four roles' code of a scheduler is more than its instruction cache
 #pragma unroll 1
-            for (int hh = 0; hh < 2; ++hh) {
+            for (int hh = 0; hh < 2 && (D % 64 == 0 || xb + hh * 16 < D); ++hh) {
                 uint32_t y[8];
                 float2 z[8];
                 __syncwarp();
@@ -537,12 +532,13 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
                 }
                 // the leading eight bits of what is left, cut off, three times: nothing remains
                 uint32_t dst = tm + lanes + ((uint32_t)(hh * 16) << 16) + L::CW + (m % L::NCW) * L::PARTS * 32 + half * 16;
-#pragma unroll 1
+#pragma unroll
                 for (int k = 0; k < L::PARTS; ++k, dst += 32) {
                     uint32_t u[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         u[e] = __byte_perm(__float_as_uint(z[e].x), __float_as_uint(z[e].y), 0x7632);
+                        if (k + 1 == L::PARTS) continue;
                         z[e] = fma2(make_float2(__uint_as_float(__float_as_uint(z[e].x) & 0xFFFF0000u),
                                                 __uint_as_float(__float_as_uint(z[e].y) & 0xFFFF0000u)),
                                     make_float2(-1.f, -1.f), z[e]);
@@ -566,13 +562,19 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
             return true;
         };
         bool ok = true;
+        if constexpr (D % 64 != 0) {  // lanes that no row of c fills
+            const uint32_t none[8] = {};
+            __syncwarp();
+            for (int c = 0; c < L::NCW * L::PARTS * 32 && xb + 32 > D; c += 8) st_cols8(tm + lanes + L::CW + c, none);
+            vla::tc_wait_st();
+        }
         if (chunks > 0) {
             publish();
             ok = decayed(0);
         }
         for (int m = 0; ok && m < chunks; ++m) {
             // the buffer's last reader, T of chunk m - 1, is done
-            if (L::NCW > 1 && m + 1 < chunks && !(ok = decayed(m + 1))) break;
+            if (m + 1 < chunks && !(ok = decayed(m + 1))) break;
             if (!(ok = wait_warp(t_done, m))) break;
             vla::tc_fence_after();
             const float wn = decay_pow(g, min(L::C, sp.n - chunk0(m)));
@@ -592,7 +594,6 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, TcLay<D>::OCC)
                 vla::tc_fence_after();
             }
             publish();
-            if (L::NCW == 1) ok = decayed(m + 1);
         }
         float* fin = STATE ? p.seg + (((size_t)ri * p.B * p.H + bh) * p.nseg + seg) * D * D
                            : (p.nseg > 1 || !r.fin ? nullptr : r.fin + (size_t)bh * D * D);
