@@ -12,16 +12,44 @@ inputs' type; states, statistics and weights are float32.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 from typing import Optional
 
 import torch
 
-from ._binding import (_DTYPES, VLA_OK, VLAError, _call_buffer, _on_stream, _ptr, _Seq, _stream_handle, _workspace,
-                       load_library, vla_get_last_device_status)
+from ._binding import (_DTYPES, VLA_OK, VLAError, _call_buffer, _Seq, _workspace, load_library,
+                       vla_get_last_device_status)
 
 _DIMS = (32, 64, 96, 128)
 _GROUP = 32
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev: torch.device, stream):
+    """The device and stream of a call made current (nothing to do where they are)."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"a stream of {stream.device} for tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _handle(dev: torch.device, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+
+
+def _ptr(x: Optional[torch.Tensor]):
+    return None if x is None else x.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _decay_scratch(B: int, H: int, T: int, d: int, backward: int, device_index: int) -> int:
+    """vla_decay_scratch_bytes on a device (made current by the caller)."""
+    return int(load_library().vla_decay_scratch_bytes(B, H, T, d, backward))
 
 
 def _in_place(x: torch.Tensor) -> bool:
@@ -118,7 +146,7 @@ def vla_decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
     lib = load_library()
     B, H, T, d = q.shape
     dev = q.device
-    with torch.cuda.device(dev), _on_stream(stream):
+    with _on(dev, stream):
         log_decay = _check_f32(log_decay, (H,), dev, "log_decay")
         S0 = _check_f32(state, (B, H, d, d), dev, "state")
         lengths = _check_index(lengths, B, dev, "lengths")
@@ -130,11 +158,11 @@ def vla_decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
             _check_out(o, (B, H, T, d), q.dtype, dev, "out[0]", strided=True)
             _check_out(S, (B, H, d, d), torch.float32, dev, "out[1]")
         q, k, v = (_seq_in(x) for x in (q, k, v))
-        nbytes = int(lib.vla_decay_scratch_bytes(B, H, T, d, 0))
+        nbytes = _decay_scratch(B, H, T, d, 0, dev.index)
         scratch = _call_buffer(dev, nbytes, False) if nbytes else None
         st = lib.vla_decay_forward(_seq(q), _seq(k), _seq(v), _DTYPES[q.dtype], B, H, T, d, _ptr(log_decay), scale,
                                    _ptr(lengths), _ptr(S0), _seq(o), _ptr(S), _ptr(scratch), nbytes,
-                                   _ptr(_workspace(dev)), ctypes.c_void_p(_stream_handle(dev, stream)))
+                                   _ptr(_workspace(dev)), _handle(dev, stream))
     _done(st, "vla_decay_forward", dev, stream, check)
     return o, S
 
@@ -159,7 +187,7 @@ def vla_decay_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
     lib = load_library()
     B, H, T, d = q.shape
     dev = q.device
-    with torch.cuda.device(dev), _on_stream(stream):
+    with _on(dev, stream):
         log_decay = _check_f32(log_decay, (H,), dev, "log_decay")
         S0 = _check_f32(state, (B, H, d, d), dev, "state")
         dS_T = _check_f32(grad_state, (B, H, d, d), dev, "grad_state")
@@ -177,12 +205,12 @@ def vla_decay_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
                 _check_out(x, (B, H, T, d), q.dtype, dev, f"out[{i}]", strided=True)
             _check_out(dS0, (B, H, d, d), torch.float32, dev, "out[3]")
         q, k, v, grad_o = (_seq_in(x) for x in (q, k, v, grad_o))
-        nbytes = int(lib.vla_decay_scratch_bytes(B, H, T, d, 1))
+        nbytes = _decay_scratch(B, H, T, d, 1, dev.index)
         scratch = _call_buffer(dev, nbytes, False) if nbytes else None
         st = lib.vla_decay_backward(_seq(q), _seq(k), _seq(v), _seq(grad_o), _DTYPES[q.dtype], B, H, T, d,
                                     _ptr(log_decay), scale, _ptr(lengths), _ptr(S0), _ptr(dS_T),
                                     *(_seq(x) for x in grads), _ptr(dS0), _ptr(scratch), nbytes,
-                                    _ptr(_workspace(dev)), ctypes.c_void_p(_stream_handle(dev, stream)))
+                                    _ptr(_workspace(dev)), _handle(dev, stream))
     _done(st, "vla_decay_backward", dev, stream, check)
     return tuple(grads), dS0
 
@@ -213,18 +241,18 @@ def vla_decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay:
     _check_out(state, (N, H, d, d), torch.float32, dev, "state")
     if slots is None and B > N:
         raise ValueError(f"{B} sequences for {N} states")
-    with torch.cuda.device(dev), _on_stream(stream):
+    with _on(dev, stream):
         log_decay = _check_f32(log_decay, (H,), dev, "log_decay")
         slots = _check_index(slots, B, dev, "slots")
         if out is None:
             out = torch.empty((B, H, d), dtype=q.dtype, device=dev)
         else:
             _check_out(out, (B, H, d), q.dtype, dev, "out")
-        q, k, v = (x.contiguous() if x.data_ptr() % 16 == 0 else x.clone(memory_format=torch.contiguous_format)
-                   for x in (q, k, v))
+        q, k, v = (x if x.is_contiguous() and x.data_ptr() % 16 == 0
+                   else x.clone(memory_format=torch.contiguous_format) for x in (q, k, v))
         st = lib.vla_decay_step(_ptr(q), _ptr(k), _ptr(v), _DTYPES[q.dtype], B, H, d, _ptr(log_decay), scale,
                                 _ptr(state), N, _ptr(slots), _ptr(out), _ptr(_workspace(dev)),
-                                ctypes.c_void_p(_stream_handle(dev, stream)))
+                                _handle(dev, stream))
     _done(st, "vla_decay_step", dev, stream, check)
     return out
 
@@ -256,7 +284,7 @@ def vla_head_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
     dev = x.device
     if weight is not None and bias is not None and weight.shape != bias.shape:
         raise ValueError("weight and bias must have the same shape")
-    with torch.cuda.device(dev), _on_stream(stream):
+    with _on(dev, stream):
         weight = _norm_weight(weight, H, d, dev, "weight")
         bias = _norm_weight(bias, H, d, dev, "bias")
         shared = next((w.dim() == 1 for w in (weight, bias) if w is not None), False)
@@ -268,7 +296,7 @@ def vla_head_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: 
         rstd = torch.empty((B, H, T), dtype=torch.float32, device=dev)
         x = _seq_in(x)
         st = lib.vla_head_norm(_seq(x), _DTYPES[x.dtype], B, H, T, d, _ptr(weight), _ptr(bias), int(shared), eps,
-                               _seq(out), _ptr(mean), _ptr(rstd), ctypes.c_void_p(_stream_handle(dev, stream)))
+                               _seq(out), _ptr(mean), _ptr(rstd), _handle(dev, stream))
     _done(st, "vla_head_norm", dev, stream, False)
     return out, (mean, rstd)
 
@@ -287,7 +315,7 @@ def vla_head_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, stats, weight:
     B, H, T, d = x.shape
     dev = x.device
     mean, rstd = stats
-    with torch.cuda.device(dev), _on_stream(stream):
+    with _on(dev, stream):
         weight = _norm_weight(weight, H, d, dev, "weight")
         mean = _check_f32(mean, (B, H, T), dev, "mean")
         rstd = _check_f32(rstd, (B, H, T), dev, "rstd")
@@ -302,7 +330,7 @@ def vla_head_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, stats, weight:
         scratch = _call_buffer(dev, nbytes, False) if nbytes else None
         st = lib.vla_head_norm_backward(_seq(grad_y), _seq(x), _DTYPES[x.dtype], B, H, T, d, _ptr(weight), int(shared),
                                         _ptr(mean), _ptr(rstd), _seq(out), _ptr(dw), _ptr(db), _ptr(scratch), nbytes,
-                                        ctypes.c_void_p(_stream_handle(dev, stream)))
+                                        _handle(dev, stream))
     _done(st, "vla_head_norm_backward", dev, stream, False)
     return out, dw, db
 
@@ -365,11 +393,11 @@ def vla_state_store(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
     B = x.shape[0]
     if slots is None and B > N:
         raise ValueError(f"{B} states for {N} slots")
-    with torch.cuda.device(dev), _on_stream(stream):
+    with _on(dev, stream):
         x = _check_f32(x, (B, *shape), dev, "x")
         slots = _check_index(slots, B, dev, "slots")
         st = lib.vla_state_store(_ptr(x), B, _rows(shape), shape[-1], bits, _ptr(codes), _ptr(scales), N, _ptr(slots),
-                                 _ptr(_workspace(dev)), ctypes.c_void_p(_stream_handle(dev, stream)))
+                                 _ptr(_workspace(dev)), _handle(dev, stream))
     _done(st, "vla_state_store", dev, stream, check)
 
 
@@ -387,13 +415,13 @@ def vla_state_load(codes: torch.Tensor, scales: torch.Tensor, slots: Optional[to
     if slots is not None and slots.dim() != 1:
         raise ValueError("slots must be [B]")
     B = N if slots is None else slots.shape[0]
-    with torch.cuda.device(dev), _on_stream(stream):
+    with _on(dev, stream):
         slots = _check_index(slots, B, dev, "slots")
         if out is None:
             out = torch.empty((B, *shape), dtype=torch.float32, device=dev)
         else:
             _check_out(out, (B, *shape), torch.float32, dev, "out")
         st = lib.vla_state_load(_ptr(codes), _ptr(scales), N, _ptr(slots), B, _rows(shape), shape[-1], bits, _ptr(out),
-                                _ptr(_workspace(dev)), ctypes.c_void_p(_stream_handle(dev, stream)))
+                                _ptr(_workspace(dev)), _handle(dev, stream))
     _done(st, "vla_state_load", dev, stream, check)
     return out

@@ -199,11 +199,8 @@ vla_status launch(const Call& c, cudaStream_t s) {
     };
     if constexpr (TC) {
         using L = TcLay<D>;
-        auto main = vla_decay_tc_kernel<D, false>;
-        auto own = vla_decay_tc_kernel<D, true>;
-        if (cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess ||
-            cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
-            return VLA_ERR_CUDA;
+        constexpr auto main = vla_decay_tc_kernel<D, false>, own = vla_decay_tc_kernel<D, true>;
+        if (!allow_smem<main>(L::SMEM) || !allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
         if (c.main.nseg > 1) {
             own<<<blocks * c.state_roles, L::THREADS, L::SMEM, s>>>(c.states, c.maps, c.state_roles);
             scan();
@@ -211,11 +208,8 @@ vla_status launch(const Call& c, cudaStream_t s) {
         main<<<blocks * c.roles, L::THREADS, L::SMEM, s>>>(c.main, c.maps, c.roles);
     } else {
         using L = FmaLay<D>;
-        auto main = vla_decay_fma_kernel<D, T, false>;
-        auto own = vla_decay_fma_kernel<D, T, true>;
-        if (cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess ||
-            cudaFuncSetAttribute(own, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
-            return VLA_ERR_CUDA;
+        constexpr auto main = vla_decay_fma_kernel<D, T, false>, own = vla_decay_fma_kernel<D, T, true>;
+        if (!allow_smem<main>(L::SMEM) || !allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
         if (c.main.nseg > 1) {
             own<<<dim3(blocks, c.state_roles), L::THREADS, L::SMEM, s>>>(c.states);
             scan();

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 // vla_device.cuh defines this function with external linkage: it has another
 // name in this translation unit than in vla_forward.cu's
 #define mbar_wait_slow mbar_wait_slow_layer
@@ -28,13 +30,19 @@ __device__ __forceinline__ T* row_of(const Seq& s, int b, int h, long long t) {
     return reinterpret_cast<T*>(s.p) + (b * s.sb + h * s.sh + t * s.st);
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+// Eight values of a row in two steps, so that several loads can be under way at once.
+struct Raw8F {
+    float4 a, b;
+};
+__device__ __forceinline__ Raw8F raw8(const float* p) {
+    return Raw8F{*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)};
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ uint4 raw8(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void open8(const Raw8F& r, float (&x)[8]) {
+    x[0] = r.a.x, x[1] = r.a.y, x[2] = r.a.z, x[3] = r.a.w, x[4] = r.b.x, x[5] = r.b.y, x[6] = r.b.z, x[7] = r.b.w;
+}
+__device__ __forceinline__ void open8(const uint4& r, float (&x)[8]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(w[i] << 16);
@@ -44,6 +52,10 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
     *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+    open8(raw8(p), x);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -109,12 +121,25 @@ inline Seq to_seq(const S* s, int B, int H, int T) {
 
 // SMs of the current device, asked once per device (152 where none answers)
 inline int sm_count() {
-    static int known[64] = {};
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
-    if (known[dev]) return known[dev];
+    if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
-    return known[dev] = n;
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// Dynamic shared memory of kernel K raised to `bytes`, once per device.
+template <auto K>
+inline bool allow_smem(int bytes) {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    if (done[dev].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done[dev].store(true, std::memory_order_release);
+    return true;
 }
 
 }  // namespace vla_layer

@@ -5,7 +5,7 @@
 // and are bound by memory. A lane holds eight consecutive values of a row in
 // fp32 (16 bytes of bf16), so that d / 8 lanes hold a row and its sums are
 // butterflies over 4, 8 or 16 lanes; the mean is taken before the squares of
-// the differences, both from registers. A block stays on one head, with that
+// the differences, both from registers. A thread has four rows under way. A block stays on one head, with that
 // head's weight and bias in registers.
 //
 // Gradients, with g = dy weight and n = (x - mean) rstd:
@@ -60,31 +60,42 @@ __global__ void __launch_bounds__(NORM_THREADS) vla_head_norm_kernel(const NormA
     const int wo = (a.shared ? 0 : h * D) + col;
     if (on && a.weight) load8(a.weight + wo, w);
     if (on && a.bias) load8(a.bias + wo, bi);
-#pragma unroll 4
-    for (int r = r0; r < ROWS; r += L::PER) {
-        const long long t = t0 + r;
-        const bool in = on && t < a.T;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (in) load8(row_of<T>(a.x, b, h, t) + col, x);
-        float s = 0.f;
+    constexpr int U = ROWS / L::PER < 4 ? ROWS / L::PER : 4;  // rows under way at once
+    static_assert(ROWS % (U * L::PER) == 0, "whole passes");
+#pragma unroll 1
+    for (int r = r0; r < ROWS; r += U * L::PER) {
+        decltype(raw8((const T*)nullptr)) raw[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += x[i];
-        const float mean = row_sum<L::W>(s) * (1.f / D);
-        float q = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] -= mean;
-            q = fmaf(x[i], x[i], q);
+        for (int k = 0; k < U; ++k) {
+            const long long t = t0 + r + k * L::PER;
+            raw[k] = {};
+            if (on && t < a.T) raw[k] = raw8(row_of<T>(a.x, b, h, t) + col);
         }
-        q = row_sum<L::W>(on ? q : 0.f);
-        const float rstd = rsqrtf(q * (1.f / D) + a.eps);
-        if (in) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i] * rstd, w[i], bi[i]);
-            store8(row_of<T>(a.out, b, h, t) + col, x);
-            if (lane == 0) {
-                if (a.mean) a.mean[(long long)bh * a.T + t] = mean;
-                if (a.rstd) a.rstd[(long long)bh * a.T + t] = rstd;
+        for (int k = 0; k < U; ++k) {
+            const long long t = t0 + r + k * L::PER;
+            float x[8];
+            open8(raw[k], x);
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += x[i];
+            const float mean = row_sum<L::W>(s) * (1.f / D);
+            float q = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] -= mean;
+                q = fmaf(x[i], x[i], q);
+            }
+            q = row_sum<L::W>(on ? q : 0.f);
+            const float rstd = rsqrtf(q * (1.f / D) + a.eps);
+            if (on && t < a.T) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i] * rstd, w[i], bi[i]);
+                store8(row_of<T>(a.out, b, h, t) + col, x);
+                if (lane == 0) {
+                    if (a.mean) a.mean[(long long)bh * a.T + t] = mean;
+                    if (a.rstd) a.rstd[(long long)bh * a.T + t] = rstd;
+                }
             }
         }
     }
@@ -103,34 +114,45 @@ __global__ void __launch_bounds__(NORM_THREADS) vla_head_norm_backward_kernel(co
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = 1.f, dw[i] = 0.f, db[i] = 0.f;
     if (on && a.weight) load8(a.weight + (a.shared ? 0 : h * D) + col, w);
-#pragma unroll 2
-    for (int r = r0; r < ROWS; r += L::PER) {
-        const long long t = t0 + r;
-        const bool in = on && t < a.T;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, g[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        float mean = 0.f, rstd = 0.f;
-        if (in) {
-            load8(row_of<T>(a.x, b, h, t) + col, x);
-            load8(row_of<T>(a.dy, b, h, t) + col, g);
-            mean = a.mean[(long long)bh * a.T + t];
-            rstd = a.rstd[(long long)bh * a.T + t];
-        }
-        float s = 0.f, p = 0.f;
+    constexpr int U = ROWS / L::PER < 4 || sizeof(T) == 4 ? 2 : 4;  // rows under way at once
+    static_assert(ROWS % (U * L::PER) == 0, "whole passes");
+#pragma unroll 1
+    for (int r = r0; r < ROWS; r += U * L::PER) {
+        decltype(raw8((const T*)nullptr)) rx[U], rg[U];
+        float mean[U], rstd[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = (x[i] - mean) * rstd;
-            dw[i] = fmaf(g[i], x[i], dw[i]);
-            db[i] += g[i];
-            g[i] *= w[i];
-            s += g[i];
-            p = fmaf(g[i], x[i], p);
+        for (int k = 0; k < U; ++k) {
+            const long long t = t0 + r + k * L::PER;
+            rx[k] = {}, rg[k] = {}, mean[k] = rstd[k] = 0.f;
+            if (on && t < a.T) {
+                rx[k] = raw8(row_of<T>(a.x, b, h, t) + col);
+                rg[k] = raw8(row_of<T>(a.dy, b, h, t) + col);
+                mean[k] = a.mean[(long long)bh * a.T + t];
+                rstd[k] = a.rstd[(long long)bh * a.T + t];
+            }
         }
-        s = row_sum<L::W>(s) * (1.f / D);
-        p = row_sum<L::W>(p) * (1.f / D);
-        if (in) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = (g[i] - s - x[i] * p) * rstd;
-            store8(row_of<T>(a.out, b, h, t) + col, x);
+        for (int k = 0; k < U; ++k) {
+            const long long t = t0 + r + k * L::PER;
+            float x[8], g[8], s = 0.f, p = 0.f;
+            open8(rx[k], x);
+            open8(rg[k], g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = (x[i] - mean[k]) * rstd[k];
+                dw[i] = fmaf(g[i], x[i], dw[i]);
+                db[i] += g[i];
+                g[i] *= w[i];
+                s += g[i];
+                p = fmaf(g[i], x[i], p);
+            }
+            s = row_sum<L::W>(s) * (1.f / D);
+            p = row_sum<L::W>(p) * (1.f / D);
+            if (on && t < a.T) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = (g[i] - s - x[i] * p) * rstd[k];
+                store8(row_of<T>(a.out, b, h, t) + col, x);
+            }
         }
     }
     if (!a.partial) return;
@@ -157,6 +179,7 @@ __global__ void __launch_bounds__(NORM_THREADS) vla_head_norm_sums_kernel(const 
     const int h = blockIdx.x;
     const long long n = (long long)B * tb * (shared ? H : 1);
     float s = 0.f;
+#pragma unroll 8
     for (long long m = k; m < n; m += 8) {
         const long long blk = shared ? m : (m / tb * H + h) * tb + m % tb;
         s += partial[blk * 2 * D + i];
