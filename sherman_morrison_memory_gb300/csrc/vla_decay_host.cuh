@@ -14,8 +14,9 @@ namespace {
 
 // States of the segments (each its own, from zero) to the states they start
 // from: the running sum over the segments in the role's order, with the whole
-// decays between; the sum over all of them is the final state. A thread per
-// value of S.
+// decays between; the sum over all of them is the final state. A thread has
+// four values of S, and up to eight segments' of them under way at once: it
+// writes where it reads, so the compiler would wait for each.
 struct ScanRole {
     const float* init;
     float* fin;
@@ -28,26 +29,49 @@ struct ScanArgs {
     vla::DeviceStatus* status;
 };
 
+constexpr int SCAN_THREADS = 128;
+
 template <int D>
-__global__ void __launch_bounds__(256) vla_decay_scan_kernel(const __grid_constant__ DecayArgs p,
-                                                             const __grid_constant__ ScanArgs q) {
-    const int bh = blockIdx.x / (D * D / 256), i = (blockIdx.x % (D * D / 256)) * 256 + threadIdx.x;
+__global__ void __launch_bounds__(SCAN_THREADS) vla_decay_scan_kernel(const __grid_constant__ DecayArgs p,
+                                                                      const __grid_constant__ ScanArgs q) {
+    constexpr int BLOCKS = D * D / 4 / SCAN_THREADS, AHEAD = 8;
+    const int bh = blockIdx.x / BLOCKS, i = ((blockIdx.x % BLOCKS) * SCAN_THREADS + threadIdx.x) * 4;
     const int b = bh / p.H, h = bh % p.H;
     const ScanRole& r = q.role[blockIdx.y];
     const float g = p.log_decay[h];
-    const int at = r.init_t ? (i % D) * D + i / D : i;
-    float s = r.init ? r.init[(size_t)bh * D * D + at] : 0.f;
-    float* seg = p.seg + ((size_t)blockIdx.y * p.B * p.H + bh) * p.nseg * D * D + i;
-#pragma unroll 4
-    for (int k = 0; k < p.nseg; ++k) {
-        const int m = r.reverse ? p.nseg - 1 - k : k;
-        const float own = seg[(size_t)m * D * D];
-        seg[(size_t)m * D * D] = s;
-        s = fmaf(decay_pow(g, span_of(p, b, m).n), s, own);
+    const int x = i / D, y = i % D;  // four columns of a row
+    const size_t at = (size_t)bh * D * D;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r.init) {
+        const float* m = r.init + at;
+        s = r.init_t ? make_float4(m[y * D + x], m[(y + 1) * D + x], m[(y + 2) * D + x], m[(y + 3) * D + x])
+                     : *reinterpret_cast<const float4*>(m + i);
+    }
+    float4* seg = reinterpret_cast<float4*>(p.seg + ((size_t)blockIdx.y * p.B * p.H + bh) * p.nseg * D * D + i);
+    auto place = [&](int k) { return r.reverse ? p.nseg - 1 - k : k; };
+    for (int k0 = 0; k0 < p.nseg; k0 += AHEAD) {
+        float4 own[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (k0 + k < p.nseg) own[k] = seg[(size_t)place(k0 + k) * (D * D / 4)];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (k0 + k >= p.nseg) break;
+            const int m = place(k0 + k);
+            const float w = decay_pow(g, span_of(p, b, m).n);
+            seg[(size_t)m * (D * D / 4)] = s;
+            s = make_float4(fmaf(w, s.x, own[k].x), fmaf(w, s.y, own[k].y), fmaf(w, s.z, own[k].z),
+                            fmaf(w, s.w, own[k].w));
+        }
     }
     if (r.fin) {
-        r.fin[(size_t)bh * D * D + at] = s;
-        if (!(fabsf(s) <= 3.4028235e38f) && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, p.T);
+        float* m = r.fin + at;
+        if (r.init_t)
+            m[y * D + x] = s.x, m[(y + 1) * D + x] = s.y, m[(y + 2) * D + x] = s.z, m[(y + 3) * D + x] = s.w;
+        else
+            *reinterpret_cast<float4*>(m + i) = s;
+        const float bad = fmaf(s.x, 0.f, fmaf(s.y, 0.f, fmaf(s.z, 0.f, s.w * 0.f)));
+        if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, p.T);
     }
 }
 
@@ -192,10 +216,11 @@ template <int D, bool TC, typename T>
 vla_status launch(const Call& c, cudaStream_t s) {
     const long long BH = (long long)c.main.B * c.main.H;
     const long long grid = BH * c.main.nseg * c.roles;
-    if (grid > 2147483647LL || BH * (D * D / 256) > 2147483647LL) return VLA_ERR_INVALID_ARG;
+    if (grid > 2147483647LL || BH * (D * D / 4 / SCAN_THREADS) > 2147483647LL) return VLA_ERR_INVALID_ARG;
     const unsigned blocks = (unsigned)(BH * c.main.nseg);
     auto scan = [&] {
-        vla_decay_scan_kernel<D><<<dim3((unsigned)(BH * (D * D / 256)), c.state_roles), 256, 0, s>>>(c.main, c.scan);
+        vla_decay_scan_kernel<D>
+            <<<dim3((unsigned)(BH * (D * D / 4 / SCAN_THREADS)), c.state_roles), SCAN_THREADS, 0, s>>>(c.main, c.scan);
     };
     if constexpr (TC) {
         using L = TcLay<D>;

@@ -170,24 +170,29 @@ __global__ void __launch_bounds__(NORM_THREADS) vla_head_norm_backward_kernel(co
 }
 
 // dweight, dbias of head h (all heads where shared): the blocks' sums
-// [B][H][tb][2][D], 8 threads a column and the threads' sums in order.
+// [B][H][tb][2][D], 32 threads a column, each over every 32nd block, and the
+// threads' sums in order.
+constexpr int SUMS_THREADS = 1024;
+
 template <int D>
-__global__ void __launch_bounds__(NORM_THREADS) vla_head_norm_sums_kernel(const float* __restrict__ partial, int B, int H,
-                                                                     int tb, int shared, float* dw, float* db) {
-    __shared__ float sums[8][32];
-    const int i = blockIdx.y * 32 + threadIdx.x % 32, k = threadIdx.x / 32;  // of the 2 D columns; one of 8 parts
+__global__ void __launch_bounds__(SUMS_THREADS) vla_head_norm_sums_kernel(const float* __restrict__ partial, int B, int H,
+                                                                          int tb, int shared, float* dw, float* db) {
+    __shared__ float sums[32][33];
+    const int col = threadIdx.x % 32, k = threadIdx.x / 32;
+    const int i = blockIdx.y * 32 + col;  // of the 2 D columns
     const int h = blockIdx.x;
     const long long n = (long long)B * tb * (shared ? H : 1);
     float s = 0.f;
 #pragma unroll 8
-    for (long long m = k; m < n; m += 8) {
+    for (long long m = k; m < n; m += 32) {
         const long long blk = shared ? m : (m / tb * H + h) * tb + m % tb;
         s += partial[blk * 2 * D + i];
     }
-    sums[k][threadIdx.x % 32] = s;
+    sums[k][col] = s;
     __syncthreads();
     if (k == 0) {
-        for (int j = 1; j < 8; ++j) s += sums[j][threadIdx.x];
+#pragma unroll
+        for (int j = 1; j < 32; ++j) s += sums[j][col];
         (i < D ? dw : db)[h * D + i % D] = s;
     }
 }
@@ -296,10 +301,10 @@ vla_status vla_head_norm_backward(const vla_seq* dy, const vla_seq* x, vla_dtype
     if (st != VLA_OK || !dweight) return st;
     const dim3 grid((unsigned)(shared ? 1 : H), (unsigned)(2 * d / 32));
     switch (d) {
-        case 32: vla_head_norm_sums_kernel<32><<<grid, NORM_THREADS, 0, s>>>(a.partial, B, H, a.tb, a.shared, dweight, dbias); break;
-        case 64: vla_head_norm_sums_kernel<64><<<grid, NORM_THREADS, 0, s>>>(a.partial, B, H, a.tb, a.shared, dweight, dbias); break;
-        case 96: vla_head_norm_sums_kernel<96><<<grid, NORM_THREADS, 0, s>>>(a.partial, B, H, a.tb, a.shared, dweight, dbias); break;
-        default: vla_head_norm_sums_kernel<128><<<grid, NORM_THREADS, 0, s>>>(a.partial, B, H, a.tb, a.shared, dweight, dbias); break;
+        case 32: vla_head_norm_sums_kernel<32><<<grid, SUMS_THREADS, 0, s>>>(a.partial, B, H, a.tb, a.shared, dweight, dbias); break;
+        case 64: vla_head_norm_sums_kernel<64><<<grid, SUMS_THREADS, 0, s>>>(a.partial, B, H, a.tb, a.shared, dweight, dbias); break;
+        case 96: vla_head_norm_sums_kernel<96><<<grid, SUMS_THREADS, 0, s>>>(a.partial, B, H, a.tb, a.shared, dweight, dbias); break;
+        default: vla_head_norm_sums_kernel<128><<<grid, SUMS_THREADS, 0, s>>>(a.partial, B, H, a.tb, a.shared, dweight, dbias); break;
     }
     return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
 }

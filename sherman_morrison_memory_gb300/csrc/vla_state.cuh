@@ -17,17 +17,21 @@ constexpr int STATE_THREADS = 256;
 constexpr int UNROLL = 4;                          // float4 a thread has in flight
 constexpr int BLOCK_VALUES = STATE_THREADS * UNROLL * 4;  // values a block handles
 
-// Code of value a >= 0 for the scale s > 0 (inv its reciprocal, rounded): the
-// whole number nearest to a / s, ties to the even one, at most TOP. floor(a
-// inv) may be one off where a / s is next to a whole number k; the comparison
-// with the midpoint behind it gives k either way. fma rounds a - (k + 1/2) s
-// once, so its sign is that of the exact difference.
-template <int TOP>
-__device__ __forceinline__ int code_of(float a, float s, float inv) {
-    const float k = floorf(fminf(a * inv, (float)TOP));
-    const float r = fmaf(-(k + 0.5f), s, a);
-    const int c = (int)k + ((r > 0.f || (r == 0.f && ((int)k & 1))) ? 1 : 0);
-    return c < TOP ? c : TOP;
+// 1.5 2^23: a float added to it is rounded to a whole number (ties to even),
+// which the sum's low bits hold in two's complement.
+constexpr float WHOLE = 12582912.f;
+
+// WHOLE plus the code of value x for the scale s > 0 (inv its reciprocal,
+// rounded): the whole number nearest to x / s, ties to the even one. x inv is
+// rounded, so that its nearest whole number c may be the wrong neighbour where
+// x / s is next to the middle between two. r = x - c s is exact there (a
+// multiple of half of s's last place, at most about s / 2), so |r| against s / 2
+// tells.
+__device__ __forceinline__ float code_of(float x, float s, float inv) {
+    float t = fmaf(x, inv, WHOLE);
+    const float r = fmaf(-(t - WHOLE), s, x), half = 0.5f * s;
+    if (fabsf(r) >= half && (fabsf(r) > half || (__float_as_int(t) & 1))) t += copysignf(1.f, r);
+    return t;
 }
 
 template <int BITS>
@@ -47,41 +51,46 @@ __global__ void __launch_bounds__(STATE_THREADS) vla_state_store_kernel(const fl
     const int slot = slot_of(slots, b, N, true, status);
     if (slot < 0) return;
     const long long base = (long long)slot * per;
+    // the groups' largest sizes, as bits: NaN and Inf lie above all others
+    uint32_t top[UNROLL];
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+        const uint32_t f[4] = {__float_as_uint(v[i].x), __float_as_uint(v[i].y), __float_as_uint(v[i].z),
+                               __float_as_uint(v[i].w)};
+        top[i] = max(max(f[0] & 0x7FFFFFFFu, f[1] & 0x7FFFFFFFu), max(f[2] & 0x7FFFFFFFu, f[3] & 0x7FFFFFFFu));
+#pragma unroll
+        for (int m = 1; m < 8; m <<= 1) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], m));
+    }
+    // of a group's eight lanes, lane i divides for group i
+    static_assert(UNROLL == 4, "lanes 0-3");
+    const int lane8 = threadIdx.x & 7;
+    const uint32_t mine = lane8 & 2 ? (lane8 & 1 ? top[3] : top[2]) : (lane8 & 1 ? top[1] : top[0]);
+    float scale = __fdiv_rn(__uint_as_float(mine), (float)TOP);
+    if (scale < 1.17549435e-38f) scale = 0.f;
+    if (mine >= 0x7F800000u) scale = __uint_as_float(0x7FC00000u);
+    const float recip = scale > 0.f ? __fdividef(1.f, scale) : 0.f;
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < UNROLL; ++i) {
         const long long e = first + (long long)i * STATE_THREADS * 4;
+        const float s = __shfl_sync(0xffffffffu, scale, i, 8), inv = __shfl_sync(0xffffffffu, recip, i, 8);
+        // a group stored as zero, and one that is not finite, has codes of 0
+        const bool none = !(s > 0.f);
         const float f[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        float amax = 0.f, nan = 0.f;
+        uint32_t c[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            amax = fmaxf(amax, fabsf(f[j]));
-            nan = fmaf(f[j], 0.f, nan);  // NaN once a value is NaN or infinite
-        }
-        if (nan != nan) amax = INFINITY;
-#pragma unroll
-        for (int m = 1; m < 8; m <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-        const bool bad = amax == INFINITY;
-        float s = __fdiv_rn(amax, (float)TOP);
-        if (s < 1.17549435e-38f) s = 0.f;
-        const float inv = __fdividef(1.f, s);
-        int c[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            c[j] = (s == 0.f || bad) ? 0 : code_of<TOP>(fabsf(f[j]), s, inv);
-            if (f[j] < 0.f) c[j] = -c[j];
-        }
+        for (int j = 0; j < 4; ++j) c[j] = none ? 0u : (uint32_t)__float_as_int(code_of(f[j], s, inv));
         if (e < per) {
             const long long at = base + e;
             if constexpr (BITS == 8) {
-                const uint32_t w = (c[0] & 255) | (c[1] & 255) << 8 | (c[2] & 255) << 16 | (uint32_t)(c[3] & 255) << 24;
+                const uint32_t w = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
                 *reinterpret_cast<uint32_t*>(static_cast<char*>(codes) + at) = w;
             } else {
                 const uint32_t w = (c[0] & 15) | (c[1] & 15) << 4 | (c[2] & 15) << 8 | (c[3] & 15) << 12;
                 *reinterpret_cast<uint16_t*>(static_cast<char*>(codes) + at / 2) = (uint16_t)w;
             }
-            if ((threadIdx.x & 7) == 0) scales[at / 32] = bad ? __uint_as_float(0x7FC00000u) : s;
-            odd |= bad;
+            if (lane8 == 0) scales[at / 32] = s;
+            odd |= s != s;
         }
     }
     if (odd && status) vla::record_failure(status, vla::BIT_NONFINITE, kRoleSlot, b, slot);
