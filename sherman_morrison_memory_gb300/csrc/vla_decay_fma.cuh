@@ -39,7 +39,7 @@ __device__ __forceinline__ float dot4(float4 x, float4 y, float s) {
 }
 
 template <int D, typename T, bool STATE>
-__global__ void __launch_bounds__(256, 1) vla_decay_fma_kernel(const __grid_constant__ DecayArgs p) {
+__global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_constant__ DecayArgs p) {
     using L = FmaLay<D>;
     extern __shared__ __align__(16) float fma_sm[];
     float* sm = fma_sm;
@@ -93,12 +93,15 @@ __global__ void __launch_bounds__(256, 1) vla_decay_fma_kernel(const __grid_cons
             }
             __syncthreads();
             if (tid < L::CG * L::RG) {
-                const int c = (tid % L::CG) * 4, i0 = (tid / L::CG) * L::RPT;
+                // columns c, c + CG, ...: neighbouring lanes read neighbouring rows of S, whose pitch
+                // puts them in different banks, and write neighbouring values
+                const int c = tid % L::CG, i0 = (tid / L::CG) * L::RPT;
                 float acc[L::RPT][4] = {};
+#pragma unroll 2
                 for (int k = 0; k < D; k += 4) {
                     float4 s[4];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) s[m] = *reinterpret_cast<float4*>(sm + L::S + (c + m) * L::LD + k);
+                    for (int m = 0; m < 4; ++m) s[m] = *reinterpret_cast<float4*>(sm + L::S + (c + m * L::CG) * L::LD + k);
 #pragma unroll
                     for (int i = 0; i < L::RPT; ++i) {
                         const float4 a = *reinterpret_cast<float4*>(sm + L::A + (i0 + i) * L::LD + k);
@@ -110,15 +113,16 @@ __global__ void __launch_bounds__(256, 1) vla_decay_fma_kernel(const __grid_cons
                 for (int i = 0; i < L::RPT; ++i)
 #pragma unroll
                     for (int m = 0; m < 4; ++m) acc[i][m] *= sm[L::W + L::C + i0 + i];
+#pragma unroll 4
                 for (int j = 0; j < n; ++j) {
-                    const float4 v = *reinterpret_cast<float4*>(sm + L::CC + j * L::LD + c);
+                    float v[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) v[m] = sm[L::CC + j * L::LD + c + m * L::CG];
 #pragma unroll
                     for (int i = 0; i < L::RPT; ++i) {
                         const float w = sm[L::P + (i0 + i) * (L::C + 1) + j];
-                        acc[i][0] = fmaf(w, v.x, acc[i][0]);
-                        acc[i][1] = fmaf(w, v.y, acc[i][1]);
-                        acc[i][2] = fmaf(w, v.z, acc[i][2]);
-                        acc[i][3] = fmaf(w, v.w, acc[i][3]);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) acc[i][m] = fmaf(w, v[m], acc[i][m]);
                     }
                 }
 #pragma unroll
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(256, 1) vla_decay_fma_kernel(const __grid_cons
                     T* o = row_of<T>(r.out, b, h, t0 + i0 + i) + c;
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
-                        o[m] = (T)acc[i][m];
+                        o[m * L::CG] = (T)acc[i][m];
                         bad = fmaf(acc[i][m], 0.f, bad);
                     }
                 }
@@ -142,6 +146,7 @@ __global__ void __launch_bounds__(256, 1) vla_decay_fma_kernel(const __grid_cons
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int m = 0; m < 4; ++m) acc[i][m] = whole * sm[L::S + (x + i) * L::LD + y + m];
+#pragma unroll 4
             for (int j = 0; j < n; ++j) {
                 const float w = sm[L::W + 2 * L::C + j];
                 const float4 cv = *reinterpret_cast<float4*>(sm + L::CC + j * L::LD + x);

@@ -162,7 +162,8 @@ void plan(long long runs, long long state_runs, int T, int d, vla_dtype dt, int*
     const double ends = dt == VLA_BF16 ? 6 : 1;
     double best = 0;
     int best_len = chunks;
-    for (int n = 1; n <= 64 && n * 4 <= std::max(4, chunks); ++n) {
+    const int shortest = dt == VLA_BF16 ? 4 : 1;  // chunks of a segment
+    for (int n = 1; n <= 64 && n * shortest <= std::max(shortest, chunks); ++n) {
         const int len = (chunks + n - 1) / n, segs = (chunks + len - 1) / len;
         double t = (double)waves(runs * segs) * (len + ends);
         if (segs > 1) t += 0.7 * (double)waves(state_runs * segs) * (len + ends) + 5 * ends / 6 + 0.1 * segs;
