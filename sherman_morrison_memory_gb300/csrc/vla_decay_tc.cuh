@@ -25,11 +25,10 @@
 // (16x256b) that stmatrix writes in whole 16-byte rows; and the weights, which
 // in fragments depend on the lane alone, stay in registers.
 //
-// d is padded to DP = 64 or 128 columns by TMA's zero fill. Where DP is 64 the
-// A operands repeat their 64 rows (in shared memory by a stride of 0 between
-// the 64-row halves), so that lanes 64-127 hold a copy and the output's four
-// warps take half of the tokens each. SC uses M = 128 with the upper 64 rows
-// reading what follows the tile in shared memory; nothing reads those lanes.
+// d is padded to DP = 64 or 128 columns by TMA's zero fill. DP is also the MMAs'
+// M, so that at d <= 64 a warp's quarter of the TMEM lanes holds 16 rows of the
+// state (lanes 0-15), at d > 64 32. SC has M = 128 with the upper 64 rows reading
+// what follows the tile in shared memory; nothing reads those lanes.
 //
 // Warps: 0-3 output, 4-11 decayed c and S, 12-13 P, 14 TMA loads and the MMAs of
 // the state (OE, T), 15 those of the pairs (SC, OI).
@@ -62,22 +61,25 @@ struct TcLay {
     static constexpr int NST = DP == 64 ? 8 : 4;  // chunks in flight
     static constexpr int PARTS = 3;               // of the decayed c
     static constexpr int NCW = 2;                 // its buffers
+    // buffers of SC with OI behind it, and of P (where TMEM has room: the pairs then run a chunk ahead)
+    static constexpr int NX = DP == 64 ? 2 : 1;
+    static constexpr int RW = DP / 4, NH = RW / 16;  // rows of the state in a warp's lanes; groups of 16
     static constexpr int THREADS = 512;
     // shared memory
     static constexpr int ST = 0;                           // [NST] a | b | c
     static constexpr int P = ST + NST * 3 * TILE;
-    static constexpr int OUT = P + BOX;
+    static constexpr int OUT = P + NX * BOX;
     // weights of 64 each: the state to tokens, tokens to the state, pairs by
     // their lag. Tokens behind a chunk's end read into the next table and pairs
     // against the order of time into the one before; what they get is thrown away
     static constexpr int WO = OUT + TILE, WK = WO + 64 * 4, WP = WK + 64 * 4;
     static constexpr int BAR = WP + 64 * 4;
-    static constexpr int NBAR = 2 * NST + 13;
+    static constexpr int NBAR = 2 * NST + 16;
     static constexpr int MISC = BAR + NBAR * 8;
     static constexpr int SMEM = MISC + 16;
     static_assert(SMEM <= 227 * 1024, "shared memory");
     // TMEM columns. OI takes SC's place once P is made of it.
-    static constexpr int SB = 0, CW = SB + DP / 2, OE = CW + NCW * PARTS * 32, X = OE + 64, T = X + 64;
+    static constexpr int SB = 0, CW = SB + DP / 2, OE = CW + NCW * PARTS * 32, X = OE + 64, T = X + NX * 64;
     static constexpr int COLS = 512;
     static_assert(T + DP <= COLS, "tensor memory");
 };
@@ -114,8 +116,8 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 // Fragments: of 16 lanes, thread l holds rows l / 4 and l / 4 + 8. ld_frag:
-// columns 8 k + 2 (l % 4) + {0, 1} of both rows in v[4 k ..]; st_frag8: column
-// 4 k + l % 4 of the two rows in v[2 k], v[2 k + 1].
+// columns 8 k + 2 (l % 4) + {0, 1} of both rows in v[4 k ..]; st_frag: column
+// 4 k + l % 4 of the two rows, the 2 k-th and the next value.
 __device__ __forceinline__ void ld_frag64(uint32_t taddr, float (&v)[32]) {
     uint32_t r[32];
     asm volatile(
@@ -153,6 +155,10 @@ __device__ __forceinline__ void ld_frag16(uint32_t taddr, float (&v)[8]) {
 __device__ __forceinline__ void st_frag8(uint32_t taddr, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void st_frag4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
 // four 8 x 8 blocks of 16-bit values: lane l gives the address of row l % 8 of
@@ -220,8 +226,9 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
     const uint32_t sb = vla::smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
     uint64_t *full = bar, *empty = full + L::NST, *cw_full = empty + L::NST, *p_ready = cw_full + 2,
-             *sc_done = cw_full + 3, *o_done = cw_full + 4, *sb_ready = cw_full + 5, *oe_done = cw_full + 6,
-             *oe_free = cw_full + 7, *o_free = cw_full + 8, *t_done = cw_full + 9, *cleared = cw_full + 10, *drained = cw_full + 11;
+             *sc_done = cw_full + 4, *o_done = cw_full + 6, *sb_ready = cw_full + 8, *oe_done = cw_full + 9,
+             *oe_free = cw_full + 10, *o_free = cw_full + 11, *t_done = cw_full + 12, *cleared = cw_full + 13,
+             *drained = cw_full + 14;
     float *WP = reinterpret_cast<float*>(sm + L::WP), *WK = reinterpret_cast<float*>(sm + L::WK),
           *WO = reinterpret_cast<float*>(sm + L::WO);
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::MISC);
@@ -245,16 +252,18 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
         WO[tid] = r.w_st * decay_pow(g, rev ? down : up);
         WP[tid] = r.w_in * decay_pow(g, tid);
     }
-    for (int i = tid; i < L::BOX / 16; i += L::THREADS)  // the pairs that no chunk writes stay zero
+    for (int i = tid; i < L::NX * L::BOX / 16; i += L::THREADS)  // the pairs that no chunk writes stay zero
         *reinterpret_cast<uint4*>(sm + L::P + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     vla::fence_proxy_async_smem();
     if (tid == 0) {
         for (int i = 0; i < L::NST; ++i) vla::mbar_init(full + i, 1), vla::mbar_init(empty + i, STATE ? 1 : 2);
-        // two, by the chunk's parity: a warp may be a chunk ahead of the others here
-        for (int i = 0; i < 2; ++i) vla::mbar_init(cw_full + i, 8);
-        vla::mbar_init(sc_done, 1);
-        vla::mbar_init(o_done, 1);
-        vla::mbar_init(p_ready, 2);
+        // two, by the chunk's parity, where one side may be a chunk ahead of the other or of its own other warps
+        for (int i = 0; i < 2; ++i) {
+            vla::mbar_init(cw_full + i, 8);
+            vla::mbar_init(p_ready + i, 2);
+            vla::mbar_init(sc_done + i, 1);
+            vla::mbar_init(o_done + i, 1);
+        }
         vla::mbar_init(sb_ready, 8);
         vla::mbar_init(oe_done, 1);
         vla::mbar_init(oe_free, 4);
@@ -289,14 +298,13 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
     // The whole warps run the MMA loops, so that operands stay in uniform
     // registers, and one elected thread issues: issued under a test of the lane,
     // each MMA took 100 cycles.
-    const uint32_t id_k = idesc_bf16(128, 64, 0, 0);    // SC, OE
-    constexpr uint32_t HALF = L::NB == 2 ? L::BOX : 0;  // second 64 rows of an A operand: the next box, or again
+    constexpr uint32_t HALF = L::NB == 2 ? L::BOX : 16;  // from an MN-major operand's first 64 rows to the next
     const uint64_t dk = desc_sw128(0, 16, 1024), dm = desc_sw128(0, HALF, 1024);
     auto at = [](uint64_t d, uint32_t addr) { return d + (uint64_t)(addr >> 4); };
 
     if (warp == 14) {  // ---- TMA loads, MMAs of the state
         const bool one = elect_one();
-        const uint32_t id_t = idesc_bf16(128, D, 0, 1);
+        const uint32_t id_t = idesc_bf16(L::DP, D, 0, 1), id_oe = idesc_bf16(L::DP, 64, 0, 0);
         const int id[3] = {r.map_a, r.map_b, r.map_c};
         auto load = [&](int m) {
             const int i = m % L::NST, t = sp.t0 + chunk0(m);
@@ -317,30 +325,37 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
             const int i = m % L::NST;
             const uint32_t ta = sb + L::ST + i * 3 * L::TILE, tb = ta + L::TILE;
             if (!wait_warp(full + i, m / L::NST)) break;
-            if (!wait_warp(sb_ready, m)) break;  // and T's last reader is done
-            if (!STATE) {
-                if (m > 0 && !wait_warp(oe_free, m - 1)) break;
+            if (!wait_warp(sb_ready, m)) break;  // T's last reader is done
+            auto to_state = [&] {  // T
+                if (!wait_warp(cw_full + m % 2, m / 2)) return false;
+                const uint32_t cw = tm + L::CW + (m % L::NCW) * L::PARTS * 32;
+                vla::tc_fence_after();
+                if (one) {
+#pragma unroll
+                    for (int part = 0; part < L::PARTS; ++part)
+#pragma unroll
+                        for (int k = 0; k < L::C / 16; ++k)
+                            mma_ts(tm + L::T, cw + part * 32 + k * 8, at(dm, tb + k * 2048), id_t, part > 0 || k > 0);
+                    vla::tc_commit(t_done);
+                }
+                __syncwarp();
+                return true;
+            };
+            auto from_state = [&] {  // OE
+                if (m > 0 && !wait_warp(oe_free, m - 1)) return false;
                 vla::tc_fence_after();
                 if (one) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        mma_ts(tm + L::OE, tm + L::SB + k * 8, at(dk, ta + (k / 4) * L::BOX + (k % 4) * 32), id_k, k > 0);
+                        mma_ts(tm + L::OE, tm + L::SB + k * 8, at(dk, ta + (k / 4) * L::BOX + (k % 4) * 32), id_oe, k > 0);
                     vla::tc_commit(oe_done);
                 }
                 __syncwarp();
-            }
-            if (!wait_warp(cw_full + m % 2, m / 2)) break;
-            const uint32_t cw = tm + L::CW + (m % L::NCW) * L::PARTS * 32;
-            vla::tc_fence_after();
-            if (one) {
-#pragma unroll
-                for (int part = 0; part < L::PARTS; ++part)
-#pragma unroll
-                    for (int k = 0; k < L::C / 16; ++k)
-                        mma_ts(tm + L::T, cw + part * 32 + k * 8, at(dm, tb + k * 2048), id_t, part > 0 || k > 0);
-                vla::tc_commit(t_done);
-                vla::tc_commit(empty + i);
-            }
+                return true;
+            };
+            // the chain through S is the longer one where T is short, the outputs' where it is long
+            if (STATE ? !to_state() : L::NH == 1 ? !to_state() || !from_state() : !from_state() || !to_state()) break;
+            if (one) vla::tc_commit(empty + i);
             __syncwarp();
             if (m > 0 && loaded < chunks) {  // the stage of the chunk before takes a new one
                 if (!wait_warp(empty + (m - 1) % L::NST, (m - 1) / L::NST)) break;
@@ -355,31 +370,39 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
         vla::mbar_wait(drained, 0, nullptr, p.wait_ns);
     } else if (warp == 15) {  // ---- MMAs of the pairs
         const bool one = elect_one();
-        const uint32_t id_oi = idesc_bf16(128, 64, 1, 0);
-        if (!STATE) {
-            for (int m = 0; m < chunks; ++m) {
-                const int i = m % L::NST;
-                const uint32_t ta = sb + L::ST + i * 3 * L::TILE, tb = ta + L::TILE, tc = tb + L::TILE;
-                if (!wait_warp(full + i, m / L::NST)) break;
-                if (m > 0 && !wait_warp(o_free, m - 1)) break;
-                vla::tc_fence_after();
-                if (one) {
+        const uint32_t id_sc = idesc_bf16(128, 64, 0, 0), id_oi = idesc_bf16(L::DP, 64, 1, 0);
+        auto pairs = [&](int m) {  // SC
+            const int i = m % L::NST;
+            const uint32_t ta = sb + L::ST + i * 3 * L::TILE, tb = ta + L::TILE, x = tm + L::X + (m % L::NX) * 64;
+            if (!wait_warp(full + i, m / L::NST)) return false;
+            if (m >= L::NX && !wait_warp(o_free, m - L::NX)) return false;
+            vla::tc_fence_after();
+            if (one) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = (k / 4) * L::BOX + (k % 4) * 32;
-                        mma_ss(tm + L::X, at(dk, ta + off), at(dk, tb + off), id_k, k > 0);
-                    }
-                    vla::tc_commit(sc_done);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * L::BOX + (k % 4) * 32;
+                    mma_ss(x, at(dk, ta + off), at(dk, tb + off), id_sc, k > 0);
                 }
-                __syncwarp();
-                if (!wait_warp(p_ready, m)) break;
+                vla::tc_commit(sc_done + m % 2);
+            }
+            __syncwarp();
+            return true;
+        };
+        if (!STATE) {
+            bool ok = L::NX == 1 || chunks == 0 || pairs(0);
+            for (int m = 0; ok && m < chunks; ++m) {
+                const int i = m % L::NST;
+                const uint32_t tc = sb + L::ST + i * 3 * L::TILE + 2 * L::TILE, x = tm + L::X + (m % L::NX) * 64;
+                const uint32_t pm = sb + L::P + (m % L::NX) * L::BOX;
+                if (m + L::NX - 1 < chunks && !pairs(m + L::NX - 1)) break;
+                if (!wait_warp(p_ready + m % 2, m / 2)) break;
                 if (sp.n - chunk0(m) < L::C && !wait_warp(cleared, 0)) break;  // c's rows behind the end, once
                 vla::tc_fence_after();
                 if (one) {
 #pragma unroll
                     for (int k = 0; k < L::C / 16; ++k)
-                        mma_ss(tm + L::X, at(dm, tc + k * 2048), at(dk, sb + L::P + k * 32), id_oi, k > 0);
-                    vla::tc_commit(o_done);
+                        mma_ss(x, at(dm, tc + k * 2048), at(dk, pm + k * 32), id_oi, k > 0);
+                    vla::tc_commit(o_done + m % 2);
                     vla::tc_commit(empty + i);
                 }
                 __syncwarp();
@@ -408,16 +431,18 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
                 const int row8 = ((lane >> 3) & 1) * 8 + (lane & 7), kk = lane >> 4;
                 for (int m = 0; m < chunks; ++m) {
                     const int n = min(L::C, sp.n - chunk0(m));
-                    if (!wait_warp(sc_done, m)) return;  // behind OI of chunk m - 1, P's last reader
+                    if (!wait_warp(sc_done + m % 2, m / 2)) return;
+                    // P's last reader; with one buffer SC of this chunk was behind it
+                    if (L::NX == 2 && m >= 2 && !wait_warp(o_done + m % 2, m / 2 - 1)) return;
                     vla::tc_fence_after();
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         const int r = RB * 4 + hh * 2;  // first of two rows of blocks
                         float v[32];
                         __syncwarp();
-                        ld_frag64(tm + ((uint32_t)(RB * 32 + hh * 16) << 16) + L::X, v);
+                        ld_frag64(tm + ((uint32_t)(RB * 32 + hh * 16) << 16) + L::X + (m % L::NX) * 64, v);
                         vla::tc_wait_ld();
-                        const uint32_t dst = sb + L::P + (r * 8 + row8) * 128;
+                        const uint32_t dst = sb + L::P + (m % L::NX) * L::BOX + (r * 8 + row8) * 128;
 #pragma unroll
                         for (int k = 0; k < 8; k += 2) {
                             if (REV ? k < r : k > r) continue;
@@ -445,7 +470,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
                     }
                     vla::tc_fence_before();
                     vla::fence_proxy_async_smem();
-                    arrive_warp(p_ready);
+                    arrive_warp(p_ready + m % 2);
                 }
             };
             using std::integral_constant;
@@ -457,12 +482,22 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
                     : body(integral_constant<int, 1>{}, integral_constant<bool, false>{});
         }
     } else if (warp >= 4) {  // ---- the decayed c in parts, and S
-        constexpr int HC = D / 2;  // columns of S a thread holds
+        // A warp has the state's rows [xb, xb + RW) and half of its columns. Where
+        // the rows fill its 32 lanes, a lane has a row's: S[k] holds columns 2 k +
+        // {0, 1} of the half. Where they are 16, in fragments: S[4 u + k] holds
+        // columns 16 u + 8 (k / 2) + {0, 1} (from the lane's first) of row lane / 4
+        // + 8 (k % 2).
+        constexpr bool FRAG = L::NH == 1;
+        constexpr int HC = D / 2, NU = HC / 16, NS = L::NH * NU * 4;
         const int id = tid - 128, half = id / 128, quad = warp & 3;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const int x = (quad * 32 + lane) & (L::DP - 1);  // this lane's row
-        const bool row_in = x < D;
-        float2 S[HC / 2];
+        const int xb = quad * L::RW;
+        const bool rows_in = xb < D;  // else zero throughout
+        auto row = [&](int k) { return xb + (FRAG ? (lane >> 2) + 8 * (k % 2) : lane); };
+        auto col = [&](int k) {
+            return half * HC + (FRAG ? 2 * (lane & 3) + 16 * (k / 4) + 8 * ((k % 4) / 2) : 2 * k);
+        };
+        float2 S[NS];
         {
             const float* init = r.init ? r.init + (size_t)bh * D * D : nullptr;
             int init_t = r.init_t;
@@ -471,44 +506,53 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
                 init_t = p.seg_t[ri];
             }
 #pragma unroll
-            for (int e = 0; e < HC / 2; ++e) {
-                const int y = half * HC + 2 * e;
-                S[e] = zero2;
-                if (init && row_in)
-                    S[e] = init_t ? make_float2(init[y * D + x], init[(y + 1) * D + x])
+            for (int k = 0; k < NS; ++k) {
+                const int x = row(k), y = col(k);
+                S[k] = zero2;
+                if (init && rows_in)
+                    S[k] = init_t ? make_float2(init[y * D + x], init[(y + 1) * D + x])
                                   : *reinterpret_cast<const float2*>(init + x * D + y);
             }
         }
+        bool first = true;
         auto publish = [&] {  // Sb = bf16(S); T has been read
-            if (!STATE) {
+            if (!STATE && (rows_in || first)) {
+                __syncwarp();
 #pragma unroll
-                for (int q = 0; q < HC / 16; ++q) {
-                    uint32_t u[8];
+                for (int u = 0; u < NS / 8; ++u) {
+                    uint32_t v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) u[e] = pack_bf16(S[q * 8 + e].x, S[q * 8 + e].y);
-                    __syncwarp();
-                    st_cols8(tm + lanes + L::SB + half * (HC / 2) + q * 8, u);
+                    for (int k = 0; k < 8; ++k) v[k] = pack_bf16(S[8 * u + k].x, S[8 * u + k].y);
+                    const uint32_t dst = tm + lanes + L::SB + half * (HC / 2);
+                    if constexpr (FRAG)
+                        st_frag8(dst + u * 16, v);
+                    else
+                        st_cols8(dst + u * 8, v);
                 }
+                if constexpr (NS % 8 != 0)
+                    st_frag4(tm + lanes + L::SB + half * (HC / 2) + NS / 8 * 16, pack_bf16(S[NS - 4].x, S[NS - 4].y),
+                             pack_bf16(S[NS - 3].x, S[NS - 3].y), pack_bf16(S[NS - 2].x, S[NS - 2].y),
+                             pack_bf16(S[NS - 1].x, S[NS - 1].y));
                 vla::tc_wait_st();
             }
+            first = false;
             vla::tc_fence_before();
             arrive_warp(sb_ready);
         };
         const int j0 = half * 32 + 2 * (lane & 3);  // this lane's tokens: j0 + 8 k + {0, 1}
         // the row of c that this lane addresses for ldmatrix: blocks (x, j), (x + 8, j), (x, j + 8), (x + 8, j + 8)
-        const int xb = (quad * 32) & (L::DP - 1);
         const uint32_t src = (xb / 64) * L::BOX + (half * 32 + (lane >> 4) * 8 + (lane & 7)) * 128;
         const int chunk16 = (xb % 64) / 8 + ((lane >> 3) & 1);
-        // Chunk m's c, decayed to the chunk's end, for this warp's 32 rows and
-        // 32 tokens; rows behind the chunk's end cleared in b and c.
+        // Chunk m's c, decayed to the chunk's end, for this warp's rows and 32
+        // tokens; rows behind the chunk's end cleared in b and c.
         auto decayed = [&](int m) {
             const int st = m % L::NST, n = min(L::C, sp.n - chunk0(m));
             if (!wait_warp(full + st, m / L::NST)) return false;
             const uint32_t tc = L::ST + st * 3 * L::TILE + 2 * L::TILE;
             const float* w = WK + j0 + (rev ? 0 : L::C - n);
-            // rolled: the four roles' code of a scheduler is more than its instruction cache
+            // rolled: the roles' code of a scheduler is more than its instruction cache
 #pragma unroll 1
-            for (int hh = 0; hh < 2 && (D % 64 == 0 || xb + hh * 16 < D); ++hh) {
+            for (int hh = 0; hh < L::NH && (D % 64 == 0 || rows_in); ++hh) {
                 uint32_t y[8];
                 float2 z[8];
                 __syncwarp();
@@ -565,7 +609,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
         if constexpr (D % 64 != 0) {  // lanes that no row of c fills
             const uint32_t none[8] = {};
             __syncwarp();
-            for (int c = 0; c < L::NCW * L::PARTS * 32 && xb + 32 > D; c += 8) st_cols8(tm + lanes + L::CW + c, none);
+            for (int c = 0; c < L::NCW * L::PARTS * 32 && !rows_in; c += 8) st_cols8(tm + lanes + L::CW + c, none);
             vla::tc_wait_st();
         }
         if (chunks > 0) {
@@ -579,14 +623,23 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
             vla::tc_fence_after();
             const float wn = decay_pow(g, min(L::C, sp.n - chunk0(m)));
             const float2 w2 = make_float2(wn, wn);
+            if (rows_in) {
+                const uint32_t src_t = tm + lanes + L::T + half * HC;
 #pragma unroll
-            for (int q = 0; q < HC / 16; ++q) {
-                float v[16];
-                __syncwarp();
-                vla::tc_ld16(tm + lanes + L::T + half * HC + q * 16, v);
-                vla::tc_wait_ld();
+                for (int u = 0; u < NU; ++u) {  // 16 columns
+                    float v[16];
+                    __syncwarp();
+                    if constexpr (FRAG)
+                        ld_frag16(src_t + u * 16, *reinterpret_cast<float(*)[8]>(v));
+                    else
+                        vla::tc_ld16(src_t + u * 16, v);
+                    vla::tc_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) S[q * 8 + e] = fma2(w2, S[q * 8 + e], make_float2(v[2 * e], v[2 * e + 1]));
+                    for (int k = 0; k < NS / NU; ++k) {
+                        float2& s = S[u * (NS / NU) + k];
+                        s = fma2(w2, s, make_float2(v[2 * k], v[2 * k + 1]));
+                    }
+                }
             }
             if (m + 1 == chunks) break;
             if (!STATE) {
@@ -597,100 +650,86 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
         }
         float* fin = STATE ? p.seg + (((size_t)ri * p.B * p.H + bh) * p.nseg + seg) * D * D
                            : (p.nseg > 1 || !r.fin ? nullptr : r.fin + (size_t)bh * D * D);
-        if (ok && fin && quad * 32 + lane < D) {
+        if (ok && fin && rows_in) {
 #pragma unroll
-            for (int e = 0; e < HC / 2; e += 2) {
-                bad = fma2(S[e], zero2, bad);
-                bad = fma2(S[e + 1], zero2, bad);
-                *reinterpret_cast<float4*>(fin + x * D + half * HC + 2 * e) =
-                    make_float4(S[e].x, S[e].y, S[e + 1].x, S[e + 1].y);
+            for (int k = 0; k < NS; ++k) {
+                bad = fma2(S[k], zero2, bad);
+                *reinterpret_cast<float2*>(fin + row(k) * D + col(k)) = S[k];
             }
         }
     } else if (!STATE) {  // ---- output
-        // where the lanes hold the rows twice, each copy's warps take half of the tokens
-        constexpr int NI = L::DP == 64 ? 32 : 64, NR = NI / 2;  // tokens; values a thread has of 16 rows
-        const int i0 = L::DP == 64 ? (warp / 2) * 32 : 0;
+        constexpr int NH = L::NH;
         const int lc = 2 * (lane & 3);
-        const int xb = (warp * 32) & (L::DP - 1);
+        const int xb = warp * L::RW;
+        const bool rows_in = xb < D;  // else columns that no store takes
         // the row of the output that this lane addresses for stmatrix: blocks (x, i), (x + 8, i), (x, i + 8), (x + 8, i + 8)
-        const uint32_t dst = sb + L::OUT + (xb / 64) * L::BOX + (i0 + (lane >> 4) * 8 + (lane & 7)) * 128;
+        const uint32_t dst = sb + L::OUT + (xb / 64) * L::BOX + ((lane >> 4) * 8 + (lane & 7)) * 128;
         const int chunk16 = (xb % 64) / 8 + ((lane >> 3) & 1);
-        float2 wo[NI / 8];
-#pragma unroll
-        for (int k = 0; k < NI / 8; ++k) wo[k] = *reinterpret_cast<const float2*>(WO + i0 + lc + 8 * k);
-        constexpr int NV = NR / 2;  // values of one load: half of the tokens
-        auto load = [&](uint32_t col, int hh, int part, float* v) {
-            const uint32_t from = tm + ((uint32_t)(warp * 32 + hh * 16) << 16) + col + i0 + part * (NI / 2);
+        auto load = [&](uint32_t col, int hh, int part, float* v) {  // 32 of the 64 tokens
             __syncwarp();
-            if constexpr (NI == 64)
-                ld_frag32(from, *reinterpret_cast<float(*)[16]>(v));
-            else
-                ld_frag16(from, *reinterpret_cast<float(*)[8]>(v));
+            ld_frag32(tm + ((uint32_t)(warp * 32 + hh * 16) << 16) + col + part * 32, *reinterpret_cast<float(*)[16]>(v));
         };
         for (int m = 0; m < chunks; ++m) {
             const int c0 = chunk0(m), n = min(L::C, sp.n - c0);
-            float oe[2][NR];
+            float oe[NH][32];
             bool ok = wait_warp(oe_done, m);
             if (ok) {
                 vla::tc_fence_after();
+                if (rows_in) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) load(L::OE, k / 2, k % 2, oe[k / 2] + (k % 2) * NV);
-                vla::tc_wait_ld();
+                    for (int k = 0; k < 2 * NH; ++k) load(L::OE, k / 2, k % 2, oe[k / 2] + (k % 2) * 16);
+                    vla::tc_wait_ld();
+                }
                 vla::tc_fence_before();
                 arrive_warp(oe_free);
-                ok = wait_warp(o_done, m);
+                ok = wait_warp(o_done + m % 2, m / 2);
             }
             if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             // the last chunk has left the buffer; the four warps leave together if a wait ran out
             if (vla::bar_red_or(1, 128, !ok)) break;
             vla::tc_fence_after();
-            if (rev && n < L::C) {
+            const float* wo = WO + lc + (rev ? L::C - n : 0);
+            if (rows_in) {
 #pragma unroll
-                for (int k = 0; k < NI / 8; ++k) {
-                    const int i = i0 + lc + 8 * k + L::C - n;
-                    wo[k] = make_float2(WO[i], WO[i + 1]);
-                }
-            }
+                for (int k = 0; k < 2 * NH; ++k) {
+                    float v[16], *o = oe[k / 2] + (k % 2) * 16;
+                    load(L::X + (m % L::NX) * 64, k / 2, k % 2, v);
+                    vla::tc_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float v[NV], *o = oe[k / 2] + (k % 2) * NV;
-                load(L::X, k / 2, k % 2, v);
-                vla::tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < NV; e += 2) {
-                    const float2 y = fma2(wo[((k % 2) * NV + e) / 4], make_float2(o[e], o[e + 1]), make_float2(v[e], v[e + 1]));
-                    o[e] = y.x, o[e + 1] = y.y;
+                    for (int e = 0; e < 16; e += 2) {
+                        const float* w = wo + (k % 2) * 32 + (e / 4) * 8;
+                        const float2 y = fma2(make_float2(w[0], w[1]), make_float2(o[e], o[e + 1]), make_float2(v[e], v[e + 1]));
+                        o[e] = y.x, o[e + 1] = y.y;
+                    }
                 }
             }
             vla::tc_fence_before();
             arrive_warp(o_free);
             if (n < L::C) {
 #pragma unroll
-                for (int e = 0; e < NR; e += 2) {
-                    const int i = i0 + (e / 4) * 8 + lc;
+                for (int e = 0; e < 32; e += 2) {
+                    const int i = (e / 4) * 8 + lc;
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
+                    for (int hh = 0; hh < NH; ++hh) {
                         if (i >= n) oe[hh][e] = 0.f;
                         if (i + 1 >= n) oe[hh][e + 1] = 0.f;
                     }
                 }
             }
+            if (rows_in) {
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
+                for (int hh = 0; hh < NH; ++hh)
 #pragma unroll
-                for (int k = 0; k < NI / 8; k += 2) {
-                    uint32_t u[4];
+                    for (int k = 0; k < 8; k += 2) {
+                        uint32_t u[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 y = make_float2(oe[hh][(k + e / 2) * 4 + (e % 2) * 2], oe[hh][(k + e / 2) * 4 + (e % 2) * 2 + 1]);
-                        bad = fma2(y, zero2, bad);
-                        u[e] = pack_bf16(y.x, y.y);
+                        for (int e = 0; e < 4; ++e) {
+                            const float* y = oe[hh] + (k + e / 2) * 4 + (e % 2) * 2;
+                            bad = fma2(make_float2(y[0], y[1]), zero2, bad);
+                            u[e] = pack_bf16(y[0], y[1]);
+                        }
+                        stmatrix4_t(dst + k * 1024 + (((chunk16 + 2 * hh) ^ (lane & 7)) << 4), u[0], u[1], u[2], u[3]);
                     }
-                    stmatrix4_t(dst + k * 1024 + (((chunk16 + 2 * hh) ^ (lane & 7)) << 4), u[0], u[1], u[2], u[3]);
-                }
-            if (rev && n < L::C) {
-#pragma unroll
-                for (int k = 0; k < NI / 8; ++k) wo[k] = *reinterpret_cast<const float2*>(WO + i0 + lc + 8 * k);
             }
             vla::fence_proxy_async_smem();
             vla::named_bar(1, 128);
