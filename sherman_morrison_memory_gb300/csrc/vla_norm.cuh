@@ -2,10 +2,11 @@
 // (include/vla_layer.h).
 //
 // A row is the d values of one (b, h, t). Both passes move each value once
-// and are bound by memory. A lane holds eight consecutive values of a row in
-// fp32 (16 bytes of bf16), so that d / 8 lanes hold a row and its sums are
-// butterflies over 4, 8 or 16 lanes; the mean is taken before the squares of
-// the differences, both from registers. A thread has four rows under way. A block stays on one head, with that
+// and are bound by memory. A lane holds groups of eight consecutive values of a
+// row in fp32 (16 bytes of bf16) and a row's sums are butterflies over its
+// lanes: 4 or 8 in the forward pass, with more groups a lane, d / 8 in the
+// backward pass, which holds more of each; the mean is taken before the squares
+// of the differences, both from registers. A thread has rows under way ahead. A block stays on one head, with that
 // head's weight and bias in registers.
 //
 // Gradients, with g = dy weight and n = (x - mean) rstd:
@@ -21,7 +22,7 @@ namespace vla_layer {
 namespace {
 
 constexpr int NORM_THREADS = 256;
-constexpr int ROWS = 128;  // rows a block handles
+constexpr int ROWS = 256;  // rows a block handles
 
 struct NormArgs {
     Seq x, dy, out;
@@ -46,52 +47,73 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
+// Lanes of a row in the forward pass: few, so that the two sums take few
+// shuffles, each with V groups of eight values (W lanes apart).
+template <int D>
+struct ForwardLanes {
+    static constexpr int W = D == 128 ? 8 : 4, V = D / 8 / W;
+    static constexpr int PER = NORM_THREADS / W;
+    static constexpr int U = V >= 2 ? 2 : 4;  // rows of a thread under way at once
+    static_assert(ROWS % (U * PER) == 0, "whole passes");
+};
+
 template <int D, typename T>
-__global__ void __launch_bounds__(NORM_THREADS) vla_head_norm_kernel(const NormArgs a) {
-    using L = Lanes<D>;
+__global__ void __launch_bounds__(NORM_THREADS, D == 96 || sizeof(T) == 4 ? 2 : 3)
+    vla_head_norm_kernel(const NormArgs a) {
+    using L = ForwardLanes<D>;
+    constexpr int V = L::V;
     const int bh = blockIdx.x / a.tb, b = bh / a.H, h = bh % a.H;
     const int lane = threadIdx.x % L::W, r0 = threadIdx.x / L::W;
-    const bool on = lane < L::USED;
-    const int col = lane * 8;
     const long long t0 = (long long)(blockIdx.x % a.tb) * ROWS;
-    float w[8], bi[8];
+    float w[V][8], bi[V][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f, bi[i] = 0.f;
-    const int wo = (a.shared ? 0 : h * D) + col;
-    if (on && a.weight) load8(a.weight + wo, w);
-    if (on && a.bias) load8(a.bias + wo, bi);
-    constexpr int U = ROWS / L::PER < 4 ? ROWS / L::PER : 4;  // rows under way at once
-    static_assert(ROWS % (U * L::PER) == 0, "whole passes");
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[v][i] = 1.f, bi[v][i] = 0.f;
+        const int at = (a.shared ? 0 : h * D) + (lane + v * L::W) * 8;
+        if (a.weight) load8(a.weight + at, w[v]);
+        if (a.bias) load8(a.bias + at, bi[v]);
+    }
 #pragma unroll 1
-    for (int r = r0; r < ROWS; r += U * L::PER) {
-        decltype(raw8((const T*)nullptr)) raw[U];
+    for (int r = r0; r < ROWS; r += L::U * L::PER) {
+        decltype(raw8((const T*)nullptr)) raw[L::U][V];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
+        for (int k = 0; k < L::U; ++k) {
             const long long t = t0 + r + k * L::PER;
-            raw[k] = {};
-            if (on && t < a.T) raw[k] = raw8(row_of<T>(a.x, b, h, t) + col);
+            const T* x = row_of<T>(a.x, b, h, t) + lane * 8;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                raw[k][v] = {};
+                if (t < a.T) raw[k][v] = raw8(x + v * L::W * 8);
+            }
         }
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
+        for (int k = 0; k < L::U; ++k) {
             const long long t = t0 + r + k * L::PER;
-            float x[8];
-            open8(raw[k], x);
-            float s = 0.f;
+            float x[V][8], s = 0.f, q = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += x[i];
-            const float mean = row_sum<L::W>(s) * (1.f / D);
-            float q = 0.f;
+            for (int v = 0; v < V; ++v) {
+                open8(raw[k][v], x[v]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] -= mean;
-                q = fmaf(x[i], x[i], q);
+                for (int i = 0; i < 8; ++i) s += x[v][i];
             }
-            q = row_sum<L::W>(on ? q : 0.f);
-            const float rstd = rsqrtf(q * (1.f / D) + a.eps);
-            if (on && t < a.T) {
+            const float mean = row_sum<L::W>(s) * (1.f / D);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i] * rstd, w[i], bi[i]);
-                store8(row_of<T>(a.out, b, h, t) + col, x);
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[v][i] -= mean;
+                    q = fmaf(x[v][i], x[v][i], q);
+                }
+            const float rstd = rsqrtf(row_sum<L::W>(q) * (1.f / D) + a.eps);
+            if (t < a.T) {
+                T* y = row_of<T>(a.out, b, h, t) + lane * 8;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[v][i] = fmaf(x[v][i] * rstd, w[v][i], bi[v][i]);
+                    store8(y + v * L::W * 8, x[v]);
+                }
                 if (lane == 0) {
                     if (a.mean) a.mean[(long long)bh * a.T + t] = mean;
                     if (a.rstd) a.rstd[(long long)bh * a.T + t] = rstd;
@@ -114,7 +136,7 @@ __global__ void __launch_bounds__(NORM_THREADS) vla_head_norm_backward_kernel(co
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = 1.f, dw[i] = 0.f, db[i] = 0.f;
     if (on && a.weight) load8(a.weight + (a.shared ? 0 : h * D) + col, w);
-    constexpr int U = ROWS / L::PER < 4 || sizeof(T) == 4 ? 2 : 4;  // rows under way at once
+    constexpr int U = sizeof(T) == 4 ? 2 : 4;  // rows under way at once
     static_assert(ROWS % (U * L::PER) == 0, "whole passes");
 #pragma unroll 1
     for (int r = r0; r < ROWS; r += U * L::PER) {
