@@ -282,12 +282,14 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
     float2 bad = make_float2(0.f, 0.f);  // NaN once an output or a final state is not finite
     const float2 zero2 = make_float2(0.f, 0.f);
 
-    // bounded wait: false once this or another wait of the block has run out
-    auto wait = [&](uint64_t* w, uint32_t parity) {
-        return vla::mbar_try_wait(w, parity & 1) ||
-               wait_on(w, parity & 1, abort_flag, p.wait_ns, p.status, warp / 4, bh);
+    // Bounded wait of a whole warp: false once this or another wait of the block
+    // has run out. The lanes go into the slow path together: a call that only
+    // some of them made would leave the others' uniform registers behind.
+    auto wait_warp = [&](uint64_t* w, uint32_t parity) {
+        if (__all_sync(0xffffffffu, vla::mbar_try_wait(w, parity & 1))) return true;
+        const bool ok = wait_on(w, parity & 1, abort_flag, p.wait_ns, p.status, warp / 4, bh);
+        return __all_sync(0xffffffffu, ok) != 0;
     };
-    auto wait_warp = [&](uint64_t* w, uint32_t parity) { return __all_sync(0xffffffffu, wait(w, parity)) != 0; };
     auto arrive_warp = [&](uint64_t* w) {  // one arrival a warp
         __syncwarp();
         if (lane == 0) vla::mbar_arrive(w);

@@ -96,16 +96,16 @@ inline bool good_dtype(vla_dtype t) { return t == VLA_F32 || t == VLA_BF16; }
 inline bool good_sizes(int B, int H, int T) {
     if (B < 0 || H < 0 || T < 0) return false;
     const long long BH = (long long)B * H;
-    return BH <= 2147483647LL && (unsigned long long)BH * (unsigned long long)T <= (1ull << 48);
+    return BH <= 2147483647LL && T <= 2147483647 - 256 && (unsigned long long)BH * (unsigned long long)T <= (1ull << 48);
 }
 
 inline bool good_seq(const void* data, long long sb, long long sh, long long st, int B, int H, int T, int es) {
     if (!data || !aligned(data, 16)) return false;
-    const long long lim = 1LL << 40;
+    const long long lim = 1LL << 40;  // bytes, of a tensor map's stride
     const long long s[3] = {sb, sh, st};
     const int n[3] = {B, H, T};
     for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && (s[i] <= 0 || s[i] >= lim || (s[i] * es) % 16 != 0)) return false;
+        if (n[i] > 1 && (s[i] <= 0 || s[i] >= lim / es || (s[i] * es) % 16 != 0)) return false;
     return true;
 }
 inline bool good_seq(const vla_seq* s, int B, int H, int T, int es) {
