@@ -1,6 +1,10 @@
-// vla_decay_fma.cuh -- the operation of vla_decay.cuh on the FP32 pipes, for
-// any input type: a block per (role, head, segment) goes through its tokens 32
-// at a time with S and the three tiles in shared memory as fp32.
+// vla_decay_fma.cuh -- the operation of vla_decay.cuh on the FP32 pipes, fp32
+// inputs: a block per (role, head, segment) goes through its tokens 32 at a time
+// with S and the tiles of a, b, c and the decayed c in shared memory. The next
+// 32 tokens' rows are on their way to registers meanwhile.
+//
+// Bound by shared memory: a value read there feeds 4 to 16 multiply-adds. (d =
+// 64, 40 heads of up to 1,021 tokens: 57 us for its three launches.)
 //
 // STATE: only the segment's own state, from zero, is formed (of b and c).
 #pragma once
@@ -13,32 +17,23 @@ template <int D>
 struct FmaLay {
     static constexpr int C = 32, THREADS = 256;
     static constexpr int LD = D + 4;  // row pitch: rows of a column of float4s lie in different banks
+    static constexpr int PP = C + 4;  // of the pairs
     static constexpr int S = 0;
-    static constexpr int A = S + D * LD, B = A + C * LD, CC = B + C * LD, P = CC + C * LD;
-    static constexpr int W = P + C * (C + 1);
-    static constexpr int FLOATS = W + 3 * C;
+    static constexpr int A = S + D * LD, B = A + C * LD, CC = B + C * LD, CW = CC + C * LD, P = CW + C * LD;
+    static constexpr int W = P + C * PP;  // weights: by lag, of the state to tokens
+    static constexpr int FLOATS = W + 2 * C;
     static constexpr int SMEM = FLOATS * 4;
-    static constexpr int CG = D / 4;                           // groups of four columns
+    static constexpr int CG = D / 4;                               // groups of four columns
     static constexpr int RG = D == 128 || D == 96 ? 8 : 1024 / D;  // row groups of the output tile
     static constexpr int RPT = C / RG;
+    static constexpr int NPT = (C * (D / 8) + THREADS - 1) / THREADS;  // 8-value pieces of a tile a thread moves
 };
-
-template <int D, typename T>
-__device__ __forceinline__ void load_tile(float* dst, const Seq& s, int b, int h, int t0, int n) {
-    using L = FmaLay<D>;
-    for (int i = threadIdx.x; i < L::C * (D / 8); i += L::THREADS) {
-        const int r = i / (D / 8), c = (i % (D / 8)) * 8;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (r < n) load8(row_of<T>(s, b, h, t0 + r) + c, x);
-        store8(dst + r * L::LD + c, x);
-    }
-}
 
 __device__ __forceinline__ float dot4(float4 x, float4 y, float s) {
     return fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
 }
 
-template <int D, typename T, bool STATE>
+template <int D, bool STATE>
 __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_constant__ DecayArgs p) {
     using L = FmaLay<D>;
     extern __shared__ __align__(16) float fma_sm[];
@@ -51,6 +46,25 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
     const bool rev = r.reverse;
     float bad = 0.f;  // NaN once an output or a final state is not finite
 
+    const int chunks = (sp.n + L::C - 1) / L::C;
+    // first token (within the segment) of the m-th 32 in the role's order
+    auto chunk0 = [&](int m) { return (rev ? chunks - 1 - m : m) * L::C; };
+    Raw8F ra[L::NPT], rb[L::NPT], rc[L::NPT];
+    auto fetch = [&](int m) {
+        const int c0 = chunk0(m), n = min(L::C, sp.n - c0), t0 = sp.t0 + c0;
+#pragma unroll
+        for (int k = 0; k < L::NPT; ++k) {
+            const int i = tid + k * L::THREADS, row = i / (D / 8), col = (i % (D / 8)) * 8;
+            ra[k] = rb[k] = rc[k] = Raw8F{};
+            if (row < n) {
+                if (!STATE) ra[k] = raw8(row_of<float>(r.a, b, h, t0 + row) + col);
+                rb[k] = raw8(row_of<float>(r.b, b, h, t0 + row) + col);
+                rc[k] = raw8(row_of<float>(r.c, b, h, t0 + row) + col);
+            }
+        }
+    };
+    if (chunks > 0) fetch(0);
+
     const float* init = r.init ? r.init + (size_t)bh * D * D : nullptr;
     int init_t = r.init_t;
     if (p.nseg > 1) {
@@ -62,33 +76,50 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
         const float v = init ? init[i] : 0.f;
         sm[L::S + (init_t ? y * L::LD + x : x * L::LD + y)] = v;
     }
-    const int chunks = (sp.n + L::C - 1) / L::C;
+    if (tid < L::C) sm[L::W + tid] = r.w_in * decay_pow(g, tid);
+
     for (int ci = 0; ci < chunks; ++ci) {
-        const int c0 = (rev ? chunks - 1 - ci : ci) * L::C;  // first token within the segment
-        const int n = min(L::C, sp.n - c0), t0 = sp.t0 + c0;
+        const int c0 = chunk0(ci), n = min(L::C, sp.n - c0), t0 = sp.t0 + c0;
         __syncthreads();
-        if (!STATE) load_tile<D, T>(sm + L::A, r.a, b, h, t0, n);
-        load_tile<D, T>(sm + L::B, r.b, b, h, t0, n);
-        load_tile<D, T>(sm + L::CC, r.c, b, h, t0, n);
-        if (tid < L::C) {
-            const int back = n - 1 - tid;  // tokens behind this one
-            const bool in = tid < n;
-            sm[L::W + tid] = decay_pow(g, tid);                                              // l^lag
-            sm[L::W + L::C + tid] = in ? r.w_st * decay_pow(g, rev ? back : tid + 1) : 0.f;   // state to output
-            sm[L::W + 2 * L::C + tid] = in ? r.k_st * decay_pow(g, rev ? tid + 1 : back) : 0.f;  // token to state
+#pragma unroll
+        for (int k = 0; k < L::NPT; ++k) {
+            const int i = tid + k * L::THREADS, row = i / (D / 8), col = (i % (D / 8)) * 8;
+            if (row < L::C) {
+                float x[8];
+                if (!STATE) {
+                    open8(ra[k], x);
+                    store8(sm + L::A + row * L::LD + col, x);
+                }
+                open8(rb[k], x);
+                store8(sm + L::B + row * L::LD + col, x);
+                open8(rc[k], x);
+                if (!STATE) store8(sm + L::CC + row * L::LD + col, x);
+                // token to state
+                const float w = row < n ? r.k_st * decay_pow(g, rev ? row + 1 : n - 1 - row) : 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= w;
+                store8(sm + L::CW + row * L::LD + col, x);
+            }
         }
+        if (tid < L::C)  // state to token
+            sm[L::W + L::C + tid] = tid < n ? r.w_st * decay_pow(g, rev ? n - 1 - tid : tid + 1) : 0.f;
         __syncthreads();
+        if (ci + 1 < chunks) fetch(ci + 1);
         if (!STATE) {
             {
-                const int i = tid / 8;
-                for (int j = tid % 8; j < L::C; j += 8) {
-                    float s = 0.f;
+                const int i = tid / 8, j0 = tid % 8;
+                float acc[4] = {};
+#pragma unroll 8
+                for (int k = 0; k < D; k += 4) {
+                    const float4 a = *reinterpret_cast<float4*>(sm + L::A + i * L::LD + k);
 #pragma unroll
-                    for (int k = 0; k < D; k += 4)
-                        s = dot4(*reinterpret_cast<float4*>(sm + L::A + i * L::LD + k),
-                                 *reinterpret_cast<float4*>(sm + L::B + j * L::LD + k), s);
-                    const int lag = rev ? j - i : i - j;
-                    sm[L::P + i * (L::C + 1) + j] = lag >= 0 && i < n && j < n ? r.w_in * s * sm[L::W + lag] : 0.f;
+                    for (int m = 0; m < 4; ++m)
+                        acc[m] = dot4(a, *reinterpret_cast<float4*>(sm + L::B + (j0 + 8 * m) * L::LD + k), acc[m]);
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int j = j0 + 8 * m, lag = rev ? j - i : i - j;
+                    sm[L::P + i * L::PP + j] = lag >= 0 && i < n && j < n ? acc[m] * sm[L::W + max(lag, 0)] : 0.f;
                 }
             }
             __syncthreads();
@@ -97,7 +128,7 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
                 // puts them in different banks, and write neighbouring values
                 const int c = tid % L::CG, i0 = (tid / L::CG) * L::RPT;
                 float acc[L::RPT][4] = {};
-#pragma unroll 2
+#pragma unroll 4
                 for (int k = 0; k < D; k += 4) {
                     float4 s[4];
 #pragma unroll
@@ -113,25 +144,28 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
                 for (int i = 0; i < L::RPT; ++i)
 #pragma unroll
                     for (int m = 0; m < 4; ++m) acc[i][m] *= sm[L::W + L::C + i0 + i];
-#pragma unroll 4
-                for (int j = 0; j < n; ++j) {
-                    float v[4];
+#pragma unroll 2
+                for (int j = 0; j < L::C; j += 4) {  // rows behind the end are zero in both
+                    float v[4][4];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) v[m] = sm[L::CC + j * L::LD + c + m * L::CG];
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) v[q][m] = sm[L::CC + (j + q) * L::LD + c + m * L::CG];
 #pragma unroll
                     for (int i = 0; i < L::RPT; ++i) {
-                        const float w = sm[L::P + (i0 + i) * (L::C + 1) + j];
+                        const float4 w = *reinterpret_cast<float4*>(sm + L::P + (i0 + i) * L::PP + j);
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) acc[i][m] = fmaf(w, v[m], acc[i][m]);
+                        for (int m = 0; m < 4; ++m)
+                            acc[i][m] = fmaf(w.x, v[0][m], fmaf(w.y, v[1][m], fmaf(w.z, v[2][m], fmaf(w.w, v[3][m], acc[i][m]))));
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < L::RPT; ++i) {
                     if (i0 + i >= n) continue;
-                    T* o = row_of<T>(r.out, b, h, t0 + i0 + i) + c;
+                    float* o = row_of<float>(r.out, b, h, t0 + i0 + i) + c;
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
-                        o[m * L::CG] = (T)acc[i][m];
+                        o[m * L::CG] = acc[i][m];
                         bad = fmaf(acc[i][m], 0.f, bad);
                     }
                 }
@@ -143,15 +177,15 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
             const int x = (blk / L::CG) * 4, y = (blk % L::CG) * 4;
             float acc[4][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) acc[i][m] = whole * sm[L::S + (x + i) * L::LD + y + m];
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) {
-                const float w = sm[L::W + 2 * L::C + j];
-                const float4 cv = *reinterpret_cast<float4*>(sm + L::CC + j * L::LD + x);
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = *reinterpret_cast<float4*>(sm + L::S + (x + i) * L::LD + y);
+                acc[i][0] = whole * v.x, acc[i][1] = whole * v.y, acc[i][2] = whole * v.z, acc[i][3] = whole * v.w;
+            }
+#pragma unroll 8
+            for (int j = 0; j < L::C; ++j) {
+                const float4 cv = *reinterpret_cast<float4*>(sm + L::CW + j * L::LD + x);
                 const float4 bv = *reinterpret_cast<float4*>(sm + L::B + j * L::LD + y);
-                const float cw[4] = {cv.x * w, cv.y * w, cv.z * w, cv.w * w};
+                const float cw[4] = {cv.x, cv.y, cv.z, cv.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     acc[i][0] = fmaf(cw[i], bv.x, acc[i][0]);
@@ -172,7 +206,7 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
         const int behind = min(p.seg_len, p.T - sp.t0) - sp.n;
         const float zero[8] = {};
         for (int i = tid; i < behind * (D / 8); i += L::THREADS)
-            store8(row_of<T>(r.out, b, h, sp.t0 + sp.n + i / (D / 8)) + (i % (D / 8)) * 8, zero);
+            store8(row_of<float>(r.out, b, h, sp.t0 + sp.n + i / (D / 8)) + (i % (D / 8)) * 8, zero);
     }
     float* fin = STATE ? p.seg + (((size_t)blockIdx.y * p.B * p.H + bh) * p.nseg + seg) * D * D
                        : (p.nseg > 1 || !r.fin ? nullptr : r.fin + (size_t)bh * D * D);

@@ -213,7 +213,7 @@ struct Call {
     DecayMaps maps;
 };
 
-template <int D, bool TC, typename T>
+template <int D, bool TC>
 vla_status launch(const Call& c, cudaStream_t s) {
     const long long BH = (long long)c.main.B * c.main.H;
     const long long grid = BH * c.main.nseg * c.roles;
@@ -234,7 +234,7 @@ vla_status launch(const Call& c, cudaStream_t s) {
         main<<<blocks * c.roles, L::THREADS, L::SMEM, s>>>(c.main, c.maps, c.roles);
     } else {
         using L = FmaLay<D>;
-        constexpr auto main = vla_decay_fma_kernel<D, T, false>, own = vla_decay_fma_kernel<D, T, true>;
+        constexpr auto main = vla_decay_fma_kernel<D, false>, own = vla_decay_fma_kernel<D, true>;
         if (!allow_smem<main>(L::SMEM) || !allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
         if (c.main.nseg > 1) {
             own<<<dim3(blocks, c.state_roles), L::THREADS, L::SMEM, s>>>(c.states);
@@ -248,17 +248,17 @@ vla_status launch(const Call& c, cudaStream_t s) {
 vla_status launch_call(const Call& c, int d, vla_dtype dt, cudaStream_t s) {
     if (dt == VLA_BF16) {
         switch (d) {
-            case 32: return launch<32, true, __nv_bfloat16>(c, s);
-            case 64: return launch<64, true, __nv_bfloat16>(c, s);
-            case 96: return launch<96, true, __nv_bfloat16>(c, s);
-            default: return launch<128, true, __nv_bfloat16>(c, s);
+            case 32: return launch<32, true>(c, s);
+            case 64: return launch<64, true>(c, s);
+            case 96: return launch<96, true>(c, s);
+            default: return launch<128, true>(c, s);
         }
     }
     switch (d) {
-        case 32: return launch<32, false, float>(c, s);
-        case 64: return launch<64, false, float>(c, s);
-        case 96: return launch<96, false, float>(c, s);
-        default: return launch<128, false, float>(c, s);
+        case 32: return launch<32, false>(c, s);
+        case 64: return launch<64, false>(c, s);
+        case 96: return launch<96, false>(c, s);
+        default: return launch<128, false>(c, s);
     }
 }
 
