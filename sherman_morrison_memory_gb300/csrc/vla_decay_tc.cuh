@@ -437,13 +437,16 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
                     // P's last reader; with one buffer SC of this chunk was behind it
                     if (L::NX == 2 && m >= 2 && !wait_warp(o_done + m % 2, m / 2 - 1)) return;
                     vla::tc_fence_after();
+                    float both[2][32];
+                    __syncwarp();
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh)
+                        ld_frag64(tm + ((uint32_t)(RB * 32 + hh * 16) << 16) + L::X + (m % L::NX) * 64, both[hh]);
+                    vla::tc_wait_ld();
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         const int r = RB * 4 + hh * 2;  // first of two rows of blocks
-                        float v[32];
-                        __syncwarp();
-                        ld_frag64(tm + ((uint32_t)(RB * 32 + hh * 16) << 16) + L::X + (m % L::NX) * 64, v);
-                        vla::tc_wait_ld();
+                        const float* v = both[hh];
                         const uint32_t dst = sb + L::P + (m % L::NX) * L::BOX + (r * 8 + row8) * 128;
 #pragma unroll
                         for (int k = 0; k < 8; k += 2) {
@@ -510,10 +513,16 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
                 const int x = row(k), y = col(k);
-                S[k] = zero2;
-                if (init && rows_in)
-                    S[k] = init_t ? make_float2(init[y * D + x], init[(y + 1) * D + x])
-                                  : *reinterpret_cast<const float2*>(init + x * D + y);
+                if (FRAG || k % 2 == 0 || !init || init_t) S[k] = zero2;
+                if (!init || !rows_in) continue;
+                if (init_t) {
+                    S[k] = make_float2(init[y * D + x], init[(y + 1) * D + x]);
+                } else if constexpr (FRAG) {
+                    S[k] = *reinterpret_cast<const float2*>(init + x * D + y);
+                } else if (k % 2 == 0) {
+                    const float4 v = *reinterpret_cast<const float4*>(init + x * D + y);
+                    S[k] = make_float2(v.x, v.y), S[k + 1] = make_float2(v.z, v.w);
+                }
             }
         }
         bool first = true;
@@ -656,7 +665,11 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
                 bad = fma2(S[k], zero2, bad);
-                *reinterpret_cast<float2*>(fin + row(k) * D + col(k)) = S[k];
+                if constexpr (FRAG)
+                    *reinterpret_cast<float2*>(fin + row(k) * D + col(k)) = S[k];
+                else if (k % 2 == 0)
+                    *reinterpret_cast<float4*>(fin + row(k) * D + col(k)) =
+                        make_float4(S[k].x, S[k].y, S[k + 1].x, S[k + 1].y);
             }
         }
     } else if (!STATE) {  // ---- output
@@ -693,13 +706,14 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
             const float* wo = WO + lc + (rev ? L::C - n : 0);
             if (rows_in) {
 #pragma unroll
-                for (int k = 0; k < 2 * NH; ++k) {
-                    float v[16], *o = oe[k / 2] + (k % 2) * 16;
-                    load(L::X + (m % L::NX) * 64, k / 2, k % 2, v);
+                for (int hh = 0; hh < NH; ++hh) {
+                    float v[32], *o = oe[hh];
+                    load(L::X + (m % L::NX) * 64, hh, 0, v);
+                    load(L::X + (m % L::NX) * 64, hh, 1, v + 16);
                     vla::tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float* w = wo + (k % 2) * 32 + (e / 4) * 8;
+                    for (int e = 0; e < 32; e += 2) {
+                        const float* w = wo + (e / 4) * 8;
                         const float2 y = fma2(make_float2(w[0], w[1]), make_float2(o[e], o[e + 1]), make_float2(v[e], v[e + 1]));
                         o[e] = y.x, o[e + 1] = y.y;
                     }
