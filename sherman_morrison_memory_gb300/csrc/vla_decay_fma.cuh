@@ -1,5 +1,5 @@
-// vla_decay_fma.cuh -- the operation of vla_decay.cuh on the FP32 pipes, fp32
-// inputs: a block per (role, head, segment) goes through its tokens 32 at a time
+// vla_decay_fma.cuh -- the operation of vla_decay.cuh on the FP32 pipes, for fp32
+// inputs and for the shortest bf16 calls: a block per (role, head, segment) goes through its tokens 32 at a time
 // with S and the tiles of a, b, c and the decayed c in shared memory. The next
 // 32 tokens' rows are on their way to registers meanwhile.
 //
@@ -33,7 +33,12 @@ __device__ __forceinline__ float dot4(float4 x, float4 y, float s) {
     return fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
 }
 
-template <int D, bool STATE>
+// bf16 calls of up to this many tokens run here too: their rows have so few
+// terms that the tensor cores' bf16 pairs do not average out and would show in
+// the result. (One token, 32 heads, d = 128: 12 us against the tensor cores' 10.)
+constexpr int FMA_T = 8;
+
+template <int D, typename T, bool STATE>
 __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_constant__ DecayArgs p) {
     using L = FmaLay<D>;
     extern __shared__ __align__(16) float fma_sm[];
@@ -49,17 +54,18 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
     const int chunks = (sp.n + L::C - 1) / L::C;
     // first token (within the segment) of the m-th 32 in the role's order
     auto chunk0 = [&](int m) { return (rev ? chunks - 1 - m : m) * L::C; };
-    Raw8F ra[L::NPT], rb[L::NPT], rc[L::NPT];
+    using Raw = decltype(raw8((const T*)nullptr));
+    Raw ra[L::NPT], rb[L::NPT], rc[L::NPT];
     auto fetch = [&](int m) {
         const int c0 = chunk0(m), n = min(L::C, sp.n - c0), t0 = sp.t0 + c0;
 #pragma unroll
         for (int k = 0; k < L::NPT; ++k) {
             const int i = tid + k * L::THREADS, row = i / (D / 8), col = (i % (D / 8)) * 8;
-            ra[k] = rb[k] = rc[k] = Raw8F{};
+            ra[k] = rb[k] = rc[k] = Raw{};
             if (row < n) {
-                if (!STATE) ra[k] = raw8(row_of<float>(r.a, b, h, t0 + row) + col);
-                rb[k] = raw8(row_of<float>(r.b, b, h, t0 + row) + col);
-                rc[k] = raw8(row_of<float>(r.c, b, h, t0 + row) + col);
+                if (!STATE) ra[k] = raw8(row_of<T>(r.a, b, h, t0 + row) + col);
+                rb[k] = raw8(row_of<T>(r.b, b, h, t0 + row) + col);
+                rc[k] = raw8(row_of<T>(r.c, b, h, t0 + row) + col);
             }
         }
     };
@@ -71,15 +77,22 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
         init = STATE ? nullptr : p.seg + (((size_t)p.seg_role[blockIdx.y] * p.B * p.H + bh) * p.nseg + seg) * D * D;
         init_t = p.seg_t[blockIdx.y];
     }
-    for (int i = tid; i < D * D; i += L::THREADS) {
+#pragma unroll 4
+    for (int i = tid * 4; i < D * D; i += L::THREADS * 4) {
         const int x = i / D, y = i % D;
-        const float v = init ? init[i] : 0.f;
-        sm[L::S + (init_t ? y * L::LD + x : x * L::LD + y)] = v;
+        const float4 v = init ? *reinterpret_cast<const float4*>(init + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (init_t) {
+            float* to = sm + L::S + y * L::LD + x;
+            to[0] = v.x, to[L::LD] = v.y, to[2 * L::LD] = v.z, to[3 * L::LD] = v.w;
+        } else {
+            *reinterpret_cast<float4*>(sm + L::S + x * L::LD + y) = v;
+        }
     }
     if (tid < L::C) sm[L::W + tid] = r.w_in * decay_pow(g, tid);
 
     for (int ci = 0; ci < chunks; ++ci) {
         const int c0 = chunk0(ci), n = min(L::C, sp.n - c0), t0 = sp.t0 + c0;
+        const int n8 = (n + 7) & ~7;  // rows from n on are zero in c and the pairs
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < L::NPT; ++k) {
@@ -123,7 +136,7 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
                 }
             }
             __syncthreads();
-            if (tid < L::CG * L::RG) {
+            if (tid < L::CG * L::RG && tid / L::CG * L::RPT < n) {
                 // columns c, c + CG, ...: neighbouring lanes read neighbouring rows of S, whose pitch
                 // puts them in different banks, and write neighbouring values
                 const int c = tid % L::CG, i0 = (tid / L::CG) * L::RPT;
@@ -145,7 +158,7 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
 #pragma unroll
                     for (int m = 0; m < 4; ++m) acc[i][m] *= sm[L::W + L::C + i0 + i];
 #pragma unroll 2
-                for (int j = 0; j < L::C; j += 4) {  // rows behind the end are zero in both
+                for (int j = 0; j < n8; j += 4) {
                     float v[4][4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -162,10 +175,10 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < L::RPT; ++i) {
                     if (i0 + i >= n) continue;
-                    float* o = row_of<float>(r.out, b, h, t0 + i0 + i) + c;
+                    T* o = row_of<T>(r.out, b, h, t0 + i0 + i) + c;
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
-                        o[m * L::CG] = acc[i][m];
+                        o[m * L::CG] = (T)acc[i][m];
                         bad = fmaf(acc[i][m], 0.f, bad);
                     }
                 }
@@ -182,7 +195,7 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
                 acc[i][0] = whole * v.x, acc[i][1] = whole * v.y, acc[i][2] = whole * v.z, acc[i][3] = whole * v.w;
             }
 #pragma unroll 8
-            for (int j = 0; j < L::C; ++j) {
+            for (int j = 0; j < n8; ++j) {
                 const float4 cv = *reinterpret_cast<float4*>(sm + L::CW + j * L::LD + x);
                 const float4 bv = *reinterpret_cast<float4*>(sm + L::B + j * L::LD + y);
                 const float cw[4] = {cv.x, cv.y, cv.z, cv.w};
@@ -206,15 +219,16 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
         const int behind = min(p.seg_len, p.T - sp.t0) - sp.n;
         const float zero[8] = {};
         for (int i = tid; i < behind * (D / 8); i += L::THREADS)
-            store8(row_of<float>(r.out, b, h, sp.t0 + sp.n + i / (D / 8)) + (i % (D / 8)) * 8, zero);
+            store8(row_of<T>(r.out, b, h, sp.t0 + sp.n + i / (D / 8)) + (i % (D / 8)) * 8, zero);
     }
     float* fin = STATE ? p.seg + (((size_t)blockIdx.y * p.B * p.H + bh) * p.nseg + seg) * D * D
                        : (p.nseg > 1 || !r.fin ? nullptr : r.fin + (size_t)bh * D * D);
     if (fin) {
-        for (int i = tid; i < D * D; i += L::THREADS) {
-            const float v = sm[L::S + (i / D) * L::LD + i % D];
-            fin[i] = v;
-            bad = fmaf(v, 0.f, bad);
+#pragma unroll 4
+        for (int i = tid * 4; i < D * D; i += L::THREADS * 4) {
+            const float4 v = *reinterpret_cast<float4*>(sm + L::S + (i / D) * L::LD + i % D);
+            *reinterpret_cast<float4*>(fin + i) = v;
+            bad = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, fmaf(v.w, 0.f, bad))));
         }
     }
     if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, sp.t0);

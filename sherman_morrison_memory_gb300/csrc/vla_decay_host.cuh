@@ -213,7 +213,7 @@ struct Call {
     DecayMaps maps;
 };
 
-template <int D, bool TC>
+template <int D, bool TC, typename T>
 vla_status launch(const Call& c, cudaStream_t s) {
     const long long BH = (long long)c.main.B * c.main.H;
     const long long grid = BH * c.main.nseg * c.roles;
@@ -234,7 +234,7 @@ vla_status launch(const Call& c, cudaStream_t s) {
         main<<<blocks * c.roles, L::THREADS, L::SMEM, s>>>(c.main, c.maps, c.roles);
     } else {
         using L = FmaLay<D>;
-        constexpr auto main = vla_decay_fma_kernel<D, false>, own = vla_decay_fma_kernel<D, true>;
+        constexpr auto main = vla_decay_fma_kernel<D, T, false>, own = vla_decay_fma_kernel<D, T, true>;
         if (!allow_smem<main>(L::SMEM) || !allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
         if (c.main.nseg > 1) {
             own<<<dim3(blocks, c.state_roles), L::THREADS, L::SMEM, s>>>(c.states);
@@ -245,21 +245,19 @@ vla_status launch(const Call& c, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
 }
 
-vla_status launch_call(const Call& c, int d, vla_dtype dt, cudaStream_t s) {
-    if (dt == VLA_BF16) {
-        switch (d) {
-            case 32: return launch<32, true>(c, s);
-            case 64: return launch<64, true>(c, s);
-            case 96: return launch<96, true>(c, s);
-            default: return launch<128, true>(c, s);
-        }
-    }
+template <bool TC, typename T>
+vla_status launch_d(const Call& c, int d, cudaStream_t s) {
     switch (d) {
-        case 32: return launch<32, false>(c, s);
-        case 64: return launch<64, false>(c, s);
-        case 96: return launch<96, false>(c, s);
-        default: return launch<128, false>(c, s);
+        case 32: return launch<32, TC, T>(c, s);
+        case 64: return launch<64, TC, T>(c, s);
+        case 96: return launch<96, TC, T>(c, s);
+        default: return launch<128, TC, T>(c, s);
     }
+}
+
+vla_status launch_call(const Call& c, int d, vla_dtype dt, cudaStream_t s) {
+    if (dt == VLA_F32) return launch_d<false, float>(c, d, s);
+    return c.main.T <= FMA_T ? launch_d<false, __nv_bfloat16>(c, d, s) : launch_d<true, __nv_bfloat16>(c, d, s);
 }
 
 // scratch of the larger of the two types' cuts, so that it need not be told the type
