@@ -8,7 +8,9 @@ Sequences are [B, H, T, d] float32 or bfloat16 with any strides: a
 projection's [B, T, H, d] output is passed as ``x.transpose(1, 2)`` and read
 in place. One whose last dimension is not dense, or whose rows do not start on
 16-byte boundaries, is copied first. Results that are sequences have the
-inputs' type; states, statistics and weights are float32.
+inputs' type; states, statistics and weights are float32. Any call may be
+captured in a CUDA graph after one eager call of the package on the device
+(which lays out the shared status record).
 """
 from __future__ import annotations
 
@@ -138,7 +140,6 @@ def vla_decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
     sequence b has only its first lengths[b] tokens; o is zero behind them.
     ``out`` = (o, S) preallocated; S may be ``state``. ``check=True``
     synchronises and raises on an in-kernel failure or a non-finite result.
-    May be captured in a CUDA graph after one eager call on the device.
     """
     for name, x in (("q", q), ("k", k), ("v", v)):
         _check_seq(x, name, None if x is q else q)

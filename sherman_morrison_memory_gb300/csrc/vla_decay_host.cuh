@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) vla_decay_scan_kernel(const __gr
                      : *reinterpret_cast<const float4*>(m + i);
     }
     float4* seg = reinterpret_cast<float4*>(p.seg + ((size_t)blockIdx.y * p.B * p.H + bh) * p.nseg * D * D + i);
+    SlowDecay slow(g, p.seg_len);
     auto place = [&](int k) { return r.reverse ? p.nseg - 1 - k : k; };
     for (int k0 = 0; k0 < p.nseg; k0 += AHEAD) {
         float4 own[AHEAD];
@@ -58,7 +59,8 @@ __global__ void __launch_bounds__(SCAN_THREADS) vla_decay_scan_kernel(const __gr
         for (int k = 0; k < AHEAD; ++k) {
             if (k0 + k >= p.nseg) break;
             const int m = place(k0 + k);
-            const float w = decay_pow(g, span_of(p, b, m).n);
+            const int n = span_of(p, b, m).n;
+            const float w = n < p.seg_len ? decay_pow(g, n) : slow.next();
             seg[(size_t)m * (D * D / 4)] = s;
             s = make_float4(fmaf(w, s.x, own[k].x), fmaf(w, s.y, own[k].y), fmaf(w, s.z, own[k].z),
                             fmaf(w, s.w, own[k].w));
@@ -154,7 +156,10 @@ constexpr unsigned long long kWaitNs = 2000000000ull;
 // waves of blocks that the SMs hold at once, each as long as a segment and what
 // a block's start and end take (6 chunks; 1 of the fp32 kernel's, which are as
 // much slower), and 5 for the scan. (At 32 heads
-// of 65,536 tokens, d = 128: 2.1 ms in one piece, 0.66 ms in 4, 0.58 ms in 19.)
+// of 65,536 tokens, d = 128: 1,394 us in one piece, 602 in 4, 571 in the 9 it
+// takes, 590 in 19; gradients of 2 x 32 heads of 8,191 tokens: 389 us in the one
+// piece it takes, 454 in 2; fp32, 40 heads of 1,021 tokens, d = 64: 174 in one,
+// 86 in the 6 it takes.)
 void plan(long long runs, long long state_runs, int T, int d, vla_dtype dt, int* nseg, int* seg_len) {
     const long long slots = (long long)(dt == VLA_BF16 ? 1 : 2) * sm_count();
     const int chunks = (T + 63) / 64;

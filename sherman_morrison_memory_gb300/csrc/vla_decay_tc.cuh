@@ -18,12 +18,16 @@
 // result (two parts left it 2e-6 off). P and Sb are rounded to bf16 once: o is
 // rounded to bf16 afterwards anyway, and a term meets only one of the two.
 //
-// What bounds it: shared memory. Per chunk at d = 128 its 128 bytes a cycle
-// carry 48 KB of loads and 16 KB of results through TMA, and the operands that
-// the MMAs fetch. So the decayed c goes to TMEM, not to shared memory, from
-// ldmatrix's transposed fragments; SC and the outputs are read in fragments
-// (16x256b) that stmatrix writes in whole 16-byte rows; and the weights, which
-// in fragments depend on the lane alone, stay in registers.
+// What bounds it. At d = 128 on all SMs memory: 64 KB a chunk, 1.5 us of 1.55.
+// Else the chain of one chunk's products through SC, P, OI and the read-out of
+// its accumulator, 0.9 us at d = 64 and 1.25 us at d = 96 and 128, beside the
+// chain through S (decayed c, T, S, Sb) of about the same length. The MMAs take a
+// third to a half of it: at N = 64 they are fed at shared memory's 128 bytes a
+// cycle. So the decayed c goes to TMEM, not to shared memory, from ldmatrix's
+// transposed fragments; SC and the outputs are read in fragments (16x256b) that
+// stmatrix writes in whole 16-byte rows; and the pairs' weights, which in
+// fragments depend on the lane and the blocks' distance, stay in registers.
+// (8 x 16 heads of 4,096 tokens, d = 96: 89 us, 4.5 TB/s of its sequences.)
 //
 // d is padded to DP = 64 or 128 columns by TMA's zero fill. DP is also the MMAs'
 // M, so that at d <= 64 a warp's quarter of the TMEM lanes holds 16 rows of the
@@ -617,6 +621,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
             return true;
         };
         bool ok = true;
+        SlowDecay whole(g, L::C);
         if constexpr (D % 64 != 0) {  // lanes that no row of c fills
             const uint32_t none[8] = {};
             __syncwarp();
@@ -632,7 +637,8 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
             if (m + 1 < chunks && !(ok = decayed(m + 1))) break;
             if (!(ok = wait_warp(t_done, m))) break;
             vla::tc_fence_after();
-            const float wn = decay_pow(g, min(L::C, sp.n - chunk0(m)));
+            const int n = min(L::C, sp.n - chunk0(m));
+            const float wn = n < L::C ? decay_pow(g, n) : whole.next();  // at most one chunk is shorter
             const float2 w2 = make_float2(wn, wn);
             if (rows_in) {
                 const uint32_t src_t = tm + lanes + L::T + half * HC;

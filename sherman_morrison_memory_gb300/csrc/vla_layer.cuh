@@ -69,6 +69,29 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
 // exp(g n) for a whole number n >= 0: 1 for n = 0 also where g is -inf
 __device__ __forceinline__ float decay_pow(float g, int n) { return n == 0 ? 1.f : expf(g * (float)n); }
 
+// The decay over n tokens, exp(g n), for a state that is multiplied by it again
+// and again: each factor is rounded, and what their roundings add up to is put
+// right by the next ones, so that a slow decay stays the same over a long
+// sequence (factors that are all rounded the same way can leave a state 1e-4
+// off over 65,536 tokens). 1 + expm1(x) shows the rounding where it matters: near 1.
+struct SlowDecay {
+    float w, rest, inv;  // the rounded factor, how far (relative) it is below the true one, 1 / w
+    float owed;          // ... and the product of all so far
+    __device__ __forceinline__ SlowDecay(float g, int n) {  // n > 0
+        const float m = expm1f(g * (float)n);
+        w = 1.f + m;
+        inv = w > 0.5f ? 1.f / w : 0.f;
+        rest = (m - (w - 1.f)) * inv;
+        owed = 0.f;
+    }
+    __device__ __forceinline__ float next() {
+        owed += rest;
+        const float v = fmaf(w, owed, w);
+        owed = fmaf(w - v, inv, owed);
+        return v;
+    }
+};
+
 // The pool entry of sequence b, or -1 for none: a negative slot, or, recorded
 // in the status, one out of range or (`unique`) one that an earlier sequence
 // of the call has. Called by a whole block, which gets one answer.

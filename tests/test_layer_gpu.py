@@ -294,6 +294,45 @@ def test_streams_and_graphs(d):
         assert same(w, res)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("H", [1, 200])
+def test_slow_decays_over_long_sequences(H, dtype):
+    """One write, then nothing: the state decays by the same factor thousands of times (in segments and in one piece)."""
+    d, T = 32, 65536
+    g = -torch.logspace(-6, -4, H).cuda()
+    k, v = (torch.zeros(1, H, T, d, dtype=dtype, device="cuda") for _ in range(2))
+    k[:, :, 0], v[:, :, 0] = (x[:, :, 0] for x in seqs(2, 1, H, 1, d, dtype))
+    S = vla.vla_decay_forward(k, k, v, g, check=True)[1].double().cpu()
+    want = torch.exp(g.double().cpu() * (T - 1))[None, :, None, None] * (v[:, :, 0, :, None].double() * k[:, :, 0, None, :].double()).cpu()
+    # T / 32 products, each off by at most half a step on its own: six times their standard deviation, and the
+    # factors' own roundings, which do not add up (bf16: the write itself in three exact parts)
+    bound = (6 * (T / 32 / 12) ** 0.5 + 8) * 2 * R.U
+    assert float(((S - want).abs() / want.abs().clamp(min=1e-30)).max()) <= bound
+
+
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+def test_more_heads_than_sms(d):
+    """Several blocks an SM one after another, lengths at every edge of a chunk, the same bits each time."""
+    B, H, T = 9, 24, 200
+    q, k, v, do = seqs(4, B, H, T, d, BF, seed=d)
+    g = -torch.exp2(torch.linspace(-8, 0, H)).cuda()
+    n = torch.tensor([200, 199, 193, 192, 191, 129, 64, 9, 1], dtype=torch.int32, device="cuda")
+    S0, dS = state_like(B, H, d, 1), state_like(B, H, d, 2)
+    fwd = vla.vla_decay_forward(q, k, v, g, 0.2, S0, lengths=n, check=True)
+    bwd = vla.vla_decay_backward(q, k, v, g, 0.2, S0, do, dS, lengths=n, check=True)
+    for _ in range(20):
+        o, S = vla.vla_decay_forward(q, k, v, g, 0.2, S0, lengths=n)
+        grads, dS0 = vla.vla_decay_backward(q, k, v, g, 0.2, S0, do, dS, lengths=n)
+        assert torch.equal(o, fwd[0]) and torch.equal(S, fwd[1]) and torch.equal(dS0, bwd[1])
+        assert all(torch.equal(a, b) for a, b in zip(grads, bwd[0]))
+    # every third head against the definition
+    pick = slice(None, None, 3)
+    part = lambda x: x[:, pick]  # noqa: E731
+    check_forward(part(q), part(k), part(v), g[pick], 0.2, part(S0), n, tuple(part(x) for x in fwd))
+    check_backward(part(q), part(k), part(v), g[pick], 0.2, part(S0), part(do), part(dS), n,
+                   (tuple(part(x) for x in bwd[0]), part(bwd[1])))
+
+
 # ---- single tokens ------------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", [F32, BF])
@@ -354,6 +393,32 @@ def test_long_pools():
     vla.vla_state_store(S, codes, scales, slots, check=True)
     assert torch.equal(vla.vla_state_load(codes, scales, slots, check=True).cpu(), R.store(S, 8)[0])
     assert not codes[1:N - 1].any()
+
+
+def test_serving_calls_in_a_graph():
+    """Step, store and load captured once and replayed: each replay goes one token on."""
+    B, H, d = 3, 2, 96
+    q, k, v = seqs(3, B, H, 4, d, BF, seed=6)
+    g = decays(H)
+    slots = torch.tensor([4, 0, 2], dtype=torch.int32, device="cuda")
+    pool = torch.zeros(5, H, d, d, device="cuda")
+    codes, scales = vla.vla_state_cache(3, (H, d, d), 8)
+    x = [torch.empty(B, H, d, dtype=BF, device="cuda") for _ in range(3)]
+    vla.vla_decay_step(*(s[:, :, 0] for s in (q, k, v)), g, pool.clone(), slots=slots)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = vla.vla_decay_step(*x, g, pool, 0.3, slots=slots)
+        vla.vla_state_store(pool[2:], codes, scales)
+        back = vla.vla_state_load(codes, scales)
+    pool.zero_()
+    outs = []
+    for t in range(4):
+        for a, s in zip(x, (q, k, v)):
+            a.copy_(s[:, :, t])
+        graph.replay()
+        outs.append(o.clone())
+        assert torch.equal(back.cpu(), R.store(pool[2:], 8)[0])
+    check_forward(q, k, v, g, 0.3, None, None, (torch.stack(outs, 2), pool[slots.long()]))
 
 
 # ---- layer norm of the readout ------------------------------------------------------------------------------------
