@@ -40,10 +40,11 @@ struct DecayArgs {
     const float* log_decay;
     const int* lengths;
     vla::DeviceStatus* status;
-    float* seg;    // states of segments [state role][BH][nseg][d][d], in place of init and fin where nseg > 1
+    float* seg;    // states of segments [state role][bhs][nseg][d][d], in place of init and fin where nseg > 1
     int seg_role[MAX_ROLES];  // which of them a role starts from
     int seg_t[MAX_ROLES];     // ... transposed
     int B, H, T;
+    int bh0, bhs;       // the launch's heads: [bh0, bh0 + bhs) of the B x H
     int nseg, seg_len;  // segments of the sequence and their tokens (a multiple of 64)
     unsigned long long wait_ns;
 };
@@ -54,6 +55,10 @@ struct Span {
 };
 __device__ __forceinline__ int seq_len(const DecayArgs& p, int b) {
     return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
+}
+// State of segment s of head bh for state role `role`.
+__device__ __forceinline__ float* seg_of(const DecayArgs& p, int role, int bh, int s, int d) {
+    return p.seg + (((size_t)role * p.bhs + (bh - p.bh0)) * p.nseg + s) * d * d;
 }
 __device__ __forceinline__ Span span_of(const DecayArgs& p, int b, int s) {
     const int t0 = s * p.seg_len;

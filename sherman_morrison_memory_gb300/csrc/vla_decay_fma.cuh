@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
     extern __shared__ __align__(16) float fma_sm[];
     float* sm = fma_sm;
     const int tid = threadIdx.x;
-    const int seg = blockIdx.x % p.nseg, bh = blockIdx.x / p.nseg, b = bh / p.H, h = bh % p.H;
+    const int seg = blockIdx.x % p.nseg, bh = p.bh0 + blockIdx.x / p.nseg, b = bh / p.H, h = bh % p.H;
     const Role& r = p.role[blockIdx.y];
     const float g = p.log_decay[h];
     const Span sp = span_of(p, b, seg);
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
     const float* init = r.init ? r.init + (size_t)bh * D * D : nullptr;
     int init_t = r.init_t;
     if (p.nseg > 1) {
-        init = STATE ? nullptr : p.seg + (((size_t)p.seg_role[blockIdx.y] * p.B * p.H + bh) * p.nseg + seg) * D * D;
+        init = STATE ? nullptr : seg_of(p, p.seg_role[blockIdx.y], bh, seg, D);
         init_t = p.seg_t[blockIdx.y];
     }
 #pragma unroll 4
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
         for (int i = tid; i < behind * (D / 8); i += L::THREADS)
             store8(row_of<T>(r.out, b, h, sp.t0 + sp.n + i / (D / 8)) + (i % (D / 8)) * 8, zero);
     }
-    float* fin = STATE ? p.seg + (((size_t)blockIdx.y * p.B * p.H + bh) * p.nseg + seg) * D * D
+    float* fin = STATE ? seg_of(p, blockIdx.y, bh, seg, D)
                        : (p.nseg > 1 || !r.fin ? nullptr : r.fin + (size_t)bh * D * D);
     if (fin) {
 #pragma unroll 4

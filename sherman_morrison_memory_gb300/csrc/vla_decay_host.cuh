@@ -35,7 +35,7 @@ template <int D>
 __global__ void __launch_bounds__(SCAN_THREADS) vla_decay_scan_kernel(const __grid_constant__ DecayArgs p,
                                                                       const __grid_constant__ ScanArgs q) {
     constexpr int BLOCKS = D * D / 4 / SCAN_THREADS, AHEAD = 8;
-    const int bh = blockIdx.x / BLOCKS, i = ((blockIdx.x % BLOCKS) * SCAN_THREADS + threadIdx.x) * 4;
+    const int bh = p.bh0 + blockIdx.x / BLOCKS, i = ((blockIdx.x % BLOCKS) * SCAN_THREADS + threadIdx.x) * 4;
     const int b = bh / p.H, h = bh % p.H;
     const ScanRole& r = q.role[blockIdx.y];
     const float g = p.log_decay[h];
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) vla_decay_scan_kernel(const __gr
         s = r.init_t ? make_float4(m[y * D + x], m[(y + 1) * D + x], m[(y + 2) * D + x], m[(y + 3) * D + x])
                      : *reinterpret_cast<const float4*>(m + i);
     }
-    float4* seg = reinterpret_cast<float4*>(p.seg + ((size_t)blockIdx.y * p.B * p.H + bh) * p.nseg * D * D + i);
+    float4* seg = reinterpret_cast<float4*>(seg_of(p, blockIdx.y, bh, 0, D) + i);
     SlowDecay slow(g, p.seg_len);
     auto place = [&](int k) { return r.reverse ? p.nseg - 1 - k : k; };
     for (int k0 = 0; k0 < p.nseg; k0 += AHEAD) {
@@ -149,19 +149,26 @@ __global__ void __launch_bounds__(STEP_THREADS) vla_decay_step_kernel(const T* _
 
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
-// The cut of a call into segments: `runs` runs of blocks (roles x B x H) for the
-// outputs and `state_runs` for the segments' own states. A cut costs the second
-// pass, over two of the three sequences, which takes 0.7 of the first; it pays
-// where the runs leave SMs idle. Time is counted in chunks of 64 tokens: the
-// waves of blocks that the SMs hold at once, each as long as a segment and what
-// a block's start and end take (6 chunks; 1 of the fp32 kernel's, which are as
-// much slower), and 5 for the scan. (At 32 heads
-// of 65,536 tokens, d = 128: 1,394 us in one piece, 602 in 4, 571 in the 9 it
-// takes, 590 in 19; gradients of 2 x 32 heads of 8,191 tokens: 389 us in the one
-// piece it takes, 454 in 2; fp32, 40 heads of 1,021 tokens, d = 64: 174 in one,
-// 86 in the 6 it takes.)
-void plan(long long runs, long long state_runs, int T, int d, vla_dtype dt, int* nseg, int* seg_len) {
-    const long long slots = (long long)(dt == VLA_BF16 ? 1 : 2) * sm_count();
+// A launch's heads and their cut into segments.
+struct Cut {
+    int bh0, bhs, nseg, seg_len;
+};
+
+int slots_of(int d, vla_dtype dt) { return (dt == VLA_BF16 ? 1 : 2) * sm_count(); }
+
+// The cut of `heads` heads, each `roles` runs of blocks for the outputs and
+// `state_roles` for the segments' own states, into segments; returns its time.
+// A cut costs the second pass, over two of the three sequences, which takes 0.7
+// of the first; it pays where the runs leave SMs idle. Time is counted in chunks
+// of 64 tokens: the waves of blocks that the SMs hold at once, each as long as a
+// segment and what a block's start and end take (6 chunks; 1 of the fp32
+// kernel's, which are as much slower), and 5 for the scan. (At 32 heads of 65,536
+// tokens, d = 128: 1,394 us in one piece, 602 in 4, 571 in the 9 it takes, 590
+// in 19; gradients of 4 x 8 heads of 4,096 tokens, d = 64: 67 us in the one
+// piece it takes, 91 in 4; fp32, 40 heads of 1,021 tokens, d = 64: 174 in one, 86
+// in the 6 it takes.)
+double plan(long long heads, int roles, int state_roles, int T, int d, vla_dtype dt, Cut* cut) {
+    const long long slots = slots_of(d, dt);
     const int chunks = (T + 63) / 64;
     auto waves = [&](long long blocks) { return (blocks + slots - 1) / slots; };
     const double ends = dt == VLA_BF16 ? 6 : 1;
@@ -170,12 +177,32 @@ void plan(long long runs, long long state_runs, int T, int d, vla_dtype dt, int*
     const int shortest = dt == VLA_BF16 ? 4 : 1;  // chunks of a segment
     for (int n = 1; n <= 64 && n * shortest <= std::max(shortest, chunks); ++n) {
         const int len = (chunks + n - 1) / n, segs = (chunks + len - 1) / len;
-        double t = (double)waves(runs * segs) * (len + ends);
-        if (segs > 1) t += 0.7 * (double)waves(state_runs * segs) * (len + ends) + 5 * ends / 6 + 0.1 * segs;
+        double t = (double)waves(heads * roles * segs) * (len + ends);
+        if (segs > 1) t += 0.7 * (double)waves(heads * state_roles * segs) * (len + ends) + 5 * ends / 6 + 0.1 * segs;
         if (n == 1 || t < best) best = t, best_len = len;
     }
-    *seg_len = std::max(1, best_len) * 64;
-    *nseg = std::max(1, (chunks + best_len - 1) / std::max(1, best_len));
+    cut->seg_len = std::max(1, best_len) * 64;
+    cut->nseg = std::max(1, (chunks + best_len - 1) / std::max(1, best_len));
+    return best;
+}
+
+// The launches of a call: all heads alike, or, where that is shorter, as many as
+// fill whole waves in one piece and the rest cut into segments after them.
+// (Gradients of 2 x 32 heads of 8,191 tokens, d = 128, 192 blocks on 152 SMs.)
+int plan_call(int B, int H, int roles, int state_roles, int T, int d, vla_dtype dt, Cut (&cut)[2]) {
+    const long long BH = (long long)B * H, wave = slots_of(d, dt) / roles;
+    cut[0] = Cut{0, (int)BH, 1, 0};
+    const double all = plan(BH, roles, state_roles, T, d, dt, &cut[0]);
+    const long long whole = wave > 0 ? BH / wave * wave : 0;
+    if (whole == 0 || whole == BH) return 1;
+    const int chunks = (T + 63) / 64;
+    Cut rest{(int)whole, (int)(BH - whole), 1, 0};
+    const double t = (double)(whole / wave) * (chunks + (dt == VLA_BF16 ? 6 : 1)) +
+                     plan(BH - whole, roles, state_roles, T, d, dt, &rest) + 2;
+    if (rest.nseg == 1 || t >= all) return 1;
+    cut[0] = Cut{0, (int)whole, 1, std::max(1, chunks) * 64};
+    cut[1] = rest;
+    return 2;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -216,42 +243,48 @@ struct Call {
     int roles, state_roles;
     ScanArgs scan;
     DecayMaps maps;
+    Cut cut[2];
+    int cuts;
 };
 
 template <int D, bool TC, typename T>
-vla_status launch(const Call& c, cudaStream_t s) {
-    const long long BH = (long long)c.main.B * c.main.H;
-    const long long grid = BH * c.main.nseg * c.roles;
-    if (grid > 2147483647LL || BH * (D * D / 4 / SCAN_THREADS) > 2147483647LL) return VLA_ERR_INVALID_ARG;
-    const unsigned blocks = (unsigned)(BH * c.main.nseg);
-    auto scan = [&] {
-        vla_decay_scan_kernel<D>
-            <<<dim3((unsigned)(BH * (D * D / 4 / SCAN_THREADS)), c.state_roles), SCAN_THREADS, 0, s>>>(c.main, c.scan);
-    };
-    if constexpr (TC) {
-        using L = TcLay<D>;
-        constexpr auto main = vla_decay_tc_kernel<D, false>, own = vla_decay_tc_kernel<D, true>;
-        if (!allow_smem<main>(L::SMEM) || !allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
-        if (c.main.nseg > 1) {
-            own<<<blocks * c.state_roles, L::THREADS, L::SMEM, s>>>(c.states, c.maps, c.state_roles);
-            scan();
+vla_status launch(Call& c, cudaStream_t s) {
+    for (int i = 0; i < c.cuts; ++i) {
+        const Cut& cut = c.cut[i];
+        for (DecayArgs* p : {&c.main, &c.states})
+            p->bh0 = cut.bh0, p->bhs = cut.bhs, p->nseg = cut.nseg, p->seg_len = cut.seg_len;
+        const long long grid = (long long)cut.bhs * cut.nseg * c.roles;
+        const long long scan_blocks = (long long)cut.bhs * (D * D / 4 / SCAN_THREADS);
+        if (grid > 2147483647LL || scan_blocks > 2147483647LL) return VLA_ERR_INVALID_ARG;
+        const unsigned blocks = (unsigned)(cut.bhs * cut.nseg);
+        auto scan = [&] {
+            vla_decay_scan_kernel<D><<<dim3((unsigned)scan_blocks, c.state_roles), SCAN_THREADS, 0, s>>>(c.main, c.scan);
+        };
+        if constexpr (TC) {
+            using L = TcLay<D>;
+            constexpr auto main = vla_decay_tc_kernel<D, false>, own = vla_decay_tc_kernel<D, true>;
+            if (!allow_smem<main>(L::SMEM) || !allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
+            if (cut.nseg > 1) {
+                own<<<blocks * c.state_roles, L::THREADS, L::SMEM, s>>>(c.states, c.maps, c.state_roles);
+                scan();
+            }
+            main<<<blocks * c.roles, L::THREADS, L::SMEM, s>>>(c.main, c.maps, c.roles);
+        } else {
+            using L = FmaLay<D>;
+            constexpr auto main = vla_decay_fma_kernel<D, T, false>, own = vla_decay_fma_kernel<D, T, true>;
+            if (!allow_smem<main>(L::SMEM) || !allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
+            if (cut.nseg > 1) {
+                own<<<dim3(blocks, c.state_roles), L::THREADS, L::SMEM, s>>>(c.states);
+                scan();
+            }
+            main<<<dim3(blocks, c.roles), L::THREADS, L::SMEM, s>>>(c.main);
         }
-        main<<<blocks * c.roles, L::THREADS, L::SMEM, s>>>(c.main, c.maps, c.roles);
-    } else {
-        using L = FmaLay<D>;
-        constexpr auto main = vla_decay_fma_kernel<D, T, false>, own = vla_decay_fma_kernel<D, T, true>;
-        if (!allow_smem<main>(L::SMEM) || !allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
-        if (c.main.nseg > 1) {
-            own<<<dim3(blocks, c.state_roles), L::THREADS, L::SMEM, s>>>(c.states);
-            scan();
-        }
-        main<<<dim3(blocks, c.roles), L::THREADS, L::SMEM, s>>>(c.main);
     }
     return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
 }
 
 template <bool TC, typename T>
-vla_status launch_d(const Call& c, int d, cudaStream_t s) {
+vla_status launch_d(Call& c, int d, cudaStream_t s) {
     switch (d) {
         case 32: return launch<32, TC, T>(c, s);
         case 64: return launch<64, TC, T>(c, s);
@@ -260,7 +293,7 @@ vla_status launch_d(const Call& c, int d, cudaStream_t s) {
     }
 }
 
-vla_status launch_call(const Call& c, int d, vla_dtype dt, cudaStream_t s) {
+vla_status launch_call(Call& c, int d, vla_dtype dt, cudaStream_t s) {
     if (dt == VLA_F32) return launch_d<false, float>(c, d, s);
     return c.main.T <= FMA_T ? launch_d<false, __nv_bfloat16>(c, d, s) : launch_d<true, __nv_bfloat16>(c, d, s);
 }
@@ -268,14 +301,15 @@ vla_status launch_call(const Call& c, int d, vla_dtype dt, cudaStream_t s) {
 // scratch of the larger of the two types' cuts, so that it need not be told the type
 size_t scratch_bytes_of(int B, int H, int T, int d, bool backward) {
     if (!good_sizes(B, H, T) || !good_d(d) || B == 0 || H == 0 || T == 0) return 0;
-    const long long BH = (long long)B * H;
-    int most = 1;
+    size_t most = 0;
     for (vla_dtype dt : {VLA_F32, VLA_BF16}) {
-        int nseg, len;
-        plan(BH * (backward ? 3 : 1), BH * (backward ? 2 : 1), T, d, dt, &nseg, &len);
-        most = std::max(most, nseg);
+        Cut cut[2];
+        const int n = plan_call(B, H, backward ? 3 : 1, backward ? 2 : 1, T, d, dt, cut);
+        const Cut& last = cut[n - 1];
+        if (last.nseg > 1)
+            most = std::max(most, (size_t)last.bhs * last.nseg * (backward ? 2 : 1) * d * d * sizeof(float));
     }
-    return most > 1 ? (size_t)BH * most * (backward ? 2 : 1) * d * d * sizeof(float) : 0;
+    return most;
 }
 
 vla_status copy_state(float* dst, const float* src, size_t n, cudaStream_t s) {
@@ -320,7 +354,7 @@ vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
     p.lengths = lengths;
     p.status = static_cast<vla::DeviceStatus*>(status);
     p.wait_ns = kWaitNs;
-    plan((long long)B * H, (long long)B * H, T, d, dtype, &p.nseg, &p.seg_len);
+    c.cuts = plan_call(B, H, 1, 1, T, d, dtype, c.cut);
     p.seg = static_cast<float*>(scratch);
     p.role[0] = Role{to_seq(q, B, H, T), to_seq(k, B, H, T), to_seq(v, B, H, T), to_seq(o, B, H, T),
                      S0, S_out, 0, 0, scale, scale, 1.f, 0, 1, 2};
@@ -364,7 +398,7 @@ vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
     p.lengths = lengths;
     p.status = static_cast<vla::DeviceStatus*>(status);
     p.wait_ns = kWaitNs;
-    plan(3LL * B * H, 2LL * B * H, T, d, dtype, &p.nseg, &p.seg_len);
+    c.cuts = plan_call(B, H, 3, 2, T, d, dtype, c.cut);
     p.seg = static_cast<float*>(scratch);
     p.role[0] = Role{G, V, K, to_seq(dq, B, H, T), S0, nullptr, 1, 0, scale, scale, 1.f, 3, 2, 1};
     p.role[1] = Role{V, G, Q, to_seq(dk, B, H, T), dS_T, nullptr, 1, 1, scale, 1.f, scale, 2, 3, 0};

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int ri = blockIdx.x % roles, rest = blockIdx.x / roles;
-    const int seg = rest % p.nseg, bh = rest / p.nseg, b = bh / p.H, h = bh % p.H;
+    const int seg = rest % p.nseg, bh = p.bh0 + rest / p.nseg, b = bh / p.H, h = bh % p.H;
     const Role& r = p.role[ri];
     const float g = p.log_decay[h];
     const Span sp = span_of(p, b, seg);
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
             const float* init = r.init ? r.init + (size_t)bh * D * D : nullptr;
             int init_t = r.init_t;
             if (p.nseg > 1) {
-                init = STATE ? nullptr : p.seg + (((size_t)p.seg_role[ri] * p.B * p.H + bh) * p.nseg + seg) * D * D;
+                init = STATE ? nullptr : seg_of(p, p.seg_role[ri], bh, seg, D);
                 init_t = p.seg_t[ri];
             }
 #pragma unroll
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
             }
             publish();
         }
-        float* fin = STATE ? p.seg + (((size_t)ri * p.B * p.H + bh) * p.nseg + seg) * D * D
+        float* fin = STATE ? seg_of(p, ri, bh, seg, D)
                            : (p.nseg > 1 || !r.fin ? nullptr : r.fin + (size_t)bh * D * D);
         if (ok && fin && rows_in) {
 #pragma unroll

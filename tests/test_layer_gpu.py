@@ -310,6 +310,23 @@ def test_slow_decays_over_long_sequences(H, dtype):
     assert float(((S - want).abs() / want.abs().clamp(min=1e-30)).max()) <= bound
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("B,H,T,d", [(1, 155, 700, 64), (2, 80, 1025, 32), (1, 56, 1500, 128)])
+def test_whole_waves_and_the_rest(B, H, T, d, dtype):
+    """A few heads more than fill the SMs: those are cut into segments, the others not."""
+    q, k, v, do = seqs(4, B, H, T, d, dtype, seed=d)
+    g = -torch.exp2(torch.linspace(-9, 0, H)).cuda()
+    n = torch.full((B,), T - 3, dtype=torch.int32, device="cuda")
+    S0, dS = state_like(B, H, d, 1), state_like(B, H, d, 2)
+    fwd = vla.vla_decay_forward(q, k, v, g, 0.2, S0, lengths=n, check=True)
+    bwd = vla.vla_decay_backward(q, k, v, g, 0.2, S0, do, dS, lengths=n, check=True)
+    pick = torch.tensor([0, H // 2, H - 4, H - 1])
+    part = lambda x: x[:, pick]  # noqa: E731
+    check_forward(part(q), part(k), part(v), g[pick], 0.2, part(S0), n, tuple(part(x) for x in fwd))
+    check_backward(part(q), part(k), part(v), g[pick], 0.2, part(S0), part(do), part(dS), n,
+                   (tuple(part(x) for x in bwd[0]), part(bwd[1])))
+
+
 @pytest.mark.parametrize("d", [32, 64, 96, 128])
 def test_more_heads_than_sms(d):
     """Several blocks an SM one after another, lengths at every edge of a chunk, the same bits each time."""
