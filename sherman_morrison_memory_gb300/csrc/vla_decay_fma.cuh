@@ -1,10 +1,17 @@
 // vla_decay_fma.cuh -- the operation of vla_decay.cuh on the FP32 pipes, for fp32
-// inputs and for the shortest bf16 calls: a block per (role, head, segment) goes through its tokens 32 at a time
-// with S and the tiles of a, b, c and the decayed c in shared memory. The next
-// 32 tokens' rows are on their way to registers meanwhile.
+// inputs and for the shortest bf16 calls: a block per (role, head, segment) goes
+// through its tokens 32 at a time with S and the tiles of a, b, c and the decayed c
+// in shared memory. The next 32 tokens' rows are on their way to registers meanwhile.
 //
-// Bound by shared memory: a value read there feeds 4 to 16 multiply-adds. (d =
-// 64, 40 heads of up to 1,021 tokens: 63 us for the outputs' launch, of 84 us.)
+// Bound by shared memory: its pipe gives a warp one value a lane a cycle, against
+// four multiply-adds, so a thread's tiles are as large as its registers allow: of S
+// 8 x 8 at d = 128, 6 x 6 at 96, 4 x 4 at 64, of the output 4 rows of d/32 columns.
+// (fp32, 4 x 16 heads of 4,096 tokens: d = 128 966 us, 1,139 with half as large
+// tiles; d = 64 343 against 399; gradients of d = 128 2,090 against 3,210.) At d =
+// 32 two warps a block give a thread four times as much of each tile (4 x 32 heads:
+// 220 us, 355 with eight); at d = 64 they leave too few warps an SM (355 us, eight
+// 343), and short bf16 calls want the threads for their latency (4 tokens, d = 64:
+// 5.0 us, 7.3 with two warps).
 //
 // STATE: only the segment's own state, from zero, is formed (of b and c).
 #pragma once
@@ -13,9 +20,9 @@
 
 namespace vla_layer {
 
-template <int D>
+template <int D, typename T>
 struct FmaLay {
-    static constexpr int C = 32, THREADS = 256;
+    static constexpr int C = 32, THREADS = D == 32 && sizeof(T) == 4 ? 64 : 256;
     static constexpr int LD = D + 4;  // row pitch: rows of a column of float4s lie in different banks
     static constexpr int PP = C + 4;  // of the pairs
     static constexpr int S = 0;
@@ -23,10 +30,15 @@ struct FmaLay {
     static constexpr int W = P + C * PP;  // weights: by lag, of the state to tokens
     static constexpr int FLOATS = W + 2 * C;
     static constexpr int SMEM = FLOATS * 4;
-    static constexpr int CG = D / 4;                               // groups of four columns
-    static constexpr int RG = D == 128 || D == 96 ? 8 : 1024 / D;  // row groups of the output tile
-    static constexpr int RPT = C / RG;
+    static constexpr int OCC = D == 128 ? 1 : D == 96 ? 2 : D == 64 ? 3 : THREADS == 64 ? 7 : 4;  // blocks an SM holds
+    static_assert(OCC * (SMEM + 1024) <= 228 * 1024, "shared memory");
     static constexpr int NPT = (C * (D / 8) + THREADS - 1) / THREADS;  // 8-value pieces of a tile a thread moves
+    // tiles of a thread: pairs, PR rows of columns j, j + PJ, ..; output, 4 rows
+    // of columns c, c + CG, ..; state, NG x NG squares of GW values, TW GW apart
+    static constexpr int PJ = THREADS == 64 ? 8 : 16, PC = C / PJ, PR = C * PJ / THREADS;
+    static constexpr int CG = THREADS / 8, OC = D / CG;
+    static constexpr int TW = THREADS == 64 ? 8 : 16, GW = D % (4 * TW) ? 2 : 4, NG = D / (GW * TW);
+    static_assert(NG * GW * TW == D && TW * TW == THREADS, "tiles");
 };
 
 __device__ __forceinline__ float dot4(float4 x, float4 y, float s) {
@@ -35,12 +47,13 @@ __device__ __forceinline__ float dot4(float4 x, float4 y, float s) {
 
 // bf16 calls of up to this many tokens run here too: their rows have so few
 // terms that the tensor cores' bf16 pairs do not average out and would show in
-// the result. (One token, 32 heads, d = 128: 12 us against the tensor cores' 10.)
+// the result. (One token, 32 heads, d = 128: 9.3 us against the tensor cores' 8.1.)
 constexpr int FMA_T = 8;
 
 template <int D, typename T, bool STATE>
-__global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_constant__ DecayArgs p) {
-    using L = FmaLay<D>;
+__global__ void __launch_bounds__(FmaLay<D, T>::THREADS, FmaLay<D, T>::OCC)
+    vla_decay_fma_kernel(const __grid_constant__ DecayArgs p) {
+    using L = FmaLay<D, T>;
     extern __shared__ __align__(16) float fma_sm[];
     float* sm = fma_sm;
     const int tid = threadIdx.x;
@@ -121,64 +134,70 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
         if (ci + 1 < chunks) fetch(ci + 1);
         if (!STATE) {
             {
-                const int i = tid / 8, j0 = tid % 8;
-                float acc[4] = {};
-#pragma unroll 8
-                for (int k = 0; k < D; k += 4) {
-                    const float4 a = *reinterpret_cast<float4*>(sm + L::A + i * L::LD + k);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        acc[m] = dot4(a, *reinterpret_cast<float4*>(sm + L::B + (j0 + 8 * m) * L::LD + k), acc[m]);
-                }
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int j = j0 + 8 * m, lag = rev ? j - i : i - j;
-                    sm[L::P + i * L::PP + j] = lag >= 0 && i < n && j < n ? acc[m] * sm[L::W + max(lag, 0)] : 0.f;
-                }
-            }
-            __syncthreads();
-            if (tid < L::CG * L::RG && tid / L::CG * L::RPT < n) {
-                // columns c, c + CG, ...: neighbouring lanes read neighbouring rows of S, whose pitch
-                // puts them in different banks, and write neighbouring values
-                const int c = tid % L::CG, i0 = (tid / L::CG) * L::RPT;
-                float acc[L::RPT][4] = {};
+                const int i0 = tid / L::PJ * L::PR, j0 = tid % L::PJ;
+                float acc[L::PR][L::PC] = {};
 #pragma unroll 4
                 for (int k = 0; k < D; k += 4) {
-                    float4 s[4];
+                    float4 a[L::PR];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) s[m] = *reinterpret_cast<float4*>(sm + L::S + (c + m * L::CG) * L::LD + k);
+                    for (int i = 0; i < L::PR; ++i) a[i] = *reinterpret_cast<float4*>(sm + L::A + (i0 + i) * L::LD + k);
 #pragma unroll
-                    for (int i = 0; i < L::RPT; ++i) {
-                        const float4 a = *reinterpret_cast<float4*>(sm + L::A + (i0 + i) * L::LD + k);
+                    for (int m = 0; m < L::PC; ++m) {
+                        const float4 v = *reinterpret_cast<float4*>(sm + L::B + (j0 + L::PJ * m) * L::LD + k);
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) acc[i][m] = dot4(a, s[m], acc[i][m]);
+                        for (int i = 0; i < L::PR; ++i) acc[i][m] = dot4(a[i], v, acc[i][m]);
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < L::RPT; ++i)
+                for (int i = 0; i < L::PR; ++i)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) acc[i][m] *= sm[L::W + L::C + i0 + i];
+                    for (int m = 0; m < L::PC; ++m) {
+                        const int j = j0 + L::PJ * m, lag = rev ? j - (i0 + i) : i0 + i - j;
+                        sm[L::P + (i0 + i) * L::PP + j] =
+                            lag >= 0 && i0 + i < n && j < n ? acc[i][m] * sm[L::W + max(lag, 0)] : 0.f;
+                    }
+            }
+            __syncthreads();
+            const int c = tid % L::CG, i0 = tid / L::CG * 4;
+            if (i0 < n) {
+                // columns c, c + CG, ...: neighbouring lanes read neighbouring rows of S, whose pitch
+                // puts them in different banks, and write neighbouring values
+                float acc[4][L::OC] = {};
 #pragma unroll 2
-                for (int j = 0; j < n8; j += 4) {
-                    float v[4][4];
+                for (int k = 0; k < D; k += 4) {
+                    float4 a[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<float4*>(sm + L::A + (i0 + i) * L::LD + k);
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) v[q][m] = sm[L::CC + (j + q) * L::LD + c + m * L::CG];
+                    for (int m = 0; m < L::OC; ++m) {
+                        const float4 v = *reinterpret_cast<float4*>(sm + L::S + (c + m * L::CG) * L::LD + k);
 #pragma unroll
-                    for (int i = 0; i < L::RPT; ++i) {
-                        const float4 w = *reinterpret_cast<float4*>(sm + L::P + (i0 + i) * L::PP + j);
-#pragma unroll
-                        for (int m = 0; m < 4; ++m)
-                            acc[i][m] = fmaf(w.x, v[0][m], fmaf(w.y, v[1][m], fmaf(w.z, v[2][m], fmaf(w.w, v[3][m], acc[i][m]))));
+                        for (int i = 0; i < 4; ++i) acc[i][m] = dot4(a[i], v, acc[i][m]);
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < L::RPT; ++i) {
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int m = 0; m < L::OC; ++m) acc[i][m] *= sm[L::W + L::C + i0 + i];
+#pragma unroll 1
+                for (int j = 0; j < n8; j += 4) {
+                    float4 w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<float4*>(sm + L::P + (i0 + i) * L::PP + j);
+#pragma unroll
+                    for (int m = 0; m < L::OC; ++m) {
+                        const float* v = sm + L::CC + j * L::LD + c + m * L::CG;
+                        const float4 x = make_float4(v[0], v[L::LD], v[2 * L::LD], v[3 * L::LD]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[i][m] = dot4(w[i], x, acc[i][m]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
                     if (i0 + i >= n) continue;
                     T* o = row_of<T>(r.out, b, h, t0 + i0 + i) + c;
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
+                    for (int m = 0; m < L::OC; ++m) {
                         o[m * L::CG] = (T)acc[i][m];
                         bad = fmaf(acc[i][m], 0.f, bad);
                     }
@@ -186,32 +205,53 @@ __global__ void __launch_bounds__(256, 2) vla_decay_fma_kernel(const __grid_cons
             }
             __syncthreads();
         }
-        const float whole = n < L::C ? decay_pow(g, n) : slow.next();
-        for (int blk = tid; blk < L::CG * L::CG; blk += L::THREADS) {
-            const int x = (blk / L::CG) * 4, y = (blk % L::CG) * 4;
-            float acc[4][4];
+        {
+            constexpr int N = L::NG * L::GW;
+            const float whole = n < L::C ? decay_pow(g, n) : slow.next();
+            const int x0 = tid / L::TW * L::GW, y0 = tid % L::TW * L::GW;
+            // GW values of each of NG groups
+            auto values = [&](const float* from, float (&v)[N]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 v = *reinterpret_cast<float4*>(sm + L::S + (x + i) * L::LD + y);
-                acc[i][0] = whole * v.x, acc[i][1] = whole * v.y, acc[i][2] = whole * v.z, acc[i][3] = whole * v.w;
-            }
-#pragma unroll 8
-            for (int j = 0; j < n8; ++j) {
-                const float4 cv = *reinterpret_cast<float4*>(sm + L::CW + j * L::LD + x);
-                const float4 bv = *reinterpret_cast<float4*>(sm + L::B + j * L::LD + y);
-                const float cw[4] = {cv.x, cv.y, cv.z, cv.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[i][0] = fmaf(cw[i], bv.x, acc[i][0]);
-                    acc[i][1] = fmaf(cw[i], bv.y, acc[i][1]);
-                    acc[i][2] = fmaf(cw[i], bv.z, acc[i][2]);
-                    acc[i][3] = fmaf(cw[i], bv.w, acc[i][3]);
+                for (int q = 0; q < L::NG; ++q) {
+                    const float* at = from + q * L::TW * L::GW;
+                    if constexpr (L::GW == 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(at);
+                        v[4 * q] = t.x, v[4 * q + 1] = t.y, v[4 * q + 2] = t.z, v[4 * q + 3] = t.w;
+                    } else {
+                        const float2 t = *reinterpret_cast<const float2*>(at);
+                        v[2 * q] = t.x, v[2 * q + 1] = t.y;
+                    }
                 }
+            };
+            float acc[N][N];
+            auto row = [&](int i) { return sm + L::S + (x0 + i / L::GW * L::TW * L::GW + i % L::GW) * L::LD + y0; };
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                values(row(i), acc[i]);
+#pragma unroll
+                for (int m = 0; m < N; ++m) acc[i][m] *= whole;
+            }
+#pragma unroll 2
+            for (int j = 0; j < n8; ++j) {
+                float cv[N], bv[N];
+                values(sm + L::CW + j * L::LD + x0, cv);
+                values(sm + L::B + j * L::LD + y0, bv);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int m = 0; m < N; ++m) acc[i][m] = fmaf(cv[i], bv[m], acc[i][m]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(sm + L::S + (x + i) * L::LD + y) =
-                    make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int q = 0; q < L::NG; ++q) {
+                    float* to = row(i) + q * L::TW * L::GW;
+                    if constexpr (L::GW == 4)
+                        *reinterpret_cast<float4*>(to) =
+                            make_float4(acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]);
+                    else
+                        *reinterpret_cast<float2*>(to) = make_float2(acc[i][2 * q], acc[i][2 * q + 1]);
+                }
         }
     }
     __syncthreads();

@@ -154,31 +154,47 @@ struct Cut {
     int bh0, bhs, nseg, seg_len;
 };
 
-int slots_of(int d, vla_dtype dt) { return (dt == VLA_BF16 ? 1 : 2) * sm_count(); }
+// The time of so many blocks, in that of one with an SM to itself. The bf16
+// kernel has an SM to itself; the fp32 kernel's blocks share one, but leave little
+// idle to share. (us a 64 tokens for 1, 2, 3, .. of them an SM: d = 32 8.5, 9, 11
+// and, for 7, 18.5; d = 64 10.8, 17, 25; d = 96 15.5, 27.5; d = 128 23.)
+double waves(long long blocks, int d, vla_dtype dt) {
+    int fit = 1;
+    double more = 0;
+    if (dt == VLA_F32 && d == 32) fit = FmaLay<32, float>::OCC, more = 0.2;
+    if (dt == VLA_F32 && d == 64) fit = FmaLay<64, float>::OCC, more = 0.65;
+    if (dt == VLA_F32 && d == 96) fit = FmaLay<96, float>::OCC, more = 0.77;
+    const long long sms = sm_count(), full = blocks / (sms * fit), rest = (blocks - full * sms * fit + sms - 1) / sms;
+    return (double)full * (1 + more * (fit - 1)) + (rest ? 1 + more * (double)(rest - 1) : 0);
+}
+
+// what a block's start and end take, in chunks of 64 tokens
+double ends_of(vla_dtype dt) { return dt == VLA_BF16 ? 6 : 0.5; }
 
 // The cut of `heads` heads, each `roles` runs of blocks for the outputs and
 // `state_roles` for the segments' own states, into segments; returns its time.
 // A cut costs the second pass, over two of the three sequences, which takes 0.7
-// of the first; it pays where the runs leave SMs idle. Time is counted in chunks
-// of 64 tokens: the waves of blocks that the SMs hold at once, each as long as a
-// segment and what a block's start and end take (6 chunks; 1 of the fp32
-// kernel's, which are as much slower), and 5 for the scan. (At 32 heads of 65,536
-// tokens, d = 128: 1,394 us in one piece, 602 in 4, 571 in the 9 it takes, 590
-// in 19; gradients of 4 x 8 heads of 4,096 tokens, d = 64: 67 us in the one
-// piece it takes, 91 in 4; fp32, 40 heads of 1,021 tokens, d = 64: 174 in one, 86
-// in the 6 it takes.)
+// of the first (0.33 in fp32, where it leaves out most of the products); it pays
+// where the runs leave SMs idle. Time is counted in chunks of 64 tokens: that of
+// the blocks, each as long as a segment and its start and end, and of the scan.
+// (At 32 heads of 65,536 tokens, d = 128: 1,394 us in one piece, 602 in 4, 571 in
+// the 9 it takes, 590 in 19; gradients of 4 x 8 heads of 4,096 tokens, d = 64: 67
+// us in the one piece it takes, 91 in 4; fp32, 40 heads of 1,021 tokens, d = 64:
+// 178 in one, 85 in 6, 79 in the 8 it takes; their gradients 180 in the one piece
+// it takes, 198 in 8.)
 double plan(long long heads, int roles, int state_roles, int T, int d, vla_dtype dt, Cut* cut) {
-    const long long slots = slots_of(d, dt);
     const int chunks = (T + 63) / 64;
-    auto waves = [&](long long blocks) { return (blocks + slots - 1) / slots; };
-    const double ends = dt == VLA_BF16 ? 6 : 1;
+    const bool bf16 = dt == VLA_BF16;
+    const double ends = ends_of(dt), second = bf16 ? 0.7 : 0.33;
     double best = 0;
     int best_len = chunks;
-    const int shortest = dt == VLA_BF16 ? 4 : 1;  // chunks of a segment
+    const int shortest = bf16 ? 4 : 1;  // chunks of a segment
     for (int n = 1; n <= 64 && n * shortest <= std::max(shortest, chunks); ++n) {
         const int len = (chunks + n - 1) / n, segs = (chunks + len - 1) / len;
-        double t = (double)waves(heads * roles * segs) * (len + ends);
-        if (segs > 1) t += 0.7 * (double)waves(heads * state_roles * segs) * (len + ends) + 5 * ends / 6 + 0.1 * segs;
+        double t = waves(heads * roles * segs, d, dt) * (len + ends);
+        if (segs > 1)
+            t += second * waves(heads * state_roles * segs, d, dt) * (len + ends) +
+                 (bf16 ? 5 + 0.1 * segs : 0.5 + 0.01 * segs);
         if (n == 1 || t < best) best = t, best_len = len;
     }
     cut->seg_len = std::max(1, best_len) * 64;
@@ -190,14 +206,14 @@ double plan(long long heads, int roles, int state_roles, int T, int d, vla_dtype
 // fill whole waves in one piece and the rest cut into segments after them.
 // (Gradients of 2 x 32 heads of 8,191 tokens, d = 128, 192 blocks on 152 SMs.)
 int plan_call(int B, int H, int roles, int state_roles, int T, int d, vla_dtype dt, Cut (&cut)[2]) {
-    const long long BH = (long long)B * H, wave = slots_of(d, dt) / roles;
+    const long long BH = (long long)B * H, wave = sm_count() / roles;
     cut[0] = Cut{0, (int)BH, 1, 0};
     const double all = plan(BH, roles, state_roles, T, d, dt, &cut[0]);
     const long long whole = wave > 0 ? BH / wave * wave : 0;
     if (whole == 0 || whole == BH) return 1;
     const int chunks = (T + 63) / 64;
     Cut rest{(int)whole, (int)(BH - whole), 1, 0};
-    const double t = (double)(whole / wave) * (chunks + (dt == VLA_BF16 ? 6 : 1)) +
+    const double t = waves(whole / wave * sm_count(), d, dt) * (chunks + ends_of(dt)) +
                      plan(BH - whole, roles, state_roles, T, d, dt, &rest) + 2;
     if (rest.nseg == 1 || t >= all) return 1;
     cut[0] = Cut{0, (int)whole, 1, std::max(1, chunks) * 64};
@@ -270,7 +286,7 @@ vla_status launch(Call& c, cudaStream_t s) {
             }
             main<<<blocks * c.roles, L::THREADS, L::SMEM, s>>>(c.main, c.maps, c.roles);
         } else {
-            using L = FmaLay<D>;
+            using L = FmaLay<D, T>;
             constexpr auto main = vla_decay_fma_kernel<D, T, false>, own = vla_decay_fma_kernel<D, T, true>;
             if (!allow_smem<main>(L::SMEM) || !allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
             if (cut.nseg > 1) {
