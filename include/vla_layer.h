@@ -56,7 +56,9 @@ typedef struct {
  * them are written as zero, whatever the inputs hold there, and the final
  * state is the one after the sequence's own last token.
  *
- * A NaN or Inf in an output or a final state sets VLA_ERR_NONFINITE in the
+ * A token's NaN or Inf reaches the results that depend on it, as the formulas
+ * have it, and no others: no earlier row of o or dq, no later one of dk or dv.
+ * One in an output or a final state sets VLA_ERR_NONFINITE in the
  * status record; a bounded in-kernel wait that ran out VLA_ERR_TIMEOUT. */
 
 /* Device scratch a call needs (0 when it needs none, or for sizes the call

@@ -65,4 +65,112 @@ __device__ __forceinline__ Span span_of(const DecayArgs& p, int b, int s) {
     return Span{t0, max(0, min(p.seg_len, seq_len(p, b) - t0))};
 }
 
+// Start of a role's S (null for 0; `init_t`: transposed) and where its end goes (or null).
+template <int D, bool STATE>
+__device__ __forceinline__ const float* start_of(const DecayArgs& p, int role, int bh, int seg, int& init_t) {
+    const Role& r = p.role[role];
+    init_t = p.nseg > 1 ? p.seg_t[role] : r.init_t;
+    if (p.nseg > 1) return STATE ? nullptr : seg_of(p, p.seg_role[role], bh, seg, D);
+    return r.init ? r.init + (size_t)bh * D * D : nullptr;
+}
+template <int D, bool STATE>
+__device__ __forceinline__ float* end_of(const DecayArgs& p, int role, int bh, int seg) {
+    if (STATE) return seg_of(p, role, bh, seg, D);
+    return p.nseg > 1 || !p.role[role].fin ? nullptr : p.role[role].fin + (size_t)bh * D * D;
+}
+
+// A block whose outputs are not all finite asks whether they are that before their
+// time: a chunk's pairs, zero above the diagonal, carry an Inf or NaN in c to the
+// tokens that come before it in its chunk of C (zero times Inf). True if a
+// column's first such value has any. `first`: D ints of shared memory.
+template <int D, typename T, int THREADS, int C>
+__device__ __forceinline__ bool seen_too_early(const DecayArgs& p, const Role& r, int b, int h, const Span sp, int* first) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += THREADS) first[i] = sp.n;
+    __syncthreads();
+    for (int i = threadIdx.x; i < sp.n * (D / 8); i += THREADS) {
+        const int j = i / (D / 8), col = i % (D / 8) * 8;
+        float v[8];
+        load8(row_of<T>(r.c, b, h, sp.t0 + j) + col, v);
+        for (int e = 0; e < 8; ++e)
+            if (!(fabsf(v[e]) < __int_as_float(0x7F800000))) atomicMin(first + col + e, r.reverse ? sp.n - 1 - j : j);
+    }
+    __syncthreads();
+    bool early = false;
+    for (int i = threadIdx.x; i < D; i += THREADS) {
+        // against time a segment's first chunk in order is the one that may be shorter
+        const int f = first[i], head = r.reverse ? (sp.n - 1) % C + 1 : C;
+        early |= f < sp.n && (f < head ? f > 0 : (f - head) % C != 0);
+    }
+    return __syncthreads_or(early);
+}
+
+// The operation a token at a time, as the recurrence has it:
+//   S <- l S + k_st c b^T,  out = w_st S a        (in the order of time)
+//   S <- S + k_st c b^T,  out = w_st S a,  S <- l S   (against it)
+// for the tokens of a block whose chunks cannot give it (seen_too_early()). S is in
+// shared memory, with LN lanes a row, which nobody else reads; tokens come in 8 at a
+// time. (152 heads of 4,096 tokens, d = 128, an Inf in the middle of each: 6.6 ms, 0.15 without.)
+template <int D, typename T, int THREADS, bool STATE>
+__device__ __noinline__ void by_token(const DecayArgs& p, int role, int bh, int seg, float* sm) {
+    constexpr int LN = THREADS >= 4 * D ? 4 : 2, LD = D + 4, TOK = 8;
+    static_assert(THREADS >= LN * D && LN * D % 32 == 0, "whole warps of rows");
+    float *S = sm, *rows = sm + D * LD;  // [D][LD] and a, b, c of TOK tokens, D * LD + 3 * TOK * D floats
+    const Role& r = p.role[role];
+    const int tid = threadIdx.x, lane = tid % LN, x = tid / LN, b = bh / p.H, h = bh % p.H;
+    const bool rev = r.reverse;
+    const float g = p.log_decay[h];
+    const Span sp = span_of(p, b, seg);
+    int init_t;
+    const float* init = start_of<D, STATE>(p, role, bh, seg, init_t);
+    if (x < D)
+        for (int y = lane; y < D; y += LN) S[x * LD + y] = !init ? 0.f : init_t ? init[y * D + x] : init[x * D + y];
+    float bad = 0.f;
+    SlowDecay slow(g, 1);
+    for (int m = 0; m < sp.n; m += TOK) {
+        const int k = min(TOK, sp.n - m);
+        auto token = [&](int j) { return sp.t0 + (rev ? sp.n - 1 - (m + j) : m + j); };
+        __syncthreads();
+        for (int i = tid; i < 3 * TOK * (D / 8); i += THREADS) {
+            const int q = i / (TOK * (D / 8)), j = i / (D / 8) % TOK, col = i % (D / 8) * 8;
+            if (j >= k || (STATE && q == 0)) continue;
+            float v[8];
+            load8(row_of<T>(q == 0 ? r.a : q == 1 ? r.b : r.c, b, h, token(j)) + col, v);
+            store8(rows + (q * TOK + j) * D + col, v);
+        }
+        __syncthreads();
+        if (x >= D) continue;
+        for (int j = 0; j < k; ++j) {
+            const float l = slow.next(), c = r.k_st * rows[(2 * TOK + j) * D + x];
+            const float *av = rows + j * D, *bv = rows + (TOK + j) * D;
+            float acc = 0.f;
+            for (int y = lane; y < D; y += LN) {
+                const float s = fmaf(c, bv[y], rev ? S[x * LD + y] : l * S[x * LD + y]);
+                if (!STATE) acc = fmaf(s, av[y], acc);
+                S[x * LD + y] = rev ? l * s : s;
+            }
+            if constexpr (!STATE) {
+#pragma unroll
+                for (int i = 1; i < LN; i <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, i);
+                acc *= r.w_st;
+                bad = fmaf(acc, 0.f, bad);
+                if (lane == 0) row_of<T>(r.out, b, h, token(j))[x] = (T)acc;
+            }
+        }
+    }
+    if (!STATE) {  // rows behind the sequence's last token
+        const int behind = min(p.seg_len, p.T - sp.t0) - sp.n;
+        const float zero[8] = {};
+        for (int i = tid; i < behind * (D / 8); i += THREADS)
+            store8(row_of<T>(r.out, b, h, sp.t0 + sp.n + i / (D / 8)) + (i % (D / 8)) * 8, zero);
+    }
+    float* fin = end_of<D, STATE>(p, role, bh, seg);
+    if (fin && x < D)
+        for (int y = lane; y < D; y += LN) {
+            fin[x * D + y] = S[x * LD + y];
+            bad = fmaf(S[x * LD + y], 0.f, bad);
+        }
+    if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, sp.t0);
+}
+
 }  // namespace vla_layer

@@ -84,12 +84,8 @@ __global__ void __launch_bounds__(FmaLay<D, T>::THREADS, FmaLay<D, T>::OCC)
     };
     if (chunks > 0) fetch(0);
 
-    const float* init = r.init ? r.init + (size_t)bh * D * D : nullptr;
-    int init_t = r.init_t;
-    if (p.nseg > 1) {
-        init = STATE ? nullptr : seg_of(p, p.seg_role[blockIdx.y], bh, seg, D);
-        init_t = p.seg_t[blockIdx.y];
-    }
+    int init_t;
+    const float* init = start_of<D, STATE>(p, blockIdx.y, bh, seg, init_t);
 #pragma unroll 4
     for (int i = tid * 4; i < D * D; i += L::THREADS * 4) {
         const int x = i / D, y = i % D;
@@ -255,16 +251,21 @@ __global__ void __launch_bounds__(FmaLay<D, T>::THREADS, FmaLay<D, T>::OCC)
         }
     }
     __syncthreads();
-    // rows behind the sequence's last token
-    if (!STATE) {
+    if constexpr (!STATE) {
+        // fin, which may be init, is not written yet
+        static_assert(L::FLOATS >= D * (D + 4) + 24 * D, "by_token's floats");
+        if (__syncthreads_or(bad != bad) &&
+            seen_too_early<D, T, L::THREADS, L::C>(p, r, b, h, sp, reinterpret_cast<int*>(sm + L::A))) {
+            by_token<D, T, L::THREADS, STATE>(p, blockIdx.y, bh, seg, sm);
+            return;
+        }
+        // rows behind the sequence's last token
         const int behind = min(p.seg_len, p.T - sp.t0) - sp.n;
         const float zero[8] = {};
         for (int i = tid; i < behind * (D / 8); i += L::THREADS)
             store8(row_of<T>(r.out, b, h, sp.t0 + sp.n + i / (D / 8)) + (i % (D / 8)) * 8, zero);
     }
-    float* fin = STATE ? seg_of(p, blockIdx.y, bh, seg, D)
-                       : (p.nseg > 1 || !r.fin ? nullptr : r.fin + (size_t)bh * D * D);
-    if (fin) {
+    if (float* fin = end_of<D, STATE>(p, blockIdx.y, bh, seg)) {
 #pragma unroll 4
         for (int i = tid * 4; i < D * D; i += L::THREADS * 4) {
             const float4 v = *reinterpret_cast<float4*>(sm + L::S + (i / D) * L::LD + i % D);

@@ -294,12 +294,31 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
         const bool ok = wait_on(w, parity & 1, abort_flag, p.wait_ns, p.status, warp / 4, bh);
         return __all_sync(0xffffffffu, ok) != 0;
     };
+    // The same for what has to end before the block does, also where a wait has run out.
+    auto drain_warp = [&](uint64_t* w, uint32_t parity) {
+        if (!__all_sync(0xffffffffu, vla::mbar_try_wait(w, parity & 1)))
+            vla::mbar_wait_slow(w, parity & 1, nullptr, p.wait_ns);
+        __syncwarp();
+    };
     auto arrive_warp = [&](uint64_t* w) {  // one arrival a warp
         __syncwarp();
         if (lane == 0) vla::mbar_arrive(w);
     };
     // first token (within the segment) of the m-th chunk in the role's order
     auto chunk0 = [&](int m) { return (rev ? chunks - 1 - m : m) * L::C; };
+
+    // S, of warps 4-11. A warp has the rows [xb, xb + RW), xb = RW quad, and half of
+    // the columns. Where the rows fill its 32 lanes, a lane has a row's: S[k] holds
+    // columns 2 k + {0, 1} of the half. Where they are 16, in fragments: S[4 u + k]
+    // holds columns 16 u + 8 (k / 2) + {0, 1} (from the lane's first) of row lane / 4
+    // + 8 (k % 2).
+    constexpr bool FRAG = L::NH == 1;
+    constexpr int HC = D / 2, NU = HC / 16, NS = L::NH * NU * 4;
+    const int id = tid - 128, half = id / 128, quad = warp & 3;
+    auto row = [&](int k) { return quad * L::RW + (FRAG ? (lane >> 2) + 8 * (k % 2) : lane); };
+    auto col = [&](int k) { return half * HC + (FRAG ? 2 * (lane & 3) + 16 * (k / 4) + 8 * ((k % 4) / 2) : 2 * k); };
+    float2 S[NS];
+    bool state_ok = false;  // S is the end state
 
     // The whole warps run the MMA loops, so that operands stay in uniform
     // registers, and one elected thread issues: issued under a test of the lane,
@@ -370,10 +389,10 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
         }
         if (*abort_flag)  // leave only once the copies under way have landed
             for (int m = max(0, loaded - L::NST); m < loaded; ++m)
-                vla::mbar_wait(full + m % L::NST, (m / L::NST) & 1, nullptr, p.wait_ns);
+                drain_warp(full + m % L::NST, m / L::NST);
         if (one) vla::tc_commit(drained);  // what was issued has finished before the block frees its TMEM
         __syncwarp();
-        vla::mbar_wait(drained, 0, nullptr, p.wait_ns);
+        drain_warp(drained, 0);
     } else if (warp == 15) {  // ---- MMAs of the pairs
         const bool one = elect_one();
         const uint32_t id_sc = idesc_bf16(128, 64, 0, 0), id_oi = idesc_bf16(L::DP, 64, 1, 0);
@@ -415,7 +434,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
             }
             if (one) vla::tc_commit(drained + 1);
             __syncwarp();
-            vla::mbar_wait(drained + 1, 0, nullptr, p.wait_ns);
+            drain_warp(drained + 1, 0);
         }
     } else if (warp >= 12) {  // ---- P
         // In blocks of 8 x 8 pairs: those of the later half of pairs are never
@@ -491,29 +510,12 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
                     : body(integral_constant<int, 1>{}, integral_constant<bool, false>{});
         }
     } else if (warp >= 4) {  // ---- the decayed c in parts, and S
-        // A warp has the state's rows [xb, xb + RW) and half of its columns. Where
-        // the rows fill its 32 lanes, a lane has a row's: S[k] holds columns 2 k +
-        // {0, 1} of the half. Where they are 16, in fragments: S[4 u + k] holds
-        // columns 16 u + 8 (k / 2) + {0, 1} (from the lane's first) of row lane / 4
-        // + 8 (k % 2).
-        constexpr bool FRAG = L::NH == 1;
-        constexpr int HC = D / 2, NU = HC / 16, NS = L::NH * NU * 4;
-        const int id = tid - 128, half = id / 128, quad = warp & 3;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const int xb = quad * L::RW;
         const bool rows_in = xb < D;  // else zero throughout
-        auto row = [&](int k) { return xb + (FRAG ? (lane >> 2) + 8 * (k % 2) : lane); };
-        auto col = [&](int k) {
-            return half * HC + (FRAG ? 2 * (lane & 3) + 16 * (k / 4) + 8 * ((k % 4) / 2) : 2 * k);
-        };
-        float2 S[NS];
         {
-            const float* init = r.init ? r.init + (size_t)bh * D * D : nullptr;
-            int init_t = r.init_t;
-            if (p.nseg > 1) {
-                init = STATE ? nullptr : seg_of(p, p.seg_role[ri], bh, seg, D);
-                init_t = p.seg_t[ri];
-            }
+            int init_t;
+            const float* init = start_of<D, STATE>(p, ri, bh, seg, init_t);
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
                 const int x = row(k), y = col(k);
@@ -665,19 +667,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
             }
             publish();
         }
-        float* fin = STATE ? seg_of(p, ri, bh, seg, D)
-                           : (p.nseg > 1 || !r.fin ? nullptr : r.fin + (size_t)bh * D * D);
-        if (ok && fin && rows_in) {
-#pragma unroll
-            for (int k = 0; k < NS; ++k) {
-                bad = fma2(S[k], zero2, bad);
-                if constexpr (FRAG)
-                    *reinterpret_cast<float2*>(fin + row(k) * D + col(k)) = S[k];
-                else if (k % 2 == 0)
-                    *reinterpret_cast<float4*>(fin + row(k) * D + col(k)) =
-                        make_float4(S[k].x, S[k].y, S[k + 1].x, S[k + 1].y);
-            }
-        }
+        state_ok = ok;
     } else if (!STATE) {  // ---- output
         constexpr int NH = L::NH;
         const int lc = 2 * (lane & 3);
@@ -766,13 +756,35 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
     }
 
     __syncwarp();
-    // rows behind the sequence's last chunk (those within it were stored as zero)
-    if (!STATE) {
+    bool again = false;
+    if constexpr (!STATE) {
+        // All copies and MMAs of the block are done; the final state, which may
+        // replace the initial one, is written only after this.
+        static_assert(L::SMEM >= (D * (D + 4) + 24 * D) * 4, "by_token's floats");
+        if (__syncthreads_or(bad.x != bad.x || bad.y != bad.y) && *abort_flag == 0)
+            again = seen_too_early<D, __nv_bfloat16, L::THREADS, L::C>(p, r, b, h, sp, reinterpret_cast<int*>(sm));
+        if (again) {
+            by_token<D, __nv_bfloat16, L::THREADS, STATE>(p, ri, bh, seg, reinterpret_cast<float*>(sm));
+            bad = zero2;  // recorded there
+        }
+        // rows behind the sequence's last chunk (those within it were stored as zero)
         const int done = min(chunks * L::C, p.T - sp.t0);
         const int behind = min(p.seg_len, p.T - sp.t0) - done;
         const float zero[8] = {};
         for (int i = tid; i < behind * (D / 8); i += L::THREADS)
             store8(row_of<__nv_bfloat16>(r.out, b, h, sp.t0 + done + i / (D / 8)) + (i % (D / 8)) * 8, zero);
+    }
+    float* fin = again || !state_ok ? nullptr : end_of<D, STATE>(p, ri, bh, seg);
+    if (fin && quad * L::RW < D) {
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            bad = fma2(S[k], zero2, bad);
+            if constexpr (FRAG)
+                *reinterpret_cast<float2*>(fin + row(k) * D + col(k)) = S[k];
+            else if (k % 2 == 0)
+                *reinterpret_cast<float4*>(fin + row(k) * D + col(k)) =
+                    make_float4(S[k].x, S[k].y, S[k + 1].x, S[k + 1].y);
+        }
     }
     if ((bad.x != bad.x || bad.y != bad.y) && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, sp.t0);
     vla::tc_fence_before();
