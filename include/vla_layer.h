@@ -48,8 +48,11 @@ typedef struct {
  * S has the layout of vla.h's states ([B, H, d, d], S[i][j] maps key
  * coordinate j to output coordinate i). log_decay: [H] float32; 0 gives
  * the plain cumulative state, -inf forgets everything before the token,
- * positive values are taken as they are (the state grows). It is a constant of
- * the layer like lambda0 of vla_forward(): no gradient is formed for it.
+ * positive values are taken as they are: the state grows, and results that
+ * overflow are Inf or NaN. (A head that grows by more than a factor of two a
+ * token in bf16, or four in fp32, is computed a token at a time.) It is a
+ * constant of the layer like lambda0 of vla_forward(): no gradient is formed
+ * for it.
  *
  * lengths: NULL, or [B] int32 on the device: sequence b has
  * min(max(lengths[b], 0), T) tokens. Rows of o (or of the gradients) behind

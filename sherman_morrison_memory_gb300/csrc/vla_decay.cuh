@@ -79,6 +79,11 @@ __device__ __forceinline__ float* end_of(const DecayArgs& p, int role, int bh, i
     return p.nseg > 1 || !p.role[role].fin ? nullptr : p.role[role].fin + (size_t)bh * D * D;
 }
 
+// Whether the powers of a growing head's factor over a chunk of C tokens are too
+// large to be formed apart from what they multiply (2^64, half of the exponent's
+// range): a block then goes token by token.
+__device__ __forceinline__ bool outgrows(float g, int C) { return g * (float)C > 44.f; }
+
 // A block whose outputs are not all finite asks whether they are that before their
 // time: a chunk's pairs, zero above the diagonal, carry an Inf or NaN in c to the
 // tokens that come before it in its chunk of C (zero times Inf). True if a
@@ -108,7 +113,7 @@ __device__ __forceinline__ bool seen_too_early(const DecayArgs& p, const Role& r
 // The operation a token at a time, as the recurrence has it:
 //   S <- l S + k_st c b^T,  out = w_st S a        (in the order of time)
 //   S <- S + k_st c b^T,  out = w_st S a,  S <- l S   (against it)
-// for the tokens of a block whose chunks cannot give it (seen_too_early()). S is in
+// for the tokens of a block whose chunks cannot give it (seen_too_early(), outgrows()). S is in
 // shared memory, with LN lanes a row, which nobody else reads; tokens come in 8 at a
 // time. (152 heads of 4,096 tokens, d = 128, an Inf in the middle of each: 6.6 ms, 0.15 without.)
 template <int D, typename T, int THREADS, bool STATE>
@@ -127,6 +132,8 @@ __device__ __noinline__ void by_token(const DecayArgs& p, int role, int bh, int 
         for (int y = lane; y < D; y += LN) S[x * LD + y] = !init ? 0.f : init_t ? init[y * D + x] : init[x * D + y];
     float bad = 0.f;
     SlowDecay slow(g, 1);
+    const bool steep = g > 1.f;  // roundings that add up matter for a slow decay alone
+    const float once = expf(g);
     for (int m = 0; m < sp.n; m += TOK) {
         const int k = min(TOK, sp.n - m);
         auto token = [&](int j) { return sp.t0 + (rev ? sp.n - 1 - (m + j) : m + j); };
@@ -141,7 +148,7 @@ __device__ __noinline__ void by_token(const DecayArgs& p, int role, int bh, int 
         __syncthreads();
         if (x >= D) continue;
         for (int j = 0; j < k; ++j) {
-            const float l = slow.next(), c = r.k_st * rows[(2 * TOK + j) * D + x];
+            const float l = steep ? once : slow.next(), c = r.k_st * rows[(2 * TOK + j) * D + x];
             const float *av = rows + j * D, *bv = rows + (TOK + j) * D;
             float acc = 0.f;
             for (int y = lane; y < D; y += LN) {

@@ -64,6 +64,12 @@ __global__ void __launch_bounds__(FmaLay<D, T>::THREADS, FmaLay<D, T>::OCC)
     const bool rev = r.reverse;
     float bad = 0.f;  // NaN once an output or a final state is not finite
 
+    static_assert(L::FLOATS >= D * (D + 4) + 24 * D, "by_token's floats");
+    if (outgrows(g, L::C)) {
+        by_token<D, T, L::THREADS, STATE>(p, blockIdx.y, bh, seg, sm);
+        return;
+    }
+
     const int chunks = (sp.n + L::C - 1) / L::C;
     // first token (within the segment) of the m-th 32 in the role's order
     auto chunk0 = [&](int m) { return (rev ? chunks - 1 - m : m) * L::C; };
@@ -253,7 +259,6 @@ __global__ void __launch_bounds__(FmaLay<D, T>::THREADS, FmaLay<D, T>::OCC)
     __syncthreads();
     if constexpr (!STATE) {
         // fin, which may be init, is not written yet
-        static_assert(L::FLOATS >= D * (D + 4) + 24 * D, "by_token's floats");
         if (__syncthreads_or(bad != bad) &&
             seen_too_early<D, T, L::THREADS, L::C>(p, r, b, h, sp, reinterpret_cast<int*>(sm + L::A))) {
             by_token<D, T, L::THREADS, STATE>(p, blockIdx.y, bh, seg, sm);

@@ -31,6 +31,16 @@ struct ScanArgs {
 
 constexpr int SCAN_THREADS = 128;
 
+// exp(g n) s where the factor alone may overflow (g > 0), a part of the tokens at a time
+__device__ __noinline__ float grown(float s, float g, int n) {
+    while (n > 0 && s != 0.f && fabsf(s) < __int_as_float(0x7F800000)) {
+        const int m = min(n, max(1, (int)(80.f / g)));
+        s *= expf(g * (float)m);
+        n -= m;
+    }
+    return s;
+}
+
 template <int D>
 __global__ void __launch_bounds__(SCAN_THREADS) vla_decay_scan_kernel(const __grid_constant__ DecayArgs p,
                                                                       const __grid_constant__ ScanArgs q) {
@@ -60,10 +70,15 @@ __global__ void __launch_bounds__(SCAN_THREADS) vla_decay_scan_kernel(const __gr
             if (k0 + k >= p.nseg) break;
             const int m = place(k0 + k);
             const int n = span_of(p, b, m).n;
-            const float w = n < p.seg_len ? decay_pow(g, n) : slow.next();
             seg[(size_t)m * (D * D / 4)] = s;
-            s = make_float4(fmaf(w, s.x, own[k].x), fmaf(w, s.y, own[k].y), fmaf(w, s.z, own[k].z),
-                            fmaf(w, s.w, own[k].w));
+            if (g * (float)n > 80.f) {
+                s = make_float4(own[k].x + grown(s.x, g, n), own[k].y + grown(s.y, g, n), own[k].z + grown(s.z, g, n),
+                                own[k].w + grown(s.w, g, n));
+            } else {
+                const float w = n < p.seg_len ? decay_pow(g, n) : slow.next();
+                s = make_float4(fmaf(w, s.x, own[k].x), fmaf(w, s.y, own[k].y), fmaf(w, s.z, own[k].z),
+                                fmaf(w, s.w, own[k].w));
+            }
         }
     }
     if (r.fin) {

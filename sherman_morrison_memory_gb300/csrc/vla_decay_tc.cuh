@@ -247,6 +247,12 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
     const bool rev = r.reverse != 0;
     const int chunks = (sp.n + L::C - 1) / L::C;
 
+    static_assert(L::SMEM >= (D * (D + 4) + 24 * D) * 4, "by_token's floats");
+    if (outgrows(g, L::C)) {
+        by_token<D, __nv_bfloat16, L::THREADS, STATE>(p, ri, bh, seg, reinterpret_cast<float*>(sm));
+        return;
+    }
+
     // With time, a token's weight towards the state counts from the chunk's
     // end; against it, its weight from the state does: those tables hold the
     // powers 63, 62, .. and a chunk of n tokens begins 64 - n behind.
@@ -760,7 +766,6 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
     if constexpr (!STATE) {
         // All copies and MMAs of the block are done; the final state, which may
         // replace the initial one, is written only after this.
-        static_assert(L::SMEM >= (D * (D + 4) + 24 * D) * 4, "by_token's floats");
         if (__syncthreads_or(bad.x != bad.x || bad.y != bad.y) && *abort_flag == 0)
             again = seen_too_early<D, __nv_bfloat16, L::THREADS, L::C>(p, r, b, h, sp, reinterpret_cast<int*>(sm));
         if (again) {

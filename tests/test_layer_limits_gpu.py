@@ -4,7 +4,7 @@ import torch
 
 import layer_ref as R
 import sherman_morrison_memory_gb300 as vla
-from test_layer_gpu import seqs, state_like
+from test_layer_gpu import check_backward, check_forward, seqs, state_like
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +87,45 @@ def test_every_place_of_a_value_that_is_not_finite(lengths, dtype):
         want = torch.zeros(B, H, T, d, dtype=torch.bool, device="cuda")
         want[..., x] = after & (t < live) & (at < live)
         assert torch.equal(torch.isnan(got), want) and torch.isfinite(got[~want]).all()
+    assert vla.vla_get_last_device_status()[0] == vla._binding.VLA_ERR_NONFINITE  # read and cleared
+
+
+# ---- heads that grow ----------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("T", [90, 300, 1300])
+def test_growth_beyond_the_range_of_a_factor(T, d, dtype):
+    """A chunk's factor overflows, the sequence's results do not: nothing but zeros are multiplied by it."""
+    B, H, live = 2, 4, 20
+    q, k, v, do = seqs(4, B, H, T, d, dtype, seed=d + T)
+    g = torch.tensor([2.5, 1.4, 0.2, -0.1], device="cuda")
+    for x in (k, v):
+        x[:, :, :T - live] = 0
+    check_forward(q, k, v, g, 0.3, None, None)
+    check_forward(q, k, v, g, 0.3, torch.zeros(B, H, d, d, device="cuda"), None)
+    do[:, :, live:] = 0
+    check_backward(q, k, v, g, 0.3, None, do, None, None)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,d,g", [(63, 64, 1.3), (78, 128, 1.0), (78, 32, 1.0), (110, 96, 0.72), (700, 64, 0.1)])
+def test_growth_with_every_token(T, d, g, dtype):
+    q, k, v, do = seqs(4, 1, 3, T, d, dtype, seed=d)
+    g = torch.tensor([g, -0.2, g], device="cuda")
+    n = torch.tensor([T - 2], dtype=torch.int32, device="cuda")
+    S0, dS = state_like(1, 3, d, 1), state_like(1, 3, d, 2)
+    check_forward(q, k, v, g, 0.3, S0, n)
+    check_backward(q, k, v, g, 0.3, S0, do, dS, n)
+
+
+def test_growth_as_in_single_tokens():
+    """A prompt of a head that grows a hundredfold a token, and the same tokens one at a time."""
+    B, H, T, d = 2, 2, 12, 64
+    q, k, v = seqs(3, B, H, T, d, F32, seed=7)
+    g = torch.tensor([4.6, 0.8], device="cuda")
+    S0 = state_like(B, H, d, 1)
+    o, S = check_forward(q, k, v, g, 0.1, S0, None)
+    pool = S0.clone()
+    rows = [vla.vla_decay_step(q[:, :, t], k[:, :, t], v[:, :, t], g, pool, 0.1, check=True) for t in range(T)]
+    check_forward(q, k, v, g, 0.1, S0, None, (torch.stack(rows, 2), pool))
