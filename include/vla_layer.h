@@ -12,6 +12,11 @@
  * place. And results that are sequences (o, y, the gradients) have the inputs'
  * type, rounded once at the end.
  *
+ * An output of a call overlaps neither itself nor an input nor another output
+ * (nor the call's scratch), except in place where an entry point says so: blocks
+ * of a call read what others write. Rows that lie between those of another array
+ * do not overlap it. Checked: VLA_ERR_INVALID_ARG.
+ *
  * `status` is the 256-byte status record that the workspace of vla_forward()
  * begins with (zero-filled before the first use, 16-byte aligned); several
  * calls and streams may share it. vla_get_last_device_status(status, ...)
@@ -35,7 +40,7 @@ typedef struct {
     long long stride_b, stride_h, stride_t;
 } vla_seq;
 
-/* The same for an output; its rows must not overlap each other or an input. */
+/* The same for an output. */
 typedef struct {
     void* data;
     long long stride_b, stride_h, stride_t;
@@ -82,8 +87,7 @@ vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
  *   dq_t = scale S_t^T dO_t,
  *   R_t = l R_{t+1} + scale dO_t q_t^T (R holds dS_T behind the last token),
  *   dk_t = R_t^T v_t,  dv_t = R_t k_t,  dS0 = l R_1.
- * Nothing is kept from the forward call. dS0 must not be S0 or dS_T, which
- * other blocks of the call read (VLA_ERR_INVALID_ARG). */
+ * Nothing is kept from the forward call. dS0 is neither S0 nor dS_T. */
 vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO,
                               vla_dtype dtype, int B, int H, int T, int d, const float* log_decay, float scale,
                               const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,

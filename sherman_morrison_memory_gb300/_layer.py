@@ -8,8 +8,10 @@ Sequences are [B, H, T, d] float32 or bfloat16 with any strides: a
 projection's [B, T, H, d] output is passed as ``x.transpose(1, 2)`` and read
 in place. One whose last dimension is not dense, or whose rows do not start on
 16-byte boundaries, is copied first. Results that are sequences have the
-inputs' type; states, statistics and weights are float32. Any call may be
-captured in a CUDA graph after one eager call of the package on the device
+inputs' type; states, statistics and weights are float32. Preallocated outputs
+share no memory with inputs or each other (VLAError), except where a call says
+that it works in place; rows that lie between those of another array are fine.
+Any call may be captured in a CUDA graph after one eager call of the package on the device
 (which lays out the shared status record).
 """
 from __future__ import annotations

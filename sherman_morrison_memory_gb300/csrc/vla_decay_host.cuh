@@ -371,6 +371,9 @@ vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
         !aligned(S_out, 16) || !aligned(status, 16))
         return VLA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const long long states = (long long)B * H * d * d;
+    const Region S_in = region(S0, states, 32), S_end = region(S_out, states, 32);
+    if (!apart({S_end}, {S_in}, 1)) return VLA_ERR_INVALID_ARG;
     if (T == 0) return copy_state(S_out, S0, (size_t)B * H * d * d, s);
     const int es = dtype == VLA_BF16 ? 2 : 4;
     if (!good_seq(q, B, H, T, es) || !good_seq(k, B, H, T, es) || !good_seq(v, B, H, T, es) ||
@@ -378,6 +381,10 @@ vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
         return VLA_ERR_INVALID_ARG;
     const size_t need = scratch_bytes_of(B, H, T, d, false);
     if (need && (!scratch || !aligned(scratch, 256) || scratch_bytes < need)) return VLA_ERR_INVALID_ARG;
+    if (!apart({S_end, region(o, B, H, T, d, es), region(scratch, need, 8)},
+               {S_in, region(q, B, H, T, d, es), region(k, B, H, T, d, es), region(v, B, H, T, d, es),
+                region(log_decay, H, 32), region(lengths, B, 32)}, 1))
+        return VLA_ERR_INVALID_ARG;
     Call c{};
     DecayArgs& p = c.main;
     p.B = B, p.H = H, p.T = T;
@@ -411,7 +418,9 @@ vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
         !aligned(dS0, 16) || !aligned(status, 16))
         return VLA_ERR_INVALID_ARG;
     // the blocks of dk read dS_T and those of dq S0, when those of dv write dS0
-    if (dS0 && (dS0 == S0 || dS0 == dS_T)) return VLA_ERR_INVALID_ARG;
+    const long long states = (long long)B * H * d * d;
+    const Region S_in = region(S0, states, 32), G_in = region(dS_T, states, 32), G_end = region(dS0, states, 32);
+    if (!apart({G_end}, {S_in, G_in})) return VLA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) return copy_state(dS0, dS_T, (size_t)B * H * d * d, s);
     const int es = dtype == VLA_BF16 ? 2 : 4;
@@ -421,6 +430,11 @@ vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
         return VLA_ERR_INVALID_ARG;
     const size_t need = scratch_bytes_of(B, H, T, d, true);
     if (need && (!scratch || !aligned(scratch, 256) || scratch_bytes < need)) return VLA_ERR_INVALID_ARG;
+    if (!apart({region(dq, B, H, T, d, es), region(dk, B, H, T, d, es), region(dv, B, H, T, d, es), G_end,
+                region(scratch, need, 8)},
+               {region(q, B, H, T, d, es), region(k, B, H, T, d, es), region(v, B, H, T, d, es),
+                region(dO, B, H, T, d, es), S_in, G_in, region(log_decay, H, 32), region(lengths, B, 32)}))
+        return VLA_ERR_INVALID_ARG;
     const Seq Q = to_seq(q, B, H, T), K = to_seq(k, B, H, T), V = to_seq(v, B, H, T), G = to_seq(dO, B, H, T);
     Call c{};
     DecayArgs& p = c.main;
@@ -466,6 +480,12 @@ vla_status vla_decay_step(const void* q, const void* k, const void* v, vla_dtype
         return VLA_ERR_INVALID_ARG;
     const long long grid = (long long)B * H * (d / STEP_ROWS);
     if (grid > 2147483647LL) return VLA_ERR_INVALID_ARG;
+    // each block reads all of q and k of its head, o is written by several
+    const long long rows = (long long)B * H * d;
+    const int bits = dtype == VLA_BF16 ? 16 : 32;
+    if (!apart({region(o, rows, bits), region(states, (__int128)N * H * d * d, 32)},
+               {region(q, rows, bits), region(k, rows, bits), region(v, rows, bits), region(log_decay, H, 32), region(slots, B, 32)}))
+        return VLA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto* ds = static_cast<vla::DeviceStatus*>(status);
     auto go = [&](auto tag, auto dim) {

@@ -14,6 +14,7 @@
 #include "vla_device.cuh"
 #include "vla_internal.h"
 #include "vla_layer.h"
+#include "vla_overlap.h"
 
 namespace vla_layer {
 

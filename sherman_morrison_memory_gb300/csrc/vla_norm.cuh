@@ -270,6 +270,10 @@ vla_status vla_head_norm(const vla_seq* x, vla_dtype dtype, int B, int H, int T,
     if (!good_seq(x, B, H, T, es) || !good_seq(y, B, H, T, es) || !aligned(weight, 16) || !aligned(bias, 16) ||
         !aligned(mean, 4) || !aligned(rstd, 4))
         return VLA_ERR_INVALID_ARG;
+    const long long weights = (shared ? 1LL : (long long)H) * d, stats = (long long)B * H * T;
+    if (!apart({region(y, B, H, T, d, es), region(mean, stats, 32), region(rstd, stats, 32)},
+               {region(x, B, H, T, d, es), region(weight, weights, 32), region(bias, weights, 32)}, 1))
+        return VLA_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = to_seq(x, B, H, T);
     a.out = to_seq(y, B, H, T);
@@ -306,6 +310,12 @@ vla_status vla_head_norm_backward(const vla_seq* dy, const vla_seq* x, vla_dtype
         !mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4))
         return VLA_ERR_INVALID_ARG;
     if (dweight && (!scratch || !aligned(scratch, 16) || scratch_bytes < vla_head_norm_scratch_bytes(B, H, T, d)))
+        return VLA_ERR_INVALID_ARG;
+    const long long weights = (shared ? 1LL : (long long)H) * d, stats = (long long)B * H * T;
+    const long long parts = dweight ? (long long)vla_head_norm_scratch_bytes(B, H, T, d) : 0;
+    if (!apart({region(dx, B, H, T, d, es), region(dweight, weights, 32), region(dbias, weights, 32), region(scratch, parts, 8)},
+               {region(x, B, H, T, d, es), region(dy, B, H, T, d, es), region(weight, weights, 32), region(mean, stats, 32),
+                region(rstd, stats, 32)}, 2))
         return VLA_ERR_INVALID_ARG;
     NormArgs a{};
     a.x = to_seq(x, B, H, T);

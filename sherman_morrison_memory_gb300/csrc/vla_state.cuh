@@ -157,6 +157,9 @@ vla_status vla_state_store(const float* x, int B, long long rows, int d, int bit
     const vla_status st = check_cache(codes, scales, N, B, rows, d, bits, x, slots, status);
     if (st != VLA_OK || B == 0 || rows == 0) return st;
     const long long per = rows * d;
+    const __int128 all = (__int128)N * per;
+    const Region states = region(x, (__int128)B * per, 32), c = region(codes, all, bits), f = region(scales, all / 32, 32);
+    if (!apart({c, f}, {states, region(slots, B, 32)})) return VLA_ERR_INVALID_ARG;
     const dim3 grid((unsigned)((per + BLOCK_VALUES - 1) / BLOCK_VALUES), (unsigned)B);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto* ds = static_cast<vla::DeviceStatus*>(status);
@@ -173,6 +176,9 @@ vla_status vla_state_load(const void* codes, const float* scales, int N, const i
     const vla_status st = check_cache(codes, scales, N, B, rows, d, bits, x, slots, status);
     if (st != VLA_OK || B == 0 || rows == 0) return st;
     const long long per = rows * d;
+    const __int128 all = (__int128)N * per;
+    const Region states = region(x, (__int128)B * per, 32), c = region(codes, all, bits), f = region(scales, all / 32, 32);
+    if (!apart({states}, {c, f, region(slots, B, 32)})) return VLA_ERR_INVALID_ARG;
     const dim3 grid((unsigned)((per + BLOCK_VALUES - 1) / BLOCK_VALUES), (unsigned)B);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto* ds = static_cast<vla::DeviceStatus*>(status);

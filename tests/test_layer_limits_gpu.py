@@ -4,7 +4,7 @@ import torch
 
 import layer_ref as R
 import sherman_morrison_memory_gb300 as vla
-from test_layer_gpu import check_backward, check_forward, seqs, state_like
+from test_layer_gpu import check_backward, check_forward, decays, seqs, state_like
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +129,60 @@ def test_growth_as_in_single_tokens():
     pool = S0.clone()
     rows = [vla.vla_decay_step(q[:, :, t], k[:, :, t], v[:, :, t], g, pool, 0.1, check=True) for t in range(T)]
     check_forward(q, k, v, g, 0.1, S0, None, (torch.stack(rows, 2), pool))
+
+
+# ---- outputs on top of inputs -------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_outputs_on_top_of_inputs_are_refused(dtype):
+    """Blocks of one call read what others write: refused, and nothing is written."""
+    B, H, T, d = 2, 2, 90, 64
+    q, k, v, do = seqs(4, B, H, T, d, dtype, seed=3)
+    g = decays(H)
+    S, dS, dS0 = (state_like(B, H, d, i) for i in range(3))
+    pool = state_like(3 * B, H, d, 4)
+    w = torch.ones(H, d, device="cuda")
+    one = [x[:, :, 0].contiguous() for x in (q, k, v)]
+    longer = torch.zeros(B, H, T + 1, d, dtype=dtype, device="cuda")
+    x = longer[:, :, :T]
+    everything = [q, k, v, do, S, dS, dS0, pool, *one, longer]
+    before = [t.clone() for t in everything]
+    fresh = lambda: torch.empty_like(q)  # noqa: E731
+    stats = vla.vla_head_norm(q)[1]
+    calls = [lambda y=y: vla.vla_decay_forward(q, k, v, g, 1.0, S, out=(y, torch.empty_like(S))) for y in (q, k, v)]
+    calls += [lambda y=y: vla.vla_decay_backward(q, k, v, g, 1.0, S, do, dS, out=(*y, dS0))
+              for y in ((q, k, v), (fresh(), fresh(), do), (q, fresh(), fresh()), (x, x, fresh()))]
+    calls += [lambda y=y: vla.vla_decay_backward(q, k, v, g, 1.0, pool[:B], do, pool[2 * B:], out=(fresh(), fresh(), fresh(), y))
+              for y in (pool[1:B + 1], pool[2 * B - 1:3 * B - 1], pool[:B])]
+    calls += [lambda: vla.vla_decay_forward(q, k, v, g, 1.0, pool[:B], out=(fresh(), pool[1:B + 1]))]
+    calls += [lambda y=y: vla.vla_decay_step(*one, g, S, out=y) for y in one]
+    calls += [lambda: vla.vla_head_norm(x, w, out=longer[:, :, 1:]),
+              lambda: vla.vla_head_norm_backward(x, q, stats, w, out=longer[:, :, 1:])]
+    for call in calls:
+        with pytest.raises(vla.VLAError) as e:
+            call()
+        assert e.value.status == vla._binding.VLA_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(everything, before))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [32, 96])
+def test_outputs_between_each_others_rows(d, dtype):
+    """dq, dk and dv as slices of one projection's gradient [B, T, 3, H, d], whose input's slices are q, k and v."""
+    B, H, T = 2, 3, 70
+    qkv = torch.randn(B, T, 3, H, d, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(dtype)
+    q, k, v = (qkv[:, :, i].transpose(1, 2) for i in range(3))
+    do, = seqs(1, B, H, T, d, dtype, seed=2)
+    g = torch.tensor([-0.01, -0.1, -1.0], device="cuda")
+    dqkv = torch.empty_like(qkv)
+    out = [dqkv[:, :, i].transpose(1, 2) for i in range(3)]
+    dS0 = torch.empty(B, H, d, d, device="cuda")
+    got = vla.vla_decay_backward(q, k, v, g, 0.3, None, do, out=(*out, dS0), check=True)
+    check_backward(q, k, v, g, 0.3, None, do, None, None, got)
+    # o beside q in the rows of a wider buffer
+    wide = torch.randn(B, H, T, 2 * d, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(dtype)
+    left = wide[..., :d].clone()
+    got = vla.vla_decay_forward(wide[..., :d], k, v, g, 0.3, out=(wide[..., d:], dS0), check=True)
+    assert torch.equal(wide[..., :d], left)
+    check_forward(left, k, v, g, 0.3, None, None, got)
