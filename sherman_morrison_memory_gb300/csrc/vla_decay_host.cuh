@@ -58,26 +58,34 @@ __global__ void __launch_bounds__(SCAN_THREADS) vla_decay_scan_kernel(const __gr
                      : *reinterpret_cast<const float4*>(m + i);
     }
     float4* seg = reinterpret_cast<float4*>(seg_of(p, blockIdx.y, bh, 0, D) + i);
-    SlowDecay slow(g, p.seg_len);
     auto place = [&](int k) { return r.reverse ? p.nseg - 1 - k : k; };
-    for (int k0 = 0; k0 < p.nseg; k0 += AHEAD) {
-        float4 own[AHEAD];
+    auto join = [&](const float4& own, float4 w) {
+        s = make_float4(fmaf(w.x, s.x, own.x), fmaf(w.y, s.y, own.y), fmaf(w.z, s.z, own.z), fmaf(w.w, s.w, own.w));
+    };
+    if (g * (float)p.seg_len > 80.f) {  // a segment's factor may overflow
+        for (int k = 0; k < p.nseg; ++k) {
+            const int n = span_of(p, b, place(k)).n;
+            float4& at_k = seg[(size_t)place(k) * (D * D / 4)];
+            const float4 own = at_k;
+            at_k = s;
+            s = make_float4(grown(s.x, g, n), grown(s.y, g, n), grown(s.z, g, n), grown(s.w, g, n));
+            join(own, make_float4(1.f, 1.f, 1.f, 1.f));
+        }
+    } else {
+        SlowDecay slow(g, p.seg_len);
+        for (int k0 = 0; k0 < p.nseg; k0 += AHEAD) {
+            float4 own[AHEAD];
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (k0 + k < p.nseg) own[k] = seg[(size_t)place(k0 + k) * (D * D / 4)];
+            for (int k = 0; k < AHEAD; ++k)
+                if (k0 + k < p.nseg) own[k] = seg[(size_t)place(k0 + k) * (D * D / 4)];
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            if (k0 + k >= p.nseg) break;
-            const int m = place(k0 + k);
-            const int n = span_of(p, b, m).n;
-            seg[(size_t)m * (D * D / 4)] = s;
-            if (g * (float)n > 80.f) {
-                s = make_float4(own[k].x + grown(s.x, g, n), own[k].y + grown(s.y, g, n), own[k].z + grown(s.z, g, n),
-                                own[k].w + grown(s.w, g, n));
-            } else {
+            for (int k = 0; k < AHEAD; ++k) {
+                if (k0 + k >= p.nseg) break;
+                const int m = place(k0 + k);
+                const int n = span_of(p, b, m).n;
                 const float w = n < p.seg_len ? decay_pow(g, n) : slow.next();
-                s = make_float4(fmaf(w, s.x, own[k].x), fmaf(w, s.y, own[k].y), fmaf(w, s.z, own[k].z),
-                                fmaf(w, s.w, own[k].w));
+                seg[(size_t)m * (D * D / 4)] = s;
+                join(own[k], make_float4(w, w, w, w));
             }
         }
     }

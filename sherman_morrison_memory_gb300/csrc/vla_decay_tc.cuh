@@ -324,7 +324,17 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
     auto row = [&](int k) { return quad * L::RW + (FRAG ? (lane >> 2) + 8 * (k % 2) : lane); };
     auto col = [&](int k) { return half * HC + (FRAG ? 2 * (lane & 3) + 16 * (k / 4) + 8 * ((k % 4) / 2) : 2 * k); };
     float2 S[NS];
-    bool state_ok = false;  // S is the end state
+    auto write_state = [&](float* to) {
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+            bad = fma2(S[k], zero2, bad);
+            if constexpr (FRAG)
+                *reinterpret_cast<float2*>(to + row(k) * D + col(k)) = S[k];
+            else if (k % 2 == 0)
+                *reinterpret_cast<float4*>(to + row(k) * D + col(k)) = make_float4(S[k].x, S[k].y, S[k + 1].x, S[k + 1].y);
+        }
+    };
+    float* in_place = nullptr;  // where the final state takes the initial one's place: written last
 
     // The whole warps run the MMA loops, so that operands stay in uniform
     // registers, and one elected thread issues: issued under a test of the lane,
@@ -519,9 +529,9 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const int xb = quad * L::RW;
         const bool rows_in = xb < D;  // else zero throughout
+        int init_t;
+        const float* init = start_of<D, STATE>(p, ri, bh, seg, init_t);
         {
-            int init_t;
-            const float* init = start_of<D, STATE>(p, ri, bh, seg, init_t);
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
                 const int x = row(k), y = col(k);
@@ -673,7 +683,13 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
             }
             publish();
         }
-        state_ok = ok;
+        float* fin = end_of<D, STATE>(p, ri, bh, seg);
+        if (ok && fin && rows_in) {
+            if (!STATE && fin == init)
+                in_place = fin;
+            else
+                write_state(fin);
+        }
     } else if (!STATE) {  // ---- output
         constexpr int NH = L::NH;
         const int lc = 2 * (lane & 3);
@@ -764,8 +780,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
     __syncwarp();
     bool again = false;
     if constexpr (!STATE) {
-        // All copies and MMAs of the block are done; the final state, which may
-        // replace the initial one, is written only after this.
+        // All copies and MMAs of the block are done.
         if (__syncthreads_or(bad.x != bad.x || bad.y != bad.y) && *abort_flag == 0)
             again = seen_too_early<D, __nv_bfloat16, L::THREADS, L::C>(p, r, b, h, sp, reinterpret_cast<int*>(sm));
         if (again) {
@@ -779,18 +794,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
         for (int i = tid; i < behind * (D / 8); i += L::THREADS)
             store8(row_of<__nv_bfloat16>(r.out, b, h, sp.t0 + done + i / (D / 8)) + (i % (D / 8)) * 8, zero);
     }
-    float* fin = again || !state_ok ? nullptr : end_of<D, STATE>(p, ri, bh, seg);
-    if (fin && quad * L::RW < D) {
-#pragma unroll
-        for (int k = 0; k < NS; ++k) {
-            bad = fma2(S[k], zero2, bad);
-            if constexpr (FRAG)
-                *reinterpret_cast<float2*>(fin + row(k) * D + col(k)) = S[k];
-            else if (k % 2 == 0)
-                *reinterpret_cast<float4*>(fin + row(k) * D + col(k)) =
-                    make_float4(S[k].x, S[k].y, S[k + 1].x, S[k + 1].y);
-        }
-    }
+    if (in_place && !again) write_state(in_place);
     if ((bad.x != bad.x || bad.y != bad.y) && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, sp.t0);
     vla::tc_fence_before();
     __syncthreads();
