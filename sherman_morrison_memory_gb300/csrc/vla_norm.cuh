@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(NORM_THREADS, D == 96 || sizeof(T) == 4 ? 2 : 
     for (int v = 0; v < V; ++v) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[v][i] = 1.f, bi[v][i] = 0.f;
-        const int at = (a.shared ? 0 : h * D) + (lane + v * L::W) * 8;
+        const long long at = (a.shared ? 0LL : (long long)h * D) + (lane + v * L::W) * 8;
         if (a.weight) load8(a.weight + at, w[v]);
         if (a.bias) load8(a.bias + at, bi[v]);
     }
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(NORM_THREADS) vla_head_norm_backward_kernel(co
     float w[8], dw[8], db[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = 1.f, dw[i] = 0.f, db[i] = 0.f;
-    if (on && a.weight) load8(a.weight + (a.shared ? 0 : h * D) + col, w);
+    if (on && a.weight) load8(a.weight + (a.shared ? 0LL : (long long)h * D) + col, w);
     constexpr int U = sizeof(T) == 4 ? 2 : 4;  // rows under way at once
     static_assert(ROWS % (U * L::PER) == 0, "whole passes");
 #pragma unroll 1
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(SUMS_THREADS) vla_head_norm_sums_kernel(const 
     if (k == 0) {
 #pragma unroll
         for (int j = 1; j < 32; ++j) s += sums[j][col];
-        (i < D ? dw : db)[h * D + i % D] = s;
+        (i < D ? dw : db)[(long long)h * D + i % D] = s;
     }
 }
 

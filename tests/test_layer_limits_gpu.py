@@ -186,3 +186,29 @@ def test_outputs_between_each_others_rows(d, dtype):
     got = vla.vla_decay_forward(wide[..., :d], k, v, g, 0.3, out=(wide[..., d:], dS0), check=True)
     assert torch.equal(wide[..., :d], left)
     check_forward(left, k, v, g, 0.3, None, None, got)
+
+
+# ---- offsets behind 2^31 ------------------------------------------------------------------------------------------
+
+def test_head_norm_weights_behind_two_to_the_31():
+    """More than 2^24 heads of 128 values: a head's weight, bias and their gradients lie 2^31 values and more in."""
+    H, d = (1 << 24) + 3, 128
+    heads = [0, 1, H - 4, H - 3, H - 2, H - 1]
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    some = lambda *s: torch.randn(*s, len(heads), d, generator=gen, device="cuda")  # noqa: E731
+    x, dy = (torch.zeros(1, H, 1, d, dtype=BF, device="cuda") for _ in range(2))
+    w, b = (torch.zeros(H, d, device="cuda") for _ in range(2))
+    x[0, heads, 0], dy[0, heads, 0] = some().to(BF), some().to(BF)
+    w[heads], b[heads] = some(), some()
+    part = lambda y: y[:, heads].contiguous()  # noqa: E731
+    want_y, stats = vla.vla_head_norm(part(x), w[heads], b[heads])
+    want = vla.vla_head_norm_backward(part(dy), part(x), stats, w[heads])
+    y, stats = vla.vla_head_norm(x, w, b)
+    assert torch.equal(part(y), want_y) and not y[:, 2:H - 4].any()
+    del y, b
+    dx, dw, db = vla.vla_head_norm_backward(dy, x, stats, w)
+    assert torch.equal(part(dx), want[0]) and torch.equal(dw[heads], want[1]) and torch.equal(db[heads], want[2])
+    assert not dw[2:H - 4].any() and not db[2:H - 4].any() and not dx[:, 2:H - 4].any()
+    # the few heads against the definition
+    n = R.norm_grads(part(dy), part(x), w[heads], 1e-5)
+    assert float((dw[heads].double().cpu() - n[1]).abs().max()) <= 64 * d * R.U * float(n[3].max())
