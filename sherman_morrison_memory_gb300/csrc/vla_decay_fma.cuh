@@ -1,5 +1,5 @@
 // vla_decay_fma.cuh -- the operation of vla_decay.cuh on the FP32 pipes, for fp32
-// inputs and for the shortest bf16 calls: a block per (role, head, segment) goes
+// inputs and for bf16 calls of a few tokens: a block per (role, head, segment) goes
 // through its tokens 32 at a time with S and the tiles of a, b, c and the decayed c
 // in shared memory. The next 32 tokens' rows are on their way to registers meanwhile.
 //
@@ -45,9 +45,17 @@ __device__ __forceinline__ float dot4(float4 x, float4 y, float s) {
     return fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
 }
 
-// bf16 calls of up to this many tokens run here too: their rows have so few
-// terms that the tensor cores' bf16 pairs do not average out and would show in
-// the result. (One token, 32 heads, d = 128: 9.3 us against the tensor cores' 8.1.)
+// bf16 calls of up to this many tokens run here too (never cut into segments): a
+// chunk's fixed costs on the tensor cores are as large as all their arithmetic. Here
+// against there, us, forward | gradients, 1 to 8 tokens (the same within a tenth):
+//   heads      d = 32                   d = 64                   d = 96                   d = 128
+//      32   3.7,  4.6 |  3.8,  5.5   5.4,  5.1 |  5.5,  5.8   7.4,  9.3 |  7.9,  9.7    9.9, 10.9 |  12.2,  11.3
+//     256   4.4,  9.1 |  8.5, 24.0   7.1,  9.8 | 16.1, 25.7    10, 18.3 | 29.9, 40.8   19.0, 21.3 |  60.6,  46.8
+//     512   5.8, 16.4 | 13.4, 42.9  12.3, 17.7 | 28.7, 46.3    19, 34.3 | 55.2, 74.9   36.7, 40.2 | 117.8, 110.5
+// (At d = 128 gradients pay for one block an SM.) Their pairs and states stay in fp32
+// as well, so that o is rounded once, where the tensor-core kernel's rows meet one
+// more rounding to bf16, however many tokens there are: its errors are about 1.4
+// times as large (2.3e-3 of a row's size against 1.65e-3).
 constexpr int FMA_T = 8;
 
 template <int D, typename T, bool STATE>

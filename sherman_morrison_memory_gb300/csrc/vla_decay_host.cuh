@@ -310,11 +310,15 @@ vla_status launch(Call& c, cudaStream_t s) {
             main<<<blocks * c.roles, L::THREADS, L::SMEM, s>>>(c.main, c.maps, c.roles);
         } else {
             using L = FmaLay<D, T>;
-            constexpr auto main = vla_decay_fma_kernel<D, T, false>, own = vla_decay_fma_kernel<D, T, true>;
-            if (!allow_smem<main>(L::SMEM) || !allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
-            if (cut.nseg > 1) {
-                own<<<dim3(blocks, c.state_roles), L::THREADS, L::SMEM, s>>>(c.states);
-                scan();
+            constexpr auto main = vla_decay_fma_kernel<D, T, false>;
+            if (!allow_smem<main>(L::SMEM)) return VLA_ERR_CUDA;
+            if constexpr (sizeof(T) == 4) {  // the few tokens of a bf16 call are one segment
+                constexpr auto own = vla_decay_fma_kernel<D, T, true>;
+                if (!allow_smem<own>(L::SMEM)) return VLA_ERR_CUDA;
+                if (cut.nseg > 1) {
+                    own<<<dim3(blocks, c.state_roles), L::THREADS, L::SMEM, s>>>(c.states);
+                    scan();
+                }
             }
             main<<<dim3(blocks, c.roles), L::THREADS, L::SMEM, s>>>(c.main);
         }
@@ -332,9 +336,11 @@ vla_status launch_d(Call& c, int d, cudaStream_t s) {
     }
 }
 
+bool on_tensor_cores(vla_dtype dt, int T) { return dt == VLA_BF16 && T > FMA_T; }
+
 vla_status launch_call(Call& c, int d, vla_dtype dt, cudaStream_t s) {
-    if (dt == VLA_F32) return launch_d<false, float>(c, d, s);
-    return c.main.T <= FMA_T ? launch_d<false, __nv_bfloat16>(c, d, s) : launch_d<true, __nv_bfloat16>(c, d, s);
+    if (on_tensor_cores(dt, c.main.T)) return launch_d<true, __nv_bfloat16>(c, d, s);
+    return dt == VLA_F32 ? launch_d<false, float>(c, d, s) : launch_d<false, __nv_bfloat16>(c, d, s);
 }
 
 // scratch of the larger of the two types' cuts, so that it need not be told the type
@@ -407,8 +413,9 @@ vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
     c.states = p;
     c.roles = c.state_roles = 1;
     c.scan.role[0] = ScanRole{S0, S_out, 0, 0};
-    if (dtype == VLA_BF16 && (!make_map(&c.maps.m[0], q, B, H, T, d) || !make_map(&c.maps.m[1], k, B, H, T, d) ||
-                              !make_map(&c.maps.m[2], v, B, H, T, d) || !make_map(&c.maps.out[0], o, B, H, T, d)))
+    if (on_tensor_cores(dtype, T) &&
+        (!make_map(&c.maps.m[0], q, B, H, T, d) || !make_map(&c.maps.m[1], k, B, H, T, d) ||
+         !make_map(&c.maps.m[2], v, B, H, T, d) || !make_map(&c.maps.out[0], o, B, H, T, d)))
         return VLA_ERR_CUDA;
     return launch_call(c, d, dtype, s);
 }
@@ -465,11 +472,11 @@ vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
     c.state_roles = 2;
     c.scan.role[0] = ScanRole{S0, nullptr, 1, 0};
     c.scan.role[1] = ScanRole{dS_T, dS0, 0, 1};
-    if (dtype == VLA_BF16 && (!make_map(&c.maps.m[0], q, B, H, T, d) || !make_map(&c.maps.m[1], k, B, H, T, d) ||
-                              !make_map(&c.maps.m[2], v, B, H, T, d) || !make_map(&c.maps.m[3], dO, B, H, T, d) ||
-                              !make_map(&c.maps.out[0], dq, B, H, T, d) ||
-                              !make_map(&c.maps.out[1], dk, B, H, T, d) ||
-                              !make_map(&c.maps.out[2], dv, B, H, T, d)))
+    if (on_tensor_cores(dtype, T) &&
+        (!make_map(&c.maps.m[0], q, B, H, T, d) || !make_map(&c.maps.m[1], k, B, H, T, d) ||
+         !make_map(&c.maps.m[2], v, B, H, T, d) || !make_map(&c.maps.m[3], dO, B, H, T, d) ||
+         !make_map(&c.maps.out[0], dq, B, H, T, d) || !make_map(&c.maps.out[1], dk, B, H, T, d) ||
+         !make_map(&c.maps.out[2], dv, B, H, T, d)))
         return VLA_ERR_CUDA;
     return launch_call(c, d, dtype, s);
 }
