@@ -94,6 +94,22 @@ vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
                               const vla_seq_out* dk, const vla_seq_out* dv, float* dS0, void* scratch,
                               size_t scratch_bytes, void* status, void* stream);
 
+/* Both with options (NULL: the defaults), of which the waits' are read:
+ *   wait_limit_us        limit of every in-kernel wait (0: 2,000,000). The bf16
+ *                        kernel for more than 8 tokens has such waits
+ *   test_stall_producer  TESTING ONLY: nonzero keeps back the last tokens' loads in
+ *                        that kernel, so that its waits run out: VLA_ERR_TIMEOUT in
+ *                        the status record, role = the block's group of four warps */
+vla_status vla_decay_forward_ex(const vla_seq* q, const vla_seq* k, const vla_seq* v, vla_dtype dtype, int B, int H,
+                                int T, int d, const float* log_decay, float scale, const int* lengths,
+                                const float* S0, const vla_seq_out* o, float* S_out, void* scratch,
+                                size_t scratch_bytes, void* status, void* stream, const vla_options* opts);
+vla_status vla_decay_backward_ex(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO,
+                                 vla_dtype dtype, int B, int H, int T, int d, const float* log_decay, float scale,
+                                 const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,
+                                 const vla_seq_out* dk, const vla_seq_out* dv, float* dS0, void* scratch,
+                                 size_t scratch_bytes, void* status, void* stream, const vla_options* opts);
+
 /* One token of the recurrence for B sequences, their states updated in place
  * in a pool: q, k, v, o [B, H, d] of dtype, contiguous, 16-byte aligned;
  * states [N, H, d, d] float32, 16-byte aligned. slots: [B] int32 on the

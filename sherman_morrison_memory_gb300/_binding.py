@@ -64,10 +64,13 @@ def _layer_prototypes(lib):
     """Argument types of the entry points in include/vla_layer.h."""
     vp, ci, cf, cl, cz, sq = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong, ctypes.c_size_t,
                               ctypes.POINTER(_Seq))
+    forward = [sq] * 3 + [ci] * 5 + [vp, cf, vp, vp, sq, vp, vp, cz, vp, vp]
+    backward = [sq] * 4 + [ci] * 5 + [vp, cf, vp, vp, vp, sq, sq, sq, vp, vp, cz, vp, vp]
+    options = [ctypes.POINTER(_Options)]
     for name, args, res in (
             ("vla_decay_scratch_bytes", [ci] * 5, cz),
-            ("vla_decay_forward", [sq] * 3 + [ci] * 5 + [vp, cf, vp, vp, sq, vp, vp, cz, vp, vp], ci),
-            ("vla_decay_backward", [sq] * 4 + [ci] * 5 + [vp, cf, vp, vp, vp, sq, sq, sq, vp, vp, cz, vp, vp], ci),
+            ("vla_decay_forward", forward, ci), ("vla_decay_forward_ex", forward + options, ci),
+            ("vla_decay_backward", backward, ci), ("vla_decay_backward_ex", backward + options, ci),
             ("vla_decay_step", [vp] * 3 + [ci] * 4 + [vp, cf, vp, ci, vp, vp, vp, vp], ci),
             ("vla_head_norm", [sq] + [ci] * 5 + [vp, vp, ci, cf, sq, vp, vp, vp], ci),
             ("vla_head_norm_scratch_bytes", [ci] * 4, cz),

@@ -23,7 +23,7 @@ from typing import Optional
 
 import torch
 
-from ._binding import (_DTYPES, VLA_OK, VLAError, _call_buffer, _Seq, _workspace, load_library,
+from ._binding import (_DTYPES, VLA_OK, VLAError, _call_buffer, _Options, _Seq, _workspace, load_library,
                        vla_get_last_device_status)
 
 _DIMS = (32, 64, 96, 128)
@@ -121,6 +121,10 @@ def _scale(scale) -> float:
     return scale
 
 
+def _wait_options(wait_limit_us: int, stall: bool):
+    return ctypes.byref(_Options(wait_limit_us=int(wait_limit_us), test_stall_producer=1 if stall else 0))
+
+
 def _done(st: int, name: str, device, stream, check: bool):
     if st != VLA_OK:
         raise VLAError(st, name)
@@ -132,7 +136,7 @@ def _done(st: int, name: str, device, stream, check: bool):
 
 def vla_decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, scale: float = 1.0,
                       state: Optional[torch.Tensor] = None, *, lengths: Optional[torch.Tensor] = None, out=None,
-                      stream=None, check: bool = False):
+                      stream=None, check: bool = False, wait_limit_us: int = 0, test_stall_producer: bool = False):
     """Linear attention with a decay per head over a sequence:
     S_t = exp(log_decay[h]) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.
 
@@ -142,6 +146,9 @@ def vla_decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
     sequence b has only its first lengths[b] tokens; o is zero behind them.
     ``out`` = (o, S) preallocated; S may be ``state``. ``check=True``
     synchronises and raises on an in-kernel failure or a non-finite result.
+    ``wait_limit_us`` (0: 2,000,000) bounds each in-kernel wait;
+    ``test_stall_producer=True`` (testing only) makes them run out
+    (VLA_ERR_TIMEOUT): bf16 calls of more than 8 tokens have such waits.
     """
     for name, x in (("q", q), ("k", k), ("v", v)):
         _check_seq(x, name, None if x is q else q)
@@ -163,9 +170,12 @@ def vla_decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
         q, k, v = (_seq_in(x) for x in (q, k, v))
         nbytes = _decay_scratch(B, H, T, d, 0, dev.index)
         scratch = _call_buffer(dev, nbytes, False) if nbytes else None
-        st = lib.vla_decay_forward(_seq(q), _seq(k), _seq(v), _DTYPES[q.dtype], B, H, T, d, _ptr(log_decay), scale,
-                                   _ptr(lengths), _ptr(S0), _seq(o), _ptr(S), _ptr(scratch), nbytes,
-                                   _ptr(_workspace(dev)), _handle(dev, stream))
+        args = (_seq(q), _seq(k), _seq(v), _DTYPES[q.dtype], B, H, T, d, _ptr(log_decay), scale, _ptr(lengths),
+                _ptr(S0), _seq(o), _ptr(S), _ptr(scratch), nbytes, _ptr(_workspace(dev)), _handle(dev, stream))
+        if wait_limit_us or test_stall_producer:
+            st = lib.vla_decay_forward_ex(*args, _wait_options(wait_limit_us, test_stall_producer))
+        else:
+            st = lib.vla_decay_forward(*args)
     _done(st, "vla_decay_forward", dev, stream, check)
     return o, S
 
@@ -173,7 +183,7 @@ def vla_decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
 def vla_decay_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor, scale: float = 1.0,
                        state: Optional[torch.Tensor] = None, grad_o: Optional[torch.Tensor] = None,
                        grad_state: Optional[torch.Tensor] = None, *, lengths: Optional[torch.Tensor] = None, out=None,
-                       stream=None, check: bool = False):
+                       stream=None, check: bool = False, wait_limit_us: int = 0, test_stall_producer: bool = False):
     """Gradient of a scalar loss through vla_decay_forward (reverse mode).
 
     ``grad_o`` = dL/do like q and ``grad_state`` = dL/dS [B, H, d, d] float32
@@ -181,7 +191,8 @@ def vla_decay_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
     of which nothing is kept. Returns ``((dq, dk, dv), dS0)``: like q, and
     float32 [B, H, d, d]. No gradient is formed for log_decay and scale.
     ``out`` = (dq, dk, dv, dS0) preallocated (dS0 neither ``state`` nor
-    ``grad_state``).
+    ``grad_state``). ``wait_limit_us`` and ``test_stall_producer`` as in the
+    forward call.
     """
     for name, x in (("q", q), ("k", k), ("v", v), ("grad_o", grad_o)):
         if x is not None:
@@ -210,10 +221,13 @@ def vla_decay_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
         q, k, v, grad_o = (_seq_in(x) for x in (q, k, v, grad_o))
         nbytes = _decay_scratch(B, H, T, d, 1, dev.index)
         scratch = _call_buffer(dev, nbytes, False) if nbytes else None
-        st = lib.vla_decay_backward(_seq(q), _seq(k), _seq(v), _seq(grad_o), _DTYPES[q.dtype], B, H, T, d,
-                                    _ptr(log_decay), scale, _ptr(lengths), _ptr(S0), _ptr(dS_T),
-                                    *(_seq(x) for x in grads), _ptr(dS0), _ptr(scratch), nbytes,
-                                    _ptr(_workspace(dev)), _handle(dev, stream))
+        args = (_seq(q), _seq(k), _seq(v), _seq(grad_o), _DTYPES[q.dtype], B, H, T, d, _ptr(log_decay), scale,
+                _ptr(lengths), _ptr(S0), _ptr(dS_T), *(_seq(x) for x in grads), _ptr(dS0), _ptr(scratch), nbytes,
+                _ptr(_workspace(dev)), _handle(dev, stream))
+        if wait_limit_us or test_stall_producer:
+            st = lib.vla_decay_backward_ex(*args, _wait_options(wait_limit_us, test_stall_producer))
+        else:
+            st = lib.vla_decay_backward(*args)
     _done(st, "vla_decay_backward", dev, stream, check)
     return tuple(grads), dS0
 

@@ -47,6 +47,7 @@ struct DecayArgs {
     int bh0, bhs;       // the launch's heads: [bh0, bh0 + bhs) of the B x H
     int nseg, seg_len;  // segments of the sequence and their tokens (a multiple of 64)
     unsigned long long wait_ns;
+    int stall;          // testing: the last chunk's loads are kept back
 };
 
 // Tokens [t0, t0 + n) of segment s of sequence b.

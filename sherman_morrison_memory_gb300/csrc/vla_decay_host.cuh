@@ -170,7 +170,10 @@ __global__ void __launch_bounds__(STEP_THREADS) vla_decay_step_kernel(const T* _
     if (bad != bad && status) vla::record_failure(status, vla::BIT_NONFINITE, 3, bh, 0);
 }
 
-constexpr unsigned long long kWaitNs = 2000000000ull;
+void take_options(DecayArgs& p, const vla_options* opts) {
+    p.wait_ns = 1000ull * (opts && opts->wait_limit_us ? opts->wait_limit_us : 2000000u);
+    p.stall = opts && opts->test_stall_producer;
+}
 
 // A launch's heads and their cut into segments.
 struct Cut {
@@ -373,10 +376,10 @@ size_t vla_decay_scratch_bytes(int B, int H, int T, int d, int backward) {
     return vla_layer::scratch_bytes_of(B, H, T, d, backward != 0);
 }
 
-vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* v, vla_dtype dtype, int B, int H,
-                             int T, int d, const float* log_decay, float scale, const int* lengths, const float* S0,
-                             const vla_seq_out* o, float* S_out, void* scratch, size_t scratch_bytes, void* status,
-                             void* stream) {
+vla_status vla_decay_forward_ex(const vla_seq* q, const vla_seq* k, const vla_seq* v, vla_dtype dtype, int B, int H,
+                                int T, int d, const float* log_decay, float scale, const int* lengths,
+                                const float* S0, const vla_seq_out* o, float* S_out, void* scratch,
+                                size_t scratch_bytes, void* status, void* stream, const vla_options* opts) {
     using namespace vla_layer;
     if (!good_sizes(B, H, T) || !good_dtype(dtype) || !std::isfinite(scale)) return VLA_ERR_INVALID_ARG;
     if (!good_d(d)) return VLA_ERR_UNSUPPORTED;
@@ -405,7 +408,7 @@ vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
     p.log_decay = log_decay;
     p.lengths = lengths;
     p.status = static_cast<vla::DeviceStatus*>(status);
-    p.wait_ns = kWaitNs;
+    take_options(p, opts);
     c.cuts = plan_call(B, H, 1, 1, T, d, dtype, c.cut);
     p.seg = static_cast<float*>(scratch);
     p.role[0] = Role{to_seq(q, B, H, T), to_seq(k, B, H, T), to_seq(v, B, H, T), to_seq(o, B, H, T),
@@ -420,11 +423,11 @@ vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
     return launch_call(c, d, dtype, s);
 }
 
-vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO,
-                              vla_dtype dtype, int B, int H, int T, int d, const float* log_decay, float scale,
-                              const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,
-                              const vla_seq_out* dk, const vla_seq_out* dv, float* dS0, void* scratch,
-                              size_t scratch_bytes, void* status, void* stream) {
+vla_status vla_decay_backward_ex(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO,
+                                 vla_dtype dtype, int B, int H, int T, int d, const float* log_decay, float scale,
+                                 const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,
+                                 const vla_seq_out* dk, const vla_seq_out* dv, float* dS0, void* scratch,
+                                 size_t scratch_bytes, void* status, void* stream, const vla_options* opts) {
     using namespace vla_layer;
     if (!good_sizes(B, H, T) || !good_dtype(dtype) || !std::isfinite(scale)) return VLA_ERR_INVALID_ARG;
     if (!good_d(d)) return VLA_ERR_UNSUPPORTED;
@@ -457,7 +460,7 @@ vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
     p.log_decay = log_decay;
     p.lengths = lengths;
     p.status = static_cast<vla::DeviceStatus*>(status);
-    p.wait_ns = kWaitNs;
+    take_options(p, opts);
     c.cuts = plan_call(B, H, 3, 2, T, d, dtype, c.cut);
     p.seg = static_cast<float*>(scratch);
     p.role[0] = Role{G, V, K, to_seq(dq, B, H, T), S0, nullptr, 1, 0, scale, scale, 1.f, 3, 2, 1};
@@ -479,6 +482,23 @@ vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
          !make_map(&c.maps.out[2], dv, B, H, T, d)))
         return VLA_ERR_CUDA;
     return launch_call(c, d, dtype, s);
+}
+
+vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* v, vla_dtype dtype, int B, int H,
+                             int T, int d, const float* log_decay, float scale, const int* lengths, const float* S0,
+                             const vla_seq_out* o, float* S_out, void* scratch, size_t scratch_bytes, void* status,
+                             void* stream) {
+    return vla_decay_forward_ex(q, k, v, dtype, B, H, T, d, log_decay, scale, lengths, S0, o, S_out, scratch,
+                                scratch_bytes, status, stream, nullptr);
+}
+
+vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO,
+                              vla_dtype dtype, int B, int H, int T, int d, const float* log_decay, float scale,
+                              const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,
+                              const vla_seq_out* dk, const vla_seq_out* dv, float* dS0, void* scratch,
+                              size_t scratch_bytes, void* status, void* stream) {
+    return vla_decay_backward_ex(q, k, v, dO, dtype, B, H, T, d, log_decay, scale, lengths, S0, dS_T, dq, dk, dv, dS0,
+                                 scratch, scratch_bytes, status, stream, nullptr);
 }
 
 vla_status vla_decay_step(const void* q, const void* k, const void* v, vla_dtype dtype, int B, int H, int d,

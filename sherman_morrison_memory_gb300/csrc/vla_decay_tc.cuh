@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
         auto load = [&](int m) {
             const int i = m % L::NST, t = sp.t0 + chunk0(m);
             const uint32_t dst = sb + L::ST + i * 3 * L::TILE;
-            if (one) {
+            if (one && !(p.stall && m + 1 == chunks)) {
                 vla::mbar_arrive_expect_tx(full + i, (STATE ? 2 : 3) * L::TILE);
 #pragma unroll
                 for (int q = STATE ? 1 : 0; q < 3; ++q)

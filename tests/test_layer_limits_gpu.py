@@ -212,3 +212,41 @@ def test_head_norm_weights_behind_two_to_the_31():
     # the few heads against the definition
     n = R.norm_grads(part(dy), part(x), w[heads], 1e-5)
     assert float((dw[heads].double().cpu() - n[1]).abs().max()) <= 64 * d * R.U * float(n[3].max())
+
+
+# ---- waits that run out -------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,d", [(9, 32), (64, 96), (70, 128), (700, 64), (1000, 128), (640, 96)])
+def test_a_wait_that_runs_out_is_reported(T, d):
+    """The last chunk's loads kept back: every block of the call returns within its limit, the call reports it, and the
+    next one on the stream is right. In one piece (many heads) and in segments (few)."""
+    for B, H in ((1, 2), (2, 160)):
+        q, k, v, do = seqs(4, B, H, T, d, BF, seed=T)
+        g = -torch.linspace(0.01, 0.5, H).cuda()
+        S0 = state_like(B, H, d, 1)
+        n = torch.full((B,), T - 1, dtype=torch.int32, device="cuda")
+        stall = dict(wait_limit_us=500, test_stall_producer=True, check=True, lengths=n)
+        vla.vla_get_last_device_status()
+        for _ in range(2):
+            with pytest.raises(vla.VLAError) as e:
+                vla.vla_decay_forward(q, k, v, g, 0.3, S0, **stall)
+            assert e.value.status == vla._binding.VLA_ERR_TIMEOUT and 0 <= e.value.detail[1] < B * H
+            with pytest.raises(vla.VLAError) as e:
+                vla.vla_decay_backward(q, k, v, g, 0.3, S0, do, S0, **stall)
+            assert e.value.status == vla._binding.VLA_ERR_TIMEOUT
+        # a limit that nothing reaches, and none given
+        fwd = vla.vla_decay_forward(q, k, v, g, 0.3, S0, lengths=n, wait_limit_us=1000000, check=True)
+        bwd = vla.vla_decay_backward(q, k, v, g, 0.3, S0, do, S0, lengths=n, check=True)
+        pick = [0, H - 1]
+        part = lambda x: x[:, pick]  # noqa: E731
+        check_forward(part(q), part(k), part(v), g[pick], 0.3, part(S0), n, tuple(part(x) for x in fwd))
+        check_backward(part(q), part(k), part(v), g[pick], 0.3, part(S0), part(do), part(S0), n,
+                       (tuple(part(x) for x in bwd[0]), part(bwd[1])))
+
+
+def test_calls_without_waits_do_not_stall():
+    for dtype, T in ((F32, 100), (BF, 8)):
+        q, k, v = seqs(3, 1, 2, T, 64, dtype)
+        g = decays(2)
+        got = vla.vla_decay_forward(q, k, v, g, wait_limit_us=500, test_stall_producer=True, check=True)
+        check_forward(q, k, v, g, 1.0, None, None, got)
