@@ -157,7 +157,7 @@ vla_status vla_head_norm_backward(const vla_seq* dy, const vla_seq* x, vla_dtype
  *   codes   bits 8: [N, rows, d] int8; bits 4: [N, rows, d / 2] bytes, value
  *           2 i in the low half of byte i. 16-byte aligned.
  *   scales  [N, rows, d / 32] float32
- * slots as for vla_decay_step(), NULL for slot b. B <= 65535. */
+ * (both may be NULL where N is 0). slots as for vla_decay_step(), NULL for slot b. B <= 65535. */
 
 /* Write x [B, rows, d] float32 (16-byte aligned) into slots. A negative slot is skipped; one
  * >= N or used before in the call is skipped and sets VLA_ERR_BAD_SLOT. */

@@ -384,6 +384,11 @@ def _cache(codes, scales):
     return bits, N, (*lead, d)
 
 
+def _check_count(B: int):
+    if B > 65535:
+        raise ValueError(f"{B} states in one call, more than 65,535")
+
+
 def _rows(shape) -> int:
     n = 1
     for x in shape[:-1]:
@@ -400,7 +405,8 @@ def vla_state_store(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
 
     A negative slot is skipped; one out of range or used before in the call is
     skipped and recorded (VLA_ERR_BAD_SLOT), as is a group with a NaN or Inf,
-    which reads back as NaN (VLA_ERR_NONFINITE). ``check=True`` raises.
+    which reads back as NaN (VLA_ERR_NONFINITE). ``check=True`` raises. At
+    most 65,535 states a call.
     """
     bits, N, shape = _cache(codes, scales)
     lib = load_library()
@@ -410,6 +416,7 @@ def vla_state_store(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, 
     B = x.shape[0]
     if slots is None and B > N:
         raise ValueError(f"{B} states for {N} slots")
+    _check_count(B)
     with _on(dev, stream):
         x = _check_f32(x, (B, *shape), dev, "x")
         slots = _check_index(slots, B, dev, "slots")
@@ -424,7 +431,8 @@ def vla_state_load(codes: torch.Tensor, scales: torch.Tensor, slots: Optional[to
     None: all of them) of a cache: float32 [B, ...], ready to be carried on.
 
     A negative slot reads as zero, and so does one out of range, which is
-    recorded (VLA_ERR_BAD_SLOT). ``out``: preallocated result.
+    recorded (VLA_ERR_BAD_SLOT). ``out``: preallocated result. At most 65,535
+    states a call.
     """
     bits, N, shape = _cache(codes, scales)
     lib = load_library()
@@ -432,6 +440,7 @@ def vla_state_load(codes: torch.Tensor, scales: torch.Tensor, slots: Optional[to
     if slots is not None and slots.dim() != 1:
         raise ValueError("slots must be [B]")
     B = N if slots is None else slots.shape[0]
+    _check_count(B)
     with _on(dev, stream):
         slots = _check_index(slots, B, dev, "slots")
         if out is None:

@@ -140,7 +140,7 @@ vla_status check_cache(const void* codes, const float* scales, int N, int B, lon
     if (B > 65535 || rows > (1LL << 36) / d) return VLA_ERR_INVALID_ARG;
     if (!slots && B > N) return VLA_ERR_INVALID_ARG;
     if (B == 0 || rows == 0) return VLA_OK;
-    if (!codes || !scales || !x || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(x, 16) || !aligned(slots, 4) ||
+    if ((N > 0 && (!codes || !scales)) || !x || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(x, 16) || !aligned(slots, 4) ||
         !aligned(status, 16))
         return VLA_ERR_INVALID_ARG;
     return VLA_OK;

@@ -250,3 +250,35 @@ def test_calls_without_waits_do_not_stall():
         g = decays(2)
         got = vla.vla_decay_forward(q, k, v, g, wait_limit_us=500, test_stall_producer=True, check=True)
         check_forward(q, k, v, g, 1.0, None, None, got)
+
+
+# ---- caches of no slots and of many -------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_cache_without_slots(bits):
+    """A server that parks nothing yet: idle rows are skipped and read as fresh states, any slot is out of range."""
+    codes, scales = vla.vla_state_cache(0, (2, 32, 32), bits)
+    idle = torch.tensor([-1, -1], dtype=torch.int32, device="cuda")
+    x = state_like(2, 2, 32, 1)
+    vla.vla_state_store(x, codes, scales, idle, check=True)
+    assert not vla.vla_state_load(codes, scales, idle, check=True).any()
+    assert vla.vla_state_load(codes, scales).shape == (0, 2, 32, 32)
+    assert not vla.vla_state_load(codes, scales, idle + 1).any()
+    assert vla.vla_get_last_device_status()[0] == vla._binding.VLA_ERR_BAD_SLOT
+
+
+def test_cache_of_many_slots():
+    """More slots than states a call may have: any of them, at most 65,535 at a time."""
+    N = 65540
+    codes, scales = vla.vla_state_cache(N, (32,), 8)
+    x = torch.randn(N, 32, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda")
+    slots = torch.arange(N, dtype=torch.int32, device="cuda")
+    for call in (lambda: vla.vla_state_store(x, codes, scales), lambda: vla.vla_state_load(codes, scales),
+                 lambda: vla.vla_state_load(codes, scales, slots)):
+        with pytest.raises(ValueError, match="65,535"):
+            call()
+    assert not codes.any()
+    vla.vla_state_store(x[:65535], codes, scales, check=True)
+    vla.vla_state_store(x[65535:], codes, scales, slots[65535:], check=True)
+    got = torch.cat([vla.vla_state_load(codes, scales, s.contiguous(), check=True) for s in (slots[:65535], slots[65535:])])
+    assert torch.equal(got.cpu(), R.store(x, 8)[0])
