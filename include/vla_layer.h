@@ -7,10 +7,11 @@
  * Conventions as in vla.h: device pointers owned by the caller, `stream` a
  * cudaStream_t as void*, calls asynchronous on it, argument errors returned at
  * once, head dimensions d in {32, 64, 96, 128} (else VLA_ERR_UNSUPPORTED),
- * arithmetic and states in fp32. Two things differ. Sequences may have any
- * strides (vla_seq), so that a projection's [B, T, H, d] output is read in
+ * states in fp32, sums and statistics in fp32. Two things differ. Sequences may
+ * have any strides (vla_seq), so that a projection's [B, T, H, d] output is read in
  * place. And results that are sequences (o, y, the gradients) have the inputs'
- * type, rounded once at the end.
+ * type, rounded at the end; what bf16 calls of vla_decay_*() round before that
+ * stands there.
  *
  * An output of a call overlaps neither itself nor an input nor another output
  * (nor the call's scratch), except in place where an entry point says so: blocks
@@ -64,6 +65,13 @@ typedef struct {
  * them are written as zero, whatever the inputs hold there, and the final
  * state is the one after the sequence's own last token.
  *
+ * Rounding. fp32 calls and bf16 calls of up to 8 tokens: fp32 throughout. bf16
+ * calls of more tokens: the final states as in fp32; on the way to o, dq, dk and
+ * dv the products of pairs of tokens, and the state as the tokens of a chunk of 64
+ * find it, are rounded to bf16 (a term meets one of the two, at most 2^-8 of it)
+ * and summed in fp32. Errors are then about 2.35e-3 of a row's size, where
+ * rounding the exact result to bf16 gives 1.65e-3.
+ *
  * A token's NaN or Inf reaches the results that depend on it, as the formulas
  * have it, and no others: no earlier row of o or dq, no later one of dk or dv.
  * One in an output or a final state sets VLA_ERR_NONFINITE in the
@@ -85,8 +93,9 @@ vla_status vla_decay_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
 /* Reverse mode of vla_decay_forward(): from dO = dL/do and dS_T = dL/dS_out
  * (NULL: zero) the gradients dq, dk, dv and, unless NULL, dS0 = dL/dS0:
  *   dq_t = scale S_t^T dO_t,
- *   R_t = l R_{t+1} + scale dO_t q_t^T (R holds dS_T behind the last token),
- *   dk_t = R_t^T v_t,  dv_t = R_t k_t,  dS0 = l R_1.
+ *   R_n = dS_T + scale dO_n q_n^T for a sequence's last token n,
+ *   R_t = l R_{t+1} + scale dO_t q_t^T before it,
+ *   dk_t = R_t^T v_t,  dv_t = R_t k_t,  dS0 = l R_1 (dS_T where there are no tokens).
  * Nothing is kept from the forward call. dS0 is neither S0 nor dS_T. */
 vla_status vla_decay_backward(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO,
                               vla_dtype dtype, int B, int H, int T, int d, const float* log_decay, float scale,

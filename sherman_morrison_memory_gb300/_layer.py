@@ -144,6 +144,8 @@ def vla_decay_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
     sequence's last token. ``log_decay`` [H] float32; ``state`` [B, H, d, d]
     float32 continues a previous call. ``lengths`` [B] int32 (on the device):
     sequence b has only its first lengths[b] tokens; o is zero behind them.
+    bf16 calls of more than 8 tokens round pair products and the state that a
+    chunk's tokens see to bf16 on the way to o (S itself stays fp32).
     ``out`` = (o, S) preallocated; S may be ``state``. ``check=True``
     synchronises and raises on an in-kernel failure or a non-finite result.
     ``wait_limit_us`` (0: 2,000,000) bounds each in-kernel wait;
