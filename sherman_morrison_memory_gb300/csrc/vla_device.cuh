@@ -82,8 +82,8 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // Slow path of mbar_wait: suspend in hardware between checks (no polling
 // loop that would take issue slots from working warps), give up after
 // `limit_ns` or when the abort flag (if not null) is raised.
-__device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, const volatile int* abort_flag,
-                                            uint64_t limit_ns) {
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, const volatile int* abort_flag,
+                                                   uint64_t limit_ns) {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 0; it < (1u << 24); ++it) {
         if (mbar_try_wait_suspend(bar, parity, 20000u)) return true;

@@ -8,9 +8,6 @@
 
 #include <atomic>
 
-// vla_device.cuh defines this function with external linkage: it has another
-// name in this translation unit than in vla_forward.cu's
-#define mbar_wait_slow mbar_wait_slow_layer
 #include "vla_device.cuh"
 #include "vla_internal.h"
 #include "vla_layer.h"
