@@ -20,13 +20,11 @@ namespace {
 struct ScanRole {
     const float* init;
     float* fin;
-    int init_t;   // init and fin hold the transposed state
+    int init_t;   // init holds the transposed state (of a role without fin)
     int reverse;
 };
 struct ScanArgs {
     ScanRole role[2];
-    const float* log_decay;
-    vla::DeviceStatus* status;
 };
 
 constexpr int SCAN_THREADS = 128;
@@ -90,11 +88,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) vla_decay_scan_kernel(const __gr
         }
     }
     if (r.fin) {
-        float* m = r.fin + at;
-        if (r.init_t)
-            m[y * D + x] = s.x, m[(y + 1) * D + x] = s.y, m[(y + 2) * D + x] = s.z, m[(y + 3) * D + x] = s.w;
-        else
-            *reinterpret_cast<float4*>(m + i) = s;
+        *reinterpret_cast<float4*>(r.fin + at + i) = s;
         const float bad = fmaf(s.x, 0.f, fmaf(s.y, 0.f, fmaf(s.z, 0.f, s.w * 0.f)));
         if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, p.T);
     }
