@@ -11,8 +11,8 @@ in place. One whose last dimension is not dense, or whose rows do not start on
 inputs' type; states, statistics and weights are float32. Preallocated outputs
 share no memory with inputs or each other (VLAError), except where a call says
 that it works in place; rows that lie between those of another array are fine.
-Any call may be captured in a CUDA graph after one eager call of the package on the device
-(which lays out the shared status record).
+Any call may be captured in a CUDA graph after one eager call of the package on
+the device (which lays out the shared status record).
 """
 from __future__ import annotations
 
@@ -239,11 +239,12 @@ def vla_decay_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay:
                    stream=None, check: bool = False) -> torch.Tensor:
     """One token of vla_decay_forward's recurrence for a batch of sequences.
 
-    q, k, v [B, H, d]; ``state`` [N, H, d, d] float32, contiguous, is updated
-    in place; ``slots`` [B] int32 (on the device) names each sequence's entry
-    of it (None: entry b). A negative slot is an idle row, whose o is zero; one
-    that is out of range or was used by an earlier row is left alone too and
-    recorded (VLA_ERR_BAD_SLOT, raised by ``check=True``). Returns o like q.
+    q, k, v [B, H, d] (copied unless contiguous); ``state`` [N, H, d, d]
+    float32, contiguous, is updated in place; ``slots`` [B] int32 (on the
+    device) names each sequence's entry of it (None: entry b). A negative slot
+    is an idle row, whose o is zero; one that is out of range or was used by an
+    earlier row is left alone too and recorded (VLA_ERR_BAD_SLOT, raised by
+    ``check=True``). Returns o like q.
     """
     if q.dim() != 3 or q.dtype not in _DTYPES or q.device.type != "cuda" or q.shape[-1] not in _DIMS:
         raise ValueError(f"q must be a [B, H, d] float32 or bfloat16 CUDA tensor, d in {_DIMS}")

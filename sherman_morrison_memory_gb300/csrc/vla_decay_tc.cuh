@@ -38,6 +38,9 @@
 // the state (OE, T), 15 those of the pairs (SC, OI).
 // Every wait is bounded; one that runs out raises the block's abort flag.
 //
+// P's zeros above the diagonal are multiplied too: where c holds an Inf or NaN, and
+// for heads whose powers overflow, a block goes token by token (by_token()).
+//
 // STATE: only the segment's own state, from zero (b and c).
 #pragma once
 
@@ -300,7 +303,8 @@ __global__ void __launch_bounds__(TcLay<D>::THREADS, 1)
         const bool ok = wait_on(w, parity & 1, abort_flag, p.wait_ns, p.status, warp / 4, bh);
         return __all_sync(0xffffffffu, ok) != 0;
     };
-    // The same for what has to end before the block does, also where a wait has run out.
+    // The same for what has to end before the block does, also where a wait has run
+    // out; the warp leaves it whole, as a barrier counts a split warp twice.
     auto drain_warp = [&](uint64_t* w, uint32_t parity) {
         if (!__all_sync(0xffffffffu, vla::mbar_try_wait(w, parity & 1)))
             vla::mbar_wait_slow(w, parity & 1, nullptr, p.wait_ns);
