@@ -201,7 +201,8 @@ double ends_of(vla_dtype dt) { return dt == VLA_BF16 ? 6 : 0.5; }
 // the 9 it takes, 590 in 19; gradients of 4 x 8 heads of 4,096 tokens, d = 64: 67
 // us in the one piece it takes, 91 in 4; fp32, 40 heads of 1,021 tokens, d = 64:
 // 178 in one, 85 in 6, 79 in the 8 it takes; their gradients 180 in the one piece
-// it takes, 198 in 8.)
+// it takes, 198 in 8. At most 64 segments: their states are the call's scratch, and
+// the scan goes over them in turn; more were not measured.)
 double plan(long long heads, int roles, int state_roles, int T, int d, vla_dtype dt, Cut* cut) {
     const int chunks = (T + 63) / 64;
     const bool bf16 = dt == VLA_BF16;

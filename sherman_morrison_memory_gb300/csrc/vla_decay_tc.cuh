@@ -27,7 +27,7 @@
 // transposed fragments; SC and the outputs are read in fragments (16x256b) that
 // stmatrix writes in whole 16-byte rows; and the pairs' weights, which in
 // fragments depend on the lane and the blocks' distance, stay in registers.
-// (8 x 16 heads of 4,096 tokens, d = 96: 89 us, 4.5 TB/s of its sequences.)
+// (8 x 16 heads of 4,096 tokens, d = 96: 90 us, 4.5 TB/s of its sequences.)
 //
 // d is padded to DP = 64 or 128 columns by TMA's zero fill. DP is also the MMAs'
 // M, so that at d <= 64 a warp's quarter of the TMEM lanes holds 16 rows of the
