@@ -130,6 +130,80 @@ vla_status vla_decay_step(const void* q, const void* k, const void* v, vla_dtype
                           const float* log_decay, float scale, float* states, int N, const int* slots, void* o,
                           void* status, void* stream);
 
+/* ---- the gated delta rule -----------------------------------------------------
+ *
+ *   S_t = a_t S_{t-1} + beta_t (v_t - a_t S_{t-1} k_t) k_t^T,   o_t = scale S_t q_t,
+ *   a_t = exp(log_decay_t)
+ *
+ * Each token corrects what the decayed memory gives for its key towards its value:
+ * beta 1 and a unit key replace it, beta 0 leaves it. S as above. Keys are taken
+ * as they are (vla_qk_norm() makes them unit rows); where beta |k|^2 is above 2 the
+ * recurrence itself grows without bound.
+ *
+ * log_decay and beta are float32 gates for each token and head, at any strides
+ * (vla_gate). log_decay NULL: 0. Values below -256 count as -256 (a factor of 0);
+ * values above 0 are taken as they are, and a head that grows beyond float32 within
+ * 32 tokens gives Inf or NaN. lengths: as for vla_decay_forward().
+ *
+ * Rounding. fp32 calls, and of bf16 calls the states, dS0 and the gates' gradients:
+ * fp32 throughout. bf16 o, dq and dk: beside the result, each term is rounded to
+ * bf16 once on its way (the state, a pair product or dv, as they meet the token), at
+ * most 2^-8 of it; errors are then about 2.35e-3 of a row's size, where rounding the
+ * exact result gives 1.65e-3. dv is rounded at the end alone.
+ *
+ * A token's NaN or Inf reaches the results that depend on it, and may reach those of
+ * other tokens of its block of 64 in the same head. One in an output sets VLA_ERR_NONFINITE
+ * in the status record. */
+
+/* Gates [B, H, T] float32: element (b, h, t) is data[b * stride_b + h * stride_h +
+ * t * stride_t]. data is 4-byte aligned; the strides of dimensions longer than 1
+ * are not negative; 0 repeats a value (else VLA_ERR_INVALID_ARG). */
+typedef struct {
+    const float* data;
+    long long stride_b, stride_h, stride_t;
+} vla_gate;
+
+/* The same for an output; the strides are positive. */
+typedef struct {
+    float* data;
+    long long stride_b, stride_h, stride_t;
+} vla_gate_out;
+
+/* The rule over T tokens. S0, S_out and T == 0 as for vla_decay_forward(); S_out
+ * may be S0. */
+vla_status vla_delta_forward(const vla_seq* q, const vla_seq* k, const vla_seq* v, vla_dtype dtype, int B, int H, int T,
+                             int d, const vla_gate* log_decay, const vla_gate* beta, float scale, const int* lengths,
+                             const float* S0, const vla_seq_out* o, float* S_out, void* status, void* stream);
+
+/* Device scratch of vla_delta_backward(), 256-byte aligned, one call's own (0 for
+ * sizes that it refuses): the recurrence's corrections, 4 d bytes a token and head,
+ * and two states every 64 tokens (32 in fp32). */
+size_t vla_delta_scratch_bytes(vla_dtype dtype, int B, int H, int T, int d);
+
+/* Reverse mode of vla_delta_forward(): from dO = dL/do and dS_T = dL/dS_out (NULL:
+ * zero) the gradients dq, dk, dv, dlog_decay (may be NULL), dbeta and, unless NULL,
+ * dS0 = dL/dS0. With R the gradient of S_t (scale dO_t q_t^T and later tokens' part),
+ * e_t = v_t - a_t S_{t-1} k_t and D_t = a_t S_{t-1}:
+ *   dq_t = scale S_t^T dO_t,  dbeta_t = (R k_t) . e_t,  dv_t = beta_t R k_t,
+ *   dk_t = beta_t R^T e_t - D_t^T dv_t,  R' = R - dv_t k_t^T,
+ *   dlog_decay_t = <R', D_t>,  and a_t R' is what S_{t-1} gets.
+ * Nothing is kept from the forward call. Rows behind a sequence's end are written
+ * as zero. dS0 is neither S0 nor dS_T. A gate of stride 0 gets its gradients
+ * token by token; their sum is the caller's. */
+vla_status vla_delta_backward(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO, vla_dtype dtype,
+                              int B, int H, int T, int d, const vla_gate* log_decay, const vla_gate* beta, float scale,
+                              const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,
+                              const vla_seq_out* dk, const vla_seq_out* dv, const vla_gate_out* dlog_decay,
+                              const vla_gate_out* dbeta, float* dS0, void* scratch, size_t scratch_bytes, void* status,
+                              void* stream);
+
+/* One token of the rule for B sequences, their states updated in place in a pool;
+ * log_decay (NULL: 0) and beta [B, H] float32, contiguous; the rest as for
+ * vla_decay_step(). fp32 throughout. */
+vla_status vla_delta_step(const void* q, const void* k, const void* v, vla_dtype dtype, int B, int H, int d,
+                          const float* log_decay, const float* beta, float scale, float* states, int N,
+                          const int* slots, void* o, void* status, void* stream);
+
 /* ---- layer norm of each head's readout --------------------------------------
  *
  *   y = (x - mean) rstd weight[h] + bias[h] over the d values of a row,

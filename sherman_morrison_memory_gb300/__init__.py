@@ -15,7 +15,8 @@ path of a caller holding host buffers).
 
 Around it (``include/vla_layer.h``, CUDA tensors): linear attention with a
 decay per head (``vla_decay_forward``, ``vla_decay_backward``,
-``vla_decay_step``), the layer norm of each head's readout (``vla_head_norm``,
+``vla_decay_step``), the gated delta rule (``vla_delta_forward``,
+``vla_delta_backward``, ``vla_delta_step``), the layer norm of each head's readout (``vla_head_norm``,
 ``vla_head_norm_backward``) and a quantised cache of states
 (``vla_state_cache``, ``vla_state_store``, ``vla_state_load``).
 """
@@ -46,6 +47,11 @@ from ._binding import (  # noqa: F401
     vla_status_string,
     vla_workspace_bytes,
 )
+from ._delta import (  # noqa: F401
+    vla_delta_backward,
+    vla_delta_forward,
+    vla_delta_step,
+)
 from ._layer import (  # noqa: F401
     vla_decay_backward,
     vla_decay_forward,
@@ -67,6 +73,9 @@ __all__ = [
     "vla_decay_forward",
     "vla_decay_backward",
     "vla_decay_step",
+    "vla_delta_forward",
+    "vla_delta_backward",
+    "vla_delta_step",
     "vla_head_norm",
     "vla_head_norm_backward",
     "vla_state_cache",

@@ -72,6 +72,10 @@ def _layer_prototypes(lib):
             ("vla_decay_forward", forward, ci), ("vla_decay_forward_ex", forward + options, ci),
             ("vla_decay_backward", backward, ci), ("vla_decay_backward_ex", backward + options, ci),
             ("vla_decay_step", [vp] * 3 + [ci] * 4 + [vp, cf, vp, ci, vp, vp, vp, vp], ci),
+            ("vla_delta_scratch_bytes", [ci] * 5, cz),
+            ("vla_delta_forward", [sq] * 3 + [ci] * 5 + [sq, sq, cf, vp, vp, sq, vp, vp, vp], ci),
+            ("vla_delta_backward", [sq] * 4 + [ci] * 5 + [sq, sq, cf, vp, vp, vp] + [sq] * 5 + [vp, vp, cz, vp, vp], ci),
+            ("vla_delta_step", [vp] * 3 + [ci] * 4 + [vp, vp, cf, vp, ci, vp, vp, vp, vp], ci),
             ("vla_head_norm", [sq] + [ci] * 5 + [vp, vp, ci, cf, sq, vp, vp, vp], ci),
             ("vla_head_norm_scratch_bytes", [ci] * 4, cz),
             ("vla_head_norm_backward", [sq] * 2 + [ci] * 5 + [vp, ci, vp, vp, sq, vp, vp, vp, cz, vp], ci),

@@ -1,0 +1,540 @@
+// vla_delta_backward.cuh -- gradients of the gated delta rule (vla_delta.cuh), in
+// three launches: the forward recurrence again, which keeps S before every block
+// of tokens, E and o . dO; the reverse recurrence, which gives dV and keeps R
+// behind every block; and, all blocks side by side, dQ, dK and the gates'
+// gradients. With i, j tokens of a block, S before and R behind it, u = b e:
+//
+//   X[i][j] = scale exp(G_i - G_j) dO_i . u_j  (j <= i),   M[i][j] = -exp(G_i - G_j) dV_i . u_j  (j < i)
+//   dQ = scale diag(exp(G)) dO S + X K
+//   dK = diag(exp(G_C - G)) U R - diag(exp(G)) dV S + X^T Q + M K + M^T K
+//
+// A log decay touches q exp(G), v exp(-G) and the state behind a block alone, so
+//   dg_t = sum over the block's i >= t of (o_i . dO_i - v_i . dV_i) + <R, S> behind the block,
+// of fp32 results of the two recurrences. Before a first token without a state
+// nothing decays: its dg is 0, where the sum would leave its roundings.
+#pragma once
+
+#include "vla_delta.cuh"
+
+namespace vla_layer {
+
+template <int D, typename T>
+struct DeltaReverse {
+    static constexpr int NP = PARTS<T>;
+    static constexpr int TILES = NP == 1 ? 4 : 3;  // K, Q, dO and V (fp32: read where it is used)
+    using L = DeltaLay<D, T, TILES, 3>;
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_reverse_kernel(const __grid_constant__ DeltaArgs p) {
+    using F = DeltaReverse<D, T>;
+    using L = typename F::L;
+    constexpr int NP = F::NP, LD = L::LD, SPAN = BLOCK<T>;
+    extern __shared__ __align__(128) char sm[];
+    const int splits = D / p.rows, bh = blockIdx.x / splits, row0 = (blockIdx.x % splits) * p.rows;
+    const int b = bh / p.H, h = bh % p.H;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, workers = p.rows / 16;
+    const long long n = delta_len(p, b);
+    const int chunks = (int)((n + DC - 1) / DC);
+    // the m-th chunk in the order of work
+    auto tile = [&](int m, int i) { return sm + L::IN + ((m % L::STAGES) * F::TILES + i) * L::TILE; };
+    auto prep = [&](int m) { return sm + L::PREPS + (m & 1) * L::PREP; };
+
+    if (warp >= workers) {
+        const int tid = threadIdx.x - workers * 32, hw = warp - workers;
+        auto load = [&](int m) {
+            if (m < chunks) {
+                const long long t0 = (long long)(chunks - 1 - m) * DC;
+                load_tile<LD, T>(tile(m, 0), p.k, b, h, t0, 0, D, n, tid);
+                load_tile<LD, T>(tile(m, 1), p.q, b, h, t0, 0, D, n, tid);
+                load_tile<LD, T>(tile(m, 2), p.dO, b, h, t0, row0, p.rows, n, tid);
+                if constexpr (F::TILES == 4) load_tile<LD, T>(tile(m, 3), p.v, b, h, t0, row0, p.rows, n, tid);
+            }
+            cp_async_commit();
+        };
+        Whole whole;
+        float g = 0.f, beta = 0.f;
+        auto gates = [&](int m) {
+            const long long t = (long long)(chunks - 1 - m) * DC + lane;
+            const bool on = t >= 0 && t < n;
+            g = on && p.g.p ? *p.g.at(b, h, t) : 0.f;
+            beta = on ? *p.beta.at(b, h, t) : 0.f;
+        };
+        load(0);
+        gates(0);
+        for (int m = 0; m <= chunks; ++m) {  // chunk m is prepared while chunk m - 1 is computed
+            if (m < chunks) {
+                if (NP > 1 && m) load(m);
+                cp_async_wait<0>();
+                vla::named_bar(1, HELPERS);
+                if (NP == 1) load(m + 1);
+                const float gm = g, bm = beta;
+                gates(m + 1);
+                prepare_chunk<L, D, NP, 3, true>(sm, tile(m, 0), tile(m, 1), prep(m), gm, bm, p.scale, whole, hw, lane);
+            }
+            __syncthreads();
+        }
+        zero_tokens<T>(p.dv, b, h, (long long)chunks * DC, p.T, row0, p.rows);
+        return;
+    }
+
+    const int r = lane >> 2, t2 = (lane & 3) * 2, my_row = row0 + warp * 16;
+    float s[D / 8][4];
+    load_rows<D>(s, p.dS_T ? p.dS_T + (size_t)bh * D * D + my_row * D : nullptr, lane);
+    float bad = 0.f;
+    char* stage = sm + L::OUT + warp * DC * L::OUT_LD * 2;
+    __syncthreads();
+    for (int m = 0; m < chunks; ++m) {
+        const long long t0 = (long long)(chunks - 1 - m) * DC;
+        if (m == 0 || (t0 + DC) % SPAN == 0) {
+            const long long blk = t0 / SPAN;
+            const size_t at = ((size_t)bh * (p.blocks + 1) + blk) * D * D + my_row * D;
+            store_rows<D>(s, p.behind + at, lane);
+            const float* S = p.before + at + (size_t)D * D;
+            float dot = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const float2 a = *reinterpret_cast<const float2*>(S + r * D + i * 8 + t2);
+                const float2 c = *reinterpret_cast<const float2*>(S + (r + 8) * D + i * 8 + t2);
+                dot = fmaf(s[i][0], a.x, fmaf(s[i][1], a.y, fmaf(s[i][2], c.x, fmaf(s[i][3], c.y, dot))));
+            }
+#pragma unroll
+            for (int i = 1; i < 32; i <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
+            if (lane == 0) p.ends[((size_t)bh * p.blocks + blk) * (D / 16) + my_row / 16] = dot;
+        }
+        const uint32_t kt = vla::smem_u32(tile(m, 0)), qt = vla::smem_u32(tile(m, 1));
+        const uint32_t ot = vla::smem_u32(tile(m, 2)) + (across_down<LD>(lane) + warp * 16) * 2;
+        const char* pr = prep(m);
+        const float* gates = reinterpret_cast<const float*>(pr + L::GATES);
+        float e[4][4];
+        const float* E = p.E + ((size_t)bh * p.T + t0) * D + my_row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = i * 8 + t2 + (k & 1);
+                e[i][k] = t0 + j < n ? E[(size_t)j * D + r + (k & 2) * 4] : 0.f;
+            }
+        float x[4][4];
+        times_rows<D, LD, NP, 0, L::PLANE>(x, e, s, kt + across_down<LD>(lane) * 2, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 far = *reinterpret_cast<const float2*>(gates + GATE_FAR + i * 8 + t2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[i][k] *= k & 1 ? far.y : far.x;
+        }
+        {
+            float low[4][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                uint32_t a[NP][4];
+#pragma unroll
+                for (int q = 0; q < NP; ++q) ldsm_t(a[q], ot + q * L::PLANE + ks * 16 * LD * 2);
+                times_triangle<3, NP, L::PAIR, false>(x, low, a, ks, vla::smem_u32(pr + L::P) + down_across<PLD>(lane) * 2);
+            }
+            join(x, low);
+        }
+        float u[4][4] = {};
+        {
+            float low[4][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                uint32_t a[3][4];
+                to_operand<3>(a, x[2 * ks], x[2 * ks + 1]);
+                times_triangle<INV_PARTS, 3, L::PAIR, false>(u, low, a, ks, vla::smem_u32(pr + L::INV) + down_across<PLD>(lane) * 2);
+            }
+            join(u, low);
+        }
+        float bd[8], vd[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 beta = *reinterpret_cast<const float2*>(gates + GATE_BETA + i * 8 + t2);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) bd[2 * i + k] = over_rows(fmaf(u[i][k], e[i][k], u[i][2 + k] * e[i][2 + k]));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[i][k] *= k & 1 ? beta.y : beta.x;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            float v0[4], v1[4];
+            if constexpr (NP == 1) {
+                columns_of<1, L::PLANE>(v0, v1, vla::smem_u32(tile(m, 3)) + (across_down<LD>(lane) + warp * 16 + (i / 2) * 16 * LD) * 2);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const long long t = t0 + i * 8 + (k >> 2) * 8 + t2 + (k & 1);
+                    const float v = t < n ? row_of<float>(p.v, b, h, t)[my_row + r + (k & 2) * 4] : 0.f;
+                    (k < 4 ? v0 : v1)[k & 3] = v;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                vd[2 * i + k] = over_rows(fmaf(u[i][k], v0[k], u[i][2 + k] * v0[2 + k]));
+                vd[2 * i + 2 + k] = over_rows(fmaf(u[i + 1][k], v1[k], u[i + 1][2 + k] * v1[2 + k]));
+            }
+        }
+        if (lane < 4) {
+            const size_t at = ((size_t)bh * (D / 16) + my_row / 16) * p.T + t0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = (i >> 1) * 8 + t2 + (i & 1);
+                if (t0 + j < n) p.bd[at + j] = bd[i], p.vd[at + j] = vd[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (t0 + i * 8 + t2 + (k & 1) < n) bad = fmaf(u[i][k], 0.f, bad);
+        store_tokens<T, L::OUT_LD>(u, stage, p.dv, b, h, t0, my_row, n, p.T, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 near = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + t2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[i][k] *= -(k & 1 ? near.y : near.x);
+        }
+        add_outer<D, LD, NP, L::PLANE>(s, gates[GATE_WHOLE], u, kt + down_across<LD>(lane) * 2);
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) columns_of<NP, L::PLANE>(x[i], x[i + 1], ot + (i / 2) * 16 * LD * 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 near = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + t2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[i][k] *= p.scale * (k & 1 ? near.y : near.x);
+        }
+        add_outer<D, LD, NP, L::PLANE>(s, 1.f, x, qt + down_across<LD>(lane) * 2);
+        __syncthreads();
+    }
+    if (p.dS0) {
+        store_rows<D>(s, p.dS0 + (size_t)bh * D * D + my_row * D, lane);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bad = fmaf(s[i][k], 0.f, bad);
+    }
+    zero_tokens<T>(p.dv, b, h, (long long)chunks * DC, p.T, row0, p.rows);
+    if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, 0);
+}
+
+// dQ, dK and the gates' gradients of a block of tokens: a warp per 16 columns of d. bf16 calls round a term once
+// on its way beside the result: dV as it was written, or S, R or X; U, M and S where dV meets it are two parts.
+template <int D, typename T>
+struct DeltaGrads {
+    static constexpr int NP = PARTS<T>, TB = BLOCK<T>, MT = TB / 16;
+    static constexpr int UP = NP == 1 ? 2 : 3, XP = UP, MP = UP;
+    static constexpr int LD = D + 8, PLANE = TB * LD * 2, XLD = TB + 8, XPLANE = TB * XLD * 2;
+    static constexpr int Q = 0, K = Q + NP * PLANE, O = K + NP * PLANE, V = O + NP * PLANE, U = V + NP * PLANE,
+                         X = U + UP * PLANE, M = X + XP * XPLANE, GATES = M + MP * XPLANE, BYTES = GATES + 5 * TB * 4;
+    static constexpr int THREADS = D * 2;
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(D * 2) vla_delta_grads_kernel(const __grid_constant__ DeltaArgs p) {
+    using L = DeltaGrads<D, T>;
+    constexpr int NP = L::NP, TB = L::TB, MT = L::MT, LD = L::LD, XLD = L::XLD, UP = L::UP, THREADS = L::THREADS;
+    extern __shared__ __align__(128) char sm[];
+    const int bh = blockIdx.x / p.blocks, blk = blockIdx.x % p.blocks, b = bh / p.H, h = bh % p.H;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const long long t0 = (long long)blk * TB, n = delta_len(p, b);
+    const int rows = (int)min((long long)TB, p.T - t0), live = (int)max(0LL, min((long long)TB, n - t0));
+    if (live == 0) {
+        const float zero[8] = {};
+        for (int i = tid; i < rows * (D / 8); i += THREADS) {
+            store8(row_of<T>(p.dq, b, h, t0 + i / (D / 8)) + i % (D / 8) * 8, zero);
+            store8(row_of<T>(p.dk, b, h, t0 + i / (D / 8)) + i % (D / 8) * 8, zero);
+        }
+        for (int i = tid; i < rows; i += THREADS) {
+            if (p.dg.p) *p.dg.at(b, h, t0 + i) = 0.f;
+            *p.dbeta.at(b, h, t0 + i) = 0.f;
+        }
+        return;
+    }
+    // gates: the sums of g as two floats, b, exp(G), exp(G_C - G)
+    float* gates = reinterpret_cast<float*>(sm + L::GATES);
+    if (warp == 0) {
+        double before = 0.0, G[TB / 32];
+#pragma unroll
+        for (int k = 0; k < TB / 32; ++k) {
+            const int j = k * 32 + lane;
+            const float g = j < live && p.g.p ? *p.g.at(b, h, t0 + j) : 0.f;
+            double x = g < -256.f ? -256.0 : (double)g;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, x, m);
+                if (lane >= m) x += y;
+            }
+            G[k] = before + x;
+            before = __shfl_sync(0xffffffffu, G[k], 31);
+        }
+#pragma unroll
+        for (int k = 0; k < TB / 32; ++k) {
+            const int j = k * 32 + lane;
+            const float hi = (float)G[k];
+            gates[j] = hi;
+            gates[TB + j] = (float)(G[k] - (double)hi);
+            gates[2 * TB + j] = j < live ? *p.beta.at(b, h, t0 + j) : 0.f;
+            gates[3 * TB + j] = expf(hi);
+            gates[4 * TB + j] = expf((float)(before - G[k]));
+        }
+    }
+    auto load = [&](int at, const Seq& s) {
+#pragma unroll 4
+        for (int i = tid; i < TB * (D / 8); i += THREADS) {
+            const int row = i / (D / 8), c = i % (D / 8) * 8;
+            char* dst = sm + at + (row * LD + c) * 2;
+            const T* src = row_of<T>(s, b, h, row < live ? t0 + row : 0) + c;
+            if constexpr (NP == 1) {
+                cp_async16(vla::smem_u32(dst), src, row < live ? 16 : 0);
+            } else {
+                float x[8] = {};
+                if (row < live) load8(src, x);
+                uint32_t w[4][NP];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) split<NP>(x[2 * j], x[2 * j + 1], w[j]);
+#pragma unroll
+                for (int q = 0; q < NP; ++q) *reinterpret_cast<uint4*>(dst + q * L::PLANE) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+            }
+        }
+    };
+    load(L::O, p.dO);
+    load(L::V, p.dv);
+    load(L::K, p.k);
+    load(L::Q, p.q);
+    cp_async_commit();
+    {
+        const float* E = p.E + ((size_t)bh * p.T + t0) * D;
+#pragma unroll 4
+        for (int i = tid; i < TB * (D / 8); i += THREADS) {
+            const int row = i / (D / 8), c = i % (D / 8) * 8;
+            float x[8] = {};
+            if (row < live) {
+                load8(E + (size_t)row * D + c, x);
+                const float beta = *p.beta.at(b, h, t0 + row);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= beta;
+            }
+            uint32_t w[4][UP];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split<UP>(x[2 * j], x[2 * j + 1], w[j]);
+#pragma unroll
+            for (int q = 0; q < UP; ++q)
+                *reinterpret_cast<uint4*>(sm + L::U + q * L::PLANE + (row * LD + c) * 2) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+
+    const int r = lane >> 2, t2 = (lane & 3) * 2;
+    const uint32_t base = vla::smem_u32(sm);
+    // X and M, a 16 x 16 block at a time
+    constexpr int UNITS = MT * (MT + 1) / 2;
+    for (int unit = warp; unit < 2 * UNITS; unit += D / 16) {
+        const bool of_m = unit >= UNITS;
+        int mt = 0, np = unit % UNITS;
+        while (np > mt) np -= ++mt;
+        float c[2][4] = {}, cl[2][4] = {};
+        const uint32_t a_at = base + (of_m ? L::V : L::O) + (mt * 16 * LD + down_across<LD>(lane)) * 2;
+        const uint32_t b_at = base + L::U + (np * 16 * LD + across_down<LD>(lane)) * 2;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t a[NP][4], u[UP][4];
+#pragma unroll
+            for (int q = 0; q < NP; ++q) ldsm(a[q], a_at + q * L::PLANE + ks * 32);
+#pragma unroll
+            for (int q = 0; q < UP; ++q) ldsm(u[q], b_at + q * L::PLANE + ks * 32);
+            mma_parts<NP>(c[0], cl[0], a, u, 0);
+            mma_parts<NP>(c[1], cl[1], a, u, 1);
+        }
+        join(c, cl);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int i = mt * 16 + hf * 8 + r, j = np * 16 + k * 8 + t2;
+                float x[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float w = expf((gates[i] - gates[j + q]) + (gates[TB + i] - gates[TB + j + q]));
+                    x[q] = (of_m ? j + q < i : j + q <= i) ? c[k][2 * hf + q] * w * (of_m ? -1.f : p.scale) : 0.f;
+                }
+                if (of_m) {
+                    uint32_t w[L::MP];
+                    split<L::MP>(x[0], x[1], w);
+#pragma unroll
+                    for (int q = 0; q < L::MP; ++q) *reinterpret_cast<uint32_t*>(sm + L::M + q * L::XPLANE + (i * XLD + j) * 2) = w[q];
+                } else {
+                    uint32_t w[L::XP];
+                    split<L::XP>(x[0], x[1], w);
+#pragma unroll
+                    for (int q = 0; q < L::XP; ++q) *reinterpret_cast<uint32_t*>(sm + L::X + q * L::XPLANE + (i * XLD + j) * 2) = w[q];
+                }
+            }
+    }
+
+    // dq and dk of the warp's 16 columns: first the states
+    const int col0 = warp * 16;
+    float dq[MT][2][4] = {}, dk[MT][2][4] = {}, small[3][MT][2][4] = {};
+    float(&ql)[MT][2][4] = NP > 1 ? small[0] : dq;  // fp32 results: the small products apart
+    float(&kl)[MT][2][4] = NP > 1 ? small[1] : dk;
+    // the parts of 16 rows of a state at the warp's columns, as B operands
+    auto state_of = [&](const float* S, int ks, auto& w) {
+        constexpr int N = sizeof(w) / 16;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float* at = S + (size_t)(ks * 16 + (k & 1) * 8 + t2) * D + col0 + (k >> 1) * 8 + r;
+            uint32_t x[N];
+            split<N>(at[0], at[D], x);
+#pragma unroll
+            for (int q = 0; q < N; ++q) w[q][k] = x[q];
+        }
+    };
+    const size_t at = ((size_t)bh * (p.blocks + 1) + blk) * D * D;
+#pragma unroll 2
+    for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t w[UP][4], w1[NP][4];
+        state_of(p.before + at, ks, w);
+#pragma unroll
+        for (int q = 0; q < NP; ++q)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w1[q][k] = w[q][k];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a[NP][4];
+#pragma unroll
+            for (int q = 0; q < NP; ++q) ldsm(a[q], base + L::O + q * L::PLANE + (mt * 16 * LD + ks * 16 + down_across<LD>(lane)) * 2);
+            mma_parts<NP>(dq[mt][0], ql[mt][0], a, w1, 0);
+            mma_parts<NP>(dq[mt][1], ql[mt][1], a, w1, 1);
+#pragma unroll
+            for (int q = 0; q < NP; ++q) ldsm(a[q], base + L::V + q * L::PLANE + (mt * 16 * LD + ks * 16 + down_across<LD>(lane)) * 2);
+            mma_parts<NP>(dk[mt][0], kl[mt][0], a, w, 0);
+            mma_parts<NP>(dk[mt][1], kl[mt][1], a, w, 1);
+        }
+    }
+    {
+        float y[MT][2][4] = {};
+        float(&yl)[MT][2][4] = NP > 1 ? small[2] : y;
+#pragma unroll 2
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t w[NP][4];
+            state_of(p.behind + at, ks, w);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                uint32_t a[UP][4];
+#pragma unroll
+                for (int q = 0; q < UP; ++q) ldsm(a[q], base + L::U + q * L::PLANE + (mt * 16 * LD + ks * 16 + down_across<LD>(lane)) * 2);
+                mma_parts<UP>(y[mt][0], yl[mt][0], a, w, 0);
+                mma_parts<UP>(y[mt][1], yl[mt][1], a, w, 1);
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = mt * 16 + (e >> 1) * 8 + r;
+                    if constexpr (NP > 1) {
+                        dq[mt][k][e] += ql[mt][k][e], dk[mt][k][e] += kl[mt][k][e], y[mt][k][e] += yl[mt][k][e];
+                        ql[mt][k][e] = kl[mt][k][e] = 0.f;
+                    }
+                    dq[mt][k][e] *= p.scale * gates[3 * TB + i];
+                    dk[mt][k][e] = fmaf(gates[4 * TB + i], y[mt][k][e], -gates[3 * TB + i] * dk[mt][k][e]);
+                }
+    }
+    __syncthreads();  // X and M are complete
+    // ... then the pairs
+#pragma unroll
+    for (int ks = 0; ks < MT; ++ks) {
+        uint32_t kk[NP][4], qq[NP][4];
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            ldsm_t(kk[q], base + L::K + q * L::PLANE + (ks * 16 * LD + col0 + down_across<LD>(lane)) * 2);
+            ldsm_t(qq[q], base + L::Q + q * L::PLANE + (ks * 16 * LD + col0 + down_across<LD>(lane)) * 2);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            if (mt >= ks) {  // rows mt of X and M, columns ks
+                uint32_t x[L::XP][4], m[L::MP][4];
+#pragma unroll
+                for (int q = 0; q < L::XP; ++q) ldsm(x[q], base + L::X + q * L::XPLANE + (mt * 16 * XLD + ks * 16 + down_across<XLD>(lane)) * 2);
+#pragma unroll
+                for (int q = 0; q < L::MP; ++q) ldsm(m[q], base + L::M + q * L::XPLANE + (mt * 16 * XLD + ks * 16 + down_across<XLD>(lane)) * 2);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    mma_parts<L::XP>(dq[mt][k], ql[mt][k], x, kk, k);
+                    mma_parts<L::MP>(dk[mt][k], kl[mt][k], m, kk, k);
+                }
+            }
+            if (mt <= ks) {  // rows ks, columns mt, transposed
+                uint32_t x[L::XP][4], m[L::MP][4];
+#pragma unroll
+                for (int q = 0; q < L::XP; ++q) ldsm_t(x[q], base + L::X + q * L::XPLANE + (ks * 16 * XLD + mt * 16 + across_down<XLD>(lane)) * 2);
+#pragma unroll
+                for (int q = 0; q < L::MP; ++q) ldsm_t(m[q], base + L::M + q * L::XPLANE + (ks * 16 * XLD + mt * 16 + across_down<XLD>(lane)) * 2);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    mma_parts<L::XP>(dk[mt][k], kl[mt][k], x, qq, k);
+                    mma_parts<L::MP>(dk[mt][k], kl[mt][k], m, kk, k);
+                }
+            }
+        }
+    }
+    if constexpr (NP > 1) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) join(dq[mt], ql[mt]), join(dk[mt], kl[mt]);
+    }
+    float bad = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int i = mt * 16 + hf * 8 + r;
+            if (i >= rows) continue;
+            T *yq = row_of<T>(p.dq, b, h, t0 + i) + col0 + t2, *yk = row_of<T>(p.dk, b, h, t0 + i) + col0 + t2;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float2 vq = make_float2(dq[mt][k][2 * hf], dq[mt][k][2 * hf + 1]), vk = make_float2(dk[mt][k][2 * hf], dk[mt][k][2 * hf + 1]);
+                if (i >= live) vq = vk = make_float2(0.f, 0.f);
+                bad = fmaf(vq.x, 0.f, fmaf(vq.y, 0.f, fmaf(vk.x, 0.f, fmaf(vk.y, 0.f, bad))));
+                if constexpr (NP == 1) {
+                    *reinterpret_cast<uint32_t*>(yq + k * 8) = pack_bf16(vq.x, vq.y);
+                    *reinterpret_cast<uint32_t*>(yk + k * 8) = pack_bf16(vk.x, vk.y);
+                } else {
+                    *reinterpret_cast<float2*>(yq + k * 8) = vq;
+                    *reinterpret_cast<float2*>(yk + k * 8) = vk;
+                }
+            }
+        }
+    // the gates: sums over the warps' rows, and of them over the tokens from the block's end
+    if (warp == 0) {
+        double behind = 0.0;
+        for (int w = 0; w < D / 16; ++w) behind += (double)p.ends[((size_t)bh * p.blocks + blk) * (D / 16) + w];
+#pragma unroll
+        for (int k = TB / 32 - 1; k >= 0; --k) {
+            const int j = k * 32 + lane;
+            float db = 0.f;
+            double x = 0.0;
+            if (j < live)
+                for (int w = 0; w < D / 16; ++w) {
+                    const size_t i = ((size_t)bh * (D / 16) + w) * p.T + t0 + j;
+                    db += p.bd[i];
+                    x += (double)p.od[i] - (double)p.vd[i];
+                }
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const double y = __shfl_down_sync(0xffffffffu, x, m);
+                if (lane + m < 32) x += y;
+            }
+            x += behind;
+            behind = __shfl_sync(0xffffffffu, x, 0);
+            if (j >= rows) continue;
+            if (j >= live || (!p.S0 && t0 + j == 0)) x = 0.0;
+            bad = fmaf((float)x, 0.f, fmaf(db, 0.f, bad));
+            if (p.dg.p) *p.dg.at(b, h, t0 + j) = (float)x;
+            *p.dbeta.at(b, h, t0 + j) = db;
+        }
+    }
+    if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, (int)t0);
+}
+
+}  // namespace vla_layer

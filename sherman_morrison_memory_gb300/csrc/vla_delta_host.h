@@ -1,0 +1,98 @@
+// vla_delta_host.h -- host side that the gated delta rule's translation units share.
+#pragma once
+
+#include <type_traits>
+
+#include "vla_delta.cuh"
+
+namespace vla_layer {
+
+vla_status delta_backward_launch(DeltaArgs& p, vla_dtype dtype, int d, cudaStream_t s);
+
+template <typename G>
+inline bool good_gate(const G* g, int B, int H, int T, bool out) {
+    if (!g || !g->data || !aligned(g->data, 4)) return false;
+    const long long s[3] = {g->stride_b, g->stride_h, g->stride_t}, lim = 1LL << 40;
+    const int n[3] = {B, H, T};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && (s[i] < (out ? 1 : 0) || s[i] >= lim)) return false;
+    return true;
+}
+template <typename G>
+inline Gate to_gate(const G* g, int B, int H, int T) {
+    if (!g) return Gate{};
+    return Gate{const_cast<float*>(g->data), B > 1 ? g->stride_b : 0, H > 1 ? g->stride_h : 0, T > 1 ? g->stride_t : 0};
+}
+// a gate's memory: a dimension of stride 0 is the same values again
+template <typename G>
+inline Region gate_region(const G* g, int B, int H, int T) {
+    if (!g) return Region{};
+    auto len = [](int n, long long st) { return st == 0 ? 1 : n; };
+    const int b = len(B, g->stride_b), h = len(H, g->stride_h), t = len(T, g->stride_t);
+    return Region{reinterpret_cast<uintptr_t>(g->data), 4, {b > 1 ? g->stride_b * 4 : 0, h > 1 ? g->stride_h * 4 : 0, t > 1 ? g->stride_t * 4 : 0},
+                  {b, h, t}};
+}
+
+template <typename F>
+inline vla_status delta_pick(vla_dtype dtype, int d, F f) {
+    auto with = [&](auto tag) {
+        switch (d) {
+            case 32: return f(tag, std::integral_constant<int, 32>{});
+            case 64: return f(tag, std::integral_constant<int, 64>{});
+            case 96: return f(tag, std::integral_constant<int, 96>{});
+            default: return f(tag, std::integral_constant<int, 128>{});
+        }
+    };
+    return dtype == VLA_BF16 ? with(__nv_bfloat16{}) : with(float{});
+}
+
+// Rows of S of a block: all of a head's, or a half, a quarter, ... while the blocks are fewer than the SMs.
+inline int delta_rows(long long heads, int d) {
+    int rows = d;
+    while (rows % 32 == 0 && heads * (d / (rows / 2)) <= sm_count()) rows /= 2;
+    return rows;
+}
+
+// One of the recurrences: a warp per 16 rows and the helpers.
+template <auto K, int D, typename L>
+inline vla_status delta_run(DeltaArgs& p, cudaStream_t s) {
+    const long long heads = (long long)p.B * p.H;
+    p.rows = delta_rows(heads, D);
+    const long long grid = heads * (D / p.rows);
+    if (grid > 2147483647LL) return VLA_ERR_INVALID_ARG;
+    if (!allow_smem<K>(L::BYTES)) return VLA_ERR_CUDA;
+    K<<<(unsigned)grid, p.rows * 2 + HELPERS, L::BYTES, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
+}
+
+inline vla_status delta_copy_state(float* dst, const float* src, size_t n, cudaStream_t s) {
+    if (!dst || dst == src || n == 0) return VLA_OK;
+    const cudaError_t e = src ? cudaMemcpyAsync(dst, src, n * sizeof(float), cudaMemcpyDeviceToDevice, s)
+                              : cudaMemsetAsync(dst, 0, n * sizeof(float), s);
+    return e == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
+}
+
+// What a backward call keeps between its launches, laid out from `base` (p null: its bytes alone).
+inline size_t delta_scratch(DeltaArgs* p, void* base, vla_dtype dtype, int B, int H, int T, int d) {
+    const int span = dtype == VLA_BF16 ? BLOCK<__nv_bfloat16> : BLOCK<float>;
+    const int blocks = (T + span - 1) / span;
+    const size_t heads = (size_t)B * H, states = heads * (blocks + 1) * d * d, per_warp = heads * (d / 16) * T;
+    size_t at = 0;
+    auto take = [&](float** to, size_t n) {
+        if (p) *to = reinterpret_cast<float*>(static_cast<char*>(base) + at);
+        at += (n * sizeof(float) + 255) / 256 * 256;
+    };
+    DeltaArgs none;
+    DeltaArgs& a = p ? *p : none;
+    take(&a.E, heads * T * d);
+    take(&a.before, states);
+    take(&a.behind, states);
+    take(&a.od, per_warp);
+    take(&a.vd, per_warp);
+    take(&a.bd, per_warp);
+    take(&a.ends, heads * blocks * (d / 16));
+    a.blocks = blocks;
+    return at;
+}
+
+}  // namespace vla_layer
