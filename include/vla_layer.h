@@ -204,6 +204,42 @@ vla_status vla_delta_step(const void* q, const void* k, const void* v, vla_dtype
                           const float* log_decay, const float* beta, float scale, float* states, int N,
                           const int* slots, void* o, void* status, void* stream);
 
+/* ---- norm and position rotation of queries and keys ----------------------------
+ *
+ * For each row x (the d values of a q or k of one (b, h, t)):
+ *   z = x rstd weight[h],  rstd = 1 / sqrt(mean(x^2) + eps), or 1 / sqrt(sum(x^2) + eps)
+ * where unit is nonzero (rows of length 1 for a delta rule), and then, with m = rot / 2
+ * and the angles a_i = position freqs[i],
+ *   y_i = z_i cos a_i - z_(i+m) sin a_i,  y_(i+m) = z_(i+m) cos a_i + z_i sin a_i  (i < m),
+ * the coordinates from rot on as they are. rot is a multiple of 16, 0 (none) to d.
+ *
+ * weight_q, weight_k: float32, 16-byte aligned, [H, d], or [d] where shared is nonzero;
+ * NULL: 1. freqs: [rot / 2] float64 on the device, radians a position (not read where
+ * rot is 0). positions: int32 on the device, that of token t of sequence b at
+ * positions[b * positions_stride_b + t] (stride 0: the same for all), or NULL for t.
+ * Angles are exact to 2^-32 of a turn at any position. fp32 throughout; y rounded at
+ * the end. rstd_q, rstd_k: [B, H, T] float32, written (NULL: not) by the forward call and
+ * read by the backward call. yq may be the rows of q, and yk those of k. */
+vla_status vla_qk_norm(const vla_seq* q, const vla_seq* k, vla_dtype dtype, int B, int H, int T, int d,
+                       const float* weight_q, const float* weight_k, int shared, int unit, float eps,
+                       const double* freqs, int rot, const int* positions, long long positions_stride_b,
+                       const vla_seq_out* yq, const vla_seq_out* yk, float* rstd_q, float* rstd_k, void* stream);
+
+/* Bytes of scratch vla_qk_norm_backward() needs for the weights' gradients, on the
+ * current device. */
+size_t vla_qk_norm_scratch_bytes(int B, int H, int T, int d);
+
+/* Reverse mode: dq, dk of dtype from dyq, dyk and the forward call's q, k and rstd;
+ * dweight_q, dweight_k (float32, shaped as the weights; both or neither NULL) are sums
+ * over the rows in an order that depends on the sizes and the device alone. dq may be the
+ * rows of dyq or q, and dk those of dyk or k. */
+vla_status vla_qk_norm_backward(const vla_seq* dyq, const vla_seq* dyk, const vla_seq* q, const vla_seq* k,
+                                vla_dtype dtype, int B, int H, int T, int d, const float* weight_q,
+                                const float* weight_k, int shared, int unit, const double* freqs, int rot,
+                                const int* positions, long long positions_stride_b, const float* rstd_q,
+                                const float* rstd_k, const vla_seq_out* dq, const vla_seq_out* dk, float* dweight_q,
+                                float* dweight_k, void* scratch, size_t scratch_bytes, void* stream);
+
 /* ---- layer norm of each head's readout --------------------------------------
  *
  *   y = (x - mean) rstd weight[h] + bias[h] over the d values of a row,

@@ -16,7 +16,8 @@ path of a caller holding host buffers).
 Around it (``include/vla_layer.h``, CUDA tensors): linear attention with a
 decay per head (``vla_decay_forward``, ``vla_decay_backward``,
 ``vla_decay_step``), the gated delta rule (``vla_delta_forward``,
-``vla_delta_backward``, ``vla_delta_step``), the layer norm of each head's readout (``vla_head_norm``,
+``vla_delta_backward``, ``vla_delta_step``), the norm and position rotation of
+queries and keys (``vla_qk_norm``, ``vla_qk_norm_backward``), the layer norm of each head's readout (``vla_head_norm``,
 ``vla_head_norm_backward``) and a quantised cache of states
 (``vla_state_cache``, ``vla_state_store``, ``vla_state_load``).
 """
@@ -62,6 +63,11 @@ from ._layer import (  # noqa: F401
     vla_state_load,
     vla_state_store,
 )
+from ._qk import (  # noqa: F401
+    vla_qk_norm,
+    vla_qk_norm_backward,
+    vla_rotation_frequencies,
+)
 
 __all__ = [
     "vla_forward",
@@ -76,6 +82,9 @@ __all__ = [
     "vla_delta_forward",
     "vla_delta_backward",
     "vla_delta_step",
+    "vla_qk_norm",
+    "vla_qk_norm_backward",
+    "vla_rotation_frequencies",
     "vla_head_norm",
     "vla_head_norm_backward",
     "vla_state_cache",

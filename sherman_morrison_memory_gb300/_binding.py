@@ -76,6 +76,10 @@ def _layer_prototypes(lib):
             ("vla_delta_forward", [sq] * 3 + [ci] * 5 + [sq, sq, cf, vp, vp, sq, vp, vp, vp], ci),
             ("vla_delta_backward", [sq] * 4 + [ci] * 5 + [sq, sq, cf, vp, vp, vp] + [sq] * 5 + [vp, vp, cz, vp, vp], ci),
             ("vla_delta_step", [vp] * 3 + [ci] * 4 + [vp, vp, cf, vp, ci, vp, vp, vp, vp], ci),
+            ("vla_qk_norm", [sq, sq] + [ci] * 5 + [vp, vp, ci, ci, cf, vp, ci, vp, cl, sq, sq, vp, vp, vp], ci),
+            ("vla_qk_norm_scratch_bytes", [ci] * 4, cz),
+            ("vla_qk_norm_backward", [sq] * 4 + [ci] * 5 + [vp, vp, ci, ci, vp, ci, vp, cl, vp, vp, sq, sq, vp, vp, vp, cz,
+                                                            vp], ci),
             ("vla_head_norm", [sq] + [ci] * 5 + [vp, vp, ci, cf, sq, vp, vp, vp], ci),
             ("vla_head_norm_scratch_bytes", [ci] * 4, cz),
             ("vla_head_norm_backward", [sq] * 2 + [ci] * 5 + [vp, ci, vp, vp, sq, vp, vp, vp, cz, vp], ci),

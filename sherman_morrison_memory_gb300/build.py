@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libvla_gb300.so")
 SOURCES = [os.path.join(CSRC, n) for n in ("vla_forward.cu", "vla_host.cpp", "vla_probe.cu", "vla_layer.cu", "vla_delta.cu",
-                                           "vla_delta_backward.cu")]
+                                           "vla_delta_backward.cu", "vla_qk.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
