@@ -217,7 +217,7 @@ vla_status vla_delta_step(const void* q, const void* k, const void* v, vla_dtype
  * NULL: 1. freqs: [rot / 2] float64 on the device, radians a position (not read where
  * rot is 0). positions: int32 on the device, that of token t of sequence b at
  * positions[b * positions_stride_b + t] (stride 0: the same for all), or NULL for t.
- * Angles are exact to 2^-32 of a turn at any position. fp32 throughout; y rounded at
+ * Angles are as exact as products of float64 values at any position. fp32 throughout; y rounded at
  * the end. rstd_q, rstd_k: [B, H, T] float32, written (NULL: not) by the forward call and
  * read by the backward call. yq may be the rows of q, and yk those of k. */
 vla_status vla_qk_norm(const vla_seq* q, const vla_seq* k, vla_dtype dtype, int B, int H, int T, int d,
