@@ -23,7 +23,7 @@
 // bits and bf16 inputs are one part as they are, so states, E and gates' gradients
 // are fp32 results. Blocks of fewer rows than d use more SMs for few heads.
 // Four helper warps work a chunk ahead: loads, N, P and the inverse, of which the
-// two 16 x 16 blocks on the diagonal are solved a lane a column and joined.
+// two 16 x 16 blocks on the diagonal are solved a lane a column and joined by products.
 #pragma once
 
 #include "vla_mma.cuh"
@@ -88,22 +88,25 @@ struct DeltaLay {
 // gates of a chunk: exp(G), exp(G_C - G), b of each token, then exp(G_C)
 enum { GATE_NEAR = 0, GATE_FAR = DC, GATE_BETA = 2 * DC, GATE_WHOLE = 3 * DC };
 
-// Rows [t0, t0 + DC) of a sequence's `cols` columns to a tile; those from `n` on are zero.
-template <int LD, typename T>
+// Rows [t0, t0 + DC) of a sequence's `cols` columns to a tile, by THREADS threads; those from `n` on are zero.
+template <int LD, int THREADS, typename T>
 __device__ __forceinline__ void load_tile(char* tile, const Seq& s, int b, int h, long long t0, int col0, int cols, long long n,
                                           int tid) {
     constexpr int NP = PARTS<T>, PLANE = DC * LD * 2;
-    const int per = cols / 8;
-    for (int i = tid; i < DC * per; i += HELPERS) {
-        const int r = i / per, c = i % per * 8;
-        char* dst = tile + (r * LD + c) * 2;
-        const bool on = t0 + r < n;
-        const T* src = row_of<T>(s, b, h, on ? t0 + r : 0) + col0 + c;
+    const int per = cols / 8, wide = per <= 2 ? 1 : per <= 4 ? 2 : per <= 8 ? 3 : 4;  // threads of a row, a power of two
+    const int c = (tid & ((1 << wide) - 1)) * 8, first = tid >> wide, step = THREADS >> wide;
+    if (c >= cols) return;
+    const int live = (int)min((long long)DC, n - t0);
+    const T* src = row_of<T>(s, b, h, t0) + col0 + c;
+    char* dst = tile + (first * LD + c) * 2;
+#pragma unroll 4
+    for (int r = first; r < DC; r += step, dst += step * LD * 2) {
+        const T* at = r < live ? src + r * s.st : src;
         if constexpr (NP == 1) {
-            cp_async16(vla::smem_u32(dst), src, on ? 16 : 0);
+            cp_async16(vla::smem_u32(dst), at, r < live ? 16 : 0);
         } else {
             float x[8] = {};
-            if (on) load8(src, x);
+            if (r < live) load8(at, x);
             uint32_t w[4][NP];
 #pragma unroll
             for (int j = 0; j < 4; ++j) split<NP>(x[2 * j], x[2 * j + 1], w[j]);
@@ -133,139 +136,164 @@ struct Whole {
     }
 };
 
-// The helpers' part of a chunk: gates, P and the inverse. Warps 0 and 1 form the rows 0-15 and 16-31 of N, 2 and
-// 3 those of P; then warp 0 inverts. ROWS: 1 + diag(b) N, else 1 + N diag(b).
+// A operand (16 rows x 16 tokens) of N parts from two tiles of fragments.
+template <int N>
+__device__ __forceinline__ void to_operand(uint32_t (&a)[N][4], const float (&x0)[4], const float (&x1)[4]) {
+    uint32_t w[4][N];
+    split<N>(x0[0], x0[1], w[0]);
+    split<N>(x0[2], x0[3], w[1]);
+    split<N>(x1[0], x1[1], w[2]);
+    split<N>(x1[2], x1[3], w[3]);
+#pragma unroll
+    for (int p = 0; p < N; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[p][i] = w[i][p];
+}
+
+// The sums of g up to each lane's token, as two floats whose sum holds 48 bits: a difference of sums far from zero
+// keeps its precision.
+__device__ __forceinline__ void sums_of(float g, int lane, float& hi, float& lo) {
+    hi = g < -256.f ? -256.f : g;  // exp(-256) is 0
+    lo = 0.f;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float a = __shfl_up_sync(0xffffffffu, hi, m), al = __shfl_up_sync(0xffffffffu, lo, m);
+        if (lane >= m) {
+            const float s = a + hi, d = s - a;
+            lo += al + ((a - (s - d)) + (hi - d));
+            hi = s;
+        }
+    }
+}
+
+// The helpers' part of a chunk: gates, P and the inverse. Warps 0, 1, 2 have the 16 x 16 blocks (0, 0), (1, 0) and
+// (1, 1) of both triangles; 0 and 2 invert theirs of 1 + N, a lane a column, 1 joins them: (1 + N)^-1 has -T22 N21 T11
+// below. The inverse is kept transposed, [j][i]. ROWS: 1 + diag(b) N, else 1 + N diag(b).
 template <typename L, int D, int NP, int PP, bool ROWS>
 __device__ __forceinline__ void prepare_chunk(char* sm, const char* kt, const char* qt, char* prep, float g, float beta, float scale,
                                               Whole& whole, int hw, int lane) {
-    // the sum of g in 64 bits, as two floats: a difference of sums far from zero keeps its precision
-    double G = g < -256.f ? -256.0 : (double)g;  // exp(-256) is 0
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, G, m);
-        if (lane >= m) G += x;
-    }
-    const float Gh = (float)G, Gl = (float)(G - (double)Gh);
-    const double all = __shfl_sync(0xffffffffu, G, 31);
-    if (hw == 0) {
+    float Gh, Gl;
+    sums_of(g, lane, Gh, Gl);
+    if (hw == 1) {
+        const float all = __shfl_sync(0xffffffffu, Gh, 31), rest = __shfl_sync(0xffffffffu, Gl, 31);
         float* gates = reinterpret_cast<float*>(prep + L::GATES);
-        gates[GATE_NEAR + lane] = expf(Gh);
-        gates[GATE_FAR + lane] = expf((float)(all - G));
+        gates[GATE_NEAR + lane] = expf(Gh + Gl);
+        gates[GATE_FAR + lane] = expf((all - Gh) + (rest - Gl));
         gates[GATE_BETA + lane] = beta;
-        const float w = whole.next((float)all);
+        const float w = whole.next(all + rest);
         if (lane == 0) gates[GATE_WHOLE] = w;
     }
-    const int mt = hw & 1;
-    const bool of_q = hw >= 2;
-    float c[4][4] = {}, cl[4][4] = {};
-    const uint32_t a_at = vla::smem_u32(of_q ? qt : kt) + (mt * 16 * L::LD + down_across<L::LD>(lane)) * 2;
-    const uint32_t b_at = vla::smem_u32(kt) + across_down<L::LD>(lane) * 2;
-#pragma unroll 2
+    const int mt = hw ? 1 : 0, np = hw == 2 ? 1 : 0;
+    float c[4][4] = {}, cl[4][4] = {};  // K K^T, Q K^T
+    const uint32_t k_at = vla::smem_u32(kt) + (mt * 16 * L::LD + down_across<L::LD>(lane)) * 2;
+    const uint32_t q_at = vla::smem_u32(qt) + (mt * 16 * L::LD + down_across<L::LD>(lane)) * 2;
+    const uint32_t b_at = vla::smem_u32(kt) + (np * 16 * L::LD + across_down<L::LD>(lane)) * 2;
+#pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t a[NP][4];
+        uint32_t a[NP][4], q[NP][4], bb[2][NP][2];
 #pragma unroll
-        for (int p = 0; p < NP; ++p) ldsm(a[p], a_at + p * L::PLANE + ks * 32);
-#pragma unroll
-        for (int np = 0; np < 2; ++np) {
-            if (np > mt) break;
-            uint32_t bb[NP][4];
-#pragma unroll
-            for (int p = 0; p < NP; ++p) ldsm(bb[p], b_at + p * L::PLANE + np * 16 * L::LD * 2 + ks * 32);
-            mma_parts<NP>(c[2 * np], cl[2 * np], a, bb, 0);
-            mma_parts<NP>(c[2 * np + 1], cl[2 * np + 1], a, bb, 1);
+        for (int p = 0; p < NP; ++p) {
+            ldsm(a[p], k_at + p * L::PLANE + ks * 32);
+            ldsm(q[p], q_at + p * L::PLANE + ks * 32);
+            ldsm_pair(bb, 0, p, b_at + p * L::PLANE + ks * 32);
         }
+        mma_tiles<NP>(c, cl, a, bb);
+        mma_tiles<NP>(c + 2, cl + 2, q, bb);
     }
     if constexpr (NP > 1) join(c, cl);
     const int r = lane >> 2, t2 = (lane & 3) * 2;
-    float* N = reinterpret_cast<float*>(sm + L::N);
+    float* N = reinterpret_cast<float*>(sm + L::N) + (hw >> 1) * 16 * NLD;
+    float x[2][4];  // the block's N
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-        const int i = mt * 16 + hf * 8 + r;
-        const float gi = __shfl_sync(0xffffffffu, Gh, i), li = __shfl_sync(0xffffffffu, Gl, i), bi = __shfl_sync(0xffffffffu, beta, i);
+    for (int n = 0; n < 2; ++n) {
+        const int j = np * 16 + n * 8 + t2;
+        float gj[2], lj[2], bj[2];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            float x[2];
+        for (int e = 0; e < 2; ++e) {
+            gj[e] = __shfl_sync(0xffffffffu, Gh, j + e), lj[e] = __shfl_sync(0xffffffffu, Gl, j + e);
+            bj[e] = __shfl_sync(0xffffffffu, beta, j + e);
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int i = mt * 16 + hf * 8 + r;
+            const float gi = __shfl_sync(0xffffffffu, Gh, i), li = __shfl_sync(0xffffffffu, Gl, i), bi = __shfl_sync(0xffffffffu, beta, i);
+            float y[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int j = n * 8 + t2 + e;
-                const float gj = __shfl_sync(0xffffffffu, Gh, j), lj = __shfl_sync(0xffffffffu, Gl, j),
-                            bj = __shfl_sync(0xffffffffu, beta, j);
-                const float w = expf((gi - gj) + (li - lj)) * (of_q ? scale : ROWS ? bi : bj);
-                x[e] = (of_q ? j <= i : j < i) ? c[n][2 * hf + e] * w : 0.f;
+                const float w = expf((gi - gj[e]) + (li - lj[e]));
+                x[n][2 * hf + e] = j + e < i ? c[n][2 * hf + e] * w * (ROWS ? bi : bj[e]) : 0.f;
+                y[e] = j + e <= i ? c[2 + n][2 * hf + e] * w * scale : 0.f;
             }
-            if (n >= 2 * (mt + 1)) continue;
-            if (of_q) {
-                uint32_t w[PP];
-                split<PP>(x[0], x[1], w);
+            uint32_t w[PP];
+            split<PP>(y[0], y[1], w);
 #pragma unroll
-                for (int p = 0; p < PP; ++p)
-                    *reinterpret_cast<uint32_t*>(prep + L::P + p * L::PAIR + (i * PLD + n * 8 + t2) * 2) = w[p];
-            } else {
-                *reinterpret_cast<float2*>(N + i * NLD + n * 8 + t2) = make_float2(x[0], x[1]);
+            for (int p = 0; p < PP; ++p) *reinterpret_cast<uint32_t*>(prep + L::P + p * L::PAIR + (i * PLD + j) * 2) = w[p];
+            if (hw != 1) *reinterpret_cast<float2*>(N + (hf * 8 + r) * NLD + n * 8 + t2) = make_float2(x[n][2 * hf], x[n][2 * hf + 1]);
+        }
+    }
+    if (hw != 1) {
+        __syncwarp();
+        float t[16];
+        const int col = lane & 15;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == col ? 1.f : 0.f, s2 = 0.f;
+#pragma unroll
+            for (int m = 0; m < i; m += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(N + i * NLD + m);
+                s = fmaf(-w.x, t[m], s);
+                if (m + 1 < i) s2 = fmaf(-w.y, t[m + 1], s2);
+                if (m + 2 < i) s = fmaf(-w.z, t[m + 2], s);
+                if (m + 3 < i) s2 = fmaf(-w.w, t[m + 3], s2);
+            }
+            t[i] = s + s2;
+        }
+        if (lane < 16) {
+            uint32_t w[8][INV_PARTS];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) split<INV_PARTS>(t[2 * i], t[2 * i + 1], w[i]);
+#pragma unroll
+            for (int p = 0; p < INV_PARTS; ++p) {
+                uint4* to = reinterpret_cast<uint4*>(prep + L::INV + p * L::PAIR + ((mt * 16 + col) * PLD + mt * 16) * 2);
+                to[0] = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+                to[1] = make_uint4(w[4][p], w[5][p], w[6][p], w[7][p]);
             }
         }
     }
-    vla::named_bar(1, HELPERS);
-    if (hw != 0) return;
-    // the inverses of both blocks on the diagonal: lane (h, c) has column c of block h
-    const int h = lane >> 4, col = lane & 15;
-    float x[16];
-    const float* Nd = N + h * (16 * NLD + 16);
+    vla::named_bar(2, 96);
+    if (hw != 1) return;
+    // T21^T = -(T11^T N21^T) T22^T
+    uint32_t a[INV_PARTS][4], w[2][INV_PARTS][2];
+    const uint32_t inv = vla::smem_u32(prep + L::INV);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float s = i == col ? 1.f : 0.f, s2 = 0.f;
+    for (int p = 0; p < INV_PARTS; ++p) ldsm(a[p], inv + p * L::PAIR + down_across<PLD>(lane) * 2);
 #pragma unroll
-        for (int m = 0; m < i; m += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(Nd + i * NLD + m);
-            s = fmaf(-w.x, x[m], s);
-            if (m + 1 < i) s2 = fmaf(-w.y, x[m + 1], s2);
-            if (m + 2 < i) s = fmaf(-w.z, x[m + 2], s);
-            if (m + 3 < i) s2 = fmaf(-w.w, x[m + 3], s2);
+    for (int n = 0; n < 2; ++n)  // eight rows of N21, their 16 values down
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t y[INV_PARTS];
+            split<INV_PARTS>(x[k][2 * n], x[k][2 * n + 1], y);
+#pragma unroll
+            for (int p = 0; p < INV_PARTS; ++p) w[n][p][k] = y[p];
         }
-        x[i] = s + s2;
-    }
-    // the block below: -T22 (N21 T11), a lane's rows 8 h .. 8 h + 7 of its column
-    float y[8] = {};
+    float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {}, zl[2][4] = {};
+    mma_tiles<INV_PARTS>(y, yl, a, w);
+    join(y, yl);
+    to_operand<INV_PARTS>(a, y[0], y[1]);
 #pragma unroll
-    for (int m = 0; m < 16; m += 4) {
-        float t[4];
+    for (int p = 0; p < INV_PARTS; ++p) ldsm_pair_t(w, 0, p, inv + p * L::PAIR + (16 * PLD + 16 + down_across<PLD>(lane)) * 2);
+    mma_tiles<INV_PARTS>(z, zl, a, w);
+    join(z, zl);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = __shfl_sync(0xffffffffu, x[m + e], col);
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float4 w = *reinterpret_cast<const float4*>(N + (16 + 8 * h + i) * NLD + m);
-            y[i] = fmaf(w.x, t[0], fmaf(w.y, t[1], fmaf(w.z, t[2], fmaf(w.w, t[3], y[i]))));
+        for (int hf = 0; hf < 2; ++hf) {
+            uint32_t v[INV_PARTS];
+            split<INV_PARTS>(-z[n][2 * hf], -z[n][2 * hf + 1], v);
+#pragma unroll
+            for (int p = 0; p < INV_PARTS; ++p)
+                *reinterpret_cast<uint32_t*>(prep + L::INV + p * L::PAIR + ((hf * 8 + r) * PLD + 16 + n * 8 + t2) * 2) = v[p];
         }
-    }
-    __syncwarp();
-    if (h == 1) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) N[(16 + i) * NLD + 16 + col] = x[i];
-    }
-    __syncwarp();
-    float z[8] = {};
-#pragma unroll
-    for (int m = 0; m < 16; m += 4) {
-        float t[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = __shfl_sync(0xffffffffu, y[(m + e) & 7], ((m + e) >> 3) * 16 + col);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float4 w = *reinterpret_cast<const float4*>(N + (16 + 8 * h + i) * NLD + 16 + m);
-            z[i] = fmaf(-w.x, t[0], fmaf(-w.y, t[1], fmaf(-w.z, t[2], fmaf(-w.w, t[3], z[i]))));
-        }
-    }
-    auto put = [&](int i, int j, float v) {
-        uint32_t w[INV_PARTS];
-        split<INV_PARTS>(v, 0.f, w);
-#pragma unroll
-        for (int p = 0; p < INV_PARTS; ++p)
-            *reinterpret_cast<uint16_t*>(prep + L::INV + p * L::PAIR + (i * PLD + j) * 2) = (uint16_t)w[p];
-    };
-#pragma unroll
-    for (int i = 0; i < 16; ++i) put(16 * h + i, 16 * h + col, x[i]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) put(16 + 8 * h + i, col, z[i]);
 }
 
 // Fragments (16 rows of S, eight columns a tile) from and to [d][d] float32 rows.
@@ -289,20 +317,6 @@ __device__ __forceinline__ void store_rows(const float (&s)[D / 8][4], float* m,
     }
 }
 
-// A operand (16 rows x 16 tokens) of N parts from two tiles of fragments.
-template <int N>
-__device__ __forceinline__ void to_operand(uint32_t (&a)[N][4], const float (&x0)[4], const float (&x1)[4]) {
-    uint32_t w[4][N];
-    split<N>(x0[0], x0[1], w[0]);
-    split<N>(x0[2], x0[3], w[1]);
-    split<N>(x1[0], x1[1], w[2]);
-    split<N>(x1[2], x1[3], w[3]);
-#pragma unroll
-    for (int p = 0; p < N; ++p)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[p][i] = w[i][p];
-}
-
 // X^T (16 rows x 32 tokens) = S A^T of a tile's 32 rows A, and of the first SP parts of S and a second tile Y^T =
 // S A2^T (SP 0: none). `at`: the tiles with across_down.
 template <int D, int LD, int NP, int SP, int PLANE>
@@ -314,42 +328,48 @@ __device__ __forceinline__ void times_rows(float (&x)[4][4], float (&y)[4][4], c
         for (int e = 0; e < 4; ++e) x[i][e] = 0.f, y[i][e] = SP ? 0.f : y[i][e];
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t a[3][4];
+        uint32_t a[3][4], b[4][NP][2];
         to_operand<3>(a, s[2 * ks], s[2 * ks + 1]);
 #pragma unroll
-        for (int np = 0; np < 2; ++np) {
-            uint32_t b[NP][4];
+        for (int np = 0; np < 2; ++np)
 #pragma unroll
-            for (int p = 0; p < NP; ++p) ldsm(b[p], at + p * PLANE + (np * 16 * LD + ks * 16) * 2);
-            mma_parts<3>(x[2 * np], xl[2 * np], a, b, 0);
-            mma_parts<3>(x[2 * np + 1], xl[2 * np + 1], a, b, 1);
-            if constexpr (SP > 0) {
+            for (int p = 0; p < NP; ++p) ldsm_pair(b, 2 * np, p, at + p * PLANE + (np * 16 * LD + ks * 16) * 2);
+        mma_tiles<3>(x, xl, a, b);
+        if constexpr (SP > 0) {
 #pragma unroll
-                for (int p = 0; p < NP; ++p) ldsm(b[p], at2 + p * PLANE + (np * 16 * LD + ks * 16) * 2);
-                mma_parts<SP>(y[2 * np], a, b, 0);
-                mma_parts<SP>(y[2 * np + 1], a, b, 1);
-            }
+            for (int np = 0; np < 2; ++np)
+#pragma unroll
+                for (int p = 0; p < NP; ++p) ldsm_pair(b, 2 * np, p, at2 + p * PLANE + (np * 16 * LD + ks * 16) * 2);
+            mma_tiles<SP>(y, y, a, b);
         }
     }
     join(x, xl);
 }
 
-// X^T (16 rows x 32 tokens) += U^T W^T (`across`: W's rows, j <= i) or U^T W (else: W's columns), of a lower triangle
-// W of WP parts at `at` with across_down, or down_across and ldsm_t.
-template <int WP, int UP, int PAIR, bool ACROSS>
+// X^T (16 rows x 32 tokens) += U^T W over 16 of W's 32 rows (`ks`), W upper triangular (AFTER: columns from its row on)
+// or lower, in WP parts: from W's rows (TRANS: `at` with down_across) or W^T's (with across_down).
+template <int WP, int UP, int PAIR, bool AFTER, bool TRANS>
 __device__ __forceinline__ void times_triangle(float (&x)[4][4], float (&xl)[4][4], const uint32_t (&a)[UP][4], int ks, uint32_t at) {
+    uint32_t w[4][WP][2];
+    const int first = AFTER ? ks : 0, last = AFTER ? 1 : ks;
 #pragma unroll
-    for (int np = ACROSS ? ks : 0; np < (ACROSS ? 2 : ks + 1); ++np) {
-        uint32_t w[WP][4];
+    for (int np = first; np <= last; ++np)
 #pragma unroll
         for (int q = 0; q < WP; ++q) {
-            if constexpr (ACROSS)
-                ldsm(w[q], at + q * PAIR + (np * 16 * PLD + ks * 16) * 2);
+            if constexpr (TRANS)
+                ldsm_pair_t(w, 2 * np, q, at + q * PAIR + (ks * 16 * PLD + np * 16) * 2);
             else
-                ldsm_t(w[q], at + q * PAIR + (ks * 16 * PLD + np * 16) * 2);
+                ldsm_pair(w, 2 * np, q, at + q * PAIR + (np * 16 * PLD + ks * 16) * 2);
         }
-        mma_parts<UP>(x[2 * np], xl[2 * np], a, w, 0);
-        mma_parts<UP>(x[2 * np + 1], xl[2 * np + 1], a, w, 1);
+    if (first == last) {
+        uint32_t one[2][WP][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int q = 0; q < WP; ++q) one[n][q][0] = w[2 * first + n][q][0], one[n][q][1] = w[2 * first + n][q][1];
+        mma_tiles<UP>(x + 2 * first, xl + 2 * first, a, one);
+    } else {
+        mma_tiles<UP>(x, xl, a, w);
     }
 }
 
@@ -381,20 +401,21 @@ __device__ __forceinline__ void add_outer(float (&s)[D / 8][4], float whole, con
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) to_operand<3>(a[ks], u[2 * ks], u[2 * ks + 1]);
 #pragma unroll
-    for (int np = 0; np < D / 16; ++np) {
-        float t[2][4] = {}, low[2][4] = {};
+    for (int n4 = 0; n4 < D / 32; ++n4) {
+        float t[4][4] = {}, low[4][4] = {};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            uint32_t b[NP][4];
+            uint32_t b[4][NP][2];
 #pragma unroll
-            for (int p = 0; p < NP; ++p) ldsm_t(b[p], at + p * PLANE + ks * 16 * LD * 2 + np * 32);
-            mma_parts<3>(t[0], low[0], a[ks], b, 0);
-            mma_parts<3>(t[1], low[1], a[ks], b, 1);
+            for (int np = 0; np < 2; ++np)
+#pragma unroll
+                for (int p = 0; p < NP; ++p) ldsm_pair_t(b, 2 * np, p, at + p * PLANE + ks * 16 * LD * 2 + (2 * n4 + np) * 32);
+            mma_tiles<3>(t, low, a[ks], b);
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[2 * np + k][e] = fmaf(whole, s[2 * np + k][e], t[k][e] + low[k][e]);
+            for (int e = 0; e < 4; ++e) s[4 * n4 + k][e] = fmaf(whole, s[4 * n4 + k][e], t[k][e] + low[k][e]);
     }
 }
 

@@ -42,14 +42,15 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_reverse_kernel(cons
 
     if (warp >= workers) {
         const int tid = threadIdx.x - workers * 32, hw = warp - workers;
+        // bf16: the last helper warp loads; fp32: all, as values are cut into parts on the way
+        constexpr int LOADERS = NP == 1 ? 32 : HELPERS;
         auto load = [&](int m) {
-            if (m < chunks) {
-                const long long t0 = (long long)(chunks - 1 - m) * DC;
-                load_tile<LD, T>(tile(m, 0), p.k, b, h, t0, 0, D, n, tid);
-                load_tile<LD, T>(tile(m, 1), p.q, b, h, t0, 0, D, n, tid);
-                load_tile<LD, T>(tile(m, 2), p.dO, b, h, t0, row0, p.rows, n, tid);
-                if constexpr (F::TILES == 4) load_tile<LD, T>(tile(m, 3), p.v, b, h, t0, row0, p.rows, n, tid);
-            }
+            const int at = tid & (LOADERS - 1);
+            const long long t0 = (long long)(chunks - 1 - m) * DC;
+            load_tile<LD, LOADERS, T>(tile(m, 0), p.k, b, h, t0, 0, D, n, at);
+            load_tile<LD, LOADERS, T>(tile(m, 1), p.q, b, h, t0, 0, D, n, at);
+            load_tile<LD, LOADERS, T>(tile(m, 2), p.dO, b, h, t0, row0, p.rows, n, at);
+            if constexpr (F::TILES == 4) load_tile<LD, LOADERS, T>(tile(m, 3), p.v, b, h, t0, row0, p.rows, n, at);
             cp_async_commit();
         };
         Whole whole;
@@ -60,17 +61,26 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_reverse_kernel(cons
             g = on && p.g.p ? *p.g.at(b, h, t) : 0.f;
             beta = on ? *p.beta.at(b, h, t) : 0.f;
         };
-        load(0);
         gates(0);
+        if (NP == 1 && hw == 3 && chunks) load(0);
+        if constexpr (NP == 1) {
+            cp_async_wait<0>();
+            vla::named_bar(1, HELPERS);
+        }
         for (int m = 0; m <= chunks; ++m) {  // chunk m is prepared while chunk m - 1 is computed
             if (m < chunks) {
-                if (NP > 1 && m) load(m);
-                cp_async_wait<0>();
-                vla::named_bar(1, HELPERS);
-                if (NP == 1) load(m + 1);
-                const float gm = g, bm = beta;
-                gates(m + 1);
-                prepare_chunk<L, D, NP, 3, true>(sm, tile(m, 0), tile(m, 1), prep(m), gm, bm, p.scale, whole, hw, lane);
+                if constexpr (NP > 1) {
+                    load(m);
+                    vla::named_bar(1, HELPERS);
+                }
+                if (hw < 3) {
+                    const float gm = g, bm = beta;
+                    gates(m + 1);
+                    prepare_chunk<L, D, NP, 3, true>(sm, tile(m, 0), tile(m, 1), prep(m), gm, bm, p.scale, whole, hw, lane);
+                } else if (NP == 1 && m + 1 < chunks) {
+                    load(m + 1);
+                    cp_async_wait<0>();
+                }
             }
             __syncthreads();
         }
@@ -130,7 +140,7 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_reverse_kernel(cons
                 uint32_t a[NP][4];
 #pragma unroll
                 for (int q = 0; q < NP; ++q) ldsm_t(a[q], ot + q * L::PLANE + ks * 16 * LD * 2);
-                times_triangle<3, NP, L::PAIR, false>(x, low, a, ks, vla::smem_u32(pr + L::P) + down_across<PLD>(lane) * 2);
+                times_triangle<3, NP, L::PAIR, false, true>(x, low, a, ks, vla::smem_u32(pr + L::P) + down_across<PLD>(lane) * 2);
             }
             join(x, low);
         }
@@ -141,7 +151,7 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_reverse_kernel(cons
             for (int ks = 0; ks < 2; ++ks) {
                 uint32_t a[3][4];
                 to_operand<3>(a, x[2 * ks], x[2 * ks + 1]);
-                times_triangle<INV_PARTS, 3, L::PAIR, false>(u, low, a, ks, vla::smem_u32(pr + L::INV) + down_across<PLD>(lane) * 2);
+                times_triangle<INV_PARTS, 3, L::PAIR, false, false>(u, low, a, ks, vla::smem_u32(pr + L::INV) + across_down<PLD>(lane) * 2);
             }
             join(u, low);
         }

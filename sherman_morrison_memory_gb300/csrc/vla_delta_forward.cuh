@@ -31,14 +31,15 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_forward_kernel(cons
 
     if (warp >= workers) {
         const int tid = threadIdx.x - workers * 32, hw = warp - workers;
+        // bf16: the last helper warp loads; fp32: all, as values are cut into parts on the way
+        constexpr int LOADERS = NP == 1 ? 32 : HELPERS;
         auto load = [&](int c) {
-            if (c < chunks) {
-                const long long t0 = (long long)c * DC;
-                load_tile<LD, T>(tile(c, 0), p.k, b, h, t0, 0, D, n, tid);
-                load_tile<LD, T>(tile(c, 1), p.q, b, h, t0, 0, D, n, tid);
-                load_tile<LD, T>(tile(c, 2), p.v, b, h, t0, row0, p.rows, n, tid);
-                if constexpr (F::TILES == 4) load_tile<LD, T>(tile(c, 3), p.dO, b, h, t0, row0, p.rows, n, tid);
-            }
+            const int at = tid & (LOADERS - 1);
+            const long long t0 = (long long)c * DC;
+            load_tile<LD, LOADERS, T>(tile(c, 0), p.k, b, h, t0, 0, D, n, at);
+            load_tile<LD, LOADERS, T>(tile(c, 1), p.q, b, h, t0, 0, D, n, at);
+            load_tile<LD, LOADERS, T>(tile(c, 2), p.v, b, h, t0, row0, p.rows, n, at);
+            if constexpr (F::TILES == 4) load_tile<LD, LOADERS, T>(tile(c, 3), p.dO, b, h, t0, row0, p.rows, n, at);
             cp_async_commit();
         };
         Whole whole;
@@ -48,17 +49,26 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_forward_kernel(cons
             g = t < n && p.g.p ? *p.g.at(b, h, t) : 0.f;
             beta = t < n ? *p.beta.at(b, h, t) : 0.f;
         };
-        load(0);
         gates(0);
+        if (NP == 1 && hw == 3 && chunks) load(0);
+        if constexpr (NP == 1) {
+            cp_async_wait<0>();
+            vla::named_bar(1, HELPERS);
+        }
         for (int c = 0; c <= chunks; ++c) {  // chunk c is prepared while chunk c - 1 is computed
             if (c < chunks) {
-                if (NP > 1 && c) load(c);  // fp32: cut into parts on the way, nothing under way behind
-                cp_async_wait<0>();
-                vla::named_bar(1, HELPERS);
-                if (NP == 1) load(c + 1);
-                const float gc = g, bc = beta;
-                gates(c + 1);
-                prepare_chunk<L, D, NP, PP, false>(sm, tile(c, 0), tile(c, 1), prep(c), gc, bc, p.scale, whole, hw, lane);
+                if constexpr (NP > 1) {
+                    load(c);
+                    vla::named_bar(1, HELPERS);
+                }
+                if (hw < 3) {
+                    const float gc = g, bc = beta;
+                    gates(c + 1);
+                    prepare_chunk<L, D, NP, PP, false>(sm, tile(c, 0), tile(c, 1), prep(c), gc, bc, p.scale, whole, hw, lane);
+                } else if (NP == 1 && c + 1 < chunks) {
+                    load(c + 1);
+                    cp_async_wait<0>();
+                }
             }
             __syncthreads();
         }
@@ -111,7 +121,7 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_forward_kernel(cons
         for (int ks = 0; ks < 2; ++ks) {
             uint32_t a[3][4];
             to_operand<3>(a, x[2 * ks], x[2 * ks + 1]);
-            times_triangle<INV_PARTS, 3, L::PAIR, true>(u, low, a, ks, vla::smem_u32(pr + L::INV) + across_down<PLD>(lane) * 2);
+            times_triangle<INV_PARTS, 3, L::PAIR, true, true>(u, low, a, ks, vla::smem_u32(pr + L::INV) + down_across<PLD>(lane) * 2);
         }
         join(u, low);
         if constexpr (TAPE) {
@@ -138,7 +148,7 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_forward_kernel(cons
             for (int ks = 0; ks < 2; ++ks) {
                 uint32_t a[F::UP][4];
                 to_operand<F::UP>(a, u[2 * ks], u[2 * ks + 1]);
-                times_triangle<PP, F::UP, L::PAIR, true>(o, F::FULL ? ol : o, a, ks, vla::smem_u32(pr + L::P) + across_down<PLD>(lane) * 2);
+                times_triangle<PP, F::UP, L::PAIR, true, false>(o, F::FULL ? ol : o, a, ks, vla::smem_u32(pr + L::P) + across_down<PLD>(lane) * 2);
             }
             if constexpr (F::FULL) join(o, ol);
         }

@@ -57,10 +57,38 @@ __device__ __forceinline__ int across_down(int lane) {
     return ((lane & 7) + ((lane >> 4) << 3)) * LD + ((lane >> 3) & 1) * 8;
 }
 
-// c + low += A B over the first NA parts of A and the parts of B: the products whose size is at least that of the
-// last part kept of either. The tensor cores cut the sum off at every addition, always towards zero, so the many
-// small products have a sum of their own and only those of the first parts are added at full size (fp32 results
-// were up to 4e-6 off with one sum, where a head's products add up 48 times).
+// c + low += A B for N tiles of eight columns: over the first NA parts of A and the parts of B, the products whose size
+// is at least that of the last part kept of either. b[n][part]: a tile's operand. The tensor cores cut the sum off at
+// every addition, always towards zero, so the many small products have a sum of their own and only those of the first
+// parts are added at full size (fp32 results were up to 4e-6 off with one sum, where a head's products add up 48 times).
+// The tiles come innermost: a product waits for the one before it on the same sum, 21 cycles at 8 a product.
+template <int NA, int NT, int M, int NB>
+__device__ __forceinline__ void mma_tiles(float (*c)[4], float (*low)[4], const uint32_t (&a)[M][4], const uint32_t (&b)[NT][NB][2]) {
+    constexpr int MOST = (NA > NB ? NA : NB) - 1;
+#pragma unroll
+    for (int sum = 0; sum <= MOST; ++sum)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int i = sum - j;
+            if (i < 0 || i >= NA) continue;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma(sum ? low[n] : c[n], a[i], b[n][j][0], b[n][j][1]);
+        }
+}
+// The operands of two tiles from a 16 x 16 block.
+template <int NT, int NB>
+__device__ __forceinline__ void ldsm_pair(uint32_t (&b)[NT][NB][2], int n, int part, uint32_t at) {
+    uint32_t r[4];
+    ldsm(r, at);
+    b[n][part][0] = r[0], b[n][part][1] = r[1], b[n + 1][part][0] = r[2], b[n + 1][part][1] = r[3];
+}
+template <int NT, int NB>
+__device__ __forceinline__ void ldsm_pair_t(uint32_t (&b)[NT][NB][2], int n, int part, uint32_t at) {
+    uint32_t r[4];
+    ldsm_t(r, at);
+    b[n][part][0] = r[0], b[n][part][1] = r[1], b[n + 1][part][0] = r[2], b[n + 1][part][1] = r[3];
+}
+// One tile, its operand a half of what ldsm gives.
 template <int NA, int M, int NB>
 __device__ __forceinline__ void mma_parts(float (&c)[4], float (&low)[4], const uint32_t (&a)[M][4], const uint32_t (&b)[NB][4],
                                           int half) {
@@ -70,11 +98,6 @@ __device__ __forceinline__ void mma_parts(float (&c)[4], float (&low)[4], const 
 #pragma unroll
         for (int j = 0; j < NB; ++j)
             if (i + j <= MOST) mma(i + j ? low : c, a[i], b[j][2 * half], b[j][2 * half + 1]);
-}
-// The same with one sum, for results that are rounded to bf16.
-template <int NA, int M, int NB>
-__device__ __forceinline__ void mma_parts(float (&c)[4], const uint32_t (&a)[M][4], const uint32_t (&b)[NB][4], int half) {
-    mma_parts<NA>(c, c, a, b, half);
 }
 template <int N>
 __device__ __forceinline__ void join(float (&c)[N][4], const float (&low)[N][4]) {
