@@ -16,12 +16,14 @@
 //   U'  = (1 + diag(b) N)^-T (P^T dO + diag(exp(G_C - G)) K R^T),   dV = diag(b) U',   db_i = U'_i . E_i
 //   R  <- exp(G_C) R + (scale diag(exp(G)) dO)^T Q - (diag(exp(G)) dV)^T K
 //
-// The rows of S and R (coordinates of v) need nothing of each other. So a warp
-// keeps 16 of them in registers, as sums of warp-level products whose fragments
-// are, cut into bf16 parts, the next product's operands: S to K S^T to E to S
-// without shared memory or a barrier between. Three parts hold an fp32 value's 24
-// bits and bf16 inputs are one part as they are, so states, E and gates' gradients
-// are fp32 results. Blocks of fewer rows than d use more SMs for few heads.
+// The rows of S and R (coordinates of v) need nothing of each other. So a pair of
+// warps keeps 16 of them in registers, a half of the columns each, as sums of
+// warp-level products whose fragments are, cut into bf16 parts, the next product's
+// operands: S to K S^T to E to S. Only K S^T, a sum over the columns, goes through
+// shared memory between the two; what follows from it for all tokens both form (E),
+// and a half of the tokens each what is written (O, dV). Three parts hold an fp32
+// value's 24 bits and bf16 inputs are one part as they are, so states, E and gates'
+// gradients are fp32 results. Blocks of fewer rows use more SMs for few heads.
 // Four helper warps work a chunk ahead: loads, N, P and the inverse, of which the
 // two 16 x 16 blocks on the diagonal are solved a lane a column and joined by products.
 #pragma once
@@ -58,7 +60,7 @@ struct DeltaArgs {
     float* E;               // [BH][T][d]
     float *before, *behind; // [BH][blocks + 1][d][d]: S before a block of tokens (the last one behind all), R behind it
     float *od, *vd, *bd;    // [BH][d / 16][T]: o . dO, v . dV and U' . E of 16 rows
-    float* ends;            // [BH][blocks][d / 16]: <R, S> behind a block, of 16 rows
+    float* ends;            // [BH][blocks][d / 8]: <R, S> behind a block, of 16 rows and half of the columns
     int blocks;             // blocks of tokens of a sequence of T
 };
 
@@ -72,7 +74,13 @@ constexpr int PARTS = sizeof(T) == 2 ? 1 : 3;
 template <typename T>
 constexpr int BLOCK = sizeof(T) == 2 ? 64 : 32;
 
-// Shared memory of a block: stages of input tiles, and two chunks' pairs and gates.
+// rows of S of a block at most: two warps for 16, with the helpers' 16 warps or 12
+template <int D>
+constexpr int MOST_ROWS = D == 128 ? 64 : D;
+template <int D>
+constexpr int DELTA_THREADS = MOST_ROWS<D> * 4 + HELPERS;
+
+// Shared memory of a block: stages of input tiles, two chunks' pairs and gates, and what pairs of warps exchange.
 template <int D, typename T, int TILES, int PP>
 struct DeltaLay {
     static constexpr int NP = PARTS<T>;
@@ -81,9 +89,13 @@ struct DeltaLay {
     static constexpr int STAGES = NP == 1 ? 3 : 2;
     static constexpr int PAIR = DC * PLD * 2;              // bytes of a part of P or of the inverse
     static constexpr int INV = 0, P = INV_PARTS * PAIR, GATES = P + PP * PAIR, PREP = GATES + 5 * DC * 4;
-    static constexpr int IN = 0, PREPS = STAGES * TILES * TILE, N = PREPS + 2 * PREP, OUT = N + DC * NLD * 4;
+    static constexpr int IN = 0, PREPS = STAGES * TILES * TILE, N = PREPS + 2 * PREP, SWAP = N + DC * NLD * 4;
+    static constexpr int WARPS = MOST_ROWS<D> / 8;
+    static constexpr int SWAPS = 24 * 32 * 4;              // of a warp: 16 values of K S^T a lane and 8 of o
+    static constexpr int OUT = SWAP + WARPS * SWAPS;
     static constexpr int OUT_LD = 24;                      // elements of a row of a warp's staged outputs
-    static constexpr int BYTES = OUT + (D / 16) * DC * OUT_LD * 2;
+    static constexpr int OUTS = NP == 1 ? 16 * OUT_LD * 2 : 0;
+    static constexpr int BYTES = OUT + WARPS * OUTS;
 };
 // gates of a chunk: exp(G), exp(G_C - G), b of each token, then exp(G_C)
 enum { GATE_NEAR = 0, GATE_FAR = DC, GATE_BETA = 2 * DC, GATE_WHOLE = 3 * DC };
@@ -296,38 +308,38 @@ __device__ __forceinline__ void prepare_chunk(char* sm, const char* kt, const ch
         }
 }
 
-// Fragments (16 rows of S, eight columns a tile) from and to [d][d] float32 rows.
-template <int D>
-__device__ __forceinline__ void load_rows(float (&s)[D / 8][4], const float* m, int lane) {
+// Fragments (16 rows of S, eight columns a tile, W in all) from and to [..][D] float32 rows.
+template <int D, int W>
+__device__ __forceinline__ void load_rows(float (&s)[W / 8][4], const float* m, int lane) {
     const int r = lane >> 2, t2 = (lane & 3) * 2;
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
+    for (int n = 0; n < W / 8; ++n) {
         const float2 a = m ? *reinterpret_cast<const float2*>(m + r * D + n * 8 + t2) : make_float2(0.f, 0.f);
         const float2 b = m ? *reinterpret_cast<const float2*>(m + (r + 8) * D + n * 8 + t2) : make_float2(0.f, 0.f);
         s[n][0] = a.x, s[n][1] = a.y, s[n][2] = b.x, s[n][3] = b.y;
     }
 }
-template <int D>
-__device__ __forceinline__ void store_rows(const float (&s)[D / 8][4], float* m, int lane) {
+template <int D, int W>
+__device__ __forceinline__ void store_rows(const float (&s)[W / 8][4], float* m, int lane) {
     const int r = lane >> 2, t2 = (lane & 3) * 2;
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
+    for (int n = 0; n < W / 8; ++n) {
         *reinterpret_cast<float2*>(m + r * D + n * 8 + t2) = make_float2(s[n][0], s[n][1]);
         *reinterpret_cast<float2*>(m + (r + 8) * D + n * 8 + t2) = make_float2(s[n][2], s[n][3]);
     }
 }
 
-// X^T (16 rows x 32 tokens) = S A^T of a tile's 32 rows A, and of the first SP parts of S and a second tile Y^T =
-// S A2^T (SP 0: none). `at`: the tiles with across_down.
-template <int D, int LD, int NP, int SP, int PLANE>
-__device__ __forceinline__ void times_rows(float (&x)[4][4], float (&y)[4][4], const float (&s)[D / 8][4], uint32_t at, uint32_t at2) {
+// X^T (16 rows x 32 tokens) = S A^T over W columns of S and of a tile's 32 rows A, and of the first SP parts of S and a
+// second tile Y^T = S A2^T (SP 0: none). `at`: the tiles with across_down.
+template <int W, int LD, int NP, int SP, int PLANE>
+__device__ __forceinline__ void times_rows(float (&x)[4][4], float (&y)[4][4], const float (&s)[W / 8][4], uint32_t at, uint32_t at2) {
     float xl[4][4] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[i][e] = 0.f, y[i][e] = SP ? 0.f : y[i][e];
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
+    for (int ks = 0; ks < W / 16; ++ks) {
         uint32_t a[3][4], b[4][NP][2];
         to_operand<3>(a, s[2 * ks], s[2 * ks + 1]);
 #pragma unroll
@@ -346,31 +358,57 @@ __device__ __forceinline__ void times_rows(float (&x)[4][4], float (&y)[4][4], c
     join(x, xl);
 }
 
+// A tile pair of X^T (16 rows x 16 tokens) += U^T of 16 tokens times a 16 x 16 block of WP parts: from its rows (TRANS:
+// `at` with down_across) or those of its transpose (with across_down).
+template <int WP, int UP, int PAIR, bool TRANS>
+__device__ __forceinline__ void times_block(float (*x)[4], float (*xl)[4], const uint32_t (&a)[UP][4], uint32_t at) {
+    uint32_t w[2][WP][2];
+#pragma unroll
+    for (int q = 0; q < WP; ++q) {
+        if constexpr (TRANS)
+            ldsm_pair_t(w, 0, q, at + q * PAIR);
+        else
+            ldsm_pair(w, 0, q, at + q * PAIR);
+    }
+    mma_tiles<UP>(x, xl, a, w);
+}
+
 // X^T (16 rows x 32 tokens) += U^T W over 16 of W's 32 rows (`ks`), W upper triangular (AFTER: columns from its row on)
-// or lower, in WP parts: from W's rows (TRANS: `at` with down_across) or W^T's (with across_down).
+// or lower: as times_block.
 template <int WP, int UP, int PAIR, bool AFTER, bool TRANS>
 __device__ __forceinline__ void times_triangle(float (&x)[4][4], float (&xl)[4][4], const uint32_t (&a)[UP][4], int ks, uint32_t at) {
-    uint32_t w[4][WP][2];
-    const int first = AFTER ? ks : 0, last = AFTER ? 1 : ks;
-#pragma unroll
-    for (int np = first; np <= last; ++np)
-#pragma unroll
-        for (int q = 0; q < WP; ++q) {
-            if constexpr (TRANS)
-                ldsm_pair_t(w, 2 * np, q, at + q * PAIR + (ks * 16 * PLD + np * 16) * 2);
-            else
-                ldsm_pair(w, 2 * np, q, at + q * PAIR + (np * 16 * PLD + ks * 16) * 2);
-        }
-    if (first == last) {
-        uint32_t one[2][WP][2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int q = 0; q < WP; ++q) one[n][q][0] = w[2 * first + n][q][0], one[n][q][1] = w[2 * first + n][q][1];
-        mma_tiles<UP>(x + 2 * first, xl + 2 * first, a, one);
+    auto place = [&](int np) { return at + (TRANS ? ks * 16 * PLD + np * 16 : np * 16 * PLD + ks * 16) * 2; };
+    if (ks == (AFTER ? 1 : 0)) {
+        times_block<WP, UP, PAIR, TRANS>(x + 2 * ks, xl + 2 * ks, a, place(ks));
     } else {
+        uint32_t w[4][WP][2];
+#pragma unroll
+        for (int np = 0; np < 2; ++np)
+#pragma unroll
+            for (int q = 0; q < WP; ++q) {
+                if constexpr (TRANS)
+                    ldsm_pair_t(w, 2 * np, q, place(np) + q * PAIR);
+                else
+                    ldsm_pair(w, 2 * np, q, place(np) + q * PAIR);
+            }
         mma_tiles<UP>(x, xl, a, w);
     }
+}
+
+// What a warp gives its pair's other warp: four values a lane at a time.
+__device__ __forceinline__ void give(char* swap, int i, const float (&x)[4], int lane) {
+    reinterpret_cast<float4*>(swap)[i * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void take(const char* swap, int i, float (&x)[4], int lane) {
+    const float4 w = reinterpret_cast<const float4*>(swap)[i * 32 + lane];
+    x[0] += w.x, x[1] += w.y, x[2] += w.z, x[3] += w.w;
+}
+// A warp's half of the tokens.
+__device__ __forceinline__ void half_of(float (&y)[2][4], const float (&x)[4][4], int half) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[i][e] = half ? x[2 + i][e] : x[i][e];
 }
 
 // The values of the 16 rows at two tiles of 8 tokens, as fragments, from a tile's 16 tokens (at: of the warp's
@@ -393,40 +431,41 @@ __device__ __forceinline__ void columns_of(float (&x0)[4], float (&x1)[4], uint3
     }
 }
 
-// S = whole S + U^T A, U^T (16 rows x 32 tokens) given as fragments, A a tile's 32 rows: `at` with down_across. The
-// products have a sum of their own, which an fp32 addition rounds once into S.
-template <int D, int LD, int NP, int PLANE>
-__device__ __forceinline__ void add_outer(float (&s)[D / 8][4], float whole, const float (&u)[4][4], uint32_t at) {
+// S = whole S + U^T A, U^T (16 rows x 32 tokens) given as fragments, A W columns of a tile's 32 rows: `at` with
+// down_across. The products have a sum of their own, which an fp32 addition rounds once into S.
+template <int W, int LD, int NP, int PLANE>
+__device__ __forceinline__ void add_outer(float (&s)[W / 8][4], float whole, const float (&u)[4][4], uint32_t at) {
     uint32_t a[2][3][4];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) to_operand<3>(a[ks], u[2 * ks], u[2 * ks + 1]);
+    constexpr int NT = W % 32 == 0 ? 4 : 2;  // tiles at a time
 #pragma unroll
-    for (int n4 = 0; n4 < D / 32; ++n4) {
-        float t[4][4] = {}, low[4][4] = {};
+    for (int n0 = 0; n0 < W / 8; n0 += NT) {
+        float t[NT][4] = {}, low[NT][4] = {};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            uint32_t b[4][NP][2];
+            uint32_t b[NT][NP][2];
 #pragma unroll
-            for (int np = 0; np < 2; ++np)
+            for (int n = 0; n < NT; n += 2)
 #pragma unroll
-                for (int p = 0; p < NP; ++p) ldsm_pair_t(b, 2 * np, p, at + p * PLANE + ks * 16 * LD * 2 + (2 * n4 + np) * 32);
+                for (int p = 0; p < NP; ++p) ldsm_pair_t(b, n, p, at + p * PLANE + ks * 16 * LD * 2 + (n0 + n) * 16);
             mma_tiles<3>(t, low, a[ks], b);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < NT; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[4 * n4 + k][e] = fmaf(whole, s[4 * n4 + k][e], t[k][e] + low[k][e]);
+            for (int e = 0; e < 4; ++e) s[n0 + k][e] = fmaf(whole, s[n0 + k][e], t[k][e] + low[k][e]);
     }
 }
 
-// A warp's fragments (16 columns of d, 32 tokens) to rows of a sequence: rows below n, zeros up to T.
+// A warp's fragments (16 columns of d, 16 tokens) to rows of a sequence from t0: rows below n, zeros up to T.
 template <typename T, int OUT_LD>
-__device__ __forceinline__ void store_tokens(const float (&x)[4][4], char* stage, const Seq& s, int b, int h, long long t0, int col0,
+__device__ __forceinline__ void store_tokens(const float (&x)[2][4], char* stage, const Seq& s, int b, int h, long long t0, int col0,
                                              long long n, long long T_, int lane) {
     const int r = lane >> 2, t2 = (lane & 3) * 2;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const long long t = t0 + i * 8 + t2 + e;
@@ -437,21 +476,16 @@ __device__ __forceinline__ void store_tokens(const float (&x)[4][4], char* stage
             }
     } else {
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i)  // 16 tokens: blocks (tokens, columns) as across_down
-            stsm_t(vla::smem_u32(stage) + (i * 16 * OUT_LD + across_down<OUT_LD>(lane)) * 2, pack_bf16(x[2 * i][0], x[2 * i][1]),
-                   pack_bf16(x[2 * i][2], x[2 * i][3]), pack_bf16(x[2 * i + 1][0], x[2 * i + 1][1]),
-                   pack_bf16(x[2 * i + 1][2], x[2 * i + 1][3]));
+        // blocks (tokens, columns) as across_down
+        stsm_t(vla::smem_u32(stage) + across_down<OUT_LD>(lane) * 2, pack_bf16(x[0][0], x[0][1]), pack_bf16(x[0][2], x[0][3]),
+               pack_bf16(x[1][0], x[1][1]), pack_bf16(x[1][2], x[1][3]));
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = i * 16 + (lane >> 1), c = (lane & 1) * 8;
-            const long long t = t0 + row;
-            if (t >= T_) continue;
-            uint4 w = *reinterpret_cast<const uint4*>(stage + (row * OUT_LD + c) * 2);
-            if (t >= n) w = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(row_of<T>(s, b, h, t) + col0 + c) = w;
-        }
+        const int row = lane >> 1, c = (lane & 1) * 8;
+        const long long t = t0 + row;
+        if (t >= T_) return;
+        uint4 w = *reinterpret_cast<const uint4*>(stage + (row * OUT_LD + c) * 2);
+        if (t >= n) w = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(row_of<T>(s, b, h, t) + col0 + c) = w;
     }
 }
 

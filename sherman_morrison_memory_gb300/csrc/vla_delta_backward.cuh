@@ -26,14 +26,14 @@ struct DeltaReverse {
 };
 
 template <int D, typename T>
-__global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_reverse_kernel(const __grid_constant__ DeltaArgs p) {
+__global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_reverse_kernel(const __grid_constant__ DeltaArgs p) {
     using F = DeltaReverse<D, T>;
     using L = typename F::L;
     constexpr int NP = F::NP, LD = L::LD, SPAN = BLOCK<T>;
     extern __shared__ __align__(128) char sm[];
     const int splits = D / p.rows, bh = blockIdx.x / splits, row0 = (blockIdx.x % splits) * p.rows;
     const int b = bh / p.H, h = bh % p.H;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, workers = p.rows / 16;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, workers = p.rows / 8;
     const long long n = delta_len(p, b);
     const int chunks = (int)((n + DC - 1) / DC);
     // the m-th chunk in the order of work
@@ -88,47 +88,60 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_reverse_kernel(cons
         return;
     }
 
-    const int r = lane >> 2, t2 = (lane & 3) * 2, my_row = row0 + warp * 16;
-    float s[D / 8][4];
-    load_rows<D>(s, p.dS_T ? p.dS_T + (size_t)bh * D * D + my_row * D : nullptr, lane);
+    constexpr int W = D / 2;  // columns of a warp
+    const int r = lane >> 2, t2 = (lane & 3) * 2, pair = warp >> 1, half = warp & 1, my_row = row0 + pair * 16;
+    const size_t own = (size_t)my_row * D + half * W;
+    float s[W / 8][4];
+    load_rows<D, W>(s, p.dS_T ? p.dS_T + (size_t)bh * D * D + own : nullptr, lane);
     float bad = 0.f;
-    char* stage = sm + L::OUT + warp * DC * L::OUT_LD * 2;
+    char* stage = sm + L::OUT + warp * L::OUTS;
+    char *mine = sm + L::SWAP + warp * L::SWAPS, *other = sm + L::SWAP + (warp ^ 1) * L::SWAPS;
     __syncthreads();
     for (int m = 0; m < chunks; ++m) {
-        const long long t0 = (long long)(chunks - 1 - m) * DC;
+        const long long t0 = (long long)(chunks - 1 - m) * DC, h0 = t0 + half * 16;
+        const uint32_t kt = vla::smem_u32(tile(m, 0)) + half * W * 2, qt = vla::smem_u32(tile(m, 1)) + half * W * 2;
+        const uint32_t ot = vla::smem_u32(tile(m, 2)) + (across_down<LD>(lane) + pair * 16) * 2;
+        const char* pr = prep(m);
+        const float* gates = reinterpret_cast<const float*>(pr + L::GATES);
+        float e[2][4], v[2][4];
+        {
+            const float* E = p.E + ((size_t)bh * p.T + h0) * D + my_row + r;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = i * 8 + t2 + (k & 1);
+                    e[i][k] = h0 + j < n ? E[(size_t)j * D + (k & 2) * 4] : 0.f;
+                    if constexpr (NP > 1) v[i][k] = h0 + j < n ? row_of<float>(p.v, b, h, h0 + j)[my_row + r + (k & 2) * 4] : 0.f;
+                }
+        }
         if (m == 0 || (t0 + DC) % SPAN == 0) {
             const long long blk = t0 / SPAN;
-            const size_t at = ((size_t)bh * (p.blocks + 1) + blk) * D * D + my_row * D;
-            store_rows<D>(s, p.behind + at, lane);
+            const size_t at = ((size_t)bh * (p.blocks + 1) + blk) * D * D + own;
+            store_rows<D, W>(s, p.behind + at, lane);
             const float* S = p.before + at + (size_t)D * D;
             float dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
+            for (int i = 0; i < W / 8; ++i) {
                 const float2 a = *reinterpret_cast<const float2*>(S + r * D + i * 8 + t2);
                 const float2 c = *reinterpret_cast<const float2*>(S + (r + 8) * D + i * 8 + t2);
                 dot = fmaf(s[i][0], a.x, fmaf(s[i][1], a.y, fmaf(s[i][2], c.x, fmaf(s[i][3], c.y, dot))));
             }
 #pragma unroll
             for (int i = 1; i < 32; i <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
-            if (lane == 0) p.ends[((size_t)bh * p.blocks + blk) * (D / 16) + my_row / 16] = dot;
+            if (lane == 0) p.ends[((size_t)bh * p.blocks + blk) * (D / 8) + my_row / 8 + half] = dot;
         }
-        const uint32_t kt = vla::smem_u32(tile(m, 0)), qt = vla::smem_u32(tile(m, 1));
-        const uint32_t ot = vla::smem_u32(tile(m, 2)) + (across_down<LD>(lane) + warp * 16) * 2;
-        const char* pr = prep(m);
-        const float* gates = reinterpret_cast<const float*>(pr + L::GATES);
-        float e[4][4];
-        const float* E = p.E + ((size_t)bh * p.T + t0) * D + my_row;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = i * 8 + t2 + (k & 1);
-                e[i][k] = t0 + j < n ? E[(size_t)j * D + r + (k & 2) * 4] : 0.f;
-            }
         float x[4][4];
-        times_rows<D, LD, NP, 0, L::PLANE>(x, e, s, kt + across_down<LD>(lane) * 2, 0);
+        {
+            float none[4][4];
+            times_rows<W, LD, NP, 0, L::PLANE>(x, none, s, kt + across_down<LD>(lane) * 2, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) give(mine, i, x[i], lane);
+        vla::named_bar(3 + pair, 64);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            take(other, i, x[i], lane);
             const float2 far = *reinterpret_cast<const float2*>(gates + GATE_FAR + i * 8 + t2);
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[i][k] *= k & 1 ? far.y : far.x;
@@ -155,55 +168,39 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_reverse_kernel(cons
             }
             join(u, low);
         }
-        float bd[8], vd[8];
+        // the half of the tokens whose results it writes
+        float y[2][4];
+        half_of(y, u, half);
+        if constexpr (NP == 1)
+            columns_of<1, L::PLANE>(v[0], v[1], vla::smem_u32(tile(m, 3)) + (half * 16 * LD + across_down<LD>(lane) + pair * 16) * 2);
+        {
+            const size_t at = ((size_t)bh * (D / 16) + my_row / 16) * p.T + h0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 beta = *reinterpret_cast<const float2*>(gates + GATE_BETA + i * 8 + t2);
+            for (int i = 0; i < 2; ++i) {
+                const float2 beta = *reinterpret_cast<const float2*>(gates + GATE_BETA + (half * 2 + i) * 8 + t2);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) bd[2 * i + k] = over_rows(fmaf(u[i][k], e[i][k], u[i][2 + k] * e[i][2 + k]));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) u[i][k] *= k & 1 ? beta.y : beta.x;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            float v0[4], v1[4];
-            if constexpr (NP == 1) {
-                columns_of<1, L::PLANE>(v0, v1, vla::smem_u32(tile(m, 3)) + (across_down<LD>(lane) + warp * 16 + (i / 2) * 16 * LD) * 2);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const long long t = t0 + i * 8 + (k >> 2) * 8 + t2 + (k & 1);
-                    const float v = t < n ? row_of<float>(p.v, b, h, t)[my_row + r + (k & 2) * 4] : 0.f;
-                    (k < 4 ? v0 : v1)[k & 3] = v;
+                for (int k = 0; k < 2; ++k) {
+                    const float bd = over_rows(fmaf(y[i][k], e[i][k], y[i][2 + k] * e[i][2 + k]));
+                    y[i][k] *= k ? beta.y : beta.x;
+                    y[i][2 + k] *= k ? beta.y : beta.x;
+                    const float vd = over_rows(fmaf(y[i][k], v[i][k], y[i][2 + k] * v[i][2 + k]));
+                    const int j = i * 8 + t2 + k;
+                    if (h0 + j < n) {
+                        if (lane < 4) p.bd[at + j] = bd, p.vd[at + j] = vd;
+                        bad = fmaf(y[i][k], 0.f, fmaf(y[i][2 + k], 0.f, bad));
+                    }
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                vd[2 * i + k] = over_rows(fmaf(u[i][k], v0[k], u[i][2 + k] * v0[2 + k]));
-                vd[2 * i + 2 + k] = over_rows(fmaf(u[i + 1][k], v1[k], u[i + 1][2 + k] * v1[2 + k]));
-            }
         }
-        if (lane < 4) {
-            const size_t at = ((size_t)bh * (D / 16) + my_row / 16) * p.T + t0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = (i >> 1) * 8 + t2 + (i & 1);
-                if (t0 + j < n) p.bd[at + j] = bd[i], p.vd[at + j] = vd[i];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (t0 + i * 8 + t2 + (k & 1) < n) bad = fmaf(u[i][k], 0.f, bad);
-        store_tokens<T, L::OUT_LD>(u, stage, p.dv, b, h, t0, my_row, n, p.T, lane);
+        store_tokens<T, L::OUT_LD>(y, stage, p.dv, b, h, h0, my_row, n, p.T, lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 near = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + t2);
+            const float2 beta = *reinterpret_cast<const float2*>(gates + GATE_BETA + i * 8 + t2);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) u[i][k] *= -(k & 1 ? near.y : near.x);
+            for (int k = 0; k < 4; ++k) u[i][k] *= -((k & 1 ? near.y : near.x) * (k & 1 ? beta.y : beta.x));
         }
-        add_outer<D, LD, NP, L::PLANE>(s, gates[GATE_WHOLE], u, kt + down_across<LD>(lane) * 2);
+        add_outer<W, LD, NP, L::PLANE>(s, gates[GATE_WHOLE], u, kt + down_across<LD>(lane) * 2);
 #pragma unroll
         for (int i = 0; i < 4; i += 2) columns_of<NP, L::PLANE>(x[i], x[i + 1], ot + (i / 2) * 16 * LD * 2);
 #pragma unroll
@@ -212,13 +209,13 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_reverse_kernel(cons
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[i][k] *= p.scale * (k & 1 ? near.y : near.x);
         }
-        add_outer<D, LD, NP, L::PLANE>(s, 1.f, x, qt + down_across<LD>(lane) * 2);
+        add_outer<W, LD, NP, L::PLANE>(s, 1.f, x, qt + down_across<LD>(lane) * 2);
         __syncthreads();
     }
     if (p.dS0) {
-        store_rows<D>(s, p.dS0 + (size_t)bh * D * D + my_row * D, lane);
+        store_rows<D, W>(s, p.dS0 + (size_t)bh * D * D + own, lane);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
+        for (int i = 0; i < W / 8; ++i)
 #pragma unroll
             for (int k = 0; k < 4; ++k) bad = fmaf(s[i][k], 0.f, bad);
     }
@@ -518,7 +515,7 @@ __global__ void __launch_bounds__(D * 2) vla_delta_grads_kernel(const __grid_con
     // the gates: sums over the warps' rows, and of them over the tokens from the block's end
     if (warp == 0) {
         double behind = 0.0;
-        for (int w = 0; w < D / 16; ++w) behind += (double)p.ends[((size_t)bh * p.blocks + blk) * (D / 16) + w];
+        for (int w = 0; w < D / 8; ++w) behind += (double)p.ends[((size_t)bh * p.blocks + blk) * (D / 8) + w];
 #pragma unroll
         for (int k = TB / 32 - 1; k >= 0; --k) {
             const int j = k * 32 + lane;

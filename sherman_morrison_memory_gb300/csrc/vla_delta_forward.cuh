@@ -16,14 +16,14 @@ struct DeltaForward {
 };
 
 template <int D, typename T, bool TAPE>
-__global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_forward_kernel(const __grid_constant__ DeltaArgs p) {
+__global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_forward_kernel(const __grid_constant__ DeltaArgs p) {
     using F = DeltaForward<D, T, TAPE>;
     using L = typename F::L;
     constexpr int NP = F::NP, PP = F::PP, LD = L::LD, SPAN = BLOCK<T>;
     extern __shared__ __align__(128) char sm[];
     const int splits = D / p.rows, bh = blockIdx.x / splits, row0 = (blockIdx.x % splits) * p.rows;
     const int b = bh / p.H, h = bh % p.H;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, workers = p.rows / 16;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, workers = p.rows / 8;
     const long long n = delta_len(p, b);
     const int chunks = (int)((n + DC - 1) / DC);
     auto tile = [&](int c, int i) { return sm + L::IN + ((c % L::STAGES) * F::TILES + i) * L::TILE; };
@@ -76,64 +76,89 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_forward_kernel(cons
         return;
     }
 
-    const int r = lane >> 2, t2 = (lane & 3) * 2, my_row = row0 + warp * 16;
-    float s[D / 8][4];
-    load_rows<D>(s, p.S0 ? p.S0 + (size_t)bh * D * D + my_row * D : nullptr, lane);
+    constexpr int W = D / 2;  // columns of a warp
+    const int r = lane >> 2, t2 = (lane & 3) * 2, pair = warp >> 1, half = warp & 1, my_row = row0 + pair * 16;
+    const size_t at = (size_t)my_row * D + half * W;
+    float s[W / 8][4];
+    load_rows<D, W>(s, p.S0 ? p.S0 + (size_t)bh * D * D + at : nullptr, lane);
     float bad = 0.f;
-    char* stage = sm + L::OUT + warp * DC * L::OUT_LD * 2;
+    char* stage = sm + L::OUT + warp * L::OUTS;
+    char *mine = sm + L::SWAP + warp * L::SWAPS, *other = sm + L::SWAP + (warp ^ 1) * L::SWAPS;
     __syncthreads();
     for (int c = 0; c < chunks; ++c) {
-        const long long t0 = (long long)c * DC;
+        const long long t0 = (long long)c * DC, h0 = t0 + half * 16;  // the chunk's tokens, those whose results it writes
         if constexpr (TAPE) {
-            if (t0 % SPAN == 0)
-                store_rows<D>(s, p.before + ((size_t)bh * (p.blocks + 1) + t0 / SPAN) * D * D + my_row * D, lane);
+            if (t0 % SPAN == 0) store_rows<D, W>(s, p.before + ((size_t)bh * (p.blocks + 1) + t0 / SPAN) * D * D + at, lane);
         }
-        const uint32_t kt = vla::smem_u32(tile(c, 0)), qt = vla::smem_u32(tile(c, 1));
-        const uint32_t vt = vla::smem_u32(tile(c, 2)) + (across_down<LD>(lane) + warp * 16) * 2;
+        const uint32_t kt = vla::smem_u32(tile(c, 0)) + half * W * 2, qt = vla::smem_u32(tile(c, 1)) + half * W * 2;
+        const uint32_t vt = vla::smem_u32(tile(c, 2)) + (across_down<LD>(lane) + pair * 16) * 2;
         const char* pr = prep(c);
+        const uint32_t inv = vla::smem_u32(pr + L::INV) + down_across<PLD>(lane) * 2;
         const float* gates = reinterpret_cast<const float*>(pr + L::GATES);
-        float x[4][4], o[4][4];
-        if constexpr (F::FULL) {
-            times_rows<D, LD, NP, 0, L::PLANE>(x, o, s, kt + across_down<LD>(lane) * 2, 0);
-            times_rows<D, LD, NP, 0, L::PLANE>(o, x, s, qt + across_down<LD>(lane) * 2, 0);
-        } else {
-            times_rows<D, LD, NP, 1, L::PLANE>(x, o, s, kt + across_down<LD>(lane) * 2, qt + across_down<LD>(lane) * 2);
-        }
-        // what the state gets wrong about the tokens' values, each token on its own
+        float x[4][4], o[2][4];
+        {
+            float all[4][4], away[2][4];
+            if constexpr (F::FULL) {
+                times_rows<W, LD, NP, 0, L::PLANE>(x, all, s, kt + across_down<LD>(lane) * 2, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 near = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + t2);
-            if (i % 2 == 0) {
-                float v0[4], v1[4];
-                columns_of<NP, L::PLANE>(v0, v1, vt + (i / 2) * 16 * LD * 2);
+                for (int i = 0; i < 4; ++i) give(mine, i, x[i], lane);
+                times_rows<W, LD, NP, 0, L::PLANE>(all, x, s, qt + across_down<LD>(lane) * 2, 0);
+            } else {
+                times_rows<W, LD, NP, 1, L::PLANE>(x, all, s, kt + across_down<LD>(lane) * 2, qt + across_down<LD>(lane) * 2);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[i][e] = fmaf(-(e & 1 ? near.y : near.x), x[i][e], v0[e]);
-                const float2 next = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + 8 + t2);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[i + 1][e] = fmaf(-(e & 1 ? next.y : next.x), x[i + 1][e], v1[e]);
+                for (int i = 0; i < 4; ++i) give(mine, i, x[i], lane);
             }
+            half_of(away, all, !half);
+            give(mine, 4, away[0], lane);
+            give(mine, 5, away[1], lane);
+            half_of(o, all, half);
+        }
+        vla::named_bar(3 + pair, 64);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) take(other, i, x[i], lane);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            take(other, 4 + i, o[i], lane);
+            const float2 near = *reinterpret_cast<const float2*>(gates + GATE_NEAR + (half * 2 + i) * 8 + t2);
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] *= p.scale * (e & 1 ? near.y : near.x);
         }
-        // ... and after the tokens before it in the chunk
-        float u[4][4] = {}, low[4][4] = {};
+        // what the state gets wrong about the tokens' values, each token on its own
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            uint32_t a[3][4];
-            to_operand<3>(a, x[2 * ks], x[2 * ks + 1]);
-            times_triangle<INV_PARTS, 3, L::PAIR, true, true>(u, low, a, ks, vla::smem_u32(pr + L::INV) + down_across<PLD>(lane) * 2);
+        for (int i = 0; i < 4; i += 2) {
+            float v[2][4];
+            columns_of<NP, L::PLANE>(v[0], v[1], vt + (i / 2) * 16 * LD * 2);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 near = *reinterpret_cast<const float2*>(gates + GATE_NEAR + (i + k) * 8 + t2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i + k][e] = fmaf(-(e & 1 ? near.y : near.x), x[i + k][e], v[k][e]);
+            }
         }
-        join(u, low);
+        // ... and after the tokens before it in the chunk
+        float u[4][4] = {};
+        {
+            float low[4][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                uint32_t a[3][4];
+                to_operand<3>(a, x[2 * ks], x[2 * ks + 1]);
+                times_triangle<INV_PARTS, 3, L::PAIR, true, true>(u, low, a, ks, inv);
+            }
+            join(u, low);
+        }
         if constexpr (TAPE) {
-            float* E = p.E + ((size_t)bh * p.T + t0) * D + my_row;
+            float e[2][4];
+            half_of(e, u, half);
+            float* E = p.E + ((size_t)bh * p.T + h0) * D + my_row + r;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = i * 8 + t2 + e;
-                    if (t0 + j >= n) continue;
-                    E[(size_t)j * D + r] = u[i][e];
-                    E[(size_t)j * D + r + 8] = u[i][2 + e];
+                for (int k = 0; k < 2; ++k) {
+                    const int j = i * 8 + t2 + k;
+                    if (h0 + j >= n) continue;
+                    E[(size_t)j * D] = e[i][k];
+                    E[(size_t)j * D + 8] = e[i][2 + k];
                 }
         }
 #pragma unroll
@@ -143,14 +168,45 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_forward_kernel(cons
             for (int e = 0; e < 4; ++e) u[i][e] *= e & 1 ? beta.y : beta.x;
         }
         {
-            float ol[4][4] = {};
+            float low[2][4] = {};
+            const uint32_t pairs = vla::smem_u32(pr + L::P) + (half * 16 * PLD + across_down<PLD>(lane)) * 2;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
+                if (ks > half) break;
                 uint32_t a[F::UP][4];
                 to_operand<F::UP>(a, u[2 * ks], u[2 * ks + 1]);
-                times_triangle<PP, F::UP, L::PAIR, true, false>(o, F::FULL ? ol : o, a, ks, vla::smem_u32(pr + L::P) + across_down<PLD>(lane) * 2);
+                times_block<PP, F::UP, L::PAIR, false>(o, low, a, pairs + ks * 32);
             }
-            if constexpr (F::FULL) join(o, ol);
+            join(o, low);
+        }
+        if constexpr (TAPE) {
+            float d[2][4];
+            if constexpr (NP == 1) {
+                columns_of<1, L::PLANE>(d[0], d[1], vla::smem_u32(tile(c, 3)) + (half * 16 * LD + across_down<LD>(lane) + pair * 16) * 2);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const long long t = h0 + i * 8 + t2 + (e & 1);
+                        d[i][e] = t < n ? row_of<float>(p.dO, b, h, t)[my_row + r + (e & 2) * 4] : 0.f;
+                    }
+            }
+            float* od = p.od + ((size_t)bh * (D / 16) + my_row / 16) * p.T + h0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float y = over_rows(fmaf(o[i][e], d[i][e], o[i][2 + e] * d[i][2 + e]));
+                    if (lane < 4 && h0 + i * 8 + t2 + e < n) od[i * 8 + t2 + e] = y;
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (h0 + i * 8 + t2 + (e & 1) < n) bad = fmaf(o[i][e], 0.f, bad);
+            store_tokens<T, L::OUT_LD>(o, stage, p.out, b, h, h0, my_row, n, p.T, lane);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -158,53 +214,16 @@ __global__ void __launch_bounds__(D * 2 + HELPERS) vla_delta_forward_kernel(cons
 #pragma unroll
             for (int e = 0; e < 4; ++e) u[i][e] *= e & 1 ? far.y : far.x;
         }
-        add_outer<D, LD, NP, L::PLANE>(s, gates[GATE_WHOLE], u, kt + down_across<LD>(lane) * 2);
-        if constexpr (TAPE) {
-            float od[8];
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                float d0[4], d1[4];
-                if constexpr (NP == 1) {
-                    columns_of<1, L::PLANE>(d0, d1, vla::smem_u32(tile(c, 3)) + (across_down<LD>(lane) + warp * 16 + (i / 2) * 16 * LD) * 2);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const long long t = t0 + i * 8 + (e >> 2) * 8 + t2 + (e & 1);
-                        const float v = t < n ? row_of<float>(p.dO, b, h, t)[my_row + r + (e & 2) * 4] : 0.f;
-                        (e < 4 ? d0 : d1)[e & 3] = v;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    od[2 * i + e] = over_rows(fmaf(o[i][e], d0[e], o[i][2 + e] * d0[2 + e]));
-                    od[2 * i + 2 + e] = over_rows(fmaf(o[i + 1][e], d1[e], o[i + 1][2 + e] * d1[2 + e]));
-                }
-            }
-            if (lane < 4) {
-                float* out = p.od + ((size_t)bh * (D / 16) + my_row / 16) * p.T + t0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = (i >> 1) * 8 + t2 + (i & 1);
-                    if (t0 + j < n) out[j] = od[i];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (t0 + i * 8 + t2 + (e & 1) < n) bad = fmaf(o[i][e], 0.f, bad);
-            store_tokens<T, L::OUT_LD>(o, stage, p.out, b, h, t0, my_row, n, p.T, lane);
-        }
+        add_outer<W, LD, NP, L::PLANE>(s, gates[GATE_WHOLE], u, kt + down_across<LD>(lane) * 2);
         __syncthreads();
     }
     if constexpr (TAPE) {
         const long long last = (n + SPAN - 1) / SPAN;
-        store_rows<D>(s, p.before + ((size_t)bh * (p.blocks + 1) + last) * D * D + my_row * D, lane);
+        store_rows<D, W>(s, p.before + ((size_t)bh * (p.blocks + 1) + last) * D * D + at, lane);
     } else {
-        store_rows<D>(s, p.S + (size_t)bh * D * D + my_row * D, lane);
+        store_rows<D, W>(s, p.S + (size_t)bh * D * D + at, lane);
 #pragma unroll
-        for (int m = 0; m < D / 8; ++m)
+        for (int m = 0; m < W / 8; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e) bad = fmaf(s[m][e], 0.f, bad);
         zero_tokens<T>(p.out, b, h, (long long)chunks * DC, p.T, row0, p.rows);

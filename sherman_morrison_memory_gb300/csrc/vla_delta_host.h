@@ -46,22 +46,21 @@ inline vla_status delta_pick(vla_dtype dtype, int d, F f) {
     return dtype == VLA_BF16 ? with(__nv_bfloat16{}) : with(float{});
 }
 
-// Rows of S of a block: all of a head's, or a half, a quarter, ... while the blocks are fewer than the SMs.
-inline int delta_rows(long long heads, int d) {
-    int rows = d;
+// Rows of S of a block: as many as it can have, or a half, a quarter, ... while the blocks are fewer than the SMs.
+inline int delta_rows(long long heads, int d, int rows) {
     while (rows % 32 == 0 && heads * (d / (rows / 2)) <= sm_count()) rows /= 2;
     return rows;
 }
 
-// One of the recurrences: a warp per 16 rows and the helpers.
+// One of the recurrences: two warps for 16 rows and the helpers.
 template <auto K, int D, typename L>
 inline vla_status delta_run(DeltaArgs& p, cudaStream_t s) {
     const long long heads = (long long)p.B * p.H;
-    p.rows = delta_rows(heads, D);
+    p.rows = delta_rows(heads, D, MOST_ROWS<D>);
     const long long grid = heads * (D / p.rows);
     if (grid > 2147483647LL) return VLA_ERR_INVALID_ARG;
     if (!allow_smem<K>(L::BYTES)) return VLA_ERR_CUDA;
-    K<<<(unsigned)grid, p.rows * 2 + HELPERS, L::BYTES, s>>>(p);
+    K<<<(unsigned)grid, p.rows * 4 + HELPERS, L::BYTES, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
 }
 
@@ -90,7 +89,7 @@ inline size_t delta_scratch(DeltaArgs* p, void* base, vla_dtype dtype, int B, in
     take(&a.od, per_warp);
     take(&a.vd, per_warp);
     take(&a.bd, per_warp);
-    take(&a.ends, heads * blocks * (d / 16));
+    take(&a.ends, heads * blocks * (d / 8));
     a.blocks = blocks;
     return at;
 }
