@@ -178,7 +178,7 @@ __device__ __forceinline__ void sums_of(float g, int lane, float& hi, float& lo)
     }
 }
 
-// The helpers' part of a chunk: gates, P and the inverse. Warps 0, 1, 2 have the 16 x 16 blocks (0, 0), (1, 0) and
+// The helpers' part of a chunk: gates (warp 3), P and the inverse. Warps 0, 1, 2 have the 16 x 16 blocks (0, 0), (1, 0) and
 // (1, 1) of both triangles; 0 and 2 invert theirs of 1 + N, a lane a column, 1 joins them: (1 + N)^-1 has -T22 N21 T11
 // below. The inverse is kept transposed, [j][i]. ROWS: 1 + diag(b) N, else 1 + N diag(b).
 template <typename L, int D, int NP, int PP, bool ROWS>
@@ -186,7 +186,7 @@ __device__ __forceinline__ void prepare_chunk(char* sm, const char* kt, const ch
                                               Whole& whole, int hw, int lane) {
     float Gh, Gl;
     sums_of(g, lane, Gh, Gl);
-    if (hw == 1) {
+    if (hw == 3) {
         const float all = __shfl_sync(0xffffffffu, Gh, 31), rest = __shfl_sync(0xffffffffu, Gl, 31);
         float* gates = reinterpret_cast<float*>(prep + L::GATES);
         gates[GATE_NEAR + lane] = expf(Gh + Gl);
@@ -194,6 +194,7 @@ __device__ __forceinline__ void prepare_chunk(char* sm, const char* kt, const ch
         gates[GATE_BETA + lane] = beta;
         const float w = whole.next(all + rest);
         if (lane == 0) gates[GATE_WHOLE] = w;
+        return;
     }
     const int mt = hw ? 1 : 0, np = hw == 2 ? 1 : 0;
     float c[4][4] = {}, cl[4][4] = {};  // K K^T, Q K^T
@@ -373,26 +374,29 @@ __device__ __forceinline__ void times_block(float (*x)[4], float (*xl)[4], const
     mma_tiles<UP>(x, xl, a, w);
 }
 
-// X^T (16 rows x 32 tokens) += U^T W over 16 of W's 32 rows (`ks`), W upper triangular (AFTER: columns from its row on)
-// or lower: as times_block.
+// X^T (16 rows x 32 tokens) += U^T W, W upper triangular (AFTER) or lower, in WP parts: as times_block. a[ks]: U^T of 16
+// tokens. The four tiles of the whole block row go first, the two of the other after them.
 template <int WP, int UP, int PAIR, bool AFTER, bool TRANS>
-__device__ __forceinline__ void times_triangle(float (&x)[4][4], float (&xl)[4][4], const uint32_t (&a)[UP][4], int ks, uint32_t at) {
-    auto place = [&](int np) { return at + (TRANS ? ks * 16 * PLD + np * 16 : np * 16 * PLD + ks * 16) * 2; };
-    if (ks == (AFTER ? 1 : 0)) {
-        times_block<WP, UP, PAIR, TRANS>(x + 2 * ks, xl + 2 * ks, a, place(ks));
-    } else {
-        uint32_t w[4][WP][2];
+__device__ __forceinline__ void times_triangle(float (&x)[4][4], float (&xl)[4][4], const uint32_t (&a)[2][UP][4], uint32_t at) {
+    constexpr int ks = AFTER ? 0 : 1, one = 1 - ks;
+    auto place = [&](int ks, int np) { return at + (TRANS ? ks * 16 * PLD + np * 16 : np * 16 * PLD + ks * 16) * 2; };
+    uint32_t w[4][WP][2], v[2][WP][2];
 #pragma unroll
-        for (int np = 0; np < 2; ++np)
+    for (int q = 0; q < WP; ++q) {
 #pragma unroll
-            for (int q = 0; q < WP; ++q) {
-                if constexpr (TRANS)
-                    ldsm_pair_t(w, 2 * np, q, place(np) + q * PAIR);
-                else
-                    ldsm_pair(w, 2 * np, q, place(np) + q * PAIR);
-            }
-        mma_tiles<UP>(x, xl, a, w);
+        for (int np = 0; np < 2; ++np) {
+            if constexpr (TRANS)
+                ldsm_pair_t(w, 2 * np, q, place(ks, np) + q * PAIR);
+            else
+                ldsm_pair(w, 2 * np, q, place(ks, np) + q * PAIR);
+        }
+        if constexpr (TRANS)
+            ldsm_pair_t(v, 0, q, place(one, one) + q * PAIR);
+        else
+            ldsm_pair(v, 0, q, place(one, one) + q * PAIR);
     }
+    mma_tiles<UP>(x, xl, a[ks], w);
+    mma_tiles<UP>(x + 2 * one, xl + 2 * one, a[one], v);
 }
 
 // What a warp gives its pair's other warp: four values a lane at a time.

@@ -73,14 +73,11 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_reverse_kernel(con
                     load(m);
                     vla::named_bar(1, HELPERS);
                 }
-                if (hw < 3) {
-                    const float gm = g, bm = beta;
-                    gates(m + 1);
-                    prepare_chunk<L, D, NP, 3, true>(sm, tile(m, 0), tile(m, 1), prep(m), gm, bm, p.scale, whole, hw, lane);
-                } else if (NP == 1 && m + 1 < chunks) {
-                    load(m + 1);
-                    cp_async_wait<0>();
-                }
+                if (NP == 1 && hw == 3 && m + 1 < chunks) load(m + 1);
+                const float gm = g, bm = beta;
+                gates(m + 1);
+                prepare_chunk<L, D, NP, 3, true>(sm, tile(m, 0), tile(m, 1), prep(m), gm, bm, p.scale, whole, hw, lane);
+                cp_async_wait<0>();
             }
             __syncthreads();
         }
@@ -148,24 +145,21 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_reverse_kernel(con
         }
         {
             float low[4][4] = {};
+            uint32_t a[2][NP][4];
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                uint32_t a[NP][4];
+            for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int q = 0; q < NP; ++q) ldsm_t(a[q], ot + q * L::PLANE + ks * 16 * LD * 2);
-                times_triangle<3, NP, L::PAIR, false, true>(x, low, a, ks, vla::smem_u32(pr + L::P) + down_across<PLD>(lane) * 2);
-            }
+                for (int q = 0; q < NP; ++q) ldsm_t(a[ks][q], ot + q * L::PLANE + ks * 16 * LD * 2);
+            times_triangle<3, NP, L::PAIR, false, true>(x, low, a, vla::smem_u32(pr + L::P) + down_across<PLD>(lane) * 2);
             join(x, low);
         }
         float u[4][4] = {};
         {
             float low[4][4] = {};
+            uint32_t a[2][3][4];
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                uint32_t a[3][4];
-                to_operand<3>(a, x[2 * ks], x[2 * ks + 1]);
-                times_triangle<INV_PARTS, 3, L::PAIR, false, false>(u, low, a, ks, vla::smem_u32(pr + L::INV) + across_down<PLD>(lane) * 2);
-            }
+            for (int ks = 0; ks < 2; ++ks) to_operand<3>(a[ks], x[2 * ks], x[2 * ks + 1]);
+            times_triangle<INV_PARTS, 3, L::PAIR, false, false>(u, low, a, vla::smem_u32(pr + L::INV) + across_down<PLD>(lane) * 2);
             join(u, low);
         }
         // the half of the tokens whose results it writes

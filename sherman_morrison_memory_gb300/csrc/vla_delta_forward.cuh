@@ -61,14 +61,11 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_forward_kernel(con
                     load(c);
                     vla::named_bar(1, HELPERS);
                 }
-                if (hw < 3) {
-                    const float gc = g, bc = beta;
-                    gates(c + 1);
-                    prepare_chunk<L, D, NP, PP, false>(sm, tile(c, 0), tile(c, 1), prep(c), gc, bc, p.scale, whole, hw, lane);
-                } else if (NP == 1 && c + 1 < chunks) {
-                    load(c + 1);
-                    cp_async_wait<0>();
-                }
+                if (NP == 1 && hw == 3 && c + 1 < chunks) load(c + 1);
+                const float gc = g, bc = beta;
+                gates(c + 1);
+                prepare_chunk<L, D, NP, PP, false>(sm, tile(c, 0), tile(c, 1), prep(c), gc, bc, p.scale, whole, hw, lane);
+                cp_async_wait<0>();
             }
             __syncthreads();
         }
@@ -139,12 +136,10 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_forward_kernel(con
         float u[4][4] = {};
         {
             float low[4][4] = {};
+            uint32_t a[2][3][4];
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                uint32_t a[3][4];
-                to_operand<3>(a, x[2 * ks], x[2 * ks + 1]);
-                times_triangle<INV_PARTS, 3, L::PAIR, true, true>(u, low, a, ks, inv);
-            }
+            for (int ks = 0; ks < 2; ++ks) to_operand<3>(a[ks], x[2 * ks], x[2 * ks + 1]);
+            times_triangle<INV_PARTS, 3, L::PAIR, true, true>(u, low, a, inv);
             join(u, low);
         }
         if constexpr (TAPE) {

@@ -6,15 +6,17 @@
 
 namespace vla_layer {
 
-// x as the sum of N bf16 parts, each the rest of those before it, rounded; two values at a time.
+// x as the sum of N bf16 parts, two values at a time: the first is x rounded (it may stand for x alone), the others are
+// of what is left, eight bits at a time; three parts hold the value's 24 bits. The last of two is rounded too.
 template <int N>
 __device__ __forceinline__ void split(float x0, float x1, uint32_t (&p)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        p[i] = pack_bf16(x0, x1);
+        const bool cut = N == 3 && i > 0;
+        p[i] = cut ? __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632) : pack_bf16(x0, x1);
         if (i + 1 < N) {
-            x0 -= __uint_as_float(p[i] << 16);
-            x1 -= __uint_as_float(p[i] & 0xFFFF0000u);
+            x0 -= cut ? __uint_as_float(__float_as_uint(x0) & 0xFFFF0000u) : __uint_as_float(p[i] << 16);
+            x1 -= cut ? __uint_as_float(__float_as_uint(x1) & 0xFFFF0000u) : __uint_as_float(p[i] & 0xFFFF0000u);
         }
     }
 }
