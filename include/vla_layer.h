@@ -153,7 +153,7 @@ vla_status vla_decay_step(const void* q, const void* k, const void* v, vla_dtype
  *
  * A token's NaN or Inf reaches the results that depend on it, and may reach those of
  * other tokens of its block of 64 in the same head. One in an output sets VLA_ERR_NONFINITE
- * in the status record. */
+ * in the status record; a bounded in-kernel wait that ran out VLA_ERR_TIMEOUT. */
 
 /* Gates [B, H, T] float32: element (b, h, t) is data[b * stride_b + h * stride_h +
  * t * stride_t]. data is 4-byte aligned; the strides of dimensions longer than 1
@@ -196,6 +196,19 @@ vla_status vla_delta_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
                               const vla_seq_out* dk, const vla_seq_out* dv, const vla_gate_out* dlog_decay,
                               const vla_gate_out* dbeta, float* dS0, void* scratch, size_t scratch_bytes, void* status,
                               void* stream);
+
+/* Both with options, as vla_decay_forward_ex() and vla_decay_backward_ex(): bf16 calls of
+ * more than 64 tokens have in-kernel waits. */
+vla_status vla_delta_forward_ex(const vla_seq* q, const vla_seq* k, const vla_seq* v, vla_dtype dtype, int B, int H, int T,
+                                int d, const vla_gate* log_decay, const vla_gate* beta, float scale, const int* lengths,
+                                const float* S0, const vla_seq_out* o, float* S_out, void* status, void* stream,
+                                const vla_options* opts);
+vla_status vla_delta_backward_ex(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO, vla_dtype dtype,
+                                 int B, int H, int T, int d, const vla_gate* log_decay, const vla_gate* beta, float scale,
+                                 const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,
+                                 const vla_seq_out* dk, const vla_seq_out* dv, const vla_gate_out* dlog_decay,
+                                 const vla_gate_out* dbeta, float* dS0, void* scratch, size_t scratch_bytes, void* status,
+                                 void* stream, const vla_options* opts);
 
 /* One token of the rule for B sequences, their states updated in place in a pool;
  * log_decay (NULL: 0) and beta [B, H] float32, contiguous; the rest as for

@@ -66,6 +66,8 @@ def _layer_prototypes(lib):
                               ctypes.POINTER(_Seq))
     forward = [sq] * 3 + [ci] * 5 + [vp, cf, vp, vp, sq, vp, vp, cz, vp, vp]
     backward = [sq] * 4 + [ci] * 5 + [vp, cf, vp, vp, vp, sq, sq, sq, vp, vp, cz, vp, vp]
+    delta_forward = [sq] * 3 + [ci] * 5 + [sq, sq, cf, vp, vp, sq, vp, vp, vp]
+    delta_backward = [sq] * 4 + [ci] * 5 + [sq, sq, cf, vp, vp, vp] + [sq] * 5 + [vp, vp, cz, vp, vp]
     options = [ctypes.POINTER(_Options)]
     for name, args, res in (
             ("vla_decay_scratch_bytes", [ci] * 5, cz),
@@ -73,8 +75,8 @@ def _layer_prototypes(lib):
             ("vla_decay_backward", backward, ci), ("vla_decay_backward_ex", backward + options, ci),
             ("vla_decay_step", [vp] * 3 + [ci] * 4 + [vp, cf, vp, ci, vp, vp, vp, vp], ci),
             ("vla_delta_scratch_bytes", [ci] * 5, cz),
-            ("vla_delta_forward", [sq] * 3 + [ci] * 5 + [sq, sq, cf, vp, vp, sq, vp, vp, vp], ci),
-            ("vla_delta_backward", [sq] * 4 + [ci] * 5 + [sq, sq, cf, vp, vp, vp] + [sq] * 5 + [vp, vp, cz, vp, vp], ci),
+            ("vla_delta_forward", delta_forward, ci), ("vla_delta_forward_ex", delta_forward + options, ci),
+            ("vla_delta_backward", delta_backward, ci), ("vla_delta_backward_ex", delta_backward + options, ci),
             ("vla_delta_step", [vp] * 3 + [ci] * 4 + [vp, vp, cf, vp, ci, vp, vp, vp, vp], ci),
             ("vla_qk_norm", [sq, sq] + [ci] * 5 + [vp, vp, ci, ci, cf, vp, ci, vp, cl, sq, sq, vp, vp, vp], ci),
             ("vla_qk_norm_scratch_bytes", [ci] * 4, cz),

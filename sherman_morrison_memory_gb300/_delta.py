@@ -13,7 +13,7 @@ import torch
 
 from ._binding import _DTYPES, _call_buffer, _Seq, _workspace, load_library
 from ._layer import (_check_f32, _check_index, _check_out, _check_seq, _done, _handle, _on, _ptr, _scale, _seq, _seq_in,
-                     _DIMS)
+                     _wait_options, _DIMS)
 
 
 @functools.lru_cache(maxsize=256)
@@ -41,7 +41,8 @@ def _gate_out(x: torch.Tensor, shape, device, name: str):
 
 def vla_delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: Optional[torch.Tensor],
                       beta: torch.Tensor, scale: float = 1.0, state: Optional[torch.Tensor] = None, *,
-                      lengths: Optional[torch.Tensor] = None, out=None, stream=None, check: bool = False):
+                      lengths: Optional[torch.Tensor] = None, out=None, stream=None, check: bool = False,
+                      wait_limit_us: int = 0, test_stall_producer: bool = False):
     """The gated delta rule over a sequence, a_t = exp(log_decay_t):
     S_t = a_t S_{t-1} + beta_t (v_t - a_t S_{t-1} k_t) k_t^T, o_t = scale S_t q_t.
 
@@ -53,7 +54,10 @@ def vla_delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
     zero behind them. bf16 calls round pair products and the state that a token
     sees to bf16 on the way to o (S itself stays fp32). ``out`` = (o, S)
     preallocated; S may be ``state``. ``check=True`` synchronises and raises on
-    a non-finite result.
+    an in-kernel failure or a non-finite result. ``wait_limit_us`` (0:
+    2,000,000) bounds each in-kernel wait; ``test_stall_producer=True`` (testing
+    only) makes them run out (VLA_ERR_TIMEOUT): bf16 calls of more than 64
+    tokens have such waits.
     """
     for name, x in (("q", q), ("k", k), ("v", v)):
         _check_seq(x, name, None if x is q else q)
@@ -74,8 +78,12 @@ def vla_delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
             _check_out(o, (B, H, T, d), q.dtype, dev, "out[0]", strided=True)
             _check_out(S, (B, H, d, d), torch.float32, dev, "out[1]")
         q, k, v = (_seq_in(x) for x in (q, k, v))
-        st = lib.vla_delta_forward(_seq(q), _seq(k), _seq(v), _DTYPES[q.dtype], B, H, T, d, _gate(g), _gate(beta), scale,
-                                   _ptr(lengths), _ptr(S0), _seq(o), _ptr(S), _ptr(_workspace(dev)), _handle(dev, stream))
+        args = (_seq(q), _seq(k), _seq(v), _DTYPES[q.dtype], B, H, T, d, _gate(g), _gate(beta), scale, _ptr(lengths),
+                _ptr(S0), _seq(o), _ptr(S), _ptr(_workspace(dev)), _handle(dev, stream))
+        if wait_limit_us or test_stall_producer:
+            st = lib.vla_delta_forward_ex(*args, _wait_options(wait_limit_us, test_stall_producer))
+        else:
+            st = lib.vla_delta_forward(*args)
     _done(st, "vla_delta_forward", dev, stream, check)
     return o, S
 
@@ -83,7 +91,8 @@ def vla_delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
 def vla_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: Optional[torch.Tensor],
                        beta: torch.Tensor, scale: float = 1.0, state: Optional[torch.Tensor] = None,
                        grad_o: Optional[torch.Tensor] = None, grad_state: Optional[torch.Tensor] = None, *,
-                       lengths: Optional[torch.Tensor] = None, out=None, stream=None, check: bool = False):
+                       lengths: Optional[torch.Tensor] = None, out=None, stream=None, check: bool = False,
+                       wait_limit_us: int = 0, test_stall_producer: bool = False):
     """Gradient of a scalar loss through vla_delta_forward (reverse mode).
 
     ``grad_o`` = dL/do like q and ``grad_state`` = dL/dS [B, H, d, d] float32
@@ -92,7 +101,8 @@ def vla_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
     like q, [B, H, T] float32 (dlog_decay None for a None log_decay), and
     float32 [B, H, d, d]. A gate that is expanded gets its gradient for each
     token, not their sum. ``out`` = (dq, dk, dv, dlog_decay, dbeta, dS0)
-    preallocated (dS0 neither ``state`` nor ``grad_state``).
+    preallocated (dS0 neither ``state`` nor ``grad_state``). ``wait_limit_us``
+    and ``test_stall_producer`` as in the forward call.
     """
     for name, x in (("q", q), ("k", k), ("v", v), ("grad_o", grad_o)):
         if x is not None:
@@ -129,10 +139,13 @@ def vla_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
         q, k, v, grad_o = (_seq_in(x) for x in (q, k, v, grad_o))
         nbytes = _scratch(_DTYPES[q.dtype], B, H, T, d)
         scratch = _call_buffer(dev, nbytes, False) if nbytes else None
-        st = lib.vla_delta_backward(_seq(q), _seq(k), _seq(v), _seq(grad_o), _DTYPES[q.dtype], B, H, T, d, _gate(g),
-                                    _gate(beta), scale, _ptr(lengths), _ptr(S0), _ptr(dS_T), *(_seq(x) for x in grads),
-                                    _gate(dg), _gate(db), _ptr(dS0), _ptr(scratch), nbytes, _ptr(_workspace(dev)),
-                                    _handle(dev, stream))
+        args = (_seq(q), _seq(k), _seq(v), _seq(grad_o), _DTYPES[q.dtype], B, H, T, d, _gate(g), _gate(beta), scale,
+                _ptr(lengths), _ptr(S0), _ptr(dS_T), *(_seq(x) for x in grads), _gate(dg), _gate(db), _ptr(dS0),
+                _ptr(scratch), nbytes, _ptr(_workspace(dev)), _handle(dev, stream))
+        if wait_limit_us or test_stall_producer:
+            st = lib.vla_delta_backward_ex(*args, _wait_options(wait_limit_us, test_stall_producer))
+        else:
+            st = lib.vla_delta_backward(*args)
     _done(st, "vla_delta_backward", dev, stream, check)
     return tuple(grads), (dg, db), dS0
 

@@ -3,7 +3,6 @@
 #include <cmath>
 #include <type_traits>
 
-#include "vla_delta_forward.cuh"
 #include "vla_delta_host.h"
 
 namespace vla_layer {
@@ -82,9 +81,9 @@ __global__ void __launch_bounds__(STEP_THREADS) vla_delta_step_kernel(const T* _
     if (bad != bad && status) vla::record_failure(status, vla::BIT_NONFINITE, 3, bh, 0);
 }
 
-template <int D, typename T>
-vla_status forward(DeltaArgs& p, cudaStream_t s) {
-    return delta_run<vla_delta_forward_kernel<D, T, false>, D, typename DeltaForward<D, T, false>::L>(p, s);
+void take_options(DeltaArgs& p, const vla_options* opts) {
+    p.wait_ns = 1000ull * (opts && opts->wait_limit_us ? opts->wait_limit_us : 2000000u);
+    p.stall = opts && opts->test_stall_producer;
 }
 
 }  // namespace
@@ -98,9 +97,10 @@ size_t vla_delta_scratch_bytes(vla_dtype dtype, int B, int H, int T, int d) {
     return delta_scratch(nullptr, nullptr, dtype, B, H, T, d);
 }
 
-vla_status vla_delta_forward(const vla_seq* q, const vla_seq* k, const vla_seq* v, vla_dtype dtype, int B, int H, int T,
-                             int d, const vla_gate* log_decay, const vla_gate* beta, float scale, const int* lengths,
-                             const float* S0, const vla_seq_out* o, float* S_out, void* status, void* stream) {
+vla_status vla_delta_forward_ex(const vla_seq* q, const vla_seq* k, const vla_seq* v, vla_dtype dtype, int B, int H, int T,
+                                int d, const vla_gate* log_decay, const vla_gate* beta, float scale, const int* lengths,
+                                const float* S0, const vla_seq_out* o, float* S_out, void* status, void* stream,
+                                const vla_options* opts) {
     using namespace vla_layer;
     if (!good_sizes(B, H, T) || !good_dtype(dtype) || !std::isfinite(scale)) return VLA_ERR_INVALID_ARG;
     if (!good_d(d)) return VLA_ERR_UNSUPPORTED;
@@ -128,15 +128,16 @@ vla_status vla_delta_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
     p.lengths = lengths;
     p.S0 = S0, p.S = S_out;
     p.status = static_cast<vla::DeviceStatus*>(status);
-    return delta_pick(dtype, d, [&](auto tag, auto dim) { return forward<decltype(dim)::value, decltype(tag)>(p, s); });
+    take_options(p, opts);
+    return delta_pick(dtype, d, [&](auto tag, auto dim) { return delta_forward_run<decltype(dim)::value, decltype(tag), false>(p, s); });
 }
 
-vla_status vla_delta_backward(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO, vla_dtype dtype,
-                              int B, int H, int T, int d, const vla_gate* log_decay, const vla_gate* beta, float scale,
-                              const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,
-                              const vla_seq_out* dk, const vla_seq_out* dv, const vla_gate_out* dlog_decay,
-                              const vla_gate_out* dbeta, float* dS0, void* scratch, size_t scratch_bytes, void* status,
-                              void* stream) {
+vla_status vla_delta_backward_ex(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO, vla_dtype dtype,
+                                 int B, int H, int T, int d, const vla_gate* log_decay, const vla_gate* beta, float scale,
+                                 const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,
+                                 const vla_seq_out* dk, const vla_seq_out* dv, const vla_gate_out* dlog_decay,
+                                 const vla_gate_out* dbeta, float* dS0, void* scratch, size_t scratch_bytes, void* status,
+                                 void* stream, const vla_options* opts) {
     using namespace vla_layer;
     if (!good_sizes(B, H, T) || !good_dtype(dtype) || !std::isfinite(scale)) return VLA_ERR_INVALID_ARG;
     if (!good_d(d)) return VLA_ERR_UNSUPPORTED;
@@ -171,8 +172,26 @@ vla_status vla_delta_backward(const vla_seq* q, const vla_seq* k, const vla_seq*
     p.lengths = lengths;
     p.S0 = S0, p.dS_T = dS_T, p.dS0 = dS0;
     p.status = static_cast<vla::DeviceStatus*>(status);
+    take_options(p, opts);
     delta_scratch(&p, scratch, dtype, B, H, T, d);
     return delta_backward_launch(p, dtype, d, s);
+}
+
+vla_status vla_delta_forward(const vla_seq* q, const vla_seq* k, const vla_seq* v, vla_dtype dtype, int B, int H, int T,
+                             int d, const vla_gate* log_decay, const vla_gate* beta, float scale, const int* lengths,
+                             const float* S0, const vla_seq_out* o, float* S_out, void* status, void* stream) {
+    return vla_delta_forward_ex(q, k, v, dtype, B, H, T, d, log_decay, beta, scale, lengths, S0, o, S_out, status, stream,
+                                nullptr);
+}
+
+vla_status vla_delta_backward(const vla_seq* q, const vla_seq* k, const vla_seq* v, const vla_seq* dO, vla_dtype dtype,
+                              int B, int H, int T, int d, const vla_gate* log_decay, const vla_gate* beta, float scale,
+                              const int* lengths, const float* S0, const float* dS_T, const vla_seq_out* dq,
+                              const vla_seq_out* dk, const vla_seq_out* dv, const vla_gate_out* dlog_decay,
+                              const vla_gate_out* dbeta, float* dS0, void* scratch, size_t scratch_bytes, void* status,
+                              void* stream) {
+    return vla_delta_backward_ex(q, k, v, dO, dtype, B, H, T, d, log_decay, beta, scale, lengths, S0, dS_T, dq, dk, dv,
+                                 dlog_decay, dbeta, dS0, scratch, scratch_bytes, status, stream, nullptr);
 }
 
 vla_status vla_delta_step(const void* q, const void* k, const void* v, vla_dtype dtype, int B, int H, int d,

@@ -56,6 +56,8 @@ struct DeltaArgs {
     int B, H, T;
     int rows;               // rows of S of a block
     vla::DeviceStatus* status;
+    unsigned long long wait_ns;
+    int stall;              // testing: the last chunk's loads are kept back
     // kept between the launches of a backward call
     float* E;               // [BH][T][d]
     float *before, *behind; // [BH][blocks + 1][d][d]: S before a block of tokens (the last one behind all), R behind it

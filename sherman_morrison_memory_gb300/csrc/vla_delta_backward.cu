@@ -1,6 +1,5 @@
 // vla_delta_backward.cu -- the launches of the gated delta rule's gradients.
 #include "vla_delta_backward.cuh"
-#include "vla_delta_forward.cuh"
 #include "vla_delta_host.h"
 
 namespace vla_layer {
@@ -8,7 +7,7 @@ namespace {
 
 template <int D, typename T>
 vla_status backward(DeltaArgs& p, cudaStream_t s) {
-    vla_status st = delta_run<vla_delta_forward_kernel<D, T, true>, D, typename DeltaForward<D, T, true>::L>(p, s);
+    vla_status st = delta_forward_run<D, T, true>(p, s);
     if (st != VLA_OK) return st;
     st = delta_run<vla_delta_reverse_kernel<D, T>, D, typename DeltaReverse<D, T>::L>(p, s);
     if (st != VLA_OK) return st;

@@ -4,6 +4,8 @@
 #include <type_traits>
 
 #include "vla_delta.cuh"
+#include "vla_delta_forward.cuh"
+#include "vla_delta_tc.cuh"
 
 namespace vla_layer {
 
@@ -62,6 +64,35 @@ inline vla_status delta_run(DeltaArgs& p, cudaStream_t s) {
     if (!allow_smem<K>(L::BYTES)) return VLA_ERR_CUDA;
     K<<<(unsigned)grid, p.rows * 4 + HELPERS, L::BYTES, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
+}
+
+// Tokens behind which a bf16 call's forward recurrence runs on tcgen05.
+constexpr int DELTA_TC = 64;
+
+template <int D, int R, bool TAPE>
+inline vla_status delta_tc_run(DeltaArgs& p, cudaStream_t s) {
+    using L = DeltaTc<D, R, TAPE>;
+    const long long grid = (long long)p.B * p.H * (D > R ? D / R : 1);
+    if (grid > 2147483647LL) return VLA_ERR_INVALID_ARG;
+    if (!allow_smem<vla_delta_tc_kernel<D, R, TAPE>>(L::BYTES)) return VLA_ERR_CUDA;
+    vla_delta_tc_kernel<D, R, TAPE><<<(unsigned)grid, L::THREADS, L::BYTES, s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
+}
+
+// The forward recurrence, or (TAPE) what its gradients need of it.
+template <int D, typename T, bool TAPE>
+inline vla_status delta_forward_run(DeltaArgs& p, cudaStream_t s) {
+    if constexpr (sizeof(T) == 2) {
+        if (p.T > DELTA_TC) {
+            if constexpr (D == 128) {
+                if ((long long)p.B * p.H * 2 > sm_count()) return delta_tc_run<128, 128, TAPE>(p, s);
+                return delta_tc_run<128, 64, TAPE>(p, s);
+            } else {
+                return delta_tc_run<D, D == 96 ? 128 : 64, TAPE>(p, s);
+            }
+        }
+    }
+    return delta_run<vla_delta_forward_kernel<D, T, TAPE>, D, typename DeltaForward<D, T, TAPE>::L>(p, s);
 }
 
 inline vla_status delta_copy_state(float* dst, const float* src, size_t n, cudaStream_t s) {

@@ -1,0 +1,630 @@
+// vla_delta_tc.cuh -- the gated delta rule over a sequence (vla_delta.cuh) on the
+// tcgen05 tensor cores, bf16 inputs: outputs and final state, or (TAPE) what its
+// gradients need of it. A block per head (R = 64 of d = 128: two) takes DC = 32
+// tokens at a time, its R rows of S on the TMEM lanes:
+//
+//   [X | Y][x][i] = sum_y S[x][y] [k_i | q_i][y]     A: S in three bf16 parts (Y: its first), TMEM
+//   Z[x][j]  = v_j[x] - exp(G_j) X[x][j]
+//   E[x][i]  = sum_j Z[x][j] Inv[i][j]               A: Z in three parts; Inv in three, six products
+//   T[x][y]  = sum_j (b_j exp(G_C - G_j) E[x][j]) k_j[y]    A: in three parts
+//   S        = exp(G_C) S + T                        fp32, in registers
+//   o_i[x]   = scale exp(G_i) Y[x][i] + sum_j b_j E[x][j] P[i][j]   A: b E in two parts
+//
+// The workers' fragments of S, Z and E are what tcgen05.ld and st move (16x256b,
+// 16x128b) and what ldmatrix gives of v, so that nothing but o and the helpers' small
+// matrices passes through shared memory.
+//
+// What bounds it: the chain S, X, Z, E, T, S of a chunk, three products that
+// wait for the workers and the workers for them. So S goes out and comes in by
+// pieces of its columns, the products of the first beside the work on the next,
+// and o is formed beside the next chunk's X.
+//
+// Warps: 0-7 S (a quarter of the lanes, a half of the columns and of the
+// tokens), 8 MMAs, 9 loads, 12-15 the helpers' part of a chunk ahead.
+// Every wait is bounded; one that runs out raises the block's abort flag.
+#pragma once
+
+#include "vla_delta.cuh"
+#include "vla_tcgen.cuh"
+
+namespace vla_layer {
+
+template <int D, int R, bool TAPE>
+struct DeltaTc {
+    static constexpr int NB = D > 64 ? 2 : 1, VB = R / 64;  // boxes of 64 columns x 32 tokens
+    static constexpr int BOX = DC * 128;
+    static constexpr int NST = 4;
+    // a stage: for each box of d, K and Q; V (and dO) at the block's rows
+    static constexpr int V = NB * 2 * BOX, O = V + VB * BOX, STAGE = O + (TAPE ? VB * BOX : 0);
+    static constexpr int PP = TAPE ? 3 : 1, UP = TAPE ? 3 : 2;  // parts of P and of b E
+    // a chunk's matrices, two of 64 columns: the inverse's parts 0 | 1, its 2 | P's 0, P's 1 | 2; gates
+    static constexpr int MATS = (TAPE ? 3 : 2) * BOX, PREP = MATS + 1024;
+    static constexpr int PREPS = NST * STAGE, N = PREPS + 2 * PREP, OUT = N + 2 * 16 * NLD * 4;
+    static constexpr int OUT_LD = 40;                      // elements of a row of a warp's staged outputs, 32 columns
+    static constexpr int BAR = OUT + 8 * 16 * OUT_LD * 2;
+    static constexpr int NBAR = NST + 2 * 2 + 8 + 2, MISC = BAR + NBAR * 8, BYTES = MISC + 16;
+    static_assert(BYTES <= 227 * 1024, "shared memory");
+    static constexpr int W = D / 2, NH = R / 64;           // a worker's columns, groups of 16 rows
+    static constexpr int PIECES = (W + 31) / 32;
+    // TMEM columns; E takes X's place once Z is made of it, and what T is made of Z's
+    static constexpr int SB = 0, ZP = SB + 3 * (D / 2), UPC = ZP + 48, X = UPC + UP * 16, OP = X + 64, TC = OP + 32, COLS = 512;
+    static_assert(TC + D <= COLS, "tensor memory");
+    static constexpr int THREADS = 512;
+    __host__ __device__ static constexpr int stage_of(int c) { return c % NST * STAGE; }  // the stage of a chunk
+};
+
+// Address of 16 bytes in a box: row `row`, group `j` of eight values
+__device__ __forceinline__ uint32_t in_box(int row, int j) { return (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4)); }
+
+// prepare_chunk() for tiles in boxes; matrices in rows of i.
+template <typename L, int D>
+__device__ __forceinline__ void prepare_boxes(char* sm, uint32_t stage, char* prep, float g, float beta, float scale, Whole& whole,
+                                              int hw, int lane) {
+    float Gh, Gl;
+    sums_of(g, lane, Gh, Gl);
+    if (hw == 3) {
+        const float all = __shfl_sync(0xffffffffu, Gh, 31), rest = __shfl_sync(0xffffffffu, Gl, 31);
+        float* gates = reinterpret_cast<float*>(prep + L::MATS);
+        gates[GATE_NEAR + lane] = expf(Gh + Gl);
+        gates[GATE_FAR + lane] = expf((all - Gh) + (rest - Gl));
+        gates[GATE_BETA + lane] = beta;
+        const float w = whole.next(all + rest);
+        if (lane == 0) gates[GATE_WHOLE] = w;
+        return;
+    }
+    const int mt = hw ? 1 : 0, np = hw == 2 ? 1 : 0;
+    const int down = lane & 15, across = (lane & 7) + ((lane >> 4) << 3);  // rows of a 16 x 16 block for its four 8 x 8 ones
+    float c[4][4] = {};  // K K^T, Q K^T
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t box = stage + (ks >> 2) * 2 * L::BOX;
+        uint32_t a[1][4], q[1][4], b[2][1][2];
+        const uint32_t at = in_box(mt * 16 + down, (ks & 3) * 2 + (lane >> 4));
+        ldsm(a[0], box + at);
+        ldsm(q[0], box + L::BOX + at);
+        ldsm_pair(b, 0, 0, box + in_box(np * 16 + across, (ks & 3) * 2 + ((lane >> 3) & 1)));
+        mma_tiles<1>(c, c, a, b);
+        mma_tiles<1>(c + 2, c + 2, q, b);
+    }
+    const int r = lane >> 2, t2 = (lane & 3) * 2;
+    float* N = reinterpret_cast<float*>(sm + L::N) + (hw >> 1) * 16 * NLD;  // transposed
+    auto part_at = [&](int part, int row, int j8) {  // eight values of a part of the inverse
+        return in_box(row, (part & 1) * 4 + j8) + (part >> 1) * L::BOX;
+    };
+    float x[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        const int j = np * 16 + n * 8 + t2;
+        float gj[2], lj[2], bj[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            gj[e] = __shfl_sync(0xffffffffu, Gh, j + e), lj[e] = __shfl_sync(0xffffffffu, Gl, j + e);
+            bj[e] = __shfl_sync(0xffffffffu, beta, j + e);
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int i = mt * 16 + hf * 8 + r;
+            const float gi = __shfl_sync(0xffffffffu, Gh, i), li = __shfl_sync(0xffffffffu, Gl, i);
+            float y[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float w = expf((gi - gj[e]) + (li - lj[e]));
+                x[n][2 * hf + e] = j + e < i ? c[n][2 * hf + e] * w * bj[e] : 0.f;
+                y[e] = j + e <= i ? c[2 + n][2 * hf + e] * w * scale : 0.f;
+                if (hw != 1) N[(n * 8 + t2 + e) * NLD + hf * 8 + r] = x[n][2 * hf + e];
+            }
+            uint32_t w[L::PP];
+            split<L::PP>(y[0], y[1], w);
+#pragma unroll
+            for (int p = 0; p < L::PP; ++p)  // behind the inverse's three parts
+                *reinterpret_cast<uint32_t*>(prep + part_at(3 + p, i, np * 2 + n) + t2 * 2) = w[p];
+        }
+    }
+    if (hw != 1) {
+        __syncwarp();
+        float t[16];
+        const int row = lane & 15;
+#pragma unroll
+        for (int j = 15; j >= 0; --j) {  // T (1 + N) = 1, a lane a row
+            float s = j == row ? 1.f : 0.f, s2 = 0.f;
+#pragma unroll
+            for (int m = j / 4 * 4; m < 16; m += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(N + j * NLD + m);
+                if (m > j) s2 = fmaf(-w.x, t[m], s2);
+                if (m + 1 > j) s = fmaf(-w.y, t[m + 1], s);
+                if (m + 2 > j) s2 = fmaf(-w.z, t[m + 2], s2);
+                if (m + 3 > j) s = fmaf(-w.w, t[m + 3], s);
+            }
+            t[j] = s + s2;
+        }
+        if (lane < 16) {
+            uint32_t w[8][INV_PARTS];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) split<INV_PARTS>(t[2 * i], t[2 * i + 1], w[i]);
+#pragma unroll
+            for (int p = 0; p < INV_PARTS; ++p) {
+                *reinterpret_cast<uint4*>(prep + part_at(p, mt * 16 + row, mt * 2)) = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+                *reinterpret_cast<uint4*>(prep + part_at(p, mt * 16 + row, mt * 2 + 1)) = make_uint4(w[4][p], w[5][p], w[6][p], w[7][p]);
+                // nothing above the diagonal
+                if (mt == 0) {
+                    *reinterpret_cast<uint4*>(prep + part_at(p, row, 2)) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(prep + part_at(p, row, 3)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            if (mt == 0)
+#pragma unroll
+                for (int p = 0; p < L::PP; ++p) {
+                    *reinterpret_cast<uint4*>(prep + part_at(3 + p, row, 2)) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(prep + part_at(3 + p, row, 3)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+        }
+    }
+    vla::named_bar(2, 96);
+    if (hw != 1) return;
+    // T21^T = -(T11^T N21^T) T22^T
+    uint32_t a[INV_PARTS][4], w[2][INV_PARTS][2];
+    const uint32_t inv = vla::smem_u32(prep);
+#pragma unroll
+    for (int p = 0; p < INV_PARTS; ++p) ldsm_t(a[p], inv + part_at(p, across, (lane >> 3) & 1));
+#pragma unroll
+    for (int n = 0; n < 2; ++n)  // eight rows of N21, their 16 values down
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t y[INV_PARTS];
+            split<INV_PARTS>(x[k][2 * n], x[k][2 * n + 1], y);
+#pragma unroll
+            for (int p = 0; p < INV_PARTS; ++p) w[n][p][k] = y[p];
+        }
+    float y[2][4] = {}, yl[2][4] = {}, z[2][4] = {}, zl[2][4] = {};
+    mma_tiles<INV_PARTS>(y, yl, a, w);
+    join(y, yl);
+    to_operand<INV_PARTS>(a, y[0], y[1]);
+#pragma unroll
+    for (int p = 0; p < INV_PARTS; ++p) ldsm_pair(w, 0, p, inv + part_at(p, 16 + across, 2 + ((lane >> 3) & 1)));
+    mma_tiles<INV_PARTS>(z, zl, a, w);
+    join(z, zl);
+    // its fragments are rows of j; blocks (j, i), (j + 8, i), (j, i + 8), (j + 8, i + 8) written as rows of i
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[p][e] = -z[p][e];
+    uint32_t v[4][INV_PARTS];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split<INV_PARTS>(z[i >> 1][(i & 1) * 2], z[i >> 1][(i & 1) * 2 + 1], v[i]);
+#pragma unroll
+    for (int p = 0; p < INV_PARTS; ++p) stsm_t(inv + part_at(p, 16 + across, (lane >> 3) & 1), v[0][p], v[1][p], v[2][p], v[3][p]);
+}
+
+// 16 lanes, NT tiles of eight 32-bit columns, as fragments
+template <int NT>
+__device__ __forceinline__ void ld_tiles(uint32_t at, float (*x)[4]) {
+    if constexpr (NT == 4) {
+        ld_frag32(at, *reinterpret_cast<float(*)[16]>(x));
+    } else {
+        ld_frag16(at, *reinterpret_cast<float(*)[8]>(x));
+    }
+}
+
+template <int D, int R, bool TAPE>
+__global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_constant__ DeltaArgs p) {
+    using T = __nv_bfloat16;
+    using L = DeltaTc<D, R, TAPE>;
+    constexpr int SPAN = BLOCK<T>, NH = L::NH, W = L::W, SPLITS = D > R ? D / R : 1;
+    extern __shared__ __align__(1024) char sm[];
+    const uint32_t sb = vla::smem_u32(sm);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
+    uint64_t *full = bar, *prep_ready = full + L::NST, *done = prep_ready + 2, *s_ready = done + 2, *x_done = s_ready + 2,
+             *z_ready = x_done + 1, *e_done = x_done + 2, *u_ready = x_done + 3, *t_done = x_done + 4, *o_done = x_done + 5,
+             *drained = x_done + 6;
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC + 4);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int bh = blockIdx.x / SPLITS, row0 = blockIdx.x % SPLITS * R, b = bh / p.H, h = bh % p.H;
+    const int rows = min(R, D - row0);
+    const long long n = delta_len(p, b);
+    const int chunks = (int)((n + DC - 1) / DC);
+
+    for (int i = tid; i < L::NST * L::STAGE / 16; i += L::THREADS)  // columns that no load fills stay zero
+        *reinterpret_cast<uint4*>(sm + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) {
+        for (int i = 0; i < L::NST; ++i) vla::mbar_init(full + i, 1);
+        for (int i = 0; i < 2; ++i) {
+            vla::mbar_init(prep_ready + i, 4);
+            vla::mbar_init(done + i, 8);
+            vla::mbar_init(s_ready + i, 8);
+        }
+        vla::mbar_init(x_done, 1);
+        vla::mbar_init(z_ready, 8);
+        vla::mbar_init(e_done, 1);
+        vla::mbar_init(u_ready, 8);
+        vla::mbar_init(t_done, 1);
+        vla::mbar_init(o_done, 1);
+        vla::mbar_init(drained, 1);
+        *abort_flag = 0;
+        vla::fence_mbar_init();
+    }
+    if (warp == 8) vla::tc_alloc(tmem_ptr, L::COLS);
+    vla::fence_proxy_async_smem();
+    vla::tc_fence_before();
+    __syncthreads();
+    vla::tc_fence_after();
+    const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_ptr, 0);
+    float bad = 0.f;
+
+    auto wait_warp = [&](uint64_t* w, uint32_t parity) {
+        if (__all_sync(0xffffffffu, vla::mbar_try_wait(w, parity & 1))) return true;
+        const bool ok = wait_on(w, parity & 1, abort_flag, p.wait_ns, p.status, warp / 4, bh);
+        return __all_sync(0xffffffffu, ok) != 0;
+    };
+    auto arrive_warp = [&](uint64_t* w) {  // one arrival a warp
+        __syncwarp();
+        if (lane == 0) vla::mbar_arrive(w);
+    };
+
+    if (warp == 8) {  // ---- MMAs, issued by one lane of a whole warp
+        const bool one = elect_one();
+        const uint32_t id64 = idesc_bf16(R, 64, 0, 0), id32 = idesc_bf16(R, 32, 0, 0), id_t = idesc_bf16(R, D, 0, 1);
+        const uint64_t dk = desc_sw128(0, 16, 1024), dm = desc_sw128(0, L::NB == 2 ? 2 * L::BOX : 16, 1024);
+        auto at = [](uint64_t d, uint32_t addr) { return d + (uint64_t)(addr >> 4); };
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t st = sb + L::stage_of(c), pr = sb + L::PREPS + (c & 1) * L::PREP;
+            if (!wait_warp(full + c % L::NST, c / L::NST)) break;
+            bool ok = true;
+#pragma unroll
+            for (int q = 0; q < L::PIECES; ++q) {
+                if (!(ok = wait_warp(s_ready + q, c))) break;
+                vla::tc_fence_after();
+                if (one) {
+#pragma unroll
+                    for (int part = 0; part < 3; ++part)
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            if (ks % (W / 16) / 2 != q) continue;
+                            mma_ts(tm + L::X, tm + L::SB + part * (D / 2) + ks * 8, at(dk, st + (ks >> 2) * 2 * L::BOX + (ks & 3) * 32),
+                                   part == 0 || TAPE ? id64 : id32, q > 0 || part > 0 || ks > 0);
+                        }
+                    if (q + 1 == L::PIECES) vla::tc_commit(x_done);
+                }
+                __syncwarp();
+            }
+            if (!ok || !wait_warp(prep_ready + (c & 1), c / 2) || !wait_warp(z_ready, c)) break;
+            vla::tc_fence_after();
+            if (one) {
+#pragma unroll
+                for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                    for (int q = 0; q <= sum; ++q)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            mma_ts(tm + L::X, tm + L::ZP + (sum - q) * 16 + k * 8, at(dk, pr + (q & 1) * 64 + (q >> 1) * L::BOX + k * 32), id32,
+                                   !(sum == 2 && q == 0 && k == 0));
+                vla::tc_commit(e_done);
+            }
+            __syncwarp();
+            if (!wait_warp(u_ready, c)) break;
+            vla::tc_fence_after();
+            if (one) {
+#pragma unroll
+                for (int part = 2; part >= 0; --part)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        mma_ts(tm + L::TC, tm + L::ZP + part * 16 + k * 8, at(dm, st + k * 2048), id_t, !(part == 2 && k == 0));
+                vla::tc_commit(t_done);
+#pragma unroll
+                for (int part = L::UP - 1; part >= 0; --part)
+#pragma unroll
+                    for (int q = 0; q < L::PP; ++q) {
+                        if (part + q >= L::UP) continue;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            mma_ts(tm + L::OP, tm + L::UPC + part * 16 + k * 8,
+                                   at(dk, pr + ((3 + q) & 1) * 64 + ((3 + q) >> 1) * L::BOX + k * 32), id32,
+                                   !(part == L::UP - 1 && q == 0 && k == 0));
+                    }
+                vla::tc_commit(o_done);
+            }
+            __syncwarp();
+        }
+        if (one) vla::tc_commit(drained);  // what was issued has finished before the block frees its TMEM
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, vla::mbar_try_wait(drained, 0))) vla::mbar_wait_slow(drained, 0, nullptr, p.wait_ns);
+        __syncwarp();
+    } else if (warp == 9) {  // ---- loads, two chunks under way behind the one that is waited for
+        auto load = [&](int c) {
+            if (c < chunks && !(p.stall && c + 1 == chunks)) {
+                const long long t0 = (long long)c * DC;
+                const int live = (int)min((long long)DC, n - t0);
+                auto tile = [&](uint32_t dst, int box_step, const Seq& s, int col0, int cols) {
+                    const int wide = cols <= 32 ? 2 : cols <= 64 ? 3 : 4, g8 = lane & ((1 << wide) - 1);
+                    if (g8 * 8 >= cols) return;
+                    const T* src = row_of<T>(s, b, h, t0) + col0 + g8 * 8;
+                    dst += (g8 >> 3) * box_step;
+#pragma unroll 4
+                    for (int r = lane >> wide; r < DC; r += 32 >> wide)
+                        cp_async16(dst + in_box(r, g8 & 7), r < live ? src + r * s.st : src, r < live ? 16 : 0);
+                };
+                const uint32_t st = sb + L::stage_of(c);
+                tile(st, 2 * L::BOX, p.k, 0, D);
+                tile(st + L::BOX, 2 * L::BOX, p.q, 0, D);
+                tile(st + L::V, L::BOX, p.v, row0, rows);
+                if constexpr (TAPE) tile(st + L::O, L::BOX, p.dO, row0, rows);
+            }
+            cp_async_commit();
+        };
+        load(0);
+        load(1);
+        for (int c = 0; c < chunks; ++c) {
+            if (c + 2 >= L::NST && c + 2 < chunks && !wait_warp(done + ((c + 2) & 1), (c + 2 - L::NST) / 2)) break;
+            load(c + 2);
+            cp_async_wait<2>();
+            vla::fence_proxy_async_smem();
+            if (!(p.stall && c + 1 == chunks)) arrive_warp(full + c % L::NST);
+        }
+        cp_async_wait<0>();
+    } else if (warp >= 12) {  // ---- the helpers' part
+        const int hw = warp - 12;
+        Whole whole;
+        float g = 0.f, beta = 0.f;
+        auto gates = [&](int c) {
+            const long long t = (long long)c * DC + lane;
+            g = t < n && p.g.p ? *p.g.at(b, h, t) : 0.f;
+            beta = t < n ? *p.beta.at(b, h, t) : 0.f;
+        };
+        gates(0);
+        for (int c = 0; c < chunks; ++c) {
+            const float gc = g, bc = beta;
+            gates(c + 1);
+            // the three warps that meet at a barrier leave together if a wait ran out
+            const bool ok = wait_warp(full + c % L::NST, c / L::NST) && (c < 2 || wait_warp(done + (c & 1), c / 2 - 1));
+            if (vla::bar_red_or(1, HELPERS, !ok)) break;
+            prepare_boxes<L, D>(sm, sb + L::stage_of(c), sm + L::PREPS + (c & 1) * L::PREP, gc, bc, p.scale, whole, hw, lane);
+            vla::fence_proxy_async_smem();
+            arrive_warp(prep_ready + (c & 1));
+        }
+    } else if (warp < 8) {  // ---- S
+        const int quad = warp & 3, half = warp >> 2, r = lane >> 2, t2 = (lane & 3) * 2;
+        const int xb = quad * (R / 4);                      // first row of the warp's in the block
+        const bool rows_in = xb < rows;                     // else zero throughout
+        const uint32_t lanes = tm + ((uint32_t)(quad * 32) << 16);
+        auto lane16 = [&](int hh) { return lanes + ((uint32_t)(hh * 16) << 16); };
+        float s[NH][W / 8][4];
+#pragma unroll
+        for (int hh = 0; hh < NH; ++hh)
+            load_rows<D, W>(s[hh], p.S0 && rows_in ? p.S0 + ((size_t)bh * D + row0 + xb + hh * 16) * D + half * W : nullptr, lane);
+        char* stage = sm + L::OUT + warp * 16 * L::OUT_LD * 2;
+        // a piece of S in three parts
+        auto publish = [&](int q, int hh) {
+            constexpr int NT = W % 32 == 0 ? 4 : 2;
+#pragma unroll
+            for (int k0 = 0; k0 < 4; k0 += NT) {
+                if (q * 4 + k0 >= W / 8) continue;
+                uint32_t v[3][2 * NT];
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t y[3];
+                        split<3>(s[hh][q * 4 + k0 + k][2 * e], s[hh][q * 4 + k0 + k][2 * e + 1], y);
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) v[i][2 * k + e] = y[i];
+                    }
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const uint32_t to = lane16(hh) + L::SB + i * (D / 2) + half * (W / 2) + (q * 4 + k0) * 4;
+                    if constexpr (NT == 4)
+                        st_frag8(to, *reinterpret_cast<const uint32_t(*)[8]>(v[i]));
+                    else
+                        st_frag4(to, v[i][0], v[i][1], v[i][2], v[i][3]);
+                }
+            }
+        };
+        auto ready = [&](uint64_t* w) {
+            vla::tc_wait_st();
+            vla::tc_fence_before();
+            arrive_warp(w);
+        };
+        auto parts16 = [&](auto nc, uint32_t col, const float (&x)[2][4]) {  // 16 rows x 16 tokens
+            constexpr int N = decltype(nc)::value;
+            uint32_t y[4][N];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split<N>(x[i >> 1][(i & 1) * 2], x[i >> 1][(i & 1) * 2 + 1], y[i]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) st_frag4(col + i * 16 + half * 8, y[0][i], y[1][i], y[2][i], y[3][i]);
+        };
+        if (chunks > 0) {
+#pragma unroll
+            for (int q = 0; q < L::PIECES; ++q) {
+                __syncwarp();
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) publish(q, hh);
+                ready(s_ready + q);
+            }
+        }
+        bool ok = true;
+        for (int c = 0; c < chunks; ++c) {
+            const long long t0 = (long long)c * DC, h0 = t0 + half * 16;
+            if constexpr (TAPE) {
+                if (t0 % SPAN == 0 && rows_in)
+#pragma unroll
+                    for (int hh = 0; hh < NH; ++hh)
+                        store_rows<D, W>(s[hh], p.before + (((size_t)bh * (p.blocks + 1) + t0 / SPAN) * D + row0 + xb + hh * 16) * D + half * W, lane);
+            }
+            const float* gates = reinterpret_cast<const float*>(sm + L::PREPS + (c & 1) * L::PREP + L::MATS) + half * 16;
+            const uint32_t st = sb + L::stage_of(c);
+            // this warp's 16 columns of a tile at its 16 tokens
+            auto columns = [&](int tile, int hh, float (&x)[2][4]) {
+                const int g16 = xb / 16 + hh;
+                uint32_t w[4];
+                ldsm_t(w, st + tile + (g16 >> 2) * L::BOX +
+                              in_box(half * 16 + (lane & 7) + ((lane >> 4) << 3), (g16 & 3) * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    x[i][0] = low_of(w[2 * i]), x[i][1] = high_of(w[2 * i]), x[i][2] = low_of(w[2 * i + 1]), x[i][3] = high_of(w[2 * i + 1]);
+            };
+            if (!(ok = wait_warp(prep_ready + (c & 1), c / 2) && wait_warp(full + c % L::NST, c / L::NST))) break;
+            float2 near[2], far[2], beta[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                near[i] = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + t2);
+                far[i] = *reinterpret_cast<const float2*>(gates + GATE_FAR + i * 8 + t2);
+                beta[i] = *reinterpret_cast<const float2*>(gates + GATE_BETA + i * 8 + t2);
+            }
+            const float whole = gates[GATE_WHOLE - half * 16];
+            float v[NH][2][4], o[NH][2][4];
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) columns(L::V, hh, v[hh]);
+            if (!(ok = wait_warp(x_done, c))) break;
+            vla::tc_fence_after();
+            __syncwarp();
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                float x[2][4];
+                ld_tiles<2>(lane16(hh) + L::X + half * 16, x);
+                vla::tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[i][e] = fmaf(-(e & 1 ? near[i].y : near[i].x), x[i][e], v[hh][i][e]);
+                parts16(std::integral_constant<int, 3>{}, lane16(hh) + L::ZP, x);
+            }
+            ready(z_ready);
+            __syncwarp();
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                ld_tiles<2>(lane16(hh) + L::X + 32 + half * 16, o[hh]);
+                vla::tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[hh][i][e] *= p.scale * (e & 1 ? near[i].y : near[i].x);
+            }
+            if (!(ok = wait_warp(e_done, c))) break;
+            vla::tc_fence_after();
+            __syncwarp();
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                float u[2][4], f[2][4];
+                ld_tiles<2>(lane16(hh) + L::X + half * 16, u);
+                vla::tc_wait_ld();
+                if constexpr (TAPE) {
+                    if (rows_in) {
+                        float* E = p.E + ((size_t)bh * p.T + h0) * D + row0 + xb + hh * 16 + r;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int j = i * 8 + t2 + (e & 1);
+                                if (h0 + j < n) E[(size_t)j * D + (e & 2) * 4] = u[i][e];
+                            }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        u[i][e] *= e & 1 ? beta[i].y : beta[i].x;
+                        f[i][e] = u[i][e] * (e & 1 ? far[i].y : far[i].x);
+                    }
+                parts16(std::integral_constant<int, 3>{}, lane16(hh) + L::ZP, f);
+                parts16(std::integral_constant<int, L::UP>{}, lane16(hh) + L::UPC, u);
+            }
+            ready(u_ready);
+            if (!(ok = wait_warp(t_done, c))) break;
+            vla::tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < L::PIECES; ++q) {
+                constexpr int NT = W % 32 == 0 ? 4 : 2;
+                __syncwarp();
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+                    float y[4][4];
+#pragma unroll
+                    for (int k0 = 0; k0 < 4; k0 += NT)
+                        if (q * 4 + k0 < W / 8) ld_tiles<NT>(lane16(hh) + L::TC + half * W + (q * 4 + k0) * 8, y + k0);
+                    vla::tc_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (q * 4 + k < W / 8) s[hh][q * 4 + k][e] = fmaf(whole, s[hh][q * 4 + k][e], y[k][e]);
+                    if (c + 1 < chunks) publish(q, hh);
+                }
+                if (c + 1 < chunks) ready(s_ready + q);
+            }
+            if (!(ok = wait_warp(o_done, c))) break;
+            vla::tc_fence_after();
+            __syncwarp();
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                float x[2][4];
+                ld_tiles<2>(lane16(hh) + L::OP + half * 16, x);
+                vla::tc_wait_ld();
+                join(o[hh], x);
+            }
+            vla::tc_fence_before();
+            if constexpr (TAPE) {
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+                    float d[2][4];
+                    columns(L::O, hh, d);
+                    float* od = p.od + ((size_t)bh * (D / 16) + (row0 + xb) / 16 + hh) * p.T + h0;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float y = over_rows(fmaf(o[hh][i][e], d[i][e], o[hh][i][2 + e] * d[i][2 + e]));
+                            if (lane < 4 && rows_in && h0 + i * 8 + t2 + e < n) od[i * 8 + t2 + e] = y;
+                        }
+                }
+            } else if (rows_in) {
+                // rows of tokens through the warp's buffer: 16 or 32 values of each
+                __syncwarp();
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (h0 + i * 8 + t2 + (e & 1) < n) bad = fmaf(o[hh][i][e], 0.f, bad);
+                    stsm_t(vla::smem_u32(stage) + (across_down<L::OUT_LD>(lane) + hh * 16) * 2, pack_bf16(o[hh][0][0], o[hh][0][1]),
+                           pack_bf16(o[hh][0][2], o[hh][0][3]), pack_bf16(o[hh][1][0], o[hh][1][1]), pack_bf16(o[hh][1][2], o[hh][1][3]));
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < NH; ++k) {
+                    const int i = k * 32 + lane, row = i / (2 * NH), col = i % (2 * NH) * 8;
+                    const long long t = h0 + row;
+                    if (t >= p.T) continue;
+                    uint4 w = *reinterpret_cast<const uint4*>(stage + (row * L::OUT_LD + col) * 2);
+                    if (t >= n) w = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>(row_of<T>(p.out, b, h, t) + row0 + xb + col) = w;
+                }
+            }
+            arrive_warp(done + (c & 1));
+        }
+        if (ok && rows_in) {
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) {
+                float* to = TAPE ? p.before + ((size_t)bh * (p.blocks + 1) + (n + SPAN - 1) / SPAN) * D * D : p.S + (size_t)bh * D * D;
+                store_rows<D, W>(s[hh], to + (size_t)(row0 + xb + hh * 16) * D + half * W, lane);
+                if constexpr (!TAPE) {
+#pragma unroll
+                    for (int m = 0; m < W / 8; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) bad = fmaf(s[hh][m][e], 0.f, bad);
+                }
+            }
+        }
+    }
+    if constexpr (!TAPE) zero_tokens<T>(p.out, b, h, (long long)chunks * DC, p.T, row0, rows);
+    if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, 0);
+    vla::tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        vla::tc_fence_after();
+        vla::tc_dealloc(tm, L::COLS);
+    }
+}
+
+}  // namespace vla_layer
