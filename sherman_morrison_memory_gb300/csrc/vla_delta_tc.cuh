@@ -39,10 +39,11 @@ struct DeltaTc {
     static constexpr int PP = TAPE ? 3 : 1, UP = TAPE ? 3 : 2;  // parts of P and of b E
     // a chunk's matrices, two of 64 columns: the inverse's parts 0 | 1, its 2 | P's 0, P's 1 | 2; gates
     static constexpr int MATS = (TAPE ? 3 : 2) * BOX, PREP = MATS + 1024;
-    static constexpr int PREPS = NST * STAGE, N = PREPS + 2 * PREP, OUT = N + 2 * 16 * NLD * 4;
+    static constexpr int NPR = 3;  // chunks' matrices: a chunk's are free once the next one's Z is out
+    static constexpr int PREPS = NST * STAGE, N = PREPS + NPR * PREP, OUT = N + 2 * 16 * NLD * 4;
     static constexpr int OUT_LD = 40;                      // elements of a row of a warp's staged outputs, 32 columns
     static constexpr int BAR = OUT + 8 * 16 * OUT_LD * 2;
-    static constexpr int NBAR = NST + 2 * 2 + 8 + 2, MISC = BAR + NBAR * 8, BYTES = MISC + 16;
+    static constexpr int NBAR = NST + 2 * NPR + 10, MISC = BAR + NBAR * 8, BYTES = MISC + 16;
     static_assert(BYTES <= 227 * 1024, "shared memory");
     static constexpr int W = D / 2, NH = R / 64;           // a worker's columns, groups of 16 rows
     static constexpr int PIECES = (W + 31) / 32;
@@ -213,9 +214,9 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
     extern __shared__ __align__(1024) char sm[];
     const uint32_t sb = vla::smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
-    uint64_t *full = bar, *prep_ready = full + L::NST, *done = prep_ready + 2, *s_ready = done + 2, *x_done = s_ready + 2,
-             *z_ready = x_done + 1, *e_done = x_done + 2, *u_ready = x_done + 3, *t_done = x_done + 4, *o_done = x_done + 5,
-             *drained = x_done + 6;
+    uint64_t *full = bar, *prep_ready = full + L::NST, *done = prep_ready + L::NPR, *s_ready = done + L::NPR, *x_done = s_ready + 2,
+             *z_ready = x_done + 1, *e_done = x_done + 2, *f_ready = x_done + 3, *t_done = x_done + 4, *u_ready = x_done + 5,
+             *o_done = x_done + 6, *drained = x_done + 7;
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC + 4);
 
@@ -229,14 +230,12 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
         *reinterpret_cast<uint4*>(sm + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) {
         for (int i = 0; i < L::NST; ++i) vla::mbar_init(full + i, 1);
-        for (int i = 0; i < 2; ++i) {
-            vla::mbar_init(prep_ready + i, 4);
-            vla::mbar_init(done + i, 8);
-            vla::mbar_init(s_ready + i, 8);
-        }
+        for (int i = 0; i < L::NPR; ++i) vla::mbar_init(prep_ready + i, 4), vla::mbar_init(done + i, 8);
+        for (int i = 0; i < 2; ++i) vla::mbar_init(s_ready + i, 8);
         vla::mbar_init(x_done, 1);
         vla::mbar_init(z_ready, 8);
         vla::mbar_init(e_done, 1);
+        vla::mbar_init(f_ready, 8);
         vla::mbar_init(u_ready, 8);
         vla::mbar_init(t_done, 1);
         vla::mbar_init(o_done, 1);
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
         const uint64_t dk = desc_sw128(0, 16, 1024), dm = desc_sw128(0, L::NB == 2 ? 2 * L::BOX : 16, 1024);
         auto at = [](uint64_t d, uint32_t addr) { return d + (uint64_t)(addr >> 4); };
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t st = sb + L::stage_of(c), pr = sb + L::PREPS + (c & 1) * L::PREP;
+            const uint32_t st = sb + L::stage_of(c), pr = sb + L::PREPS + c % L::NPR * L::PREP;
             if (!wait_warp(full + c % L::NST, c / L::NST)) break;
             bool ok = true;
 #pragma unroll
@@ -288,7 +287,7 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
                 }
                 __syncwarp();
             }
-            if (!ok || !wait_warp(prep_ready + (c & 1), c / 2) || !wait_warp(z_ready, c)) break;
+            if (!ok || !wait_warp(prep_ready + c % L::NPR, c / L::NPR) || !wait_warp(z_ready, c)) break;
             vla::tc_fence_after();
             if (one) {
 #pragma unroll
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
                 vla::tc_commit(e_done);
             }
             __syncwarp();
-            if (!wait_warp(u_ready, c)) break;
+            if (!wait_warp(f_ready, c)) break;
             vla::tc_fence_after();
             if (one) {
 #pragma unroll
@@ -311,6 +310,11 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
                     for (int k = 0; k < 2; ++k)
                         mma_ts(tm + L::TC, tm + L::ZP + part * 16 + k * 8, at(dm, st + k * 2048), id_t, !(part == 2 && k == 0));
                 vla::tc_commit(t_done);
+            }
+            __syncwarp();
+            if (!wait_warp(u_ready, c)) break;
+            vla::tc_fence_after();
+            if (one) {
 #pragma unroll
                 for (int part = L::UP - 1; part >= 0; --part)
 #pragma unroll
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
         __syncwarp();
         if (!__all_sync(0xffffffffu, vla::mbar_try_wait(drained, 0))) vla::mbar_wait_slow(drained, 0, nullptr, p.wait_ns);
         __syncwarp();
-    } else if (warp == 9) {  // ---- loads, two chunks under way behind the one that is waited for
+    } else if (warp == 9) {  // ---- loads, a chunk under way behind the one that is waited for
         auto load = [&](int c) {
             if (c < chunks && !(p.stall && c + 1 == chunks)) {
                 const long long t0 = (long long)c * DC;
@@ -355,11 +359,11 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
         load(0);
         load(1);
         for (int c = 0; c < chunks; ++c) {
-            if (c + 2 >= L::NST && c + 2 < chunks && !wait_warp(done + ((c + 2) & 1), (c + 2 - L::NST) / 2)) break;
-            load(c + 2);
-            cp_async_wait<2>();
+            cp_async_wait<1>();
             vla::fence_proxy_async_smem();
             if (!(p.stall && c + 1 == chunks)) arrive_warp(full + c % L::NST);
+            if (c + 2 >= L::NST && c + 2 < chunks && !wait_warp(done + (c + 2 - L::NST) % L::NPR, (c + 2 - L::NST) / L::NPR)) break;
+            load(c + 2);
         }
         cp_async_wait<0>();
     } else if (warp >= 12) {  // ---- the helpers' part
@@ -376,11 +380,11 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
             const float gc = g, bc = beta;
             gates(c + 1);
             // the three warps that meet at a barrier leave together if a wait ran out
-            const bool ok = wait_warp(full + c % L::NST, c / L::NST) && (c < 2 || wait_warp(done + (c & 1), c / 2 - 1));
+            const bool ok = wait_warp(full + c % L::NST, c / L::NST) && (c < L::NPR || wait_warp(done + c % L::NPR, c / L::NPR - 1));
             if (vla::bar_red_or(1, HELPERS, !ok)) break;
-            prepare_boxes<L, D>(sm, sb + L::stage_of(c), sm + L::PREPS + (c & 1) * L::PREP, gc, bc, p.scale, whole, hw, lane);
+            prepare_boxes<L, D>(sm, sb + L::stage_of(c), sm + L::PREPS + c % L::NPR * L::PREP, gc, bc, p.scale, whole, hw, lane);
             vla::fence_proxy_async_smem();
-            arrive_warp(prep_ready + (c & 1));
+            arrive_warp(prep_ready + c % L::NPR);
         }
     } else if (warp < 8) {  // ---- S
         const int quad = warp & 3, half = warp >> 2, r = lane >> 2, t2 = (lane & 3) * 2;
@@ -441,168 +445,210 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
                 ready(s_ready + q);
             }
         }
+        // this warp's 16 columns of a chunk's tile at its 16 tokens
+        auto columns = [&](int c, int tile, int hh, float (&x)[2][4]) {
+            const int g16 = xb / 16 + hh;
+            uint32_t w[4];
+            ldsm_t(w, sb + L::stage_of(c) + tile + (g16 >> 2) * L::BOX +
+                          in_box(half * 16 + (lane & 7) + ((lane >> 4) << 3), (g16 & 3) * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                x[i][0] = low_of(w[2 * i]), x[i][1] = high_of(w[2 * i]), x[i][2] = low_of(w[2 * i + 1]), x[i][3] = high_of(w[2 * i + 1]);
+        };
+        float o[NH][2][4];
+        // Chunk c's outputs, from its share of the state in o and of the pairs: to the warp's buffer, or (TAPE) o . dO
+        const T* dst = TAPE ? nullptr : row_of<T>(p.out, b, h, half * 16 + lane / (2 * NH)) + row0 + xb + lane % (2 * NH) * 8;
+        float* od = TAPE ? p.od + ((size_t)bh * (D / 16) + (row0 + xb) / 16) * p.T + half * 16 : nullptr;
+        auto output = [&](int c) {
+            const int live = (int)min(16LL, n - (long long)c * DC - half * 16);
+            if (!wait_warp(o_done, c)) return false;
+            vla::tc_fence_after();
+            __syncwarp();
+            float x[NH][2][4];
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) ld_tiles<2>(lane16(hh) + L::OP + half * 16, x[hh]);
+            vla::tc_wait_ld();
+            vla::tc_fence_before();
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh) join(o[hh], x[hh]);
+            if constexpr (TAPE) {
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+                    float d[2][4];
+                    columns(c, L::O, hh, d);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float y = over_rows(fmaf(o[hh][i][e], d[i][e], o[hh][i][2 + e] * d[i][2 + e]));
+                            if (lane < 4 && rows_in && i * 8 + t2 + e < live) od[(size_t)hh * p.T + (size_t)c * DC + i * 8 + t2 + e] = y;
+                        }
+                }
+            } else {
+                if (live < 16)
+#pragma unroll
+                    for (int hh = 0; hh < NH; ++hh)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (i * 8 + t2 + (e & 1) >= live) o[hh][i][e] = 0.f;
+                __syncwarp();
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) bad = fmaf(o[hh][i][e], 0.f, bad);
+                    stsm_t(vla::smem_u32(stage) + (across_down<L::OUT_LD>(lane) + hh * 16) * 2, pack_bf16(o[hh][0][0], o[hh][0][1]),
+                           pack_bf16(o[hh][0][2], o[hh][0][3]), pack_bf16(o[hh][1][0], o[hh][1][1]), pack_bf16(o[hh][1][2], o[hh][1][3]));
+                }
+                __syncwarp();
+            }
+            arrive_warp(done + c % L::NPR);
+            return true;
+        };
+        // ... and from there to their rows: 16 or 32 values of each token, up to T
+        auto write_out = [&](int c) {
+            if constexpr (!TAPE) {
+                const int in = rows_in ? (int)min(16LL, p.T - (long long)c * DC - half * 16) : 0;
+#pragma unroll
+                for (int k = 0; k < NH; ++k) {
+                    const int row = lane / (2 * NH) + k * (16 / NH), col = lane % (2 * NH) * 8;
+                    if (row < in)
+                        *reinterpret_cast<uint4*>(const_cast<T*>(dst) + ((long long)c * DC + k * (16 / NH)) * p.out.st) =
+                            *reinterpret_cast<const uint4*>(stage + (row * L::OUT_LD + col) * 2);
+                }
+            }
+        };
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
-            const long long t0 = (long long)c * DC, h0 = t0 + half * 16;
+            const long long t0 = (long long)c * DC;
             if constexpr (TAPE) {
                 if (t0 % SPAN == 0 && rows_in)
 #pragma unroll
                     for (int hh = 0; hh < NH; ++hh)
                         store_rows<D, W>(s[hh], p.before + (((size_t)bh * (p.blocks + 1) + t0 / SPAN) * D + row0 + xb + hh * 16) * D + half * W, lane);
             }
-            const float* gates = reinterpret_cast<const float*>(sm + L::PREPS + (c & 1) * L::PREP + L::MATS) + half * 16;
-            const uint32_t st = sb + L::stage_of(c);
-            // this warp's 16 columns of a tile at its 16 tokens
-            auto columns = [&](int tile, int hh, float (&x)[2][4]) {
-                const int g16 = xb / 16 + hh;
-                uint32_t w[4];
-                ldsm_t(w, st + tile + (g16 >> 2) * L::BOX +
-                              in_box(half * 16 + (lane & 7) + ((lane >> 4) << 3), (g16 & 3) * 2 + ((lane >> 3) & 1)));
+            const float* gates = reinterpret_cast<const float*>(sm + L::PREPS + c % L::NPR * L::PREP + L::MATS) + half * 16;
+            if (!(ok = wait_warp(prep_ready + c % L::NPR, c / L::NPR))) break;  // behind its loads
+            float2 near[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    x[i][0] = low_of(w[2 * i]), x[i][1] = high_of(w[2 * i]), x[i][2] = low_of(w[2 * i + 1]), x[i][3] = high_of(w[2 * i + 1]);
-            };
-            if (!(ok = wait_warp(prep_ready + (c & 1), c / 2) && wait_warp(full + c % L::NST, c / L::NST))) break;
-            float2 near[2], far[2], beta[2];
+            for (int i = 0; i < 2; ++i) near[i] = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + t2);
+            const float whole = gates[GATE_WHOLE - half * 16];
+            {
+                float v[NH][2][4];
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) columns(c, L::V, hh, v[hh]);
+                if (c > 1) write_out(c - 2);
+                if (!(ok = wait_warp(x_done, c))) break;
+                vla::tc_fence_after();
+                __syncwarp();
+                float x[NH][2][4];
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) ld_tiles<2>(lane16(hh) + L::X + half * 16, x[hh]);
+                vla::tc_wait_ld();
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[hh][i][e] = fmaf(-(e & 1 ? near[i].y : near[i].x), x[hh][i][e], v[hh][i][e]);
+                    parts16(std::integral_constant<int, 3>{}, lane16(hh) + L::ZP, x[hh]);
+                }
+            }
+            ready(z_ready);
+            float2 far[2], beta[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                near[i] = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + t2);
                 far[i] = *reinterpret_cast<const float2*>(gates + GATE_FAR + i * 8 + t2);
                 beta[i] = *reinterpret_cast<const float2*>(gates + GATE_BETA + i * 8 + t2);
             }
-            const float whole = gates[GATE_WHOLE - half * 16];
-            float v[NH][2][4], o[NH][2][4];
-#pragma unroll
-            for (int hh = 0; hh < NH; ++hh) columns(L::V, hh, v[hh]);
-            if (!(ok = wait_warp(x_done, c))) break;
+            if (c > 0 && !(ok = output(c - 1))) break;  // beside the products of E: the chunk before's outputs
+            if (!(ok = wait_warp(e_done, c))) break;
             vla::tc_fence_after();
             __syncwarp();
+            {
+                float u[NH][2][4];
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                float x[2][4];
-                ld_tiles<2>(lane16(hh) + L::X + half * 16, x);
+                for (int hh = 0; hh < NH; ++hh) ld_tiles<2>(lane16(hh) + L::X + half * 16, u[hh]);
                 vla::tc_wait_ld();
+                if constexpr (TAPE) {
+                    const long long h0 = t0 + half * 16;
+                    if (rows_in)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                        for (int hh = 0; hh < NH; ++hh) {
+                            float* E = p.E + ((size_t)bh * p.T + h0) * D + row0 + xb + hh * 16 + r;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][e] = fmaf(-(e & 1 ? near[i].y : near[i].x), x[i][e], v[hh][i][e]);
-                parts16(std::integral_constant<int, 3>{}, lane16(hh) + L::ZP, x);
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int j = i * 8 + t2 + (e & 1);
+                                    if (h0 + j < n) E[(size_t)j * D + (e & 2) * 4] = u[hh][i][e];
+                                }
+                        }
+                }
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
+                    float f[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            u[hh][i][e] *= e & 1 ? beta[i].y : beta[i].x;
+                            f[i][e] = u[hh][i][e] * (e & 1 ? far[i].y : far[i].x);
+                        }
+                    parts16(std::integral_constant<int, 3>{}, lane16(hh) + L::ZP, f);
+                }
+                ready(f_ready);
+                __syncwarp();
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) parts16(std::integral_constant<int, L::UP>{}, lane16(hh) + L::UPC, u[hh]);
+                ready(u_ready);
             }
-            ready(z_ready);
+            // beside the products of T: this chunk's share of the state in its outputs
             __syncwarp();
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                ld_tiles<2>(lane16(hh) + L::X + 32 + half * 16, o[hh]);
-                vla::tc_wait_ld();
+            for (int hh = 0; hh < NH; ++hh) ld_tiles<2>(lane16(hh) + L::X + 32 + half * 16, o[hh]);
+            vla::tc_wait_ld();
+            vla::tc_fence_before();
+#pragma unroll
+            for (int hh = 0; hh < NH; ++hh)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[hh][i][e] *= p.scale * (e & 1 ? near[i].y : near[i].x);
-            }
-            if (!(ok = wait_warp(e_done, c))) break;
-            vla::tc_fence_after();
-            __syncwarp();
-#pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                float u[2][4], f[2][4];
-                ld_tiles<2>(lane16(hh) + L::X + half * 16, u);
-                vla::tc_wait_ld();
-                if constexpr (TAPE) {
-                    if (rows_in) {
-                        float* E = p.E + ((size_t)bh * p.T + h0) * D + row0 + xb + hh * 16 + r;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int j = i * 8 + t2 + (e & 1);
-                                if (h0 + j < n) E[(size_t)j * D + (e & 2) * 4] = u[i][e];
-                            }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        u[i][e] *= e & 1 ? beta[i].y : beta[i].x;
-                        f[i][e] = u[i][e] * (e & 1 ? far[i].y : far[i].x);
-                    }
-                parts16(std::integral_constant<int, 3>{}, lane16(hh) + L::ZP, f);
-                parts16(std::integral_constant<int, L::UP>{}, lane16(hh) + L::UPC, u);
-            }
-            ready(u_ready);
             if (!(ok = wait_warp(t_done, c))) break;
             vla::tc_fence_after();
 #pragma unroll
             for (int q = 0; q < L::PIECES; ++q) {
                 constexpr int NT = W % 32 == 0 ? 4 : 2;
                 __syncwarp();
+                float y[NH][4][4];
 #pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    float y[4][4];
+                for (int hh = 0; hh < NH; ++hh)
 #pragma unroll
                     for (int k0 = 0; k0 < 4; k0 += NT)
-                        if (q * 4 + k0 < W / 8) ld_tiles<NT>(lane16(hh) + L::TC + half * W + (q * 4 + k0) * 8, y + k0);
-                    vla::tc_wait_ld();
+                        if (q * 4 + k0 < W / 8) ld_tiles<NT>(lane16(hh) + L::TC + half * W + (q * 4 + k0) * 8, y[hh] + k0);
+                vla::tc_wait_ld();
+#pragma unroll
+                for (int hh = 0; hh < NH; ++hh) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (q * 4 + k < W / 8) s[hh][q * 4 + k][e] = fmaf(whole, s[hh][q * 4 + k][e], y[k][e]);
+                        for (int e = 0; e < 4; e += 2)
+                            if (q * 4 + k < W / 8) {
+                                float* to = s[hh][q * 4 + k] + e;
+                                const float2 w = __ffma2_rn(make_float2(whole, whole), make_float2(to[0], to[1]), make_float2(y[hh][k][e], y[hh][k][e + 1]));
+                                to[0] = w.x, to[1] = w.y;
+                            }
                     if (c + 1 < chunks) publish(q, hh);
                 }
                 if (c + 1 < chunks) ready(s_ready + q);
             }
-            if (!(ok = wait_warp(o_done, c))) break;
-            vla::tc_fence_after();
-            __syncwarp();
-#pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                float x[2][4];
-                ld_tiles<2>(lane16(hh) + L::OP + half * 16, x);
-                vla::tc_wait_ld();
-                join(o[hh], x);
-            }
-            vla::tc_fence_before();
-            if constexpr (TAPE) {
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    float d[2][4];
-                    columns(L::O, hh, d);
-                    float* od = p.od + ((size_t)bh * (D / 16) + (row0 + xb) / 16 + hh) * p.T + h0;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float y = over_rows(fmaf(o[hh][i][e], d[i][e], o[hh][i][2 + e] * d[i][2 + e]));
-                            if (lane < 4 && rows_in && h0 + i * 8 + t2 + e < n) od[i * 8 + t2 + e] = y;
-                        }
-                }
-            } else if (rows_in) {
-                // rows of tokens through the warp's buffer: 16 or 32 values of each
-                __syncwarp();
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (h0 + i * 8 + t2 + (e & 1) < n) bad = fmaf(o[hh][i][e], 0.f, bad);
-                    stsm_t(vla::smem_u32(stage) + (across_down<L::OUT_LD>(lane) + hh * 16) * 2, pack_bf16(o[hh][0][0], o[hh][0][1]),
-                           pack_bf16(o[hh][0][2], o[hh][0][3]), pack_bf16(o[hh][1][0], o[hh][1][1]), pack_bf16(o[hh][1][2], o[hh][1][3]));
-                }
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < NH; ++k) {
-                    const int i = k * 32 + lane, row = i / (2 * NH), col = i % (2 * NH) * 8;
-                    const long long t = h0 + row;
-                    if (t >= p.T) continue;
-                    uint4 w = *reinterpret_cast<const uint4*>(stage + (row * L::OUT_LD + col) * 2);
-                    if (t >= n) w = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(row_of<T>(p.out, b, h, t) + row0 + xb + col) = w;
-                }
-            }
-            arrive_warp(done + (c & 1));
         }
+        if (ok && chunks > 1) write_out(chunks - 2);
+        if (ok && chunks > 0 && (ok = output(chunks - 1))) write_out(chunks - 1);
         if (ok && rows_in) {
 #pragma unroll
             for (int hh = 0; hh < NH; ++hh) {

@@ -10,14 +10,16 @@ namespace vla_layer {
 // of what is left, eight bits at a time; three parts hold the value's 24 bits. The last of two is rounded too.
 template <int N>
 __device__ __forceinline__ void split(float x0, float x1, uint32_t (&p)[N]) {
+    float2 x = make_float2(x0, x1);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const bool cut = N == 3 && i > 0;
-        p[i] = cut ? __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632) : pack_bf16(x0, x1);
-        if (i + 1 < N) {
-            x0 -= cut ? __uint_as_float(__float_as_uint(x0) & 0xFFFF0000u) : __uint_as_float(p[i] << 16);
-            x1 -= cut ? __uint_as_float(__float_as_uint(x1) & 0xFFFF0000u) : __uint_as_float(p[i] & 0xFFFF0000u);
-        }
+        const uint32_t w0 = __float_as_uint(x.x), w1 = __float_as_uint(x.y);
+        p[i] = cut ? __byte_perm(w0, w1, 0x7632) : pack_bf16(x.x, x.y);
+        if (i + 1 < N)
+            x = __ffma2_rn(cut ? make_float2(__uint_as_float(w0 & 0xFFFF0000u), __uint_as_float(w1 & 0xFFFF0000u))
+                               : make_float2(__uint_as_float(p[i] << 16), __uint_as_float(p[i] & 0xFFFF0000u)),
+                           make_float2(-1.f, -1.f), x);
     }
 }
 __device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
