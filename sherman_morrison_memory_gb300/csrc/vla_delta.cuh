@@ -499,9 +499,10 @@ __device__ __forceinline__ void store_tokens(const float (&x)[2][4], char* stage
 template <typename T>
 __device__ __forceinline__ void zero_tokens(const Seq& s, int b, int h, long long t0, long long T_, int col0, int cols) {
     const float zero[8] = {};
-    const int per = cols / 8;
-    for (long long i = threadIdx.x; i < (T_ - t0) * per; i += blockDim.x)
-        store8(row_of<T>(s, b, h, t0 + i / per) + col0 + i % per * 8, zero);
+    for (long long t = t0 + threadIdx.x; t < T_; t += blockDim.x) {
+        T* row = row_of<T>(s, b, h, t) + col0;
+        for (int c = 0; c < cols; c += 8) store8(row + c, zero);
+    }
 }
 
 // x summed over the eight lanes that hold the same tokens of a fragment

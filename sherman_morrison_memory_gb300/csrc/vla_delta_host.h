@@ -6,6 +6,7 @@
 #include "vla_delta.cuh"
 #include "vla_delta_forward.cuh"
 #include "vla_delta_tc.cuh"
+#include "vla_maps.h"
 
 namespace vla_layer {
 
@@ -75,7 +76,13 @@ inline vla_status delta_tc_run(DeltaArgs& p, cudaStream_t s) {
     const long long grid = (long long)p.B * p.H * (D > R ? D / R : 1);
     if (grid > 2147483647LL) return VLA_ERR_INVALID_ARG;
     if (!allow_smem<vla_delta_tc_kernel<D, R, TAPE>>(L::BYTES)) return VLA_ERR_CUDA;
-    vla_delta_tc_kernel<D, R, TAPE><<<(unsigned)grid, L::THREADS, L::BYTES, s>>>(p);
+    DeltaMaps maps;
+    const Seq* seq[4] = {&p.k, &p.q, &p.v, &p.dO};
+    for (int i = 0; i < (TAPE ? 4 : 3); ++i) {
+        const vla_seq x{seq[i]->p, seq[i]->sb, seq[i]->sh, seq[i]->st};
+        if (!make_map(&maps.m[i], &x, p.B, p.H, p.T, D, DC)) return VLA_ERR_CUDA;
+    }
+    vla_delta_tc_kernel<D, R, TAPE><<<(unsigned)grid, L::THREADS, L::BYTES, s>>>(p, maps);
     return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
 }
 

@@ -19,8 +19,9 @@
 // pieces of its columns, the products of the first beside the work on the next,
 // and o is formed beside the next chunk's X.
 //
-// Warps: 0-7 S (a quarter of the lanes, a half of the columns and of the
-// tokens), 8 MMAs, 9 loads, 12-15 the helpers' part of a chunk ahead.
+// Warps: the workers (16 rows, a half of the columns and of the tokens each, 8 or
+// 16 of them), one for the MMAs, one for loads, and behind them two groups of three
+// with the helpers' part, two chunks ahead.
 // Every wait is bounded; one that runs out raises the block's abort flag.
 #pragma once
 
@@ -28,6 +29,10 @@
 #include "vla_tcgen.cuh"
 
 namespace vla_layer {
+
+struct DeltaMaps {
+    CUtensorMap m[4];  // k, q, v, dO in boxes of 64 columns x 32 tokens, 128-byte swizzle
+};
 
 template <int D, int R, bool TAPE>
 struct DeltaTc {
@@ -39,44 +44,37 @@ struct DeltaTc {
     static constexpr int PP = TAPE ? 3 : 1, UP = TAPE ? 3 : 2;  // parts of P and of b E
     // a chunk's matrices, two of 64 columns: the inverse's parts 0 | 1, its 2 | P's 0, P's 1 | 2; gates
     static constexpr int MATS = (TAPE ? 3 : 2) * BOX, PREP = MATS + 1024;
-    static constexpr int NPR = 3;  // chunks' matrices: a chunk's are free once the next one's Z is out
-    static constexpr int PREPS = NST * STAGE, N = PREPS + NPR * PREP, OUT = N + 2 * 16 * NLD * 4;
-    static constexpr int OUT_LD = 40;                      // elements of a row of a warp's staged outputs, 32 columns
-    static constexpr int BAR = OUT + 8 * 16 * OUT_LD * 2;
+    // chunks' matrices: a chunk's are free once the next one's Z is out, and two groups of helpers work on two at a time
+    static constexpr int NPR = 4, GROUPS = 2, SCRATCH = (2 * 16 * NLD + 3 * 3 * DC) * 4;
+    static constexpr int PREPS = NST * STAGE, N = PREPS + NPR * PREP, OUT = N + GROUPS * SCRATCH;
+    static constexpr int OUT_LD = 24;                      // elements of a row of a warp's staged outputs
+    static constexpr int NW = R / 8;                       // workers
+    static constexpr int BAR = OUT + NW * 16 * OUT_LD * 2;
     static constexpr int NBAR = NST + 2 * NPR + 10, MISC = BAR + NBAR * 8, BYTES = MISC + 16;
     static_assert(BYTES <= 227 * 1024, "shared memory");
-    static constexpr int W = D / 2, NH = R / 64;           // a worker's columns, groups of 16 rows
+    static constexpr int W = D / 2;                        // a worker's columns
     static constexpr int PIECES = (W + 31) / 32;
     // TMEM columns; E takes X's place once Z is made of it, and what T is made of Z's
     static constexpr int SB = 0, ZP = SB + 3 * (D / 2), UPC = ZP + 48, X = UPC + UP * 16, OP = X + 64, TC = OP + 32, COLS = 512;
     static_assert(TC + D <= COLS, "tensor memory");
-    static constexpr int THREADS = 512;
+    static constexpr int THREADS = (NW + 8) * 32;
     __host__ __device__ static constexpr int stage_of(int c) { return c % NST * STAGE; }  // the stage of a chunk
 };
 
 // Address of 16 bytes in a box: row `row`, group `j` of eight values
 __device__ __forceinline__ uint32_t in_box(int row, int j) { return (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4)); }
 
-// prepare_chunk() for tiles in boxes; matrices in rows of i.
+// prepare_chunk() for tiles in boxes, by a group of three warps; matrices in rows of i.
 template <typename L, int D>
-__device__ __forceinline__ void prepare_boxes(char* sm, uint32_t stage, char* prep, float g, float beta, float scale, Whole& whole,
-                                              int hw, int lane) {
+__device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, char* prep, float g, float beta, float scale, Whole& whole,
+                                              int group, int hw, int lane) {
     float Gh, Gl;
     sums_of(g, lane, Gh, Gl);
-    if (hw == 3) {
-        const float all = __shfl_sync(0xffffffffu, Gh, 31), rest = __shfl_sync(0xffffffffu, Gl, 31);
-        float* gates = reinterpret_cast<float*>(prep + L::MATS);
-        gates[GATE_NEAR + lane] = expf(Gh + Gl);
-        gates[GATE_FAR + lane] = expf((all - Gh) + (rest - Gl));
-        gates[GATE_BETA + lane] = beta;
-        const float w = whole.next(all + rest);
-        if (lane == 0) gates[GATE_WHOLE] = w;
-        return;
-    }
     const int mt = hw ? 1 : 0, np = hw == 2 ? 1 : 0;
     const int down = lane & 15, across = (lane & 7) + ((lane >> 4) << 3);  // rows of a 16 x 16 block for its four 8 x 8 ones
     float c[4][4] = {};  // K K^T, Q K^T
-#pragma unroll
+    // rolled: the roles' code of a scheduler is more than its instruction cache
+#pragma unroll 1
     for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t box = stage + (ks >> 2) * 2 * L::BOX;
         uint32_t a[1][4], q[1][4], b[2][1][2];
@@ -88,7 +86,10 @@ __device__ __forceinline__ void prepare_boxes(char* sm, uint32_t stage, char* pr
         mma_tiles<1>(c + 2, c + 2, q, b);
     }
     const int r = lane >> 2, t2 = (lane & 3) * 2;
-    float* N = reinterpret_cast<float*>(sm + L::N) + (hw >> 1) * 16 * NLD;  // transposed
+    float* own = reinterpret_cast<float*>(scratch) + 2 * 16 * NLD + hw * 3 * DC;  // the sums of g and b of each token
+    own[lane] = Gh * 1.4426950408889634f, own[DC + lane] = Gl * 1.4426950408889634f, own[2 * DC + lane] = beta;
+    __syncwarp();
+    float* N = reinterpret_cast<float*>(scratch) + (hw >> 1) * 16 * NLD;  // transposed
     auto part_at = [&](int part, int row, int j8) {  // eight values of a part of the inverse
         return in_box(row, (part & 1) * 4 + j8) + (part >> 1) * L::BOX;
     };
@@ -96,21 +97,17 @@ __device__ __forceinline__ void prepare_boxes(char* sm, uint32_t stage, char* pr
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         const int j = np * 16 + n * 8 + t2;
-        float gj[2], lj[2], bj[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            gj[e] = __shfl_sync(0xffffffffu, Gh, j + e), lj[e] = __shfl_sync(0xffffffffu, Gl, j + e);
-            bj[e] = __shfl_sync(0xffffffffu, beta, j + e);
-        }
+        const float2 gj = *reinterpret_cast<const float2*>(own + j), lj = *reinterpret_cast<const float2*>(own + DC + j),
+                     bj = *reinterpret_cast<const float2*>(own + 2 * DC + j);
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             const int i = mt * 16 + hf * 8 + r;
-            const float gi = __shfl_sync(0xffffffffu, Gh, i), li = __shfl_sync(0xffffffffu, Gl, i);
+            const float gi = own[i], li = own[DC + i];
             float y[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float w = expf((gi - gj[e]) + (li - lj[e]));
-                x[n][2 * hf + e] = j + e < i ? c[n][2 * hf + e] * w * bj[e] : 0.f;
+                const float w = exp2f((gi - (e ? gj.y : gj.x)) + (li - (e ? lj.y : lj.x)));
+                x[n][2 * hf + e] = j + e < i ? c[n][2 * hf + e] * w * (e ? bj.y : bj.x) : 0.f;
                 y[e] = j + e <= i ? c[2 + n][2 * hf + e] * w * scale : 0.f;
                 if (hw != 1) N[(n * 8 + t2 + e) * NLD + hf * 8 + r] = x[n][2 * hf + e];
             }
@@ -160,7 +157,16 @@ __device__ __forceinline__ void prepare_boxes(char* sm, uint32_t stage, char* pr
                 }
         }
     }
-    vla::named_bar(2, 96);
+    vla::named_bar(2 + group, 96);
+    if (hw == 0) {
+        const float all = __shfl_sync(0xffffffffu, Gh, 31), rest = __shfl_sync(0xffffffffu, Gl, 31);
+        float* gates = reinterpret_cast<float*>(prep + L::MATS);
+        gates[GATE_NEAR + lane] = expf(Gh + Gl);
+        gates[GATE_FAR + lane] = expf((all - Gh) + (rest - Gl));
+        gates[GATE_BETA + lane] = beta;
+        const float w = whole.next(all + rest);
+        if (lane == 0) gates[GATE_WHOLE] = w;
+    }
     if (hw != 1) return;
     // T21^T = -(T11^T N21^T) T22^T
     uint32_t a[INV_PARTS][4], w[2][INV_PARTS][2];
@@ -207,11 +213,13 @@ __device__ __forceinline__ void ld_tiles(uint32_t at, float (*x)[4]) {
 }
 
 template <int D, int R, bool TAPE>
-__global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_constant__ DeltaArgs p) {
+__global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_kernel(const __grid_constant__ DeltaArgs p,
+                                                                                           const __grid_constant__ DeltaMaps maps) {
     using T = __nv_bfloat16;
     using L = DeltaTc<D, R, TAPE>;
-    constexpr int SPAN = BLOCK<T>, NH = L::NH, W = L::W, SPLITS = D > R ? D / R : 1;
-    extern __shared__ __align__(1024) char sm[];
+    constexpr int SPAN = BLOCK<T>, NW = L::NW, W = L::W, SPLITS = D > R ? D / R : 1;
+    extern __shared__ __align__(1024) char delta_sm[];
+    char* sm = delta_sm;
     const uint32_t sb = vla::smem_u32(sm);
     uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
     uint64_t *full = bar, *prep_ready = full + L::NST, *done = prep_ready + L::NPR, *s_ready = done + L::NPR, *x_done = s_ready + 2,
@@ -226,25 +234,22 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
     const long long n = delta_len(p, b);
     const int chunks = (int)((n + DC - 1) / DC);
 
-    for (int i = tid; i < L::NST * L::STAGE / 16; i += L::THREADS)  // columns that no load fills stay zero
-        *reinterpret_cast<uint4*>(sm + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     if (tid == 0) {
         for (int i = 0; i < L::NST; ++i) vla::mbar_init(full + i, 1);
-        for (int i = 0; i < L::NPR; ++i) vla::mbar_init(prep_ready + i, 4), vla::mbar_init(done + i, 8);
-        for (int i = 0; i < 2; ++i) vla::mbar_init(s_ready + i, 8);
+        for (int i = 0; i < L::NPR; ++i) vla::mbar_init(prep_ready + i, 3), vla::mbar_init(done + i, NW);
+        for (int i = 0; i < 2; ++i) vla::mbar_init(s_ready + i, NW);
         vla::mbar_init(x_done, 1);
-        vla::mbar_init(z_ready, 8);
+        vla::mbar_init(z_ready, NW);
         vla::mbar_init(e_done, 1);
-        vla::mbar_init(f_ready, 8);
-        vla::mbar_init(u_ready, 8);
+        vla::mbar_init(f_ready, NW);
+        vla::mbar_init(u_ready, NW);
         vla::mbar_init(t_done, 1);
         vla::mbar_init(o_done, 1);
         vla::mbar_init(drained, 1);
         *abort_flag = 0;
         vla::fence_mbar_init();
     }
-    if (warp == 8) vla::tc_alloc(tmem_ptr, L::COLS);
-    vla::fence_proxy_async_smem();
+    if (warp == NW) vla::tc_alloc(tmem_ptr, L::COLS);
     vla::tc_fence_before();
     __syncthreads();
     vla::tc_fence_after();
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
         if (lane == 0) vla::mbar_arrive(w);
     };
 
-    if (warp == 8) {  // ---- MMAs, issued by one lane of a whole warp
+    if (warp == NW) {  // ---- MMAs, issued by one lane of a whole warp
         const bool one = elect_one();
         const uint32_t id64 = idesc_bf16(R, 64, 0, 0), id32 = idesc_bf16(R, 32, 0, 0), id_t = idesc_bf16(R, D, 0, 1);
         const uint64_t dk = desc_sw128(0, 16, 1024), dm = desc_sw128(0, L::NB == 2 ? 2 * L::BOX : 16, 1024);
@@ -334,40 +339,64 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
         __syncwarp();
         if (!__all_sync(0xffffffffu, vla::mbar_try_wait(drained, 0))) vla::mbar_wait_slow(drained, 0, nullptr, p.wait_ns);
         __syncwarp();
-    } else if (warp == 9) {  // ---- loads, a chunk under way behind the one that is waited for
+    } else if (warp == NW + 1) {  // ---- loads
+        // Whole chunks by TMA, three ahead; a last one of fewer tokens, whose other rows are zero whatever memory
+        // holds there, by plain copies.
+        const bool one = elect_one();
+        constexpr int TILES = TAPE ? 4 : 3;
         auto load = [&](int c) {
-            if (c < chunks && !(p.stall && c + 1 == chunks)) {
-                const long long t0 = (long long)c * DC;
-                const int live = (int)min((long long)DC, n - t0);
-                auto tile = [&](uint32_t dst, int box_step, const Seq& s, int col0, int cols) {
-                    const int wide = cols <= 32 ? 2 : cols <= 64 ? 3 : 4, g8 = lane & ((1 << wide) - 1);
-                    if (g8 * 8 >= cols) return;
-                    const T* src = row_of<T>(s, b, h, t0) + col0 + g8 * 8;
-                    dst += (g8 >> 3) * box_step;
-#pragma unroll 4
-                    for (int r = lane >> wide; r < DC; r += 32 >> wide)
-                        cp_async16(dst + in_box(r, g8 & 7), r < live ? src + r * s.st : src, r < live ? 16 : 0);
-                };
-                const uint32_t st = sb + L::stage_of(c);
-                tile(st, 2 * L::BOX, p.k, 0, D);
-                tile(st + L::BOX, 2 * L::BOX, p.q, 0, D);
-                tile(st + L::V, L::BOX, p.v, row0, rows);
-                if constexpr (TAPE) tile(st + L::O, L::BOX, p.dO, row0, rows);
+            const long long t0 = (long long)c * DC;
+            const int live = (int)min((long long)DC, n - t0);
+            const uint32_t st = sb + L::stage_of(c);
+            uint64_t* w = full + c % L::NST;
+            if (live == DC) {
+                if (one) {
+                    vla::mbar_arrive_expect_tx(w, (2 * L::NB + (TILES - 2) * L::VB) * L::BOX);
+#pragma unroll
+                    for (int i = 0; i < L::NB; ++i) {
+                        tma_load(st + i * 2 * L::BOX, &maps.m[0], i * 64, (int)t0, h, b, w);
+                        tma_load(st + i * 2 * L::BOX + L::BOX, &maps.m[1], i * 64, (int)t0, h, b, w);
+                    }
+#pragma unroll
+                    for (int i = 0; i < L::VB; ++i) {
+                        tma_load(st + L::V + i * L::BOX, &maps.m[2], row0 + i * 64, (int)t0, h, b, w);
+                        if constexpr (TAPE) tma_load(st + L::O + i * L::BOX, &maps.m[3], row0 + i * 64, (int)t0, h, b, w);
+                    }
+                }
+                __syncwarp();
+                return;
+            }
+#pragma unroll 1
+            for (int m = 0; m < TILES; ++m) {
+                const Seq& s = m == 0 ? p.k : m == 1 ? p.q : m == 2 ? p.v : p.dO;
+                const int boxes = m < 2 ? L::NB : L::VB, cols = m < 2 ? D : rows;
+                const uint32_t to = m == 0 ? 0 : m == 1 ? L::BOX : m == 2 ? L::V : L::O;
+                for (int i = lane; i < boxes * DC * 8; i += 32) {
+                    const int g8 = i % (boxes * 8), r = i / (boxes * 8);
+                    const bool on = r < live && g8 * 8 < cols;
+                    const T* src = row_of<T>(s, b, h, on ? t0 + r : t0) + (on ? (m < 2 ? 0 : row0) + g8 * 8 : 0);
+                    cp_async16(st + to + (g8 >> 3) * (m < 2 ? 2 * L::BOX : L::BOX) + in_box(r, g8 & 7), src, on ? 16 : 0);
+                }
             }
             cp_async_commit();
-        };
-        load(0);
-        load(1);
-        for (int c = 0; c < chunks; ++c) {
-            cp_async_wait<1>();
+            cp_async_wait<0>();
             vla::fence_proxy_async_smem();
-            if (!(p.stall && c + 1 == chunks)) arrive_warp(full + c % L::NST);
-            if (c + 2 >= L::NST && c + 2 < chunks && !wait_warp(done + (c + 2 - L::NST) % L::NPR, (c + 2 - L::NST) / L::NPR)) break;
-            load(c + 2);
+            arrive_warp(w);
+        };
+        int loaded = 0;
+        for (; loaded < chunks; ++loaded) {
+            const int before = loaded - L::NST;  // the stage's last chunk
+            if (before >= 0 && !wait_warp(done + before % L::NPR, before / L::NPR)) break;
+            if (!(p.stall && loaded + 1 == chunks)) load(loaded);
         }
-        cp_async_wait<0>();
-    } else if (warp >= 12) {  // ---- the helpers' part
-        const int hw = warp - 12;
+        if (*abort_flag)  // leave only once the copies under way have landed
+            for (int c = max(0, loaded - L::NST); c < loaded && !(p.stall && c + 1 == chunks); ++c) {
+                if (!__all_sync(0xffffffffu, vla::mbar_try_wait(full + c % L::NST, (c / L::NST) & 1)))
+                    vla::mbar_wait_slow(full + c % L::NST, (c / L::NST) & 1, nullptr, p.wait_ns);
+                __syncwarp();
+            }
+    } else if (warp >= NW + 2) {  // ---- the helpers' part, two groups for every other chunk
+        const int group = (warp - NW - 2) / 3, hw = (warp - NW - 2) % 3;
         Whole whole;
         float g = 0.f, beta = 0.f;
         auto gates = [&](int c) {
@@ -375,30 +404,28 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
             g = t < n && p.g.p ? *p.g.at(b, h, t) : 0.f;
             beta = t < n ? *p.beta.at(b, h, t) : 0.f;
         };
-        gates(0);
-        for (int c = 0; c < chunks; ++c) {
+        gates(group);
+        for (int c = group; c < chunks; c += L::GROUPS) {
             const float gc = g, bc = beta;
-            gates(c + 1);
+            gates(c + L::GROUPS);
             // the three warps that meet at a barrier leave together if a wait ran out
             const bool ok = wait_warp(full + c % L::NST, c / L::NST) && (c < L::NPR || wait_warp(done + c % L::NPR, c / L::NPR - 1));
-            if (vla::bar_red_or(1, HELPERS, !ok)) break;
-            prepare_boxes<L, D>(sm, sb + L::stage_of(c), sm + L::PREPS + c % L::NPR * L::PREP, gc, bc, p.scale, whole, hw, lane);
+            if (vla::bar_red_or(2 + group, 96, !ok)) break;
+            prepare_boxes<L, D>(sm + L::N + group * L::SCRATCH, sb + L::stage_of(c), sm + L::PREPS + c % L::NPR * L::PREP, gc, bc, p.scale,
+                                whole, group, hw, lane);
             vla::fence_proxy_async_smem();
             arrive_warp(prep_ready + c % L::NPR);
         }
-    } else if (warp < 8) {  // ---- S
-        const int quad = warp & 3, half = warp >> 2, r = lane >> 2, t2 = (lane & 3) * 2;
-        const int xb = quad * (R / 4);                      // first row of the warp's in the block
+    } else if (warp < NW) {  // ---- S
+        const int quad = warp & 3, half = (warp >> 2) & 1, r = lane >> 2, t2 = (lane & 3) * 2;
+        const int xb = quad * (R / 4) + (warp >> 3) * 16;   // first of the warp's 16 rows in the block
         const bool rows_in = xb < rows;                     // else zero throughout
-        const uint32_t lanes = tm + ((uint32_t)(quad * 32) << 16);
-        auto lane16 = [&](int hh) { return lanes + ((uint32_t)(hh * 16) << 16); };
-        float s[NH][W / 8][4];
-#pragma unroll
-        for (int hh = 0; hh < NH; ++hh)
-            load_rows<D, W>(s[hh], p.S0 && rows_in ? p.S0 + ((size_t)bh * D + row0 + xb + hh * 16) * D + half * W : nullptr, lane);
+        const uint32_t lanes = tm + ((uint32_t)(quad * 32 + (warp >> 3) * 16) << 16);
+        float s[W / 8][4];
+        load_rows<D, W>(s, p.S0 && rows_in ? p.S0 + ((size_t)bh * D + row0 + xb) * D + half * W : nullptr, lane);
         char* stage = sm + L::OUT + warp * 16 * L::OUT_LD * 2;
         // a piece of S in three parts
-        auto publish = [&](int q, int hh) {
+        auto publish = [&](int q) {
             constexpr int NT = W % 32 == 0 ? 4 : 2;
 #pragma unroll
             for (int k0 = 0; k0 < 4; k0 += NT) {
@@ -409,13 +436,13 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         uint32_t y[3];
-                        split<3>(s[hh][q * 4 + k0 + k][2 * e], s[hh][q * 4 + k0 + k][2 * e + 1], y);
+                        split<3>(s[q * 4 + k0 + k][2 * e], s[q * 4 + k0 + k][2 * e + 1], y);
 #pragma unroll
                         for (int i = 0; i < 3; ++i) v[i][2 * k + e] = y[i];
                     }
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
-                    const uint32_t to = lane16(hh) + L::SB + i * (D / 2) + half * (W / 2) + (q * 4 + k0) * 4;
+                    const uint32_t to = lanes + L::SB + i * (D / 2) + half * (W / 2) + (q * 4 + k0) * 4;
                     if constexpr (NT == 4)
                         st_frag8(to, *reinterpret_cast<const uint32_t(*)[8]>(v[i]));
                     else
@@ -440,14 +467,13 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
 #pragma unroll
             for (int q = 0; q < L::PIECES; ++q) {
                 __syncwarp();
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) publish(q, hh);
+                publish(q);
                 ready(s_ready + q);
             }
         }
         // this warp's 16 columns of a chunk's tile at its 16 tokens
-        auto columns = [&](int c, int tile, int hh, float (&x)[2][4]) {
-            const int g16 = xb / 16 + hh;
+        auto columns = [&](int c, int tile, float (&x)[2][4]) {
+            const int g16 = xb / 16;
             uint32_t w[4];
             ldsm_t(w, sb + L::stage_of(c) + tile + (g16 >> 2) * L::BOX +
                           in_box(half * 16 + (lane & 7) + ((lane >> 4) << 3), (g16 & 3) * 2 + ((lane >> 3) & 1)));
@@ -455,70 +481,55 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
             for (int i = 0; i < 2; ++i)
                 x[i][0] = low_of(w[2 * i]), x[i][1] = high_of(w[2 * i]), x[i][2] = low_of(w[2 * i + 1]), x[i][3] = high_of(w[2 * i + 1]);
         };
-        float o[NH][2][4];
+        float o[2][4];
         // Chunk c's outputs, from its share of the state in o and of the pairs: to the warp's buffer, or (TAPE) o . dO
-        const T* dst = TAPE ? nullptr : row_of<T>(p.out, b, h, half * 16 + lane / (2 * NH)) + row0 + xb + lane % (2 * NH) * 8;
+        T* dst = TAPE ? nullptr : row_of<T>(p.out, b, h, half * 16 + lane / 2) + row0 + xb + lane % 2 * 8;
         float* od = TAPE ? p.od + ((size_t)bh * (D / 16) + (row0 + xb) / 16) * p.T + half * 16 : nullptr;
         auto output = [&](int c) {
             const int live = (int)min(16LL, n - (long long)c * DC - half * 16);
             if (!wait_warp(o_done, c)) return false;
             vla::tc_fence_after();
             __syncwarp();
-            float x[NH][2][4];
-#pragma unroll
-            for (int hh = 0; hh < NH; ++hh) ld_tiles<2>(lane16(hh) + L::OP + half * 16, x[hh]);
+            float x[2][4];
+            ld_tiles<2>(lanes + L::OP + half * 16, x);
             vla::tc_wait_ld();
             vla::tc_fence_before();
-#pragma unroll
-            for (int hh = 0; hh < NH; ++hh) join(o[hh], x[hh]);
+            join(o, x);
             if constexpr (TAPE) {
+                float d[2][4];
+                columns(c, L::O, d);
 #pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    float d[2][4];
-                    columns(c, L::O, hh, d);
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float y = over_rows(fmaf(o[hh][i][e], d[i][e], o[hh][i][2 + e] * d[i][2 + e]));
-                            if (lane < 4 && rows_in && i * 8 + t2 + e < live) od[(size_t)hh * p.T + (size_t)c * DC + i * 8 + t2 + e] = y;
-                        }
-                }
+                    for (int e = 0; e < 2; ++e) {
+                        const float y = over_rows(fmaf(o[i][e], d[i][e], o[i][2 + e] * d[i][2 + e]));
+                        if (lane < 4 && rows_in && i * 8 + t2 + e < live) od[(size_t)c * DC + i * 8 + t2 + e] = y;
+                    }
             } else {
                 if (live < 16)
 #pragma unroll
-                    for (int hh = 0; hh < NH; ++hh)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (i * 8 + t2 + (e & 1) >= live) o[hh][i][e] = 0.f;
-                __syncwarp();
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-#pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) bad = fmaf(o[hh][i][e], 0.f, bad);
-                    stsm_t(vla::smem_u32(stage) + (across_down<L::OUT_LD>(lane) + hh * 16) * 2, pack_bf16(o[hh][0][0], o[hh][0][1]),
-                           pack_bf16(o[hh][0][2], o[hh][0][3]), pack_bf16(o[hh][1][0], o[hh][1][1]), pack_bf16(o[hh][1][2], o[hh][1][3]));
-                }
+                        for (int e = 0; e < 4; ++e)
+                            if (i * 8 + t2 + (e & 1) >= live) o[i][e] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) bad = fmaf(o[i][e], 0.f, bad);
+                __syncwarp();
+                stsm_t(vla::smem_u32(stage) + across_down<L::OUT_LD>(lane) * 2, pack_bf16(o[0][0], o[0][1]), pack_bf16(o[0][2], o[0][3]),
+                       pack_bf16(o[1][0], o[1][1]), pack_bf16(o[1][2], o[1][3]));
                 __syncwarp();
             }
             arrive_warp(done + c % L::NPR);
             return true;
         };
-        // ... and from there to their rows: 16 or 32 values of each token, up to T
+        // ... and from there to their rows, up to T
         auto write_out = [&](int c) {
             if constexpr (!TAPE) {
-                const int in = rows_in ? (int)min(16LL, p.T - (long long)c * DC - half * 16) : 0;
-#pragma unroll
-                for (int k = 0; k < NH; ++k) {
-                    const int row = lane / (2 * NH) + k * (16 / NH), col = lane % (2 * NH) * 8;
-                    if (row < in)
-                        *reinterpret_cast<uint4*>(const_cast<T*>(dst) + ((long long)c * DC + k * (16 / NH)) * p.out.st) =
-                            *reinterpret_cast<const uint4*>(stage + (row * L::OUT_LD + col) * 2);
-                }
+                if (rows_in && (long long)c * DC + half * 16 + lane / 2 < p.T)
+                    *reinterpret_cast<uint4*>(dst + (long long)c * DC * p.out.st) =
+                        *reinterpret_cast<const uint4*>(stage + (lane / 2 * L::OUT_LD + lane % 2 * 8) * 2);
             }
         };
         bool ok = true;
@@ -526,140 +537,112 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
             const long long t0 = (long long)c * DC;
             if constexpr (TAPE) {
                 if (t0 % SPAN == 0 && rows_in)
-#pragma unroll
-                    for (int hh = 0; hh < NH; ++hh)
-                        store_rows<D, W>(s[hh], p.before + (((size_t)bh * (p.blocks + 1) + t0 / SPAN) * D + row0 + xb + hh * 16) * D + half * W, lane);
+                    store_rows<D, W>(s, p.before + (((size_t)bh * (p.blocks + 1) + t0 / SPAN) * D + row0 + xb) * D + half * W, lane);
             }
             const float* gates = reinterpret_cast<const float*>(sm + L::PREPS + c % L::NPR * L::PREP + L::MATS) + half * 16;
             if (!(ok = wait_warp(prep_ready + c % L::NPR, c / L::NPR))) break;  // behind its loads
             float2 near[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) near[i] = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + t2);
-            const float whole = gates[GATE_WHOLE - half * 16];
             {
-                float v[NH][2][4];
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) columns(c, L::V, hh, v[hh]);
+                float x[2][4], v[2][4];
+                columns(c, L::V, v);
                 if (c > 1) write_out(c - 2);
                 if (!(ok = wait_warp(x_done, c))) break;
                 vla::tc_fence_after();
                 __syncwarp();
-                float x[NH][2][4];
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) ld_tiles<2>(lane16(hh) + L::X + half * 16, x[hh]);
+                ld_tiles<2>(lanes + L::X + half * 16, x);
                 vla::tc_wait_ld();
 #pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[hh][i][e] = fmaf(-(e & 1 ? near[i].y : near[i].x), x[hh][i][e], v[hh][i][e]);
-                    parts16(std::integral_constant<int, 3>{}, lane16(hh) + L::ZP, x[hh]);
-                }
+                    for (int e = 0; e < 4; ++e) x[i][e] = fmaf(-(e & 1 ? near[i].y : near[i].x), x[i][e], v[i][e]);
+                parts16(std::integral_constant<int, 3>{}, lanes + L::ZP, x);
             }
             ready(z_ready);
-            float2 far[2], beta[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                far[i] = *reinterpret_cast<const float2*>(gates + GATE_FAR + i * 8 + t2);
-                beta[i] = *reinterpret_cast<const float2*>(gates + GATE_BETA + i * 8 + t2);
-            }
             if (c > 0 && !(ok = output(c - 1))) break;  // beside the products of E: the chunk before's outputs
             if (!(ok = wait_warp(e_done, c))) break;
             vla::tc_fence_after();
             __syncwarp();
             {
-                float u[NH][2][4];
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) ld_tiles<2>(lane16(hh) + L::X + half * 16, u[hh]);
+                float u[2][4], f[2][4];
+                ld_tiles<2>(lanes + L::X + half * 16, u);
                 vla::tc_wait_ld();
                 if constexpr (TAPE) {
                     const long long h0 = t0 + half * 16;
-                    if (rows_in)
+                    if (rows_in) {
+                        float* E = p.E + ((size_t)bh * p.T + h0) * D + row0 + xb + r;
 #pragma unroll
-                        for (int hh = 0; hh < NH; ++hh) {
-                            float* E = p.E + ((size_t)bh * p.T + h0) * D + row0 + xb + hh * 16 + r;
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int j = i * 8 + t2 + (e & 1);
-                                    if (h0 + j < n) E[(size_t)j * D + (e & 2) * 4] = u[hh][i][e];
-                                }
-                        }
+                            for (int e = 0; e < 4; ++e) {
+                                const int j = i * 8 + t2 + (e & 1);
+                                if (h0 + j < n) E[(size_t)j * D + (e & 2) * 4] = u[i][e];
+                            }
+                    }
                 }
 #pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
-                    float f[2][4];
+                for (int i = 0; i < 2; ++i) {
+                    const float2 far = *reinterpret_cast<const float2*>(gates + GATE_FAR + i * 8 + t2);
+                    const float2 beta = *reinterpret_cast<const float2*>(gates + GATE_BETA + i * 8 + t2);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            u[hh][i][e] *= e & 1 ? beta[i].y : beta[i].x;
-                            f[i][e] = u[hh][i][e] * (e & 1 ? far[i].y : far[i].x);
-                        }
-                    parts16(std::integral_constant<int, 3>{}, lane16(hh) + L::ZP, f);
+                    for (int e = 0; e < 4; ++e) {
+                        u[i][e] *= e & 1 ? beta.y : beta.x;
+                        f[i][e] = u[i][e] * (e & 1 ? far.y : far.x);
+                    }
                 }
+                parts16(std::integral_constant<int, 3>{}, lanes + L::ZP, f);
                 ready(f_ready);
                 __syncwarp();
-#pragma unroll
-                for (int hh = 0; hh < NH; ++hh) parts16(std::integral_constant<int, L::UP>{}, lane16(hh) + L::UPC, u[hh]);
+                parts16(std::integral_constant<int, L::UP>{}, lanes + L::UPC, u);
                 ready(u_ready);
             }
             // beside the products of T: this chunk's share of the state in its outputs
             __syncwarp();
-#pragma unroll
-            for (int hh = 0; hh < NH; ++hh) ld_tiles<2>(lane16(hh) + L::X + 32 + half * 16, o[hh]);
+            ld_tiles<2>(lanes + L::X + 32 + half * 16, o);
             vla::tc_wait_ld();
             vla::tc_fence_before();
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[hh][i][e] *= p.scale * (e & 1 ? near[i].y : near[i].x);
+                for (int e = 0; e < 4; ++e) o[i][e] *= p.scale * (e & 1 ? near[i].y : near[i].x);
+            const float whole = gates[GATE_WHOLE - half * 16];
             if (!(ok = wait_warp(t_done, c))) break;
             vla::tc_fence_after();
 #pragma unroll
             for (int q = 0; q < L::PIECES; ++q) {
                 constexpr int NT = W % 32 == 0 ? 4 : 2;
                 __syncwarp();
-                float y[NH][4][4];
+                float y[4][4];
 #pragma unroll
-                for (int hh = 0; hh < NH; ++hh)
-#pragma unroll
-                    for (int k0 = 0; k0 < 4; k0 += NT)
-                        if (q * 4 + k0 < W / 8) ld_tiles<NT>(lane16(hh) + L::TC + half * W + (q * 4 + k0) * 8, y[hh] + k0);
+                for (int k0 = 0; k0 < 4; k0 += NT)
+                    if (q * 4 + k0 < W / 8) ld_tiles<NT>(lanes + L::TC + half * W + (q * 4 + k0) * 8, y + k0);
                 vla::tc_wait_ld();
 #pragma unroll
-                for (int hh = 0; hh < NH; ++hh) {
+                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int e = 0; e < 4; e += 2)
-                            if (q * 4 + k < W / 8) {
-                                float* to = s[hh][q * 4 + k] + e;
-                                const float2 w = __ffma2_rn(make_float2(whole, whole), make_float2(to[0], to[1]), make_float2(y[hh][k][e], y[hh][k][e + 1]));
-                                to[0] = w.x, to[1] = w.y;
-                            }
-                    if (c + 1 < chunks) publish(q, hh);
+                    for (int e = 0; e < 4; e += 2)
+                        if (q * 4 + k < W / 8) {
+                            float* to = s[q * 4 + k] + e;
+                            const float2 w = __ffma2_rn(make_float2(whole, whole), make_float2(to[0], to[1]), make_float2(y[k][e], y[k][e + 1]));
+                            to[0] = w.x, to[1] = w.y;
+                        }
+                if (c + 1 < chunks) {
+                    publish(q);
+                    ready(s_ready + q);
                 }
-                if (c + 1 < chunks) ready(s_ready + q);
             }
         }
         if (ok && chunks > 1) write_out(chunks - 2);
         if (ok && chunks > 0 && (ok = output(chunks - 1))) write_out(chunks - 1);
         if (ok && rows_in) {
+            float* to = TAPE ? p.before + ((size_t)bh * (p.blocks + 1) + (n + SPAN - 1) / SPAN) * D * D : p.S + (size_t)bh * D * D;
+            store_rows<D, W>(s, to + (size_t)(row0 + xb) * D + half * W, lane);
+            if constexpr (!TAPE) {
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh) {
-                float* to = TAPE ? p.before + ((size_t)bh * (p.blocks + 1) + (n + SPAN - 1) / SPAN) * D * D : p.S + (size_t)bh * D * D;
-                store_rows<D, W>(s[hh], to + (size_t)(row0 + xb + hh * 16) * D + half * W, lane);
-                if constexpr (!TAPE) {
+                for (int m = 0; m < W / 8; ++m)
 #pragma unroll
-                    for (int m = 0; m < W / 8; ++m)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) bad = fmaf(s[hh][m][e], 0.f, bad);
-                }
+                    for (int e = 0; e < 4; ++e) bad = fmaf(s[m][e], 0.f, bad);
             }
         }
     }
@@ -667,7 +650,7 @@ __global__ void __launch_bounds__(512, 1) vla_delta_tc_kernel(const __grid_const
     if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, 0);
     vla::tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == NW) {
         vla::tc_fence_after();
         vla::tc_dealloc(tm, L::COLS);
     }
