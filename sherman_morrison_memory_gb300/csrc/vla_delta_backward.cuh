@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_reverse_kernel(con
     if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, 0);
 }
 
-// dQ, dK and the gates' gradients of a block of tokens: a warp per 16 columns of d. bf16 calls round a term once
+// dQ, dK and the gates' gradients of a block of tokens: two warps for 16 columns of d, a half of the tokens each. bf16 calls round a term once
 // on its way beside the result: dV as it was written, or S, R or X; U, M and S where dV meets it are two parts.
 template <int D, typename T>
 struct DeltaGrads {
@@ -226,13 +226,13 @@ struct DeltaGrads {
     static constexpr int LD = D + 8, PLANE = TB * LD * 2, XLD = TB + 8, XPLANE = TB * XLD * 2;
     static constexpr int Q = 0, K = Q + NP * PLANE, O = K + NP * PLANE, V = O + NP * PLANE, U = V + NP * PLANE,
                          X = U + UP * PLANE, M = X + XP * XPLANE, GATES = M + MP * XPLANE, BYTES = GATES + 5 * TB * 4;
-    static constexpr int THREADS = D * 2;
+    static constexpr int THREADS = D * 4, MH = MT / 2;  // a warp's tiles of 16 tokens
 };
 
 template <int D, typename T>
-__global__ void __launch_bounds__(D * 2) vla_delta_grads_kernel(const __grid_constant__ DeltaArgs p) {
+__global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_constant__ DeltaArgs p) {
     using L = DeltaGrads<D, T>;
-    constexpr int NP = L::NP, TB = L::TB, MT = L::MT, LD = L::LD, XLD = L::XLD, UP = L::UP, THREADS = L::THREADS;
+    constexpr int NP = L::NP, TB = L::TB, MT = L::MT, MH = L::MH, LD = L::LD, XLD = L::XLD, UP = L::UP, THREADS = L::THREADS;
     extern __shared__ __align__(128) char sm[];
     const int bh = blockIdx.x / p.blocks, blk = blockIdx.x % p.blocks, b = bh / p.H, h = bh % p.H;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(D * 2) vla_delta_grads_kernel(const __grid_con
     const uint32_t base = vla::smem_u32(sm);
     // X and M, a 16 x 16 block at a time
     constexpr int UNITS = MT * (MT + 1) / 2;
-    for (int unit = warp; unit < 2 * UNITS; unit += D / 16) {
+    for (int unit = warp; unit < 2 * UNITS; unit += THREADS / 32) {
         const bool of_m = unit >= UNITS;
         int mt = 0, np = unit % UNITS;
         while (np > mt) np -= ++mt;
@@ -372,11 +372,11 @@ __global__ void __launch_bounds__(D * 2) vla_delta_grads_kernel(const __grid_con
             }
     }
 
-    // dq and dk of the warp's 16 columns: first the states
-    const int col0 = warp * 16;
-    float dq[MT][2][4] = {}, dk[MT][2][4] = {}, small[3][MT][2][4] = {};
-    float(&ql)[MT][2][4] = NP > 1 ? small[0] : dq;  // fp32 results: the small products apart
-    float(&kl)[MT][2][4] = NP > 1 ? small[1] : dk;
+    // dq and dk of the warp's 16 columns at its tokens: first the states
+    const int col0 = warp % (D / 16) * 16, m0 = warp / (D / 16) * MH;
+    float dq[MH][2][4] = {}, dk[MH][2][4] = {}, small[3][MH][2][4] = {};
+    float(&ql)[MH][2][4] = NP > 1 ? small[0] : dq;  // fp32 results: the small products apart
+    float(&kl)[MH][2][4] = NP > 1 ? small[1] : dk;
     // the parts of 16 rows of a state at the warp's columns, as B operands
     auto state_of = [&](const float* S, int ks, auto& w) {
         constexpr int N = sizeof(w) / 16;
@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(D * 2) vla_delta_grads_kernel(const __grid_con
         }
     };
     const size_t at = ((size_t)bh * (p.blocks + 1) + blk) * D * D;
-#pragma unroll 2
+    const uint32_t rows_at = base + (m0 * 16 * LD + down_across<LD>(lane)) * 2;
+#pragma unroll 4
     for (int ks = 0; ks < D / 16; ++ks) {
         uint32_t w[UP][4], w1[NP][4];
         state_of(p.before + at, ks, w);
@@ -399,52 +400,52 @@ __global__ void __launch_bounds__(D * 2) vla_delta_grads_kernel(const __grid_con
 #pragma unroll
             for (int k = 0; k < 4; ++k) w1[q][k] = w[q][k];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int m = 0; m < MH; ++m) {
             uint32_t a[NP][4];
 #pragma unroll
-            for (int q = 0; q < NP; ++q) ldsm(a[q], base + L::O + q * L::PLANE + (mt * 16 * LD + ks * 16 + down_across<LD>(lane)) * 2);
-            mma_parts<NP>(dq[mt][0], ql[mt][0], a, w1, 0);
-            mma_parts<NP>(dq[mt][1], ql[mt][1], a, w1, 1);
+            for (int q = 0; q < NP; ++q) ldsm(a[q], rows_at + L::O + q * L::PLANE + (m * 16 * LD + ks * 16) * 2);
+            mma_parts<NP>(dq[m][0], ql[m][0], a, w1, 0);
+            mma_parts<NP>(dq[m][1], ql[m][1], a, w1, 1);
 #pragma unroll
-            for (int q = 0; q < NP; ++q) ldsm(a[q], base + L::V + q * L::PLANE + (mt * 16 * LD + ks * 16 + down_across<LD>(lane)) * 2);
-            mma_parts<NP>(dk[mt][0], kl[mt][0], a, w, 0);
-            mma_parts<NP>(dk[mt][1], kl[mt][1], a, w, 1);
+            for (int q = 0; q < NP; ++q) ldsm(a[q], rows_at + L::V + q * L::PLANE + (m * 16 * LD + ks * 16) * 2);
+            mma_parts<NP>(dk[m][0], kl[m][0], a, w, 0);
+            mma_parts<NP>(dk[m][1], kl[m][1], a, w, 1);
         }
     }
     {
-        float y[MT][2][4] = {};
-        float(&yl)[MT][2][4] = NP > 1 ? small[2] : y;
-#pragma unroll 2
+        float y[MH][2][4] = {};
+        float(&yl)[MH][2][4] = NP > 1 ? small[2] : y;
+#pragma unroll 4
         for (int ks = 0; ks < D / 16; ++ks) {
             uint32_t w[NP][4];
             state_of(p.behind + at, ks, w);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+            for (int m = 0; m < MH; ++m) {
                 uint32_t a[UP][4];
 #pragma unroll
-                for (int q = 0; q < UP; ++q) ldsm(a[q], base + L::U + q * L::PLANE + (mt * 16 * LD + ks * 16 + down_across<LD>(lane)) * 2);
-                mma_parts<UP>(y[mt][0], yl[mt][0], a, w, 0);
-                mma_parts<UP>(y[mt][1], yl[mt][1], a, w, 1);
+                for (int q = 0; q < UP; ++q) ldsm(a[q], rows_at + L::U + q * L::PLANE + (m * 16 * LD + ks * 16) * 2);
+                mma_parts<UP>(y[m][0], yl[m][0], a, w, 0);
+                mma_parts<UP>(y[m][1], yl[m][1], a, w, 1);
             }
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int m = 0; m < MH; ++m)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = mt * 16 + (e >> 1) * 8 + r;
+                    const int i = (m0 + m) * 16 + (e >> 1) * 8 + r;
                     if constexpr (NP > 1) {
-                        dq[mt][k][e] += ql[mt][k][e], dk[mt][k][e] += kl[mt][k][e], y[mt][k][e] += yl[mt][k][e];
-                        ql[mt][k][e] = kl[mt][k][e] = 0.f;
+                        dq[m][k][e] += ql[m][k][e], dk[m][k][e] += kl[m][k][e], y[m][k][e] += yl[m][k][e];
+                        ql[m][k][e] = kl[m][k][e] = 0.f;
                     }
-                    dq[mt][k][e] *= p.scale * gates[3 * TB + i];
-                    dk[mt][k][e] = fmaf(gates[4 * TB + i], y[mt][k][e], -gates[3 * TB + i] * dk[mt][k][e]);
+                    dq[m][k][e] *= p.scale * gates[3 * TB + i];
+                    dk[m][k][e] = fmaf(gates[4 * TB + i], y[m][k][e], -gates[3 * TB + i] * dk[m][k][e]);
                 }
     }
     __syncthreads();  // X and M are complete
     // ... then the pairs
-#pragma unroll
+#pragma unroll 1
     for (int ks = 0; ks < MT; ++ks) {
         uint32_t kk[NP][4], qq[NP][4];
 #pragma unroll
@@ -453,48 +454,48 @@ __global__ void __launch_bounds__(D * 2) vla_delta_grads_kernel(const __grid_con
             ldsm_t(qq[q], base + L::Q + q * L::PLANE + (ks * 16 * LD + col0 + down_across<LD>(lane)) * 2);
         }
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int m = 0; m < MH; ++m) {
+            const int mt = m0 + m;
+            uint32_t x[L::XP][4], y[L::MP][4];
             if (mt >= ks) {  // rows mt of X and M, columns ks
-                uint32_t x[L::XP][4], m[L::MP][4];
 #pragma unroll
                 for (int q = 0; q < L::XP; ++q) ldsm(x[q], base + L::X + q * L::XPLANE + (mt * 16 * XLD + ks * 16 + down_across<XLD>(lane)) * 2);
 #pragma unroll
-                for (int q = 0; q < L::MP; ++q) ldsm(m[q], base + L::M + q * L::XPLANE + (mt * 16 * XLD + ks * 16 + down_across<XLD>(lane)) * 2);
+                for (int q = 0; q < L::MP; ++q) ldsm(y[q], base + L::M + q * L::XPLANE + (mt * 16 * XLD + ks * 16 + down_across<XLD>(lane)) * 2);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    mma_parts<L::XP>(dq[mt][k], ql[mt][k], x, kk, k);
-                    mma_parts<L::MP>(dk[mt][k], kl[mt][k], m, kk, k);
+                    mma_parts<L::XP>(dq[m][k], ql[m][k], x, kk, k);
+                    mma_parts<L::MP>(dk[m][k], kl[m][k], y, kk, k);
                 }
             }
             if (mt <= ks) {  // rows ks, columns mt, transposed
-                uint32_t x[L::XP][4], m[L::MP][4];
 #pragma unroll
                 for (int q = 0; q < L::XP; ++q) ldsm_t(x[q], base + L::X + q * L::XPLANE + (ks * 16 * XLD + mt * 16 + across_down<XLD>(lane)) * 2);
 #pragma unroll
-                for (int q = 0; q < L::MP; ++q) ldsm_t(m[q], base + L::M + q * L::XPLANE + (ks * 16 * XLD + mt * 16 + across_down<XLD>(lane)) * 2);
+                for (int q = 0; q < L::MP; ++q) ldsm_t(y[q], base + L::M + q * L::XPLANE + (ks * 16 * XLD + mt * 16 + across_down<XLD>(lane)) * 2);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    mma_parts<L::XP>(dk[mt][k], kl[mt][k], x, qq, k);
-                    mma_parts<L::MP>(dk[mt][k], kl[mt][k], m, kk, k);
+                    mma_parts<L::XP>(dk[m][k], kl[m][k], x, qq, k);
+                    mma_parts<L::MP>(dk[m][k], kl[m][k], y, kk, k);
                 }
             }
         }
     }
     if constexpr (NP > 1) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) join(dq[mt], ql[mt]), join(dk[mt], kl[mt]);
+        for (int m = 0; m < MH; ++m) join(dq[m], ql[m]), join(dk[m], kl[m]);
     }
     float bad = 0.f;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int m = 0; m < MH; ++m)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-            const int i = mt * 16 + hf * 8 + r;
+            const int i = (m0 + m) * 16 + hf * 8 + r;
             if (i >= rows) continue;
             T *yq = row_of<T>(p.dq, b, h, t0 + i) + col0 + t2, *yk = row_of<T>(p.dk, b, h, t0 + i) + col0 + t2;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                float2 vq = make_float2(dq[mt][k][2 * hf], dq[mt][k][2 * hf + 1]), vk = make_float2(dk[mt][k][2 * hf], dk[mt][k][2 * hf + 1]);
+                float2 vq = make_float2(dq[m][k][2 * hf], dq[m][k][2 * hf + 1]), vk = make_float2(dk[m][k][2 * hf], dk[m][k][2 * hf + 1]);
                 if (i >= live) vq = vk = make_float2(0.f, 0.f);
                 bad = fmaf(vq.x, 0.f, fmaf(vq.y, 0.f, fmaf(vk.x, 0.f, fmaf(vk.y, 0.f, bad))));
                 if constexpr (NP == 1) {
