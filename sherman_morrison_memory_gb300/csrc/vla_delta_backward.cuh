@@ -225,7 +225,9 @@ struct DeltaGrads {
     static constexpr int UP = NP == 1 ? 2 : 3, XP = UP, MP = UP;
     static constexpr int LD = D + 8, PLANE = TB * LD * 2, XLD = TB + 8, XPLANE = TB * XLD * 2;
     static constexpr int Q = 0, K = Q + NP * PLANE, O = K + NP * PLANE, V = O + NP * PLANE, U = V + NP * PLANE,
-                         X = U + UP * PLANE, M = X + XP * XPLANE, GATES = M + MP * XPLANE, BYTES = GATES + 5 * TB * 4;
+                         X = U + UP * PLANE, M = X + XP * XPLANE, GATES = M + MP * XPLANE, RING = GATES + 5 * TB * 4;
+    // the states, 16 rows at a time, three of them under way
+    static constexpr int SLD = D + 4, SLICE = 16 * SLD * 4, SLICES = 4, BYTES = RING + SLICES * SLICE;
     static constexpr int THREADS = D * 4, MH = MT / 2;  // a warp's tiles of 16 tokens
 };
 
@@ -302,6 +304,17 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
     load(L::K, p.k);
     load(L::Q, p.q);
     cp_async_commit();
+    const size_t at = ((size_t)bh * (p.blocks + 1) + blk) * D * D;
+    auto slice = [&](int i) {  // the i-th 16 rows of S, then of R: 16 bytes a thread
+        if (i < D / 8) {
+            const float* from = (i < D / 16 ? p.before : p.behind) + at + (size_t)(i % (D / 16)) * 16 * D;
+            const int row = tid / (D / 4), c = tid % (D / 4) * 4;
+            cp_async16(vla::smem_u32(sm + L::RING + i % L::SLICES * L::SLICE) + (row * L::SLD + c) * 4, from + row * D + c, 16);
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < L::SLICES - 1; ++i) slice(i);
     {
         const float* E = p.E + ((size_t)bh * p.T + t0) * D;
 #pragma unroll 4
@@ -322,7 +335,7 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
                 *reinterpret_cast<uint4*>(sm + L::U + q * L::PLANE + (row * LD + c) * 2) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
         }
     }
-    cp_async_wait<0>();
+    cp_async_wait<L::SLICES - 1>();
     __syncthreads();
 
     const int r = lane >> 2, t2 = (lane & 3) * 2;
@@ -377,24 +390,27 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
     float dq[MH][2][4] = {}, dk[MH][2][4] = {}, small[3][MH][2][4] = {};
     float(&ql)[MH][2][4] = NP > 1 ? small[0] : dq;  // fp32 results: the small products apart
     float(&kl)[MH][2][4] = NP > 1 ? small[1] : dk;
-    // the parts of 16 rows of a state at the warp's columns, as B operands
-    auto state_of = [&](const float* S, int ks, auto& w) {
+    // the parts of the i-th 16 rows of the states at the warp's columns, as B operands
+    auto state_of = [&](int i, auto& w) {
         constexpr int N = sizeof(w) / 16;
+        cp_async_wait<L::SLICES - 2>();
+        __syncthreads();
+        slice(i + L::SLICES - 1);  // in the place of the one before, which everyone has read
+        const float* S = reinterpret_cast<const float*>(sm + L::RING + i % L::SLICES * L::SLICE) + col0 + r;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float* at = S + (size_t)(ks * 16 + (k & 1) * 8 + t2) * D + col0 + (k >> 1) * 8 + r;
+            const float* at = S + ((k & 1) * 8 + t2) * L::SLD + (k >> 1) * 8;
             uint32_t x[N];
-            split<N>(at[0], at[D], x);
+            split<N>(at[0], at[L::SLD], x);
 #pragma unroll
             for (int q = 0; q < N; ++q) w[q][k] = x[q];
         }
     };
-    const size_t at = ((size_t)bh * (p.blocks + 1) + blk) * D * D;
     const uint32_t rows_at = base + (m0 * 16 * LD + down_across<LD>(lane)) * 2;
-#pragma unroll 4
+#pragma unroll 2
     for (int ks = 0; ks < D / 16; ++ks) {
         uint32_t w[UP][4], w1[NP][4];
-        state_of(p.before + at, ks, w);
+        state_of(ks, w);
 #pragma unroll
         for (int q = 0; q < NP; ++q)
 #pragma unroll
@@ -415,10 +431,10 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
     {
         float y[MH][2][4] = {};
         float(&yl)[MH][2][4] = NP > 1 ? small[2] : y;
-#pragma unroll 4
+#pragma unroll 2
         for (int ks = 0; ks < D / 16; ++ks) {
             uint32_t w[NP][4];
-            state_of(p.behind + at, ks, w);
+            state_of(D / 16 + ks, w);
 #pragma unroll
             for (int m = 0; m < MH; ++m) {
                 uint32_t a[UP][4];
