@@ -164,11 +164,9 @@ __device__ __forceinline__ void to_operand(uint32_t (&a)[N][4], const float (&x0
         for (int i = 0; i < 4; ++i) a[p][i] = w[i][p];
 }
 
-// The sums of g up to each lane's token, as two floats whose sum holds 48 bits: a difference of sums far from zero
+// The sums of hi (+ lo) up to each lane, as two floats whose sum holds 48 bits: a difference of sums far from zero
 // keeps its precision.
-__device__ __forceinline__ void sums_of(float g, int lane, float& hi, float& lo) {
-    hi = g < -256.f ? -256.f : g;  // exp(-256) is 0
-    lo = 0.f;
+__device__ __forceinline__ void running_sums(float& hi, float& lo, int lane) {
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
         const float a = __shfl_up_sync(0xffffffffu, hi, m), al = __shfl_up_sync(0xffffffffu, lo, m);
@@ -178,6 +176,12 @@ __device__ __forceinline__ void sums_of(float g, int lane, float& hi, float& lo)
             hi = s;
         }
     }
+}
+// ... of g: exp(-256) is 0
+__device__ __forceinline__ void sums_of(float g, int lane, float& hi, float& lo) {
+    hi = g < -256.f ? -256.f : g;
+    lo = 0.f;
+    running_sums(hi, lo, lane);
 }
 
 // The helpers' part of a chunk: gates (warp 3), P and the inverse. Warps 0, 1, 2 have the 16 x 16 blocks (0, 0), (1, 0) and

@@ -226,8 +226,8 @@ struct DeltaGrads {
     static constexpr int LD = D + 8, PLANE = TB * LD * 2, XLD = TB + 8, XPLANE = TB * XLD * 2;
     static constexpr int Q = 0, K = Q + NP * PLANE, O = K + NP * PLANE, V = O + NP * PLANE, U = V + NP * PLANE,
                          X = U + UP * PLANE, M = X + XP * XPLANE, GATES = M + MP * XPLANE, RING = GATES + 5 * TB * 4;
-    // the states, 16 rows at a time, three of them under way
-    static constexpr int SLD = D + 4, SLICE = 16 * SLD * 4, SLICES = 4, BYTES = RING + SLICES * SLICE;
+    // the states, 32 rows at a time, two of them under way; the rows' shares of the gates' gradients
+    static constexpr int SLD = D + 4, SLICE = 32 * SLD * 4, SLICES = 3, SHARES = RING + SLICES * SLICE, BYTES = SHARES + (D / 16) * TB * 8;
     static constexpr int THREADS = D * 4, MH = MT / 2;  // a warp's tiles of 16 tokens
 };
 
@@ -252,34 +252,32 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
         }
         return;
     }
-    // gates: the sums of g as two floats, b, exp(G), exp(G_C - G)
-    float* gates = reinterpret_cast<float*>(sm + L::GATES);
-    if (warp == 0) {
-        double before = 0.0, G[TB / 32];
+    // what goes through registers is under way first
+    constexpr int EK = TB / 32;  // groups of eight values of E a thread
+    Raw8F e_raw[EK];
+    float e_beta[EK], share[3] = {}, g_in[TB / 32], b_in[TB / 32], end_in = 0.f;
 #pragma unroll
-        for (int k = 0; k < TB / 32; ++k) {
-            const int j = k * 32 + lane;
-            const float g = j < live && p.g.p ? *p.g.at(b, h, t0 + j) : 0.f;
-            double x = g < -256.f ? -256.0 : (double)g;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, x, m);
-                if (lane >= m) x += y;
-            }
-            G[k] = before + x;
-            before = __shfl_sync(0xffffffffu, G[k], 31);
-        }
-#pragma unroll
-        for (int k = 0; k < TB / 32; ++k) {
-            const int j = k * 32 + lane;
-            const float hi = (float)G[k];
-            gates[j] = hi;
-            gates[TB + j] = (float)(G[k] - (double)hi);
-            gates[2 * TB + j] = j < live ? *p.beta.at(b, h, t0 + j) : 0.f;
-            gates[3 * TB + j] = expf(hi);
-            gates[4 * TB + j] = expf((float)(before - G[k]));
+    for (int k = 0; k < EK; ++k) {
+        const int i = tid + k * THREADS, row = i / (D / 8), c = i % (D / 8) * 8;
+        e_raw[k] = {}, e_beta[k] = 0.f;
+        if (row < live) {
+            e_raw[k] = raw8(p.E + ((size_t)bh * p.T + t0 + row) * D + c);
+            e_beta[k] = *p.beta.at(b, h, t0 + row);
         }
     }
+    const int sj = tid % TB, sw = tid / TB;  // the thread's share: a token of 16 rows
+    if (sw < D / 16 && sj < live) {
+        const size_t i = ((size_t)bh * (D / 16) + sw) * p.T + t0 + sj;
+        share[0] = p.od[i], share[1] = p.vd[i], share[2] = p.bd[i];
+    }
+    if (warp == 0)
+#pragma unroll
+        for (int k = 0; k < TB / 32; ++k) {
+            const int j = k * 32 + lane;
+            g_in[k] = j < live && p.g.p ? *p.g.at(b, h, t0 + j) : 0.f;
+            b_in[k] = j < live ? *p.beta.at(b, h, t0 + j) : 0.f;
+        }
+    if (warp == THREADS / 32 - 1 && lane < D / 8) end_in = p.ends[((size_t)bh * p.blocks + blk) * (D / 8) + lane];
     auto load = [&](int at, const Seq& s) {
 #pragma unroll 4
         for (int i = tid; i < TB * (D / 8); i += THREADS) {
@@ -305,84 +303,132 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
     load(L::Q, p.q);
     cp_async_commit();
     const size_t at = ((size_t)bh * (p.blocks + 1) + blk) * D * D;
-    auto slice = [&](int i) {  // the i-th 16 rows of S, then of R: 16 bytes a thread
-        if (i < D / 8) {
-            const float* from = (i < D / 16 ? p.before : p.behind) + at + (size_t)(i % (D / 16)) * 16 * D;
-            const int row = tid / (D / 4), c = tid % (D / 4) * 4;
-            cp_async16(vla::smem_u32(sm + L::RING + i % L::SLICES * L::SLICE) + (row * L::SLD + c) * 4, from + row * D + c, 16);
+    auto slice = [&](int i) {  // the i-th 32 rows of S, then of R: 32 bytes a thread
+        if (i < D / 16) {
+            const float* from = (i < D / 32 ? p.before : p.behind) + at + (size_t)(i % (D / 32)) * 32 * D;
+            const uint32_t to = vla::smem_u32(sm + L::RING + i % L::SLICES * L::SLICE);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int row = tid / (D / 4) + k * 16, c = tid % (D / 4) * 4;
+                cp_async16(to + (row * L::SLD + c) * 4, from + row * D + c, 16);
+            }
         }
         cp_async_commit();
     };
 #pragma unroll
     for (int i = 0; i < L::SLICES - 1; ++i) slice(i);
-    {
-        const float* E = p.E + ((size_t)bh * p.T + t0) * D;
-#pragma unroll 4
-        for (int i = tid; i < TB * (D / 8); i += THREADS) {
-            const int row = i / (D / 8), c = i % (D / 8) * 8;
-            float x[8] = {};
-            if (row < live) {
-                load8(E + (size_t)row * D + c, x);
-                const float beta = *p.beta.at(b, h, t0 + row);
+    // the rows' shares of the gates' gradients: o . dO - v . dV and U' . E
+    float2* shares = reinterpret_cast<float2*>(sm + L::SHARES);
+    if (sw < D / 16) shares[sw * TB + sj] = make_float2(share[0] - share[1], share[2]);
+    // gates: the sums of g as two floats, b, exp(G), exp(G_C - G)
+    float* gates = reinterpret_cast<float*>(sm + L::GATES);
+    if (warp == 0) {
+        float hi[TB / 32], lo[TB / 32];
+        float all = 0.f, rest = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= beta;
-            }
-            uint32_t w[4][UP];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) split<UP>(x[2 * j], x[2 * j + 1], w[j]);
-#pragma unroll
-            for (int q = 0; q < UP; ++q)
-                *reinterpret_cast<uint4*>(sm + L::U + q * L::PLANE + (row * LD + c) * 2) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
+        for (int k = 0; k < TB / 32; ++k) {
+            sums_of(g_in[k], lane, hi[k], lo[k]);
+            const float s = all + hi[k], d = s - all;
+            lo[k] += rest + ((all - (s - d)) + (hi[k] - d));
+            hi[k] = s;
+            all = __shfl_sync(0xffffffffu, hi[k], 31), rest = __shfl_sync(0xffffffffu, lo[k], 31);
         }
+#pragma unroll
+        for (int k = 0; k < TB / 32; ++k) {
+            const int j = k * 32 + lane;
+            gates[j] = hi[k], gates[TB + j] = lo[k], gates[2 * TB + j] = b_in[k];
+            gates[3 * TB + j] = expf(hi[k] + lo[k]);
+            gates[4 * TB + j] = expf((all - hi[k]) + (rest - lo[k]));
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < EK; ++k) {
+        const int i = tid + k * THREADS, row = i / (D / 8), c = i % (D / 8) * 8;
+        float x[8];
+        open8(e_raw[k], x);
+        uint32_t w[4][UP];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split<UP>(x[2 * j] * e_beta[k], x[2 * j + 1] * e_beta[k], w[j]);
+#pragma unroll
+        for (int q = 0; q < UP; ++q)
+            *reinterpret_cast<uint4*>(sm + L::U + q * L::PLANE + (row * LD + c) * 2) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
     }
     cp_async_wait<L::SLICES - 1>();
     __syncthreads();
 
     const int r = lane >> 2, t2 = (lane & 3) * 2;
     const uint32_t base = vla::smem_u32(sm);
-    // X and M, a 16 x 16 block at a time
+    // X and M, a 16 x 16 block of both at a time
     constexpr int UNITS = MT * (MT + 1) / 2;
-    for (int unit = warp; unit < 2 * UNITS; unit += THREADS / 32) {
-        const bool of_m = unit >= UNITS;
-        int mt = 0, np = unit % UNITS;
+    for (int unit = warp; unit < UNITS; unit += THREADS / 32) {
+        int mt = 0, np = unit;
         while (np > mt) np -= ++mt;
-        float c[2][4] = {}, cl[2][4] = {};
-        const uint32_t a_at = base + (of_m ? L::V : L::O) + (mt * 16 * LD + down_across<LD>(lane)) * 2;
+        float c[2][2][4] = {}, cl[2][2][4] = {};
+        const uint32_t a_at = base + (mt * 16 * LD + down_across<LD>(lane)) * 2;
         const uint32_t b_at = base + L::U + (np * 16 * LD + across_down<LD>(lane)) * 2;
-#pragma unroll
+#pragma unroll 2
         for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t a[NP][4], u[UP][4];
+            uint32_t a[NP][4], v[NP][4], u[2][UP][2];
 #pragma unroll
-            for (int q = 0; q < NP; ++q) ldsm(a[q], a_at + q * L::PLANE + ks * 32);
+            for (int q = 0; q < NP; ++q) ldsm(a[q], a_at + L::O + q * L::PLANE + ks * 32);
 #pragma unroll
-            for (int q = 0; q < UP; ++q) ldsm(u[q], b_at + q * L::PLANE + ks * 32);
-            mma_parts<NP>(c[0], cl[0], a, u, 0);
-            mma_parts<NP>(c[1], cl[1], a, u, 1);
+            for (int q = 0; q < NP; ++q) ldsm(v[q], a_at + L::V + q * L::PLANE + ks * 32);
+#pragma unroll
+            for (int q = 0; q < UP; ++q) ldsm_pair(u, 0, q, b_at + q * L::PLANE + ks * 32);
+            mma_tiles<NP>(c[0], cl[0], a, u);
+            mma_tiles<NP>(c[1], cl[1], v, u);
         }
-        join(c, cl);
+        join(c[0], cl[0]);
+        join(c[1], cl[1]);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int i = mt * 16 + hf * 8 + r, j = np * 16 + k * 8 + t2;
-                float x[2];
+                float x[2], m[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const float w = expf((gates[i] - gates[j + q]) + (gates[TB + i] - gates[TB + j + q]));
-                    x[q] = (of_m ? j + q < i : j + q <= i) ? c[k][2 * hf + q] * w * (of_m ? -1.f : p.scale) : 0.f;
+                    x[q] = j + q <= i ? c[0][k][2 * hf + q] * w * p.scale : 0.f;
+                    m[q] = j + q < i ? -c[1][k][2 * hf + q] * w : 0.f;
                 }
-                if (of_m) {
-                    uint32_t w[L::MP];
-                    split<L::MP>(x[0], x[1], w);
+                uint32_t w[L::XP], y[L::MP];
+                split<L::XP>(x[0], x[1], w);
+                split<L::MP>(m[0], m[1], y);
 #pragma unroll
-                    for (int q = 0; q < L::MP; ++q) *reinterpret_cast<uint32_t*>(sm + L::M + q * L::XPLANE + (i * XLD + j) * 2) = w[q];
-                } else {
-                    uint32_t w[L::XP];
-                    split<L::XP>(x[0], x[1], w);
+                for (int q = 0; q < L::XP; ++q) *reinterpret_cast<uint32_t*>(sm + L::X + q * L::XPLANE + (i * XLD + j) * 2) = w[q];
 #pragma unroll
-                    for (int q = 0; q < L::XP; ++q) *reinterpret_cast<uint32_t*>(sm + L::X + q * L::XPLANE + (i * XLD + j) * 2) = w[q];
-                }
+                for (int q = 0; q < L::MP; ++q) *reinterpret_cast<uint32_t*>(sm + L::M + q * L::XPLANE + (i * XLD + j) * 2) = y[q];
             }
+    }
+    // The gates' gradients: the sums of the rows' shares, and of those over the tokens from the block's end. The last
+    // warp has no pairs, or few.
+    float bad = 0.f;
+    if (warp == THREADS / 32 - 1) {
+#pragma unroll
+        for (int m = 1; m < 16; m <<= 1) end_in += __shfl_xor_sync(0xffffffffu, end_in, m);
+        float behind = __shfl_sync(0xffffffffu, end_in, 0), rest = 0.f;
+#pragma unroll
+        for (int k = TB / 32 - 1; k >= 0; --k) {
+            const int j = k * 32 + 31 - lane;  // from the end
+            float db = 0.f, hi = 0.f, lo = 0.f;
+#pragma unroll
+            for (int w = 0; w < D / 16; ++w) {
+                const float2 y = shares[w * TB + j];
+                hi += y.x;
+                db += y.y;
+            }
+            running_sums(hi, lo, lane);
+            const float s = behind + hi, d = s - behind;
+            lo += rest + ((behind - (s - d)) + (hi - d));
+            float x = s + lo;
+            behind = __shfl_sync(0xffffffffu, s, 31), rest = __shfl_sync(0xffffffffu, lo, 31);
+            if (j >= rows) continue;
+            if (j >= live || (!p.S0 && t0 + j == 0)) x = 0.f;
+            bad = fmaf(x, 0.f, fmaf(db, 0.f, bad));
+            if (p.dg.p) *p.dg.at(b, h, t0 + j) = x;
+            *p.dbeta.at(b, h, t0 + j) = db;
+        }
     }
 
     // dq and dk of the warp's 16 columns at its tokens: first the states
@@ -393,10 +439,12 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
     // the parts of the i-th 16 rows of the states at the warp's columns, as B operands
     auto state_of = [&](int i, auto& w) {
         constexpr int N = sizeof(w) / 16;
-        cp_async_wait<L::SLICES - 2>();
-        __syncthreads();
-        slice(i + L::SLICES - 1);  // in the place of the one before, which everyone has read
-        const float* S = reinterpret_cast<const float*>(sm + L::RING + i % L::SLICES * L::SLICE) + col0 + r;
+        if (i % 2 == 0) {
+            cp_async_wait<L::SLICES - 2>();
+            __syncthreads();
+            slice(i / 2 + L::SLICES - 1);  // in the place of the one before, which everyone has read
+        }
+        const float* S = reinterpret_cast<const float*>(sm + L::RING + i / 2 % L::SLICES * L::SLICE) + i % 2 * 16 * L::SLD + col0 + r;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float* at = S + ((k & 1) * 8 + t2) * L::SLD + (k >> 1) * 8;
@@ -501,7 +549,6 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
 #pragma unroll
         for (int m = 0; m < MH; ++m) join(dq[m], ql[m]), join(dk[m], kl[m]);
     }
-    float bad = 0.f;
 #pragma unroll
     for (int m = 0; m < MH; ++m)
 #pragma unroll
@@ -523,35 +570,6 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
                 }
             }
         }
-    // the gates: sums over the warps' rows, and of them over the tokens from the block's end
-    if (warp == 0) {
-        double behind = 0.0;
-        for (int w = 0; w < D / 8; ++w) behind += (double)p.ends[((size_t)bh * p.blocks + blk) * (D / 8) + w];
-#pragma unroll
-        for (int k = TB / 32 - 1; k >= 0; --k) {
-            const int j = k * 32 + lane;
-            float db = 0.f;
-            double x = 0.0;
-            if (j < live)
-                for (int w = 0; w < D / 16; ++w) {
-                    const size_t i = ((size_t)bh * (D / 16) + w) * p.T + t0 + j;
-                    db += p.bd[i];
-                    x += (double)p.od[i] - (double)p.vd[i];
-                }
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double y = __shfl_down_sync(0xffffffffu, x, m);
-                if (lane + m < 32) x += y;
-            }
-            x += behind;
-            behind = __shfl_sync(0xffffffffu, x, 0);
-            if (j >= rows) continue;
-            if (j >= live || (!p.S0 && t0 + j == 0)) x = 0.0;
-            bad = fmaf((float)x, 0.f, fmaf(db, 0.f, bad));
-            if (p.dg.p) *p.dg.at(b, h, t0 + j) = (float)x;
-            *p.dbeta.at(b, h, t0 + j) = db;
-        }
-    }
     if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, (int)t0);
 }
 
