@@ -70,35 +70,41 @@ inline vla_status delta_run(DeltaArgs& p, cudaStream_t s) {
 // Tokens behind which a bf16 call's forward recurrence runs on tcgen05.
 constexpr int DELTA_TC = 64;
 
-template <int D, int R, bool TAPE>
+template <int D, int R, bool TAPE, bool BACK = false>
 inline vla_status delta_tc_run(DeltaArgs& p, cudaStream_t s) {
     using L = DeltaTc<D, R, TAPE>;
     const long long grid = (long long)p.B * p.H * (D > R ? D / R : 1);
     if (grid > 2147483647LL) return VLA_ERR_INVALID_ARG;
-    if (!allow_smem<vla_delta_tc_kernel<D, R, TAPE>>(L::BYTES)) return VLA_ERR_CUDA;
     DeltaMaps maps;
     const Seq* seq[4] = {&p.k, &p.q, &p.v, &p.dO};
     for (int i = 0; i < (TAPE ? 4 : 3); ++i) {
         const vla_seq x{seq[i]->p, seq[i]->sb, seq[i]->sh, seq[i]->st};
         if (!make_map(&maps.m[i], &x, p.B, p.H, p.T, D, DC)) return VLA_ERR_CUDA;
     }
-    vla_delta_tc_kernel<D, R, TAPE><<<(unsigned)grid, L::THREADS, L::BYTES, s>>>(p, maps);
+    if constexpr (BACK) {
+        if (!allow_smem<vla_delta_tc_reverse_kernel<D, R>>(L::BYTES)) return VLA_ERR_CUDA;
+        vla_delta_tc_reverse_kernel<D, R><<<(unsigned)grid, L::THREADS, L::BYTES, s>>>(p, maps);
+    } else {
+        if (!allow_smem<vla_delta_tc_kernel<D, R, TAPE>>(L::BYTES)) return VLA_ERR_CUDA;
+        vla_delta_tc_kernel<D, R, TAPE><<<(unsigned)grid, L::THREADS, L::BYTES, s>>>(p, maps);
+    }
     return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
+}
+
+// A bf16 recurrence on tcgen05: few heads of d = 128 take two blocks each.
+template <int D, bool TAPE, bool BACK = false>
+inline vla_status delta_tc_pick(DeltaArgs& p, cudaStream_t s) {
+    if constexpr (D == 128) {
+        if ((long long)p.B * p.H * 2 <= sm_count()) return delta_tc_run<D, 64, TAPE, BACK>(p, s);
+    }
+    return delta_tc_run<D, (D > 64 ? 128 : 64), TAPE, BACK>(p, s);
 }
 
 // The forward recurrence, or (TAPE) what its gradients need of it.
 template <int D, typename T, bool TAPE>
 inline vla_status delta_forward_run(DeltaArgs& p, cudaStream_t s) {
-    if constexpr (sizeof(T) == 2) {
-        if (p.T > DELTA_TC) {
-            if constexpr (D == 128) {
-                if ((long long)p.B * p.H * 2 > sm_count()) return delta_tc_run<128, 128, TAPE>(p, s);
-                return delta_tc_run<128, 64, TAPE>(p, s);
-            } else {
-                return delta_tc_run<D, D == 96 ? 128 : 64, TAPE>(p, s);
-            }
-        }
-    }
+    if constexpr (sizeof(T) == 2)
+        if (p.T > DELTA_TC) return delta_tc_pick<D, TAPE>(p, s);
     return delta_run<vla_delta_forward_kernel<D, T, TAPE>, D, typename DeltaForward<D, T, TAPE>::L>(p, s);
 }
 

@@ -64,8 +64,8 @@ struct DeltaTc {
 // Address of 16 bytes in a box: row `row`, group `j` of eight values
 __device__ __forceinline__ uint32_t in_box(int row, int j) { return (uint32_t)(row * 128 + ((j ^ (row & 7)) << 4)); }
 
-// prepare_chunk() for tiles in boxes, by a group of three warps; matrices in rows of i.
-template <typename L, int D>
+// prepare_chunk() for tiles in boxes, by a group of three warps; matrices in rows of i, or (BACK: of 1 + diag(b) N) of j.
+template <typename L, int D, bool BACK>
 __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, char* prep, float g, float beta, float scale, Whole& whole,
                                               int group, int hw, int lane) {
     float Gh, Gl;
@@ -89,11 +89,12 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
     float* own = reinterpret_cast<float*>(scratch) + 2 * 16 * NLD + hw * 3 * DC;  // the sums of g and b of each token
     own[lane] = Gh * 1.4426950408889634f, own[DC + lane] = Gl * 1.4426950408889634f, own[2 * DC + lane] = beta;
     __syncwarp();
-    float* N = reinterpret_cast<float*>(scratch) + (hw >> 1) * 16 * NLD;  // transposed
+    float* N = reinterpret_cast<float*>(scratch) + (hw >> 1) * 16 * NLD;  // BACK, else transposed
     auto part_at = [&](int part, int row, int j8) {  // eight values of a part of the inverse
         return in_box(row, (part & 1) * 4 + j8) + (part >> 1) * L::BOX;
     };
     float x[2][4];
+    uint32_t pw[4][L::PP];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         const int j = np * 16 + n * 8 + t2;
@@ -107,21 +108,40 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float w = exp2f((gi - (e ? gj.y : gj.x)) + (li - (e ? lj.y : lj.x)));
-                x[n][2 * hf + e] = j + e < i ? c[n][2 * hf + e] * w * (e ? bj.y : bj.x) : 0.f;
+                x[n][2 * hf + e] = j + e < i ? c[n][2 * hf + e] * w * (BACK ? own[2 * DC + i] : e ? bj.y : bj.x) : 0.f;
                 y[e] = j + e <= i ? c[2 + n][2 * hf + e] * w * scale : 0.f;
-                if (hw != 1) N[(n * 8 + t2 + e) * NLD + hf * 8 + r] = x[n][2 * hf + e];
+                if (hw != 1) N[BACK ? (hf * 8 + r) * NLD + n * 8 + t2 + e : (n * 8 + t2 + e) * NLD + hf * 8 + r] = x[n][2 * hf + e];
             }
-            uint32_t w[L::PP];
-            split<L::PP>(y[0], y[1], w);
+            split<L::PP>(y[0], y[1], pw[2 * n + hf]);
+            if constexpr (!BACK)
 #pragma unroll
-            for (int p = 0; p < L::PP; ++p)  // behind the inverse's three parts
-                *reinterpret_cast<uint32_t*>(prep + part_at(3 + p, i, np * 2 + n) + t2 * 2) = w[p];
+                for (int p = 0; p < L::PP; ++p)  // behind the inverse's three parts
+                    *reinterpret_cast<uint32_t*>(prep + part_at(3 + p, i, np * 2 + n) + t2 * 2) = pw[2 * n + hf][p];
         }
     }
+    if constexpr (BACK)
+#pragma unroll
+        for (int p = 0; p < L::PP; ++p)
+            stsm_t(vla::smem_u32(prep) + part_at(3 + p, np * 16 + across, mt * 2 + ((lane >> 3) & 1)), pw[0][p], pw[1][p], pw[2][p], pw[3][p]);
     if (hw != 1) {
         __syncwarp();
         float t[16];
         const int row = lane & 15;
+        if constexpr (BACK) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {  // (1 + N) T = 1, a lane a column
+                float s = i == row ? 1.f : 0.f, s2 = 0.f;
+#pragma unroll
+                for (int m = 0; m < i; m += 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(N + i * NLD + m);
+                    s = fmaf(-w.x, t[m], s);
+                    if (m + 1 < i) s2 = fmaf(-w.y, t[m + 1], s2);
+                    if (m + 2 < i) s = fmaf(-w.z, t[m + 2], s);
+                    if (m + 3 < i) s2 = fmaf(-w.w, t[m + 3], s2);
+                }
+                t[i] = s + s2;
+            }
+        } else
 #pragma unroll
         for (int j = 15; j >= 0; --j) {  // T (1 + N) = 1, a lane a row
             float s = j == row ? 1.f : 0.f, s2 = 0.f;
@@ -143,18 +163,14 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
             for (int p = 0; p < INV_PARTS; ++p) {
                 *reinterpret_cast<uint4*>(prep + part_at(p, mt * 16 + row, mt * 2)) = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
                 *reinterpret_cast<uint4*>(prep + part_at(p, mt * 16 + row, mt * 2 + 1)) = make_uint4(w[4][p], w[5][p], w[6][p], w[7][p]);
-                // nothing above the diagonal
-                if (mt == 0) {
-                    *reinterpret_cast<uint4*>(prep + part_at(p, row, 2)) = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(prep + part_at(p, row, 3)) = make_uint4(0u, 0u, 0u, 0u);
-                }
             }
-            if (mt == 0)
+            if (mt == (BACK ? 1 : 0)) {  // nothing above the diagonal
 #pragma unroll
-                for (int p = 0; p < L::PP; ++p) {
-                    *reinterpret_cast<uint4*>(prep + part_at(3 + p, row, 2)) = make_uint4(0u, 0u, 0u, 0u);
-                    *reinterpret_cast<uint4*>(prep + part_at(3 + p, row, 3)) = make_uint4(0u, 0u, 0u, 0u);
-                }
+                for (int p = 0; p < INV_PARTS + L::PP; ++p)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<uint4*>(prep + part_at(p, mt * 16 + row, (BACK ? 0 : 2) + k)) = make_uint4(0u, 0u, 0u, 0u);
+            }
         }
     }
     vla::named_bar(2 + group, 96);
@@ -172,7 +188,12 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
     uint32_t a[INV_PARTS][4], w[2][INV_PARTS][2];
     const uint32_t inv = vla::smem_u32(prep);
 #pragma unroll
-    for (int p = 0; p < INV_PARTS; ++p) ldsm_t(a[p], inv + part_at(p, across, (lane >> 3) & 1));
+    for (int p = 0; p < INV_PARTS; ++p) {
+        if constexpr (BACK)
+            ldsm(a[p], inv + part_at(p, down, lane >> 4));
+        else
+            ldsm_t(a[p], inv + part_at(p, across, (lane >> 3) & 1));
+    }
 #pragma unroll
     for (int n = 0; n < 2; ++n)  // eight rows of N21, their 16 values down
 #pragma unroll
@@ -187,10 +208,15 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
     join(y, yl);
     to_operand<INV_PARTS>(a, y[0], y[1]);
 #pragma unroll
-    for (int p = 0; p < INV_PARTS; ++p) ldsm_pair(w, 0, p, inv + part_at(p, 16 + across, 2 + ((lane >> 3) & 1)));
+    for (int p = 0; p < INV_PARTS; ++p) {
+        if constexpr (BACK)
+            ldsm_pair_t(w, 0, p, inv + part_at(p, 16 + down, 2 + (lane >> 4)));
+        else
+            ldsm_pair(w, 0, p, inv + part_at(p, 16 + across, 2 + ((lane >> 3) & 1)));
+    }
     mma_tiles<INV_PARTS>(z, zl, a, w);
     join(z, zl);
-    // its fragments are rows of j; blocks (j, i), (j + 8, i), (j, i + 8), (j + 8, i + 8) written as rows of i
+    // its fragments are rows of j: blocks (j, i), (j + 8, i), (j, i + 8), (j + 8, i + 8)
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -199,7 +225,12 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
 #pragma unroll
     for (int i = 0; i < 4; ++i) split<INV_PARTS>(z[i >> 1][(i & 1) * 2], z[i >> 1][(i & 1) * 2 + 1], v[i]);
 #pragma unroll
-    for (int p = 0; p < INV_PARTS; ++p) stsm_t(inv + part_at(p, 16 + across, (lane >> 3) & 1), v[0][p], v[1][p], v[2][p], v[3][p]);
+    for (int p = 0; p < INV_PARTS; ++p) {
+        if constexpr (BACK)
+            stmatrix4(inv + part_at(p, down, 2 + (lane >> 4)), v[0][p], v[1][p], v[2][p], v[3][p]);
+        else
+            stsm_t(inv + part_at(p, 16 + across, (lane >> 3) & 1), v[0][p], v[1][p], v[2][p], v[3][p]);
+    }
 }
 
 // 16 lanes, NT tiles of eight 32-bit columns, as fragments
@@ -411,7 +442,7 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
             // the three warps that meet at a barrier leave together if a wait ran out
             const bool ok = wait_warp(full + c % L::NST, c / L::NST) && (c < L::NPR || wait_warp(done + c % L::NPR, c / L::NPR - 1));
             if (vla::bar_red_or(2 + group, 96, !ok)) break;
-            prepare_boxes<L, D>(sm + L::N + group * L::SCRATCH, sb + L::stage_of(c), sm + L::PREPS + c % L::NPR * L::PREP, gc, bc, p.scale,
+            prepare_boxes<L, D, false>(sm + L::N + group * L::SCRATCH, sb + L::stage_of(c), sm + L::PREPS + c % L::NPR * L::PREP, gc, bc, p.scale,
                                 whole, group, hw, lane);
             vla::fence_proxy_async_smem();
             arrive_warp(prep_ready + c % L::NPR);
@@ -647,6 +678,442 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
         }
     }
     if constexpr (!TAPE) zero_tokens<T>(p.out, b, h, (long long)chunks * DC, p.T, row0, rows);
+    if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, 0);
+    vla::tc_fence_before();
+    __syncthreads();
+    if (warp == NW) {
+        vla::tc_fence_after();
+        vla::tc_dealloc(tm, L::COLS);
+    }
+}
+
+// The reverse recurrence (vla_delta_backward.cuh) in the same way, R rows of the states' gradient (R here, S in the code) on
+// the lanes; X, D and Z with j against i:
+//
+//   X[x][j] = sum_y R[x][y] k_j[y],   D[x][j] = sum_i dO_i[x] P[i][j]     A of D: dO from shared memory
+//   Z[x][j] = exp(G_C - G_j) X[x][j] + D[x][j],   U'[x][j] = sum_i Z[x][i] Inv[i][j]
+//   T[x][y] = sum_i (scale exp(G_i) dO_i[x]) q_i[y] - sum_j (b_j exp(G_j) U'[x][j]) k_j[y]    A: both in three parts
+//   R       = exp(G_C) R + T
+template <int D>
+struct ReverseTmem {
+    static constexpr int SB = 0, ZP = SB + 3 * (D / 2), A2 = ZP + 48, X = A2 + 48, PD = X + 32, TC = PD + 32;
+    static_assert(TC + D <= 512, "tensor memory");
+};
+
+template <int D, int R>
+__global__ void __launch_bounds__(DeltaTc<D, R, true>::THREADS, 1) vla_delta_tc_reverse_kernel(const __grid_constant__ DeltaArgs p,
+                                                                                           const __grid_constant__ DeltaMaps maps) {
+    using T = __nv_bfloat16;
+    using L = DeltaTc<D, R, true>;
+    using M = ReverseTmem<D>;
+    constexpr int SPAN = BLOCK<T>, NW = L::NW, W = L::W, SPLITS = D > R ? D / R : 1;
+    extern __shared__ __align__(1024) char delta_sm[];
+    char* sm = delta_sm;
+    const uint32_t sb = vla::smem_u32(sm);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + L::BAR);
+    uint64_t *full = bar, *prep_ready = full + L::NST, *done = prep_ready + L::NPR, *s_ready = done + L::NPR, *x_done = s_ready + 2,
+             *z_ready = x_done + 1, *e_done = x_done + 2, *f_ready = x_done + 3, *t_done = x_done + 4,
+             *drained = x_done + 5;
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC + 4);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int bh = blockIdx.x / SPLITS, row0 = blockIdx.x % SPLITS * R, b = bh / p.H, h = bh % p.H;
+    const int rows = min(R, D - row0);
+    const long long n = delta_len(p, b);
+    const int chunks = (int)((n + DC - 1) / DC);
+
+    if (tid == 0) {
+        for (int i = 0; i < L::NST; ++i) vla::mbar_init(full + i, 1);
+        for (int i = 0; i < L::NPR; ++i) vla::mbar_init(prep_ready + i, 3), vla::mbar_init(done + i, NW);
+        for (int i = 0; i < 2; ++i) vla::mbar_init(s_ready + i, NW);
+        vla::mbar_init(x_done, 1);
+        vla::mbar_init(z_ready, NW);
+        vla::mbar_init(e_done, 1);
+        vla::mbar_init(f_ready, NW);
+        vla::mbar_init(t_done, 1);
+        vla::mbar_init(drained, 1);
+        *abort_flag = 0;
+        vla::fence_mbar_init();
+    }
+    if (warp == NW) vla::tc_alloc(tmem_ptr, L::COLS);
+    vla::tc_fence_before();
+    __syncthreads();
+    vla::tc_fence_after();
+    const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_ptr, 0);
+    float bad = 0.f;
+
+    auto wait_warp = [&](uint64_t* w, uint32_t parity) {
+        if (__all_sync(0xffffffffu, vla::mbar_try_wait(w, parity & 1))) return true;
+        const bool ok = wait_on(w, parity & 1, abort_flag, p.wait_ns, p.status, warp / 4, bh);
+        return __all_sync(0xffffffffu, ok) != 0;
+    };
+    auto arrive_warp = [&](uint64_t* w) {  // one arrival a warp
+        __syncwarp();
+        if (lane == 0) vla::mbar_arrive(w);
+    };
+
+    if (warp == NW) {  // ---- MMAs, issued by one lane of a whole warp
+        const bool one = elect_one();
+        const uint32_t id32 = idesc_bf16(R, 32, 0, 0), id_o = idesc_bf16(R, 32, 1, 0), id_t = idesc_bf16(R, D, 0, 1);
+        const uint64_t dk = desc_sw128(0, 16, 1024), dm = desc_sw128(0, L::NB == 2 ? 2 * L::BOX : 16, 1024),
+                       dx = desc_sw128(0, L::VB == 2 ? L::BOX : 16, 1024);
+        auto at = [](uint64_t d, uint32_t addr) { return d + (uint64_t)(addr >> 4); };
+        auto part = [](int q) { return (uint32_t)((q & 1) * 64 + (q >> 1) * L::BOX); };
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t st = sb + L::stage_of(c), pr = sb + L::PREPS + c % L::NPR * L::PREP;
+            if (!wait_warp(full + c % L::NST, c / L::NST) || !wait_warp(prep_ready + c % L::NPR, c / L::NPR)) break;
+            vla::tc_fence_after();
+            if (one) {  // P^T dO
+#pragma unroll
+                for (int q = 2; q >= 0; --q)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        mma_ss(tm + M::PD, at(dx, st + L::V + k * 2048), at(dk, pr + part(3 + q) + k * 32), id_o, !(q == 2 && k == 0));
+            }
+            __syncwarp();
+            bool ok = true;
+#pragma unroll
+            for (int q = 0; q < L::PIECES; ++q) {
+                if (!(ok = wait_warp(s_ready + q, c))) break;
+                vla::tc_fence_after();
+                if (one) {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            if (ks % (W / 16) / 2 != q) continue;
+                            mma_ts(tm + M::X, tm + M::SB + i * (D / 2) + ks * 8, at(dk, st + (ks >> 2) * 2 * L::BOX + (ks & 3) * 32), id32,
+                                   q > 0 || i > 0 || ks > 0);
+                        }
+                    if (q + 1 == L::PIECES) vla::tc_commit(x_done);
+                }
+                __syncwarp();
+            }
+            if (!ok || !wait_warp(z_ready, c)) break;
+            vla::tc_fence_after();
+            if (one) {
+#pragma unroll
+                for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                    for (int q = 0; q <= sum; ++q)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            mma_ts(tm + M::X, tm + M::ZP + (sum - q) * 16 + k * 8, at(dk, pr + part(q) + k * 32), id32,
+                                   !(sum == 2 && q == 0 && k == 0));
+                vla::tc_commit(e_done);
+#pragma unroll
+                for (int i = 2; i >= 0; --i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        mma_ts(tm + M::TC, tm + M::A2 + i * 16 + k * 8, at(dm, st + L::BOX + k * 2048), id_t, !(i == 2 && k == 0));
+            }
+            __syncwarp();
+            if (!wait_warp(f_ready, c)) break;
+            vla::tc_fence_after();
+            if (one) {
+#pragma unroll
+                for (int i = 2; i >= 0; --i)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) mma_ts(tm + M::TC, tm + M::ZP + i * 16 + k * 8, at(dm, st + k * 2048), id_t, 1);
+                vla::tc_commit(t_done);
+            }
+            __syncwarp();
+        }
+        if (one) vla::tc_commit(drained);  // what was issued has finished before the block frees its TMEM
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, vla::mbar_try_wait(drained, 0))) vla::mbar_wait_slow(drained, 0, nullptr, p.wait_ns);
+        __syncwarp();
+    } else if (warp == NW + 1) {  // ---- loads
+        // Whole chunks by TMA, three ahead; a last one of fewer tokens, whose other rows are zero whatever memory
+        // holds there, by plain copies.
+        const bool one = elect_one();
+        constexpr int TILES = 4;
+        auto load = [&](int c) {
+            const long long t0 = (long long)(chunks - 1 - c) * DC;
+            const int live = (int)min((long long)DC, n - t0);
+            const uint32_t st = sb + L::stage_of(c);
+            uint64_t* w = full + c % L::NST;
+            if (live == DC) {
+                if (one) {
+                    vla::mbar_arrive_expect_tx(w, (2 * L::NB + (TILES - 2) * L::VB) * L::BOX);
+#pragma unroll
+                    for (int i = 0; i < L::NB; ++i) {
+                        tma_load(st + i * 2 * L::BOX, &maps.m[0], i * 64, (int)t0, h, b, w);
+                        tma_load(st + i * 2 * L::BOX + L::BOX, &maps.m[1], i * 64, (int)t0, h, b, w);
+                    }
+#pragma unroll
+                    for (int i = 0; i < L::VB; ++i) {
+                        tma_load(st + L::V + i * L::BOX, &maps.m[3], row0 + i * 64, (int)t0, h, b, w);
+                        tma_load(st + L::O + i * L::BOX, &maps.m[2], row0 + i * 64, (int)t0, h, b, w);
+                    }
+                }
+                __syncwarp();
+                return;
+            }
+#pragma unroll 1
+            for (int m = 0; m < TILES; ++m) {
+                const Seq& s = m == 0 ? p.k : m == 1 ? p.q : m == 2 ? p.dO : p.v;
+                const int boxes = m < 2 ? L::NB : L::VB, cols = m < 2 ? D : rows;
+                const uint32_t to = m == 0 ? 0 : m == 1 ? L::BOX : m == 2 ? L::V : L::O;
+                for (int i = lane; i < boxes * DC * 8; i += 32) {
+                    const int g8 = i % (boxes * 8), r = i / (boxes * 8);
+                    const bool on = r < live && g8 * 8 < cols;
+                    const T* src = row_of<T>(s, b, h, on ? t0 + r : t0) + (on ? (m < 2 ? 0 : row0) + g8 * 8 : 0);
+                    cp_async16(st + to + (g8 >> 3) * (m < 2 ? 2 * L::BOX : L::BOX) + in_box(r, g8 & 7), src, on ? 16 : 0);
+                }
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            vla::fence_proxy_async_smem();
+            arrive_warp(w);
+        };
+        int loaded = 0;
+        for (; loaded < chunks; ++loaded) {
+            const int before = loaded - L::NST;  // the stage's last chunk
+            if (before >= 0 && !wait_warp(done + before % L::NPR, before / L::NPR)) break;
+            if (!(p.stall && loaded + 1 == chunks)) load(loaded);
+        }
+        if (*abort_flag)  // leave only once the copies under way have landed
+            for (int c = max(0, loaded - L::NST); c < loaded && !(p.stall && c + 1 == chunks); ++c) {
+                if (!__all_sync(0xffffffffu, vla::mbar_try_wait(full + c % L::NST, (c / L::NST) & 1)))
+                    vla::mbar_wait_slow(full + c % L::NST, (c / L::NST) & 1, nullptr, p.wait_ns);
+                __syncwarp();
+            }
+    } else if (warp >= NW + 2) {  // ---- the helpers' part, two groups for every other chunk
+        const int group = (warp - NW - 2) / 3, hw = (warp - NW - 2) % 3;
+        Whole whole;
+        float g = 0.f, beta = 0.f;
+        auto gates = [&](int c) {
+            const long long t = (long long)(chunks - 1 - c) * DC + lane;
+            g = t >= 0 && t < n && p.g.p ? *p.g.at(b, h, t) : 0.f;
+            beta = t >= 0 && t < n ? *p.beta.at(b, h, t) : 0.f;
+        };
+        gates(group);
+        for (int c = group; c < chunks; c += L::GROUPS) {
+            const float gc = g, bc = beta;
+            gates(c + L::GROUPS);
+            // the three warps that meet at a barrier leave together if a wait ran out
+            const bool ok = wait_warp(full + c % L::NST, c / L::NST) && (c < L::NPR || wait_warp(done + c % L::NPR, c / L::NPR - 1));
+            if (vla::bar_red_or(2 + group, 96, !ok)) break;
+            prepare_boxes<L, D, true>(sm + L::N + group * L::SCRATCH, sb + L::stage_of(c), sm + L::PREPS + c % L::NPR * L::PREP, gc, bc, p.scale,
+                                whole, group, hw, lane);
+            vla::fence_proxy_async_smem();
+            arrive_warp(prep_ready + c % L::NPR);
+        }
+    } else if (warp < NW) {  // ---- S
+        const int quad = warp & 3, half = (warp >> 2) & 1, r = lane >> 2, t2 = (lane & 3) * 2;
+        const int xb = quad * (R / 4) + (warp >> 3) * 16;   // first of the warp's 16 rows in the block
+        const bool rows_in = xb < rows;                     // else zero throughout
+        const uint32_t lanes = tm + ((uint32_t)(quad * 32 + (warp >> 3) * 16) << 16);
+        float s[W / 8][4];
+        load_rows<D, W>(s, p.dS_T && rows_in ? p.dS_T + ((size_t)bh * D + row0 + xb) * D + half * W : nullptr, lane);
+        char* stage = sm + L::OUT + warp * 16 * L::OUT_LD * 2;
+        // a piece of S in three parts
+        auto publish = [&](int q) {
+            constexpr int NT = W % 32 == 0 ? 4 : 2;
+#pragma unroll
+            for (int k0 = 0; k0 < 4; k0 += NT) {
+                if (q * 4 + k0 >= W / 8) continue;
+                uint32_t v[3][2 * NT];
+#pragma unroll
+                for (int k = 0; k < NT; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t y[3];
+                        split<3>(s[q * 4 + k0 + k][2 * e], s[q * 4 + k0 + k][2 * e + 1], y);
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) v[i][2 * k + e] = y[i];
+                    }
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const uint32_t to = lanes + M::SB + i * (D / 2) + half * (W / 2) + (q * 4 + k0) * 4;
+                    if constexpr (NT == 4)
+                        st_frag8(to, *reinterpret_cast<const uint32_t(*)[8]>(v[i]));
+                    else
+                        st_frag4(to, v[i][0], v[i][1], v[i][2], v[i][3]);
+                }
+            }
+        };
+        auto ready = [&](uint64_t* w) {
+            vla::tc_wait_st();
+            vla::tc_fence_before();
+            arrive_warp(w);
+        };
+        auto parts16 = [&](auto nc, uint32_t col, const float (&x)[2][4]) {  // 16 rows x 16 tokens
+            constexpr int N = decltype(nc)::value;
+            uint32_t y[4][N];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split<N>(x[i >> 1][(i & 1) * 2], x[i >> 1][(i & 1) * 2 + 1], y[i]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) st_frag4(col + i * 16 + half * 8, y[0][i], y[1][i], y[2][i], y[3][i]);
+        };
+        if (chunks > 0) {
+#pragma unroll
+            for (int q = 0; q < L::PIECES; ++q) {
+                __syncwarp();
+                publish(q);
+                ready(s_ready + q);
+            }
+        }
+        // this warp's 16 columns of a chunk's tile at its 16 tokens
+        auto columns = [&](int c, int tile, float (&x)[2][4]) {
+            const int g16 = xb / 16;
+            uint32_t w[4];
+            ldsm_t(w, sb + L::stage_of(c) + tile + (g16 >> 2) * L::BOX +
+                          in_box(half * 16 + (lane & 7) + ((lane >> 4) << 3), (g16 & 3) * 2 + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                x[i][0] = low_of(w[2 * i]), x[i][1] = high_of(w[2 * i]), x[i][2] = low_of(w[2 * i + 1]), x[i][3] = high_of(w[2 * i + 1]);
+        };
+        T* dst = row_of<T>(p.dv, b, h, half * 16 + lane / 2) + row0 + xb + lane % 2 * 8;
+        const size_t shares = ((size_t)bh * (D / 16) + (row0 + xb) / 16) * p.T + half * 16;
+        auto first_of = [&](int c) { return (long long)(chunks - 1 - c) * DC; };
+        // chunk c's dV from the warp's buffer to its rows, up to T
+        auto write_out = [&](int c) {
+            const long long t0 = first_of(c);
+            if (rows_in && t0 + half * 16 + lane / 2 < p.T)
+                *reinterpret_cast<uint4*>(dst + t0 * p.dv.st) = *reinterpret_cast<const uint4*>(stage + (lane / 2 * L::OUT_LD + lane % 2 * 8) * 2);
+        };
+        bool ok = true;
+        for (int c = 0; c < chunks; ++c) {
+            const long long t0 = first_of(c);
+            const int live = (int)min(16LL, n - t0 - half * 16);  // of the warp's tokens
+            float e[2][4];
+            {
+                const float* E = p.E + ((size_t)bh * p.T + t0 + half * 16) * D + row0 + xb + r;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = i * 8 + t2 + (k & 1);
+                        e[i][k] = rows_in && j < live ? E[(size_t)j * D + (k & 2) * 4] : 0.f;
+                    }
+            }
+            if (rows_in && (c == 0 || (t0 + DC) % SPAN == 0)) {
+                const long long blk = t0 / SPAN;
+                const size_t own = (((size_t)bh * (p.blocks + 1) + blk) * D + row0 + xb) * D + half * W;
+                store_rows<D, W>(s, p.behind + own, lane);
+                const float* S = p.before + own + (size_t)D * D;
+                float dot = 0.f;
+#pragma unroll
+                for (int i = 0; i < W / 8; ++i) {
+                    const float2 y = *reinterpret_cast<const float2*>(S + r * D + i * 8 + t2);
+                    const float2 z = *reinterpret_cast<const float2*>(S + (r + 8) * D + i * 8 + t2);
+                    dot = fmaf(s[i][0], y.x, fmaf(s[i][1], y.y, fmaf(s[i][2], z.x, fmaf(s[i][3], z.y, dot))));
+                }
+#pragma unroll
+                for (int i = 1; i < 32; i <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
+                if (lane == 0) p.ends[((size_t)bh * p.blocks + blk) * (D / 8) + (row0 + xb) / 8 + half] = dot;
+            }
+            const float* gates = reinterpret_cast<const float*>(sm + L::PREPS + c % L::NPR * L::PREP + L::MATS) + half * 16;
+            if (!(ok = wait_warp(prep_ready + c % L::NPR, c / L::NPR))) break;  // behind its loads
+            float2 near[2], beta[2];
+            {  // scale exp(G) dO for the products with q
+                float x[2][4];
+                columns(c, L::V, x);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    near[i] = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + t2);
+                    beta[i] = *reinterpret_cast<const float2*>(gates + GATE_BETA + i * 8 + t2);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[i][k] *= p.scale * (k & 1 ? near[i].y : near[i].x);
+                }
+                __syncwarp();
+                parts16(std::integral_constant<int, 3>{}, lanes + M::A2, x);
+            }
+            if (c > 0) write_out(c - 1);
+            if (!(ok = wait_warp(x_done, c))) break;
+            vla::tc_fence_after();
+            {
+                float x[2][4], y[2][4];
+                __syncwarp();
+                ld_tiles<2>(lanes + M::X + half * 16, x);
+                ld_tiles<2>(lanes + M::PD + half * 16, y);
+                vla::tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 far = *reinterpret_cast<const float2*>(gates + GATE_FAR + i * 8 + t2);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[i][k] = fmaf(k & 1 ? far.y : far.x, x[i][k], y[i][k]);
+                }
+                parts16(std::integral_constant<int, 3>{}, lanes + M::ZP, x);
+            }
+            ready(z_ready);
+            float v[2][4], u[2][4];
+            columns(c, L::O, v);
+            if (!(ok = wait_warp(e_done, c))) break;
+            vla::tc_fence_after();
+            __syncwarp();
+            ld_tiles<2>(lanes + M::X + half * 16, u);
+            vla::tc_wait_ld();
+            {
+                float f[2][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) f[i][k] = u[i][k] * -((k & 1 ? near[i].y : near[i].x) * (k & 1 ? beta[i].y : beta[i].x));
+                parts16(std::integral_constant<int, 3>{}, lanes + M::ZP, f);
+            }
+            ready(f_ready);
+            // beside the products of T: dV, and the rows' shares of the gates' gradients
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float bt = k ? beta[i].y : beta[i].x;
+                    const float bd = over_rows(fmaf(u[i][k], e[i][k], u[i][2 + k] * e[i][2 + k]));
+                    u[i][k] *= bt, u[i][2 + k] *= bt;
+                    const float vd = over_rows(fmaf(u[i][k], v[i][k], u[i][2 + k] * v[i][2 + k]));
+                    const int j = i * 8 + t2 + k;
+                    if (j >= live)
+                        u[i][k] = u[i][2 + k] = 0.f;
+                    else if (lane < 4 && rows_in)
+                        p.bd[shares + t0 + j] = bd, p.vd[shares + t0 + j] = vd;
+                    bad = fmaf(u[i][k], 0.f, fmaf(u[i][2 + k], 0.f, bad));
+                }
+            __syncwarp();
+            stsm_t(vla::smem_u32(stage) + across_down<L::OUT_LD>(lane) * 2, pack_bf16(u[0][0], u[0][1]), pack_bf16(u[0][2], u[0][3]),
+                   pack_bf16(u[1][0], u[1][1]), pack_bf16(u[1][2], u[1][3]));
+            __syncwarp();
+            const float whole = gates[GATE_WHOLE - half * 16];
+            if (!(ok = wait_warp(t_done, c))) break;
+            vla::tc_fence_after();
+            arrive_warp(done + c % L::NPR);
+#pragma unroll
+            for (int q = 0; q < L::PIECES; ++q) {
+                constexpr int NT = W % 32 == 0 ? 4 : 2;
+                __syncwarp();
+                float y[4][4];
+#pragma unroll
+                for (int k0 = 0; k0 < 4; k0 += NT)
+                    if (q * 4 + k0 < W / 8) ld_tiles<NT>(lanes + M::TC + half * W + (q * 4 + k0) * 8, y + k0);
+                vla::tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2)
+                        if (q * 4 + k < W / 8) {
+                            float* to = s[q * 4 + k] + i;
+                            const float2 w = __ffma2_rn(make_float2(whole, whole), make_float2(to[0], to[1]), make_float2(y[k][i], y[k][i + 1]));
+                            to[0] = w.x, to[1] = w.y;
+                        }
+                if (c + 1 < chunks) {
+                    publish(q);
+                    ready(s_ready + q);
+                }
+            }
+        }
+        if (ok && chunks > 0) write_out(chunks - 1);
+        if (ok && rows_in && p.dS0) {
+            store_rows<D, W>(s, p.dS0 + ((size_t)bh * D + row0 + xb) * D + half * W, lane);
+#pragma unroll
+            for (int m = 0; m < W / 8; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) bad = fmaf(s[m][i], 0.f, bad);
+        }
+    }
+    zero_tokens<T>(p.dv, b, h, (long long)chunks * DC, p.T, row0, rows);
     if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, 0);
     vla::tc_fence_before();
     __syncthreads();
