@@ -87,7 +87,7 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
     }
     const int r = lane >> 2, t2 = (lane & 3) * 2;
     float* own = reinterpret_cast<float*>(scratch) + 2 * 16 * NLD + hw * 3 * DC;  // the sums of g and b of each token
-    own[lane] = Gh * 1.4426950408889634f, own[DC + lane] = Gl * 1.4426950408889634f, own[2 * DC + lane] = beta;
+    own[lane] = Gh, own[DC + lane] = Gl, own[2 * DC + lane] = beta;
     __syncwarp();
     float* N = reinterpret_cast<float*>(scratch) + (hw >> 1) * 16 * NLD;  // BACK, else transposed
     auto part_at = [&](int part, int row, int j8) {  // eight values of a part of the inverse
@@ -107,7 +107,7 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
             float y[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float w = exp2f((gi - (e ? gj.y : gj.x)) + (li - (e ? lj.y : lj.x)));
+                const float w = exp2f(((gi - (e ? gj.y : gj.x)) + (li - (e ? lj.y : lj.x))) * 1.4426950408889634f);
                 x[n][2 * hf + e] = j + e < i ? c[n][2 * hf + e] * w * (BACK ? own[2 * DC + i] : e ? bj.y : bj.x) : 0.f;
                 y[e] = j + e <= i ? c[2 + n][2 * hf + e] * w * scale : 0.f;
                 if (hw != 1) N[BACK ? (hf * 8 + r) * NLD + n * 8 + t2 + e : (n * 8 + t2 + e) * NLD + hf * 8 + r] = x[n][2 * hf + e];

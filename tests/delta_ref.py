@@ -56,8 +56,8 @@ def delta(q, k, v, g, beta, scale=1.0, state=None, lengths=None):
 
 
 def delta_grads(q, k, v, g, beta, scale, state, do, dS, lengths=None):
-    """dq, dk, dv, dg, dbeta, dS0 by the reverse recurrence, and the magnitudes of dq's and dk's terms that are
-    rounded once."""
+    """dq, dk, dv, dg, dbeta, dS0 by the reverse recurrence, the magnitudes of dq's and dk's terms that are rounded
+    once, and |R k| |e| of dbeta's scalar products."""
     q, k, v, g, beta, state, do, dS = (_in(x) for x in (q, k, v, g, beta, state, do, dS))
     B, H, T, d = q.shape
     g = torch.zeros(B, H, T, dtype=torch.float64) if g is None else g
@@ -76,7 +76,7 @@ def delta_grads(q, k, v, g, beta, scale, state, do, dS, lengths=None):
         S = D + (beta[:, :, t, None] * e)[..., :, None] * k[:, :, t, None, :]
         Ds.append(D), es.append(e), Ss.append(S)
     dq, dk, dv = (torch.zeros_like(q) for _ in range(3))
-    dg, db = (torch.zeros_like(g) for _ in range(2))
+    dg, db, mb = (torch.zeros_like(g) for _ in range(3))
     for t in reversed(range(T)):
         if t == T - 1 or (t + 1) % BLOCK == 0:
             ends[t // BLOCK] = R
@@ -85,6 +85,7 @@ def delta_grads(q, k, v, g, beta, scale, state, do, dS, lengths=None):
         R = R + scale * do[:, :, t, :, None] * q[:, :, t, None, :]
         du = (R @ k[:, :, t, :, None])[..., 0]
         db[:, :, t] = (du * e).sum(-1)
+        mb[:, :, t] = du.norm(dim=-1) * e.norm(dim=-1)
         dv[:, :, t] = beta[:, :, t, None] * du
         dk[:, :, t] = ((beta[:, :, t, None] * e)[..., None, :] @ R - dv[:, :, t, None, :] @ D)[..., 0, :]
         R = R - dv[:, :, t, :, None] * k[:, :, t, None, :]
@@ -102,7 +103,7 @@ def delta_grads(q, k, v, g, beta, scale, state, do, dS, lengths=None):
         mk[:, :, at] = (far * (u @ R1.abs()) + near * (dv[:, :, at].abs() @ S0.abs()) + pairs @ k[:, :, at].abs()
                         + pairs.transpose(-1, -2) @ k[:, :, at].abs())
     zero = lambda x: torch.where(live if x.dim() == 3 else live[..., None], x, 0.0)  # noqa: E731
-    return (zero(dq), zero(dk), dv, zero(dg), zero(db), R), (mq, mk)
+    return (zero(dq), zero(dk), dv, zero(dg), zero(db), R), (mq, mk, zero(mb))
 
 
 def assert_normwise(x, ref, limit, what):
