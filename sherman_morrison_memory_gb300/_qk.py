@@ -2,12 +2,13 @@
 with the conventions of _layer.py."""
 from __future__ import annotations
 
+import ctypes
 import functools
 from typing import Optional
 
 import torch
 
-from ._binding import _DTYPES, _call_buffer, load_library
+from ._binding import _DTYPES, _call_buffer, _Seq, load_library
 from ._layer import _check_f32, _check_out, _check_seq, _done, _handle, _norm_weight, _on, _ptr, _seq, _seq_in
 
 
@@ -24,6 +25,17 @@ def vla_rotation_frequencies(rot: int, base: float = 10000.0, device=None) -> to
         raise ValueError(f"rot must be a positive multiple of 16, got {rot}")
     device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     return float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+
+
+def _rows(x: torch.Tensor):
+    """x where the kernels can read it (copied if it has to be) and its vla_seq. The common case, every stride positive
+    and a multiple of 16 bytes, is decided here: small calls are bound by this file's work."""
+    s0, s1, s2, s3 = x.stride()
+    p = x.data_ptr()
+    if s3 == 1 and not p & 15 and s0 > 0 and s1 > 0 and s2 > 0 and not (s0 | s1 | s2) & (7 if x.dtype == torch.bfloat16 else 3):
+        return x, ctypes.byref(_Seq(p, s0, s1, s2))
+    x = _seq_in(x)
+    return x, _seq(x)
 
 
 def _rotation(freqs, positions, B, T, d, dev):
@@ -77,18 +89,18 @@ def vla_qk_norm(q: torch.Tensor, k: torch.Tensor, weight_q: Optional[torch.Tenso
         wq, wk = _weights(weight_q, weight_k, H, d, dev)
         freqs, rot, positions, stride = _rotation(freqs, positions, B, T, d, dev)
         if out is None:
-            yq, yk = (torch.empty((B, H, T, d), dtype=q.dtype, device=dev) for _ in range(2))
+            yq, yk = torch.empty((2, B, H, T, d), dtype=q.dtype, device=dev).unbind(0)
         else:
             yq, yk = out
             for i, x in enumerate((yq, yk)):
                 _check_out(x, (B, H, T, d), q.dtype, dev, f"out[{i}]", strided=True)
-        rstd = torch.empty((2, B, H, T), dtype=torch.float32, device=dev)
-        q, k = _seq_in(q), _seq_in(k)
-        st = lib.vla_qk_norm(_seq(q), _seq(k), _DTYPES[q.dtype], B, H, T, d, _ptr(wq), _ptr(wk),
-                             int(wq is not None and wq.dim() == 1), int(bool(unit)), eps, _ptr(freqs), rot, _ptr(positions),
-                             stride, _seq(yq), _seq(yk), _ptr(rstd[0]), _ptr(rstd[1]), _handle(dev, stream))
+        rstd = torch.empty((2, B, H, T), dtype=torch.float32, device=dev).unbind(0)
+        (q, sq), (k, sk) = _rows(q), _rows(k)
+        st = lib.vla_qk_norm(sq, sk, _DTYPES[q.dtype], B, H, T, d, _ptr(wq), _ptr(wk), int(wq is not None and wq.dim() == 1),
+                             int(bool(unit)), eps, _ptr(freqs), rot, _ptr(positions), stride, _seq(yq), _seq(yk),
+                             rstd[0].data_ptr(), rstd[1].data_ptr(), _handle(dev, stream))
     _done(st, "vla_qk_norm", dev, stream, False)
-    return (yq, yk), (rstd[0], rstd[1])
+    return (yq, yk), rstd
 
 
 def vla_qk_norm_backward(grad_q: torch.Tensor, grad_k: torch.Tensor, q: torch.Tensor, k: torch.Tensor, stats,
@@ -117,7 +129,7 @@ def vla_qk_norm_backward(grad_q: torch.Tensor, grad_k: torch.Tensor, q: torch.Te
         rstd_k = _check_f32(rstd_k, (B, H, T), dev, "rstd_k")
         freqs, rot, positions, stride = _rotation(freqs, positions, B, T, d, dev)
         if out is None:
-            dq, dk = (torch.empty((B, H, T, d), dtype=q.dtype, device=dev) for _ in range(2))
+            dq, dk = torch.empty((2, B, H, T, d), dtype=q.dtype, device=dev).unbind(0)
         else:
             dq, dk = out
             for i, x in enumerate((dq, dk)):
@@ -128,8 +140,8 @@ def vla_qk_norm_backward(grad_q: torch.Tensor, grad_k: torch.Tensor, q: torch.Te
             dwq, dwk = torch.empty_like(wq), torch.empty_like(wk)
             nbytes = _scratch(B, H, T, d, dev.index)
             scratch = _call_buffer(dev, nbytes, False) if nbytes else None
-        q, k, grad_q, grad_k = (_seq_in(x) for x in (q, k, grad_q, grad_k))
-        st = lib.vla_qk_norm_backward(_seq(grad_q), _seq(grad_k), _seq(q), _seq(k), _DTYPES[q.dtype], B, H, T, d, _ptr(wq),
+        (q, sq), (k, sk), (grad_q, sgq), (grad_k, sgk) = _rows(q), _rows(k), _rows(grad_q), _rows(grad_k)
+        st = lib.vla_qk_norm_backward(sgq, sgk, sq, sk, _DTYPES[q.dtype], B, H, T, d, _ptr(wq),
                                       _ptr(wk), int(wq is not None and wq.dim() == 1), int(bool(unit)), _ptr(freqs), rot,
                                       _ptr(positions), stride, _ptr(rstd_q), _ptr(rstd_k), _seq(dq), _seq(dk), _ptr(dwq),
                                       _ptr(dwk), _ptr(scratch), nbytes, _handle(dev, stream))

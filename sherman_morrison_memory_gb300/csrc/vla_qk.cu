@@ -12,8 +12,13 @@
 // whole numbers, so that a far position loses nothing and no product in 64-bit floating
 // point is left but one a frequency and block. A warp takes a head's q or k rows, its
 // weight in registers; a lane holds eight values of a row and the eight they are turned
-// with, in fp32, and has the loads of several rows under way. (q and k of 32 heads of
-// 32,768 tokens, d = 128, bf16: see the table of measured forms at launch_forward().)
+// with, in fp32, and has the loads of several rows under way.
+//
+// Measured: q and k of 32 heads of 32,768 tokens, d = 128, bf16: forward 183 us (1.07 GB, 5.85 TB/s), 164 without the
+// rotation; gradients 412 us (1.61 GB, 3.9 TB/s), which are short of registers for loads under way: two blocks of 128
+// registers a thread on an SM. Loads through a ring of shared memory instead were slower (244 and 529 us), as was
+// fetching a row's successors while it is worked on (469 us: it spills). fp32 operations in pairs took the forward
+// pass from 214 to 183 us, the gradients from 468 to 432.
 #include <cmath>
 #include <type_traits>
 
@@ -42,11 +47,13 @@ struct QkArgs {
     float* partial;         // backward: [B][spans][2][H][d] sums dz n
 };
 
-template <int D>
+template <int D, bool BACKWARD>
 struct QkLay {
     static constexpr int L = D / 16;          // lanes of a row
     static constexpr int ROWS = 32 / L;       // rows of a warp at a time (d = 96: five, of 30 lanes)
-    static constexpr int DEEP = 4, TT = ROWS * DEEP;  // tokens of a tile
+    // rows of a lane in a tile (q and k of 32 heads of 32,768 tokens, d = 128: forward 182 us for 4, 190 for 8, gradients
+    // 432 and 408)
+    static constexpr int DEEP = BACKWARD ? 8 : 4, TT = ROWS * DEEP;
 };
 
 // The sum over a row's lanes, the same in each.
@@ -74,12 +81,11 @@ __device__ __forceinline__ float2 turn_of(unsigned long long u) {
     return make_float2((quarter + 1) & 2 ? -x : x, quarter & 2 ? -y : y);
 }
 
-// The tile's (cos, sin): frequency 8 l + j of a token is at [token][j / 2][l], two frequencies to a float4, so that
-// the lanes of a row read in order.
-template <int D>
-__device__ __forceinline__ void make_turns(const QkArgs& a, float2* turns, const unsigned long long* fraction, const bool* odd, int b,
+// The tile's cosines and sines: frequencies 8 l + j and j + 1 of a token are at [token][j / 2][l], two cosines and two
+// sines to a float4, so that the lanes of a row read in order.
+template <typename Q>
+__device__ __forceinline__ void make_turns(const QkArgs& a, float* turns, const unsigned long long* fraction, const bool* odd, int b,
                                            long long t0) {
-    using Q = QkLay<D>;
     const int m = a.rot / 2, per = a.rot / 16;
     for (int i = threadIdx.x; i < Q::TT * m; i += QK_THREADS) {
         const int tok = i / m, f = i - tok * m;
@@ -87,8 +93,9 @@ __device__ __forceinline__ void make_turns(const QkArgs& a, float2* turns, const
         if (t >= a.T) break;
         const int pos = a.pos ? a.pos[b * a.pos_sb + t] : (int)t;
         const float nan = __int_as_float(0x7FC00000);
-        turns[((tok * 4 + (f & 7) / 2) * per + f / 8) * 2 + (f & 1)] =
-            odd[f] ? make_float2(nan, nan) : turn_of((unsigned long long)(long long)pos * fraction[f]);
+        const float2 w = odd[f] ? make_float2(nan, nan) : turn_of((unsigned long long)(long long)pos * fraction[f]);
+        float* at = turns + ((tok * 4 + (f & 7) / 2) * per + f / 8) * 4 + (f & 1);
+        at[0] = w.x, at[2] = w.y;
     }
 }
 
@@ -105,27 +112,44 @@ __device__ __forceinline__ void make_fractions(const QkArgs& a, unsigned long lo
     __syncthreads();
 }
 
+// Eight values as pairs: two fp32 operations an instruction, which is what the passes are short of beside memory.
+__device__ __forceinline__ void open_pairs(const Raw8F& r, float2 (&x)[4]) {
+    x[0] = make_float2(r.a.x, r.a.y), x[1] = make_float2(r.a.z, r.a.w), x[2] = make_float2(r.b.x, r.b.y), x[3] = make_float2(r.b.z, r.b.w);
+}
+__device__ __forceinline__ void open_pairs(const uint4& r, float2 (&x)[4]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store_pairs(float* p, const float2 (&x)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+}
+__device__ __forceinline__ void store_pairs(__nv_bfloat16* p, const float2 (&x)[4]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y), pack_bf16(x[2].x, x[2].y), pack_bf16(x[3].x, x[3].y));
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // a and b, a lane's values and those they are turned with, by +- the token's angles
 template <int SIGN>
-__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float2* turns, int tok, int per, int l) {
+__device__ __forceinline__ void turn(float2 (&a)[4], float2 (&b)[4], const float* turns, int tok, int per, int l) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float4 w = *reinterpret_cast<const float4*>(turns + ((tok * 4 + i) * per + l) * 2);
-        const float c[2] = {w.x, w.z}, s[2] = {SIGN * w.y, SIGN * w.w};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float x = a[2 * i + e], y = b[2 * i + e];
-            a[2 * i + e] = fmaf(x, c[e], -y * s[e]);
-            b[2 * i + e] = fmaf(y, c[e], x * s[e]);
-        }
+        const float4 w = *reinterpret_cast<const float4*>(turns + ((tok * 4 + i) * per + l) * 4);  // two cosines, two sines
+        const float2 c = make_float2(w.x, w.y), s = make_float2(SIGN * w.z, SIGN * w.w), x = a[i], y = b[i];
+        a[i] = __ffma2_rn(x, c, __fmul2_rn(y, make_float2(-s.x, -s.y)));
+        b[i] = __ffma2_rn(y, c, __fmul2_rn(x, s));
     }
 }
 
 template <int D, typename T, bool BACKWARD>
-__global__ void __launch_bounds__(QK_THREADS) vla_qk_kernel(const __grid_constant__ QkArgs a) {
-    using Q = QkLay<D>;
-    constexpr int L = Q::L, AT_ONCE = sizeof(T) == 4 || BACKWARD ? 2 : 4;  // rows of a lane under way
-    __shared__ __align__(16) float2 turns[Q::TT * D / 2];
+__global__ void __launch_bounds__(QK_THREADS, sizeof(T) == 4 && !BACKWARD ? 3 : 2) vla_qk_kernel(const __grid_constant__ QkArgs a) {
+    using Q = QkLay<D, BACKWARD>;
+    // rows of a lane under way, as the registers of two blocks on an SM (three: fp32 forward) allow: d = 96, 8 x 16 heads of
+    // 4,096, bf16: gradients 232 us for 1, 209 for 2, more for 4, whose registers spill; fp32, d = 64, 4 x 16 heads: forward
+    // 56.9 us for 1, 61.8 for 2
+    constexpr int L = Q::L, AT_ONCE = sizeof(T) == 4 ? 1 : BACKWARD ? 2 : 4;
+    __shared__ __align__(16) float turns[2][Q::TT * D];                    // of a tile and of the next one
     __shared__ unsigned long long fraction[D / 2];
     __shared__ bool odd[D / 2];
     const int span = blockIdx.x % a.spans, bg = blockIdx.x / a.spans, h0 = bg % a.groups * a.heads, b = bg / a.groups;
@@ -133,137 +157,145 @@ __global__ void __launch_bounds__(QK_THREADS) vla_qk_kernel(const __grid_constan
     const int P = a.rot ? a.rot / 16 : L;  // lanes whose two groups are turned with each other
     const bool turned = a.rot && l < P, on = row < Q::ROWS;
     const int c0 = (l < P ? l : P + l) * 8, c1 = (l < P ? l + P : L + l) * 8;
-    if (a.rot) make_fractions(a, fraction, odd);
-    float dw[2][8] = {};
-    for (int k = 0; k < a.tiles; ++k) {
-        const long long t0 = ((long long)span * a.tiles + k) * Q::TT;
-        if (t0 >= a.T) break;
-        if (a.rot) {
-            if (k) __syncthreads();
-            make_turns<D>(a, turns, fraction, odd, b, t0);
-            __syncthreads();
-        }
+    const long long first = (long long)span * a.tiles * Q::TT;
+    const int tiles = (int)min((long long)a.tiles, (a.T - first + Q::TT - 1) / Q::TT);
+    if (a.rot) {
+        make_fractions(a, fraction, odd);
+        make_turns<Q>(a, turns[0], fraction, odd, b, first);
+        __syncthreads();
+    }
+    float2 dw[2][4] = {};
+#pragma unroll 1
+    for (int k = 0; k < tiles; ++k) {
+        const long long t0 = first + (long long)k * Q::TT;
+        if (a.rot && k + 1 < tiles) make_turns<Q>(a, turns[(k + 1) & 1], fraction, odd, b, t0 + Q::TT);
+        const float* turn_at = turns[k & 1];
         for (int unit = warp; unit < 2 * a.heads; unit += QK_WARPS) {
             const int h = h0 + unit / 2;
             if (h >= a.H) break;
             const QkRows& r = a.r[unit & 1];
-            float w[2][8];
+            float2 w[2][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[0][i] = w[1][i] = 1.f;
+            for (int i = 0; i < 4; ++i) w[0][i] = w[1][i] = both(1.f);
             if (r.w) {
                 const float* p = r.w + (a.shared ? 0 : (size_t)h * D);
-                load8(p + c0, w[0]);
-                load8(p + c1, w[1]);
+                open_pairs(raw8(p + c0), w[0]);
+                open_pairs(raw8(p + c1), w[1]);
             }
-            const size_t stats = ((size_t)b * a.H + h) * a.T;
+            float* stats = r.rstd + ((size_t)b * a.H + h) * a.T;
+            const T *from = row_of<T>(r.x, b, h, t0 + row), *grad = BACKWARD ? row_of<T>(r.dy, b, h, t0 + row) : nullptr;
+            T* to = row_of<T>(r.out, b, h, t0 + row);
+            const int left = (int)min((long long)Q::TT, a.T - t0) - row;  // of the tile, from this lane's first row
+            decltype(raw8((const T*)nullptr)) raw[AT_ONCE][2], rg[AT_ONCE][2];
+            float rs[AT_ONCE];
+            auto load = [&](int e, int m) {  // a row to slot e
+                raw[e][0] = raw[e][1] = rg[e][0] = rg[e][1] = {};
+                rs[e] = 0.f;
+                if (!on || m >= left) return;
+                const T* x = from + m * r.x.st;
+                raw[e][0] = raw8(x + c0), raw[e][1] = raw8(x + c1);
+                if constexpr (BACKWARD) {
+                    const T* g = grad + m * r.dy.st;
+                    rg[e][0] = raw8(g + c0), rg[e][1] = raw8(g + c1);
+                    rs[e] = stats[t0 + row + m];
+                }
+            };
 #pragma unroll 1
             for (int u = 0; u < Q::DEEP; u += AT_ONCE) {
-                decltype(raw8((const T*)nullptr)) raw[AT_ONCE][2], rg[AT_ONCE][2];
-                float rs[AT_ONCE];
+#pragma unroll
+                for (int e = 0; e < AT_ONCE; ++e) load(e, (u + e) * Q::ROWS);
 #pragma unroll
                 for (int e = 0; e < AT_ONCE; ++e) {
-                    const long long t = t0 + (u + e) * Q::ROWS + row;
-                    raw[e][0] = raw[e][1] = rg[e][0] = rg[e][1] = {};
-                    rs[e] = 0.f;
-                    if (!on || t >= a.T) continue;
-                    const T* x = row_of<T>(r.x, b, h, t);
-                    raw[e][0] = raw8(x + c0), raw[e][1] = raw8(x + c1);
-                    if constexpr (BACKWARD) {
-                        const T* g = row_of<T>(r.dy, b, h, t);
-                        rg[e][0] = raw8(g + c0), rg[e][1] = raw8(g + c1);
-                        rs[e] = r.rstd[stats + t];
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < AT_ONCE; ++e) {
-                    const int tok = (u + e) * Q::ROWS + row;
-                    const long long t = t0 + tok;
-                    const bool live = on && t < a.T;
-                    float x[2][8], sum = 0.f;
-                    open8(raw[e][0], x[0]);
-                    open8(raw[e][1], x[1]);
+                    const int m = (u + e) * Q::ROWS, tok = m + row;
+                    const bool live = on && m < left;
+                    float2 x[2][4], sum = both(0.f);
+                    open_pairs(raw[e][0], x[0]);
+                    open_pairs(raw[e][1], x[1]);
+                    T* y = to + m * r.out.st;
                     if constexpr (!BACKWARD) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) sum = fmaf(x[0][i], x[0][i], fmaf(x[1][i], x[1][i], sum));
-                        const float rstd = rsqrtf(fmaf(a.c, row_total<L>(sum, lane), a.eps));
+                        for (int i = 0; i < 4; ++i) sum = __ffma2_rn(x[0][i], x[0][i], __ffma2_rn(x[1][i], x[1][i], sum));
+                        const float rstd = rsqrtf(fmaf(a.c, row_total<L>(sum.x + sum.y, lane), a.eps));
                         if (!live) continue;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[0][i] *= rstd * w[0][i], x[1][i] *= rstd * w[1][i];
-                        if (turned) turn<1>(x[0], x[1], turns, tok, P, l);
-                        T* y = row_of<T>(r.out, b, h, t);
-                        store8(y + c0, x[0]);
-                        store8(y + c1, x[1]);
-                        if (l == 0 && r.rstd) r.rstd[stats + t] = rstd;
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[q][i] = __fmul2_rn(x[q][i], __fmul2_rn(both(rstd), w[q][i]));
+                        if (turned) turn<1>(x[0], x[1], turn_at, tok, P, l);
+                        store_pairs(y + c0, x[0]);
+                        store_pairs(y + c1, x[1]);
+                        if (l == 0 && r.rstd) stats[t0 + tok] = rstd;
                     } else {
-                        float g[2][8];
-                        open8(rg[e][0], g[0]);
-                        open8(rg[e][1], g[1]);
-                        if (turned && live) turn<-1>(g[0], g[1], turns, tok, P, l);
+                        float2 g[2][4];
+                        open_pairs(rg[e][0], g[0]);
+                        open_pairs(rg[e][1], g[1]);
+                        const float rstd = rs[e];
+                        if (turned && live) turn<-1>(g[0], g[1], turn_at, tok, P, l);
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                x[q][i] *= rs[e];
-                                dw[q][i] = fmaf(g[q][i], x[q][i], dw[q][i]);
-                                g[q][i] *= w[q][i];
-                                sum = fmaf(g[q][i], x[q][i], sum);
+                            for (int i = 0; i < 4; ++i) {
+                                x[q][i] = __fmul2_rn(x[q][i], both(rstd));
+                                dw[q][i] = __ffma2_rn(g[q][i], x[q][i], dw[q][i]);
+                                g[q][i] = __fmul2_rn(g[q][i], w[q][i]);
+                                sum = __ffma2_rn(g[q][i], x[q][i], sum);
                             }
-                        sum = a.c * row_total<L>(sum, lane);
+                        const float share = a.c * row_total<L>(sum.x + sum.y, lane);
                         if (!live) continue;
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) g[q][i] = fmaf(-sum, x[q][i], g[q][i]) * rs[e];
-                        T* y = row_of<T>(r.out, b, h, t);
-                        store8(y + c0, g[0]);
-                        store8(y + c1, g[1]);
+                            for (int i = 0; i < 4; ++i) g[q][i] = __fmul2_rn(__ffma2_rn(both(-share), x[q][i], g[q][i]), both(rstd));
+                        store_pairs(y + c0, g[0]);
+                        store_pairs(y + c1, g[1]);
                     }
                 }
             }
         }
+        if (a.rot) __syncthreads();  // the next tile's angles are there, and this one's are read
     }
     if constexpr (BACKWARD) {
         // one unit a warp: its rows' sums, in the order of the lanes
         const int h = h0 + warp / 2;
         if (!a.partial || h >= a.H || warp >= 2 * a.heads) return;
+        auto over_rows = [&](float s) {
+            if (!on) s = 0.f;
+            if constexpr (L == 6) {
+                float all = 0.f;
+#pragma unroll
+                for (int k = 0; k < Q::ROWS; ++k) all += __shfl_sync(0xffffffffu, s, k * L + l);
+                return all;
+            } else {
+#pragma unroll
+                for (int m = L; m < 32; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+                return s;
+            }
+        };
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float s = on ? dw[q][i] : 0.f;
-                if constexpr (L == 6) {
-                    float all = 0.f;
-#pragma unroll
-                    for (int k = 0; k < Q::ROWS; ++k) all += __shfl_sync(0xffffffffu, s, k * L + l);
-                    s = all;
-                } else {
-#pragma unroll
-                    for (int m = L; m < 32; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-                }
-                dw[q][i] = s;
-            }
+            for (int i = 0; i < 4; ++i) dw[q][i] = make_float2(over_rows(dw[q][i].x), over_rows(dw[q][i].y));
         if (row == 0) {
             float* out = a.partial + ((((size_t)b * a.spans + span) * 2 + (warp & 1)) * a.H + h) * D;
-            store8(out + c0, dw[0]);
-            store8(out + c1, dw[1]);
+            store_pairs(out + c0, dw[0]);
+            store_pairs(out + c1, dw[1]);
         }
     }
 }
 
-// dw of q and k from the blocks' sums [n][2][H][d]: a block per 32 columns of (q or k, head), 32 threads a column, each
-// over every 32nd of the sums, and the threads' sums in order.
+// dw of q and k from the blocks' sums [n][2][H][d]: a block per 32 columns of (q or k, head, or all heads), 32 threads a
+// column, each over every 32nd of the n, and the threads' sums in order.
 constexpr int QK_SUMS = 1024;
 __global__ void __launch_bounds__(QK_SUMS) vla_qk_sums_kernel(const float* __restrict__ partial, int n, int H, int d, int shared,
                                                               float* dwq, float* dwk) {
     __shared__ float sums[32][33];
     const int col = threadIdx.x % 32, k = threadIdx.x / 32, which = blockIdx.z;
-    const int i = blockIdx.y * 32 + col;
-    const long long all = (long long)n * (shared ? H : 1);
+    const int i = blockIdx.y * 32 + col, h0 = blockIdx.x, heads = shared ? H : 1;
     float s = 0.f;
+    for (int m = k; m < n; m += 32) {
+        const float* at = partial + (((size_t)m * 2 + which) * H + h0) * d + i;
 #pragma unroll 8
-    for (long long m = k; m < all; m += 32) {
-        const long long blk = shared ? m / H : m, h = shared ? m % H : blockIdx.x;
-        s += partial[((blk * 2 + which) * H + h) * d + i];
+        for (int h = 0; h < heads; ++h) s += at[(size_t)h * d];
     }
     sums[k][col] = s;
     __syncthreads();
@@ -274,7 +306,10 @@ __global__ void __launch_bounds__(QK_SUMS) vla_qk_sums_kernel(const float* __res
     }
 }
 
-int tile_of(int d) { return d == 128 ? QkLay<128>::TT : d == 96 ? QkLay<96>::TT : d == 64 ? QkLay<64>::TT : QkLay<32>::TT; }
+template <bool BACKWARD>
+int tile_of(int d) {
+    return d == 128 ? QkLay<128, BACKWARD>::TT : d == 96 ? QkLay<96, BACKWARD>::TT : d == 64 ? QkLay<64, BACKWARD>::TT : QkLay<32, BACKWARD>::TT;
+}
 
 // A block's heads and tiles. Forward: a tile of as many heads as leave every SM four blocks, for which its angles
 // are formed once. Backward: a head of q and of k a warp, and tiles enough that the sums over the rows are few.
@@ -283,13 +318,14 @@ struct QkPlan {
     long long grid;
 };
 QkPlan qk_plan(bool backward, int B, int H, int T, int d) {
-    const long long tiles = ((long long)T + tile_of(d) - 1) / tile_of(d), enough = 4LL * sm_count();
+    const int tile = backward ? tile_of<true>(d) : tile_of<false>(d);
+    const long long tiles = ((long long)T + tile - 1) / tile, enough = 4LL * sm_count();
     QkPlan p;
     p.heads = QK_WARPS / 2;
     p.tiles = 1;
     if (backward) {
         const long long groups = (H + p.heads - 1) / p.heads;
-        while (p.tiles < 16 && (long long)B * groups * ((tiles + 2 * p.tiles - 1) / (2 * p.tiles)) >= enough) p.tiles *= 2;
+        while (p.tiles < 8 && (long long)B * groups * ((tiles + 2 * p.tiles - 1) / (2 * p.tiles)) >= enough) p.tiles *= 2;
     } else {
         while (p.heads < H && (long long)B * tiles * ((H + 2 * p.heads - 1) / (2 * p.heads)) >= enough) p.heads *= 2;
     }
