@@ -9,10 +9,10 @@ template <int D, typename T>
 vla_status backward(DeltaArgs& p, cudaStream_t s) {
     vla_status st = delta_forward_run<D, T, true>(p, s);
     if (st != VLA_OK) return st;
+    bool on_tc = false;
     if constexpr (sizeof(T) == 2)
-        st = p.T > DELTA_TC ? delta_tc_pick<D, true, true>(p, s) : delta_run<vla_delta_reverse_kernel<D, T>, D, typename DeltaReverse<D, T>::L>(p, s);
-    else
-        st = delta_run<vla_delta_reverse_kernel<D, T>, D, typename DeltaReverse<D, T>::L>(p, s);
+        if ((on_tc = delta_on_tc(p))) st = delta_tc_pick<D, true, true>(p, s);
+    if (!on_tc) st = delta_run<vla_delta_reverse_kernel<D, T>, D, typename DeltaReverse<D, T>::L>(p, s);
     if (st != VLA_OK) return st;
     using L = DeltaGrads<D, T>;
     const long long grid = (long long)p.B * p.H * p.blocks;

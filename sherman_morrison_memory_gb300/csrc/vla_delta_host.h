@@ -49,7 +49,11 @@ inline vla_status delta_pick(vla_dtype dtype, int d, F f) {
     return dtype == VLA_BF16 ? with(__nv_bfloat16{}) : with(float{});
 }
 
-// Rows of S of a block: as many as it can have, or a half, a quarter, ... while the blocks are fewer than the SMs.
+// Rows of S of a block on the warp-level path: as many as it can have, or a half, a quarter, ... while all blocks run at
+// once, an SM each. Each block prepares its chunks for itself and one fills an SM's registers, so fewer rows shorten a
+// chunk but not the work: fp32 outputs of 1,024 tokens, d = 128: 16 heads 184 us with 64 rows, 144 with 32, 125 with 16;
+// 38 heads 191, 153, 288; 76 heads 211, 322, 586; 304 heads 834, 1,296, 2,326. d = 64: 38 heads 140, 121, 111; 76 heads
+// 149, 130, 252; 100 heads 201, 331, 481.
 inline int delta_rows(long long heads, int d, int rows) {
     while (rows % 32 == 0 && heads * (d / (rows / 2)) <= sm_count()) rows /= 2;
     return rows;
@@ -67,8 +71,15 @@ inline vla_status delta_run(DeltaArgs& p, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
 }
 
-// Tokens behind which a bf16 call's forward recurrence runs on tcgen05.
-constexpr int DELTA_TC = 64;
+// Whether a bf16 call's recurrences run on tcgen05, one block to an SM, or as warp-level products, which start sooner and
+// can be cut finer. Outputs, us, warp-level against tcgen05, of 8 heads, 64 heads, 304 heads (the gradients' agree):
+//   tokens  d = 32                                d = 64                               d = 128
+//   64      8.2, 8.3;  8.4, 8.4;   10.3, 14.4     8.3, 8.4;   8.4, 8.4;   18.5, 15.0   9.0, 10.4;  12.5, 10.5; 39.2, 24.7
+//   128     10.5, 10.3; 10.5, 10.4; 14.5, 18.4    10.5, 10.5; 12.4, 11.9; 26.7, 20.6   12.5, 12.9; 17.7, 14.4; 61.3, 35.1
+//   256     16.5, 14.4; 16.6, 14.5; 22.8, 26.7    16.6, 16.6; 18.6, 16.6; 43.2, 30.9   20.5, 20.5; 28.9, 20.7; 107, 60.0
+// and d = 96 between the last two. The rule goes by the tokens alone: a head's results stay the same, bit for bit,
+// whatever else is in the call.
+inline bool delta_on_tc(const DeltaArgs& p) { return p.T > 64; }
 
 template <int D, int R, bool TAPE, bool BACK = false>
 inline vla_status delta_tc_run(DeltaArgs& p, cudaStream_t s) {
@@ -91,11 +102,15 @@ inline vla_status delta_tc_run(DeltaArgs& p, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? VLA_OK : VLA_ERR_CUDA;
 }
 
-// A bf16 recurrence on tcgen05: few heads of d = 128 take two blocks each.
+// A bf16 recurrence on tcgen05: heads of d = 128 take two blocks where that is sooner done, a block of 64 rows taking
+// about 5/8 of the time of one of 128 (4,096 tokens: 219 us and 345). Outputs of 76 heads, one block and two: 348 and
+// 221 us; 100 heads 349, 436; 153 heads 685, 648; 304 heads 699, 876. Gradients: 1,527, 1,086; 1,663, 1,833; 3,058,
+// 2,744; 3,976, 4,288.
 template <int D, bool TAPE, bool BACK = false>
 inline vla_status delta_tc_pick(DeltaArgs& p, cudaStream_t s) {
     if constexpr (D == 128) {
-        if ((long long)p.B * p.H * 2 <= sm_count()) return delta_tc_run<D, 64, TAPE, BACK>(p, s);
+        const long long heads = (long long)p.B * p.H, sms = sm_count();
+        if ((2 * heads + sms - 1) / sms * 5 < (heads + sms - 1) / sms * 8) return delta_tc_run<D, 64, TAPE, BACK>(p, s);
     }
     return delta_tc_run<D, (D > 64 ? 128 : 64), TAPE, BACK>(p, s);
 }
@@ -104,7 +119,7 @@ inline vla_status delta_tc_pick(DeltaArgs& p, cudaStream_t s) {
 template <int D, typename T, bool TAPE>
 inline vla_status delta_forward_run(DeltaArgs& p, cudaStream_t s) {
     if constexpr (sizeof(T) == 2)
-        if (p.T > DELTA_TC) return delta_tc_pick<D, TAPE>(p, s);
+        if (delta_on_tc(p)) return delta_tc_pick<D, TAPE>(p, s);
     return delta_run<vla_delta_forward_kernel<D, T, TAPE>, D, typename DeltaForward<D, T, TAPE>::L>(p, s);
 }
 

@@ -618,13 +618,14 @@ def test_calls_without_waits_do_not_stall():
         check_backward(q, k, v, g, beta, 1.0, None, do, None, None, vla.vla_delta_backward(q, k, v, g, beta, 1.0, None, do, **kw))
 
 
-@pytest.mark.parametrize("d", [64, 96, 128])
-def test_more_heads_than_sms(d):
-    """Several blocks an SM one after another, lengths at every edge of a chunk, the same bits each time."""
-    B, H, T = 9, 24, 200
+@pytest.mark.parametrize("d,H,T", [(32, 24, 200), (64, 24, 200), (96, 24, 200), (128, 24, 200), (128, 12, 200),
+                                   (32, 24, 20), (64, 24, 20), (96, 24, 40), (128, 24, 1)])
+def test_more_heads_than_sms(d, H, T):
+    """One block or several an SM, lengths at every edge of a chunk, the same bits each time."""
+    B = 9
     q, k, v, do = inputs(4, B, H, T, d, BF, seed=d)
     g, beta = gates(B, H, T)
-    n = torch.tensor([200, 199, 193, 192, 191, 129, 64, 9, 1], dtype=torch.int32, device="cuda")
+    n = torch.tensor([200, 199, 193, 192, 191, 129, 64, 9, 1], dtype=torch.int32, device="cuda").clamp(max=T)
     S0, dS = state_like(B, H, d, 1), state_like(B, H, d, 2)
 
     def call():
