@@ -79,6 +79,7 @@ constexpr int BLOCK = sizeof(T) == 2 ? 64 : 32;
 // rows of S of a block at most: two warps for 16, with the helpers' 16 warps or 12
 template <int D>
 constexpr int MOST_ROWS = D == 128 ? 64 : D;
+// (d = 32: registers for two blocks on an SM, 304 heads of 1,024 tokens, fp32 gradients: 429 us and 500)
 template <int D>
 constexpr int DELTA_THREADS = MOST_ROWS<D> * 4 + HELPERS;
 
@@ -102,33 +103,58 @@ struct DeltaLay {
 // gates of a chunk: exp(G), exp(G_C - G), b of each token, then exp(G_C)
 enum { GATE_NEAR = 0, GATE_FAR = DC, GATE_BETA = 2 * DC, GATE_WHOLE = 3 * DC };
 
-// Rows [t0, t0 + DC) of a sequence's `cols` columns to a tile, by THREADS threads; those from `n` on are zero.
-template <int LD, int THREADS, typename T>
-__device__ __forceinline__ void load_tile(char* tile, const Seq& s, int b, int h, long long t0, int col0, int cols, long long n,
-                                          int tid) {
-    constexpr int NP = PARTS<T>, PLANE = DC * LD * 2;
+// Rows [t0, t0 + DC) of a bf16 sequence to a tile, by a warp; those from `n` on are zero.
+template <int LD, typename T>
+__device__ __forceinline__ void load_tile(char* tile, const Seq& s, int b, int h, long long t0, int col0, int cols, long long n, int lane) {
     const int per = cols / 8, wide = per <= 2 ? 1 : per <= 4 ? 2 : per <= 8 ? 3 : 4;  // threads of a row, a power of two
-    const int c = (tid & ((1 << wide) - 1)) * 8, first = tid >> wide, step = THREADS >> wide;
+    const int c = (lane & ((1 << wide) - 1)) * 8, first = lane >> wide, step = 32 >> wide;
     if (c >= cols) return;
     const int live = (int)min((long long)DC, n - t0);
     const T* src = row_of<T>(s, b, h, t0) + col0 + c;
     char* dst = tile + (first * LD + c) * 2;
 #pragma unroll 4
-    for (int r = first; r < DC; r += step, dst += step * LD * 2) {
-        const T* at = r < live ? src + r * s.st : src;
-        if constexpr (NP == 1) {
-            cp_async16(vla::smem_u32(dst), at, r < live ? 16 : 0);
-        } else {
-            float x[8] = {};
-            if (r < live) load8(at, x);
-            uint32_t w[4][NP];
+    for (int r = first; r < DC; r += step, dst += step * LD * 2) cp_async16(vla::smem_u32(dst), r < live ? src + r * s.st : src, r < live ? 16 : 0);
+}
+
+// The same of an fp32 sequence by the helpers, in two steps: rows to registers, then their parts to the tile, so that the
+// loads of several tiles are under way together. The chunk `ahead` tokens on is asked into the L2 cache.
+template <int D>
+struct Rows32 {
+    static constexpr int MOST = D > 64 ? 4 : D / 32;  // rows of a thread at most
+    Raw8F x[MOST];
+    int c, first, step;
+
+    __device__ __forceinline__ void load(const Seq& s, int b, int h, long long t0, int col0, int cols, long long n, int tid, int ahead) {
+        const int per = cols / 8, wide = per <= 2 ? 1 : per <= 4 ? 2 : per <= 8 ? 3 : 4;
+        c = (tid & ((1 << wide) - 1)) * 8, first = tid >> wide, step = HELPERS >> wide;
+        if (c >= cols) first = DC;
+        const int live = (int)min((long long)DC, n - t0);
+        const float* src = row_of<float>(s, b, h, t0) + col0 + c;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split<NP>(x[2 * j], x[2 * j + 1], w[j]);
-#pragma unroll
-            for (int p = 0; p < NP; ++p) *reinterpret_cast<uint4*>(dst + p * PLANE) = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+        for (int i = 0; i < MOST; ++i) {
+            const int r = first + i * step;
+            x[i] = {};
+            if (r < live) x[i] = raw8(src + r * s.st);
+            const long long next = t0 + r + ahead;
+            if (r < DC && next >= 0 && next < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (r + ahead) * s.st));
         }
     }
-}
+    template <int LD>
+    __device__ __forceinline__ void put(char* tile) const {
+        char* dst = tile + (first * LD + c) * 2;
+#pragma unroll
+        for (int i = 0; i < MOST; ++i, dst += step * LD * 2) {
+            if (first + i * step >= DC) break;
+            float y[8];
+            open8(x[i], y);
+            uint32_t w[4][3];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split<3>(y[2 * j], y[2 * j + 1], w[j]);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<uint4*>(dst + p * DC * LD * 2) = make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+        }
+    }
+};
 
 // A decay over a chunk that multiplies a state again and again: what the
 // roundings of the factors add up to is put right by the next ones (SlowDecay of

@@ -26,7 +26,7 @@ struct DeltaReverse {
 };
 
 template <int D, typename T>
-__global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_reverse_kernel(const __grid_constant__ DeltaArgs p) {
+__global__ void __launch_bounds__(DELTA_THREADS<D>, D == 32 ? 2 : 1) vla_delta_reverse_kernel(const __grid_constant__ DeltaArgs p) {
     using F = DeltaReverse<D, T>;
     using L = typename F::L;
     constexpr int NP = F::NP, LD = L::LD, SPAN = BLOCK<T>;
@@ -43,15 +43,33 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_reverse_kernel(con
     if (warp >= workers) {
         const int tid = threadIdx.x - workers * 32, hw = warp - workers;
         // bf16: the last helper warp loads; fp32: all, as values are cut into parts on the way
-        constexpr int LOADERS = NP == 1 ? 32 : HELPERS;
         auto load = [&](int m) {
-            const int at = tid & (LOADERS - 1);
             const long long t0 = (long long)(chunks - 1 - m) * DC;
-            load_tile<LD, LOADERS, T>(tile(m, 0), p.k, b, h, t0, 0, D, n, at);
-            load_tile<LD, LOADERS, T>(tile(m, 1), p.q, b, h, t0, 0, D, n, at);
-            load_tile<LD, LOADERS, T>(tile(m, 2), p.dO, b, h, t0, row0, p.rows, n, at);
-            if constexpr (F::TILES == 4) load_tile<LD, LOADERS, T>(tile(m, 3), p.v, b, h, t0, row0, p.rows, n, at);
-            cp_async_commit();
+            if constexpr (NP == 1) {
+                load_tile<LD, T>(tile(m, 0), p.k, b, h, t0, 0, D, n, lane);
+                load_tile<LD, T>(tile(m, 1), p.q, b, h, t0, 0, D, n, lane);
+                load_tile<LD, T>(tile(m, 2), p.dO, b, h, t0, row0, p.rows, n, lane);
+                if constexpr (F::TILES == 4) load_tile<LD, T>(tile(m, 3), p.v, b, h, t0, row0, p.rows, n, lane);
+                cp_async_commit();
+            }
+        };
+        // fp32: as in the forward kernel
+        Rows32<NP == 1 ? 32 : D> x, y, z;
+        constexpr bool AHEAD = D <= 64;
+        auto fetch = [&](int m) {
+            const long long t0 = (long long)(chunks - 1 - m) * DC;
+            x.load(p.k, b, h, t0, 0, D, n, tid, -DC);
+            y.load(p.q, b, h, t0, 0, D, n, tid, -DC);
+            if constexpr (AHEAD) z.load(p.dO, b, h, t0, row0, p.rows, n, tid, -DC);
+        };
+        auto put = [&](int m) {
+            x.template put<LD>(tile(m, 0));
+            if constexpr (!AHEAD) x.load(p.dO, b, h, (long long)(chunks - 1 - m) * DC, row0, p.rows, n, tid, -DC);
+            y.template put<LD>(tile(m, 1));
+            if constexpr (AHEAD)
+                z.template put<LD>(tile(m, 2));
+            else
+                x.template put<LD>(tile(m, 2));
         };
         Whole whole;
         float g = 0.f, beta = 0.f;
@@ -62,6 +80,8 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_reverse_kernel(con
             beta = on ? *p.beta.at(b, h, t) : 0.f;
         };
         gates(0);
+        if constexpr (NP > 1 && AHEAD)
+            if (chunks) fetch(0);
         if (NP == 1 && hw == 3 && chunks) load(0);
         if constexpr (NP == 1) {
             cp_async_wait<0>();
@@ -70,8 +90,10 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_reverse_kernel(con
         for (int m = 0; m <= chunks; ++m) {  // chunk m is prepared while chunk m - 1 is computed
             if (m < chunks) {
                 if constexpr (NP > 1) {
-                    load(m);
+                    if (!AHEAD) fetch(m);
+                    put(m);
                     vla::named_bar(1, HELPERS);
+                    if (AHEAD && m + 1 < chunks) fetch(m + 1);
                 }
                 if (NP == 1 && hw == 3 && m + 1 < chunks) load(m + 1);
                 const float gm = g, bm = beta;

@@ -16,7 +16,7 @@ struct DeltaForward {
 };
 
 template <int D, typename T, bool TAPE>
-__global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_forward_kernel(const __grid_constant__ DeltaArgs p) {
+__global__ void __launch_bounds__(DELTA_THREADS<D>, D == 32 ? 2 : 1) vla_delta_forward_kernel(const __grid_constant__ DeltaArgs p) {
     using F = DeltaForward<D, T, TAPE>;
     using L = typename F::L;
     constexpr int NP = F::NP, PP = F::PP, LD = L::LD, SPAN = BLOCK<T>;
@@ -32,15 +32,35 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_forward_kernel(con
     if (warp >= workers) {
         const int tid = threadIdx.x - workers * 32, hw = warp - workers;
         // bf16: the last helper warp loads; fp32: all, as values are cut into parts on the way
-        constexpr int LOADERS = NP == 1 ? 32 : HELPERS;
         auto load = [&](int c) {
-            const int at = tid & (LOADERS - 1);
             const long long t0 = (long long)c * DC;
-            load_tile<LD, LOADERS, T>(tile(c, 0), p.k, b, h, t0, 0, D, n, at);
-            load_tile<LD, LOADERS, T>(tile(c, 1), p.q, b, h, t0, 0, D, n, at);
-            load_tile<LD, LOADERS, T>(tile(c, 2), p.v, b, h, t0, row0, p.rows, n, at);
-            if constexpr (F::TILES == 4) load_tile<LD, LOADERS, T>(tile(c, 3), p.dO, b, h, t0, row0, p.rows, n, at);
-            cp_async_commit();
+            if constexpr (NP == 1) {
+                load_tile<LD, T>(tile(c, 0), p.k, b, h, t0, 0, D, n, lane);
+                load_tile<LD, T>(tile(c, 1), p.q, b, h, t0, 0, D, n, lane);
+                load_tile<LD, T>(tile(c, 2), p.v, b, h, t0, row0, p.rows, n, lane);
+                if constexpr (F::TILES == 4) load_tile<LD, T>(tile(c, 3), p.dO, b, h, t0, row0, p.rows, n, lane);
+                cp_async_commit();
+            }
+        };
+        // fp32: a chunk's rows are loaded while the one before it is prepared, where registers hold them (304 heads of 1,024
+        // tokens, d = 64: 412 us with a tile loaded and cut after the other, 268 with the loads under way together, 258 ahead
+        // too; d = 128: 834, 750, and 875 ahead, which spills)
+        Rows32<NP == 1 ? 32 : D> x, y, z;
+        constexpr bool AHEAD = D <= 64;
+        auto fetch = [&](int c) {
+            const long long t0 = (long long)c * DC;
+            x.load(p.k, b, h, t0, 0, D, n, tid, DC);
+            y.load(p.q, b, h, t0, 0, D, n, tid, DC);
+            if constexpr (AHEAD) z.load(p.v, b, h, t0, row0, p.rows, n, tid, DC);
+        };
+        auto put = [&](int c) {
+            x.template put<LD>(tile(c, 0));
+            if constexpr (!AHEAD) x.load(p.v, b, h, (long long)c * DC, row0, p.rows, n, tid, DC);
+            y.template put<LD>(tile(c, 1));
+            if constexpr (AHEAD)
+                z.template put<LD>(tile(c, 2));
+            else
+                x.template put<LD>(tile(c, 2));
         };
         Whole whole;
         float g = 0.f, beta = 0.f;
@@ -50,6 +70,8 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_forward_kernel(con
             beta = t < n ? *p.beta.at(b, h, t) : 0.f;
         };
         gates(0);
+        if constexpr (NP > 1 && AHEAD)
+            if (chunks) fetch(0);
         if (NP == 1 && hw == 3 && chunks) load(0);
         if constexpr (NP == 1) {
             cp_async_wait<0>();
@@ -58,8 +80,10 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>) vla_delta_forward_kernel(con
         for (int c = 0; c <= chunks; ++c) {  // chunk c is prepared while chunk c - 1 is computed
             if (c < chunks) {
                 if constexpr (NP > 1) {
-                    load(c);
+                    if (!AHEAD) fetch(c);
+                    put(c);
                     vla::named_bar(1, HELPERS);
+                    if (AHEAD && c + 1 < chunks) fetch(c + 1);
                 }
                 if (NP == 1 && hw == 3 && c + 1 < chunks) load(c + 1);
                 const float gc = g, bc = beta;

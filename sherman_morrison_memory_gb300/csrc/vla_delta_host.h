@@ -51,9 +51,9 @@ inline vla_status delta_pick(vla_dtype dtype, int d, F f) {
 
 // Rows of S of a block on the warp-level path: as many as it can have, or a half, a quarter, ... while all blocks run at
 // once, an SM each. Each block prepares its chunks for itself and one fills an SM's registers, so fewer rows shorten a
-// chunk but not the work: fp32 outputs of 1,024 tokens, d = 128: 16 heads 184 us with 64 rows, 144 with 32, 125 with 16;
-// 38 heads 191, 153, 288; 76 heads 211, 322, 586; 304 heads 834, 1,296, 2,326. d = 64: 38 heads 140, 121, 111; 76 heads
-// 149, 130, 252; 100 heads 201, 331, 481.
+// chunk but not the work: fp32 outputs of 1,024 tokens, d = 128: 16 heads 183 us with 64 rows, 144 with 32, 139 with 16;
+// 38 heads 184, 158, 299; 76 heads 189, 319, 598; 304 heads 750, 1,275, 2,290. d = 64: 16 heads 131, 103, 92; 76 heads
+// 131, 119, 222; 100 heads 131, 213, 308.
 inline int delta_rows(long long heads, int d, int rows) {
     while (rows % 32 == 0 && heads * (d / (rows / 2)) <= sm_count()) rows /= 2;
     return rows;
