@@ -1,8 +1,9 @@
 /*
  * vla_layer.h -- operators of libvla_gb300.so around the recurrence of vla.h:
- * linear attention with a decay per head (prompt, gradient, single token), the
- * layer norm of each head's readout with its gradients, and a quantised cache
- * of the heads' states.
+ * linear attention with a decay per head and the gated delta rule (prompt,
+ * gradient, single token), the norm and position rotation of queries and keys and
+ * the layer norm of each head's readout with their gradients, and a quantised
+ * cache of the heads' states.
  *
  * Conventions as in vla.h: device pointers owned by the caller, `stream` a
  * cudaStream_t as void*, calls asynchronous on it, argument errors returned at
@@ -10,8 +11,8 @@
  * states in fp32, sums and statistics in fp32. Two things differ. Sequences may
  * have any strides (vla_seq), so that a projection's [B, T, H, d] output is read in
  * place. And results that are sequences (o, y, the gradients) have the inputs'
- * type, rounded at the end; what bf16 calls of vla_decay_*() round before that
- * stands there.
+ * type, rounded at the end; what bf16 calls of vla_decay_*() and vla_delta_*()
+ * round before that stands there.
  *
  * An output of a call overlaps neither itself nor an input nor another output
  * (nor the call's scratch), except in place where an entry point says so: blocks

@@ -22,7 +22,7 @@ def _scratch(dtype: int, B: int, H: int, T: int, d: int) -> int:
 
 
 def _gate_in(x: torch.Tensor, shape, device, name: str) -> torch.Tensor:
-    """A gate, at its own strides (copied where one is negative)."""
+    """A gate, read at its own strides."""
     if tuple(x.shape) != tuple(shape) or x.dtype != torch.float32 or x.device != device:
         raise ValueError(f"{name} must be float32 {tuple(shape)} on {device}, got {x.dtype} {tuple(x.shape)} {x.device}")
     return x

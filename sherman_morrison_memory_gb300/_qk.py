@@ -89,12 +89,13 @@ def vla_qk_norm(q: torch.Tensor, k: torch.Tensor, weight_q: Optional[torch.Tenso
         wq, wk = _weights(weight_q, weight_k, H, d, dev)
         freqs, rot, positions, stride = _rotation(freqs, positions, B, T, d, dev)
         if out is None:
-            yq, yk = torch.empty((2, B, H, T, d), dtype=q.dtype, device=dev).unbind(0)
+            yq = torch.empty((B, H, T, d), dtype=q.dtype, device=dev)
+            yk = torch.empty((B, H, T, d), dtype=q.dtype, device=dev)
         else:
             yq, yk = out
             for i, x in enumerate((yq, yk)):
                 _check_out(x, (B, H, T, d), q.dtype, dev, f"out[{i}]", strided=True)
-        rstd = torch.empty((2, B, H, T), dtype=torch.float32, device=dev).unbind(0)
+        rstd = (torch.empty((B, H, T), dtype=torch.float32, device=dev), torch.empty((B, H, T), dtype=torch.float32, device=dev))
         (q, sq), (k, sk) = _rows(q), _rows(k)
         st = lib.vla_qk_norm(sq, sk, _DTYPES[q.dtype], B, H, T, d, _ptr(wq), _ptr(wk), int(wq is not None and wq.dim() == 1),
                              int(bool(unit)), eps, _ptr(freqs), rot, _ptr(positions), stride, _seq(yq), _seq(yk),
@@ -129,7 +130,8 @@ def vla_qk_norm_backward(grad_q: torch.Tensor, grad_k: torch.Tensor, q: torch.Te
         rstd_k = _check_f32(rstd_k, (B, H, T), dev, "rstd_k")
         freqs, rot, positions, stride = _rotation(freqs, positions, B, T, d, dev)
         if out is None:
-            dq, dk = torch.empty((2, B, H, T, d), dtype=q.dtype, device=dev).unbind(0)
+            dq = torch.empty((B, H, T, d), dtype=q.dtype, device=dev)
+            dk = torch.empty((B, H, T, d), dtype=q.dtype, device=dev)
         else:
             dq, dk = out
             for i, x in enumerate((dq, dk)):

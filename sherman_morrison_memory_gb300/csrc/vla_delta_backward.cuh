@@ -12,6 +12,15 @@
 //   dg_t = sum over the block's i >= t of (o_i . dO_i - v_i . dV_i) + <R, S> behind the block,
 // of fp32 results of the two recurrences. Before a first token without a state
 // nothing decays: its dg is 0, where the sum would leave its roundings.
+//
+// What bounds them: the recurrences' chains, as forward; the third launch moves two
+// fp32 states of every 64 tokens (fp32: 32), E and seven sequences. bf16, 4 x 8 heads
+// of 4,096 tokens, d = 64: 577 us, of which 212, 271 and 91; 2 x 32 heads of 4,095,
+// d = 128: 1,017 us, of 283, 368 and 361 (1.1 GB, 165 us at the memory's rate; its
+// shared memory pipes are 56% busy). States every 64 tokens and not 32: half the bytes,
+// and the pairs' products still are a small part. The states come through a ring of
+// shared memory, 32 rows at a time, two slices under way (1,620 us in all without it,
+// 1,474 with it); loads of registers first, and X and M of a block together, gave another 220.
 #pragma once
 
 #include "vla_delta.cuh"

@@ -102,12 +102,14 @@ __device__ __forceinline__ void make_turns(const QkArgs& a, float* turns, const 
 // The frequencies as fractions of a turn, and which are not finite (NaN at every position)
 __device__ __forceinline__ void make_fractions(const QkArgs& a, unsigned long long* fraction, bool* odd) {
     for (int f = threadIdx.x; f < a.rot / 2; f += QK_THREADS) {
-        const double turns = a.freqs[f] * 0.15915494309189533577;
+        // of its size, as what is left of a small negative number beside the whole turn below it is rounded, to 1 even
+        const double turns = fabs(a.freqs[f]) * 0.15915494309189533577;
         const double part = turns - floor(turns);
         odd[f] = !isfinite(turns);
         // in two halves, as a product of 2^64 and a part near 1 would not fit
         const double high = floor(part * 4294967296.0);
-        fraction[f] = ((unsigned long long)(uint32_t)high << 32) + (unsigned long long)((part * 4294967296.0 - high) * 4294967296.0);
+        const unsigned long long u = ((unsigned long long)(uint32_t)high << 32) + (unsigned long long)((part * 4294967296.0 - high) * 4294967296.0);
+        fraction[f] = a.freqs[f] < 0 ? 0ull - u : u;
     }
     __syncthreads();
 }

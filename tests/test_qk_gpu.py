@@ -75,6 +75,9 @@ def test_far_positions(d):
     # frequencies of more than a turn a position, against time, and 0
     freqs = torch.tensor([7.0, -0.3, 0.0, 1e-9, 3.0, 100.0, -6.5, 0.7], dtype=torch.float64, device="cuda")
     check(q, k, gq, gk, (None, None), True, freqs, pos)
+    # ... and hardly any, either way
+    freqs = torch.tensor([-1e-20, 1e-20, -1e-17, -1e-12, 3e-12, -2.0 ** -40, -0.0, -1e-10], dtype=torch.float64, device="cuda")
+    check(q, k, gq, gk, (None, None), True, freqs, pos)
 
 
 def test_a_frequency_that_is_not_finite():
