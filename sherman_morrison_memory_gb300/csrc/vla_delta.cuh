@@ -62,7 +62,6 @@ struct DeltaArgs {
     float* E;               // [BH][T][d]
     float *before, *behind; // [BH][blocks + 1][d][d]: S before a block of tokens (the last one behind all), R behind it
     float *od, *vd, *bd;    // [BH][d / 16][T]: o . dO, v . dV and U' . E of 16 rows
-    float* ends;            // [BH][blocks][d / 8]: <R, S> behind a block, of 16 rows and half of the columns
     int blocks;             // blocks of tokens of a sequence of T
 };
 

@@ -147,17 +147,6 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>, D == 32 ? 2 : 1) vla_delta_r
             const long long blk = t0 / SPAN;
             const size_t at = ((size_t)bh * (p.blocks + 1) + blk) * D * D + own;
             store_rows<D, W>(s, p.behind + at, lane);
-            const float* S = p.before + at + (size_t)D * D;
-            float dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < W / 8; ++i) {
-                const float2 a = *reinterpret_cast<const float2*>(S + r * D + i * 8 + t2);
-                const float2 c = *reinterpret_cast<const float2*>(S + (r + 8) * D + i * 8 + t2);
-                dot = fmaf(s[i][0], a.x, fmaf(s[i][1], a.y, fmaf(s[i][2], c.x, fmaf(s[i][3], c.y, dot))));
-            }
-#pragma unroll
-            for (int i = 1; i < 32; i <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
-            if (lane == 0) p.ends[((size_t)bh * p.blocks + blk) * (D / 8) + my_row / 8 + half] = dot;
         }
         float x[4][4];
         {
@@ -258,7 +247,8 @@ struct DeltaGrads {
     static constexpr int Q = 0, K = Q + NP * PLANE, O = K + NP * PLANE, V = O + NP * PLANE, U = V + NP * PLANE,
                          X = U + UP * PLANE, M = X + XP * XPLANE, GATES = M + MP * XPLANE, RING = GATES + 5 * TB * 4;
     // the states, 32 rows at a time, two of them under way; the rows' shares of the gates' gradients
-    static constexpr int SLD = D + 4, SLICE = 32 * SLD * 4, SLICES = 3, SHARES = RING + SLICES * SLICE, BYTES = SHARES + (D / 16) * TB * 8;
+    static constexpr int SLD = D + 4, SLICE = 32 * SLD * 4, SLICES = 3, SHARES = RING + SLICES * SLICE,
+                         ENDS = SHARES + (D / 16) * TB * 8, BYTES = ENDS + D / 8 * 4;
     static constexpr int THREADS = D * 4, MH = MT / 2;  // a warp's tiles of 16 tokens
 };
 
@@ -286,7 +276,7 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
     // what goes through registers is under way first
     constexpr int EK = TB / 32;  // groups of eight values of E a thread
     Raw8F e_raw[EK];
-    float e_beta[EK], share[3] = {}, g_in[TB / 32], b_in[TB / 32], end_in = 0.f;
+    float e_beta[EK], share[3] = {}, g_in[TB / 32], b_in[TB / 32];
 #pragma unroll
     for (int k = 0; k < EK; ++k) {
         const int i = tid + k * THREADS, row = i / (D / 8), c = i % (D / 8) * 8;
@@ -308,7 +298,6 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
             g_in[k] = j < live && p.g.p ? *p.g.at(b, h, t0 + j) : 0.f;
             b_in[k] = j < live ? *p.beta.at(b, h, t0 + j) : 0.f;
         }
-    if (warp == THREADS / 32 - 1 && lane < D / 8) end_in = p.ends[((size_t)bh * p.blocks + blk) * (D / 8) + lane];
     auto load = [&](int at, const Seq& s) {
 #pragma unroll 4
         for (int i = tid; i < TB * (D / 8); i += THREADS) {
@@ -432,38 +421,38 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
                 for (int q = 0; q < L::MP; ++q) *reinterpret_cast<uint32_t*>(sm + L::M + q * L::XPLANE + (i * XLD + j) * 2) = y[q];
             }
     }
-    // The gates' gradients: the sums of the rows' shares, and of those over the tokens from the block's end. The last
-    // warp has no pairs, or few.
-    float bad = 0.f;
+    // The gates' gradients, the sums of the rows' shares: dbeta, and dlog_decay's sums from the last token of a 32 on. The
+    // last warp has no pairs, or few.
+    float dg_hi[TB / 32] = {}, dg_lo[TB / 32] = {}, bad = 0.f;
     if (warp == THREADS / 32 - 1) {
 #pragma unroll
-        for (int m = 1; m < 16; m <<= 1) end_in += __shfl_xor_sync(0xffffffffu, end_in, m);
-        float behind = __shfl_sync(0xffffffffu, end_in, 0), rest = 0.f;
-#pragma unroll
-        for (int k = TB / 32 - 1; k >= 0; --k) {
-            const int j = k * 32 + 31 - lane;  // from the end
-            float db = 0.f, hi = 0.f, lo = 0.f;
+        for (int k = 0; k < TB / 32; ++k) {
+            const int j = k * 32 + 31 - lane;
+            float db = 0.f;
 #pragma unroll
             for (int w = 0; w < D / 16; ++w) {
                 const float2 y = shares[w * TB + j];
-                hi += y.x;
+                dg_hi[k] += y.x;
                 db += y.y;
             }
-            running_sums(hi, lo, lane);
-            const float s = behind + hi, d = s - behind;
-            lo += rest + ((behind - (s - d)) + (hi - d));
-            float x = s + lo;
-            behind = __shfl_sync(0xffffffffu, s, 31), rest = __shfl_sync(0xffffffffu, lo, 31);
+            running_sums(dg_hi[k], dg_lo[k], lane);
             if (j >= rows) continue;
-            if (j >= live || (!p.S0 && t0 + j == 0)) x = 0.f;
-            bad = fmaf(x, 0.f, fmaf(db, 0.f, bad));
-            if (p.dg.p) *p.dg.at(b, h, t0 + j) = x;
+            bad = fmaf(db, 0.f, bad);
             *p.dbeta.at(b, h, t0 + j) = db;
         }
     }
 
     // dq and dk of the warp's 16 columns at its tokens: first the states
     const int col0 = warp % (D / 16) * 16, m0 = warp / (D / 16) * MH;
+    // <R, S> behind the block: R as it passes, S from memory, where the next block's S is the same
+    float4 behind[2];
+    float dot = 0.f;
+    const int own_row = tid / (D / 4), own_col = tid % (D / 4) * 4;
+    auto load_behind = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) behind[k] = *reinterpret_cast<const float4*>(p.before + at + (size_t)(D + i * 32 + own_row + k * 16) * D + own_col);
+    };
+    load_behind(0);
     float dq[MH][2][4] = {}, dk[MH][2][4] = {}, small[3][MH][2][4] = {};
     float(&ql)[MH][2][4] = NP > 1 ? small[0] : dq;  // fp32 results: the small products apart
     float(&kl)[MH][2][4] = NP > 1 ? small[1] : dk;
@@ -514,6 +503,15 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
         for (int ks = 0; ks < D / 16; ++ks) {
             uint32_t w[NP][4];
             state_of(D / 16 + ks, w);
+            if (ks % 2 == 0) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float4 x = *reinterpret_cast<const float4*>(
+                        sm + L::RING + (D / 32 + ks / 2) % L::SLICES * L::SLICE + ((own_row + k * 16) * L::SLD + own_col) * 4);
+                    dot = fmaf(x.x, behind[k].x, fmaf(x.y, behind[k].y, fmaf(x.z, behind[k].z, fmaf(x.w, behind[k].w, dot))));
+                }
+                if (ks / 2 + 1 < D / 32) load_behind(ks / 2 + 1);
+            }
 #pragma unroll
             for (int m = 0; m < MH; ++m) {
                 uint32_t a[UP][4];
@@ -538,7 +536,28 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
                     dk[m][k][e] = fmaf(gates[4 * TB + i], y[m][k][e], -gates[3 * TB + i] * dk[m][k][e]);
                 }
     }
+    float* ends = reinterpret_cast<float*>(sm + L::ENDS);
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+    if (lane == 0) ends[warp] = dot;
     __syncthreads();  // X and M are complete
+    if (warp == THREADS / 32 - 1) {  // dlog_decay: what is behind the block and the tokens' sums
+        float end_in = lane < THREADS / 32 ? ends[lane] : 0.f;
+#pragma unroll
+        for (int m = 1; m < 16; m <<= 1) end_in += __shfl_xor_sync(0xffffffffu, end_in, m);
+        float after = __shfl_sync(0xffffffffu, end_in, 0), rest = 0.f;
+#pragma unroll
+        for (int k = TB / 32 - 1; k >= 0; --k) {
+            const int j = k * 32 + 31 - lane;
+            const float s = after + dg_hi[k], d = s - after, lo = dg_lo[k] + (rest + ((after - (s - d)) + (dg_hi[k] - d)));
+            float x = s + lo;
+            after = __shfl_sync(0xffffffffu, s, 31), rest = __shfl_sync(0xffffffffu, lo, 31);
+            if (j >= rows || !p.dg.p) continue;
+            if (j >= live || (!p.S0 && t0 + j == 0)) x = 0.f;
+            bad = fmaf(x, 0.f, bad);
+            *p.dg.at(b, h, t0 + j) = x;
+        }
+    }
     // ... then the pairs
 #pragma unroll 1
     for (int ks = 0; ks < MT; ++ks) {

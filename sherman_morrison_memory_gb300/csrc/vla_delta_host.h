@@ -148,7 +148,6 @@ inline size_t delta_scratch(DeltaArgs* p, void* base, vla_dtype dtype, int B, in
     take(&a.od, per_warp);
     take(&a.vd, per_warp);
     take(&a.bd, per_warp);
-    take(&a.ends, heads * blocks * (d / 8));
     a.blocks = blocks;
     return at;
 }

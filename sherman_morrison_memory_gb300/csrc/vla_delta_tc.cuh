@@ -1003,17 +1003,6 @@ __global__ void __launch_bounds__(DeltaTc<D, R, true>::THREADS, 1) vla_delta_tc_
                 const long long blk = t0 / SPAN;
                 const size_t own = (((size_t)bh * (p.blocks + 1) + blk) * D + row0 + xb) * D + half * W;
                 store_rows<D, W>(s, p.behind + own, lane);
-                const float* S = p.before + own + (size_t)D * D;
-                float dot = 0.f;
-#pragma unroll
-                for (int i = 0; i < W / 8; ++i) {
-                    const float2 y = *reinterpret_cast<const float2*>(S + r * D + i * 8 + t2);
-                    const float2 z = *reinterpret_cast<const float2*>(S + (r + 8) * D + i * 8 + t2);
-                    dot = fmaf(s[i][0], y.x, fmaf(s[i][1], y.y, fmaf(s[i][2], z.x, fmaf(s[i][3], z.y, dot))));
-                }
-#pragma unroll
-                for (int i = 1; i < 32; i <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, i);
-                if (lane == 0) p.ends[((size_t)bh * p.blocks + blk) * (D / 8) + (row0 + xb) / 8 + half] = dot;
             }
             const float* gates = reinterpret_cast<const float*>(sm + L::PREPS + c % L::NPR * L::PREP + L::MATS) + half * 16;
             if (!(ok = wait_warp(prep_ready + c % L::NPR, c / L::NPR))) break;  // behind its loads

@@ -78,7 +78,7 @@ def test_scratch(lib):
     for dtype, span in ((0, 32), (1, 64)):
         for b, h, t, d in ((1, 1, 1, 32), (2, 3, 64, 96), (1, 4, 65, 128)):
             blocks = -(-t // span)
-            parts = [b * h * t * d] + [b * h * (blocks + 1) * d * d] * 2 + [b * h * (d // 16) * t] * 3 + [b * h * blocks * (d // 8)]
+            parts = [b * h * t * d] + [b * h * (blocks + 1) * d * d] * 2 + [b * h * (d // 16) * t] * 3
             assert lib.vla_delta_scratch_bytes(dtype, b, h, t, d) == sum(-(-4 * n // 256) * 256 for n in parts)
     assert lib.vla_delta_scratch_bytes(1, 1, 1, 0, 64) == 0 and lib.vla_delta_scratch_bytes(2, 1, 1, 8, 64) == 0
 
