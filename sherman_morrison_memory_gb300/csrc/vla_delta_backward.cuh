@@ -246,8 +246,10 @@ struct DeltaGrads {
     static constexpr int LD = D + 8, PLANE = TB * LD * 2, XLD = TB + 8, XPLANE = TB * XLD * 2;
     static constexpr int Q = 0, K = Q + NP * PLANE, O = K + NP * PLANE, V = O + NP * PLANE, U = V + NP * PLANE,
                          X = U + UP * PLANE, M = X + XP * XPLANE, GATES = M + MP * XPLANE, RING = GATES + 5 * TB * 4;
-    // the states, 32 rows at a time, two of them under way; the rows' shares of the gates' gradients
-    static constexpr int SLD = D + 4, SLICE = 32 * SLD * 4, SLICES = 3, SHARES = RING + SLICES * SLICE,
+    // the states, 32 rows at a time, two of them under way, or (bf16, d = 64) one, which leaves room for two blocks on an
+    // SM (all gradients of 8 x 16 heads of 4,096 tokens: 795 us with two under way, 706 with one); the rows' shares of the
+    // gates' gradients
+    static constexpr int SLD = D + 4, SLICE = 32 * SLD * 4, SLICES = NP == 1 && D == 64 ? 2 : 3, SHARES = RING + SLICES * SLICE,
                          ENDS = SHARES + (D / 16) * TB * 8, BYTES = ENDS + D / 8 * 4;
     static constexpr int THREADS = D * 4, MH = MT / 2;  // a warp's tiles of 16 tokens
 };
