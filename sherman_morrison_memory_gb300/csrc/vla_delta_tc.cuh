@@ -575,6 +575,10 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
         bool ok = true;
         for (int c = 0; c < chunks; ++c) {
             const long long t0 = (long long)c * DC;
+            if constexpr (TAPE) {
+                if (t0 % SPAN == 0 && rows_in)
+                    store_rows<D, W>(s, p.before + (((size_t)bh * (p.blocks + 1) + t0 / SPAN) * D + row0 + xb) * D + half * W, lane);
+            }
             const float* gates = reinterpret_cast<const float*>(sm + L::PREPS + c % L::NPR * L::PREP + L::MATS) + half * 16;
             if (!(ok = wait_warp(prep_ready + c % L::NPR, c / L::NPR))) break;  // behind its loads
             float2 near[2];
@@ -596,10 +600,6 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
                 parts16(std::integral_constant<int, 3>{}, lanes + L::ZP, x);
             }
             ready(z_ready);
-            if constexpr (TAPE) {
-                if (t0 % SPAN == 0 && rows_in)
-                    store_rows<D, W>(s, p.before + (((size_t)bh * (p.blocks + 1) + t0 / SPAN) * D + row0 + xb) * D + half * W, lane);
-            }
             if (c > 0 && !(ok = output(c - 1))) break;  // beside the products of E: the chunk before's outputs
             if (!(ok = wait_warp(e_done, c))) break;
             vla::tc_fence_after();

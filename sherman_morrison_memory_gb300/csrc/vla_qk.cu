@@ -296,14 +296,14 @@ __global__ void __launch_bounds__(QK_SUMS) vla_qk_sums_kernel(const float* __res
     const int col = threadIdx.x % QK_COLS, slice = threadIdx.x / QK_COLS, which = blockIdx.z;
     const int i = blockIdx.y * QK_COLS + col, heads = shared ? H : 1;
     const float* from = partial + ((size_t)which * H + blockIdx.x) * d + i;
-    const long long rows = (long long)n * heads;
+    const unsigned rows = (unsigned)n * heads;  // of 256 bytes and more: below 2^32 in any memory
     float s = 0.f;
-    for (long long j = slice; j < rows; j += 8 * QK_SLICES) {
+    for (unsigned j = slice; j < rows; j += 8 * QK_SLICES) {
         float v[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const long long row = j + u * QK_SLICES, m = row / heads;
-            v[u] = row < rows ? from[(m * 2 * H + (row - m * heads)) * d] : 0.f;
+            const unsigned row = j + u * QK_SLICES, m = row / (unsigned)heads;
+            v[u] = row < rows ? from[((size_t)m * 2 * H + (row - m * heads)) * d] : 0.f;
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u) s += v[u];
