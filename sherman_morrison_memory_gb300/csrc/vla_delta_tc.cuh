@@ -608,6 +608,17 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
                 float u[2][4], f[2][4];
                 ld_tiles<2>(lanes + L::X + half * 16, u);
                 vla::tc_wait_ld();
+                float2 beta[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 far = *reinterpret_cast<const float2*>(gates + GATE_FAR + i * 8 + t2);
+                    beta[i] = *reinterpret_cast<const float2*>(gates + GATE_BETA + i * 8 + t2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[i][e] = u[i][e] * (e & 1 ? beta[i].y : beta[i].x) * (e & 1 ? far.y : far.x);
+                }
+                parts16(std::integral_constant<int, 3>{}, lanes + L::ZP, f);
+                ready(f_ready);
+                __syncwarp();
                 if constexpr (TAPE) {
                     const long long h0 = t0 + half * 16;
                     if (rows_in) {
@@ -622,18 +633,9 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 far = *reinterpret_cast<const float2*>(gates + GATE_FAR + i * 8 + t2);
-                    const float2 beta = *reinterpret_cast<const float2*>(gates + GATE_BETA + i * 8 + t2);
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        u[i][e] *= e & 1 ? beta.y : beta.x;
-                        f[i][e] = u[i][e] * (e & 1 ? far.y : far.x);
-                    }
-                }
-                parts16(std::integral_constant<int, 3>{}, lanes + L::ZP, f);
-                ready(f_ready);
-                __syncwarp();
+                    for (int e = 0; e < 4; ++e) u[i][e] *= e & 1 ? beta[i].y : beta[i].x;
                 parts16(std::integral_constant<int, L::UP>{}, lanes + L::UPC, u);
                 ready(u_ready);
             }
