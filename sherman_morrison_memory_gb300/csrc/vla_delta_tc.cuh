@@ -525,8 +525,11 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
         // Chunk c's outputs, from its share of the state in o and of the pairs: to the warp's buffer, or (TAPE) o . dO
         T* dst = TAPE ? nullptr : row_of<T>(p.out, b, h, half * 16 + lane / 2) + row0 + xb + lane % 2 * 8;
         float* od = TAPE ? p.od + ((size_t)bh * (D / 16) + (row0 + xb) / 16) * p.T + half * 16 : nullptr;
-        auto output = [&](int c) {
-            const int live = (int)min(16LL, n - (long long)c * DC - half * 16);
+        // 16 workers are longer at them than the products of E last, and not than those of T (8 x 16 heads of 4,096 tokens: d
+        // = 96 300 us, 275 late; gradients of d = 128 1,616, 1,575, of d = 96 1,219, 1,237), 8 are not (d = 64: 176.6 and
+        // 178.5; 32 heads of 32,768, d = 128: 1,715, 1,733)
+        constexpr bool LATE = NW == 16;
+        auto add_pairs = [&](int c) {
             if (!wait_warp(o_done, c)) return false;
             vla::tc_fence_after();
             __syncwarp();
@@ -535,6 +538,10 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
             vla::tc_wait_ld();
             vla::tc_fence_before();
             join(o, x);
+            return true;
+        };
+        auto output = [&](int c) {
+            const int live = (int)min(16LL, n - (long long)c * DC - half * 16);
             if constexpr (TAPE) {
                 float d[2][4];
                 columns(c, L::O, d);
@@ -562,7 +569,6 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
                 __syncwarp();
             }
             arrive_warp(done + c % L::NPR);
-            return true;
         };
         // ... and from there to their rows, up to T
         auto write_out = [&](int c) {
@@ -600,7 +606,10 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
                 parts16(std::integral_constant<int, 3>{}, lanes + L::ZP, x);
             }
             ready(z_ready);
-            if (c > 0 && !(ok = output(c - 1))) break;  // beside the products of E: the chunk before's outputs
+            if (c > 0) {  // beside the products of E: the chunk before's pairs, and (see LATE) what becomes of its outputs
+                if (!(ok = add_pairs(c - 1))) break;
+                if (!LATE) output(c - 1);
+            }
             if (!(ok = wait_warp(e_done, c))) break;
             vla::tc_fence_after();
             __syncwarp();
@@ -640,6 +649,7 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
                 ready(u_ready);
             }
             // beside the products of T: this chunk's share of the state in its outputs
+            if (LATE && c > 0) output(c - 1);
             __syncwarp();
             ld_tiles<2>(lanes + L::X + 32 + half * 16, o);
             vla::tc_wait_ld();
@@ -676,7 +686,10 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
             }
         }
         if (ok && chunks > 1) write_out(chunks - 2);
-        if (ok && chunks > 0 && (ok = output(chunks - 1))) write_out(chunks - 1);
+        if (ok && chunks > 0 && (ok = add_pairs(chunks - 1))) {
+            output(chunks - 1);
+            write_out(chunks - 1);
+        }
         if (ok && rows_in) {
             float* to = TAPE ? p.before + ((size_t)bh * (p.blocks + 1) + (n + SPAN - 1) / SPAN) * D * D : p.S + (size_t)bh * D * D;
             store_rows<D, W>(s, to + (size_t)(row0 + xb) * D + half * W, lane);
