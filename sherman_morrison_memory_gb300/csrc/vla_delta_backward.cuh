@@ -15,12 +15,15 @@
 //
 // What bounds them: the recurrences' chains, as forward; the third launch moves two
 // fp32 states of every 64 tokens (fp32: 32), E and seven sequences. bf16, 4 x 8 heads
-// of 4,096 tokens, d = 64: 577 us, of which 212, 271 and 91; 2 x 32 heads of 4,095,
-// d = 128: 1,017 us, of 283, 368 and 361 (1.1 GB, 165 us at the memory's rate; its
-// shared memory pipes are 56% busy). States every 64 tokens and not 32: half the bytes,
-// and the pairs' products still are a small part. The states come through a ring of
-// shared memory, 32 rows at a time, two slices under way (1,620 us in all without it,
-// 1,474 with it); loads of registers first, and X and M of a block together, gave another 220.
+// of 4,096 tokens, d = 64: 482 us, of which 205, 203 and 76; 2 x 32 heads of 2,048, d =
+// 128: 140, 139 and 194 (550 MB of DRAM, 81 us at the memory's rate; one block an SM,
+// whose loads, products and barriers follow each other, its shared memory 60% busy).
+// States every 64 tokens and not 32: half the bytes, and the pairs' products still are
+// a small part. Of 2 x 32 heads of 4,095 tokens, d = 128, in all: 1,620 us with the states
+// loaded as they are used, 1,474 through a ring of shared memory, 32 rows at a time; 1,253
+// with register loads first and X and M of a block together; 1,017 with the reverse
+// recurrence on tcgen05; 946 with <R, S> in the third launch, where R passes anyway (in the
+// reverse recurrence the loads of S stood in the chain); 921 with stores off the chain.
 #pragma once
 
 #include "vla_delta.cuh"

@@ -24,14 +24,14 @@
 // with the helpers' part, two chunks ahead.
 // Every wait is bounded; one that runs out raises the block's abort flag.
 //
-// Measured: a chunk of 32 tokens takes 1.35 us at d = 64, 2.3 at d = 96 and 2.65 at d = 128 with a head to a block, 1.67
-// at d = 128 with two blocks to a head, however many blocks run: 8 x 16 heads of 4,096 tokens 176, 302 and 345 us (60 us
-// of memory traffic at d = 96), 32 heads of 32,768 tokens, d = 128, 1,715 us. The tensor cores are busy for 24 to 41% of
-// it and the schedulers issue in 62% of the cycles of d = 96 (the workers' cutting into parts), 48% of 64 rows.
+// Measured: a chunk of 32 tokens takes 1.35 us at d = 64, 2.1 at d = 96 and 2.65 at d = 128 with a head to a block, 1.67
+// at d = 128 with two blocks to a head, however many blocks run: 8 x 16 heads of 4,096 tokens 178, 275 and 343 us (60 us
+// of memory traffic at d = 96), 32 heads of 32,768 tokens, d = 128, 1,715 us. The tensor cores are busy for 26 to 41% of
+// it and the schedulers issue in 65% of the cycles of d = 96 (the workers' cutting into parts), 48% of 64 rows.
 // Chunks of 32 tokens, as a group of helpers is longer at a chunk's pairs and inverse than the workers at the chunk, and
 // that work grows with the square of its tokens. What came before, prompt d = 96 and long d = 128: the warp-level path with loads and matrices in the workers
 // 623 and 4,200 us, in helper warps 407 and 2,668, two warps for 16 rows 421 and 1,936; this path with eight workers of
-// plain loads 377 and 2,513, TMA, a second group of helpers and 16 workers 305 and 1,721.
+// plain loads 377 and 2,513, TMA, a second group of helpers and 16 workers 305 and 1,721, the outputs later (LATE) 275.
 #pragma once
 
 #include "vla_delta.cuh"
