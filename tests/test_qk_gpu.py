@@ -170,3 +170,34 @@ def test_rows_far_apart():
     check(q, x, gq, gk, (None, None), False, None, None)
     x.copy_(gk)
     check(q, k, gq, x, weights("heads", 1, d), True, vla.vla_rotation_frequencies(64), None)
+
+
+def test_streams_and_graphs():
+    """Calls on two streams at once give the same bits each time, and a captured pair of calls follows its inputs."""
+    freqs = vla.vla_rotation_frequencies(64)
+
+    def call(x, w):
+        y, stats = vla.vla_qk_norm(x[0], x[1], *w, freqs=freqs)
+        return *y, *stats, *(t for pair in vla.vla_qk_norm_backward(x[2], x[3], x[0], x[1], stats, *w, freqs=freqs) for t in pair)
+
+    sets = [(seqs(4, 2, 6, 700, 64, BF, seed=s), weights(kind, 6, 64, s)) for s, kind in ((1, "heads"), (2, "shared"))]
+    want = [call(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(call(*s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(want, got) for a, b in zip(x, y))
+    held = [x.clone() for x in sets[0][0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(held, sets[0][1])
+    for s in (1, 0):
+        for a, b in zip(held, sets[s][0]):
+            a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, call(sets[s][0], sets[0][1])))
