@@ -147,10 +147,10 @@ vla_status vla_decay_step(const void* q, const void* k, const void* v, vla_dtype
  * 32 tokens gives Inf or NaN. lengths: as for vla_decay_forward().
  *
  * Rounding. fp32 calls, and of bf16 calls the states, dS0 and the gates' gradients:
- * fp32 throughout. bf16 o, dq and dk: beside the result, each term is rounded to
- * bf16 once on its way (the state, a pair product or dv, as they meet the token), at
- * most 2^-8 of it; errors are then about 2.35e-3 of a row's size, where rounding the
- * exact result gives 1.65e-3. dv is rounded at the end alone.
+ * fp32 throughout. bf16 o, dq and dv: rounded at the end, of terms within 2^-14, so
+ * that errors are those of rounding the exact result, about 1.65e-3 of a row's size.
+ * bf16 dk: the same of dv as it was written, whose rounding meets some of the terms:
+ * 1.7e-3 to 2e-3.
  *
  * A token's NaN or Inf reaches the results that depend on it, and may reach those of
  * other tokens of its block of 64 in the same head. One in an output sets VLA_ERR_NONFINITE

@@ -51,9 +51,8 @@ def vla_delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
     float32. Keys are taken as they are; vla_qk_norm(unit=True) makes unit rows.
     ``state`` [B, H, d, d] float32 continues a previous call. ``lengths`` [B]
     int32 (on the device): sequence b has only its first lengths[b] tokens; o is
-    zero behind them. bf16 calls round pair products and the state that a token
-    sees to bf16 on the way to o (S itself stays fp32). ``out`` = (o, S)
-    preallocated; S may be ``state``. ``check=True`` synchronises and raises on
+    zero behind them. S is fp32 in bf16 calls too, and o is rounded at the end.
+    ``out`` = (o, S) preallocated; S may be ``state``. ``check=True`` synchronises and raises on
     an in-kernel failure or a non-finite result. ``wait_limit_us`` (0:
     2,000,000) bounds each in-kernel wait; ``test_stall_producer=True`` (testing
     only) makes them run out (VLA_ERR_TIMEOUT): bf16 calls of more than 64

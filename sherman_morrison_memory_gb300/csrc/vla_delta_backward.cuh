@@ -240,8 +240,10 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>, D == 32 ? 2 : 1) vla_delta_r
     if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, 0);
 }
 
-// dQ, dK and the gates' gradients of a block of tokens: two warps for 16 columns of d, a half of the tokens each. bf16 calls round a term once
-// on its way beside the result: dV as it was written, or S, R or X; U, M and S where dV meets it are two parts.
+// dQ, dK and the gates' gradients of a block of tokens: two warps for 16 columns of d, a half of the tokens each. bf16 calls
+// take dV as it was written, the one rounding of a term to bf16 on its way (dk 2.0e-3 off where rounding the exact result
+// gives 1.65e-3; its rest would be two bytes more a value, written and read); S, R, U, X and M are two parts, 2^-16 off.
+// (One part of S against dO and of R against U: 2.2e-3 for both.)
 template <int D, typename T>
 struct DeltaGrads {
     static constexpr int NP = PARTS<T>, TB = BLOCK<T>, MT = TB / 16;
@@ -482,19 +484,15 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
     const uint32_t rows_at = base + (m0 * 16 * LD + down_across<LD>(lane)) * 2;
 #pragma unroll 2
     for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t w[UP][4], w1[NP][4];
+        uint32_t w[UP][4];
         state_of(ks, w);
-#pragma unroll
-        for (int q = 0; q < NP; ++q)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w1[q][k] = w[q][k];
 #pragma unroll
         for (int m = 0; m < MH; ++m) {
             uint32_t a[NP][4];
 #pragma unroll
             for (int q = 0; q < NP; ++q) ldsm(a[q], rows_at + L::O + q * L::PLANE + (m * 16 * LD + ks * 16) * 2);
-            mma_parts<NP>(dq[m][0], ql[m][0], a, w1, 0);
-            mma_parts<NP>(dq[m][1], ql[m][1], a, w1, 1);
+            mma_parts<NP>(dq[m][0], ql[m][0], a, w, 0);
+            mma_parts<NP>(dq[m][1], ql[m][1], a, w, 1);
 #pragma unroll
             for (int q = 0; q < NP; ++q) ldsm(a[q], rows_at + L::V + q * L::PLANE + (m * 16 * LD + ks * 16) * 2);
             mma_parts<NP>(dk[m][0], kl[m][0], a, w, 0);
@@ -506,7 +504,7 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
         float(&yl)[MH][2][4] = NP > 1 ? small[2] : y;
 #pragma unroll 2
         for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t w[NP][4];
+            uint32_t w[UP][4];
             state_of(D / 16 + ks, w);
             if (ks % 2 == 0) {
 #pragma unroll

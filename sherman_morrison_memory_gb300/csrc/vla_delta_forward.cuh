@@ -19,15 +19,15 @@ struct DeltaForward {
     static constexpr int NP = PARTS<T>;
     static constexpr int TILES = TAPE && NP == 1 ? 4 : 3;         // K, Q, V and dO (fp32: read where it is used)
     static constexpr bool FULL = TAPE || NP == 3;                 // o as an fp32 result
-    static constexpr int PP = FULL ? 3 : 1, UP = FULL ? 3 : 2;    // parts of P and of b E on their way to o
-    using L = DeltaLay<D, T, TILES, PP>;
+    static constexpr int OP = FULL ? 3 : 2;                       // parts of S, P and b E on their way to o
+    using L = DeltaLay<D, T, TILES, OP>;
 };
 
 template <int D, typename T, bool TAPE>
 __global__ void __launch_bounds__(DELTA_THREADS<D>, D == 32 ? 2 : 1) vla_delta_forward_kernel(const __grid_constant__ DeltaArgs p) {
     using F = DeltaForward<D, T, TAPE>;
     using L = typename F::L;
-    constexpr int NP = F::NP, PP = F::PP, LD = L::LD, SPAN = BLOCK<T>;
+    constexpr int NP = F::NP, OP = F::OP, LD = L::LD, SPAN = BLOCK<T>;
     extern __shared__ __align__(128) char sm[];
     const int splits = D / p.rows, bh = blockIdx.x / splits, row0 = (blockIdx.x % splits) * p.rows;
     const int b = bh / p.H, h = bh % p.H;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>, D == 32 ? 2 : 1) vla_delta_f
                 if (NP == 1 && hw == 3 && c + 1 < chunks) load(c + 1);
                 const float gc = g, bc = beta;
                 gates(c + 1);
-                prepare_chunk<L, D, NP, PP, false>(sm, tile(c, 0), tile(c, 1), prep(c), gc, bc, p.scale, whole, hw, lane);
+                prepare_chunk<L, D, NP, OP, false>(sm, tile(c, 0), tile(c, 1), prep(c), gc, bc, p.scale, whole, hw, lane);
                 cp_async_wait<0>();
             }
             __syncthreads();
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>, D == 32 ? 2 : 1) vla_delta_f
                 for (int i = 0; i < 4; ++i) give(mine, i, x[i], lane);
                 times_rows<W, LD, NP, 0, L::PLANE>(all, x, s, qt + across_down<LD>(lane) * 2, 0);
             } else {
-                times_rows<W, LD, NP, 1, L::PLANE>(x, all, s, kt + across_down<LD>(lane) * 2, qt + across_down<LD>(lane) * 2);
+                times_rows<W, LD, NP, OP, L::PLANE>(x, all, s, kt + across_down<LD>(lane) * 2, qt + across_down<LD>(lane) * 2);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) give(mine, i, x[i], lane);
             }
@@ -200,9 +200,9 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>, D == 32 ? 2 : 1) vla_delta_f
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 if (ks > half) break;
-                uint32_t a[F::UP][4];
-                to_operand<F::UP>(a, u[2 * ks], u[2 * ks + 1]);
-                times_block<PP, F::UP, L::PAIR, false>(o, low, a, pairs + ks * 32);
+                uint32_t a[OP][4];
+                to_operand<OP>(a, u[2 * ks], u[2 * ks + 1]);
+                times_block<OP, OP, L::PAIR, false>(o, low, a, pairs + ks * 32);
             }
             join(o, low);
         }

@@ -3,12 +3,12 @@
 // gradients need of it. A block per head (R = 64 of d = 128: two) takes DC = 32
 // tokens at a time, its R rows of S on the TMEM lanes:
 //
-//   [X | Y][x][i] = sum_y S[x][y] [k_i | q_i][y]     A: S in three bf16 parts (Y: its first), TMEM
+//   [X | Y][x][i] = sum_y S[x][y] [k_i | q_i][y]     A: S in three bf16 parts (Y: its first two), TMEM
 //   Z[x][j]  = v_j[x] - exp(G_j) X[x][j]
 //   E[x][i]  = sum_j Z[x][j] Inv[i][j]               A: Z in three parts; Inv in three, six products
 //   T[x][y]  = sum_j (b_j exp(G_C - G_j) E[x][j]) k_j[y]    A: in three parts
 //   S        = exp(G_C) S + T                        fp32, in registers
-//   o_i[x]   = scale exp(G_i) Y[x][i] + sum_j b_j E[x][j] P[i][j]   A: b E in two parts
+//   o_i[x]   = scale exp(G_i) Y[x][i] + sum_j b_j E[x][j] P[i][j]   A: b E in two parts, P in two
 //
 // The workers' fragments of S, Z and E are what tcgen05.ld and st move (16x256b,
 // 16x128b) and what ldmatrix gives of v, so that nothing but o and the helpers' small
@@ -50,9 +50,11 @@ struct DeltaTc {
     static constexpr int NST = 4;
     // a stage: for each box of d, K and Q; V (and dO) at the block's rows
     static constexpr int V = NB * 2 * BOX, O = V + VB * BOX, STAGE = O + (TAPE ? VB * BOX : 0);
-    static constexpr int PP = TAPE ? 3 : 1, UP = TAPE ? 3 : 2;  // parts of P and of b E
+    // parts of S, P and b E on their way to o, whose terms are then 2^-14 off at most (one part of S and of P would leave o
+    // 2.4e-3 off, where its own rounding gives 1.65e-3)
+    static constexpr int OP = TAPE ? 3 : 2;
     // a chunk's matrices, two of 64 columns: the inverse's parts 0 | 1, its 2 | P's 0, P's 1 | 2; gates
-    static constexpr int MATS = (TAPE ? 3 : 2) * BOX, PREP = MATS + 1024;
+    static constexpr int MATS = 3 * BOX, PREP = MATS + 1024;
     // chunks' matrices: a chunk's are free once the next one's Z is out, and two groups of helpers work on two at a time
     static constexpr int NPR = 4, GROUPS = 2, SCRATCH = (2 * 16 * NLD + 3 * 3 * DC) * 4;
     static constexpr int PREPS = NST * STAGE, N = PREPS + NPR * PREP, OUT = N + GROUPS * SCRATCH;
@@ -64,7 +66,7 @@ struct DeltaTc {
     static constexpr int W = D / 2;                        // a worker's columns
     static constexpr int PIECES = (W + 31) / 32;
     // TMEM columns; E takes X's place once Z is made of it, and what T is made of Z's
-    static constexpr int SB = 0, ZP = SB + 3 * (D / 2), UPC = ZP + 48, X = UPC + UP * 16, OP = X + 64, TC = OP + 32, COLS = 512;
+    static constexpr int SB = 0, ZP = SB + 3 * (D / 2), UPC = ZP + 48, X = UPC + OP * 16, PO = X + 64, TC = PO + 32, COLS = 512;
     static_assert(TC + D <= COLS, "tensor memory");
     static constexpr int THREADS = (NW + 8) * 32;
     __host__ __device__ static constexpr int stage_of(int c) { return c % NST * STAGE; }  // the stage of a chunk
@@ -103,7 +105,7 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
         return in_box(row, (part & 1) * 4 + j8) + (part >> 1) * L::BOX;
     };
     float x[2][4];
-    uint32_t pw[4][L::PP];
+    uint32_t pw[4][L::OP];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         const int j = np * 16 + n * 8 + t2;
@@ -121,16 +123,16 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
                 y[e] = j + e <= i ? c[2 + n][2 * hf + e] * w * scale : 0.f;
                 if (hw != 1) N[BACK ? (hf * 8 + r) * NLD + n * 8 + t2 + e : (n * 8 + t2 + e) * NLD + hf * 8 + r] = x[n][2 * hf + e];
             }
-            split<L::PP>(y[0], y[1], pw[2 * n + hf]);
+            split<L::OP>(y[0], y[1], pw[2 * n + hf]);
             if constexpr (!BACK)
 #pragma unroll
-                for (int p = 0; p < L::PP; ++p)  // behind the inverse's three parts
+                for (int p = 0; p < L::OP; ++p)  // behind the inverse's three parts
                     *reinterpret_cast<uint32_t*>(prep + part_at(3 + p, i, np * 2 + n) + t2 * 2) = pw[2 * n + hf][p];
         }
     }
     if constexpr (BACK)
 #pragma unroll
-        for (int p = 0; p < L::PP; ++p)
+        for (int p = 0; p < L::OP; ++p)
             stsm_t(vla::smem_u32(prep) + part_at(3 + p, np * 16 + across, mt * 2 + ((lane >> 3) & 1)), pw[0][p], pw[1][p], pw[2][p], pw[3][p]);
     if (hw != 1) {
         __syncwarp();
@@ -175,7 +177,7 @@ __device__ __forceinline__ void prepare_boxes(char* scratch, uint32_t stage, cha
             }
             if (mt == (BACK ? 1 : 0)) {  // nothing above the diagonal
 #pragma unroll
-                for (int p = 0; p < INV_PARTS + L::PP; ++p)
+                for (int p = 0; p < INV_PARTS + L::OP; ++p)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         *reinterpret_cast<uint4*>(prep + part_at(p, mt * 16 + row, (BACK ? 0 : 2) + k)) = make_uint4(0u, 0u, 0u, 0u);
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
                         for (int ks = 0; ks < D / 16; ++ks) {
                             if (ks % (W / 16) / 2 != q) continue;
                             mma_ts(tm + L::X, tm + L::SB + part * (D / 2) + ks * 8, at(dk, st + (ks >> 2) * 2 * L::BOX + (ks & 3) * 32),
-                                   part == 0 || TAPE ? id64 : id32, q > 0 || part > 0 || ks > 0);
+                                   part < L::OP ? id64 : id32, q > 0 || part > 0 || ks > 0);
                         }
                     if (q + 1 == L::PIECES) vla::tc_commit(x_done);
                 }
@@ -361,15 +363,15 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
             vla::tc_fence_after();
             if (one) {
 #pragma unroll
-                for (int part = L::UP - 1; part >= 0; --part)
+                for (int part = L::OP - 1; part >= 0; --part)
 #pragma unroll
-                    for (int q = 0; q < L::PP; ++q) {
-                        if (part + q >= L::UP) continue;
+                    for (int q = 0; q < L::OP; ++q) {
+                        if (part + q >= L::OP) continue;
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            mma_ts(tm + L::OP, tm + L::UPC + part * 16 + k * 8,
+                            mma_ts(tm + L::PO, tm + L::UPC + part * 16 + k * 8,
                                    at(dk, pr + ((3 + q) & 1) * 64 + ((3 + q) >> 1) * L::BOX + k * 32), id32,
-                                   !(part == L::UP - 1 && q == 0 && k == 0));
+                                   !(part == L::OP - 1 && q == 0 && k == 0));
                     }
                 vla::tc_commit(o_done);
             }
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
             vla::tc_fence_after();
             __syncwarp();
             float x[2][4];
-            ld_tiles<2>(lanes + L::OP + half * 16, x);
+            ld_tiles<2>(lanes + L::PO + half * 16, x);
             vla::tc_wait_ld();
             vla::tc_fence_before();
             join(o, x);
@@ -645,7 +647,7 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) u[i][e] *= e & 1 ? beta[i].y : beta[i].x;
-                parts16(std::integral_constant<int, L::UP>{}, lanes + L::UPC, u);
+                parts16(std::integral_constant<int, L::OP>{}, lanes + L::UPC, u);
                 ready(u_ready);
             }
             // beside the products of T: this chunk's share of the state in its outputs
