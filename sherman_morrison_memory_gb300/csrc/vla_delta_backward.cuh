@@ -240,6 +240,11 @@ __global__ void __launch_bounds__(DELTA_THREADS<D>, D == 32 ? 2 : 1) vla_delta_r
     if (bad != bad && p.status) vla::record_failure(p.status, vla::BIT_NONFINITE, 3, bh, 0);
 }
 
+// exp(x) as two factors, for blocks of 64 tokens: a head that grows by less than float32 holds in 32 tokens grows by up to the
+// square of that in 64, of values so small that the results are finite. Where exp(x) is small enough it is the first alone.
+__device__ __forceinline__ float grow_first(float x) { return expf(x > 64.f ? 0.5f * x : x); }
+__device__ __forceinline__ float grow_second(float x) { return x > 64.f ? expf(0.5f * x) : 1.f; }
+
 // dQ, dK and the gates' gradients of a block of tokens: two warps for 16 columns of d, a half of the tokens each. bf16 calls
 // take dV as it was written, the one rounding of a term to bf16 on its way (dk 2.0e-3 off where rounding the exact result
 // gives 1.65e-3; its rest would be two bytes more a value, written and read); S, R, U, X and M are two parts, 2^-16 off.
@@ -255,7 +260,7 @@ struct DeltaGrads {
     // SM (all gradients of 8 x 16 heads of 4,096 tokens: 795 us with two under way, 706 with one); the rows' shares of the
     // gates' gradients
     static constexpr int SLD = D + 4, SLICE = 32 * SLD * 4, SLICES = NP == 1 && D == 64 ? 2 : 3, SHARES = RING + SLICES * SLICE,
-                         ENDS = SHARES + (D / 16) * TB * 8, BYTES = ENDS + D / 8 * 4;
+                         ENDS = SHARES + (D / 16) * TB * 8, GROWS = ENDS + D / 8 * 4, BYTES = GROWS + 16;
     static constexpr int THREADS = D * 4, MH = MT / 2;  // a warp's tiles of 16 tokens
 };
 
@@ -351,9 +356,10 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
     float* gates = reinterpret_cast<float*>(sm + L::GATES);
     if (warp == 0) {
         float hi[TB / 32], lo[TB / 32];
-        float all = 0.f, rest = 0.f;
+        float all = 0.f, rest = 0.f, up = 0.f;
 #pragma unroll
         for (int k = 0; k < TB / 32; ++k) {
+            up += fmaxf(g_in[k], 0.f);
             sums_of(g_in[k], lane, hi[k], lo[k]);
             const float s = all + hi[k], d = s - all;
             lo[k] += rest + ((all - (s - d)) + (hi[k] - d));
@@ -361,11 +367,16 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
             all = __shfl_sync(0xffffffffu, hi[k], 31), rest = __shfl_sync(0xffffffffu, lo[k], 31);
         }
 #pragma unroll
+        for (int m = 1; m < 32; m <<= 1) up += __shfl_xor_sync(0xffffffffu, up, m);
+        const bool grows = TB > 32 && up > 64.f;  // no two tokens are further apart than that
+        if (lane == 0) *reinterpret_cast<int*>(sm + L::GROWS) = grows;
+#pragma unroll
         for (int k = 0; k < TB / 32; ++k) {
             const int j = k * 32 + lane;
+            const float near = hi[k] + lo[k], far = (all - hi[k]) + (rest - lo[k]);
             gates[j] = hi[k], gates[TB + j] = lo[k], gates[2 * TB + j] = b_in[k];
-            gates[3 * TB + j] = expf(hi[k] + lo[k]);
-            gates[4 * TB + j] = expf((all - hi[k]) + (rest - lo[k]));
+            gates[3 * TB + j] = grows ? grow_first(near) : expf(near);
+            gates[4 * TB + j] = grows ? grow_first(far) : expf(far);
         }
     }
 #pragma unroll
@@ -385,6 +396,7 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
 
     const int r = lane >> 2, t2 = (lane & 3) * 2;
     const uint32_t base = vla::smem_u32(sm);
+    const bool grows = TB > 32 && *reinterpret_cast<const int*>(sm + L::GROWS);
     // X and M, a 16 x 16 block of both at a time
     constexpr int UNITS = MT * (MT + 1) / 2;
     for (int unit = warp; unit < UNITS; unit += THREADS / 32) {
@@ -419,6 +431,13 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
                     x[q] = j + q <= i ? c[0][k][2 * hf + q] * w * p.scale : 0.f;
                     m[q] = j + q < i ? -c[1][k][2 * hf + q] * w : 0.f;
                 }
+                if (grows)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float a = (gates[i] - gates[j + q]) + (gates[TB + i] - gates[TB + j + q]);
+                        x[q] = j + q <= i ? c[0][k][2 * hf + q] * grow_first(a) * p.scale * grow_second(a) : 0.f;
+                        m[q] = j + q < i ? -c[1][k][2 * hf + q] * grow_first(a) * grow_second(a) : 0.f;
+                    }
                 uint32_t w[L::XP], y[L::MP];
                 split<L::XP>(x[0], x[1], w);
                 split<L::MP>(m[0], m[1], y);
@@ -524,6 +543,19 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
                 mma_parts<UP>(y[m][1], yl[m][1], a, w, 1);
             }
         }
+        if (grows)
+#pragma unroll
+            for (int m = 0; m < MH; ++m)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int i = (m0 + m) * 16 + hf * 8 + r;
+                    const float near = grow_second(gates[i] + gates[TB + i]),
+                                far = grow_second((gates[TB - 1] - gates[i]) + (gates[2 * TB - 1] - gates[TB + i]));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int e = 2 * hf; e < 2 * hf + 2; ++e) dq[m][k][e] *= near, dk[m][k][e] *= near, y[m][k][e] *= far;
+                }
 #pragma unroll
         for (int m = 0; m < MH; ++m)
 #pragma unroll

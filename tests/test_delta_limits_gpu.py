@@ -1,10 +1,11 @@
-"""The gated delta rule on the GPU where its numbers are at their ends: results that are rounded to bf16."""
+"""The gated delta rule on the GPU where its numbers are at their ends: results that are rounded to bf16, heads that
+grow."""
 import pytest
 import torch
 
 import delta_ref as R
 import sherman_morrison_memory_gb300 as vla
-from test_delta_gpu import BF, gates, inputs
+from test_delta_gpu import BF, F32, gates, inputs
 from test_layer_gpu import state_like
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +89,36 @@ def test_bf16_results_are_rounded_once(T, d):
     assert_by_token(dq, ref[0], size[0], 2 * n, "dq")
     assert_by_token(dk, ref[1], size[1], 2 * n, "dk", by_dv)
     assert_by_token(dv, ref[2], size[2], 2 * n, "dv")
+
+
+# ---- heads that grow ----------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,d", [(33, 64), (64, 64), (64, 128), (192, 32), (192, 64), (192, 96), (192, 128)])
+def test_growing_heads(T, d, dtype):
+    """A factor of e^1.5 a token: of 32 tokens that is e^48, of the 64 that a bf16 call's gradients take together e^96, which
+    float32 does not hold, of values so small that every result is finite."""
+    B, H = 1, 2
+    q, k, v, do = inputs(4, B, H, T, d, dtype, seed=T + d)
+    v, do = (1e-10 * v.float()).to(dtype), (1e-5 * do.float()).to(dtype)
+    beta = gates(B, H, T)[1]
+    g = torch.full((B, H, T), 1.5, device="cuda")
+    if T > 64:  # one block grows, the one behind it shrinks by as much
+        g[:, :, :64], g[:, :, 128:] = 0.0, -1.5
+    ro, rS, mag = R.delta(q, k, v, g, beta, 0.5)
+    ref, by_dv, size, mb = by_blocks(q, k, v, g, beta, 0.5, do)
+    assert all(float(x.abs().max()) < 1e38 for x in (ro, rS, *ref))
+    # as where nothing grows (a rounding grows as what it is a rounding of does); the exponents of up to 96 are off by half a step
+    n = 4 * R.roundings(T, d) + 2 * 96
+    o, S = vla.vla_delta_forward(q, k, v, g, beta, 0.5, check=True)
+    assert_by_token(o, ro, mag, n, "o")
+    R.assert_normwise(S, rS, n * R.U, "S")
+    (dq, dk, dv), (dg, db), dS0 = vla.vla_delta_backward(q, k, v, g, beta, 0.5, None, do, check=True)
+    for name, x, r, s, once in zip(("dq", "dk", "dv"), (dq, dk, dv), ref, size, (0.0, by_dv, 0.0)):
+        assert_by_token(x, r, s, 2 * n, name, once)
+    R.assert_normwise(dS0, ref[5], 2 * n * R.U, "dS0")
+    off = (db.double().cpu() - ref[4]).norm(dim=-1)
+    assert torch.isfinite(db).all() and bool((off <= 2 * n * R.U * (ref[4].norm(dim=-1) + mb.norm(dim=-1))).all()), ("dbeta", off)
+    terms = ((ro * do.double().cpu()).norm(dim=-1) + (v.double().cpu() * ref[2]).norm(dim=-1)).norm(dim=-1)
+    off = (dg.double().cpu() - ref[3]).norm(dim=-1)
+    assert torch.isfinite(dg).all() and bool((off <= 2 * n * R.U * (ref[3].norm(dim=-1) + 8 * terms)).all()), ("dg", off, terms)
