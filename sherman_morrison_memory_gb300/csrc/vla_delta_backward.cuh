@@ -11,7 +11,16 @@
 // A log decay touches q exp(G), v exp(-G) and the state behind a block alone, so
 //   dg_t = sum over the block's i >= t of (o_i . dO_i - v_i . dV_i) + <R, S> behind the block,
 // of fp32 results of the two recurrences. Before a first token without a state
-// nothing decays: its dg is 0, where the sum would leave its roundings.
+// nothing decays: its dg is 0, where the sum would leave its roundings. So it would
+// where exp(g_t) is small: the terms do not get smaller with it, what they leave does
+// (2e-5 of dg is lost at g = -3, 8% at -12, all of it at -16). Tokens whose decay is
+// below DeltaGrads::STRONG take what lies across it instead, every term of which has
+// the factor exp(g_t) in it:
+//   dg_t = sum i >= t of (scale exp(G_i) q_i . S^T dO_i - exp(G_i) k_i . S^T dV_i) + sum j < t of exp(G_C - G_j) k_j . R^T u_j
+//          + sum i >= t > j of (X_ij q_i . k_j + M_ij k_i . k_j) + exp(G_C) <R, S> of S before the block.
+// Only sums of such terms are formed, no differences: of 16 x 16 blocks of pairs their
+// rows' and columns' sums. A block of tokens without such a one does nothing of it (bf16
+// gradients of 8 x 16 heads of 4,096 tokens, d = 64: 710 us, 806 with one in every block).
 //
 // What bounds them: the recurrences' chains, as forward; the third launch moves two
 // fp32 states of every 64 tokens (fp32: 32), E and seven sequences. bf16, 4 x 8 heads
@@ -253,6 +262,10 @@ template <int D, typename T>
 struct DeltaGrads {
     static constexpr int NP = PARTS<T>, TB = BLOCK<T>, MT = TB / 16;
     static constexpr int UP = NP == 1 ? 2 : 3, XP = UP, MP = UP;
+    // the log decay below which dg_t is the sum of what lies across it: as exact as the parts are (fp32 2e-7; bf16 4e-5 to 2e-4,
+    // by dV as it was written), where the difference of sums loses 1e-6 at -1, 2e-5 at -3 and 4e-5 at -5
+    static constexpr float STRONG = NP == 1 ? -6.f : -2.f;
+    static constexpr int UNITS = MT * (MT + 1) / 2;  // 16 x 16 blocks of pairs
     static constexpr int LD = D + 8, PLANE = TB * LD * 2, XLD = TB + 8, XPLANE = TB * XLD * 2;
     static constexpr int Q = 0, K = Q + NP * PLANE, O = K + NP * PLANE, V = O + NP * PLANE, U = V + NP * PLANE,
                          X = U + UP * PLANE, M = X + XP * XPLANE, GATES = M + MP * XPLANE, RING = GATES + 5 * TB * 4;
@@ -260,9 +273,164 @@ struct DeltaGrads {
     // SM (all gradients of 8 x 16 heads of 4,096 tokens: 795 us with two under way, 706 with one); the rows' shares of the
     // gates' gradients
     static constexpr int SLD = D + 4, SLICE = 32 * SLD * 4, SLICES = NP == 1 && D == 64 ? 2 : 3, SHARES = RING + SLICES * SLICE,
-                         ENDS = SHARES + (D / 16) * TB * 8, GROWS = ENDS + D / 8 * 4, BYTES = GROWS + 16;
+                         ENDS = SHARES + (D / 16) * TB * 8, FLAGS = ENDS + D / 8 * 8, PAIRS = FLAGS + 16,
+                         BYTES = PAIRS + UNITS * 128;
     static constexpr int THREADS = D * 4, MH = MT / 2;  // a warp's tiles of 16 tokens
 };
+
+// Two values of a tile, their parts added up.
+template <int NP, int PLANE>
+__device__ __forceinline__ float2 two_of(const char* at) {
+    float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int q = NP - 1; q >= 0; --q) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(at + q * PLANE);
+        x.x += low_of(w), x.y += high_of(w);
+    }
+    return x;
+}
+
+// dg's terms of a 16 x 16 block of pairs, X_ij q_i . k_j + M_ij k_i . k_j for j < i: below the diagonal the sums of rows from
+// each one on in out[0..16) and of columns up to each one in out[16..32); on it out[t], of the pairs that lie across its token
+// t. By the warp that wrote X and M there.
+template <typename L, int D>
+__device__ __noinline__ void sums_across(float* out, const char* sm, int mt, int np, int lane) {
+    constexpr int NP = L::NP, LD = L::LD;
+    float z[2][2][4] = {}, zl[2][2][4] = {};  // q_i . k_j, k_i . k_j
+    const uint32_t base = vla::smem_u32(sm), a_at = base + (mt * 16 * LD + down_across<LD>(lane)) * 2, b_at = base + L::K + (np * 16 * LD + across_down<LD>(lane)) * 2;
+#pragma unroll 2
+    for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t a[NP][4], b[2][NP][2];
+#pragma unroll
+        for (int q = 0; q < NP; ++q) ldsm_pair(b, 0, q, b_at + q * L::PLANE + ks * 32);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) ldsm(a[q], a_at + L::Q + q * L::PLANE + ks * 32);
+        mma_tiles<NP>(z[0], zl[0], a, b);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) ldsm(a[q], a_at + L::K + q * L::PLANE + ks * 32);
+        mma_tiles<NP>(z[1], zl[1], a, b);
+    }
+    join(z[0], zl[0]);
+    join(z[1], zl[1]);
+    const int r = lane >> 2, t2 = (lane & 3) * 2;
+    float row[2] = {}, col[4] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int at = ((mt * 16 + hf * 8 + r) * L::XLD + np * 16 + k * 8 + t2) * 2;
+            const float2 x = two_of<L::XP, L::XPLANE>(sm + L::X + at), m = two_of<L::MP, L::XPLANE>(sm + L::M + at);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int e = 2 * hf + q;
+                const bool on = mt != np || k * 8 + t2 + q < hf * 8 + r;
+                z[0][k][e] = on ? fmaf(q ? x.y : x.x, z[0][k][e], (q ? m.y : m.x) * z[1][k][e]) : 0.f;
+                row[hf] += z[0][k][e], col[2 * k + q] += z[0][k][e];
+            }
+        }
+    if (mt == np) {
+        float s[16] = {};
+#pragma unroll
+        for (int t = 1; t < 16; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (k * 8 + t2 + (e & 1) < t && (e >> 1) * 8 + r >= t) s[t] += z[0][k][e];
+        // over all lanes: a half of the sums goes to the other half of the lanes each time
+#pragma unroll
+        for (int m = 16; m > 1; m >>= 1)
+#pragma unroll
+            for (int t = 0; t < m / 2; ++t) {
+                const bool upper = lane & m;
+                const float keep = upper ? s[t + m / 2] : s[t], give = upper ? s[t] : s[t + m / 2];
+                s[t] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+            }
+        s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+        if (!(lane & 1)) out[lane >> 1] = s[0];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        row[i] += __shfl_xor_sync(0xffffffffu, row[i], 1);
+        row[i] += __shfl_xor_sync(0xffffffffu, row[i], 2);
+        if (t2 == 0) out[i * 8 + r] = row[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        col[i] = over_rows(col[i]);
+        if (r == 0) out[16 + (i >> 1) * 8 + t2 + (i & 1)] = col[i];
+    }
+    __syncwarp();
+    float s = out[lane];
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) {
+        const float on = __shfl_down_sync(0xffffffffu, s, m, 16), back = __shfl_up_sync(0xffffffffu, s, m, 16);
+        if (lane < 16 ? lane + m < 16 : lane - 16 >= m) s += lane < 16 ? on : back;
+    }
+    out[lane] = s;
+}
+
+// dg of a block's tokens as the sums of what lies across their decays, in lane l those of tokens 31 - l and 63 - l: the states'
+// terms of the rows (shares: with S, with R), the pairs' sums, and the two states' product. By a warp.
+template <int TB, int D>
+__device__ __noinline__ float2 sums_of_decays(const float2* shares, const float* pairs, float whole, int lane) {
+    constexpr int MT = TB / 16, N = TB / 32;
+    float by_s[N] = {}, by_r[N] = {}, dg[2] = {};
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w) {
+            const float2 y = shares[w * TB + k * 32 + 31 - lane];
+            by_s[k] += y.x, by_r[k] += y.y;
+        }
+    float later = 0.f, earlier = 0.f;  // of the other groups
+#pragma unroll
+    for (int k = N - 1; k >= 0; --k) {
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, by_s[k], m);
+            if (lane >= m) by_s[k] += x;
+        }
+        by_s[k] += later;
+        later = __shfl_sync(0xffffffffu, by_s[k], 31);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const float x = __shfl_down_sync(0xffffffffu, by_r[k], m);
+            if (lane + m < 32) by_r[k] += x;
+        }
+        const float all = __shfl_sync(0xffffffffu, by_r[k], 0), before = __shfl_down_sync(0xffffffffu, by_r[k], 1);
+        const int j = k * 32 + 31 - lane, at = j / 16, t = j % 16;
+        float x = by_s[k] + (lane < 31 ? before : 0.f) + earlier + whole;
+        earlier += all;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int np = 0; np <= mt; ++np) {
+                // rows from t on, or (on the diagonal) the pairs across t; all of it; columns before t
+                const int i = mt == at ? t : np < at ? 31 : 15 + t;
+                const float s = pairs[(mt * (mt + 1) / 2 + np) * 32 + i];
+                if (mt >= at && np <= at && (mt == at || i != 15)) x += s;
+            }
+        dg[k] = x;
+    }
+    return make_float2(dg[0], dg[1]);
+}
+
+// A thread's share of <R, S> of two states in memory (in the L2 cache, as the block has read both).
+template <int D, int THREADS>
+__device__ __noinline__ float dot_of(const float* R, const float* S, int tid) {
+    float sum = 0.f;
+#pragma unroll 2
+    for (int i = tid * 4; i < D * D; i += THREADS * 4) {
+        const float4 x = *reinterpret_cast<const float4*>(R + i), s = *reinterpret_cast<const float4*>(S + i);
+        sum = fmaf(x.x, s.x, fmaf(x.y, s.y, fmaf(x.z, s.z, fmaf(x.w, s.w, sum))));
+    }
+    return sum;
+}
 
 template <int D, typename T>
 __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_constant__ DeltaArgs p) {
@@ -369,7 +537,11 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) up += __shfl_xor_sync(0xffffffffu, up, m);
         const bool grows = TB > 32 && up > 64.f;  // no two tokens are further apart than that
-        if (lane == 0) *reinterpret_cast<int*>(sm + L::GROWS) = grows;
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k < TB / 32; ++k) any |= p.dg.p && g_in[k] < L::STRONG;
+        any = __any_sync(0xffffffffu, any);
+        if (lane == 0) *reinterpret_cast<int2*>(sm + L::FLAGS) = make_int2(grows, any);
 #pragma unroll
         for (int k = 0; k < TB / 32; ++k) {
             const int j = k * 32 + lane;
@@ -396,10 +568,9 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
 
     const int r = lane >> 2, t2 = (lane & 3) * 2;
     const uint32_t base = vla::smem_u32(sm);
-    const bool grows = TB > 32 && *reinterpret_cast<const int*>(sm + L::GROWS);
+    const bool grows = TB > 32 && reinterpret_cast<const int*>(sm + L::FLAGS)[0], strong = reinterpret_cast<const int*>(sm + L::FLAGS)[1];
     // X and M, a 16 x 16 block of both at a time
-    constexpr int UNITS = MT * (MT + 1) / 2;
-    for (int unit = warp; unit < UNITS; unit += THREADS / 32) {
+    for (int unit = warp; unit < L::UNITS; unit += THREADS / 32) {
         int mt = 0, np = unit;
         while (np > mt) np -= ++mt;
         float c[2][2][4] = {}, cl[2][2][4] = {};
@@ -446,6 +617,7 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
 #pragma unroll
                 for (int q = 0; q < L::MP; ++q) *reinterpret_cast<uint32_t*>(sm + L::M + q * L::XPLANE + (i * XLD + j) * 2) = y[q];
             }
+        if (__builtin_expect(strong, false)) sums_across<L, D>(reinterpret_cast<float*>(sm + L::PAIRS) + unit * 32, sm, mt, np, lane);
     }
     // The gates' gradients, the sums of the rows' shares: dbeta, and dlog_decay's sums from the last token of a 32 on. The
     // last warp has no pairs, or few.
@@ -472,7 +644,7 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
     const int col0 = warp % (D / 16) * 16, m0 = warp / (D / 16) * MH;
     // <R, S> behind the block: R as it passes, S from memory, where the next block's S is the same
     float4 behind[2];
-    float dot = 0.f;
+    float dot = 0.f, across = 0.f;  // ... and of S before the block
     const int own_row = tid / (D / 4), own_col = tid % (D / 4) * 4;
     auto load_behind = [&](int i) {
 #pragma unroll
@@ -543,6 +715,16 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
                 mma_parts<UP>(y[m][1], yl[m][1], a, w, 1);
             }
         }
+        if constexpr (NP > 1)
+#pragma unroll
+            for (int m = 0; m < MH; ++m)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        dq[m][k][e] += ql[m][k][e], dk[m][k][e] += kl[m][k][e], y[m][k][e] += yl[m][k][e];
+                        ql[m][k][e] = kl[m][k][e] = 0.f;
+                    }
         if (grows)
 #pragma unroll
             for (int m = 0; m < MH; ++m)
@@ -556,6 +738,28 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
 #pragma unroll
                         for (int e = 2 * hf; e < 2 * hf + 2; ++e) dq[m][k][e] *= near, dk[m][k][e] *= near, y[m][k][e] *= far;
                 }
+        if (__builtin_expect(strong, false)) {  // the states' terms of a token, for the decays that they lie across
+#pragma unroll
+            for (int m = 0; m < MH; ++m)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int i = (m0 + m) * 16 + hf * 8 + r;
+                    const float near = gates[3 * TB + i], far = gates[4 * TB + i];
+                    float by_s = 0.f, by_r = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int e = 2 * hf;
+                        const float2 qv = two_of<NP, L::PLANE>(sm + L::Q + (i * LD + col0 + k * 8 + t2) * 2),
+                                     kv = two_of<NP, L::PLANE>(sm + L::K + (i * LD + col0 + k * 8 + t2) * 2);
+                        by_s = fmaf(qv.x, p.scale * near * dq[m][k][e], fmaf(qv.y, p.scale * near * dq[m][k][e + 1], by_s));
+                        by_s = fmaf(-kv.x, near * dk[m][k][e], fmaf(-kv.y, near * dk[m][k][e + 1], by_s));
+                        by_r = fmaf(kv.x, far * y[m][k][e], fmaf(kv.y, far * y[m][k][e + 1], by_r));
+                    }
+#pragma unroll
+                    for (int x = 1; x < 4; x <<= 1) by_s += __shfl_xor_sync(0xffffffffu, by_s, x), by_r += __shfl_xor_sync(0xffffffffu, by_r, x);
+                    if (t2 == 0) shares[col0 / 16 * TB + i] = make_float2(by_s, by_r);
+                }
+        }
 #pragma unroll
         for (int m = 0; m < MH; ++m)
 #pragma unroll
@@ -563,24 +767,30 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = (m0 + m) * 16 + (e >> 1) * 8 + r;
-                    if constexpr (NP > 1) {
-                        dq[m][k][e] += ql[m][k][e], dk[m][k][e] += kl[m][k][e], y[m][k][e] += yl[m][k][e];
-                        ql[m][k][e] = kl[m][k][e] = 0.f;
-                    }
                     dq[m][k][e] *= p.scale * gates[3 * TB + i];
                     dk[m][k][e] = fmaf(gates[4 * TB + i], y[m][k][e], -gates[3 * TB + i] * dk[m][k][e]);
                 }
     }
+    if (__builtin_expect(strong, false)) across = dot_of<D, THREADS>(p.behind + at, p.before + at, tid);
     float* ends = reinterpret_cast<float*>(sm + L::ENDS);
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-    if (lane == 0) ends[warp] = dot;
+    for (int m = 1; m < 32; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m), across += __shfl_xor_sync(0xffffffffu, across, m);
+    if (lane == 0) ends[warp] = dot, ends[D / 8 + warp] = across;
     __syncthreads();  // X and M are complete
     if (warp == THREADS / 32 - 1) {  // dlog_decay: what is behind the block and the tokens' sums
         float end_in = lane < THREADS / 32 ? ends[lane] : 0.f;
 #pragma unroll
         for (int m = 1; m < 16; m <<= 1) end_in += __shfl_xor_sync(0xffffffffu, end_in, m);
         float after = __shfl_sync(0xffffffffu, end_in, 0), rest = 0.f;
+        float2 sums = make_float2(0.f, 0.f);
+        if (strong) {
+            float whole = lane < D / 8 ? ends[D / 8 + lane] : 0.f;
+#pragma unroll
+            for (int m = 1; m < 16; m <<= 1) whole += __shfl_xor_sync(0xffffffffu, whole, m);
+            whole = __shfl_sync(0xffffffffu, whole, 0) * gates[4 * TB - 1];
+            if (grows) whole *= grow_second(gates[TB - 1] + gates[2 * TB - 1]);
+            sums = sums_of_decays<TB, D>(shares, reinterpret_cast<const float*>(sm + L::PAIRS), whole, lane);
+        }
 #pragma unroll
         for (int k = TB / 32 - 1; k >= 0; --k) {
             const int j = k * 32 + 31 - lane;
@@ -588,6 +798,7 @@ __global__ void __launch_bounds__(D * 4) vla_delta_grads_kernel(const __grid_con
             float x = s + lo;
             after = __shfl_sync(0xffffffffu, s, 31), rest = __shfl_sync(0xffffffffu, lo, 31);
             if (j >= rows || !p.dg.p) continue;
+            if (strong && j < live && *p.g.at(b, h, t0 + j) < L::STRONG) x = k ? sums.y : sums.x;
             if (j >= live || (!p.S0 && t0 + j == 0)) x = 0.f;
             bad = fmaf(x, 0.f, bad);
             *p.dg.at(b, h, t0 + j) = x;

@@ -1,11 +1,13 @@
 """The gated delta rule on the GPU where its numbers are at their ends: results that are rounded to bf16, heads that
-grow."""
+grow, decays that leave next to nothing."""
+import math
+
 import pytest
 import torch
 
 import delta_ref as R
 import sherman_morrison_memory_gb300 as vla
-from test_delta_gpu import BF, F32, gates, inputs
+from test_delta_gpu import BF, F32, check_backward, gates, inputs
 from test_layer_gpu import state_like
 
 pytestmark = pytest.mark.gpu
@@ -122,3 +124,91 @@ def test_growing_heads(T, d, dtype):
     terms = ((ro * do.double().cpu()).norm(dim=-1) + (v.double().cpu() * ref[2]).norm(dim=-1)).norm(dim=-1)
     off = (dg.double().cpu() - ref[3]).norm(dim=-1)
     assert torch.isfinite(dg).all() and bool((off <= 2 * n * R.U * (ref[3].norm(dim=-1) + 8 * terms)).all()), ("dg", off, terms)
+
+
+# ---- decays that leave next to nothing ----------------------------------------------------------------------------
+
+STRONG = {BF: -6.0, F32: -2.0}  # below it, dlog_decay is the sum of what the decay multiplies
+
+
+def across(q, k, v, g, beta, scale, state, do, dS, dv):
+    """What log_decay's gradient is a sum of, a token at a time, [B, H, T] each: the magnitudes of all terms that cross
+    the decay, and the 2-norm of those with dV in them, which a bf16 call takes as it was written."""
+    q, k, v, g, beta, do = (x.double().cpu() for x in (q, k, v, g, beta, do))
+    B, H, T, d = q.shape
+    S = state.double().cpu()
+    starts, us = [], []
+    for t in range(T):
+        if t % R.BLOCK == 0:
+            starts.append(S)
+        S = torch.exp(g[:, :, t])[..., None, None] * S
+        us.append(beta[:, :, t, None] * (v[:, :, t] - (S @ k[:, :, t, :, None])[..., 0]))
+        S = S + us[t][..., :, None] * k[:, :, t, None, :]
+    G, ends = dS.double().cpu(), {}
+    for t in reversed(range(T)):
+        if t == T - 1 or (t + 1) % R.BLOCK == 0:
+            ends[t // R.BLOCK] = G
+        G = torch.exp(g[:, :, t])[..., None, None] * (G + scale * do[:, :, t, :, None] * q[:, :, t, None, :]
+                                                      - dv[:, :, t, :, None] * k[:, :, t, None, :])
+    size, once = torch.zeros_like(g), torch.zeros_like(g)
+    late = lambda x, i: x.flip(i).cumsum(i).flip(i)  # noqa: E731
+    for m, S0 in enumerate(starts):
+        at = slice(m * R.BLOCK, min(T, (m + 1) * R.BLOCK))
+        c = g[:, :, at].clamp(min=-256).cumsum(-1)
+        n = c.shape[-1]
+        w = torch.exp((c[..., :, None] - c[..., None, :]).tril()).tril(-1)
+        near, far = torch.exp(c)[..., None], torch.exp(c[..., -1:] - c)[..., None]
+        u = torch.stack(us[at], 2).abs()
+        qa, ka, oa, va = (x[:, :, at].abs() for x in (q, k, abs(scale) * do, dv))
+        R1, kk = ends[m].abs(), (k[:, :, at] @ k[:, :, at].transpose(-1, -2)).abs()
+        qk = (q[:, :, at] @ k[:, :, at].transpose(-1, -2)).abs()
+        # S0[x][y]: every token from t on; R1[x][y]: every one before t
+        by_S = late((near * oa)[..., :, None] * qa[..., None, :], 2) * S0.abs()[:, :, None]
+        by_R = (far * u)[..., :, None] * ka[..., None, :]
+        by_R = (by_R.cumsum(2) - by_R) * R1[:, :, None]
+        t = torch.arange(n)
+        before = (t[None, :] < t[:, None]).double()                    # [t][j]: j before t
+        pair = (w * kk)[:, :, None] * before[None, None, :, None, :]   # [t][i][j]
+        by_V = (near * (ka @ S0.abs().transpose(-1, -2)))[:, :, None] + pair @ u[:, :, None]
+        by_V = by_V * va[:, :, None] * (1 - before)[None, None, :, :, None]
+        by_X = ((w * (oa @ u.transpose(-1, -2)) * qk)[:, :, None] * before[None, None, :, None, :]
+                * (1 - before)[None, None, :, :, None]).sum((-1, -2))
+        whole = torch.exp(c[..., -1:]) * (R1 * S0.abs()).sum((-1, -2))[..., None]
+        size[:, :, at] = by_S.sum((-1, -2)) + by_R.sum((-1, -2)) + by_V.sum((-1, -2)) + by_X + whole
+        once[:, :, at] = torch.sqrt((by_V ** 2).sum((-1, -2)))
+    return size, once
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,d", [(40, 64), (64, 32), (130, 64), (130, 96), (100, 128)])
+def test_gradients_of_strong_decays(T, d, dtype):
+    """Heads of one decay from slow to total, and one with such tokens among slow ones: dlog_decay keeps its digits where
+    the decay leaves little, and is 0 where it leaves nothing."""
+    rates = [-0.01, -1.0, -5.0, -9.5, -10.5, -16.0, -20.0, -30.0, -80.0, -256.0, -1e4, float("-inf"), 0.0]
+    B, H = 1, len(rates)
+    q, k, v, do = inputs(4, B, H, T, d, dtype, seed=T + d)
+    g = torch.tensor(rates, device="cuda")[None, :, None].repeat(B, 1, T)
+    g[:, -1] = -0.02
+    g[:, -1, 5::7], g[:, -1, 9::16], g[:, -1, 31::33] = -12.0, -25.0, float("-inf")
+    beta = gates(B, H, T)[1]
+    S0, dS = state_like(B, H, d, 1), state_like(B, H, d, 2)
+    got = vla.vla_delta_backward(q, k, v, g, beta, 0.4, S0, do, dS, check=True)
+    (dx, (dg, db), dS0), held = got, [h for h, rate in enumerate(rates) if rate > -50]  # whose states float32 holds
+    part = lambda x: x[:, held]  # noqa: E731
+    check_backward(*map(part, (q, k, v, g, beta)), 0.4, *map(part, (S0, do, dS)), None,
+                   (tuple(map(part, dx)), (part(dg), part(db)), part(dS0)))
+    ref = R.delta_grads(q, k, v, g, beta, 0.4, S0, do, dS)[0]
+    size, once = across(q, k, v, g, beta, 0.4, S0, do, dS, ref[2])
+    dg, g = dg.double().cpu(), g.double().cpu()
+    strong = g < STRONG[dtype]
+    e = 2 * R.roundings(T, d) * R.U
+    bound = e * size
+    if dtype == BF:  # terms in two parts; dV's roundings, each within 2^-8 and as often up as down: six times their deviation
+        bound = bound + 2.0 ** -14 * size + 6 * 2.0 ** -8 / math.sqrt(3) * once
+    off = (dg - ref[3]).abs()
+    assert bool((off <= bound + 1e-37)[strong].all()), float((off / (bound + 1e-37))[strong].max())
+    assert (dg[g <= -256] == 0).all()
+    limit = 0.1 if dtype == BF else 2e-3  # these bounds are far below the gradients themselves
+    for h, rate in enumerate(rates):
+        if -81 < rate < STRONG[dtype]:
+            assert float(off[:, h].norm()) <= limit * float(ref[3][:, h].norm()), (rate, float(off[:, h].norm() / ref[3][:, h].norm()))
