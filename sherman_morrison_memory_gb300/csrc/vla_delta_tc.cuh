@@ -65,8 +65,10 @@ struct DeltaTc {
     static_assert(BYTES <= 227 * 1024, "shared memory");
     static constexpr int W = D / 2;                        // a worker's columns
     static constexpr int PIECES = (W + 31) / 32;
-    // TMEM columns; E takes X's place once Z is made of it, and what T is made of Z's
-    static constexpr int SB = 0, ZP = SB + 3 * (D / 2), UPC = ZP + 48, X = UPC + OP * 16, PO = X + 64, TC = PO + 32, COLS = 512;
+    // TMEM columns; E takes X's place once Z is made of it, and what T is made of Z's. X's products with the small parts of S
+    // have a sum of their own, as the tensor cores cut a sum off at every addition (S was up to 6e-7 off with one, a state and
+    // keys of one sign, d = 128): where T's first 32 columns are, which are in registers before the next chunk's X begins.
+    static constexpr int SB = 0, ZP = SB + 3 * (D / 2), UPC = ZP + 48, X = UPC + OP * 16, PO = X + 64, TC = PO + 32, XS = TC, COLS = 512;
     static_assert(TC + D <= COLS, "tensor memory");
     static constexpr int THREADS = (NW + 8) * 32;
     __host__ __device__ static constexpr int stage_of(int c) { return c % NST * STAGE; }  // the stage of a chunk
@@ -315,6 +317,7 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
         auto at = [](uint64_t d, uint32_t addr) { return d + (uint64_t)(addr >> 4); };
         for (int c = 0; c < chunks; ++c) {
             const uint32_t st = sb + L::stage_of(c), pr = sb + L::PREPS + c % L::NPR * L::PREP;
+            const uint64_t keys = at(dk, st);
             if (!wait_warp(full + c % L::NST, c / L::NST)) break;
             bool ok = true;
 #pragma unroll
@@ -327,8 +330,14 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
                             if (ks % (W / 16) / 2 != q) continue;
-                            mma_ts(tm + L::X, tm + L::SB + part * (D / 2) + ks * 8, at(dk, st + (ks >> 2) * 2 * L::BOX + (ks & 3) * 32),
-                                   part < L::OP ? id64 : id32, q > 0 || part > 0 || ks > 0);
+                            const uint32_t s = tm + L::SB + part * (D / 2) + ks * 8;
+                            const uint64_t box = keys + (((ks >> 2) * 2 * L::BOX + (ks & 3) * 32) >> 4);
+                            if (part == 0) {
+                                mma_ts(tm + L::X, s, box, id64, q > 0 || ks > 0);
+                            } else {
+                                mma_ts(tm + L::XS, s, box, id32, q > 0 || part > 1 || ks > 0);
+                                if (part < L::OP) mma_ts(tm + L::X + 32, s, box + (L::BOX >> 4), id32, 1);
+                            }
                         }
                     if (q + 1 == L::PIECES) vla::tc_commit(x_done);
                 }
@@ -593,14 +602,18 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
 #pragma unroll
             for (int i = 0; i < 2; ++i) near[i] = *reinterpret_cast<const float2*>(gates + GATE_NEAR + i * 8 + t2);
             {
-                float x[2][4], v[2][4];
+                float x[2][4], small[2][4], v[2][4];
                 columns(c, L::V, v);
                 if (c > 1) write_out(c - 2);
                 if (!(ok = wait_warp(x_done, c))) break;
                 vla::tc_fence_after();
                 __syncwarp();
-                ld_tiles<2>(lanes + L::X + half * 16, x);
+                uint32_t here = lanes + half * 16;  // formed here: held from chunk to chunk, the addresses leave no register for s
+                asm volatile("" : "+r"(here));
+                ld_tiles<2>(here + L::X, x);
+                ld_tiles<2>(here + L::XS, small);
                 vla::tc_wait_ld();
+                join(x, small);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -722,7 +735,7 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
 //   R       = exp(G_C) R + T
 template <int D>
 struct ReverseTmem {
-    static constexpr int SB = 0, ZP = SB + 3 * (D / 2), A2 = ZP + 48, X = A2 + 48, PD = X + 32, TC = PD + 32;
+    static constexpr int SB = 0, ZP = SB + 3 * (D / 2), A2 = ZP + 48, X = A2 + 48, XS = X + 32, PD = XS + 32, TC = PD + 32;
     static_assert(TC + D <= 512, "tensor memory");
 };
 
@@ -809,8 +822,8 @@ __global__ void __launch_bounds__(DeltaTc<D, R, true>::THREADS, 1) vla_delta_tc_
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks) {
                             if (ks % (W / 16) / 2 != q) continue;
-                            mma_ts(tm + M::X, tm + M::SB + i * (D / 2) + ks * 8, at(dk, st + (ks >> 2) * 2 * L::BOX + (ks & 3) * 32), id32,
-                                   q > 0 || i > 0 || ks > 0);
+                            mma_ts(tm + (i ? M::XS : M::X), tm + M::SB + i * (D / 2) + ks * 8,
+                                   at(dk, st + (ks >> 2) * 2 * L::BOX + (ks & 3) * 32), id32, q > 0 || i > 1 || ks > 0);
                         }
                     if (q + 1 == L::PIECES) vla::tc_commit(x_done);
                 }
@@ -1036,11 +1049,13 @@ __global__ void __launch_bounds__(DeltaTc<D, R, true>::THREADS, 1) vla_delta_tc_
             if (!(ok = wait_warp(x_done, c))) break;
             vla::tc_fence_after();
             {
-                float x[2][4], y[2][4];
+                float x[2][4], small[2][4], y[2][4];
                 __syncwarp();
                 ld_tiles<2>(lanes + M::X + half * 16, x);
+                ld_tiles<2>(lanes + M::XS + half * 16, small);
                 ld_tiles<2>(lanes + M::PD + half * 16, y);
                 vla::tc_wait_ld();
+                join(x, small);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float2 far = *reinterpret_cast<const float2*>(gates + GATE_FAR + i * 8 + t2);

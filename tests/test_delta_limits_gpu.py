@@ -1,5 +1,5 @@
 """The gated delta rule on the GPU where its numbers are at their ends: results that are rounded to bf16, heads that
-grow, decays that leave next to nothing."""
+grow, decays that leave next to nothing, states of one sign."""
 import math
 
 import pytest
@@ -212,3 +212,33 @@ def test_gradients_of_strong_decays(T, d, dtype):
     for h, rate in enumerate(rates):
         if -81 < rate < STRONG[dtype]:
             assert float(off[:, h].norm()) <= limit * float(ref[3][:, h].norm()), (rate, float(off[:, h].norm() / ref[3][:, h].norm()))
+
+
+# ---- states of one sign -------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T", [64, 96])
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+def test_sums_of_one_sign(d, T):
+    """A state and keys of one sign, of which one token takes what it reads: the sum over d coordinates is cut off by
+    2^-23 at most with every 16 of them, always towards zero, and by nothing else."""
+    B, H = 1, 3
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    S0 = 1 + torch.rand(B, H, d, d, generator=gen, device="cuda")
+    k_in = 1 + torch.rand(B, H, T, d, generator=gen, device="cuda")
+    k_in = (k_in / k_in.norm(dim=-1, keepdim=True)).to(BF)
+    v, beta = torch.zeros(B, H, T, d, dtype=BF, device="cuda"), torch.zeros(B, H, T, device="cuda")
+    beta[:, :, 7] = 1
+    S = vla.vla_delta_forward(k_in, k_in, v, None, beta, 1.0, S0, check=True)[1].double().cpu()
+    x, k = S0.double().cpu(), k_in.double().cpu()[:, :, 7]
+    read = (x @ k[..., None])[..., 0]
+    want = x - read[..., :, None] * k[..., None, :]
+    # d / 16 sums cut off, and half a step each of their joining, of E, of the two ends of the product and of the new state
+    bound = (2 * (d // 16) + 6) * R.U * read[..., :, None] * k[..., None, :] + 2 * R.U * x
+    # ... and back: without a gradient of o the state's gradient goes the same way
+    dS0 = vla.vla_delta_backward(k_in, k_in, v, None, beta, 1.0, None, v, S0, check=True)[2].double().cpu()
+    for name, y in (("S", S), ("dS0", dS0)):
+        worst = float(((y - want).abs() / bound).max())
+        assert worst <= 1.0, (name, worst)
+        # what is cut off is between 0 and 2^-23 of a sum, a half of that in the mean
+        mean = float(((y - want) / (R.U * read[..., :, None] * k[..., None, :])).mean())
+        assert abs(mean) <= d // 16, (name, mean)
