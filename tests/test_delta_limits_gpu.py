@@ -1,5 +1,6 @@
 """The gated delta rule on the GPU where its numbers are at their ends: results that are rounded to bf16, heads that
-grow, decays that leave next to nothing, states of one sign."""
+grow, decays that leave next to nothing, states of one sign, strong corrections; and every number of rows that a block
+may have."""
 import math
 
 import pytest
@@ -7,7 +8,7 @@ import torch
 
 import delta_ref as R
 import sherman_morrison_memory_gb300 as vla
-from test_delta_gpu import BF, F32, check_backward, gates, inputs
+from test_delta_gpu import BF, F32, check_backward, check_forward, gates, inputs
 from test_layer_gpu import state_like
 
 pytestmark = pytest.mark.gpu
@@ -242,3 +243,60 @@ def test_sums_of_one_sign(d, T):
         # what is cut off is between 0 and 2^-23 of a sum, a half of that in the mean
         mean = float(((y - want) / (R.U * read[..., :, None] * k[..., None, :])).mean())
         assert abs(mean) <= d // 16, (name, mean)
+
+
+# ---- strong corrections -------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,d", [(64, 32), (100, 64), (129, 96), (200, 128)])
+def test_corrections_beyond_one(T, d, dtype):
+    """beta in (1, 2] on unit keys, and keys of length 1.4 with beta up to 1: the update still stretches nothing."""
+    B, H = 2, 3
+    q, k, v, do = inputs(4, B, H, T, d, dtype, seed=T)
+    g, beta = gates(B, H, T)
+    S0, dS = state_like(B, H, d, 1), state_like(B, H, d, 2)
+    check_forward(q, k, v, g, 1 + beta, 0.4, S0, more=4)
+    check_backward(q, k, v, g, 1 + beta, 0.4, S0, do, dS, more=4)
+    check_forward(q, k, v, None, torch.full_like(beta, 2.0), 0.4, S0, more=4)
+    long = (1.4 * k.float()).to(dtype)
+    check_forward(q, long, v, g, beta, 0.4, S0, more=4)
+    check_backward(q, long, v, g, beta, 0.4, S0, do, dS, more=4)
+
+
+# ---- rows of a block ----------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+def test_every_number_of_rows(d, dtype):
+    """Calls of as many heads as give a block each number of rows of S that there is on the warp-level path: a head's bits
+    are the same in all of them, and right."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    most, T = (64 if d == 128 else d), 64 if dtype == BF else 70
+
+    def rows_of(heads):  # the rule: halved while all blocks run at once
+        rows = most
+        while rows % 32 == 0 and heads * (d // (rows // 2)) <= sms:
+            rows //= 2
+        return rows
+
+    counts = {rows_of(h): h for h in range(sms + 1, 0, -1)}  # the fewest heads of each
+    assert set(counts) == {most >> i for i in range(3) if (most >> i) >= 16 and (i == 0 or (most >> (i - 1)) % 32 == 0)}
+    H = max(counts.values())
+    q, k, v, do = inputs(4, 1, H, T, d, dtype, seed=d)
+    g, beta = gates(1, H, T)
+    S0, dS = state_like(1, H, d, 1), state_like(1, H, d, 2)
+
+    def call(n):
+        x = [y[:, :n] for y in (q, k, v, do, g, beta, S0, dS)]
+        o, S = vla.vla_delta_forward(*x[:3], *x[4:6], 0.3, x[6], check=True)
+        grads, gg, dS0 = vla.vla_delta_backward(*x[:3], *x[4:6], 0.3, x[6], x[3], x[7], check=True)
+        return (o, S, *grads, *gg, dS0)
+
+    want = call(H)
+    for n in counts.values():
+        got = call(n)
+        assert all(torch.equal(a[:, :n], b) for a, b in zip(want, got)), n
+    part = lambda x: x[:, :H:max(1, H // 8)]  # noqa: E731
+    check_forward(*map(part, (q, k, v, g, beta)), 0.3, part(S0), None, tuple(map(part, want[:2])))
+    check_backward(*map(part, (q, k, v, g, beta)), 0.3, part(S0), part(do), part(dS), None,
+                   (tuple(map(part, want[2:5])), tuple(map(part, want[5:7])), part(want[7])))
