@@ -536,10 +536,10 @@ __global__ void __launch_bounds__(DeltaTc<D, R, TAPE>::THREADS, 1) vla_delta_tc_
         // Chunk c's outputs, from its share of the state in o and of the pairs: to the warp's buffer, or (TAPE) o . dO
         T* dst = TAPE ? nullptr : row_of<T>(p.out, b, h, half * 16 + lane / 2) + row0 + xb + lane % 2 * 8;
         float* od = TAPE ? p.od + ((size_t)bh * (D / 16) + (row0 + xb) / 16) * p.T + half * 16 : nullptr;
-        // 16 workers are longer at them than the products of E last, and not than those of T (8 x 16 heads of 4,096 tokens: d
-        // = 96 300 us, 275 late; gradients of d = 128 1,616, 1,575, of d = 96 1,219, 1,237), 8 are not (d = 64: 176.6 and
-        // 178.5; 32 heads of 32,768, d = 128: 1,715, 1,733)
-        constexpr bool LATE = NW == 16;
+        // 16 workers with 48 columns each are longer at them than the products of E last, and not than those of T (8 x 16 heads of
+        // 4,096 tokens, d = 96: 315 us, 287 late); others are not (d = 64: 182, 185; 32 heads, d = 128: 226, 232; 128 heads, d =
+        // 128: 354, 360), nor are the gradients', which write nothing (d = 64 707, 713; d = 96 1,273, 1,285; d = 128 1,647, 1,649)
+        constexpr bool LATE = D == 96 && !TAPE;
         auto add_pairs = [&](int c) {
             if (!wait_warp(o_done, c)) return false;
             vla::tc_fence_after();
