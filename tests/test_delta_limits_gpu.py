@@ -215,6 +215,41 @@ def test_gradients_of_strong_decays(T, d, dtype):
             assert float(off[:, h].norm()) <= limit * float(ref[3][:, h].norm()), (rate, float(off[:, h].norm() / ref[3][:, h].norm()))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_strong_decays_of_padded_batches(d, dtype):
+    """Strong and total decays at random among slow ones, without a state, in sequences of several lengths whose rows behind
+    the end are NaN; and the same gate for all tokens, read from one value."""
+    lengths, H, T = [130, 65, 64, 1], 2, 130
+    B = len(lengths)
+    q, k, v, do = inputs(4, B, H, T, d, dtype, seed=d)
+    g, beta = gates(B, H, T)
+    pick = torch.rand(B, H, T, generator=torch.Generator(device="cuda").manual_seed(d), device="cuda")
+    g = torch.where(pick < 0.2, -15.0, torch.where(pick < 0.25, float("-inf"), 0.05 * g.clamp(min=-4.0)))
+    none, dS = torch.zeros(B, H, d, d, device="cuda"), state_like(B, H, d, 2)
+    for x in (g, beta, do):
+        for b, n in enumerate(lengths):
+            x[b, :, n:] = float("nan")
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    dg = vla.vla_delta_backward(q, k, v, g, beta, 0.4, None, do, dS, lengths=n, check=True)[1][0].double().cpu()
+    e = 2 * R.roundings(T, d) * R.U
+    for b, m in enumerate(lengths):
+        x = [y[b:b + 1, :, :m] for y in (q, k, v, g, beta)]
+        ref = R.delta_grads(*x, 0.4, none[b:b + 1], do[b:b + 1, :, :m], dS[b:b + 1])[0]
+        size, once = across(*x, 0.4, none[b:b + 1], do[b:b + 1, :, :m], dS[b:b + 1], ref[2])
+        bound = e * size
+        if dtype == BF:
+            bound = bound + 2.0 ** -14 * size + 6 * 2.0 ** -8 / math.sqrt(3) * once
+        off, strong = (dg[b:b + 1, :, :m] - ref[3]).abs(), x[3].cpu() < STRONG[dtype]
+        assert bool((off <= bound + 1e-37)[strong].all()), (b, off, bound)
+        assert (dg[b:b + 1, :, :m][x[3].cpu() == float("-inf")] == 0).all() and (dg[b, :, 0] == 0).all() and (dg[b, :, m:] == 0).all()
+    flat = torch.full((1,), -9.0, device="cuda").expand(B, H, T)
+    args = (q, k, v, flat, beta.nan_to_num(0), 0.4, None, do.nan_to_num(0), dS)
+    a = vla.vla_delta_backward(*args, lengths=n, check=True)
+    b = vla.vla_delta_backward(*args[:3], flat.contiguous(), *args[4:], lengths=n, check=True)
+    assert torch.equal(a[1][0], b[1][0]) and torch.equal(a[0][1], b[0][1])
+
+
 # ---- states of one sign -------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("T", [64, 96])
