@@ -181,8 +181,9 @@ vla_status vla_delta_forward(const vla_seq* q, const vla_seq* k, const vla_seq* 
                              const float* S0, const vla_seq_out* o, float* S_out, void* status, void* stream);
 
 /* Device scratch of vla_delta_backward(), 256-byte aligned, one call's own (0 for
- * sizes that it refuses): the recurrence's corrections, 4 d bytes a token and head,
- * and two states every 64 tokens (32 in fp32). */
+ * sizes that it refuses): the recurrence's corrections, 4 d bytes a token and head;
+ * two states every 64 tokens (32 in fp32) and two more a head; 3 d / 4 bytes a token
+ * and head for the gates' gradients. */
 size_t vla_delta_scratch_bytes(vla_dtype dtype, int B, int H, int T, int d);
 
 /* Reverse mode of vla_delta_forward(): from dO = dL/do and dS_T = dL/dS_out (NULL:

@@ -52,11 +52,14 @@ def vla_delta_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
     ``state`` [B, H, d, d] float32 continues a previous call. ``lengths`` [B]
     int32 (on the device): sequence b has only its first lengths[b] tokens; o is
     zero behind them. S is fp32 in bf16 calls too, and o is rounded at the end.
-    ``out`` = (o, S) preallocated; S may be ``state``. ``check=True`` synchronises and raises on
-    an in-kernel failure or a non-finite result. ``wait_limit_us`` (0:
-    2,000,000) bounds each in-kernel wait; ``test_stall_producer=True`` (testing
-    only) makes them run out (VLA_ERR_TIMEOUT): bf16 calls of more than 64
-    tokens have such waits.
+    A token's NaN or Inf (in k, v or a gate) reaches the tokens behind it in its
+    head, and may reach those before it in its block of 32. A head that grows
+    (log_decay above 0) beyond float32 within 32 tokens gives Inf or NaN.
+    ``out`` = (o, S) preallocated; S may be ``state``. ``check=True``
+    synchronises and raises on an in-kernel failure or a non-finite result.
+    ``wait_limit_us`` (0: 2,000,000) bounds each in-kernel wait;
+    ``test_stall_producer=True`` (testing only) makes them run out
+    (VLA_ERR_TIMEOUT): bf16 calls of more than 64 tokens have such waits.
     """
     for name, x in (("q", q), ("k", k), ("v", v)):
         _check_seq(x, name, None if x is q else q)
@@ -99,7 +102,8 @@ def vla_delta_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_de
     which nothing is kept. Returns ``((dq, dk, dv), (dlog_decay, dbeta), dS0)``:
     like q, [B, H, T] float32 (dlog_decay None for a None log_decay), and
     float32 [B, H, d, d]. A gate that is expanded gets its gradient for each
-    token, not their sum. ``out`` = (dq, dk, dv, dlog_decay, dbeta, dS0)
+    token, not their sum. A NaN or Inf reaches what depends on it, and may reach
+    the other tokens of its block of 64 in the same head. ``out`` = (dq, dk, dv, dlog_decay, dbeta, dS0)
     preallocated (dS0 neither ``state`` nor ``grad_state``). ``wait_limit_us``
     and ``test_stall_producer`` as in the forward call.
     """

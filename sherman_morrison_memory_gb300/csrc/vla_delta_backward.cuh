@@ -24,15 +24,16 @@
 //
 // What bounds them: the recurrences' chains, as forward; the third launch moves two
 // fp32 states of every 64 tokens (fp32: 32), E and seven sequences. bf16, 4 x 8 heads
-// of 4,096 tokens, d = 64: 482 us, of which 205, 203 and 76; 2 x 32 heads of 2,048, d =
-// 128: 140, 139 and 194 (550 MB of DRAM, 81 us at the memory's rate; one block an SM,
-// whose loads, products and barriers follow each other, its shared memory 60% busy).
+// of 4,096 tokens, d = 64: 493 us, of which 207, 206 and 79; 2 x 32 heads of 2,048, d =
+// 128: 140, 137 and 213 (542 MB of DRAM, 80 us at the memory's rate; one block an SM,
+// whose loads, products and barriers follow each other, its shared memory 54% busy).
 // States every 64 tokens and not 32: half the bytes, and the pairs' products still are
 // a small part. Of 2 x 32 heads of 4,095 tokens, d = 128, in all: 1,620 us with the states
 // loaded as they are used, 1,474 through a ring of shared memory, 32 rows at a time; 1,253
 // with register loads first and X and M of a block together; 1,017 with the reverse
 // recurrence on tcgen05; 946 with <R, S> in the third launch, where R passes anyway (in the
-// reverse recurrence the loads of S stood in the chain); 921 with stores off the chain.
+// reverse recurrence the loads of S stood in the chain); 921 with stores off the chain; 947
+// with S and R in two parts for dQ and dK, 953 with dg of strong decays apart.
 #pragma once
 
 #include "vla_delta.cuh"
@@ -256,8 +257,9 @@ __device__ __forceinline__ float grow_second(float x) { return x > 64.f ? expf(0
 
 // dQ, dK and the gates' gradients of a block of tokens: two warps for 16 columns of d, a half of the tokens each. bf16 calls
 // take dV as it was written, the one rounding of a term to bf16 on its way (dk 2.0e-3 off where rounding the exact result
-// gives 1.65e-3; its rest would be two bytes more a value, written and read); S, R, U, X and M are two parts, 2^-16 off.
-// (One part of S against dO and of R against U: 2.2e-3 for both.)
+// gives 1.65e-3); S, R, U, X and M are two parts, 2^-16 off. (One part of S against dO and of R against U: 2.2e-3 for dq and
+// dk. dV in two parts, the second in E's low bits: 1.65e-3 for dk, but 1,043 us for 948 of 2 x 32 heads of 4,095 tokens, d =
+// 128, and 541 for 485 of 4 x 8 heads, d = 64.)
 template <int D, typename T>
 struct DeltaGrads {
     static constexpr int NP = PARTS<T>, TB = BLOCK<T>, MT = TB / 16;

@@ -3,7 +3,7 @@
 // bf16 of few tokens.
 //
 // What bounds it: the chain of a chunk's products in the workers and, beside it,
-// the helpers' next chunk. fp32, 5 x 8 heads of 1,021 tokens, d = 64: 102 us, 3.2 us
+// the helpers' next chunk. fp32, 5 x 8 heads of 1,021 tokens, d = 64: 106 us, 3.3 us
 // a chunk, for 6.4 us of memory traffic; 8 x 16 heads of 4,096 tokens: 336, 497,
 // 820 and 1,450 us for d = 32, 64, 96 and 128 (the last in two rounds of blocks).
 // The products of one fp32 part with another are six where bf16 inputs take three,

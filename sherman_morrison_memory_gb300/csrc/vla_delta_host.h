@@ -72,13 +72,15 @@ inline vla_status delta_run(DeltaArgs& p, cudaStream_t s) {
 }
 
 // Whether a bf16 call's recurrences run on tcgen05, one block to an SM, or as warp-level products, which start sooner and
-// can be cut finer. Outputs, us, warp-level against tcgen05, of 8 heads, 64 heads, 304 heads (the gradients' agree):
+// can be cut finer. Outputs, us, warp-level against tcgen05, of 8 heads, 64 heads, 304 heads:
 //   tokens  d = 32                                d = 64                               d = 128
-//   64      8.2, 8.3;  8.4, 8.4;   10.3, 14.4     8.3, 8.4;   8.4, 8.4;   18.5, 15.0   9.0, 10.4;  12.5, 10.5; 39.2, 24.7
-//   128     10.5, 10.3; 10.5, 10.4; 14.5, 18.4    10.5, 10.5; 12.4, 11.9; 26.7, 20.6   12.5, 12.9; 17.7, 14.4; 61.3, 35.1
-//   256     16.5, 14.4; 16.6, 14.5; 22.8, 26.7    16.6, 16.6; 18.6, 16.6; 43.2, 30.9   20.5, 20.5; 28.9, 20.7; 107, 60.0
-// and d = 96 between the last two. The rule goes by the tokens alone: a head's results stay the same, bit for bit,
-// whatever else is in the call.
+//   64      8.2, 8.3;  8.3, 8.5;   10.4, 14.4     8.3, 8.5;   8.5, 10.3;  18.5, 16.5   10.3, 10.4; 12.4, 10.4; 40.0, 24.6
+//   128     10.3, 10.4; 10.4, 10.4; 14.5, 18.6    10.6, 11.6; 12.3, 12.3; 26.7, 20.6   12.4, 13.7; 18.4, 14.4; 61.6, 34.9
+//   256     16.4, 14.5; 16.5, 14.5; 22.7, 28.0    16.5, 16.6; 18.5, 16.5; 43.1, 32.8   18.6, 20.6; 28.9, 20.6; 110, 57.5
+// and d = 96 between the last two; gradients of 304 heads of 64 tokens d = 32 28.7, 36.9, d = 64 53.4, 43.3, d = 128 135,
+// 88.3, of 256 tokens 78.0, 88.1; 156, 121; 409, 269. Heads would decide better (many of d = 32 are sooner on the warp level at
+// any of these lengths, many of d = 128 on tcgen05 already at 64 tokens), but then a head's bits would depend on the other
+// heads of its call. By the tokens alone they do not, and the limit is where few heads of any d lose little.
 inline bool delta_on_tc(const DeltaArgs& p) { return p.T > 64; }
 
 template <int D, int R, bool TAPE, bool BACK = false>
@@ -103,9 +105,9 @@ inline vla_status delta_tc_run(DeltaArgs& p, cudaStream_t s) {
 }
 
 // A bf16 recurrence on tcgen05: heads of d = 128 take two blocks where that is sooner done, a block of 64 rows taking
-// about 5/8 of the time of one of 128 (4,096 tokens: 219 us and 345). Outputs of 76 heads, one block and two: 348 and
-// 221 us; 100 heads 349, 436; 153 heads 685, 648; 304 heads 699, 876. Gradients: 1,527, 1,086; 1,663, 1,833; 3,058,
-// 2,744; 3,976, 4,288.
+// 5/8 to 2/3 of the time of one of 128 (4,096 tokens: 227 us and 353). Outputs of 76 heads, one block and two: 350 and
+// 228 us; 100 heads 355, 447; 153 heads 680, 665; 304 heads 729, 897. Gradients, whose third launch is the same: 1,322, 1,016;
+// 1,473, 1,678; 2,633, 2,518; 3,576, 4,020.
 template <int D, bool TAPE, bool BACK = false>
 inline vla_status delta_tc_pick(DeltaArgs& p, cudaStream_t s) {
     if constexpr (D == 128) {

@@ -22,16 +22,20 @@
 // Warps: the workers (16 rows, a half of the columns and of the tokens each, 8 or
 // 16 of them), one for the MMAs, one for loads, and behind them two groups of three
 // with the helpers' part, two chunks ahead.
-// Every wait is bounded; one that runs out raises the block's abort flag.
+// Every wait on an mbarrier is bounded; one that runs out raises the block's abort flag. What has no limit of its own is the
+// allocation of tensor memory, which waits for another block on the SM that holds some (another stream's call), and that
+// block's waits are bounded.
 //
-// Measured: a chunk of 32 tokens takes 1.35 us at d = 64, 2.1 at d = 96 and 2.65 at d = 128 with a head to a block, 1.67
-// at d = 128 with two blocks to a head, however many blocks run: 8 x 16 heads of 4,096 tokens 178, 275 and 343 us (60 us
-// of memory traffic at d = 96), 32 heads of 32,768 tokens, d = 128, 1,715 us. The tensor cores are busy for 26 to 41% of
-// it and the schedulers issue in 65% of the cycles of d = 96 (the workers' cutting into parts), 48% of 64 rows.
+// Measured: a chunk of 32 tokens takes 1.4 us at d = 64, 2.2 at d = 96 and 2.75 at d = 128 with a head to a block, 1.72
+// at d = 128 with two blocks to a head, however many blocks run: 8 x 16 heads of 4,096 tokens 180, 286 and 353 us (60 us
+// of memory traffic at d = 96), 32 heads of 32,768 tokens, d = 128, 1,757 us. The tensor cores are busy for 29 to 45% of
+// it and the schedulers issue in 66% of the cycles of d = 96 (the workers' cutting into parts), 48% of 64 rows.
 // Chunks of 32 tokens, as a group of helpers is longer at a chunk's pairs and inverse than the workers at the chunk, and
-// that work grows with the square of its tokens. What came before, prompt d = 96 and long d = 128: the warp-level path with loads and matrices in the workers
-// 623 and 4,200 us, in helper warps 407 and 2,668, two warps for 16 rows 421 and 1,936; this path with eight workers of
-// plain loads 377 and 2,513, TMA, a second group of helpers and 16 workers 305 and 1,721, the outputs later (LATE) 275.
+// that work grows with the square of its tokens. What came before, prompt d = 96 and long d = 128: the warp-level path with
+// loads and matrices in the workers 623 and 4,200 us, in helper warps 407 and 2,668, two warps for 16 rows 421 and 1,936;
+// this path with eight workers of plain loads 377 and 2,513, TMA, a second group of helpers and 16 workers 305 and 1,721,
+// the outputs later (LATE) 275. Then for accuracy: two parts of S and P for o, 279 and 1,755; a sum of its own for X's
+// small parts, 284 and 1,757.
 #pragma once
 
 #include "vla_delta.cuh"
@@ -55,7 +59,8 @@ struct DeltaTc {
     static constexpr int OP = TAPE ? 3 : 2;
     // a chunk's matrices, two of 64 columns: the inverse's parts 0 | 1, its 2 | P's 0, P's 1 | 2; gates
     static constexpr int MATS = 3 * BOX, PREP = MATS + 1024;
-    // chunks' matrices: a chunk's are free once the next one's Z is out, and two groups of helpers work on two at a time
+    // chunks' matrices: a chunk's are free once its outputs are formed, behind the next one's Z or (LATE) behind its E, and two
+    // groups of helpers work on two at a time
     static constexpr int NPR = 4, GROUPS = 2, SCRATCH = (2 * 16 * NLD + 3 * 3 * DC) * 4;
     static constexpr int PREPS = NST * STAGE, N = PREPS + NPR * PREP, OUT = N + GROUPS * SCRATCH;
     static constexpr int OUT_LD = 24;                      // elements of a row of a warp's staged outputs

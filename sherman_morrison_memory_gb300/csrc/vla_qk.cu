@@ -148,7 +148,7 @@ template <int D, typename T, bool BACKWARD>
 __global__ void __launch_bounds__(QK_THREADS, sizeof(T) == 4 && !BACKWARD ? 3 : 2) vla_qk_kernel(const __grid_constant__ QkArgs a) {
     using Q = QkLay<D, BACKWARD>;
     // rows of a lane under way, as the registers of two blocks on an SM (three: fp32 forward) allow: d = 96, 8 x 16 heads of
-    // 4,096, bf16: gradients 232 us for 1, 209 for 2, more for 4, whose registers spill; fp32, d = 64, 4 x 16 heads: forward
+    // 4,096, bf16: gradients 232 us for 1, 209 for 2 (which spill 12 to 28 bytes), more for 4, which spill more; fp32, d = 64, 4 x 16 heads: forward
     // 56.9 us for 1, 61.8 for 2
     constexpr int L = Q::L, AT_ONCE = sizeof(T) == 4 ? 1 : BACKWARD ? 2 : 4;
     __shared__ __align__(16) float turns[2][Q::TT * D];                    // of a tile and of the next one
