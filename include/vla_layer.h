@@ -154,7 +154,7 @@ vla_status vla_decay_step(const void* q, const void* k, const void* v, vla_dtype
  * multiplies where it is below -2 (bf16: -6), about 2e-7 off (bf16: up to 2e-4, by dv);
  * above that a difference of larger sums, off by about 2^-22 of |o.dO| + |v.dv| +
  * |R||S| over its block of 64 tokens (32 in fp32): up to 1e-5 of it (bf16: 1e-4) at the
- * lowest decays, less than 2e-6 at decays above -1. 0 below -256.
+ * lowest decays, less than 3e-6 at decays above -1. 0 below -256.
  *
  * A token's NaN or Inf reaches the results that depend on it, and may reach those of
  * other tokens of its block of 64 in the same head. One in an output sets VLA_ERR_NONFINITE
