@@ -146,15 +146,15 @@ vla_status vla_decay_step(const void* q, const void* k, const void* v, vla_dtype
  * values above 0 are taken as they are, and a head that grows beyond float32 within
  * 32 tokens gives Inf or NaN. lengths: as for vla_decay_forward().
  *
- * Rounding. fp32 calls, and of bf16 calls the states, dS0 and the gates' gradients:
- * fp32 throughout. bf16 o, dq and dv: rounded at the end, of terms within 2^-14, so
- * that errors are those of rounding the exact result, about 1.65e-3 of a row's size.
- * bf16 dk: the same of dv as it was written, whose rounding meets some of the terms:
- * 1.7e-3 to 2e-3. dlog_decay of a token is the sum of the terms that its decay
- * multiplies where it is below -2 (bf16: -6), about 2e-7 off (bf16: up to 2e-4, by dv);
- * above that a difference of larger sums, off by about 2^-22 of |o.dO| + |v.dv| +
- * |R||S| over its block of 64 tokens (32 in fp32): up to 1e-5 of it (bf16: 1e-4) at the
- * lowest decays, less than 3e-6 at decays above -1. 0 below -256.
+ * Rounding. fp32 calls, and of bf16 calls the states, dS0 and dbeta: fp32 throughout.
+ * bf16 o, dq and dv: rounded at the end, of terms within 2^-14, so that errors are
+ * those of rounding the exact result, about 1.65e-3 of a row's size. bf16 dk: the
+ * same of dv as it was written, whose rounding meets some of the terms: 1.7e-3 to
+ * 2e-3. dlog_decay of a token is the sum of the terms that its decay multiplies where
+ * it is below -2 (bf16: -6), about 2e-7 off (bf16: up to 2e-4, by dv); above that a
+ * difference of larger sums, off by about 2^-22 of |o.dO| + |v.dv| + |R||S| over its
+ * block of 64 tokens (32 in fp32): up to 1e-5 of it (bf16: 1e-4) at the lowest
+ * decays, less than 3e-6 at decays above -1. 0 below -256.
  *
  * A token's NaN or Inf reaches the results that depend on it, and may reach those of
  * other tokens of its block of 64 in the same head. One in an output sets VLA_ERR_NONFINITE

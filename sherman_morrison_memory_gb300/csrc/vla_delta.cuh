@@ -22,8 +22,8 @@
 // operands: S to K S^T to E to S. Only K S^T, a sum over the columns, goes through
 // shared memory between the two; what follows from it for all tokens both form (E),
 // and a half of the tokens each what is written (O, dV). Three parts hold an fp32
-// value's 24 bits and bf16 inputs are one part as they are, so states, E and gates'
-// gradients are fp32 results. Blocks of fewer rows use more SMs for few heads.
+// value's 24 bits and bf16 inputs are one part as they are, so states, E, dbeta
+// and (but for strong decays) dlog_decay are fp32 results. Blocks of fewer rows use more SMs for few heads.
 // Four helper warps work a chunk ahead: loads, N, P and the inverse, of which the
 // two 16 x 16 blocks on the diagonal are solved a lane a column and joined by products.
 #pragma once
